@@ -12,7 +12,10 @@ Entry points (same names as the C ABI):
   na_attn_decode         single-token decode with per-key probabilities
   na_decode_importance   the step's Born-rule importance (sum over heads of the probabilities)
   na_attn_decode_static_ws  na_attn_decode with library-owned scratch
-  na_prefill_workspace_size / na_decode_workspace_size / na_status_string
+  na_rope_append_kv_paged, na_attn_prefill_chunk_paged, na_attn_decode_paged
+                         the same over a paged cache of bf16 or 8-bit (E4M3) pages
+  na_prefill_workspace_size / na_decode_workspace_size / na_decode_paged_workspace_size /
+  na_status_string
 """
 from __future__ import annotations
 
@@ -31,6 +34,7 @@ NA_ERR_CAPACITY = -3
 NA_ERR_WORKSPACE = -4
 NA_ERR_CUDA = -5
 NA_ERR_DEVICE_TIMEOUT = -6
+NA_ERR_PAGE = -7
 
 NA_QK_NORM = 1
 NA_QK_NORM_ZERO_CENTERED = 2
@@ -38,11 +42,15 @@ NA_V_NORM = 4
 NA_OUT_GATE = 8
 NA_RING_CACHE = 16
 
+NA_KV_BF16 = 0
+NA_KV_E4M3 = 1
+
 # Every symbol include/na.h declares.
 EXPORTED = ("na_rope_append_kv", "na_attn_prefill_chunk", "na_attn_decode",
             "na_attn_decode_static_ws", "na_decode_importance",
             "na_prefill_workspace_size", "na_decode_workspace_size", "na_status_string",
-            "na_selftest_wait_timeout")
+            "na_selftest_wait_timeout", "na_rope_append_kv_paged", "na_attn_prefill_chunk_paged",
+            "na_attn_decode_paged", "na_decode_paged_workspace_size")
 
 
 class na_attn_cfg(ctypes.Structure):
@@ -62,6 +70,14 @@ class na_rope_params(ctypes.Structure):
 class na_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("capacity", ctypes.c_int32)]
+
+
+class na_paged_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class NAError(RuntimeError):
@@ -95,13 +111,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.na_decode_importance.argtypes = [cfgp, I32, P, I32, P, I32, P, I32, I32, P, P]
     lib.na_prefill_workspace_size.argtypes = [cfgp, I32, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.na_decode_workspace_size.argtypes = [cfgp, I32, I32, I32, ctypes.POINTER(SZ)]
+    pagedp = ctypes.POINTER(na_paged_kv_cache)
+    lib.na_rope_append_kv_paged.argtypes = [cfgp, ropep, I32, P, P, I32, P, P, P, P, P, P, pagedp,
+                                            P, P]
+    lib.na_attn_prefill_chunk_paged.argtypes = [cfgp, I32, P, P, I32, I32, I32, P, pagedp, P, P, P,
+                                                SZ, P, P]
+    lib.na_attn_decode_paged.argtypes = [cfgp, I32, P, pagedp, P, I32, P, P, P, I32, I32, P, SZ, P,
+                                         P]
+    lib.na_decode_paged_workspace_size.argtypes = [cfgp, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.na_selftest_wait_timeout.argtypes = [P, P]
     lib.na_status_string.argtypes = [ctypes.c_int]
     lib.na_status_string.restype = ctypes.c_char_p
     for name in ("na_rope_append_kv", "na_attn_prefill_chunk", "na_attn_decode",
                  "na_attn_decode_static_ws", "na_decode_importance",
                  "na_prefill_workspace_size", "na_decode_workspace_size",
-                 "na_selftest_wait_timeout"):
+                 "na_selftest_wait_timeout", "na_rope_append_kv_paged",
+                 "na_attn_prefill_chunk_paged", "na_attn_decode_paged",
+                 "na_decode_paged_workspace_size"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -167,6 +193,29 @@ class KVCache:
         return na_kv_cache(_ptr(self.k), _ptr(self.v), int(self.k.shape[0]), int(self.k.shape[2]))
 
 
+@dataclass
+class PagedKVCache:
+    """Caller-owned pages and page table.
+
+    k, v        [num_pages, num_kv_heads, page_size, head_dim], bfloat16 or float8_e4m3fn
+    page_table  int32 [batch, pages_per_seq]: the page of positions
+                [i * page_size, (i + 1) * page_size) of each sequence
+    k_scale, v_scale  with float8 pages: uint8 [num_pages, num_kv_heads], E8M0 (2^(s - 127))
+    """
+    k: "object"
+    v: "object"
+    page_table: "object"
+    k_scale: "object" = None
+    v_scale: "object" = None
+
+    def c(self) -> na_paged_kv_cache:
+        return na_paged_kv_cache(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
+                                 _ptr(self.v_scale), _ptr(self.page_table), int(self.k.shape[0]),
+                                 int(self.k.shape[2]), int(self.page_table.shape[0]),
+                                 int(self.page_table.shape[1]),
+                                 NA_KV_BF16 if self.k_scale is None else NA_KV_E4M3)
+
+
 # ---------------------------------------------------------------- helpers --
 
 def _ptr(t) -> Optional[int]:
@@ -222,6 +271,19 @@ def _want_cache(cache: "KVCache", cfg: "AttnConfig", batch: int):
     _want(cache.v, "cache.v", "bfloat16", tuple(cache.k.shape))
 
 
+def _want_paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int):
+    kind = "bfloat16" if cache.k_scale is None and cache.v_scale is None else "float8_e4m3fn"
+    _want(cache.k, "cache.k", kind, (None, cfg.num_kv_heads, None, cfg.head_dim))
+    _want(cache.v, "cache.v", kind, tuple(cache.k.shape))
+    _want(cache.page_table, "cache.page_table", "int32", (None, None), batch)
+    if kind != "bfloat16":
+        scales = (int(cache.k.shape[0]), cfg.num_kv_heads)
+        for t, name in ((cache.k_scale, "cache.k_scale"), (cache.v_scale, "cache.v_scale")):
+            if t is None:
+                raise ValueError(f"{name}: missing")
+            _want(t, name, "uint8", scales)
+
+
 def _check(fn: str, rc: int):
     if rc != NA_OK:
         raise NAError(fn, rc)
@@ -229,10 +291,9 @@ def _check(fn: str, rc: int):
 
 # ------------------------------------------------------------ entry points --
 
-def na_rope_append_kv(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache_lens, q, k, v,
-                      q_out, cache: KVCache, q_norm_w=None, k_norm_w=None, status=None,
-                      total_tokens: Optional[int] = None, stream=None):
-    lib = load_library()
+def _append_args(cfg, cu_seqlens, cache_lens, q, k, v, q_out, q_norm_w, k_norm_w, status,
+                 total_tokens):
+    """Checks of the arguments that the contiguous and the paged append share; (batch, tokens)."""
     T = int(q.shape[0]) if total_tokens is None else int(total_tokens)
     batch = int(cu_seqlens.numel()) - 1
     H, KV, d = cfg.num_heads, cfg.num_kv_heads, cfg.head_dim
@@ -245,6 +306,15 @@ def na_rope_append_kv(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache_lens,
     _want(q_norm_w, "q_norm_w", "bfloat16", (d,))
     _want(k_norm_w, "k_norm_w", "bfloat16", (d,))
     _want(status, "status", "int32", (None,), 1)
+    return batch, T
+
+
+def na_rope_append_kv(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache_lens, q, k, v,
+                      q_out, cache: KVCache, q_norm_w=None, k_norm_w=None, status=None,
+                      total_tokens: Optional[int] = None, stream=None):
+    lib = load_library()
+    batch, T = _append_args(cfg, cu_seqlens, cache_lens, q, k, v, q_out, q_norm_w, k_norm_w,
+                            status, total_tokens)
     _want_cache(cache, cfg, batch)
     c, r, kc = cfg.c(), rope.c(), cache.c()
     rc = lib.na_rope_append_kv(ctypes.byref(c), ctypes.byref(r), batch, _ptr(cu_seqlens),
@@ -252,6 +322,22 @@ def na_rope_append_kv(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache_lens,
                                _ptr(k_norm_w), _ptr(q_out), ctypes.byref(kc), _ptr(status),
                                _stream(stream))
     _check("na_rope_append_kv", rc)
+
+
+def na_rope_append_kv_paged(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache_lens, q, k, v,
+                            q_out, cache: PagedKVCache, q_norm_w=None, k_norm_w=None, status=None,
+                            total_tokens: Optional[int] = None, stream=None):
+    """na_rope_append_kv into bf16 or E4M3 pages."""
+    lib = load_library()
+    batch, T = _append_args(cfg, cu_seqlens, cache_lens, q, k, v, q_out, q_norm_w, k_norm_w,
+                            status, total_tokens)
+    _want_paged(cache, cfg, batch)
+    c, r, kc = cfg.c(), rope.c(), cache.c()
+    rc = lib.na_rope_append_kv_paged(ctypes.byref(c), ctypes.byref(r), batch, _ptr(cu_seqlens),
+                                     _ptr(cache_lens), T, _ptr(q), _ptr(k), _ptr(v),
+                                     _ptr(q_norm_w), _ptr(k_norm_w), _ptr(q_out), ctypes.byref(kc),
+                                     _ptr(status), _stream(stream))
+    _check("na_rope_append_kv_paged", rc)
 
 
 def na_prefill_workspace_size(cfg: AttnConfig, batch: int, total_tokens: int, max_new_len: int,
@@ -276,11 +362,19 @@ def na_decode_workspace_size(cfg: AttnConfig, batch: int, max_kv_len: int,
     return int(out.value)
 
 
-def na_attn_prefill_chunk(cfg: AttnConfig, cu_seqlens, cache_lens, max_new_len: int,
-                          max_total_len: int, q_rot, cache: KVCache, out, gate=None,
-                          workspace=None, status=None, total_tokens: Optional[int] = None,
-                          stream=None):
+def na_decode_paged_workspace_size(cfg: AttnConfig, batch: int, max_kv_len: int,
+                                   num_splits: int = 0) -> int:
     lib = load_library()
+    out = ctypes.c_size_t(0)
+    c = cfg.c()
+    _check("na_decode_paged_workspace_size",
+           lib.na_decode_paged_workspace_size(ctypes.byref(c), batch, max_kv_len, num_splits,
+                                              ctypes.byref(out)))
+    return int(out.value)
+
+
+def _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status, total_tokens):
+    """Checks of the arguments that both prefill calls share; (batch, tokens)."""
     T = int(q_rot.shape[0]) if total_tokens is None else int(total_tokens)
     batch = int(cu_seqlens.numel()) - 1
     H, d = cfg.num_heads, cfg.head_dim
@@ -290,6 +384,15 @@ def na_attn_prefill_chunk(cfg: AttnConfig, cu_seqlens, cache_lens, max_new_len: 
     _want(out, "out", "bfloat16", (None, H, d), T)
     _want(gate, "gate", "bfloat16", (None, H, d), T)
     _want(status, "status", "int32", (None,), 1)
+    return batch, T
+
+
+def na_attn_prefill_chunk(cfg: AttnConfig, cu_seqlens, cache_lens, max_new_len: int,
+                          max_total_len: int, q_rot, cache: KVCache, out, gate=None,
+                          workspace=None, status=None, total_tokens: Optional[int] = None,
+                          stream=None):
+    lib = load_library()
+    batch, T = _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status, total_tokens)
     _want_cache(cache, cfg, batch)
     c, kc = cfg.c(), cache.c()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -300,7 +403,24 @@ def na_attn_prefill_chunk(cfg: AttnConfig, cu_seqlens, cache_lens, max_new_len: 
     _check("na_attn_prefill_chunk", rc)
 
 
-def _want_decode(cfg, q_rot, cache, kv_lens, out, probs, gate, status):
+def na_attn_prefill_chunk_paged(cfg: AttnConfig, cu_seqlens, cache_lens, max_new_len: int,
+                                max_total_len: int, q_rot, cache: PagedKVCache, out, gate=None,
+                                workspace=None, status=None, total_tokens: Optional[int] = None,
+                                stream=None):
+    """na_attn_prefill_chunk against bf16 or E4M3 pages (workspace: na_prefill_workspace_size)."""
+    lib = load_library()
+    batch, T = _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status, total_tokens)
+    _want_paged(cache, cfg, batch)
+    c, kc = cfg.c(), cache.c()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = lib.na_attn_prefill_chunk_paged(ctypes.byref(c), batch, _ptr(cu_seqlens),
+                                         _ptr(cache_lens), T, int(max_new_len), int(max_total_len),
+                                         _ptr(q_rot), ctypes.byref(kc), _ptr(gate), _ptr(out),
+                                         _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    _check("na_attn_prefill_chunk_paged", rc)
+
+
+def _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status):
     H, d = cfg.num_heads, cfg.head_dim
     _want(q_rot, "q_rot", "bfloat16", (None, H, d))
     B = int(q_rot.shape[0])
@@ -309,15 +429,15 @@ def _want_decode(cfg, q_rot, cache, kv_lens, out, probs, gate, status):
     _want(kv_lens, "kv_lens", "int32", (None,), B)
     _want(probs, "probs", "float32", (B, H, None))
     _want(status, "status", "int32", (None,), 1)
-    _want_cache(cache, cfg, B)
+    return B
 
 
 def na_attn_decode(cfg: AttnConfig, q_rot, cache: KVCache, kv_lens, max_kv_len: int, out,
                    probs=None, gate=None, workspace=None, num_splits: int = 0, status=None,
                    stream=None):
     lib = load_library()
-    batch = int(q_rot.shape[0])
-    _want_decode(cfg, q_rot, cache, kv_lens, out, probs, gate, status)
+    batch = _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status)
+    _want_cache(cache, cfg, batch)
     c, kc = cfg.c(), cache.c()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     stride = int(probs.shape[-1]) if probs is not None else 0
@@ -328,6 +448,23 @@ def na_attn_decode(cfg: AttnConfig, q_rot, cache: KVCache, kv_lens, max_kv_len: 
     _check("na_attn_decode", rc)
 
 
+def na_attn_decode_paged(cfg: AttnConfig, q_rot, cache: PagedKVCache, kv_lens, max_kv_len: int,
+                         out, probs=None, gate=None, workspace=None, num_splits: int = 0,
+                         status=None, stream=None):
+    """na_attn_decode over bf16 or E4M3 pages (workspace: na_decode_paged_workspace_size)."""
+    lib = load_library()
+    batch = _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status)
+    _want_paged(cache, cfg, batch)
+    c, kc = cfg.c(), cache.c()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    stride = int(probs.shape[-1]) if probs is not None else 0
+    rc = lib.na_attn_decode_paged(ctypes.byref(c), batch, _ptr(q_rot), ctypes.byref(kc),
+                                  _ptr(kv_lens), int(max_kv_len), _ptr(gate), _ptr(out),
+                                  _ptr(probs), stride, int(num_splits), _ptr(workspace), ws_bytes,
+                                  _ptr(status), _stream(stream))
+    _check("na_attn_decode_paged", rc)
+
+
 def na_attn_decode_static_ws(cfg: AttnConfig, q_rot, cache: KVCache, kv_lens, max_kv_len: int,
                              out, probs=None, gate=None, num_splits: int = 0, status=None,
                              stream=None):
@@ -335,8 +472,8 @@ def na_attn_decode_static_ws(cfg: AttnConfig, q_rot, cache: KVCache, kv_lens, ma
     a fixed 20 MiB device array inside the library, for callers that cannot
     allocate device memory.  Calls that overlap on the GPU race on that array."""
     lib = load_library()
-    batch = int(q_rot.shape[0])
-    _want_decode(cfg, q_rot, cache, kv_lens, out, probs, gate, status)
+    batch = _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status)
+    _want_cache(cache, cfg, batch)
     c, kc = cfg.c(), cache.c()
     stride = int(probs.shape[-1]) if probs is not None else 0
     rc = lib.na_attn_decode_static_ws(ctypes.byref(c), batch, _ptr(q_rot), ctypes.byref(kc),

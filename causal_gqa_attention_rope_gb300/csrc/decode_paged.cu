@@ -1,0 +1,559 @@
+// decode_paged.cu -- the split pass of the single-token decode over a paged
+// cache (na_attn_decode_paged).  The arithmetic, the cut of the keys into equal
+// slices and the merge pass are those of the contiguous cache (decode.cu,
+// decode_shared.cuh); here a tile of keys is gathered from pages, and pages may
+// hold E4M3 with one power-of-two scale per (page, kv head).
+//
+// Per key a kv head reads 2 d s bytes (s = 1 or 2) for 4 HPC d multiply-adds,
+// HPC <= 8 query heads at a time: the pass is bound by HBM, and what it has to
+// avoid is spending more time on instructions than the bytes take.
+//
+// The producer warp keeps the page ids (and scales) of the next 64 pages in
+// registers, one page per lane and batch, the second batch loading while the
+// first is used; each lane then issues one box of a tile: a page's rows, or 64
+// of them, by 128 bytes.  A tile is 64 keys aligned to 64 positions, so a box
+// never leaves its page and the 16 keys of a consumer warp always share one
+// page, hence one scale pair, which the producer hands over with the tile.
+//
+// E4M3 pages: the bytes become exact bf16 values in registers (a 32-bit word
+// gives two bf16 pairs), so the products are those of the bf16 cache.  A word
+// holds four consecutive d of one key (K) or two d of two keys (V, loaded
+// transposed as 16-bit pairs); the pairs that come out, bytes 0,2 and 1,3, are
+// taken as they are and the other operand follows: Q is permuted within groups
+// of four d, and the output rows of the V product come out as even and odd d.
+// K's scale multiplies the scores in fp32, V's the probabilities ahead of their
+// rounding to bf16 (exact, a power of two).
+#include "decode_shared.cuh"
+#include "na_internal.cuh"
+#include "tc_primitives.cuh"
+
+namespace {
+
+using namespace dec;
+
+constexpr int TILE = 64;   // keys per tile: CWARPS warps x 16 keys
+constexpr int CWARPS = 4;  // consumer warps
+constexpr int THREADS = (CWARPS + 1) * 32;
+constexpr int MAX_HPC = 8;
+
+// Both page types keep 96 KB of tiles in flight per CTA at d = 128.
+template <bool E4M3>
+constexpr int kStages = E4M3 ? 6 : 3;
+
+template <int D, bool E4M3>
+struct __align__(1024) PagedSmem {
+    static constexpr int ST = kStages<E4M3>;
+    static constexpr uint32_t ROW = D * (E4M3 ? 1 : 2);           // bytes of a row
+    static constexpr uint32_t BOX = ROW < 128 ? ROW : 128;        // of a row in one box
+    static constexpr uint32_t TILE_BYTES = TILE * ROW;
+    uint8_t k[ST][TILE_BYTES];
+    uint8_t v[ST][TILE_BYTES];
+    float obuf[MAX_HPC][D];  // the warps' partial outputs, added in warp order
+    float merge_m[CWARPS][MAX_HPC];
+    float merge_l[CWARPS][MAX_HPC];
+    float2 mul[ST][CWARPS];  // a warp's K and V scale in each stage (E4M3)
+    uint64_t full[ST];
+    uint64_t empty[ST];
+    Slice slice;
+    int abort_flag;
+};
+
+// Byte offset, within a tile of K or V, of 16-byte chunk c of row r, as the
+// swizzled boxes leave it: 128-byte box rows (chunk ^ row % 8), or 64-byte ones
+// (chunk ^ (row / 2) % 4).
+template <uint32_t ROW>
+__device__ __forceinline__ uint32_t chunk_off(int r, int c)
+{
+    if constexpr (ROW == 64)
+        return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    else
+        return (uint32_t)((c >> 3) * (TILE * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// One page as the producer keeps it: its id (-1: holds no key of the piece)
+// and the scale bytes of its K and V.
+struct PageEntry {
+    int id;
+    uint32_t scales;  // K's byte | V's byte << 8
+};
+
+template <bool E4M3>
+__device__ __forceinline__ PageEntry page_entry(const DecodeParams &p, const PagedView &pg,
+                                                const int32_t *row, int i, int lo, int hi, int kvh)
+{
+    PageEntry e{-1, 0x7f7fu};
+    if (i >= lo && i <= hi) {
+        e.id = __ldcg(row + i);
+        if ((unsigned)e.id >= (unsigned)pg.num_pages) {  // reported; read page 0 instead
+            na_report(p.status, NA_ERR_PAGE);
+            e.id = 0;
+        }
+        if constexpr (E4M3) {
+            const size_t at = (size_t)e.id * p.KV + kvh;
+            e.scales = (uint32_t)__ldcg(pg.k_scale + at) | ((uint32_t)__ldcg(pg.v_scale + at) << 8);
+        }
+    }
+    return e;
+}
+
+template <int D, bool E4M3, bool CAPPED>
+__global__ void __launch_bounds__(THREADS, 2)
+    decode_paged_kernel(const DecodeParams p, const PagedView pg,
+                        const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v)
+{
+    typedef PagedSmem<D, E4M3> Smem;
+    constexpr int ST = Smem::ST;
+    constexpr int KS = D / 16;  // k-steps of the score MMA, d-blocks of the PV MMA
+    constexpr uint32_t ROW = Smem::ROW, STAGE_BYTES = Smem::TILE_BYTES;
+    extern __shared__ uint8_t smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned FULL = 0xffffffffu;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; s++) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], CWARPS);
+        }
+        sm.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == CWARPS && lane == 0) {
+        tc::prefetch_tmap(&map_k);
+        tc::prefetch_tmap(&map_v);
+    }
+    grid_dependency_wait();
+    grid_dependents_launch();
+    if (warp == CWARPS)
+        locate_slice(p, lane, sm.slice);
+    __syncthreads();
+    Walker walk;
+    walk.init(sm.slice, p);
+    Piece pc;
+
+    // A piece's keys are positions [kf + k0, kf + k1); its tiles are the
+    // TILE-aligned position ranges covering them, and keys of a tile outside
+    // the piece are masked.
+    if (warp == CWARPS) {
+        // ---------------------------------------------------------- producer --
+        const uint64_t policy = l2_policy_evict_first();  // K/V lines are read once
+        const int page = 1 << pg.page_log;
+        const int box_log = min(pg.page_log, 6), nbox = TILE >> box_log;
+        constexpr int COLS = (int)(ROW / Smem::BOX);  // boxes side by side in a row
+        // this lane's box of a tile: rows [bi << box_log, ...), column block bc, of K or of V
+        const int bi = lane & (nbox - 1), bc = (lane / nbox) % COLS, bt = lane / (nbox * COLS);
+        const uint32_t box_bytes = Smem::BOX << box_log;
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && walk.next(p, pc)) {
+            const int lo = pc.kf + pc.k0, hi = pc.kf + pc.k1;
+            const int p_lo = lo >> pg.page_log, p_hi = (hi - 1) >> pg.page_log;
+            const int32_t *row = pg.table + (size_t)pc.b * pg.pages_per_seq;
+            int wb = (lo / TILE * TILE) >> pg.page_log;  // page of lane 0's entry
+            PageEntry cur = page_entry<E4M3>(p, pg, row, wb + lane, p_lo, p_hi, pc.kvh);
+            PageEntry nxt = page_entry<E4M3>(p, pg, row, wb + 32 + lane, p_lo, p_hi, pc.kvh);
+            for (int t0 = lo / TILE * TILE; t0 < hi; t0 += TILE, it++) {
+                const int stage = it % ST;
+                if ((t0 >> pg.page_log) - wb >= 32) {
+                    cur = nxt;
+                    wb += 32;
+                    nxt = page_entry<E4M3>(p, pg, row, wb + 32 + lane, p_lo, p_hi, pc.kvh);
+                }
+                const bool free = mbar_wait_bounded(&sm.empty[stage], ((it / ST) & 1) ^ 1) &&
+                                  !*(volatile int *)&sm.abort_flag;
+                if (!__all_sync(FULL, free)) {
+                    if (lane == 0) {
+                        na_report(p.status, NA_ERR_DEVICE_TIMEOUT);
+                        *(volatile int *)&sm.abort_flag = 1;
+                    }
+                    ok = false;
+                    break;
+                }
+                const int pos = t0 + (bi << box_log);
+                const int id = __shfl_sync(FULL, cur.id, ((pos >> pg.page_log) - wb) & 31);
+                const bool mine = bt < 2 && id >= 0;
+                const uint32_t n = __popc(__ballot_sync(FULL, mine));
+                if constexpr (E4M3) {
+                    const int kp = t0 + 16 * (lane & 3);
+                    const uint32_t sc = __shfl_sync(FULL, cur.scales, ((kp >> pg.page_log) - wb) & 31);
+                    if (lane < CWARPS)
+                        sm.mul[stage][lane] = make_float2(e8m0_value(sc & 255u), e8m0_value(sc >> 8));
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sm.full[stage], n * box_bytes);
+                __syncwarp();
+                if (mine) {
+                    uint8_t *dst = (bt ? sm.v[stage] : sm.k[stage]) + bc * (TILE * 128) +
+                                   (bi << box_log) * Smem::BOX;
+                    const int y = ((id * p.KV + pc.kvh) << pg.page_log) + (pos & (page - 1));
+                    tc::tma_load_2d_hint(dst, bt ? &map_v : &map_k, bc * 64, y, &sm.full[stage],
+                                         policy);
+                }
+            }
+        }
+        // Every copy issued lands before the CTA can exit.
+        for (int s = 0; s < ST; s++) {
+            if ((int)it - 1 - s < 0)
+                break;
+            const uint32_t last = it - 1 - s;
+            if (!mbar_wait_bounded(&sm.full[last % ST], (last / ST) & 1))
+                na_report(p.status, NA_ERR_DEVICE_TIMEOUT);
+        }
+        return;
+    }
+
+    // ------------------------------------------------------------ consumers --
+    // As in the contiguous pass: warp w scores keys 16 w .. 16 w + 15 of each
+    // tile with S^T = K Q^T, lane l ends up with keys l/4 and l/4 + 8 of heads
+    // 2(l%4) and 2(l%4) + 1, and their probabilities, transposed in registers,
+    // are the B operand of O^T += V^T P^T.
+    const int hpc = p.group / p.head_chunks;
+    const int g = lane >> 2, t = lane & 3;
+    const int h0 = 2 * t, h1 = 2 * t + 1;  // this lane's heads (columns)
+    const bool v0 = h0 < hpc, v1 = h1 < hpc;
+    const uint32_t k_base = smem_addr(sm.k[0]), v_base = smem_addr(sm.v[0]);
+    // ldmatrix row addresses: lane l feeds row l % 8 of 8x8 matrix l / 8.  K's
+    // matrices (rows +0/+8, chunks +0/+1) come in the order (0,0) (8,0) (0,1)
+    // (8,1); V's (transposed) the same with E4M3, (0,0) (0,1) (8,0) (8,1) with bf16.
+    const int mi = lane >> 3, mr = lane & 7;
+    const int ka_row = warp * 16 + (mi & 1) * 8 + mr, ka_col = mi >> 1;
+    const int va_row = E4M3 ? ka_row : warp * 16 + (mi >> 1) * 8 + mr;
+    const int va_col = E4M3 ? ka_col : mi & 1;
+    uint32_t it = 0;
+    // A warp whose wait timed out keeps walking the pieces so that every warp
+    // joins the same named barriers, but does no more waits or writes.
+    bool aborted = false;
+
+    while (walk.next(p, pc)) {
+        const int lo = pc.kf + pc.k0, hi = pc.kf + pc.k1;
+        if (*(volatile int *)&sm.abort_flag)
+            aborted = true;
+        const int head0 = pc.kvh * p.group + pc.hc * hpc;
+
+        // Q as the B operand: column g is head g (zero past hpc), rows are d --
+        // with E4M3, k-step s takes d = 16 s + 4 t + {0, 2} and {1, 3}.
+        uint32_t qf[KS][2];
+        {
+            const bf16 *qrow = p.q + ((size_t)pc.b * p.H + head0 + min(g, hpc - 1)) * D;
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                uint32_t w0, w1;
+                if constexpr (E4M3) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(qrow + 16 * s + 4 * t);
+                    w0 = __byte_perm(u.x, u.y, 0x5410);
+                    w1 = __byte_perm(u.x, u.y, 0x7632);
+                } else {
+                    w0 = *reinterpret_cast<const uint32_t *>(qrow + 16 * s + 2 * t);
+                    w1 = *reinterpret_cast<const uint32_t *>(qrow + 16 * s + 2 * t + 8);
+                }
+                qf[s][0] = g < hpc ? w0 : 0u;
+                qf[s][1] = g < hpc ? w1 : 0u;
+            }
+        }
+        float acc[KS][4];
+#pragma unroll
+        for (int s = 0; s < KS; s++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                acc[s][i] = 0.f;
+        float m_ref[2] = {-INFINITY, -INFINITY};
+        float l_sum[2] = {0.f, 0.f};
+        float *prow0 = (p.probs && v0) ? p.probs + ((size_t)pc.b * p.H + head0 + h0) * p.probs_stride
+                                        : nullptr;
+        float *prow1 = (p.probs && v1) ? p.probs + ((size_t)pc.b * p.H + head0 + h1) * p.probs_stride
+                                        : nullptr;
+
+        for (int t0 = lo / TILE * TILE; t0 < hi && !aborted; t0 += TILE, it++) {
+            const int stage = it % ST;
+            const bool got = mbar_wait_bounded(&sm.full[stage], (it / ST) & 1);
+            if (!__all_sync(FULL, got)) {  // warp-uniform before the .sync.aligned MMAs
+                if (lane == 0) {
+                    na_report(p.status, NA_ERR_DEVICE_TIMEOUT);
+                    *(volatile int *)&sm.abort_flag = 1;
+                }
+                aborted = true;
+                break;
+            }
+            const uint32_t kst = k_base + stage * STAGE_BYTES;
+            const uint32_t vst = v_base + stage * STAGE_BYTES;
+            const bool partial = t0 < lo || t0 + TILE > hi;  // the same in every warp
+            if constexpr (!E4M3) {
+                if (partial) {
+                    // V rows of masked keys are zeroed: they meet a zero probability
+                    // in the PV MMA and must not be NaN (E4M3 bytes never read as one).
+                    for (int c = lane; c < 16 * (D / 8); c += 32) {
+                        const int r = warp * 16 + c / (D / 8), ch = c % (D / 8);
+                        const int pos = t0 + r;
+                        if (pos < lo || pos >= hi)
+                            *reinterpret_cast<uint4 *>(sm.v[stage] + chunk_off<ROW>(r, ch)) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+            }
+
+            // S^T = K Q^T for this warp's 16 keys.
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+            float score_mul = p.scale_log2, v_mul = 1.f;
+            if constexpr (E4M3) {
+                const float2 m = sm.mul[stage][warp];
+                score_mul = p.scale_log2 * m.x;
+                v_mul = m.y;
+#pragma unroll
+                for (int s = 0; s < KS / 2; s++) {
+                    uint32_t w[4], e[4], o[4];
+                    ldsm_x4(kst + chunk_off<ROW>(ka_row, 2 * s + ka_col), w);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        e4m3x4_to_bf16(w[i], kE4m3Unbias, e[i], o[i]);
+                    const uint32_t a0[4] = {e[0], e[1], o[0], o[1]}, a1[4] = {e[2], e[3], o[2], o[3]};
+                    mma_bf16_16816(sc, a0, qf[2 * s][0], qf[2 * s][1]);
+                    mma_bf16_16816(sc, a1, qf[2 * s + 1][0], qf[2 * s + 1][1]);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < KS; s++) {
+                    uint32_t a[4];
+                    ldsm_x4(kst + chunk_off<ROW>(ka_row, 2 * s + ka_col), a);
+                    mma_bf16_16816(sc, a, qf[s][0], qf[s][1]);
+                }
+            }
+            // Scores (log2 domain), masked outside the piece and for the padding
+            // heads; recorded for the combine pass.
+            const int pa = t0 + warp * 16 + g, pb = pa + 8;  // this lane's key positions
+            const bool ina = pa >= lo && pa < hi, inb = pb >= lo && pb < hi;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float x = sc[i] * score_mul;
+                if constexpr (CAPPED) {  // c tanh(s / c) in the log2 domain, tanh(y) = 1 - 2 / (e^2y + 1)
+                    const float e = exp2f(x * p.cap_in);
+                    x = p.cap_out * (1.0f - __fdividef(2.0f, e + 1.0f));
+                }
+                const bool ok = ((i & 2) ? inb : ina) && ((i & 1) ? v1 : v0);
+                sc[i] = ok ? x : -INFINITY;
+            }
+            if (prow0) {
+                if (ina)
+                    prow0[pa] = sc[0];
+                if (inb)
+                    prow0[pb] = sc[2];
+            }
+            if (prow1) {
+                if (ina)
+                    prow1[pa] = sc[1];
+                if (inb)
+                    prow1[pb] = sc[3];
+            }
+            // Tile maximum per head (over the 8 lanes sharing the column), then
+            // (rarely) raise the reference maximum.
+            float mx0 = fmaxf(sc[0], sc[2]), mx1 = fmaxf(sc[1], sc[3]);
+#pragma unroll
+            for (int m = 4; m < 32; m <<= 1) {
+                mx0 = fmaxf(mx0, __shfl_xor_sync(FULL, mx0, m));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(FULL, mx1, m));
+            }
+            const bool raise = mx0 > m_ref[0] + kRescaleThreshold || mx1 > m_ref[1] + kRescaleThreshold;
+            if (__any_sync(FULL, raise)) {  // warp-uniform
+                const float n0 = fmaxf(m_ref[0], mx0), n1 = fmaxf(m_ref[1], mx1);
+                const float a0 = (m_ref[0] == -INFINITY) ? 0.f : exp2f(m_ref[0] - n0);
+                const float a1 = (m_ref[1] == -INFINITY) ? 0.f : exp2f(m_ref[1] - n1);
+                m_ref[0] = n0;
+                m_ref[1] = n1;
+                l_sum[0] *= a0;
+                l_sum[1] *= a1;
+#pragma unroll
+                for (int s = 0; s < KS; s++) {
+                    acc[s][0] *= a0;
+                    acc[s][1] *= a1;
+                    acc[s][2] *= a0;
+                    acc[s][3] *= a1;
+                }
+            }
+            float pr[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                pr[i] = (sc[i] == -INFINITY) ? 0.f : exp2f(sc[i] - m_ref[i & 1]);
+                l_sum[i & 1] += pr[i];
+                if constexpr (E4M3)
+                    pr[i] *= v_mul;
+            }
+            // P^T as the B operand: keys 2(l%4).. of head l/4.
+            const uint32_t b0 = movmatrix_trans(pack_bf16x2(pr[0], pr[1]));
+            const uint32_t b1 = movmatrix_trans(pack_bf16x2(pr[2], pr[3]));
+            // O^T += V^T P^T, one 16-row block of d at a time.
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int s = 0; s < KS / 2; s++) {
+                    uint32_t w[4], e[4], o[4];
+                    ldsm_x4_trans(vst + chunk_off<ROW>(va_row, 2 * s + va_col), w);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        e4m3x4_to_bf16(w[i], kE4m3Unbias, e[i], o[i]);
+                    const uint32_t a0[4] = {e[0], o[0], e[1], o[1]}, a1[4] = {e[2], o[2], e[3], o[3]};
+                    mma_bf16_16816(acc[2 * s], a0, b0, b1);
+                    mma_bf16_16816(acc[2 * s + 1], a1, b0, b1);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < KS; s++) {
+                    uint32_t a[4];
+                    ldsm_x4_trans(vst + chunk_off<ROW>(va_row, 2 * s + va_col), a);
+                    mma_bf16_16816(acc[s], a, b0, b1);
+                }
+                if (partial)
+                    tc::fence_proxy_async_smem();  // the zeroed rows before the stage's next copy
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.empty[stage]);
+        }
+        // Sums over the 8 lanes of each column; then the warps' partials are
+        // merged in warp order.
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) {
+            l_sum[0] += __shfl_xor_sync(FULL, l_sum[0], m);
+            l_sum[1] += __shfl_xor_sync(FULL, l_sum[1], m);
+        }
+        if (g == 0) {
+            if (v0) {
+                sm.merge_m[warp][h0] = m_ref[0];
+                sm.merge_l[warp][h0] = l_sum[0];
+            }
+            if (v1) {
+                sm.merge_m[warp][h1] = m_ref[1];
+                sm.merge_l[warp][h1] = l_sum[1];
+            }
+        }
+        named_barrier_sync(1, CWARPS * 32);
+        float M0 = -INFINITY, M1 = -INFINITY;
+        if (v0)
+#pragma unroll
+            for (int ww = 0; ww < CWARPS; ww++)
+                M0 = fmaxf(M0, sm.merge_m[ww][h0]);
+        if (v1)
+#pragma unroll
+            for (int ww = 0; ww < CWARPS; ww++)
+                M1 = fmaxf(M1, sm.merge_m[ww][h1]);
+        const float f0 = (m_ref[0] == -INFINITY) ? 0.f : exp2f(m_ref[0] - M0);
+        const float f1 = (m_ref[1] == -INFINITY) ? 0.f : exp2f(m_ref[1] - M1);
+        // acc row l/4 is d = 16 s + l/4 and row l/4 + 8 is 8 further on (bf16),
+        // or d = 16 s + 2 (l/4) and the next one (E4M3).
+        const int e0 = E4M3 ? 2 * g : g;
+        constexpr int E1 = E4M3 ? 1 : 8;
+        for (int ww = 0; ww < CWARPS; ww++) {
+            if (warp == ww) {
+#pragma unroll
+                for (int s = 0; s < KS; s++) {
+                    const int e = 16 * s + e0;
+                    if (v0) {
+                        float *o0 = &sm.obuf[h0][e];
+                        o0[0] = ww == 0 ? acc[s][0] * f0 : o0[0] + acc[s][0] * f0;
+                        o0[E1] = ww == 0 ? acc[s][2] * f0 : o0[E1] + acc[s][2] * f0;
+                    }
+                    if (v1) {
+                        float *o1 = &sm.obuf[h1][e];
+                        o1[0] = ww == 0 ? acc[s][1] * f1 : o1[0] + acc[s][1] * f1;
+                        o1[E1] = ww == 0 ? acc[s][3] * f1 : o1[E1] + acc[s][3] * f1;
+                    }
+                }
+            }
+            named_barrier_sync(1, CWARPS * 32);
+        }
+        // Every consumer warp has finished this piece's tiles (or given up): the
+        // abort flag is final for the piece, and a piece of a CTA whose wait gave
+        // up is written as the marker (max -inf, sum -1) that the merge pass reports.
+        const bool bad = *(volatile int *)&sm.abort_flag != 0;
+        for (int idx = threadIdx.x; idx < hpc * D; idx += CWARPS * 32) {
+            const int h = idx / D, e = idx - h * D;
+            const size_t row = (size_t)pc.id * hpc + h;
+            if (bad) {
+                if (e == 0) {
+                    p.part_ml[row * 2] = -INFINITY;
+                    p.part_ml[row * 2 + 1] = -1.0f;
+                }
+                continue;
+            }
+            p.part_o[row * D + e] = sm.obuf[h][e];
+            if (e == 0) {
+                float M = -INFINITY;
+#pragma unroll
+                for (int ww = 0; ww < CWARPS; ww++)
+                    M = fmaxf(M, sm.merge_m[ww][h]);
+                float l = 0.f;
+#pragma unroll
+                for (int ww = 0; ww < CWARPS; ww++) {
+                    const float mw = sm.merge_m[ww][h];
+                    if (mw != -INFINITY)
+                        l += sm.merge_l[ww][h] * exp2f(mw - M);
+                }
+                p.part_ml[row * 2] = M;
+                p.part_ml[row * 2 + 1] = l;
+            }
+        }
+        if (threadIdx.x == 0) {  // the span follows from the slicing alone: always written
+            const int stream = pc.id - blockIdx.x;
+            if (pc.first)
+                p.piece_span[2 * stream] = pc.id;
+            if (pc.last)
+                p.piece_span[2 * stream + 1] = pc.id;
+        }
+        named_barrier_sync(1, CWARPS * 32);
+    }
+}
+
+template <int D, bool E4M3, bool CAPPED>
+cudaError_t launch_paged_split(const DecodeParams &p, const PagedView &pg, cudaStream_t stream)
+{
+    typedef PagedSmem<D, E4M3> Smem;
+    // K and V as 2-D tensors of cache rows ((page, kv head, slot) x D), read in
+    // boxes of a page's rows, or 64 of them, by 128 bytes (E4M3 with d = 64: 64).
+    CUtensorMap mk, mv;
+    const cuuint64_t rows = ((cuuint64_t)pg.num_pages * p.KV) << pg.page_log;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)Smem::ROW};
+    const cuuint32_t box[2] = {(cuuint32_t)(E4M3 ? Smem::BOX : Smem::BOX / 2),
+                               1u << (pg.page_log < 6 ? pg.page_log : 6)};
+    const bool ok = E4M3 ? make_u8_tile_map(&mk, p.cache_k, 2, dims, strides, box, true) &&
+                               make_u8_tile_map(&mv, p.cache_v, 2, dims, strides, box, true)
+                         : make_bf16_tile_map(&mk, p.cache_k, 2, dims, strides, box) &&
+                               make_bf16_tile_map(&mv, p.cache_v, 2, dims, strides, box);
+    if (!ok)
+        return cudaErrorInvalidValue;
+    const size_t smem = sizeof(Smem) + 1024;  // + alignment slack
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = once_per_device(configured, [smem] {
+        cudaError_t r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED>,
+                                     cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        return r;
+    });
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(decode_paged_kernel<D, E4M3, CAPPED>, dim3(p.grid), dim3(THREADS), smem,
+                         stream, p, pg, mk, mv);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_paged_t(const DecodeParams &p, const PagedView &pg, cudaStream_t stream)
+{
+    const cudaError_t e = p.cap_out > 0.f ? launch_paged_split<D, E4M3, true>(p, pg, stream)
+                                          : launch_paged_split<D, E4M3, false>(p, pg, stream);
+    return e != cudaSuccess ? e : launch_decode_combine(p, D, stream);
+}
+
+}  // namespace
+
+int decode_paged_ctas_per_sm() { return 2; }
+
+cudaError_t launch_decode_paged(const DecodeParams &p, const PagedView &pg, bool e4m3, int d,
+                                cudaStream_t stream)
+{
+    if (d == 128)
+        return e4m3 ? launch_paged_t<128, true>(p, pg, stream) : launch_paged_t<128, false>(p, pg, stream);
+    return e4m3 ? launch_paged_t<64, true>(p, pg, stream) : launch_paged_t<64, false>(p, pg, stream);
+}

@@ -144,6 +144,35 @@ int check_rope(const na_rope_params *r)
     return NA_OK;
 }
 
+// A paged cache's struct, checked; *e4m3 and the device view of it on success.
+int check_paged_cache(const na_attn_cfg *cfg, const na_paged_kv_cache *c, int batch, bool *e4m3,
+                      PagedView *view)
+{
+    if (!c || !c->k || !c->v || !c->page_table || c->num_pages <= 0 || c->pages_per_seq <= 0 ||
+        c->batch < batch)
+        return NA_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v))
+        return NA_ERR_INVALID_ARG;
+    if (c->dtype != NA_KV_BF16 && c->dtype != NA_KV_E4M3)
+        return NA_ERR_INVALID_ARG;
+    *e4m3 = c->dtype == NA_KV_E4M3;
+    if (*e4m3 && (!c->k_scale || !c->v_scale))
+        return NA_ERR_INVALID_ARG;
+    if (cfg->flags & NA_RING_CACHE)
+        return NA_ERR_UNSUPPORTED;
+    int log = 4;
+    while (log < 8 && c->page_size != 1 << log)
+        log++;
+    if (log == 8)
+        return NA_ERR_UNSUPPORTED;
+    // cache rows are addressed by 32-bit tensor-map coordinates, positions by int32
+    if ((long long)c->num_pages * cfg->num_kv_heads > (0x7fffffffLL >> log) ||
+        (long long)c->pages_per_seq > (0x7fffffffLL >> log))
+        return NA_ERR_UNSUPPORTED;
+    *view = PagedView{c->page_table, c->pages_per_seq, c->num_pages, log, c->k_scale, c->v_scale};
+    return NA_OK;
+}
+
 struct PrefillPlan {
     int pack, tile_tokens, q_tiles, full_units, tail_units, num_splits, split_len, grid;
     size_t ws_bytes;
@@ -225,7 +254,8 @@ struct DecodePlan {
 // cuts the concatenated key streams into one equal slice per CTA (at least
 // min_slice keys), so the workspace holds one partial row group per piece:
 // streams + grid pieces at most, whatever the lengths.
-DecodePlan plan_decode(const na_attn_cfg *c, int batch, int max_kv_len, int num_splits)
+DecodePlan plan_decode(const na_attn_cfg *c, int batch, int max_kv_len, int num_splits,
+                       bool paged = false)
 {
     DecodePlan pl{};
     const int tile = decode_key_tile();
@@ -233,18 +263,148 @@ DecodePlan plan_decode(const na_attn_cfg *c, int batch, int max_kv_len, int num_
     // query heads scored together (the MMA takes up to 8): each stream of
     // K/V is read once for them
     pl.heads_per_cta = (group % 8 == 0) ? 8 : (group % 4 == 0) ? 4 : ((group % 2 == 0) ? 2 : 1);
+    if (paged)  // any divisor of the group
+        for (pl.heads_per_cta = 8; group % pl.heads_per_cta != 0;)
+            pl.heads_per_cta--;
     const int len = max_kv_len > 0 ? max_kv_len : 1;
     int min_slice = num_splits > 0 ? (len + num_splits - 1) / num_splits : 4 * tile;
     if (min_slice < 1)
         min_slice = 1;
     pl.min_slice = min_slice;
-    pl.grid = decode_ctas_per_sm() * sm_count();
+    pl.grid = (paged ? decode_paged_ctas_per_sm() : decode_ctas_per_sm()) * sm_count();
     pl.streams = batch * c->num_kv_heads * (group / pl.heads_per_cta);
     pl.max_pieces = pl.streams + pl.grid;
     const size_t rows = (size_t)pl.max_pieces * pl.heads_per_cta;
     pl.ws_bytes = rows * (c->head_dim + 2) * 4 + (size_t)pl.streams * 2 * 4;
     pl.ws_bytes = (pl.ws_bytes + 15) / 16 * 16;
     return pl;
+}
+
+// The arguments that the contiguous and the paged append share, checked ahead
+// of the cache's ...
+int check_append(const na_attn_cfg *cfg, const na_rope_params *rope, int batch, int total_tokens)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if ((rc = check_rope(rope)) != NA_OK)
+        return rc;
+    return batch <= 0 || total_tokens < 0 ? NA_ERR_INVALID_ARG : NA_OK;
+}
+
+// ... and after it, with the kernel's parameters that do not depend on it.
+int fill_append(const na_attn_cfg *cfg, const na_rope_params *rope, int batch,
+                const int32_t *cu_seqlens, const int32_t *cache_lens, int total_tokens,
+                const void *q, const void *k, const void *v, const void *q_norm_w,
+                const void *k_norm_w, void *q_out, int32_t *status, RopeAppendParams *p)
+{
+    if (!cu_seqlens || !cache_lens || !q || !k || !v || !q_out)
+        return NA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out))
+        return NA_ERR_INVALID_ARG;
+    if ((cfg->flags & NA_QK_NORM) &&
+        (!q_norm_w || !k_norm_w || !aligned16(q_norm_w) || !aligned16(k_norm_w)))
+        return NA_ERR_INVALID_ARG;
+    if (rope_append_smem_bytes(cfg->num_heads, cfg->num_kv_heads, cfg->head_dim,
+                               cfg->rotary_dim) > 200 * 1024)
+        return NA_ERR_UNSUPPORTED;
+    p->H = cfg->num_heads;
+    p->KV = cfg->num_kv_heads;
+    p->d = cfg->head_dim;
+    p->rd = cfg->rotary_dim;
+    p->flags = cfg->flags;
+    p->eps = cfg->rms_eps;
+    p->rope_scale = (float)rope_attention_factor(rope);
+    p->batch = batch;
+    p->total_tokens = total_tokens;
+    p->cu_seqlens = cu_seqlens;
+    p->cache_lens = cache_lens;
+    p->q = static_cast<const bf16 *>(q);
+    p->k = static_cast<const bf16 *>(k);
+    p->v = static_cast<const bf16 *>(v);
+    p->qw = static_cast<const bf16 *>(q_norm_w);
+    p->kw = static_cast<const bf16 *>(k_norm_w);
+    p->q_out = static_cast<bf16 *>(q_out);
+    p->status = status;
+    return NA_OK;
+}
+
+// The decode kernels' parameters that do not depend on the cache.
+DecodeParams decode_params(const na_attn_cfg *cfg, const DecodePlan &pl, int batch,
+                           const void *q_rot, const int32_t *kv_lens, int max_kv_len,
+                           const void *gate, void *out, float *probs, int probs_stride,
+                           void *workspace, int32_t *status)
+{
+    DecodeParams p{};
+    p.H = cfg->num_heads;
+    p.KV = cfg->num_kv_heads;
+    p.group = p.H / p.KV;
+    p.batch = batch;
+    p.scale_log2 = score_scale_log2(cfg);
+    p.head_chunks = p.group / pl.heads_per_cta;
+    p.grid = pl.grid;
+    p.min_slice = pl.min_slice;
+    p.max_pieces = pl.max_pieces;
+    p.max_kv_len = max_kv_len;
+    p.flags = cfg->flags;
+    p.window = cfg->window;
+    if (cfg->softcap > 0.f) {  // scores are log2-domain: c tanh(s / c) -> tanh via 2^(2 s / c)
+        p.cap_in = 2.0f / cfg->softcap;
+        p.cap_out = cfg->softcap * 1.4426950408889634f;
+    }
+    p.q = static_cast<const bf16 *>(q_rot);
+    p.gate = (cfg->flags & NA_OUT_GATE) ? static_cast<const bf16 *>(gate) : nullptr;
+    p.kv_lens = kv_lens;
+    p.out = static_cast<bf16 *>(out);
+    p.probs = probs;
+    p.probs_stride = probs ? probs_stride : 0;
+    p.part_o = static_cast<float *>(workspace);
+    const size_t rows = (size_t)pl.max_pieces * pl.heads_per_cta;
+    p.part_ml = p.part_o + rows * cfg->head_dim;
+    p.piece_span = reinterpret_cast<int32_t *>(p.part_ml + rows * 2);
+    p.status = status;
+    return p;
+}
+
+// The prefill kernels' parameters that do not depend on the cache.
+PrefillParams prefill_params(const na_attn_cfg *cfg, const PrefillPlan &pl, int batch,
+                             const int32_t *cu_seqlens, const int32_t *cache_lens,
+                             int total_tokens, int max_new_len, int max_total_len,
+                             const void *q_rot, const void *gate, void *out, void *workspace,
+                             int32_t *status)
+{
+    PrefillParams p{};
+    p.H = cfg->num_heads;
+    p.KV = cfg->num_kv_heads;
+    p.group = p.H / p.KV;
+    p.batch = batch;
+    p.scale_log2 = score_scale_log2(cfg);
+    p.max_new_len = max_new_len;
+    p.max_total_len = max_total_len;
+    p.total_tokens = total_tokens;
+    p.softcap = cfg->softcap;
+    p.window = cfg->window;
+    p.pack = pl.pack;
+    p.tile_tokens = pl.tile_tokens;
+    p.q_tiles = pl.q_tiles;
+    p.HG = p.H / pl.pack;
+    p.kv_read_once = (pl.q_tiles == 1 && p.HG == p.KV) ? 1 : 0;
+    p.full_units = pl.full_units;
+    p.tail_units = pl.tail_units;
+    p.split_len = pl.split_len;
+    p.num_splits = pl.num_splits;
+    p.flags = cfg->flags;
+    p.cu_seqlens = cu_seqlens;
+    p.cache_lens = cache_lens;
+    p.q = static_cast<const bf16 *>(q_rot);
+    p.gate = (cfg->flags & NA_OUT_GATE) ? static_cast<const bf16 *>(gate) : nullptr;
+    p.out = static_cast<bf16 *>(out);
+    if (pl.ws_bytes > 0) {
+        p.part_o = static_cast<float *>(workspace);
+        p.part_ml = p.part_o + (size_t)pl.tail_units * pl.num_splits * prefill_q_tile() * cfg->head_dim;
+    }
+    p.status = status;
+    return p;
 }
 
 }  // namespace
@@ -261,6 +421,7 @@ const char *na_status_string(int status)
     case NA_ERR_WORKSPACE: return "workspace missing or too small";
     case NA_ERR_CUDA: return "CUDA runtime error";
     case NA_ERR_DEVICE_TIMEOUT: return "device wait timed out";
+    case NA_ERR_PAGE: return "page index outside the paged cache";
     default: return "unknown status";
     }
 }
@@ -271,54 +432,56 @@ int na_rope_append_kv(const na_attn_cfg *cfg, const na_rope_params *rope, int32_
                       const void *k_norm_w, void *q_out, const na_kv_cache *cache, int32_t *status,
                       void *stream)
 {
-    int rc = check_cfg(cfg);
+    int rc = check_append(cfg, rope, batch, total_tokens);
     if (rc != NA_OK)
         return rc;
-    if ((rc = check_rope(rope)) != NA_OK)
-        return rc;
-    if (batch <= 0 || total_tokens < 0)
-        return NA_ERR_INVALID_ARG;
     if ((rc = check_cache(cache, batch)) != NA_OK)
         return rc;
     if (total_tokens == 0)
         return NA_OK;
-    if (!cu_seqlens || !cache_lens || !q || !k || !v || !q_out)
-        return NA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out))
-        return NA_ERR_INVALID_ARG;
-    if ((cfg->flags & NA_QK_NORM) &&
-        (!q_norm_w || !k_norm_w || !aligned16(q_norm_w) || !aligned16(k_norm_w)))
-        return NA_ERR_INVALID_ARG;
-    if (rope_append_smem_bytes(cfg->num_heads, cfg->num_kv_heads, cfg->head_dim,
-                               cfg->rotary_dim) > 200 * 1024)
-        return NA_ERR_UNSUPPORTED;
-
+    RopeAppendParams p{};
+    if ((rc = fill_append(cfg, rope, batch, cu_seqlens, cache_lens, total_tokens, q, k, v, q_norm_w,
+                          k_norm_w, q_out, status, &p)) != NA_OK)
+        return rc;
     double inv_freq[64];
     rope_frequencies(rope, cfg->rotary_dim, inv_freq);
-    RopeAppendParams p{};
-    p.H = cfg->num_heads;
-    p.KV = cfg->num_kv_heads;
-    p.d = cfg->head_dim;
-    p.rd = cfg->rotary_dim;
-    p.flags = cfg->flags;
-    p.eps = cfg->rms_eps;
-    p.rope_scale = (float)rope_attention_factor(rope);
-    p.batch = batch;
     p.capacity = cache->capacity;
-    p.total_tokens = total_tokens;
-    p.cu_seqlens = cu_seqlens;
-    p.cache_lens = cache_lens;
-    p.q = static_cast<const bf16 *>(q);
-    p.k = static_cast<const bf16 *>(k);
-    p.v = static_cast<const bf16 *>(v);
-    p.qw = static_cast<const bf16 *>(q_norm_w);
-    p.kw = static_cast<const bf16 *>(k_norm_w);
-    p.q_out = static_cast<bf16 *>(q_out);
     p.cache_k = static_cast<bf16 *>(cache->k);
     p.cache_v = static_cast<bf16 *>(cache->v);
-    p.status = status;
     return launch_rope_append(p, inv_freq, cfg->rotary_dim / 2,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? NA_OK
+               : NA_ERR_CUDA;
+}
+
+int na_rope_append_kv_paged(const na_attn_cfg *cfg, const na_rope_params *rope, int32_t batch,
+                            const int32_t *cu_seqlens, const int32_t *cache_lens,
+                            int32_t total_tokens, const void *q, const void *k, const void *v,
+                            const void *q_norm_w, const void *k_norm_w, void *q_out,
+                            const na_paged_kv_cache *cache, int32_t *status, void *stream)
+{
+    int rc = check_append(cfg, rope, batch, total_tokens);
+    if (rc != NA_OK)
+        return rc;
+    bool e4m3;
+    PagedView pg;
+    if ((rc = check_paged_cache(cfg, cache, batch, &e4m3, &pg)) != NA_OK)
+        return rc;
+    if (total_tokens == 0)
+        return NA_OK;
+    RopeAppendParams p{};
+    if ((rc = fill_append(cfg, rope, batch, cu_seqlens, cache_lens, total_tokens, q, k, v, q_norm_w,
+                          k_norm_w, q_out, status, &p)) != NA_OK)
+        return rc;
+    if (e4m3 && cfg->num_kv_heads > 65535)  // one grid row per kv head
+        return NA_ERR_UNSUPPORTED;
+    double inv_freq[64];
+    rope_frequencies(rope, cfg->rotary_dim, inv_freq);
+    p.capacity = cache->pages_per_seq * cache->page_size;
+    p.cache_k = static_cast<bf16 *>(cache->k);
+    p.cache_v = static_cast<bf16 *>(cache->v);
+    return launch_rope_append_paged(p, pg, e4m3, inv_freq, cfg->rotary_dim / 2,
+                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? NA_OK
                : NA_ERR_CUDA;
 }
@@ -374,45 +537,62 @@ int na_attn_prefill_chunk(const na_attn_cfg *cfg, int32_t batch, const int32_t *
     if (pl.ws_bytes > 0 && (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace)))
         return NA_ERR_WORKSPACE;
 
-    PrefillParams p{};
-    p.H = cfg->num_heads;
-    p.KV = cfg->num_kv_heads;
-    p.group = p.H / p.KV;
-    p.batch = batch;
+    PrefillParams p = prefill_params(cfg, pl, batch, cu_seqlens, cache_lens, total_tokens,
+                                     max_new_len, max_total_len, q_rot, gate, out, workspace,
+                                     status);
     p.capacity = cache->capacity;
-    p.scale_log2 = score_scale_log2(cfg);
-    p.max_new_len = max_new_len;
-    p.max_total_len = max_total_len;
-    p.total_tokens = total_tokens;
-    p.softcap = cfg->softcap;
-    p.window = cfg->window;
-    p.pack = pl.pack;
-    p.tile_tokens = pl.tile_tokens;
-    p.q_tiles = pl.q_tiles;
-    p.HG = p.H / pl.pack;
-    p.kv_read_once = (pl.q_tiles == 1 && p.HG == p.KV) ? 1 : 0;
-    p.full_units = pl.full_units;
-    p.tail_units = pl.tail_units;
-    p.split_len = pl.split_len;
-    p.num_splits = pl.num_splits;
-    p.flags = cfg->flags;
-    p.cu_seqlens = cu_seqlens;
-    p.cache_lens = cache_lens;
-    p.q = static_cast<const bf16 *>(q_rot);
     p.cache_k = static_cast<const bf16 *>(cache->k);
     p.cache_v = static_cast<const bf16 *>(cache->v);
-    p.gate = gated ? static_cast<const bf16 *>(gate) : nullptr;
-    p.out = static_cast<bf16 *>(out);
-    if (pl.ws_bytes > 0) {
-        p.part_o = static_cast<float *>(workspace);
-        p.part_ml = p.part_o + (size_t)pl.tail_units * pl.num_splits * prefill_q_tile() * cfg->head_dim;
-    }
-    p.status = status;
     if ((rc = bind_context()) != NA_OK)
         return rc;
     return launch_prefill(p, cfg->head_dim, total_tokens, cache->batch,
                           static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
+               ? NA_OK
+               : NA_ERR_CUDA;
+}
+
+int na_attn_prefill_chunk_paged(const na_attn_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
+                                const int32_t *cache_lens, int32_t total_tokens,
+                                int32_t max_new_len, int32_t max_total_len, const void *q_rot,
+                                const na_paged_kv_cache *cache, const void *gate, void *out,
+                                void *workspace, size_t ws_bytes, int32_t *status, void *stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if (batch <= 0 || total_tokens < 0 || max_new_len < 0 || max_total_len < 0)
+        return NA_ERR_INVALID_ARG;
+    bool e4m3;
+    PagedView pg;
+    if ((rc = check_paged_cache(cfg, cache, batch, &e4m3, &pg)) != NA_OK)
+        return rc;
+    if (total_tokens == 0)
+        return NA_OK;
+    if (!cu_seqlens || !cache_lens || !q_rot || !out || max_new_len <= 0)
+        return NA_ERR_INVALID_ARG;
+    const int capacity = cache->pages_per_seq * cache->page_size;
+    if (max_total_len > capacity)
+        return NA_ERR_CAPACITY;
+    if ((long long)total_tokens * cfg->num_heads * cfg->head_dim >= (1ll << 40))
+        return NA_ERR_UNSUPPORTED;  // tile coordinates are 32-bit
+    if (!aligned16(q_rot) || !aligned16(out))
+        return NA_ERR_INVALID_ARG;
+    if ((cfg->flags & NA_OUT_GATE) && (!gate || !aligned16(gate)))
+        return NA_ERR_INVALID_ARG;
+    const PrefillPlan pl = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len);
+    if (pl.ws_bytes > 0 && (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace)))
+        return NA_ERR_WORKSPACE;
+    PrefillParams p = prefill_params(cfg, pl, batch, cu_seqlens, cache_lens, total_tokens,
+                                     max_new_len, max_total_len, q_rot, gate, out, workspace,
+                                     status);
+    p.capacity = capacity;
+    p.cache_k = static_cast<const bf16 *>(cache->k);
+    p.cache_v = static_cast<const bf16 *>(cache->v);
+    if ((rc = bind_context()) != NA_OK)
+        return rc;
+    return launch_prefill_paged(p, pg, e4m3, cfg->head_dim, total_tokens,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? NA_OK
                : NA_ERR_CUDA;
 }
@@ -490,41 +670,66 @@ int na_attn_decode(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
     if (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace))
         return NA_ERR_WORKSPACE;
 
-    DecodeParams p{};
-    p.H = cfg->num_heads;
-    p.KV = cfg->num_kv_heads;
-    p.group = p.H / p.KV;
-    p.batch = batch;
+    DecodeParams p = decode_params(cfg, pl, batch, q_rot, kv_lens, max_kv_len, gate, out, probs,
+                                   probs_stride, workspace, status);
     p.capacity = cache->capacity;
     p.cache_batch = cache->batch;
-    p.scale_log2 = score_scale_log2(cfg);
-    p.head_chunks = p.group / pl.heads_per_cta;
-    p.grid = pl.grid;
-    p.min_slice = pl.min_slice;
-    p.max_pieces = pl.max_pieces;
-    p.max_kv_len = max_kv_len;
-    p.flags = cfg->flags;
-    p.window = cfg->window;
-    if (cfg->softcap > 0.f) {  // scores are log2-domain: c tanh(s / c) -> tanh via 2^(2 s / c)
-        p.cap_in = 2.0f / cfg->softcap;
-        p.cap_out = cfg->softcap * 1.4426950408889634f;
-    }
-    p.q = static_cast<const bf16 *>(q_rot);
     p.cache_k = static_cast<const bf16 *>(cache->k);
     p.cache_v = static_cast<const bf16 *>(cache->v);
-    p.gate = gated ? static_cast<const bf16 *>(gate) : nullptr;
-    p.kv_lens = kv_lens;
-    p.out = static_cast<bf16 *>(out);
-    p.probs = probs;
-    p.probs_stride = probs ? probs_stride : 0;
-    p.part_o = static_cast<float *>(workspace);
-    const size_t rows = (size_t)pl.max_pieces * pl.heads_per_cta;
-    p.part_ml = p.part_o + rows * cfg->head_dim;
-    p.piece_span = reinterpret_cast<int32_t *>(p.part_ml + rows * 2);
-    p.status = status;
     if ((rc = bind_context()) != NA_OK)
         return rc;
     return launch_decode(p, cfg->head_dim, pl.heads_per_cta, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? NA_OK
+               : NA_ERR_CUDA;
+}
+
+int na_decode_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_kv_len,
+                                   int32_t num_splits, size_t *bytes)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if (!bytes || batch <= 0 || max_kv_len < 0 || num_splits < 0)
+        return NA_ERR_INVALID_ARG;
+    *bytes = plan_decode(cfg, batch, max_kv_len, num_splits, true).ws_bytes;
+    return NA_OK;
+}
+
+int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
+                         const na_paged_kv_cache *cache, const int32_t *kv_lens,
+                         int32_t max_kv_len, const void *gate, void *out, float *probs,
+                         int32_t probs_stride, int32_t num_splits, void *workspace,
+                         size_t ws_bytes, int32_t *status, void *stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if (batch <= 0 || max_kv_len < 0 || num_splits < 0)
+        return NA_ERR_INVALID_ARG;
+    bool e4m3;
+    PagedView pg;
+    if ((rc = check_paged_cache(cfg, cache, batch, &e4m3, &pg)) != NA_OK)
+        return rc;
+    if (!q_rot || !kv_lens || !out || !aligned16(q_rot) || !aligned16(out))
+        return NA_ERR_INVALID_ARG;
+    const int capacity = cache->pages_per_seq * cache->page_size;
+    if (max_kv_len > capacity || (probs && probs_stride < max_kv_len))
+        return NA_ERR_CAPACITY;
+    if ((cfg->flags & NA_OUT_GATE) && !gate)
+        return NA_ERR_INVALID_ARG;
+    const DecodePlan pl = plan_decode(cfg, batch, max_kv_len, num_splits, true);
+    if (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace))
+        return NA_ERR_WORKSPACE;
+    DecodeParams p = decode_params(cfg, pl, batch, q_rot, kv_lens, max_kv_len, gate, out, probs,
+                                   probs_stride, workspace, status);
+    p.capacity = capacity;
+    p.cache_batch = cache->batch;
+    p.cache_k = static_cast<const bf16 *>(cache->k);
+    p.cache_v = static_cast<const bf16 *>(cache->v);
+    if ((rc = bind_context()) != NA_OK)
+        return rc;
+    return launch_decode_paged(p, pg, e4m3, cfg->head_dim, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? NA_OK
                : NA_ERR_CUDA;

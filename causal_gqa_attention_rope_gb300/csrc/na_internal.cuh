@@ -56,6 +56,38 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float *f)
     return u;
 }
 
+// ------------------------------------------------------------- E4M3, E8M0 --
+
+// 2^(s - 127), the value of an E8M0 byte (255, its NaN, gives infinity).
+__device__ __forceinline__ float e8m0_value(uint32_t s)
+{
+    return __uint_as_float(s ? s << 23 : 0x00400000u);
+}
+
+// Four E4M3 values (the bytes of w) as bf16 pairs: `even` holds bytes 0 and 2,
+// `odd` bytes 1 and 3.  An E4M3 magnitude moved into the low exponent and high
+// fraction bits of a bf16 reads as the value times 2^-120 (subnormals
+// included: both formats drop the implicit bit at exponent field 0); `mul`
+// brings it back, exactly, together with any power-of-two scale folded into
+// it.  NaN bytes (0x7f, 0xff) read as +-480.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+constexpr uint32_t kE4m3Unbias = 0x7b807b80u;  // 2^120, twice
+
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t mul, uint32_t &even,
+                                               uint32_t &odd)
+{
+    const uint32_t e = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+    const uint32_t o = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+    even = mul_bf16x2(e, mul);
+    odd = mul_bf16x2(o, mul);
+}
+
 // ------------------------------------------------------ shared-memory sync --
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)
@@ -225,6 +257,21 @@ struct RopeAppendParams {
     int32_t *status;
 };
 
+// inv_freq[i] / (2 pi) in turns per position, as the 96-bit fixed-point
+// fraction hi * 2^-64 + lo * 2^-96.
+struct RopeTurns {
+    unsigned long long hi[64];  // rd / 2 <= 64 (head_dim <= 128)
+    unsigned int lo[64];
+};
+
+// A paged cache as the kernels see it (na_paged_kv_cache).
+struct PagedView {
+    const int32_t *table;      // [batch][pages_per_seq]
+    int pages_per_seq, num_pages;
+    int page_log;              // log2 of the page size, 4 .. 7
+    const uint8_t *k_scale, *v_scale;  // E8M0 [num_pages][KV] with E4M3 pages
+};
+
 struct DecodeParams {
     int H, KV, group, batch, capacity;
     int cache_batch;           // sequences the cache holds (rows of the tensor maps)
@@ -288,12 +335,22 @@ struct ImportanceParams {
 // Kernel launchers (one translation unit each).
 cudaError_t launch_rope_append(const RopeAppendParams &p, const double *inv_freq, int half,
                                cudaStream_t stream);
+cudaError_t launch_rope_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
+                                     const double *inv_freq, int half, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams &p, int d, int heads_per_cta, cudaStream_t stream);
+cudaError_t launch_decode_paged(const DecodeParams &p, const PagedView &pg, bool e4m3, int d,
+                                cudaStream_t stream);
+cudaError_t launch_decode_combine(const DecodeParams &p, int d, cudaStream_t stream);
 cudaError_t launch_importance(const ImportanceParams &p, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillParams &p, int d, int total_tokens, int cache_batch,
                            cudaStream_t stream);
+cudaError_t launch_kv_append_e4m3(const RopeAppendParams &p, const PagedView &pg,
+                                  const RopeTurns &turns, cudaStream_t stream);
+cudaError_t launch_prefill_paged(const PrefillParams &p, const PagedView &pg, bool e4m3, int d,
+                                 int total_tokens, cudaStream_t stream);
 size_t rope_append_smem_bytes(int H, int KV, int d, int rd);
 int decode_key_tile();
 int decode_ctas_per_sm();
+int decode_paged_ctas_per_sm();
 int prefill_key_tile();
 int prefill_q_tile();

@@ -33,6 +33,15 @@
 // With three S buffers the tensor core computes S_{j+1} and S_{j+2} while the
 // softmax works on tile j, and PV_j runs while it prepares P_{j+1}.
 //
+// A paged cache (na_attn_prefill_chunk_paged) differs in how a K or V tile gets
+// there.  bf16 pages: the producer warp keeps the page ids of the next 64 pages
+// in registers, one per lane and batch, and each lane issues one box (a page's
+// rows by 64 columns) straight into the tile.  E4M3 pages: the boxes land as
+// bytes in a raw ring, and four more warps (8-11) turn them into the same
+// swizzled bf16 tile, the page's power-of-two scale multiplied in -- every
+// dequantised value is a bf16 number, so the tensor cores see exactly the cache
+// that the bytes stand for, and the rest of the kernel is unchanged.
+//
 #include <climits>
 #include <cuda.h>
 #include <mutex>
@@ -44,31 +53,44 @@ namespace {
 
 constexpr int BM = 128;      // query rows per CTA (tensor-memory lanes)
 constexpr int BN = 128;      // keys per tile
-constexpr int STAGES = 3;    // K/V shared-memory ring depth
+constexpr int STAGES = 3;    // K/V shared-memory ring depth (bf16 caches)
 constexpr int NUM_S = 3;     // S/P buffers in tensor memory
 constexpr int THREADS = 256; // 8 warps: producer, S issuer, PV issuer, idle, 4 softmax
+constexpr int E4M3_THREADS = THREADS + 128;  // and 4 that convert E4M3 tiles
+constexpr int E4M3_STAGES = 2;  // bf16 K/V ring depth behind a raw ring ...
+constexpr int RAW_STAGES = 4;   // ... of this many K or V tiles in bytes
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL0 = 128;  // S buffer i at columns 128 (i + 1); O at column 0
 
-template <int D>
+// Where K and V come from.
+enum KvSource { KV_CONTIGUOUS, KV_PAGED, KV_PAGED_E4M3 };
+
+template <int D, KvSource SRC>
 struct __align__(1024) TcSmem {
     static constexpr int KB = D / 64;  // 64-wide column blocks of a row
+    static constexpr int ST = SRC == KV_PAGED_E4M3 ? E4M3_STAGES : STAGES;
+    static constexpr int RAW = SRC == KV_PAGED_E4M3 ? RAW_STAGES : 1;
+    static constexpr uint32_t RAW_BYTES = SRC == KV_PAGED_E4M3 ? BN * D : 16;
     bf16 q[KB][BM * 64];
-    bf16 k[STAGES][KB][BN * 64];
-    bf16 v[STAGES][KB][BN * 64];
+    bf16 k[ST][KB][BN * 64];
+    bf16 v[ST][KB][BN * 64];
+    uint8_t raw[RAW][RAW_BYTES];    // E4M3 tiles as they come, rows of D bytes
+    uint8_t raw_scale[RAW][8];      // E8M0 byte of each 16 keys of a raw tile
+    uint64_t raw_full[RAW], raw_empty[RAW];
     uint64_t q_full;
-    uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
+    uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST];
     uint64_t s_full[NUM_S], s_free[NUM_S], p_full[NUM_S];
     uint64_t o_done[NUM_S], drain[2];  // o_done[b]: the PVs of tiles b, b + NUM_S, ...
     uint32_t tmem_base;
     int abort_flag;
 };
 
-template <int D>
+template <int D, KvSource SRC>
 constexpr size_t tc_smem_bytes()
 {
     // at least ~116 KB so that a single CTA owns the SM (and its tensor memory)
-    return (sizeof(TcSmem<D>) + 1024) > (116u << 10) ? sizeof(TcSmem<D>) + 1024 : (116u << 10);
+    return (sizeof(TcSmem<D, SRC>) + 1024) > (116u << 10) ? sizeof(TcSmem<D, SRC>) + 1024
+                                                          : (116u << 10);
 }
 
 __device__ __forceinline__ bool aborted(const int *flag) { return *(volatile const int *)flag != 0; }
@@ -112,16 +134,81 @@ __device__ __forceinline__ float ex2_mufu(float x)
     return r;
 }
 
-template <int D, bool CAPPED>
-__global__ void __launch_bounds__(THREADS, 1)
-    prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap map_q,
+// Two E4M3 bytes of w (those that `sel` puts into the high bytes of its halves)
+// as a bf16 pair, times the powers of two in `mul`.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t w, uint32_t sel, uint32_t mul)
+{
+    const uint32_t x = __byte_perm(w, 0u, sel);
+    return mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), mul);
+}
+
+// A raw E4M3 tile (BN rows of D bytes) into a 128-byte-swizzled bf16 tile, by
+// the four converting warps; `w` is the warp's index among them.  A thread
+// turns 16 bytes into two 16-byte chunks at a time.  With D = 128 the lanes of
+// the right half of a row write their two chunks in the other order, so that
+// eight consecutive lanes always cover all eight bank groups.
+template <int D>
+__device__ __forceinline__ void convert_tile(const uint8_t *raw, const uint8_t *scale, bf16 *tile,
+                                             int w, int lane)
+{
+    constexpr int CPR = D / 16;            // 16-byte chunks per raw row
+    constexpr int RPI = 32 / CPR;          // rows per warp instruction
+    constexpr int ITERS = BN / 4 / RPI;    // a warp takes 32 consecutive rows
+    const int ch = lane % CPR;
+    const bool swap = D == 128 && ch >= 4;
+    uint8_t *out = reinterpret_cast<uint8_t *>(tile) + (ch / 4) * (BN * 128);
+    const int c0 = 2 * (ch % 4) + (swap ? 1 : 0);
+#pragma unroll
+    for (int half = 0; half < 2; half++) {  // 16 rows share a page
+        // 2^120 undoes the bias of the byte trick (na_internal.cuh); a scale above
+        // 2^7 takes a second factor
+        const int e = 120 + (int)scale[2 * w + half] - 127;
+        const int e1 = min(e, 127);
+        const uint32_t m1 = (uint32_t)(e1 + 127) << 7, mul = m1 | (m1 << 16);
+        const uint32_t m2 = (uint32_t)(e - e1 + 127) << 7, mul2 = m2 | (m2 << 16);
+        uint4 u[ITERS / 2];
+#pragma unroll
+        for (int i = 0; i < ITERS / 2; i++) {
+            const int r = w * 32 + half * 16 + i * RPI + lane / CPR;
+            u[i] = *reinterpret_cast<const uint4 *>(raw + r * D + ch * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < ITERS / 2; i++) {
+            const int r = w * 32 + half * 16 + i * RPI + lane / CPR;
+            uint32_t o[8];
+            const uint32_t in[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                o[2 * q] = e4m3x2_to_bf16(in[q], 0x1404, mul);
+                o[2 * q + 1] = e4m3x2_to_bf16(in[q], 0x3424, mul);
+            }
+            if (e > 127) {
+#pragma unroll
+                for (int q = 0; q < 8; q++)
+                    o[q] = mul_bf16x2(o[q], mul2);
+            }
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            uint8_t *row = out + r * 128;
+            *reinterpret_cast<uint4 *>(row + ((c0 ^ (r & 7)) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4 *>(row + (((c0 ^ 1) ^ (r & 7)) << 4)) = swap ? lo : hi;
+        }
+    }
+}
+
+template <int D, bool CAPPED, KvSource SRC>
+__global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS, 1)
+    prefill_tc_kernel(const PrefillParams p, const PagedView pg,
+                      const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v)
 {
+    typedef TcSmem<D, SRC> Smem;
     constexpr int KB = D / 64;
+    constexpr int STAGES = Smem::ST;
+    constexpr bool PAGED = SRC != KV_CONTIGUOUS, E4M3 = SRC == KV_PAGED_E4M3;
     extern __shared__ uint8_t smem_raw[];
-    TcSmem<D> &sm = *reinterpret_cast<TcSmem<D> *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~uintptr_t(1023));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Prologue that reads no global memory: descriptor prefetch, barriers and
@@ -131,11 +218,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
         mbar_init(&sm.q_full, 1);
-        for (int s = 0; s < STAGES; s++) {
-            mbar_init(&sm.k_full[s], 1);
-            mbar_init(&sm.v_full[s], 1);
+        for (int s = 0; s < STAGES; s++) {  // filled by copies, or by the converting warps
+            mbar_init(&sm.k_full[s], E4M3 ? 4 : 1);
+            mbar_init(&sm.v_full[s], E4M3 ? 4 : 1);
             mbar_init(&sm.k_empty[s], 1);
             mbar_init(&sm.v_empty[s], 1);
+        }
+        for (int s = 0; E4M3 && s < Smem::RAW; s++) {
+            mbar_init(&sm.raw_full[s], 1);
+            mbar_init(&sm.raw_empty[s], 4);
         }
         for (int s = 0; s < NUM_S; s++) {
             mbar_init(&sm.s_full[s], 1);
@@ -165,7 +256,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // sequence any tile below the host-known token count -- takes the tensor
     // memory before the wait and issues its first copies speculatively.
     // Other tiles may be empty padding; they check first and leave at once.
-    const bool eager = p.batch == 1 && p.window == 0 && qt * p.tile_tokens < p.total_tokens;
+    const bool eager = !PAGED && p.batch == 1 && p.window == 0 &&
+                       qt * p.tile_tokens < p.total_tokens;
     if (eager && warp == 1)
         tc::tmem_alloc(&sm.tmem_base, TMEM_COLS);
     grid_dependency_wait();
@@ -293,7 +385,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!eager && warp == 1)
         tc::tmem_alloc(&sm.tmem_base, TMEM_COLS);
     const int n_tiles = (k_end - k_begin + BN - 1) / BN;
-    const int pre = n_tiles < STAGES ? n_tiles : STAGES;  // tiles loaded before the barrier
+    // tiles loaded before the barrier (pages: none, their ids come first)
+    const int pre = PAGED ? 0 : (n_tiles < STAGES ? n_tiles : STAGES);
+    // first key that any row sees: pages before it may be gone
+    const int vis_lo = p.window > 0 ? max(k_begin, pos_lo - p.window + 1) : k_begin;
 
     if (threadIdx.x == 0) {
         // The Q tile (unless already issued) and the remaining first ring
@@ -358,7 +453,126 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp < 4 && gated_out)
         load_gate();
 
-    if (warp == 0) {
+    if (PAGED && warp == 0) {
+        // ------------------------------------------------ producer, pages --
+        // K tile j is item i = 2 j - 1 (0 for j = 0), V tile j item 2 j + 2 in the
+        // E4M3 raw ring (K runs a tile ahead of V), the last V tile closing it.
+        const int page_log = pg.page_log, nbox = BN >> page_log;  // 8 .. 1 boxes of rows per tile
+        constexpr int COLS = E4M3 ? 1 : KB;
+        constexpr uint32_t BOX_ROW = E4M3 ? D : 128;
+        const int bi = lane & (nbox - 1), bc = lane / nbox;  // this lane's box: rows, columns
+        const int p_lo = vis_lo >> page_log, p_hi = (k_end - 1) >> page_log;
+        const int32_t *row = pg.table + (size_t)b * pg.pages_per_seq;
+        struct Entry {
+            int id;
+            uint32_t scales;  // K's byte | V's byte << 8
+        };
+        auto entry = [&](int i) {
+            Entry e{-1, 0x7f7fu};
+            if (i >= p_lo && i <= p_hi) {
+                e.id = __ldcg(row + i);
+                if ((unsigned)e.id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
+                    na_report(p.status, NA_ERR_PAGE);
+                    e.id = 0;
+                }
+                if constexpr (E4M3) {
+                    const size_t at = (size_t)e.id * p.KV + kvh;
+                    e.scales = (uint32_t)__ldcg(pg.k_scale + at) |
+                               ((uint32_t)__ldcg(pg.v_scale + at) << 8);
+                }
+            }
+            return e;
+        };
+        // Page windows of 32 entries; K may be a tile ahead of V, so the window
+        // before the current one is kept too.
+        int wb = k_begin >> page_log;
+        Entry old{-1, 0x7f7fu}, cur = entry(wb + lane), nxt = entry(wb + 32 + lane);
+        bool ok = true;
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+            const bool got = mbar_wait_bounded(bar, parity) && !aborted(&sm.abort_flag);
+            if (!__all_sync(0xffffffffu, got)) {
+                if (lane == 0)
+                    set_abort(&sm.abort_flag, p.status);
+                return false;
+            }
+            return true;
+        };
+        // One tile (of K: is_v 0, of V: 1) as boxes into dst, completing on bar.
+        auto load_tile = [&](int j, int is_v, uint8_t *dst, uint64_t *bar, uint8_t *scale) {
+            const int j0 = k_begin + j * BN;
+            if ((j0 >> page_log) - wb >= 32) {
+                old = cur;
+                cur = nxt;
+                wb += 32;
+                nxt = entry(wb + 32 + lane);
+            }
+            const int pos = j0 + (bi << page_log);
+            const int at = (pos >> page_log) - wb;  // negative: the window before
+            const int from = at & 31;
+            const int id_old = __shfl_sync(0xffffffffu, old.id, from);
+            const int id_cur = __shfl_sync(0xffffffffu, cur.id, from);
+            const int id = at < 0 ? id_old : id_cur;
+            const bool mine = bc < COLS && id >= 0;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+            if constexpr (E4M3) {
+                const int a16 = ((j0 + 16 * (lane & 7)) >> page_log) - wb;
+                const uint32_t s_old = __shfl_sync(0xffffffffu, old.scales, a16 & 31);
+                const uint32_t s_cur = __shfl_sync(0xffffffffu, cur.scales, a16 & 31);
+                const uint32_t sc = a16 < 0 ? s_old : s_cur;
+                if (lane < 8)
+                    scale[lane] = (uint8_t)(is_v ? sc >> 8 : sc);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, n * (BOX_ROW << page_log));
+            __syncwarp();
+            if (mine)
+                load_kv(dst + bc * (BN * 128) + (bi << page_log) * BOX_ROW, is_v ? &map_v : &map_k,
+                        bc * 64, (id * p.KV + kvh) << page_log, bar);
+        };
+        if constexpr (E4M3) {
+            const int items = 2 * n_tiles;
+            int issued = 0;
+            for (int i = 0; ok && i < items; i++) {
+                const int is_v = i == items - 1 ? 1 : (i >= 2 && (i & 1) == 0);
+                const int j = is_v ? (i == items - 1 ? n_tiles - 1 : i / 2 - 1) : (i + 1) / 2;
+                const int rs = i % RAW_STAGES;
+                ok = wait_all(&sm.raw_empty[rs], ((i / RAW_STAGES) & 1) ^ 1);
+                if (ok) {
+                    load_tile(j, is_v, sm.raw[rs], &sm.raw_full[rs], sm.raw_scale[rs]);
+                    issued = i + 1;
+                }
+            }
+            if (lane == 0) {
+                drain_wait(&sm.q_full, 0, p.status);
+                for (int i = issued - 1; i >= 0 && i >= issued - RAW_STAGES; i--)
+                    drain_wait(&sm.raw_full[i % RAW_STAGES], (i / RAW_STAGES) & 1, p.status);
+            }
+        } else {
+            int k_issued = 0, v_issued = 0;
+            for (int j = 0; ok && j < n_tiles; j++) {
+                const int st = j % STAGES;
+                const uint32_t par = ((j / STAGES) & 1) ^ 1;
+                ok = wait_all(&sm.k_empty[st], par);
+                if (!ok)
+                    break;
+                load_tile(j, 0, reinterpret_cast<uint8_t *>(sm.k[st]), &sm.k_full[st], nullptr);
+                k_issued = j + 1;
+                ok = wait_all(&sm.v_empty[st], par);
+                if (!ok)
+                    break;
+                load_tile(j, 1, reinterpret_cast<uint8_t *>(sm.v[st]), &sm.v_full[st], nullptr);
+                v_issued = j + 1;
+            }
+            if (lane == 0) {
+                drain_wait(&sm.q_full, 0, p.status);
+                for (int j = k_issued - 1; j >= 0 && j >= k_issued - STAGES; j--)
+                    drain_wait(&sm.k_full[j % STAGES], (j / STAGES) & 1, p.status);
+                for (int j = v_issued - 1; j >= 0 && j >= v_issued - STAGES; j--)
+                    drain_wait(&sm.v_full[j % STAGES], (j / STAGES) & 1, p.status);
+            }
+        }
+    } else if (warp == 0) {
         // ------------------------------------------------------ producer --
         if (lane == 0) {
             int issued = pre;
@@ -460,6 +674,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                 drain_wait(&sm.drain[1], 0, p.status);
             }
         }
+    } else if (E4M3 && warp >= 8) {
+        // --------------------------------------- E4M3 tiles to bf16 tiles --
+        if constexpr (E4M3) {
+            const int items = 2 * n_tiles;
+            for (int i = 0; i < items; i++) {  // the producer's order
+                const int is_v = i == items - 1 ? 1 : (i >= 2 && (i & 1) == 0);
+                const int j = is_v ? (i == items - 1 ? n_tiles - 1 : i / 2 - 1) : (i + 1) / 2;
+                const int rs = i % RAW_STAGES, st = j % STAGES;
+                uint64_t *empty = is_v ? &sm.v_empty[st] : &sm.k_empty[st];
+                uint64_t *full = is_v ? &sm.v_full[st] : &sm.k_full[st];
+                if (!warp_wait(&sm.raw_full[rs], (i / RAW_STAGES) & 1, &sm.abort_flag) ||
+                    !warp_wait(empty, ((j / STAGES) & 1) ^ 1, &sm.abort_flag)) {
+                    if (lane == 0)
+                        set_abort(&sm.abort_flag, p.status);
+                    break;
+                }
+                convert_tile<D>(sm.raw[rs], sm.raw_scale[rs], is_v ? sm.v[st][0] : sm.k[st][0],
+                                warp - 8, lane);
+                tc::fence_proxy_async_smem();  // before the tensor core's reads
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(full);
+                    mbar_arrive(&sm.raw_empty[rs]);
+                }
+            }
+        }
     } else if (warp >= 4) {
         // ------------------------------------------------------- softmax --
         const int quarter = warp & 3;
@@ -554,15 +794,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float rs = (acc01.x + acc01.y) + (acc23.x + acc23.y);
             tc::tmem_wait_st();
 
-            if (j0 + BN > k_end) {
-                // Key rows past the valid range hold whatever the cache has there;
-                // zero them so P * V sees no non-finite values.
+            if (!E4M3 && (j0 + BN > k_end || (PAGED && j0 < vis_lo))) {
+                // Key rows past the valid range hold whatever the cache has there
+                // (and with pages so do those before the window: their page may
+                // be gone); zero them so P * V sees no non-finite values.  E4M3
+                // bytes never read as one.
                 const int st = j % STAGES;
                 if (!warp_wait(&sm.v_full[st], (j / STAGES) & 1, &sm.abort_flag)) {
                     ok = false;
                     break;
                 }
-                if (r >= k_end - j0) {
+                if (r >= k_end - j0 || (PAGED && r < vis_lo - j0)) {
 #pragma unroll
                     for (int kb = 0; kb < KB; kb++) {
                         uint4 *row = reinterpret_cast<uint4 *>(sm.v[st][kb] + r * 64);
@@ -650,7 +892,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     tc::fence_before_sync();
     __syncthreads();  // the staged rows are complete (unless a wait gave up)
-    if (!aborted(&sm.abort_flag)) {
+    if (!aborted(&sm.abort_flag) && warp < 8) {
         // Lanes across a row, one row per step, this warp's SR rows.
 #pragma unroll
         for (int i = 0; i < SR; i++) {
@@ -893,9 +1135,9 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillParam
         *reinterpret_cast<uint32_t *>(dst) = packed[0];
 }
 
-template <int D>
-cudaError_t launch_prefill_t(const PrefillParams &p, int total_tokens, int cache_batch,
-                             cudaStream_t stream)
+template <int D, KvSource SRC>
+cudaError_t launch_prefill_t(const PrefillParams &p, const PagedView &pg, int total_tokens,
+                             int cache_batch, cudaStream_t stream)
 {
     CUtensorMap mq, mk, mv;
     {
@@ -905,7 +1147,7 @@ cudaError_t launch_prefill_t(const PrefillParams &p, int total_tokens, int cache
         if (!make_bf16_tile_map(&mq, p.q, 3, dims, strides, box))
             return cudaErrorInvalidValue;
     }
-    {
+    if constexpr (SRC == KV_CONTIGUOUS) {
         const cuuint64_t rows = (cuuint64_t)cache_batch * p.KV * p.capacity;
         const cuuint64_t dims[2] = {(cuuint64_t)D, rows};
         const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
@@ -913,24 +1155,37 @@ cudaError_t launch_prefill_t(const PrefillParams &p, int total_tokens, int cache
         if (!make_bf16_tile_map(&mk, p.cache_k, 2, dims, strides, box) ||
             !make_bf16_tile_map(&mv, p.cache_v, 2, dims, strides, box))
             return cudaErrorInvalidValue;
+    } else {  // rows (page, kv head, slot), boxes of a page's rows
+        constexpr bool e4m3 = SRC == KV_PAGED_E4M3;
+        const cuuint64_t rows = ((cuuint64_t)pg.num_pages * p.KV) << pg.page_log;
+        const cuuint64_t dims[2] = {(cuuint64_t)D, rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)D * (e4m3 ? 1 : 2)};
+        const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? D : 64), 1u << pg.page_log};
+        const bool ok = e4m3 ? make_u8_tile_map(&mk, p.cache_k, 2, dims, strides, box, false) &&
+                                   make_u8_tile_map(&mv, p.cache_v, 2, dims, strides, box, false)
+                             : make_bf16_tile_map(&mk, p.cache_k, 2, dims, strides, box) &&
+                                   make_bf16_tile_map(&mv, p.cache_v, 2, dims, strides, box);
+        if (!ok)
+            return cudaErrorInvalidValue;
     }
-    const size_t smem = tc_smem_bytes<D>();
+    const size_t smem = tc_smem_bytes<D, SRC>();
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = once_per_device(configured, [smem] {
-        cudaError_t r = cudaFuncSetAttribute(prefill_tc_kernel<D, false>,
+        cudaError_t r = cudaFuncSetAttribute(prefill_tc_kernel<D, false, SRC>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(prefill_tc_kernel<D, true>,
+            r = cudaFuncSetAttribute(prefill_tc_kernel<D, true, SRC>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return r;
     });
     if (e != cudaSuccess)
         return e;
     const dim3 grid(p.full_units + p.tail_units * p.num_splits);
-    e = p.softcap > 0.f ? launch_kernel(prefill_tc_kernel<D, true>, grid, dim3(THREADS), smem,
-                                        stream, p, mq, mk, mv)
-                        : launch_kernel(prefill_tc_kernel<D, false>, grid, dim3(THREADS), smem,
-                                        stream, p, mq, mk, mv);
+    const dim3 block(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS);
+    e = p.softcap > 0.f ? launch_kernel(prefill_tc_kernel<D, true, SRC>, grid, block, smem, stream,
+                                        p, pg, mq, mk, mv)
+                        : launch_kernel(prefill_tc_kernel<D, false, SRC>, grid, block, smem, stream,
+                                        p, pg, mq, mk, mv);
     if (e != cudaSuccess || p.num_splits == 1)
         return e;
     return launch_kernel(prefill_combine_kernel<D>, dim3(p.tail_units, BM / kMergeRows), dim3(256),
@@ -973,13 +1228,38 @@ bool make_bf16_tile_map(CUtensorMap *map, const void *base, int rank, const cuui
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_u8_tile_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                      const cuuint64_t *strides_bytes, const cuuint32_t *box, bool swizzle)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base), dims,
+              strides_bytes, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                       : (box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B),
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int prefill_key_tile() { return BN; }
 int prefill_q_tile() { return BM; }
 
 cudaError_t launch_prefill(const PrefillParams &p, int d, int total_tokens, int cache_batch,
                            cudaStream_t stream)
 {
+    const PagedView none{};
     if (d == 128)
-        return launch_prefill_t<128>(p, total_tokens, cache_batch, stream);
-    return launch_prefill_t<64>(p, total_tokens, cache_batch, stream);
+        return launch_prefill_t<128, KV_CONTIGUOUS>(p, none, total_tokens, cache_batch, stream);
+    return launch_prefill_t<64, KV_CONTIGUOUS>(p, none, total_tokens, cache_batch, stream);
+}
+
+cudaError_t launch_prefill_paged(const PrefillParams &p, const PagedView &pg, bool e4m3, int d,
+                                 int total_tokens, cudaStream_t stream)
+{
+    if (d == 128)
+        return e4m3 ? launch_prefill_t<128, KV_PAGED_E4M3>(p, pg, total_tokens, 0, stream)
+                    : launch_prefill_t<128, KV_PAGED>(p, pg, total_tokens, 0, stream);
+    return e4m3 ? launch_prefill_t<64, KV_PAGED_E4M3>(p, pg, total_tokens, 0, stream)
+                : launch_prefill_t<64, KV_PAGED>(p, pg, total_tokens, 0, stream);
 }

@@ -53,13 +53,6 @@
 
 namespace {
 
-// inv_freq[i] / (2 pi) in turns per position, as the 96-bit fixed-point
-// fraction hi * 2^-64 + lo * 2^-96.
-struct RopeTurns {
-    unsigned long long hi[64];  // rd / 2 <= 64 (head_dim <= 128)
-    unsigned int lo[64];
-};
-
 constexpr int kStagedThreads = 256;
 
 // pi as an unevaluated sum of two doubles (the high part is pi rounded to
@@ -260,9 +253,11 @@ __device__ __forceinline__ const bf16 *row_src(const RopeAppendParams &p, int t,
     return p.v + ((size_t)t * p.KV + (r - p.H - p.KV)) * p.d;
 }
 
-__device__ __forceinline__ bf16 *row_dst(const RopeAppendParams &p, int t, int r, int b, int slot)
+// Slab b of the cache holds `cap` slots per kv head: a sequence's whole cache,
+// or one page.
+__device__ __forceinline__ bf16 *row_dst(const RopeAppendParams &p, int t, int r, int b, int slot,
+                                         size_t cap)
 {
-    const size_t cap = (size_t)p.capacity;
     if (r < p.H)
         return p.q_out + ((size_t)t * p.H + r) * p.d;
     if (r < p.H + p.KV)
@@ -296,6 +291,24 @@ __device__ __forceinline__ void owner_of(const RopeAppendParams &p, int t, int l
     }
 }
 
+// The slab, slot and slots per slab of position pos of sequence b: its page
+// with a paged cache.  False when the page index lies outside the cache.
+template <bool PAGED>
+__device__ __forceinline__ bool cache_place(const RopeAppendParams &p, const PagedView &pg, int pos,
+                                            int &b, int &slot, size_t &cap)
+{
+    if constexpr (PAGED) {
+        const int id = __ldcg(pg.table + (size_t)b * pg.pages_per_seq + (pos >> pg.page_log));
+        b = id;
+        slot = pos & ((1 << pg.page_log) - 1);
+        cap = (size_t)1 << pg.page_log;
+        return (unsigned)id < (unsigned)pg.num_pages;
+    }
+    slot = (p.flags & NA_RING_CACHE) ? pos % p.capacity : pos;
+    cap = (size_t)p.capacity;
+    return true;
+}
+
 // 16-byte read-only load kept where it is written (the compiler may not sink
 // it past the barriers that follow, so its latency overlaps theirs).
 __device__ __forceinline__ uint4 ldg_early(const void *p)
@@ -311,8 +324,9 @@ __device__ __forceinline__ uint4 ldg_early(const void *p)
 
 constexpr int kAppendThreads = 64;  // one 32-byte row unit each: 4 rows of d = 128, 8 of d = 64
 
-template <int D>
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const RopeAppendParams p,
+                                                                const PagedView pg,
                                                                 const RopeTurns turns)
 {
     constexpr int UPR = D / 16;  // 32-byte units per row
@@ -375,7 +389,13 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const RopeA
             na_report(p.status, NA_ERR_CAPACITY);
         return;
     }
-    const int slot = ring ? pos % p.capacity : pos;
+    int slot;
+    size_t cap;
+    if (!cache_place<PAGED>(p, pg, pos, b, slot, cap)) {
+        if (threadIdx.x == 0)
+            na_report(p.status, NA_ERR_PAGE);
+        return;
+    }
     __syncthreads();
     if ((int)threadIdx.x < half)  // stored [i][k] for pair 8k + i: a row's lanes read adjacent entries
         cs[(threadIdx.x & 7) * 8 + (threadIdx.x >> 3)] = cos_sin_turns((unsigned)pos, fhi, flo, kTrig.e);
@@ -450,14 +470,16 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const RopeA
             }
         }
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(row_dst(p, t, r, b, slot));
+    uint4 *dst = reinterpret_cast<uint4 *>(row_dst(p, t, r, b, slot, cap));
     dst[e0 / 8] = f32_to_bf16x8(ya);
     dst[e1 / 8] = f32_to_bf16x8(yb);
 }
 
 // -------------------------------------------------------- staged path --
 
+template <bool PAGED>
 __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(const RopeAppendParams p,
+                                                                           const PagedView pg,
                                                                            const RopeTurns turns)
 {
     extern __shared__ float smem_f[];
@@ -490,7 +512,13 @@ __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(cons
             na_report(p.status, NA_ERR_CAPACITY);
         return;
     }
-    const int slot = ring ? pos % p.capacity : pos;
+    int slot;
+    size_t cap;
+    if (!cache_place<PAGED>(p, pg, pos, b, slot, cap)) {
+        if (threadIdx.x == 0)
+            na_report(p.status, NA_ERR_PAGE);
+        return;
+    }
     if (qk_norm) {
         for (int i = threadIdx.x; i < 2 * d; i += kStagedThreads)
             wq[i] = __bfloat162float(i < d ? p.qw[i] : p.kw[i - d]);
@@ -569,7 +597,7 @@ __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(cons
 
     for (int c = threadIdx.x; c < chunks; c += kStagedThreads) {
         const int r = c / cpr, j = c - r * cpr;
-        reinterpret_cast<uint4 *>(row_dst(p, t, r, b, slot))[j] = f32_to_bf16x8(xs + r * d + j * 8);
+        reinterpret_cast<uint4 *>(row_dst(p, t, r, b, slot, cap))[j] = f32_to_bf16x8(xs + r * d + j * 8);
     }
 }
 
@@ -589,28 +617,33 @@ void turns_fixed_point(double inv_freq, unsigned long long &hi, unsigned int &lo
     lo = (unsigned int)(x & 0xffffffff);
 }
 
-}  // namespace
-
-cudaError_t launch_rope_append(const RopeAppendParams &p, const double *inv_freq, int half,
-                               cudaStream_t stream)
+RopeTurns turns_of(const double *inv_freq, int half)
 {
     RopeTurns turns{};
     for (int i = 0; i < half && i < 64; i++)
         turns_fixed_point(inv_freq[i], turns.hi[i], turns.lo[i]);
+    return turns;
+}
+
+template <bool PAGED>
+cudaError_t launch_rows(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
+                        cudaStream_t stream)
+{
     if (p.rd % 16 == 0) {
         const int rows_per_cta = kAppendThreads / (p.d / 16);
         const dim3 grid(p.total_tokens, (p.H + 2 * p.KV + rows_per_cta - 1) / rows_per_cta);
         if (p.d == 128)
-            return launch_kernel(rope_append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, p,
-                                 turns);
-        return launch_kernel(rope_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, p, turns);
+            return launch_kernel(rope_append_kernel<128, PAGED>, grid, dim3(kAppendThreads), 0,
+                                 stream, p, pg, turns);
+        return launch_kernel(rope_append_kernel<64, PAGED>, grid, dim3(kAppendThreads), 0, stream, p,
+                             pg, turns);
     }
     const size_t smem = rope_append_smem_bytes(p.H, p.KV, p.d, p.rd);
     // the largest dynamic shared memory granted so far, per device
     static std::atomic<size_t> configured[kMaxDevices];
     const int dev = current_device_index();
     if (smem > 48 * 1024 && (dev < 0 || smem > configured[dev].load(std::memory_order_acquire))) {
-        cudaError_t e = cudaFuncSetAttribute(rope_append_staged_kernel,
+        cudaError_t e = cudaFuncSetAttribute(rope_append_staged_kernel<PAGED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
         if (e != cudaSuccess)
@@ -621,8 +654,30 @@ cudaError_t launch_rope_append(const RopeAppendParams &p, const double *inv_freq
                 ;
         }
     }
-    return launch_kernel(rope_append_staged_kernel, dim3(p.total_tokens), dim3(kStagedThreads), smem,
-                         stream, p, turns);
+    return launch_kernel(rope_append_staged_kernel<PAGED>, dim3(p.total_tokens),
+                         dim3(kStagedThreads), smem, stream, p, pg, turns);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeAppendParams &p, const double *inv_freq, int half,
+                               cudaStream_t stream)
+{
+    return launch_rows<false>(p, PagedView{}, turns_of(inv_freq, half), stream);
+}
+
+// With E4M3 pages the row kernel takes the queries alone: keys and values go
+// by page, since a page's tokens share a scale.
+cudaError_t launch_rope_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
+                                     const double *inv_freq, int half, cudaStream_t stream)
+{
+    const RopeTurns turns = turns_of(inv_freq, half);
+    if (!e4m3)
+        return launch_rows<true>(p, pg, turns, stream);
+    RopeAppendParams q = p;
+    q.KV = 0;
+    const cudaError_t e = launch_rows<false>(q, pg, turns, stream);
+    return e != cudaSuccess ? e : launch_kv_append_e4m3(p, pg, turns, stream);
 }
 
 size_t rope_append_smem_bytes(int H, int KV, int d, int rd)

@@ -227,3 +227,8 @@ __device__ __forceinline__ void fence_proxy_async_smem()
 // swizzle; false when the driver rejects it.
 bool make_bf16_tile_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
                         const cuuint64_t *strides_bytes, const cuuint32_t *box);
+
+// The same for bytes (E4M3): rows of a box packed, or swizzled within 128 bytes
+// (an inner box of 128 bytes) or 64 (one of 64).
+bool make_u8_tile_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                      const cuuint64_t *strides_bytes, const cuuint32_t *box, bool swizzle);

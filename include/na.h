@@ -51,7 +51,8 @@ typedef enum na_status {
     NA_ERR_CAPACITY = -3,      /* a position does not fit the cache / probability stride */
     NA_ERR_WORKSPACE = -4,     /* workspace missing or smaller than required */
     NA_ERR_CUDA = -5,          /* a CUDA runtime call (launch, attribute) failed */
-    NA_ERR_DEVICE_TIMEOUT = -6 /* device only: a bounded wait inside a kernel gave up */
+    NA_ERR_DEVICE_TIMEOUT = -6, /* device only: a bounded wait inside a kernel gave up */
+    NA_ERR_PAGE = -7           /* device only: a page index outside the paged cache */
 } na_status;
 
 /* Option flags (na_attn_cfg.flags). */
@@ -105,6 +106,46 @@ typedef struct na_kv_cache {
     int32_t batch;
     int32_t capacity;
 } na_kv_cache;
+
+/* Element type of a paged cache (na_paged_kv_cache.dtype). */
+#define NA_KV_BF16 0
+#define NA_KV_E4M3 1 /* 8-bit floating point (4 exponent, 3 fraction bits, largest 448) with one
+                        scale per (page, kv head): a stored byte b stands for b * 2^(s - 127),
+                        s the E8M0 scale byte (0 .. 254).  Bytes 0x7f and 0xff, E4M3's NaN, read as
+                        +-480 in the attention calls. */
+
+/*
+ * Caller-owned paged cache: a pool of pages and a page table.  Position pos of
+ * sequence b lives in slot pos % page_size of page
+ * page_table[b * pages_per_seq + pos / page_size].
+ * (An addition of this library; the pages have no counterpart.)
+ *
+ *   - Pages that hold no position that the call reads or writes may have any
+ *     table entry (past a sequence's end, before a sliding window).  Any other
+ *     entry outside [0, num_pages) is reported as NA_ERR_PAGE: an append skips
+ *     its tokens, an attention call's outputs of that sequence are unspecified.
+ *   - Sequences may share pages that they only read (a common prompt).  Pages
+ *     that a call appends to belong to one sequence.
+ *   - Slots that hold no position of the sequence may hold any bits.  The values
+ *     that are attended have to be finite: a NaN or infinity of V reaches every
+ *     query row of its tile, masked or not.
+ *   - Sizes: page_size 16, 32, 64 or 128; num_pages * kv heads * page_size
+ *     <= 2^31 - 1 (NA_ERR_UNSUPPORTED otherwise).  The capacity of a sequence is
+ *     pages_per_seq * page_size.  NA_RING_CACHE is NA_ERR_UNSUPPORTED: a window
+ *     needs no ring here, its past pages can be given away.
+ */
+typedef struct na_paged_kv_cache {
+    void *k;                   /* [num_pages][num_kv_heads][page_size][head_dim], 16-byte aligned */
+    void *v;
+    uint8_t *k_scale;          /* NA_KV_E4M3: [num_pages][num_kv_heads] E8M0 bytes, else ignored */
+    uint8_t *v_scale;
+    const int32_t *page_table; /* int32 [batch][pages_per_seq] */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t batch;
+    int32_t pages_per_seq;
+    int32_t dtype;             /* NA_KV_BF16 or NA_KV_E4M3 */
+} na_paged_kv_cache;
 
 /*
  * Fused qk-norm + RoPE + cache append for a chunk of new tokens.
@@ -291,6 +332,67 @@ int na_decode_importance(const na_attn_cfg *cfg, int32_t batch, const float *pro
                          int32_t probs_stride, const int32_t *kv_lens, int32_t max_kv_len,
                          float *imp, int32_t imp_stride, int32_t accumulate, int32_t *status,
                          void *stream);
+
+/*
+ * na_rope_append_kv into a paged cache.
+ *
+ * As na_rope_append_kv, K and V rows going to their pages.  With NA_KV_BF16 pages
+ * the values are the same bit for bit.  With NA_KV_E4M3 the normed and rotated
+ * fp32 value x (within ~2^-20 of the page's largest) is rounded once, to nearest
+ * even, to the byte of x * 2^-e, where 2^e is the page's scale for this kv head
+ * and K or V: the smallest power of two with max |x| <= 448 * 2^e over the
+ * page's tokens.  A page that already holds tokens of the sequence (the chunk
+ * starts inside it) keeps its scale unless the new tokens need a larger one;
+ * then its earlier tokens are rounded to the larger one.  The scale of a page
+ * whose first token is appended depends on the new tokens alone, whatever the
+ * page held before.  q_out is bf16 in both cases.
+ *
+ *   status  NA_ERR_CAPACITY for a token whose position is not below
+ *           pages_per_seq * page_size, NA_ERR_PAGE for one whose table entry
+ *           lies outside the cache, NA_ERR_INVALID_ARG (NA_KV_E4M3) for a
+ *           sequence outside the call's tokens; such tokens are skipped (with
+ *           NA_KV_E4M3 their q_out may still be written).
+ */
+int na_rope_append_kv_paged(const na_attn_cfg *cfg, const na_rope_params *rope, int32_t batch,
+                            const int32_t *cu_seqlens, const int32_t *cache_lens,
+                            int32_t total_tokens, const void *q, const void *k, const void *v,
+                            const void *q_norm_w, const void *k_norm_w, void *q_out,
+                            const na_paged_kv_cache *cache, int32_t *status, void *stream);
+
+/*
+ * na_attn_decode over a paged cache: one query per sequence, the same arithmetic
+ * (E4M3 values become bf16 exactly; K's scale is applied to the scores in fp32,
+ * V's to the probabilities, exactly), the same outputs and probabilities.
+ *
+ *   max_kv_len  HOST upper bound of kv_lens; <= pages_per_seq * page_size.
+ *   num_splits, workspace, probs, gate, status: as in na_attn_decode, with
+ *               na_decode_paged_workspace_size() bytes of workspace.
+ */
+int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
+                         const na_paged_kv_cache *cache, const int32_t *kv_lens,
+                         int32_t max_kv_len, const void *gate, void *out, float *probs,
+                         int32_t probs_stride, int32_t num_splits, void *workspace,
+                         size_t ws_bytes, int32_t *status, void *stream);
+
+/*
+ * na_attn_prefill_chunk over a paged cache: the same arithmetic and outputs; E4M3
+ * values (their scale multiplied in) are bf16 numbers exactly, and the products
+ * are those of the bf16 cache that holds them.
+ *
+ *   max_total_len  HOST upper bound of cache_lens[b] + new length;
+ *                  <= pages_per_seq * page_size.
+ *   workspace      na_prefill_workspace_size() bytes (NULL allowed when that is 0).
+ *   Everything else as in na_attn_prefill_chunk.
+ */
+int na_attn_prefill_chunk_paged(const na_attn_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
+                                const int32_t *cache_lens, int32_t total_tokens,
+                                int32_t max_new_len, int32_t max_total_len, const void *q_rot,
+                                const na_paged_kv_cache *cache, const void *gate, void *out,
+                                void *workspace, size_t ws_bytes, int32_t *status, void *stream);
+
+/* Workspace bytes (HOST out-parameter) that na_attn_decode_paged needs for these bounds. */
+int na_decode_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_kv_len,
+                                   int32_t num_splits, size_t *bytes);
 
 /* Workspace bytes (HOST out-parameter) that na_attn_prefill_chunk needs for these bounds. */
 int na_prefill_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t total_tokens,

@@ -1,0 +1,525 @@
+"""The paged cache on the GPU: the append into bf16 and E4M3 pages and the two
+attention calls over them, against 64-bit statements (paged_ref.py)."""
+import itertools
+
+import pytest
+import torch
+
+import causal_gqa_attention_rope_gb300 as na
+from harness import Guarded
+from paged_ref import (Paged, attend, bits, dequantised, exponent, make_paged, normed_rotated,
+                       v_normed, values)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def rnd(g, *shape, mag=1.0):
+    return (torch.randn(*shape, generator=g) * mag).to(torch.bfloat16)
+
+
+def cu_of(new):
+    return ints([0] + list(itertools.accumulate(new)))
+
+
+def check(got, ref, tol, what):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), f"{what}: non-finite values"
+    off = (got - ref).abs()
+    bad = off > tol
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} values off by more than the "
+                           f"roundings allow; worst {float((off / tol.clamp(min=1e-300)).max()):.2f}x")
+
+
+# ----------------------------------------------------------------- append --
+
+APPEND = [
+    # d, rd, page, KV, H, flags, (prior, new) per sequence
+    (128, 128, 64, 8, 32, {}, [(0, 1), (63, 1), (64, 1), (65, 2)]),
+    (128, 64, 16, 4, 20, dict(yarn=True), [(5, 40), (0, 0), (16, 16), (31, 1), (0, 17)]),
+    (64, 64, 32, 2, 4, dict(qk_norm=True), [(10, 60), (100, 1), (0, 33)]),
+    (128, 34, 128, 1, 3, dict(qk_norm=True, zero=True, v_norm=True), [(120, 20), (0, 260)]),
+    (64, 18, 16, 3, 3, dict(v_norm=True), [(0, 15), (15, 2), (16, 1)]),
+    (64, 0, 64, 2, 2, {}, [(7, 64), (0, 1)]),
+    (64, 48, 128, 2, 16, {}, [(0, 128), (127, 130)]),
+    (128, 128, 32, 2, 2, {}, [(i % 70, 1 + i % 3) for i in range(75)]),
+]
+
+
+def append_case(case, seed, fmt, mag=1.0):
+    d, rd, page, KV, H, flags, seqs = case
+    prior, new = [p for p, _ in seqs], [n for _, n in seqs]
+    cache = make_paged(prior, KV, d, page, fmt, seed, room=max(new), mag=mag)
+    g = torch.Generator().manual_seed(seed + 1)
+    T = sum(new)
+    q, k, v = rnd(g, T, H, d), rnd(g, T, KV, d, mag=mag), rnd(g, T, KV, d, mag=mag)
+    qw = kw = None
+    if flags.get("qk_norm"):
+        qw, kw = rnd(g, d) * 0.1 + 1, rnd(g, d) * 0.1 + 1
+    cfg = na.AttnConfig(H, KV, d, rotary_dim=rd, qk_norm=bool(flags.get("qk_norm")),
+                        qk_norm_zero_centered=bool(flags.get("zero")),
+                        v_norm=bool(flags.get("v_norm")))
+    rope = na.RopeConfig(base=1e6, yarn=bool(flags.get("yarn")), factor=4.0, orig_max_pos=8192)
+    return cfg, rope, prior, new, cache, q, k, v, qw, kw
+
+
+def run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw):
+    mv = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    dc = cache.to(DEV)
+    gq = Guarded(q.shape, q.dtype, DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    na.na_rope_append_kv_paged(cfg, rope, cu_of(new), ints(prior), mv(q), mv(k), mv(v), gq.t, dc,
+                               q_norm_w=mv(qw), k_norm_w=mv(kw), status=status)
+    torch.cuda.synchronize()
+    gq.check("q_out")
+    return gq.t.cpu(), Paged.back(dc), int(status.item())
+
+
+def places(prior, new):
+    """(sequence, position, token row) of every new token."""
+    t = 0
+    for b, (p, n) in enumerate(zip(prior, new)):
+        for i in range(n):
+            yield b, p + i, t
+            t += 1
+
+
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"d{c[0]}rd{c[1]}p{c[2]}")
+def test_append_bf16_pages_equal_the_contiguous_append(case):
+    cfg, rope, prior, new, cache, q, k, v, qw, kw = append_case(case, 11, "bf16")
+    q_out, after, status = run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw)
+    assert status == 0
+    cap = max(p + n for p, n in zip(prior, new))
+    flat = na.KVCache(torch.zeros(len(prior), cfg.num_kv_heads, cap, cfg.head_dim,
+                                  dtype=torch.bfloat16, device=DEV),
+                      torch.zeros(len(prior), cfg.num_kv_heads, cap, cfg.head_dim,
+                                  dtype=torch.bfloat16, device=DEV))
+    mv = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    q_ref = torch.empty_like(q, device=DEV)
+    na.na_rope_append_kv(cfg, rope, cu_of(new), ints(prior), mv(q), mv(k), mv(v), q_ref, flat,
+                         q_norm_w=mv(qw), k_norm_w=mv(kw))
+    assert torch.equal(bits(q_out), bits(q_ref.cpu()))
+    for pool, was, ref in ((after.k, cache.k, flat.k.cpu()), (after.v, cache.v, flat.v.cpu())):
+        want = was.clone()
+        for b, pos, _ in places(prior, new):
+            want[int(cache.table[b, pos // cache.page]), :, pos % cache.page] = ref[b, :, pos]
+        assert torch.equal(bits(pool), bits(want))  # and nothing else was written
+
+
+def e4m3_step(y):
+    """Spacing of E4M3 at y (values of a page divided by its scale)."""
+    return torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+
+
+@pytest.mark.parametrize("mag", [1.0, 2.0 ** 20, 2.0 ** -30])
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"d{c[0]}rd{c[1]}p{c[2]}")
+def test_append_e4m3_pages(case, mag):
+    """Scales exactly by the rule; new values within half a step of E4M3 (and the
+    2^-20 of the page's largest that the fp32 arithmetic may be off); earlier
+    values of a page whose scale grew rounded to it; everything else untouched."""
+    cfg, rope, prior, new, cache, q, k, v, qw, kw = append_case(case, 12, "e4m3", mag)
+    q_out, after, status = run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw)
+    assert status == 0
+    page = cache.page
+    spots = list(places(prior, new))
+    pos = torch.tensor([p for _, p, _ in spots])
+    # eps of the norms is 1e-6 as in the config
+    rq = normed_rotated(q, pos, rope, cfg.rotary_dim, qw, 1e-6, cfg.qk_norm_zero_centered)
+    check(q_out, rq, 2.0 ** -8 * rq.abs() * (1 + 2.0 ** -10) + 2.0 ** -20, "q_out")
+    rk = normed_rotated(k, pos, rope, cfg.rotary_dim, kw, 1e-6, cfg.qk_norm_zero_centered)
+    rv = v_normed(v, 1e-6) if cfg.v_norm else v.double()
+    for name, x, pool, was, scale, scale_was in (
+            ("k", rk, after.k, cache.k, after.k_scale, cache.k_scale),
+            ("v", rv, after.v, cache.v, after.v_scale, cache.v_scale)):
+        want_bits, want_scale = bits(was).clone(), scale_was.clone()
+        by_page = {}
+        for b, p, t in spots:
+            by_page.setdefault((b, p // page), []).append((p % page, t))
+        for (b, i), rows in by_page.items():
+            pid = int(cache.table[b, i])
+            y = x[[t for _, t in rows]]  # [tokens, KV, d]
+            e = exponent(y.abs().amax(dim=(0, 2)))
+            held = rows[0][0]
+            if held:
+                e_old = scale_was[pid].double() - 127
+                e = torch.maximum(e, e_old)
+                old = (was[pid, :, :held].double() * torch.exp2(e_old - e)[:, None, None])
+                want_bits[pid, :, :held] = old.float().to(torch.float8_e4m3fn).view(torch.uint8)
+            want_scale[pid] = (e + 127).to(torch.uint8)
+            unit = torch.exp2(e)[None, :, None]
+            got = pool[pid].double()[:, [s for s, _ in rows]].transpose(0, 1) * unit
+            tol = (0.5 * e4m3_step(y / unit) + 448 * 2.0 ** -20) * unit
+            check(got, y, tol, f"{name} page {pid}")
+            for s, _ in rows:
+                want_bits[pid, :, s] = bits(pool)[pid, :, s]  # compared above
+        assert torch.equal(scale, want_scale), name
+        # minus zero and zero are the same value of a rescaled token
+        same = (bits(pool) == want_bits) | ((bits(pool) & 0x7F == 0) & (want_bits & 0x7F == 0))
+        assert same.all(), f"{name}: {int((~same).sum())} other bytes changed"
+
+
+def test_append_e4m3_token_by_token_is_the_chunk():
+    """A page filled one token at a time ends with the chunk's scale, and with its
+    values but for those that an intermediate scale pushed below E4M3's normal
+    range or rounded there twice: at most one step of the final scale's
+    subnormals apart."""
+    case = (128, 128, 32, 2, 4, {}, [(0, 50), (3, 40)])
+    cfg, rope, prior, new, cache, q, k, v, qw, kw = append_case(case, 13, "e4m3")
+    k[5::7] *= 8  # scales grow along the way
+    _, whole, _ = run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw)
+    dc = cache.to(DEV)
+    starts = [0, new[0]]
+    for i in range(max(new)):
+        live = [b for b in range(2) if i < new[b]]
+        rows = torch.tensor([starts[b] + i for b in live])
+        n = [1 if i < new[b] else 0 for b in range(2)]
+        at = [prior[b] + min(i, new[b]) for b in range(2)]
+        q_out = torch.empty(len(live), 4, 128, dtype=torch.bfloat16, device=DEV)
+        na.na_rope_append_kv_paged(cfg, rope, cu_of(n), ints(at), q[rows].to(DEV), k[rows].to(DEV),
+                                   v[rows].to(DEV), q_out, dc)
+    steps = Paged.back(dc)
+    assert torch.equal(steps.k_scale, whole.k_scale) and torch.equal(steps.v_scale, whole.v_scale)
+    for a, b in ((steps.k, whole.k), (steps.v, whole.v)):
+        a, b = a.double(), b.double()
+        both = torch.isfinite(a)
+        assert torch.equal(both, torch.isfinite(b))
+        a, b = a[both], b[both]
+        normal = b.abs() >= 2.0 ** -6
+        assert torch.equal(a[normal], b[normal])
+        assert ((a - b)[~normal].abs() <= 2.0 ** -9).all()
+
+
+# ----------------------------------------------------------------- decode --
+
+DECODE = [
+    # fmt, d, page, KV, G, lens, options
+    ("e4m3", 128, 64, 8, 4, [1, 64, 65, 700], dict(probs=True)),
+    ("e4m3", 64, 16, 2, 2, [0, 15, 16, 17, 333], dict(probs=True)),
+    ("e4m3", 128, 128, 1, 8, [129, 5000], dict(gate=True, splits=3)),
+    ("e4m3", 128, 16, 4, 5, [40, 1, 2049], dict(softcap=20.0, probs=True)),
+    ("e4m3", 64, 32, 3, 3, [200, 31, 1000], dict(window=100, probs=True)),
+    ("e4m3", 128, 32, 2, 16, [513, 3, 64], dict(window=7, gate=True)),
+    ("e4m3", 64, 128, 1, 7, [127, 128, 1300], dict(probs=True)),
+    ("bf16", 128, 64, 8, 4, [1, 64, 65, 700], dict(probs=True)),
+    ("bf16", 64, 16, 2, 2, [0, 15, 16, 17, 333], dict(probs=True, gate=True)),
+    ("bf16", 128, 16, 1, 12, [3000, 63], dict(window=1000, probs=True)),
+    ("bf16", 64, 128, 4, 1, [127, 1, 900], dict(softcap=5.0)),
+    ("bf16", 128, 32, 2, 6, [100, 31], dict(splits=2)),
+]
+
+
+def run_decode(cfg, q, cache, lens, gate=None, probs=False, splits=0):
+    B, H, d = q.shape
+    top = max(lens)
+    go = Guarded(q.shape, q.dtype, DEV)
+    gp = Guarded((B, H, max(top, 1)), torch.float32, DEV, fill=-7.0) if probs else None
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = na.workspace(na.na_decode_paged_workspace_size(cfg, B, top, splits), DEV)
+    na.na_attn_decode_paged(cfg, q.to(DEV), cache, ints(lens), top, go.t,
+                            probs=None if gp is None else gp.t,
+                            gate=None if gate is None else gate.to(DEV), workspace=ws,
+                            num_splits=splits, status=status)
+    torch.cuda.synchronize()
+    go.check("out")
+    if gp is not None:
+        gp.check("probs")
+    return go.t.cpu(), None if gp is None else gp.t.cpu(), int(status.item())
+
+
+@pytest.mark.parametrize("case", DECODE, ids=lambda c: f"{c[0]}d{c[1]}p{c[2]}g{c[4]}")
+def test_decode(case):
+    fmt, d, page, KV, G, lens, opt = case
+    H = KV * G
+    cache = make_paged(lens, KV, d, page, fmt, 21)
+    window = opt.get("window", 0)
+    if window:  # pages before every window are given away
+        for b, n in enumerate(lens):
+            cache.table[b, :max(0, n - window) // page] = -1
+    g = torch.Generator().manual_seed(22)
+    q = rnd(g, len(lens), H, d)
+    gate = rnd(g, len(lens), H, d) if opt.get("gate") else None
+    cfg = na.AttnConfig(H, KV, d, out_gate=gate is not None, softcap=opt.get("softcap", 0.0),
+                        window=window)
+    out, probs, status = run_decode(cfg, q, cache.to(DEV), lens, gate, opt.get("probs", False),
+                                    opt.get("splits", 0))
+    assert status == 0
+    ref = attend(cache, q, [(b, n - 1, 1) if n else (b, 0, 0) for b, n in enumerate(lens)],
+                 softcap=cfg.softcap, window=window, gate=gate)
+    check(out, ref.out, ref.tol, "out")
+    if probs is not None:
+        for b, n in enumerate(lens):
+            if n:
+                check(probs[b, :, :n], ref.probs[b], ref.probs_tol[b], f"probs {b}")
+            assert (probs[b, :, n:] == -7.0).all()
+
+
+@pytest.mark.parametrize("mag", [2.0 ** 30, 2.0 ** -40])
+def test_decode_e4m3_scales_far_from_one(mag):
+    """V of any magnitude, and page scales that differ by 2^10 within a sequence."""
+    lens, KV, d, page = [300, 70], 2, 128, 32
+    ks = make_paged(lens, KV, d, page, "e4m3", 23)
+    vs = make_paged(lens, KV, d, page, "e4m3", 23, mag=mag, spread=5.0)  # one seed: the same table
+    cache = Paged(ks.k, vs.v, ks.table, ks.k_scale, vs.v_scale)
+    g = torch.Generator().manual_seed(25)
+    q = rnd(g, 2, 8, d)
+    out, _, status = run_decode(na.AttnConfig(8, KV, d), q, cache.to(DEV), lens)
+    assert status == 0
+    ref = attend(cache, q, [(b, n - 1, 1) for b, n in enumerate(lens)])
+    check(out, ref.out, ref.tol, "out")
+
+
+def test_decode_shared_pages():
+    """Two sequences that share their first pages (a common prompt)."""
+    cache = make_paged([200, 150], 2, 64, 32, "e4m3", 26)
+    cache.table[1, :4] = cache.table[0, :4]
+    g = torch.Generator().manual_seed(27)
+    q = rnd(g, 2, 4, 64)
+    out, _, status = run_decode(na.AttnConfig(4, 2, 64), q, cache.to(DEV), [200, 150])
+    assert status == 0
+    ref = attend(cache, q, [(0, 199, 1), (1, 149, 1)])
+    check(out, ref.out, ref.tol, "out")
+
+
+# ---------------------------------------------------------------- prefill --
+
+PREFILL = [
+    # fmt, d, page, KV, G, (prior, new), options
+    ("bf16", 128, 64, 2, 4, [(0, 128)], {}),
+    ("bf16", 128, 16, 2, 4, [(100, 37), (0, 1), (500, 3), (0, 0), (17, 129)], dict(gate=True)),
+    ("bf16", 64, 128, 1, 8, [(1000, 5), (3, 130)], dict(softcap=10.0)),
+    ("bf16", 64, 32, 2, 3, [(700, 40), (0, 33)], dict(window=50)),
+    ("bf16", 128, 32, 1, 1, [(4000, 64)], {}),
+    ("e4m3", 128, 64, 2, 4, [(0, 128)], {}),
+    ("e4m3", 128, 16, 2, 4, [(100, 37), (0, 1), (500, 3), (0, 0), (17, 129)], dict(gate=True)),
+    ("e4m3", 64, 128, 1, 8, [(1000, 5), (3, 130)], dict(softcap=10.0)),
+    ("e4m3", 64, 32, 2, 3, [(700, 40), (0, 33)], dict(window=50)),
+    ("e4m3", 128, 32, 1, 1, [(4000, 64)], {}),
+    ("e4m3", 128, 128, 1, 2, [(250, 300)], dict(window=260)),
+    ("e4m3", 64, 16, 1, 1, [(5000, 2)], {}),
+]
+
+
+def run_prefill(cfg, q, cache, prior, new, gate=None):
+    T = sum(new)
+    top, most = max(p + n for p, n in zip(prior, new)), max(new)
+    go = Guarded(q.shape, q.dtype, DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = na.workspace(na.na_prefill_workspace_size(cfg, len(new), T, most, top), DEV)
+    na.na_attn_prefill_chunk_paged(cfg, cu_of(new), ints(prior), most, top, q.to(DEV), cache, go.t,
+                                   gate=None if gate is None else gate.to(DEV), workspace=ws,
+                                   status=status)
+    torch.cuda.synchronize()
+    go.check("out")
+    return go.t.cpu(), int(status.item())
+
+
+def prefill_case(case, seed):
+    fmt, d, page, KV, G, seqs, opt = case
+    prior, new = [p for p, _ in seqs], [n for _, n in seqs]
+    cache = make_paged([p + n for p, n in seqs], KV, d, page, fmt, seed)
+    window = opt.get("window", 0)
+    if window:
+        for b, p in enumerate(prior):
+            cache.table[b, :max(0, p - window + 1) // page] = -1
+    g = torch.Generator().manual_seed(seed + 1)
+    q = rnd(g, sum(new), KV * G, d)
+    gate = rnd(g, sum(new), KV * G, d) if opt.get("gate") else None
+    cfg = na.AttnConfig(KV * G, KV, d, out_gate=gate is not None, softcap=opt.get("softcap", 0.0),
+                        window=window)
+    starts = [0] + list(itertools.accumulate(new))
+    return cfg, cache, q, gate, prior, new, [(starts[b], p, n) for b, (p, n) in enumerate(seqs)]
+
+
+@pytest.mark.parametrize("case", PREFILL, ids=lambda c: f"{c[0]}d{c[1]}p{c[2]}g{c[4]}")
+def test_prefill(case):
+    cfg, cache, q, gate, prior, new, spans = prefill_case(case, 31)
+    out, status = run_prefill(cfg, q, cache.to(DEV), prior, new, gate)
+    assert status == 0
+    ref = attend(cache, q, spans, softcap=cfg.softcap, window=cfg.window, gate=gate)
+    check(out, ref.out, ref.tol, "out")
+
+
+@pytest.mark.parametrize("case", [c for c in PREFILL if c[0] == "e4m3"],
+                         ids=lambda c: f"d{c[1]}p{c[2]}g{c[4]}")
+def test_prefill_e4m3_is_the_bf16_cache_it_stands_for(case):
+    cfg, cache, q, gate, prior, new, _ = prefill_case(case, 33)
+    a, _ = run_prefill(cfg, q, cache.to(DEV), prior, new, gate)
+    b, _ = run_prefill(cfg, q, dequantised(cache).to(DEV), prior, new, gate)
+    assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("e", [-100, -20, 8, 30, 100])
+def test_prefill_e4m3_scales_far_from_one(e):
+    """V's scale far from one on every page (K's stays at unit scale)."""
+    case = ("e4m3", 128, 64, 1, 2, [(300, 40)], {})
+    cfg, cache, q, gate, prior, new, spans = prefill_case(case, 35)
+    live = cache.v_scale != 255
+    cache.v_scale[live] = (cache.v_scale[live].int() + e).to(torch.uint8)
+    out, status = run_prefill(cfg, q, cache.to(DEV), prior, new)
+    assert status == 0
+    ref = attend(cache, q, spans)
+    check(out, ref.out, ref.tol, "out")
+
+
+# --------------------------------------------------- together, graphs, ... --
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_prompt_then_decode_with_importance(fmt):
+    """Two prompts in chunks, then decode steps with probabilities and importance,
+    each step's attention checked against the pages as they stand."""
+    KV, G, d, page = 2, 4, 128, 16
+    H, B = KV * G, 2
+    cfg = na.AttnConfig(H, KV, d, qk_norm=True, window=0)
+    rope = na.RopeConfig(base=1e6)
+    g = torch.Generator().manual_seed(41)
+    qw, kw = (rnd(g, d) * 0.1 + 1).to(DEV), (rnd(g, d) * 0.1 + 1).to(DEV)
+    host = make_paged([0, 0], KV, d, page, fmt, 42, room=150)
+    cache = host.to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    at = [0, 0]
+    top = 150
+    imp = torch.zeros(B, top, device=DEV)
+    imp_ref = torch.zeros(B, top, dtype=torch.float64)
+    dws = na.workspace(na.na_decode_paged_workspace_size(cfg, B, top), DEV)
+    for new in ([40, 13], [70, 90], [1, 1], [1, 1], [1, 1]):
+        T = sum(new)
+        q, k, v = (rnd(g, T, n, d).to(DEV) for n in (H, KV, KV))
+        q_rot, out = torch.empty_like(q), torch.empty_like(q)
+        na.na_rope_append_kv_paged(cfg, rope, cu_of(new), ints(at), q, k, v, q_rot, cache,
+                                   q_norm_w=qw, k_norm_w=kw, status=status)
+        probs = None
+        if max(new) > 1:
+            ws = na.workspace(na.na_prefill_workspace_size(cfg, B, T, max(new), top), DEV)
+            na.na_attn_prefill_chunk_paged(cfg, cu_of(new), ints(at), max(new), top, q_rot, cache,
+                                           out, workspace=ws, status=status)
+        else:
+            lens = ints([n + 1 for n in at])
+            probs = torch.empty(B, H, top, device=DEV)
+            na.na_attn_decode_paged(cfg, q_rot, cache, lens, top, out, probs=probs, workspace=dws,
+                                    status=status)
+            na.na_decode_importance(cfg, probs, lens, top, imp, accumulate=True, status=status)
+        assert int(status.item()) == 0
+        spans = [(0, at[0], new[0]), (new[0], at[1], new[1])]
+        ref = attend(Paged.back(cache), q_rot.cpu(), spans)
+        check(out, ref.out, ref.tol, f"step {new}")
+        if probs is not None:
+            for b in range(B):
+                n = at[b] + 1
+                check(probs[b, :, :n], ref.probs[b], ref.probs_tol[b], "probs")
+                imp_ref[b, :n] += ref.probs[b].sum(0)
+        at = [a + n for a, n in zip(at, new)]
+    # three steps' sums over H heads, fp32
+    check(imp, imp_ref, (imp_ref + 1) * 2.0 ** -14, "importance")
+
+
+def test_graph_replay_with_new_lengths():
+    """A decode step (append, attend) captured once and replayed while the
+    sequences grow, on a side stream; then the same steps without the graph."""
+    KV, G, d, page = 2, 4, 64, 16
+    H, B, top = KV * G, 3, 100
+    cfg, rope = na.AttnConfig(H, KV, d), na.RopeConfig()
+    start = [0, 14, 63]
+    host = make_paged(start, KV, d, page, "e4m3", 51, room=40)
+    g = torch.Generator().manual_seed(52)
+    steps = [[rnd(g, B, n, d) for n in (H, KV, KV)] for _ in range(6)]
+
+    def run(graph):
+        cache = host.to(DEV)
+        q, k, v = (torch.zeros_like(t, device=DEV) for t in steps[0])
+        q_rot, out = torch.empty_like(q), torch.empty_like(q)
+        cu, prior, lens = cu_of([1] * B), ints(start), ints([n + 1 for n in start])
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        ws = na.workspace(na.na_decode_paged_workspace_size(cfg, B, top), DEV)
+
+        def step():
+            na.na_rope_append_kv_paged(cfg, rope, cu, prior, q, k, v, q_rot, cache, status=status)
+            na.na_attn_decode_paged(cfg, q_rot, cache, lens, top, out, workspace=ws, status=status)
+
+        s = torch.cuda.Stream()
+        outs = []
+        with torch.cuda.stream(s):
+            gr = None
+            for i, (a, b, c) in enumerate(steps):
+                q.copy_(a), k.copy_(b), v.copy_(c)
+                prior.copy_(ints([n + i for n in start]))
+                lens.copy_(ints([n + i + 1 for n in start]))
+                if not graph:
+                    step()
+                else:
+                    if gr is None:
+                        s.synchronize()
+                        gr = torch.cuda.CUDAGraph()
+                        with torch.cuda.graph(gr, stream=s):
+                            step()
+                    gr.replay()
+                outs.append(out.clone())
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        return torch.stack(outs).cpu(), Paged.back(cache)
+
+    (a, ca), (b, cb) = run(True), run(False)
+    assert torch.equal(bits(a), bits(b))
+    for x, y in ((ca.k, cb.k), (ca.v, cb.v), (ca.k_scale, cb.k_scale), (ca.v_scale, cb.v_scale)):
+        assert torch.equal(bits(x), bits(y))
+
+
+# ------------------------------------------------- reported by the device --
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_capacity_reported_and_other_sequences_served(fmt):
+    """An append past the table's pages, and lengths past the bound: reported, the
+    tokens that fit and the other sequence as usual."""
+    case = (64, 64, 16, 2, 4, {}, [(28, 4), (3, 2)])
+    cfg, rope, prior, new, cache, q, k, v, qw, kw = append_case(case, 61, fmt)
+    cache.table = cache.table[:, :2].contiguous()  # 32 positions a sequence
+    _, good, status = run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw)
+    assert status == 0
+    prior[0] = 30  # two of the four tokens are past the capacity
+    _, after, status = run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw)
+    assert status == na.NA_ERR_CAPACITY
+    pid = int(cache.table[1, 0])
+    assert torch.equal(bits(after.k)[pid, :, 3:5], bits(good.k)[pid, :, 3:5])
+    out, _, status = run_decode_bound(cfg, q[:2], good, [40, 5], 32)
+    assert status == na.NA_ERR_CAPACITY
+    assert (out[0] == 0).all()
+    ref = attend(good, q[:2], [(0, 0, 0), (1, 4, 1)])
+    check(out[1], ref.out[1], ref.tol[1], "the other sequence")
+
+
+def run_decode_bound(cfg, q, cache, lens, bound):
+    out = torch.zeros(q.shape, dtype=q.dtype, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = na.workspace(na.na_decode_paged_workspace_size(cfg, len(lens), bound), DEV)
+    na.na_attn_decode_paged(cfg, q.to(DEV), cache.to(DEV), ints(lens), bound, out, workspace=ws,
+                            status=status)
+    torch.cuda.synchronize()
+    return out.cpu(), None, int(status.item())
+
+
+@pytest.mark.parametrize("bad", [-1, 1000, 2 ** 31 - 1])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_page_index_outside_the_cache(fmt, bad):
+    """Reported as NA_ERR_PAGE by every call; the other sequence is served."""
+    case = (64, 64, 16, 2, 4, {}, [(20, 30), (40, 3)])
+    cfg, rope, prior, new, cache, q, k, v, qw, kw = append_case(case, 71, fmt)
+    _, good, _ = run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw)
+    was = int(cache.table[0, 2])
+    cache.table[0, 2] = bad  # positions 32 .. 47 of sequence 0
+    _, after, status = run_append(cfg, rope, prior, new, cache, q, k, v, qw, kw)
+    assert status == na.NA_ERR_PAGE
+    assert torch.equal(bits(after.k)[was], bits(cache.k)[was])  # its page is as it was
+    pid = int(cache.table[1, 2])
+    assert torch.equal(bits(after.k)[pid], bits(good.k)[pid])
+    good.table[0, 2] = bad
+    out, _, status = run_decode(cfg, q[:2], good.to(DEV), [50, 43])
+    assert status == na.NA_ERR_PAGE
+    ref = attend(good, q[:2], [(0, 0, 0), (1, 42, 1)])
+    check(out[1], ref.out[1], ref.tol[1], "decode of the other sequence")
+    out, status = run_prefill(cfg, q, good.to(DEV), prior, new)
+    assert status == na.NA_ERR_PAGE
+    ref = attend(good, q, [(0, 0, 0), (30, 40, 3)])
+    check(out[30:], ref.out[30:], ref.tol[30:], "prefill of the other sequence")
