@@ -19,6 +19,8 @@
 // slots [F(b), F(b + 1)) with F(b) = cu_seqlens[b] / page + 2 b, which hold that
 // many, and a CTA finds its sequence by a 32-way search for the last b with
 // F(b) <= slot (one round of loads up to 32 sequences, two up to 1024).
+#include <cuda_fp16.h>
+
 #include "na_internal.cuh"
 
 namespace {
@@ -48,10 +50,11 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(const float *y, float mul)
 // Four E4M3 bytes times `mul`, rounded again.
 __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float mul)
 {
-    uint32_t even, odd;
-    e4m3x4_to_bf16(w, kE4m3Unbias, even, odd);
-    const float y[4] = {__uint_as_float(even << 16), __uint_as_float(odd << 16),
-                        __uint_as_float(even & 0xffff0000u), __uint_as_float(odd & 0xffff0000u)};
+    uint32_t lo, hi;
+    e4m3x4_to_f16(w, lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    const float y[4] = {a.x, a.y, b.x, b.y};
     return pack_e4m3x4(y, mul);
 }
 

@@ -15,14 +15,17 @@
 // never leaves its page and the 16 keys of a consumer warp always share one
 // page, hence one scale pair, which the producer hands over with the tile.
 //
-// E4M3 pages: the bytes become exact bf16 values in registers (a 32-bit word
-// gives two bf16 pairs), so the products are those of the bf16 cache.  A word
-// holds four consecutive d of one key (K) or two d of two keys (V, loaded
-// transposed as 16-bit pairs); the pairs that come out, bytes 0,2 and 1,3, are
-// taken as they are and the other operand follows: Q is permuted within groups
-// of four d, and the output rows of the V product come out as even and odd d.
-// K's scale multiplies the scores in fp32, V's the probabilities ahead of their
-// rounding to bf16 (exact, a power of two).
+// E4M3 pages: the bytes become exact f16 values in registers (two conversions a
+// word; as bf16 they took nine integer instructions, which bound the pass), and
+// both products run on f16 MMAs.  A word holds four consecutive d of one key
+// (K) or two d of two keys (V, loaded transposed as 16-bit pairs), so its f16
+// pairs are two d of one key: for the scores they are taken as they are, Q
+// permuted to match; for V two byte permutes ahead of the conversion pair the
+// keys, and the output rows come out as even and odd d.  A query is scaled by
+// a power of two to f16's range (exact for every element that matters: down to
+// 2^-26 of the largest, within 2^-33 of it below); K's scale multiplies the
+// scores in fp32 and V's enters the weights (na_internal.cuh), which have f16's
+// 11 significand bits.
 #include "decode_shared.cuh"
 #include "na_internal.cuh"
 #include "tc_primitives.cuh"
@@ -51,7 +54,7 @@ struct __align__(1024) PagedSmem {
     float obuf[MAX_HPC][D];  // the warps' partial outputs, added in warp order
     float merge_m[CWARPS][MAX_HPC];
     float merge_l[CWARPS][MAX_HPC];
-    float2 mul[ST][CWARPS];  // a warp's K and V scale in each stage (E4M3)
+    uint16_t scales[ST][CWARPS];  // a warp's K | V << 8 scale bytes in each stage (E4M3)
     uint64_t full[ST];
     uint64_t empty[ST];
     Slice slice;
@@ -90,7 +93,10 @@ __device__ __forceinline__ PageEntry page_entry(const DecodeParams &p, const Pag
         }
         if constexpr (E4M3) {
             const size_t at = (size_t)e.id * p.KV + kvh;
-            e.scales = (uint32_t)__ldcg(pg.k_scale + at) | ((uint32_t)__ldcg(pg.v_scale + at) << 8);
+            const uint32_t vs = __ldcg(pg.v_scale + at);
+            if ((int)vs - 127 > kTopVExp)
+                na_report(p.status, NA_ERR_UNSUPPORTED);
+            e.scales = (uint32_t)__ldcg(pg.k_scale + at) | (vs << 8);
         }
     }
     return e;
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const int kp = t0 + 16 * (lane & 3);
                     const uint32_t sc = __shfl_sync(FULL, cur.scales, ((kp >> pg.page_log) - wb) & 31);
                     if (lane < CWARPS)
-                        sm.mul[stage][lane] = make_float2(e8m0_value(sc & 255u), e8m0_value(sc >> 8));
+                        sm.scales[stage][lane] = (uint16_t)sc;
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -234,23 +240,48 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int head0 = pc.kvh * p.group + pc.hc * hpc;
 
         // Q as the B operand: column g is head g (zero past hpc), rows are d --
-        // with E4M3, k-step s takes d = 16 s + 4 t + {0, 2} and {1, 3}.
+        // with E4M3, k-step s takes d = 16 s + 4 t + {0, 1} and {2, 3}, in f16 with
+        // the row's largest magnitude in [2^8, 2^9).
         uint32_t qf[KS][2];
+        float mul0 = p.scale_log2, mul1 = p.scale_log2;  // raw score to log2 domain, heads h0, h1
         {
             const bf16 *qrow = p.q + ((size_t)pc.b * p.H + head0 + min(g, hpc - 1)) * D;
 #pragma unroll
             for (int s = 0; s < KS; s++) {
-                uint32_t w0, w1;
                 if constexpr (E4M3) {
                     const uint2 u = *reinterpret_cast<const uint2 *>(qrow + 16 * s + 4 * t);
-                    w0 = __byte_perm(u.x, u.y, 0x5410);
-                    w1 = __byte_perm(u.x, u.y, 0x7632);
+                    qf[s][0] = u.x;
+                    qf[s][1] = u.y;
                 } else {
-                    w0 = *reinterpret_cast<const uint32_t *>(qrow + 16 * s + 2 * t);
-                    w1 = *reinterpret_cast<const uint32_t *>(qrow + 16 * s + 2 * t + 8);
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(qrow + 16 * s + 2 * t);
+                    const uint32_t w1 = *reinterpret_cast<const uint32_t *>(qrow + 16 * s + 2 * t + 8);
+                    qf[s][0] = g < hpc ? w0 : 0u;
+                    qf[s][1] = g < hpc ? w1 : 0u;
                 }
-                qf[s][0] = g < hpc ? w0 : 0u;
-                qf[s][1] = g < hpc ? w1 : 0u;
+            }
+            if constexpr (E4M3) {
+                uint32_t amax = 0;  // bits of the largest magnitude, bf16
+#pragma unroll
+                for (int s = 0; s < KS; s++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        amax = max(amax, max(qf[s][i] & 0x7fffu, (qf[s][i] >> 16) & 0x7fffu));
+                amax = max(amax, __shfl_xor_sync(FULL, amax, 1));
+                amax = max(amax, __shfl_xor_sync(FULL, amax, 2));
+                const int e = min(262 - (int)(amax >> 7), 254);  // 2^(e - 127) scales the row
+                const float up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+                for (int s = 0; s < KS; s++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint32_t w = qf[s][i];
+                        qf[s][i] = g < hpc ? pack_f16x2(__uint_as_float(w << 16) * up,
+                                                        __uint_as_float(w & 0xffff0000u) * up)
+                                           : 0u;
+                    }
+                const float down = e8m0_value((uint32_t)(254 - e));
+                mul0 *= __shfl_sync(FULL, down, 8 * t);  // the lane with g = h0
+                mul1 *= __shfl_sync(FULL, down, 8 * t + 4);
             }
         }
         float acc[KS][4];
@@ -280,38 +311,43 @@ __global__ void __launch_bounds__(THREADS, 2)
             const uint32_t kst = k_base + stage * STAGE_BYTES;
             const uint32_t vst = v_base + stage * STAGE_BYTES;
             const bool partial = t0 < lo || t0 + TILE > hi;  // the same in every warp
-            if constexpr (!E4M3) {
-                if (partial) {
-                    // V rows of masked keys are zeroed: they meet a zero probability
-                    // in the PV MMA and must not be NaN (E4M3 bytes never read as one).
-                    for (int c = lane; c < 16 * (D / 8); c += 32) {
-                        const int r = warp * 16 + c / (D / 8), ch = c % (D / 8);
-                        const int pos = t0 + r;
-                        if (pos < lo || pos >= hi)
-                            *reinterpret_cast<uint4 *>(sm.v[stage] + chunk_off<ROW>(r, ch)) =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                    __syncwarp();
+            if (partial) {
+                // V rows of masked keys are zeroed: they meet a zero probability
+                // in the PV MMA and must not be NaN.
+                constexpr int CPR = ROW / 16;  // chunks per row
+                for (int c = lane; c < 16 * CPR; c += 32) {
+                    const int r = warp * 16 + c / CPR, ch = c % CPR;
+                    const int pos = t0 + r;
+                    if (pos < lo || pos >= hi)
+                        *reinterpret_cast<uint4 *>(sm.v[stage] + chunk_off<ROW>(r, ch)) =
+                            make_uint4(0, 0, 0, 0);
                 }
+                __syncwarp();
             }
 
             // S^T = K Q^T for this warp's 16 keys.
             float sc[4] = {0.f, 0.f, 0.f, 0.f};
-            float score_mul = p.scale_log2, v_mul = 1.f;
+            float sm0 = mul0, sm1 = mul1, v_off = 0.f, v_inv = 1.f;
+            uint32_t v_byte = 127;
             if constexpr (E4M3) {
-                const float2 m = sm.mul[stage][warp];
-                score_mul = p.scale_log2 * m.x;
-                v_mul = m.y;
+                const uint32_t bytes = sm.scales[stage][warp];
+                const float kv = e8m0_value(bytes & 255u);
+                sm0 *= kv;
+                sm1 *= kv;
+                v_byte = bytes >> 8;
+                const int e = v_weight_exp(v_byte);
+                v_off = (float)e;
+                v_inv = exp2i(-e);
 #pragma unroll
                 for (int s = 0; s < KS / 2; s++) {
-                    uint32_t w[4], e[4], o[4];
+                    uint32_t w[4], a0[4], a1[4];
                     ldsm_x4(kst + chunk_off<ROW>(ka_row, 2 * s + ka_col), w);
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        e4m3x4_to_bf16(w[i], kE4m3Unbias, e[i], o[i]);
-                    const uint32_t a0[4] = {e[0], e[1], o[0], o[1]}, a1[4] = {e[2], e[3], o[2], o[3]};
-                    mma_bf16_16816(sc, a0, qf[2 * s][0], qf[2 * s][1]);
-                    mma_bf16_16816(sc, a1, qf[2 * s + 1][0], qf[2 * s + 1][1]);
+                    e4m3x4_to_f16(w[0], a0[0], a0[2]);
+                    e4m3x4_to_f16(w[1], a0[1], a0[3]);
+                    e4m3x4_to_f16(w[2], a1[0], a1[2]);
+                    e4m3x4_to_f16(w[3], a1[1], a1[3]);
+                    mma_f16_16816(sc, a0, qf[2 * s][0], qf[2 * s][1]);
+                    mma_f16_16816(sc, a1, qf[2 * s + 1][0], qf[2 * s + 1][1]);
                 }
             } else {
 #pragma unroll
@@ -327,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             const bool ina = pa >= lo && pa < hi, inb = pb >= lo && pb < hi;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                float x = sc[i] * score_mul;
+                float x = sc[i] * ((i & 1) ? sm1 : sm0);
                 if constexpr (CAPPED) {  // c tanh(s / c) in the log2 domain, tanh(y) = 1 - 2 / (e^2y + 1)
                     const float e = exp2f(x * p.cap_in);
                     x = p.cap_out * (1.0f - __fdividef(2.0f, e + 1.0f));
@@ -348,16 +384,18 @@ __global__ void __launch_bounds__(THREADS, 2)
                     prow1[pb] = sc[3];
             }
             // Tile maximum per head (over the 8 lanes sharing the column), then
-            // (rarely) raise the reference maximum.
-            float mx0 = fmaxf(sc[0], sc[2]), mx1 = fmaxf(sc[1], sc[3]);
+            // (rarely) raise the reference maximum.  E4M3: of score + V's exponent,
+            // and the reference stays kF16Top below it.
+            float mx0 = fmaxf(sc[0], sc[2]) + v_off, mx1 = fmaxf(sc[1], sc[3]) + v_off;
 #pragma unroll
             for (int m = 4; m < 32; m <<= 1) {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(FULL, mx0, m));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(FULL, mx1, m));
             }
-            const bool raise = mx0 > m_ref[0] + kRescaleThreshold || mx1 > m_ref[1] + kRescaleThreshold;
+            constexpr float TOP = E4M3 ? kF16Top : 0.f, LIMIT = E4M3 ? kF16Limit : kRescaleThreshold;
+            const bool raise = mx0 > m_ref[0] + LIMIT || mx1 > m_ref[1] + LIMIT;
             if (__any_sync(FULL, raise)) {  // warp-uniform
-                const float n0 = fmaxf(m_ref[0], mx0), n1 = fmaxf(m_ref[1], mx1);
+                const float n0 = fmaxf(m_ref[0], mx0 - TOP), n1 = fmaxf(m_ref[1], mx1 - TOP);
                 const float a0 = (m_ref[0] == -INFINITY) ? 0.f : exp2f(m_ref[0] - n0);
                 const float a1 = (m_ref[1] == -INFINITY) ? 0.f : exp2f(m_ref[1] - n1);
                 m_ref[0] = n0;
@@ -375,26 +413,41 @@ __global__ void __launch_bounds__(THREADS, 2)
             float pr[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                pr[i] = (sc[i] == -INFINITY) ? 0.f : exp2f(sc[i] - m_ref[i & 1]);
-                l_sum[i & 1] += pr[i];
-                if constexpr (E4M3)
-                    pr[i] *= v_mul;
+                if constexpr (E4M3) {  // a column without a key yet: m_ref is -inf too
+                    pr[i] = (sc[i] == -INFINITY) ? 0.f : ex2_mufu(sc[i] + (v_off - m_ref[i & 1]));
+                    l_sum[i & 1] = fmaf(pr[i], v_inv, l_sum[i & 1]);
+                } else {
+                    pr[i] = (sc[i] == -INFINITY) ? 0.f : exp2f(sc[i] - m_ref[i & 1]);
+                    l_sum[i & 1] += pr[i];
+                }
             }
             // P^T as the B operand: keys 2(l%4).. of head l/4.
-            const uint32_t b0 = movmatrix_trans(pack_bf16x2(pr[0], pr[1]));
-            const uint32_t b1 = movmatrix_trans(pack_bf16x2(pr[2], pr[3]));
+            const uint32_t b0 = movmatrix_trans(E4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
+            const uint32_t b1 = movmatrix_trans(E4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
             // O^T += V^T P^T, one 16-row block of d at a time.
             if constexpr (E4M3) {
+                const bool extreme = abs((int)v_byte - 127) > kMaxVExp;  // warp-uniform
+                const uint32_t rest = v_rest_f16x2(v_byte);
 #pragma unroll
                 for (int s = 0; s < KS / 2; s++) {
-                    uint32_t w[4], e[4], o[4];
+                    uint32_t w[4], a0[4], a1[4];
                     ldsm_x4_trans(vst + chunk_off<ROW>(va_row, 2 * s + va_col), w);
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        e4m3x4_to_bf16(w[i], kE4m3Unbias, e[i], o[i]);
-                    const uint32_t a0[4] = {e[0], o[0], e[1], o[1]}, a1[4] = {e[2], o[2], e[3], o[3]};
-                    mma_bf16_16816(acc[2 * s], a0, b0, b1);
-                    mma_bf16_16816(acc[2 * s + 1], a1, b0, b1);
+                    for (int i = 0; i < 4; i++)  // (key 0, key 1) of the even d, then of the odd
+                        w[i] = __byte_perm(w[i], 0u, 0x3120);
+                    e4m3x4_to_f16(w[0], a0[0], a0[1]);
+                    e4m3x4_to_f16(w[1], a0[2], a0[3]);
+                    e4m3x4_to_f16(w[2], a1[0], a1[1]);
+                    e4m3x4_to_f16(w[3], a1[2], a1[3]);
+                    if (extreme) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            a0[i] = mul_f16x2(a0[i], rest);
+                            a1[i] = mul_f16x2(a1[i], rest);
+                        }
+                    }
+                    mma_f16_16816(acc[2 * s], a0, b0, b1);
+                    mma_f16_16816(acc[2 * s + 1], a1, b0, b1);
                 }
             } else {
 #pragma unroll
@@ -403,9 +456,9 @@ __global__ void __launch_bounds__(THREADS, 2)
                     ldsm_x4_trans(vst + chunk_off<ROW>(va_row, 2 * s + va_col), a);
                     mma_bf16_16816(acc[s], a, b0, b1);
                 }
-                if (partial)
-                    tc::fence_proxy_async_smem();  // the zeroed rows before the stage's next copy
             }
+            if (partial)
+                tc::fence_proxy_async_smem();  // the zeroed rows before the stage's next copy
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm.empty[stage]);

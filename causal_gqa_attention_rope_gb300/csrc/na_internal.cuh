@@ -64,29 +64,63 @@ __device__ __forceinline__ float e8m0_value(uint32_t s)
     return __uint_as_float(s ? s << 23 : 0x00400000u);
 }
 
-// Four E4M3 values (the bytes of w) as bf16 pairs: `even` holds bytes 0 and 2,
-// `odd` bytes 1 and 3.  An E4M3 magnitude moved into the low exponent and high
-// fraction bits of a bf16 reads as the value times 2^-120 (subnormals
-// included: both formats drop the implicit bit at exponent field 0); `mul`
-// brings it back, exactly, together with any power-of-two scale folded into
-// it.  NaN bytes (0x7f, 0xff) read as +-480.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+// The four E4M3 values of w as two f16 pairs (exact): bytes 0, 1 and 2, 3.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-constexpr uint32_t kE4m3Unbias = 0x7b807b80u;  // 2^120, twice
-
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t mul, uint32_t &even,
-                                               uint32_t &odd)
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
-    const uint32_t e = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
-    const uint32_t o = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-    even = mul_bf16x2(e, mul);
-    odd = mul_bf16x2(o, mul);
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
+
+// Attention over E4M3 pages takes V's page scale 2^e into the weights: with x a
+// key's log2-domain score, y = x + e orders the terms p v by their size, the
+// weight 2^(y - m), m near the row's largest y, is what is rounded to f16 and
+// multiplies V's bytes (exact in f16), and the softmax sum takes the weight
+// times 2^-e.  A page's own magnitude thus costs no instruction per element and
+// no precision.  2^+-e and the weights have to stay within fp32: e is kept in
+// [-kMaxVExp, kMaxVExp], and a page beyond that gets the rest, 2^(e - b), multiplied
+// into its f16 values (below: they end at multiples of 2^-24; above: it fits up
+// to kTopVExp, larger scales are reported).
+constexpr int kMaxVExp = 40;
+constexpr int kTopVExp = 47;  // 448 * 2^7 is below f16's largest
+
+__device__ __forceinline__ int v_weight_exp(uint32_t byte)
+{
+    return min(max((int)byte - 127, -kMaxVExp), kMaxVExp);
+}
+
+// The rest 2^(e - b) as an f16 pair (1 for all but extreme pages).
+__device__ __forceinline__ uint32_t v_rest_f16x2(uint32_t byte)
+{
+    const int r = min((int)byte - 127 - v_weight_exp(byte), kTopVExp - kMaxVExp);
+    const uint32_t h = r >= -14 ? (uint32_t)(r + 15) << 10 : (r >= -24 ? 1u << (r + 24) : 0u);
+    return h | (h << 16);
+}
+
+// 2^x for an integer |x| <= 126.
+__device__ __forceinline__ float exp2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+
+// f16 weights: the largest of a row is raised to 2^kF16Top when it would exceed
+// 2^(kF16Top + kRaise), below f16's largest, so that weights down to 2^-21 of it
+// are normal numbers.
+constexpr float kF16Top = 7.0f, kF16Limit = 15.0f;
 
 // ------------------------------------------------------ shared-memory sync --
 

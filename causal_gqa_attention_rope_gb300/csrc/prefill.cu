@@ -36,14 +36,25 @@
 // A paged cache (na_attn_prefill_chunk_paged) differs in how a K or V tile gets
 // there.  bf16 pages: the producer warp keeps the page ids of the next 64 pages
 // in registers, one per lane and batch, and each lane issues one box (a page's
-// rows by 64 columns) straight into the tile.  E4M3 pages: the boxes land as
-// bytes in a raw ring, and four more warps (8-11) turn them into the same
-// swizzled bf16 tile, the page's power-of-two scale multiplied in -- every
-// dequantised value is a bf16 number, so the tensor cores see exactly the cache
-// that the bytes stand for, and the rest of the kernel is unchanged.
+// rows by 64 columns) straight into the tile.
+//
+// E4M3 pages.  K's bytes go to the tensor cores as they are (kind::f8f6f4, twice
+// the rate of bf16): a bf16 query has 8 significand bits and an E4M3 number 4,
+// so a query row, scaled by a power of two, is the sum of two E4M3 numbers per
+// element, and S = Q_hi K^T + Q_lo K^T costs what the bf16 product costs.  (The
+// sum is exact for elements down to 2^-10 of the row's largest and within 2^-17
+// of that below.)  The row's and K's powers of two multiply the scores in the
+// softmax, 16 keys at a time sharing a page.  V's boxes land as bytes in a raw
+// ring, and four more warps (8-11) turn them into the swizzled f16 tile, two
+// conversions a word; V's scale enters the weights (na_internal.cuh), which are
+// f16 here.  A 2048-token chunk over 28672 keys, 40/8 heads, takes 1010 us (0.65
+// of the bf16 peak); with V converted to bf16, ten integer instructions a word,
+// it took 1595 us, with K converted the same way too 2217 us, and with the tiles
+// left unconverted it would take 920 us.
 //
 #include <climits>
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <mutex>
 
 #include "na_internal.cuh"
@@ -57,8 +68,10 @@ constexpr int STAGES = 3;    // K/V shared-memory ring depth (bf16 caches)
 constexpr int NUM_S = 3;     // S/P buffers in tensor memory
 constexpr int THREADS = 256; // 8 warps: producer, S issuer, PV issuer, idle, 4 softmax
 constexpr int E4M3_THREADS = THREADS + 128;  // and 4 that convert E4M3 tiles
-constexpr int E4M3_STAGES = 2;  // bf16 K/V ring depth behind a raw ring ...
-constexpr int RAW_STAGES = 4;   // ... of this many K or V tiles in bytes
+constexpr int E4M3_K_STAGES = 4;  // K tiles in bytes
+constexpr int E4M3_V_STAGES = 2;  // bf16 V tiles behind a raw ring ...
+constexpr int RAW_STAGES = 4;     // ... of this many in bytes
+constexpr int SCALE_SLOTS = 8;    // K scales outlive their tile until its softmax (at most 7 tiles)
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL0 = 128;  // S buffer i at columns 128 (i + 1); O at column 0
 
@@ -68,19 +81,35 @@ enum KvSource { KV_CONTIGUOUS, KV_PAGED, KV_PAGED_E4M3 };
 template <int D, KvSource SRC>
 struct __align__(1024) TcSmem {
     static constexpr int KB = D / 64;  // 64-wide column blocks of a row
-    static constexpr int ST = SRC == KV_PAGED_E4M3 ? E4M3_STAGES : STAGES;
-    static constexpr int RAW = SRC == KV_PAGED_E4M3 ? RAW_STAGES : 1;
-    static constexpr uint32_t RAW_BYTES = SRC == KV_PAGED_E4M3 ? BN * D : 16;
+    static constexpr int KST = STAGES, VST = STAGES;
     bf16 q[KB][BM * 64];
-    bf16 k[ST][KB][BN * 64];
-    bf16 v[ST][KB][BN * 64];
-    uint8_t raw[RAW][RAW_BYTES];    // E4M3 tiles as they come, rows of D bytes
-    uint8_t raw_scale[RAW][8];      // E8M0 byte of each 16 keys of a raw tile
-    uint64_t raw_full[RAW], raw_empty[RAW];
+    bf16 k[KST][KB][BN * 64];
+    bf16 v[VST][KB][BN * 64];
     uint64_t q_full;
-    uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST];
+    uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST];
     uint64_t s_full[NUM_S], s_free[NUM_S], p_full[NUM_S];
     uint64_t o_done[NUM_S], drain[2];  // o_done[b]: the PVs of tiles b, b + NUM_S, ...
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int D>
+struct __align__(1024) TcSmem<D, KV_PAGED_E4M3> {
+    static constexpr int KB = D / 64;
+    static constexpr int KST = E4M3_K_STAGES, VST = E4M3_V_STAGES;
+    uint8_t q8[2][BM * D];           // high and low parts of Q, rows of D bytes, swizzled
+    uint8_t k[KST][BN * D];          // the same layout
+    uint8_t raw[RAW_STAGES][BN * D]; // V's bytes, rows of D (swizzled with D = 128)
+    bf16 v[VST][KB][BN * 64];        // (the first holds the bf16 Q tile at the start)
+    // for 32 keys of a tile, 16 and 16: K's scales, V's exponents in the weights, 2^-those
+    float4 mul_off[SCALE_SLOTS][4];
+    float2 v_inv[SCALE_SLOTS][4];
+    uint8_t v_scale[RAW_STAGES][8];  // V's E8M0 bytes
+    uint64_t raw_full[RAW_STAGES], raw_empty[RAW_STAGES];
+    uint64_t q_full, q_split;
+    uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST];
+    uint64_t s_full[NUM_S], s_free[NUM_S], p_full[NUM_S];
+    uint64_t o_done[NUM_S], drain[2];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -134,65 +163,137 @@ __device__ __forceinline__ float ex2_mufu(float x)
     return r;
 }
 
-// Two E4M3 bytes of w (those that `sel` puts into the high bytes of its halves)
-// as a bf16 pair, times the powers of two in `mul`.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t w, uint32_t sel, uint32_t mul)
+// A raw E4M3 tile (BN rows of D bytes) into a 128-byte-swizzled f16 tile, by the
+// four converting warps; `w` is the warp's index among them.  A thread turns 16
+// bytes into two 16-byte chunks at a time, and eight consecutive lanes have to
+// read and write all eight bank groups.  D = 64: two whole rows, their chunks
+// 2 c of opposite parity once swizzled.  D = 128: half of row r and of row
+// r ^ 5, whose swizzles send chunks 0 .. 3 to different halves on the raw side
+// and chunks 2 c to different parities on the f16 side.
+// EDGE: rows outside [lo, hi) hold no visible key and become zero, and V scales
+// beyond the weights' range are multiplied in.
+template <int D, bool EDGE>
+__device__ __forceinline__ void convert_rows(const uint8_t *raw, const uint8_t *scale, uint8_t *tile,
+                                             int w, int lane, int lo, int hi)
 {
-    const uint32_t x = __byte_perm(w, 0u, sel);
-    return mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), mul);
+    constexpr int RPI = 512 / D;         // rows per warp instruction
+    constexpr int ITERS = BN / 4 / RPI;  // a warp takes 32 consecutive rows
+    const int ch = D == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
+    auto row_of = [&](int i) {
+        if constexpr (D == 128) {
+            const int pair = (i & 1) * 2 + (lane >> 4);
+            return w * 32 + (i >> 1) * 8 + ((lane & 4) ? pair ^ 5 : pair);
+        }
+        return w * 32 + i * RPI + (lane >> 2);
+    };
+    uint8_t *out = tile + (ch / 4) * (BN * 128);
+    const int c0 = 2 * (ch % 4);
+    uint4 u[ITERS];
+#pragma unroll
+    for (int i = 0; i < ITERS; i++) {
+        const int r = row_of(i);
+        u[i] = *reinterpret_cast<const uint4 *>(raw + r * D + ((D == 128 ? ch ^ (r & 7) : ch) << 4));
+    }
+#pragma unroll
+    for (int i = 0; i < ITERS; i++) {
+        const int r = row_of(i);
+        uint32_t o[8];
+        e4m3x4_to_f16(u[i].x, o[0], o[1]);
+        e4m3x4_to_f16(u[i].y, o[2], o[3]);
+        e4m3x4_to_f16(u[i].z, o[4], o[5]);
+        e4m3x4_to_f16(u[i].w, o[6], o[7]);
+        if constexpr (EDGE) {
+            const uint32_t rest = v_rest_f16x2(scale[r >> 4]);
+            const bool seen = r >= lo && r < hi;
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                o[q] = seen ? mul_f16x2(o[q], rest) : 0u;
+        }
+        uint8_t *row = out + r * 128;
+        *reinterpret_cast<uint4 *>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (r & 7)) << 4)) =
+            make_uint4(o[4], o[5], o[6], o[7]);
+    }
 }
 
-// A raw E4M3 tile (BN rows of D bytes) into a 128-byte-swizzled bf16 tile, by
-// the four converting warps; `w` is the warp's index among them.  A thread
-// turns 16 bytes into two 16-byte chunks at a time.  With D = 128 the lanes of
-// the right half of a row write their two chunks in the other order, so that
-// eight consecutive lanes always cover all eight bank groups.
 template <int D>
 __device__ __forceinline__ void convert_tile(const uint8_t *raw, const uint8_t *scale, bf16 *tile,
-                                             int w, int lane)
+                                             int w, int lane, int lo, int hi)
 {
-    constexpr int CPR = D / 16;            // 16-byte chunks per raw row
-    constexpr int RPI = 32 / CPR;          // rows per warp instruction
-    constexpr int ITERS = BN / 4 / RPI;    // a warp takes 32 consecutive rows
-    const int ch = lane % CPR;
-    const bool swap = D == 128 && ch >= 4;
-    uint8_t *out = reinterpret_cast<uint8_t *>(tile) + (ch / 4) * (BN * 128);
-    const int c0 = 2 * (ch % 4) + (swap ? 1 : 0);
+    uint8_t *out = reinterpret_cast<uint8_t *>(tile);
+    const bool extreme = __any_sync(0xffffffffu, abs((int)scale[lane & 7] - 127) > kMaxVExp);
+    if (extreme || lo > 0 || hi < BN)
+        convert_rows<D, true>(raw, scale, out, w, lane, lo, hi);
+    else
+        convert_rows<D, false>(raw, scale, out, w, lane, lo, hi);
+}
+
+// 16-byte chunk c of row r of a D-byte-row tile, 128- or 64-byte swizzled.
+template <int D>
+__device__ __forceinline__ uint32_t byte_chunk_off(int r, int c)
+{
+    return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4))
+                    : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Two fp32 values as E4M3 (x0 in the low byte) and what is left of them.
+__device__ __forceinline__ uint32_t e4m3x2_split(float &x0, float &x1)
+{
+    uint16_t h;
+    uint32_t f;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(x1), "f"(x0));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+    x0 -= y.x;
+    x1 -= y.y;
+    return h;
+}
+
+// Row r of the staged bf16 Q tile as high and low E4M3 parts of row * 2^a, with
+// 2^a putting the row's largest magnitude into [128, 256); returns 2^-a.
+template <int D>
+__device__ __forceinline__ float split_q_row(const bf16 *staged, uint8_t *hi, uint8_t *lo, int r)
+{
+    auto chunk = [&](int c) {  // eight elements
+        return *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(staged) +
+                                                (c >> 3) * (BM * 128) + r * 128 +
+                                                (((c & 7) ^ (r & 7)) << 4));
+    };
+    float amax = 0.f;
 #pragma unroll
-    for (int half = 0; half < 2; half++) {  // 16 rows share a page
-        // 2^120 undoes the bias of the byte trick (na_internal.cuh); a scale above
-        // 2^7 takes a second factor
-        const int e = 120 + (int)scale[2 * w + half] - 127;
-        const int e1 = min(e, 127);
-        const uint32_t m1 = (uint32_t)(e1 + 127) << 7, mul = m1 | (m1 << 16);
-        const uint32_t m2 = (uint32_t)(e - e1 + 127) << 7, mul2 = m2 | (m2 << 16);
-        uint4 u[ITERS / 2];
+    for (int c = 0; c < D / 8; c++) {
+        float x[8];
+        bf16x8_to_f32(chunk(c), x);
 #pragma unroll
-        for (int i = 0; i < ITERS / 2; i++) {
-            const int r = w * 32 + half * 16 + i * RPI + lane / CPR;
-            u[i] = *reinterpret_cast<const uint4 *>(raw + r * D + ch * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < ITERS / 2; i++) {
-            const int r = w * 32 + half * 16 + i * RPI + lane / CPR;
-            uint32_t o[8];
-            const uint32_t in[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                o[2 * q] = e4m3x2_to_bf16(in[q], 0x1404, mul);
-                o[2 * q + 1] = e4m3x2_to_bf16(in[q], 0x3424, mul);
-            }
-            if (e > 127) {
-#pragma unroll
-                for (int q = 0; q < 8; q++)
-                    o[q] = mul_bf16x2(o[q], mul2);
-            }
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            uint8_t *row = out + r * 128;
-            *reinterpret_cast<uint4 *>(row + ((c0 ^ (r & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4 *>(row + (((c0 ^ 1) ^ (r & 7)) << 4)) = swap ? lo : hi;
-        }
+        for (int i = 0; i < 8; i++)
+            amax = fmaxf(amax, fabsf(x[i]));
     }
+    const int e = min(261 - (int)(__float_as_uint(amax) >> 23), 254);  // 2^a = 2^(e - 127)
+    const float up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll 2
+    for (int c = 0; c < D / 16; c++) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+            float x[8];
+            bf16x8_to_f32(chunk(2 * c + half), x);
+            uint32_t hh[4], ll[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
+                hh[i] = e4m3x2_split(x0, x1);
+                ll[i] = e4m3x2_split(x0, x1);
+            }
+            h[2 * half] = hh[0] | (hh[1] << 16);
+            h[2 * half + 1] = hh[2] | (hh[3] << 16);
+            l[2 * half] = ll[0] | (ll[1] << 16);
+            l[2 * half + 1] = ll[2] | (ll[3] << 16);
+        }
+        const uint32_t at = byte_chunk_off<D>(r, c);
+        *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+    return e8m0_value((uint32_t)(254 - e));
 }
 
 template <int D, bool CAPPED, KvSource SRC>
@@ -204,7 +305,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
 {
     typedef TcSmem<D, SRC> Smem;
     constexpr int KB = D / 64;
-    constexpr int STAGES = Smem::ST;
+    constexpr int KST = Smem::KST, VST = Smem::VST;
     constexpr bool PAGED = SRC != KV_CONTIGUOUS, E4M3 = SRC == KV_PAGED_E4M3;
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -218,15 +319,20 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
         mbar_init(&sm.q_full, 1);
-        for (int s = 0; s < STAGES; s++) {  // filled by copies, or by the converting warps
-            mbar_init(&sm.k_full[s], E4M3 ? 4 : 1);
-            mbar_init(&sm.v_full[s], E4M3 ? 4 : 1);
+        for (int s = 0; s < KST; s++) {
+            mbar_init(&sm.k_full[s], 1);
             mbar_init(&sm.k_empty[s], 1);
+        }
+        for (int s = 0; s < VST; s++) {  // filled by copies, or by the converting warps
+            mbar_init(&sm.v_full[s], E4M3 ? 4 : 1);
             mbar_init(&sm.v_empty[s], 1);
         }
-        for (int s = 0; E4M3 && s < Smem::RAW; s++) {
-            mbar_init(&sm.raw_full[s], 1);
-            mbar_init(&sm.raw_empty[s], 4);
+        if constexpr (E4M3) {
+            mbar_init(&sm.q_split, 4);
+            for (int s = 0; s < RAW_STAGES; s++) {
+                mbar_init(&sm.raw_full[s], 1);
+                mbar_init(&sm.raw_empty[s], 4);
+            }
         }
         for (int s = 0; s < NUM_S; s++) {
             mbar_init(&sm.s_full[s], 1);
@@ -314,16 +420,18 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     // sequence bounds arrive, overlapping that round trip (a CTA that turns out
     // to have no work waits for them before it exits).
     const bool early_q = eager;
-    if (eager && threadIdx.x == 0) {
-        mbar_arrive_expect_tx(&sm.q_full, KB * BM * 128);
-        for (int kb = 0; kb < KB; kb++)
-            tc::tma_load_3d(sm.q[kb], &map_q, kb * 64, h0, r0, &sm.q_full);
-        mbar_arrive_expect_tx(&sm.k_full[0], KB * BN * 128);
-        for (int kb = 0; kb < KB; kb++)
-            load_kv(sm.k[0][kb], &map_k, kb * 64, spec_row, &sm.k_full[0]);
-        mbar_arrive_expect_tx(&sm.v_full[0], KB * BN * 128);
-        for (int kb = 0; kb < KB; kb++)
-            load_kv(sm.v[0][kb], &map_v, kb * 64, spec_row, &sm.v_full[0]);
+    if constexpr (!PAGED) {
+        if (eager && threadIdx.x == 0) {
+            mbar_arrive_expect_tx(&sm.q_full, KB * BM * 128);
+            for (int kb = 0; kb < KB; kb++)
+                tc::tma_load_3d(sm.q[kb], &map_q, kb * 64, h0, r0, &sm.q_full);
+            mbar_arrive_expect_tx(&sm.k_full[0], KB * BN * 128);
+            for (int kb = 0; kb < KB; kb++)
+                load_kv(sm.k[0][kb], &map_k, kb * 64, spec_row, &sm.k_full[0]);
+            mbar_arrive_expect_tx(&sm.v_full[0], KB * BN * 128);
+            for (int kb = 0; kb < KB; kb++)
+                load_kv(sm.v[0][kb], &map_v, kb * 64, spec_row, &sm.v_full[0]);
+        }
     }
     if (!(p.batch > 1 && p.batch <= 32)) {
         tok0 = __ldg(p.cu_seqlens + b);
@@ -385,8 +493,8 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     if (!eager && warp == 1)
         tc::tmem_alloc(&sm.tmem_base, TMEM_COLS);
     const int n_tiles = (k_end - k_begin + BN - 1) / BN;
-    // tiles loaded before the barrier (pages: none, their ids come first)
-    const int pre = PAGED ? 0 : (n_tiles < STAGES ? n_tiles : STAGES);
+    // tiles loaded before the barrier (of pages none: their ids come first)
+    const int pre = n_tiles < STAGES ? n_tiles : STAGES;
     // first key that any row sees: pages before it may be gone
     const int vis_lo = p.window > 0 ? max(k_begin, pos_lo - p.window + 1) : k_begin;
 
@@ -397,16 +505,24 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         // barrier itself.
         if (!early_q) {
             mbar_arrive_expect_tx(&sm.q_full, KB * BM * 128);
-            for (int kb = 0; kb < KB; kb++)
-                tc::tma_load_3d(sm.q[kb], &map_q, kb * 64, h0, tok0 + r0, &sm.q_full);
+            for (int kb = 0; kb < KB; kb++) {
+                bf16 *dst;
+                if constexpr (E4M3)
+                    dst = sm.v[0][kb];
+                else
+                    dst = sm.q[kb];
+                tc::tma_load_3d(dst, &map_q, kb * 64, h0, tok0 + r0, &sm.q_full);
+            }
         }
-        for (int j = eager ? 1 : 0; j < pre; j++) {
-            mbar_arrive_expect_tx(&sm.k_full[j], KB * BN * 128);
-            for (int kb = 0; kb < KB; kb++)
-                load_kv(sm.k[j][kb], &map_k, kb * 64, tile_row(j), &sm.k_full[j]);
-            mbar_arrive_expect_tx(&sm.v_full[j], KB * BN * 128);
-            for (int kb = 0; kb < KB; kb++)
-                load_kv(sm.v[j][kb], &map_v, kb * 64, tile_row(j), &sm.v_full[j]);
+        if constexpr (!PAGED) {
+            for (int j = eager ? 1 : 0; j < pre; j++) {
+                mbar_arrive_expect_tx(&sm.k_full[j], KB * BN * 128);
+                for (int kb = 0; kb < KB; kb++)
+                    load_kv(sm.k[j][kb], &map_k, kb * 64, tile_row(j), &sm.k_full[j]);
+                mbar_arrive_expect_tx(&sm.v_full[j], KB * BN * 128);
+                for (int kb = 0; kb < KB; kb++)
+                    load_kv(sm.v[j][kb], &map_v, kb * 64, tile_row(j), &sm.v_full[j]);
+            }
         }
     }
     tc::fence_before_sync();
@@ -424,7 +540,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     constexpr int EPL = D / 32;  // elements per lane in the row stores
     constexpr int GW = D / 64;   // 32-bit words of gate per lane and row
     constexpr int SR = BM / 8;   // rows stored per warp
-    float *stage = reinterpret_cast<float *>(&sm.k[0][0][0]);  // the K ring, idle by then
+    float *stage = reinterpret_cast<float *>(&sm.k[0]);  // the K ring (and what follows), idle by then
     const bool split_out = nsplit > 1;
     // rows of this piece in the workspace: [tail unit][split][row]
     const size_t piece_row0 = ((size_t)tail_unit * p.num_splits + split) * BM;
@@ -450,257 +566,272 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             }
         }
     };
-    if (warp < 4 && gated_out)
+    if (!E4M3 && warp < 4 && gated_out)  // (E4M3: the registers are needed, all load at the end)
         load_gate();
 
-    if (PAGED && warp == 0) {
-        // ------------------------------------------------ producer, pages --
-        // K tile j is item i = 2 j - 1 (0 for j = 0), V tile j item 2 j + 2 in the
-        // E4M3 raw ring (K runs a tile ahead of V), the last V tile closing it.
-        const int page_log = pg.page_log, nbox = BN >> page_log;  // 8 .. 1 boxes of rows per tile
-        constexpr int COLS = E4M3 ? 1 : KB;
-        constexpr uint32_t BOX_ROW = E4M3 ? D : 128;
-        const int bi = lane & (nbox - 1), bc = lane / nbox;  // this lane's box: rows, columns
-        const int p_lo = vis_lo >> page_log, p_hi = (k_end - 1) >> page_log;
-        const int32_t *row = pg.table + (size_t)b * pg.pages_per_seq;
-        struct Entry {
-            int id;
-            uint32_t scales;  // K's byte | V's byte << 8
-        };
-        auto entry = [&](int i) {
-            Entry e{-1, 0x7f7fu};
-            if (i >= p_lo && i <= p_hi) {
-                e.id = __ldcg(row + i);
-                if ((unsigned)e.id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
-                    na_report(p.status, NA_ERR_PAGE);
-                    e.id = 0;
+    if (warp < 4) {
+        if (PAGED && warp == 0) {
+            // ------------------------------------------------ producer, pages --
+            const int page_log = pg.page_log, nbox = BN >> page_log;  // 8 .. 1 boxes of rows per tile
+            constexpr int COLS = E4M3 ? 1 : KB;
+            constexpr uint32_t BOX_ROW = E4M3 ? D : 128;
+            const int bi = lane & (nbox - 1), bc = lane / nbox;  // this lane's box: rows, columns
+            const int p_lo = vis_lo >> page_log, p_hi = (k_end - 1) >> page_log;
+            const int32_t *row = pg.table + (size_t)b * pg.pages_per_seq;
+            struct Entry {
+                int id;
+                uint32_t scales;  // K's byte | V's byte << 8
+            };
+            auto entry = [&](int i) {
+                Entry e{-1, 0x7f7fu};
+                if (i >= p_lo && i <= p_hi) {
+                    e.id = __ldcg(row + i);
+                    if ((unsigned)e.id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
+                        na_report(p.status, NA_ERR_PAGE);
+                        e.id = 0;
+                    }
+                    if constexpr (E4M3) {
+                        const size_t at = (size_t)e.id * p.KV + kvh;
+                        const uint32_t vs = __ldcg(pg.v_scale + at);
+                        if ((int)vs - 127 > kTopVExp)
+                            na_report(p.status, NA_ERR_UNSUPPORTED);
+                        e.scales = (uint32_t)__ldcg(pg.k_scale + at) | (vs << 8);
+                    }
                 }
-                if constexpr (E4M3) {
-                    const size_t at = (size_t)e.id * p.KV + kvh;
-                    e.scales = (uint32_t)__ldcg(pg.k_scale + at) |
-                               ((uint32_t)__ldcg(pg.v_scale + at) << 8);
+                return e;
+            };
+            int wb = k_begin >> page_log;  // page of lane 0's current entry
+            Entry cur = entry(wb + lane), nxt = entry(wb + 32 + lane);
+            bool ok = true;
+            auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+                const bool got = mbar_wait_bounded(bar, parity) && !aborted(&sm.abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    if (lane == 0)
+                        set_abort(&sm.abort_flag, p.status);
+                    return false;
                 }
-            }
-            return e;
-        };
-        // Page windows of 32 entries; K may be a tile ahead of V, so the window
-        // before the current one is kept too.
-        int wb = k_begin >> page_log;
-        Entry old{-1, 0x7f7fu}, cur = entry(wb + lane), nxt = entry(wb + 32 + lane);
-        bool ok = true;
-        auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-            const bool got = mbar_wait_bounded(bar, parity) && !aborted(&sm.abort_flag);
-            if (!__all_sync(0xffffffffu, got)) {
+                return true;
+            };
+            // One tile's boxes into dst, completing on bar.
+            auto load_tile = [&](const CUtensorMap *map, int id, int n, uint8_t *dst, uint64_t *bar) {
+                __syncwarp();
                 if (lane == 0)
-                    set_abort(&sm.abort_flag, p.status);
-                return false;
-            }
-            return true;
-        };
-        // One tile (of K: is_v 0, of V: 1) as boxes into dst, completing on bar.
-        auto load_tile = [&](int j, int is_v, uint8_t *dst, uint64_t *bar, uint8_t *scale) {
-            const int j0 = k_begin + j * BN;
-            if ((j0 >> page_log) - wb >= 32) {
-                old = cur;
-                cur = nxt;
-                wb += 32;
-                nxt = entry(wb + 32 + lane);
-            }
-            const int pos = j0 + (bi << page_log);
-            const int at = (pos >> page_log) - wb;  // negative: the window before
-            const int from = at & 31;
-            const int id_old = __shfl_sync(0xffffffffu, old.id, from);
-            const int id_cur = __shfl_sync(0xffffffffu, cur.id, from);
-            const int id = at < 0 ? id_old : id_cur;
-            const bool mine = bc < COLS && id >= 0;
-            const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
-            if constexpr (E4M3) {
-                const int a16 = ((j0 + 16 * (lane & 7)) >> page_log) - wb;
-                const uint32_t s_old = __shfl_sync(0xffffffffu, old.scales, a16 & 31);
-                const uint32_t s_cur = __shfl_sync(0xffffffffu, cur.scales, a16 & 31);
-                const uint32_t sc = a16 < 0 ? s_old : s_cur;
-                if (lane < 8)
-                    scale[lane] = (uint8_t)(is_v ? sc >> 8 : sc);
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_expect_tx(bar, n * (BOX_ROW << page_log));
-            __syncwarp();
-            if (mine)
-                load_kv(dst + bc * (BN * 128) + (bi << page_log) * BOX_ROW, is_v ? &map_v : &map_k,
-                        bc * 64, (id * p.KV + kvh) << page_log, bar);
-        };
-        if constexpr (E4M3) {
-            const int items = 2 * n_tiles;
-            int issued = 0;
-            for (int i = 0; ok && i < items; i++) {
-                const int is_v = i == items - 1 ? 1 : (i >= 2 && (i & 1) == 0);
-                const int j = is_v ? (i == items - 1 ? n_tiles - 1 : i / 2 - 1) : (i + 1) / 2;
-                const int rs = i % RAW_STAGES;
-                ok = wait_all(&sm.raw_empty[rs], ((i / RAW_STAGES) & 1) ^ 1);
-                if (ok) {
-                    load_tile(j, is_v, sm.raw[rs], &sm.raw_full[rs], sm.raw_scale[rs]);
-                    issued = i + 1;
-                }
-            }
-            if (lane == 0) {
-                drain_wait(&sm.q_full, 0, p.status);
-                for (int i = issued - 1; i >= 0 && i >= issued - RAW_STAGES; i--)
-                    drain_wait(&sm.raw_full[i % RAW_STAGES], (i / RAW_STAGES) & 1, p.status);
-            }
-        } else {
+                    mbar_arrive_expect_tx(bar, n * (BOX_ROW << page_log));
+                __syncwarp();
+                if (id >= 0)
+                    load_kv(dst + bc * (BN * 128) + (bi << page_log) * BOX_ROW, map, bc * 64,
+                            (id * p.KV + kvh) << page_log, bar);
+            };
             int k_issued = 0, v_issued = 0;
             for (int j = 0; ok && j < n_tiles; j++) {
-                const int st = j % STAGES;
-                const uint32_t par = ((j / STAGES) & 1) ^ 1;
-                ok = wait_all(&sm.k_empty[st], par);
-                if (!ok)
+                const int j0 = k_begin + j * BN;
+                if ((j0 >> page_log) - wb >= 32) {
+                    cur = nxt;
+                    wb += 32;
+                    nxt = entry(wb + 32 + lane);
+                }
+                int id = __shfl_sync(0xffffffffu, cur.id, ((j0 >> page_log) - wb + bi) & 31);
+                if (bc >= COLS)
+                    id = -1;
+                const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                const uint32_t scales = __shfl_sync(0xffffffffu, cur.scales,
+                                                    (((j0 + 16 * (lane & 7)) >> page_log) - wb) & 31);
+                const int ks = j % KST;
+                if (!(ok = wait_all(&sm.k_empty[ks], ((j / KST) & 1) ^ 1)))
                     break;
-                load_tile(j, 0, reinterpret_cast<uint8_t *>(sm.k[st]), &sm.k_full[st], nullptr);
+                if constexpr (E4M3) {
+                    if (lane < 8) {
+                        const int slot = j % SCALE_SLOTS, e = v_weight_exp(scales >> 8);
+                        float *mo = reinterpret_cast<float *>(&sm.mul_off[slot][lane >> 1]);
+                        mo[lane & 1] = e8m0_value(scales & 255u);
+                        mo[2 + (lane & 1)] = (float)e;
+                        reinterpret_cast<float *>(&sm.v_inv[slot][lane >> 1])[lane & 1] = exp2i(-e);
+                    }
+                }
+                load_tile(&map_k, id, n, reinterpret_cast<uint8_t *>(sm.k[ks]), &sm.k_full[ks]);
                 k_issued = j + 1;
-                ok = wait_all(&sm.v_empty[st], par);
-                if (!ok)
-                    break;
-                load_tile(j, 1, reinterpret_cast<uint8_t *>(sm.v[st]), &sm.v_full[st], nullptr);
+                if constexpr (E4M3) {
+                    const int rs = j % RAW_STAGES;
+                    if (!(ok = wait_all(&sm.raw_empty[rs], ((j / RAW_STAGES) & 1) ^ 1)))
+                        break;
+                    if (lane < 8)
+                        sm.v_scale[rs][lane] = (uint8_t)(scales >> 8);
+                    load_tile(&map_v, id, n, sm.raw[rs], &sm.raw_full[rs]);
+                } else {
+                    const int vs = j % VST;
+                    if (!(ok = wait_all(&sm.v_empty[vs], ((j / VST) & 1) ^ 1)))
+                        break;
+                    load_tile(&map_v, id, n, reinterpret_cast<uint8_t *>(sm.v[vs]), &sm.v_full[vs]);
+                }
                 v_issued = j + 1;
             }
+            // every copy issued lands before the CTA can exit
             if (lane == 0) {
                 drain_wait(&sm.q_full, 0, p.status);
-                for (int j = k_issued - 1; j >= 0 && j >= k_issued - STAGES; j--)
-                    drain_wait(&sm.k_full[j % STAGES], (j / STAGES) & 1, p.status);
-                for (int j = v_issued - 1; j >= 0 && j >= v_issued - STAGES; j--)
-                    drain_wait(&sm.v_full[j % STAGES], (j / STAGES) & 1, p.status);
-            }
-        }
-    } else if (warp == 0) {
-        // ------------------------------------------------------ producer --
-        if (lane == 0) {
-            int issued = pre;
-            for (int j = pre; j < n_tiles; j++) {
-                const int st = j % STAGES;
-                const uint32_t par = ((j / STAGES) & 1) ^ 1;
-                if (!mbar_wait_bounded(&sm.k_empty[st], par) || aborted(&sm.abort_flag)) {
-                    set_abort(&sm.abort_flag, p.status);
-                    break;
+                for (int j = k_issued - 1; j >= 0 && j >= k_issued - KST; j--)
+                    drain_wait(&sm.k_full[j % KST], (j / KST) & 1, p.status);
+                constexpr int VR = E4M3 ? RAW_STAGES : VST;
+                for (int j = v_issued - 1; j >= 0 && j >= v_issued - VR; j--) {
+                    uint64_t *bar;
+                    if constexpr (E4M3)
+                        bar = &sm.raw_full[j % VR];
+                    else
+                        bar = &sm.v_full[j % VR];
+                    drain_wait(bar, (j / VR) & 1, p.status);
                 }
-                mbar_arrive_expect_tx(&sm.k_full[st], KB * BN * 128);
-                for (int kb = 0; kb < KB; kb++)
-                    load_kv(sm.k[st][kb], &map_k, kb * 64, tile_row(j), &sm.k_full[st]);
-                if (!mbar_wait_bounded(&sm.v_empty[st], par) || aborted(&sm.abort_flag)) {
-                    set_abort(&sm.abort_flag, p.status);
-                    drain_wait(&sm.k_full[st], (j / STAGES) & 1, p.status);
-                    break;
+            }
+        } else if (warp == 0) {
+            // ------------------------------------------------------ producer --
+            if constexpr (!PAGED) {
+                if (lane == 0) {
+                    int issued = pre;
+                    for (int j = pre; j < n_tiles; j++) {
+                        const int st = j % STAGES;
+                        const uint32_t par = ((j / STAGES) & 1) ^ 1;
+                        if (!mbar_wait_bounded(&sm.k_empty[st], par) || aborted(&sm.abort_flag)) {
+                            set_abort(&sm.abort_flag, p.status);
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&sm.k_full[st], KB * BN * 128);
+                        for (int kb = 0; kb < KB; kb++)
+                            load_kv(sm.k[st][kb], &map_k, kb * 64, tile_row(j), &sm.k_full[st]);
+                        if (!mbar_wait_bounded(&sm.v_empty[st], par) || aborted(&sm.abort_flag)) {
+                            set_abort(&sm.abort_flag, p.status);
+                            drain_wait(&sm.k_full[st], (j / STAGES) & 1, p.status);
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&sm.v_full[st], KB * BN * 128);
+                        for (int kb = 0; kb < KB; kb++)
+                            load_kv(sm.v[st][kb], &map_v, kb * 64, tile_row(j), &sm.v_full[st]);
+                        issued = j + 1;
+                    }
+                    // every copy issued lands before the CTA can exit
+                    drain_wait(&sm.q_full, 0, p.status);
+                    for (int j = issued - 1; j >= 0 && j >= issued - STAGES; j--) {
+                        drain_wait(&sm.k_full[j % STAGES], (j / STAGES) & 1, p.status);
+                        drain_wait(&sm.v_full[j % STAGES], (j / STAGES) & 1, p.status);
+                    }
                 }
-                mbar_arrive_expect_tx(&sm.v_full[st], KB * BN * 128);
-                for (int kb = 0; kb < KB; kb++)
-                    load_kv(sm.v[st][kb], &map_v, kb * 64, tile_row(j), &sm.v_full[st]);
-                issued = j + 1;
             }
-            // every copy issued lands before the CTA can exit
-            drain_wait(&sm.q_full, 0, p.status);
-            for (int j = issued - 1; j >= 0 && j >= issued - STAGES; j--) {
-                drain_wait(&sm.k_full[j % STAGES], (j / STAGES) & 1, p.status);
-                drain_wait(&sm.v_full[j % STAGES], (j / STAGES) & 1, p.status);
-            }
-        }
-    } else if (warp == 1) {
-        // ---------------------------------------------------- S = Q K^T issue --
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN, false, false);
-            // Descriptors of the Q tile and of K stage 0; a 64-wide column block
-            // (BM = BN rows of 128 B) is BLK16 16-byte units, a K stage K_STAGE16.
-            constexpr uint32_t BLK16 = (BM * 128) >> 4;
-            constexpr uint32_t K_STAGE16 = (KB * BN * 128) >> 4;
-            static_assert(BM == BN, "one column-block stride for Q and K");
-            const uint64_t qd0 = tc::desc_kmajor_sw128(smem_addr(sm.q[0]));
-            const uint64_t kd0 = tc::desc_kmajor_sw128(smem_addr(sm.k[0][0]));
-            bool ok = mbar_wait_bounded(&sm.q_full, 0);
-            bool any = false;
-            for (int j = 0; ok && j < n_tiles; j++) {
-                const int st = j % STAGES, sb = j % NUM_S;
-                ok = mbar_wait_bounded(&sm.k_full[st], (j / STAGES) & 1);
-                if (ok && j >= NUM_S)
-                    ok = mbar_wait_bounded(&sm.s_free[sb], ((j / NUM_S) - 1) & 1);
-                if (!ok || aborted(&sm.abort_flag))
-                    break;
-                tc::fence_after_sync();
-                const uint32_t s_t = tmem + S_COL0 * (sb + 1);
-                const uint64_t kd = kd0 + (uint64_t)(st * K_STAGE16);
+        } else if (warp == 1) {
+            // ---------------------------------------------------- S = Q K^T issue --
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = E4M3 ? tc::idesc_e4m3_f32(BM, BN)
+                                                  : tc::idesc_bf16_f32(BM, BN, false, false);
+                // Descriptors of the Q tile and of K stage 0; a 64-wide column block
+                // (BM = BN rows of 128 B) is BLK16 16-byte units, a K stage K_STAGE16.
+                constexpr uint32_t BLK16 = (BM * 128) >> 4;
+                constexpr uint32_t K_STAGE16 = (E4M3 ? BN * D : KB * BN * 128) >> 4;
+                constexpr uint32_t Q_PART16 = (BM * D) >> 4;  // from the high to the low part (E4M3)
+                static_assert(BM == BN, "one column-block stride for Q and K");
+                uint64_t qd0, kd0;
+                bool ok;
+                if constexpr (E4M3) {
+                    qd0 = tc::desc_kmajor_bytes<D>(smem_addr(sm.q8[0]));
+                    kd0 = tc::desc_kmajor_bytes<D>(smem_addr(sm.k[0]));
+                    ok = mbar_wait_bounded(&sm.q_split, 0);
+                } else {
+                    qd0 = tc::desc_kmajor_sw128(smem_addr(sm.q[0]));
+                    kd0 = tc::desc_kmajor_sw128(smem_addr(sm.k[0][0]));
+                    ok = mbar_wait_bounded(&sm.q_full, 0);
+                }
+                bool any = false;
+                for (int j = 0; ok && j < n_tiles; j++) {
+                    const int st = j % KST, sb = j % NUM_S;
+                    ok = mbar_wait_bounded(&sm.k_full[st], (j / KST) & 1);
+                    if (ok && j >= NUM_S)
+                        ok = mbar_wait_bounded(&sm.s_free[sb], ((j / NUM_S) - 1) & 1);
+                    if (!ok || aborted(&sm.abort_flag))
+                        break;
+                    tc::fence_after_sync();
+                    const uint32_t s_t = tmem + S_COL0 * (sb + 1);
+                    const uint64_t kd = kd0 + (uint64_t)(st * K_STAGE16);
+                    if constexpr (E4M3) {
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) {  // descriptor start addresses advance in 16-byte units
-                    const uint32_t off = (k >> 2) * BLK16 + (k & 3) * 2;
-                    tc::mma_ss(s_t, qd0 + off, kd + off, idesc_s, k > 0);
-                }
-                tc::mma_commit(&sm.s_full[sb]);
-                tc::mma_commit(&sm.k_empty[st]);
-                any = true;
-            }
-            if (!ok)
-                set_abort(&sm.abort_flag, p.status);
-            if (any) {  // all issued MMAs complete before tensor memory is released
-                tc::mma_commit(&sm.drain[0]);
-                drain_wait(&sm.drain[0], 0, p.status);
-            }
-        }
-    } else if (warp == 2) {
-        // --------------------------------------------------- O += P V issue --
-        if (lane == 0) {
-            constexpr uint32_t idesc_o = tc::idesc_bf16_f32(BM, D, false, true);
-            constexpr uint32_t V_STAGE16 = (KB * BN * 128) >> 4;  // a V stage in 16-byte units
-            const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_addr(sm.v[0][0]), BN * 128);
-            bool ok = true, any = false;
-            for (int j = 0; ok && j < n_tiles; j++) {
-                const int st = j % STAGES, sb = j % NUM_S;
-                ok = mbar_wait_bounded(&sm.p_full[sb], (j / NUM_S) & 1);
-                if (ok)
-                    ok = mbar_wait_bounded(&sm.v_full[st], (j / STAGES) & 1);
-                if (!ok || aborted(&sm.abort_flag))
-                    break;
-                tc::fence_after_sync();
-                const uint32_t p_t = tmem + S_COL0 * (sb + 1);
-                const uint64_t vd = vd0 + (uint64_t)(st * V_STAGE16);
+                        for (int k = 0; k < D / 32; k++)  // 32 bytes of d per step
+                            tc::mma_ss_bytes(s_t, qd0 + k * 2, kd + k * 2, idesc_s, k > 0);
 #pragma unroll
-                for (int k = 0; k < BN / 16; k++)  // 16 keys = 16 rows of 128 B per step
-                    tc::mma_ts(tmem, p_t + k * 8, vd + (uint64_t)(k * 128), idesc_o, j > 0 || k > 0);
-                tc::mma_commit(&sm.s_free[sb]);
-                tc::mma_commit(&sm.v_empty[st]);
-                tc::mma_commit(&sm.o_done[sb]);
-                any = true;
+                        for (int k = 0; k < D / 32; k++)
+                            tc::mma_ss_bytes(s_t, qd0 + Q_PART16 + k * 2, kd + k * 2, idesc_s, true);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 16; k++) {  // descriptor start addresses advance in 16-byte units
+                            const uint32_t off = (k >> 2) * BLK16 + (k & 3) * 2;
+                            tc::mma_ss(s_t, qd0 + off, kd + off, idesc_s, k > 0);
+                        }
+                    }
+                    tc::mma_commit(&sm.s_full[sb]);
+                    tc::mma_commit(&sm.k_empty[st]);
+                    any = true;
+                }
+                if (!ok)
+                    set_abort(&sm.abort_flag, p.status);
+                if (any) {  // all issued MMAs complete before tensor memory is released
+                    tc::mma_commit(&sm.drain[0]);
+                    drain_wait(&sm.drain[0], 0, p.status);
+                }
             }
-            if (!ok)
-                set_abort(&sm.abort_flag, p.status);
-            if (any) {
-                tc::mma_commit(&sm.drain[1]);
-                drain_wait(&sm.drain[1], 0, p.status);
+        } else if (warp == 2) {
+            // --------------------------------------------------- O += P V issue --
+            if (lane == 0) {
+                constexpr uint32_t idesc_o = E4M3 ? tc::idesc_f16_f32(BM, D, false, true)
+                                                  : tc::idesc_bf16_f32(BM, D, false, true);
+                constexpr uint32_t V_STAGE16 = (KB * BN * 128) >> 4;  // a V stage in 16-byte units
+                const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_addr(sm.v[0][0]), BN * 128);
+                bool ok = true, any = false;
+                for (int j = 0; ok && j < n_tiles; j++) {
+                    const int st = j % VST, sb = j % NUM_S;
+                    ok = mbar_wait_bounded(&sm.p_full[sb], (j / NUM_S) & 1);
+                    if (ok)
+                        ok = mbar_wait_bounded(&sm.v_full[st], (j / VST) & 1);
+                    if (!ok || aborted(&sm.abort_flag))
+                        break;
+                    tc::fence_after_sync();
+                    const uint32_t p_t = tmem + S_COL0 * (sb + 1);
+                    const uint64_t vd = vd0 + (uint64_t)(st * V_STAGE16);
+#pragma unroll
+                    for (int k = 0; k < BN / 16; k++)  // 16 keys = 16 rows of 128 B per step
+                        tc::mma_ts(tmem, p_t + k * 8, vd + (uint64_t)(k * 128), idesc_o, j > 0 || k > 0);
+                    tc::mma_commit(&sm.s_free[sb]);
+                    tc::mma_commit(&sm.v_empty[st]);
+                    tc::mma_commit(&sm.o_done[sb]);
+                    any = true;
+                }
+                if (!ok)
+                    set_abort(&sm.abort_flag, p.status);
+                if (any) {
+                    tc::mma_commit(&sm.drain[1]);
+                    drain_wait(&sm.drain[1], 0, p.status);
+                }
             }
         }
     } else if (E4M3 && warp >= 8) {
-        // --------------------------------------- E4M3 tiles to bf16 tiles --
+        // -------------------------------------- E4M3 V tiles to f16 tiles --
         if constexpr (E4M3) {
-            const int items = 2 * n_tiles;
-            for (int i = 0; i < items; i++) {  // the producer's order
-                const int is_v = i == items - 1 ? 1 : (i >= 2 && (i & 1) == 0);
-                const int j = is_v ? (i == items - 1 ? n_tiles - 1 : i / 2 - 1) : (i + 1) / 2;
-                const int rs = i % RAW_STAGES, st = j % STAGES;
-                uint64_t *empty = is_v ? &sm.v_empty[st] : &sm.k_empty[st];
-                uint64_t *full = is_v ? &sm.v_full[st] : &sm.k_full[st];
-                if (!warp_wait(&sm.raw_full[rs], (i / RAW_STAGES) & 1, &sm.abort_flag) ||
-                    !warp_wait(empty, ((j / STAGES) & 1) ^ 1, &sm.abort_flag)) {
+            for (int j = 0; j < n_tiles; j++) {
+                const int rs = j % RAW_STAGES, st = j % VST;
+                bool ok = warp_wait(&sm.raw_full[rs], (j / RAW_STAGES) & 1, &sm.abort_flag);
+                if (ok && j == 0)  // the first V stage holds Q until it is split
+                    ok = warp_wait(&sm.q_split, 0, &sm.abort_flag);
+                if (ok)
+                    ok = warp_wait(&sm.v_empty[st], ((j / VST) & 1) ^ 1, &sm.abort_flag);
+                if (!ok) {
                     if (lane == 0)
                         set_abort(&sm.abort_flag, p.status);
                     break;
                 }
-                convert_tile<D>(sm.raw[rs], sm.raw_scale[rs], is_v ? sm.v[st][0] : sm.k[st][0],
-                                warp - 8, lane);
+                const int j0 = k_begin + j * BN;
+                convert_tile<D>(sm.raw[rs], sm.v_scale[rs], sm.v[st][0], warp - 8, lane,
+                                vis_lo - j0, k_end - j0);
                 tc::fence_proxy_async_smem();  // before the tensor core's reads
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(full);
+                    mbar_arrive(&sm.v_full[st]);
                     mbar_arrive(&sm.raw_empty[rs]);
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else {
         // ------------------------------------------------------- softmax --
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;  // query row == TMEM lane
@@ -714,10 +845,20 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         const float cap_out = capped ? p.softcap * NA_LOG2E / p.scale_log2 : 0.f;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t o_t = tmem + lane_off;
-        const float sl2 = p.scale_log2;
+        float sl2 = p.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < n_tiles; j++) {
+        if constexpr (E4M3) {
+            ok = warp_wait(&sm.q_full, 0, &sm.abort_flag);
+            if (ok) {
+                sl2 *= split_q_row<D>(sm.v[0][0], sm.q8[0], sm.q8[1], r);
+                tc::fence_proxy_async_smem();  // before the tensor core's reads
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.q_split);
+            }
+        }
+        for (int j = 0; ok && j < n_tiles; j++) {
             const int sb = j % NUM_S;
             const int j0 = k_begin + j * BN;
             const uint32_t s_t = tmem + S_COL0 * (sb + 1) + lane_off;
@@ -732,7 +873,33 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 tc::tmem_ld32(s_t + c * 32, sr[c]);
             tc::tmem_wait_ld();
 
-            if constexpr (capped) {
+            // E4M3: what turns a raw score of 16 keys into the log2 domain (the soft
+            // cap leaves it there) and V's exponent; read again where it is used, the
+            // registers hold the scores.
+            auto mul_off = [&](int c) {
+                float4 x;
+                if constexpr (E4M3) {
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                                 : "r"(smem_addr(&sm.mul_off[j % SCALE_SLOTS][c])));
+                    // positive: masked scores are -inf
+                    x.x = fmaxf(x.x * sl2, 1.2e-38f);
+                    x.y = fmaxf(x.y * sl2, 1.2e-38f);
+                }
+                return x;
+            };
+            if constexpr (capped && E4M3) {
+                const float in = 2.0f / p.softcap, out = p.softcap * NA_LOG2E;
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const float4 mo = mul_off(c);
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const float e = ex2_mufu(__uint_as_float(sr[c][i]) * (i < 16 ? mo.x : mo.y) * in);
+                        sr[c][i] = __float_as_uint(out * (1.0f - __fdividef(2.0f, e + 1.0f)));
+                    }
+                }
+            } else if constexpr (capped) {
 #pragma unroll
                 for (int c = 0; c < 4; c++)
 #pragma unroll
@@ -752,7 +919,31 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                             sr[c][i] = __float_as_uint(-INFINITY);
                     }
             }
-            // row maximum: four independent chains of 3-input max
+            // row maximum: four independent chains of 3-input max (E4M3: two per 32
+            // keys, of score + V's exponent)
+            float mxs;
+            if constexpr (E4M3) {
+                float mg[8];
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const float4 mo = mul_off(c);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t *x = &sr[c][16 * h];
+                        float m0 = max3f(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+                        float m1 = max3f(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+                        m0 = max3f(m0, __uint_as_float(x[6]), __uint_as_float(x[7]));
+                        m1 = max3f(m1, __uint_as_float(x[8]), __uint_as_float(x[9]));
+                        m0 = max3f(m0, __uint_as_float(x[10]), __uint_as_float(x[11]));
+                        m1 = max3f(m1, __uint_as_float(x[12]), __uint_as_float(x[13]));
+                        m0 = max3f(m0, __uint_as_float(x[14]), __uint_as_float(x[15]));
+                        const float mul = capped ? 1.0f : (h ? mo.y : mo.x);
+                        mg[2 * c + h] = fmaf(fmaxf(m0, m1), mul, h ? mo.w : mo.z);
+                    }
+                }
+                mxs = max3f(max3f(mg[0], mg[1], mg[2]), max3f(mg[3], mg[4], mg[5]),
+                            fmaxf(mg[6], mg[7]));
+            } else {
             float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; c++)
@@ -764,29 +955,46 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                     mxd = max3f(mxd, __uint_as_float(sr[c][i + 6]), __uint_as_float(sr[c][i + 7]));
                 }
             const float mx = max3f(mxa, mxb, fmaxf(mxc, mxd));
-            const float mxs = mx * sl2;
+            mxs = mx * sl2;
+            }
             float alpha = 1.f;
             bool corr = false;
-            if (mxs > m_ref + 8.0f) {
-                alpha = (m_ref == -INFINITY) ? 0.f : ex2_mufu(m_ref - mxs);
+            constexpr float TOP = E4M3 ? kF16Top : 0.f, LIMIT = E4M3 ? kF16Limit : 8.0f;
+            if (mxs > m_ref + LIMIT) {
+                alpha = (m_ref == -INFINITY) ? 0.f : ex2_mufu(m_ref - (mxs - TOP));
                 corr = (m_ref != -INFINITY);
-                m_ref = mxs;
+                m_ref = mxs - TOP;
             }
             const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
-            const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(neg_m, neg_m);
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; c++) {
                 uint32_t pk[16];
+                float4 mo = mul_off(c);
+                float2 inv;
+                if constexpr (E4M3)
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                                 : "=f"(inv.x), "=f"(inv.y)
+                                 : "r"(smem_addr(&sm.v_inv[j % SCALE_SLOTS][c])));
+                if constexpr (E4M3 && capped)
+                    mo.x = mo.y = 1.0f;
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
+                    const float sc = E4M3 ? (i < 8 ? mo.x : mo.y) : sl2;
+                    const float nm = E4M3 ? neg_m + (i < 8 ? mo.z : mo.w) : neg_m;
                     const float2 x = __ffma2_rn(
                         make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])),
-                        sc2, nm2);
+                        make_float2(sc, sc), make_float2(nm, nm));
                     const float2 pp = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
-                    acc[i & 3] = __fadd2_rn(acc[i & 3], pp);
-                    pk[i] = pack_bf16x2(pp.x, pp.y);
+                    if constexpr (E4M3) {
+                        const float w = i < 8 ? inv.x : inv.y;
+                        acc[i & 3] = __ffma2_rn(pp, make_float2(w, w), acc[i & 3]);
+                        pk[i] = pack_f16x2(pp.x, pp.y);
+                    } else {
+                        acc[i & 3] = __fadd2_rn(acc[i & 3], pp);
+                        pk[i] = pack_bf16x2(pp.x, pp.y);
+                    }
                 }
                 tc::tmem_st16(s_t + c * 16, pk);
             }
@@ -797,10 +1005,10 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             if (!E4M3 && (j0 + BN > k_end || (PAGED && j0 < vis_lo))) {
                 // Key rows past the valid range hold whatever the cache has there
                 // (and with pages so do those before the window: their page may
-                // be gone); zero them so P * V sees no non-finite values.  E4M3
-                // bytes never read as one.
-                const int st = j % STAGES;
-                if (!warp_wait(&sm.v_full[st], (j / STAGES) & 1, &sm.abort_flag)) {
+                // be gone); zero them so P * V sees no non-finite values.  (E4M3:
+                // the converting warps do.)
+                const int st = j % VST;
+                if (!warp_wait(&sm.v_full[st], (j / VST) & 1, &sm.abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -850,7 +1058,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         }
         // This warp's gate rows, requested now so their latency overlaps the
         // last P V product.
-        if (ok && gated_out)
+        if (!E4M3 && ok && gated_out)
             load_gate();
         if (!ok) {
             if (lane == 0)
@@ -889,6 +1097,8 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             set_abort(&sm.abort_flag, p.status);
         }
     }
+    if (E4M3 && warp < 8 && gated_out)
+        load_gate();
 
     tc::fence_before_sync();
     __syncthreads();  // the staged rows are complete (unless a wait gave up)
@@ -1161,8 +1371,8 @@ cudaError_t launch_prefill_t(const PrefillParams &p, const PagedView &pg, int to
         const cuuint64_t dims[2] = {(cuuint64_t)D, rows};
         const cuuint64_t strides[1] = {(cuuint64_t)D * (e4m3 ? 1 : 2)};
         const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? D : 64), 1u << pg.page_log};
-        const bool ok = e4m3 ? make_u8_tile_map(&mk, p.cache_k, 2, dims, strides, box, false) &&
-                                   make_u8_tile_map(&mv, p.cache_v, 2, dims, strides, box, false)
+        const bool ok = e4m3 ? make_u8_tile_map(&mk, p.cache_k, 2, dims, strides, box, true) &&
+                                   make_u8_tile_map(&mv, p.cache_v, 2, dims, strides, box, D == 128)
                              : make_bf16_tile_map(&mk, p.cache_k, 2, dims, strides, box) &&
                                    make_bf16_tile_map(&mv, p.cache_v, 2, dims, strides, box);
         if (!ok)

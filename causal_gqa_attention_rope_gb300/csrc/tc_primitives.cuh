@@ -22,7 +22,7 @@ namespace tc {
 
 // ----------------------------------------------------------- descriptors --
 
-enum : uint32_t { kSwizzleNone = 0, kSwizzle128B = 2 };
+enum : uint32_t { kSwizzleNone = 0, kSwizzle128B = 2, kSwizzle64B = 4 };
 
 // Shared-memory matrix descriptor (tcgen05): start address, leading and
 // stride byte offsets (16-byte units), descriptor version 1, swizzle mode.
@@ -44,6 +44,15 @@ __device__ __forceinline__ uint64_t desc_kmajor_sw128(uint32_t addr)
     return smem_desc(addr, 16, 1024, kSwizzle128B);
 }
 
+// K-major tile of rows of D bytes, swizzled within the row (128 or 64 bytes):
+// 8-row groups 8 D bytes apart.
+template <int D>
+__device__ __forceinline__ uint64_t desc_kmajor_bytes(uint32_t addr)
+{
+    static_assert(D == 128 || D == 64, "one swizzle span per row");
+    return smem_desc(addr, 16, 8 * D, D == 128 ? kSwizzle128B : kSwizzle64B);
+}
+
 // MN-major, 128-byte swizzled tile: K rows of 64 bf16 (128 B), 8-row groups
 // 1024 B apart, consecutive 64-wide N blocks `n_block_bytes` apart.
 __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t addr, uint32_t n_block_bytes)
@@ -62,6 +71,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
            | ((b_mn_major ? 1u : 0u) << 16)            // B major-ness
            | ((uint32_t)(N >> 3) << 17)                // N / 8
            | ((uint32_t)(M >> 4) << 24);               // M / 16
+}
+
+// The same for f16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major)
+{
+    return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: E4M3 A and B (format 0),
+// fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // --------------------------------------------------------- tensor memory --
@@ -150,6 +172,18 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// The same for byte operands (E4M3), 32 of them along K per instruction.
+__device__ __forceinline__ void mma_ss_bytes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }

@@ -111,8 +111,9 @@ typedef struct na_kv_cache {
 #define NA_KV_BF16 0
 #define NA_KV_E4M3 1 /* 8-bit floating point (4 exponent, 3 fraction bits, largest 448) with one
                         scale per (page, kv head): a stored byte b stands for b * 2^(s - 127),
-                        s the E8M0 scale byte (0 .. 254).  Bytes 0x7f and 0xff, E4M3's NaN, read as
-                        +-480 in the attention calls. */
+                        s the E8M0 scale byte (0 .. 254).  The attention calls take V's scales
+                        down to 2^-40 exactly (values of smaller ones are rounded to multiples of
+                        2^-64) and report one above 2^47 as NA_ERR_UNSUPPORTED. */
 
 /*
  * Caller-owned paged cache: a pool of pages and a page table.  Position pos of
@@ -361,8 +362,10 @@ int na_rope_append_kv_paged(const na_attn_cfg *cfg, const na_rope_params *rope, 
 
 /*
  * na_attn_decode over a paged cache: one query per sequence, the same arithmetic
- * (E4M3 values become bf16 exactly; K's scale is applied to the scores in fp32,
- * V's to the probabilities, exactly), the same outputs and probabilities.
+ * (E4M3 values are f16 numbers exactly, and so, but for elements below 2^-33 of
+ * its largest, is a query scaled by a power of two; K's scale is applied to the
+ * scores in fp32, V's in the exponent of the weights, which are rounded to f16),
+ * the same outputs and probabilities.
  *
  *   max_kv_len  HOST upper bound of kv_lens; <= pages_per_seq * page_size.
  *   num_splits, workspace, probs, gate, status: as in na_attn_decode, with
@@ -375,9 +378,11 @@ int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_ro
                          size_t ws_bytes, int32_t *status, void *stream);
 
 /*
- * na_attn_prefill_chunk over a paged cache: the same arithmetic and outputs; E4M3
- * values (their scale multiplied in) are bf16 numbers exactly, and the products
- * are those of the bf16 cache that holds them.
+ * na_attn_prefill_chunk over a paged cache: the same arithmetic and outputs.  With
+ * E4M3 pages K is multiplied as it is stored, a query element as the sum of two
+ * E4M3 numbers (exact down to 2^-10 of the row's largest magnitude, within 2^-17
+ * of that below), V as the f16 number that it exactly is, by weights rounded to
+ * f16 with V's scale in their exponent.
  *
  *   max_total_len  HOST upper bound of cache_lens[b] + new length;
  *                  <= pages_per_seq * page_size.

@@ -100,17 +100,6 @@ def values(pool, scale, ids) -> torch.Tensor:
     return x.permute(1, 0, 2, 3).reshape(x.shape[1], -1, x.shape[3])
 
 
-def dequantised(c: Paged) -> Paged:
-    """The bf16 cache that an E4M3 cache stands for (exact)."""
-    def one(pool, scale):
-        x = pool.double() * torch.exp2(scale.double() - 127)[..., None, None]
-        y = x.to(torch.bfloat16)
-        ok = torch.isfinite(x)
-        assert torch.equal(y.double()[ok], x[ok])
-        return y
-    return Paged(one(c.k, c.k_scale), one(c.v, c.v_scale), c.table, None, None)
-
-
 @dataclass
 class Rows:
     out: torch.Tensor     # [T, H, d] fp64
@@ -129,7 +118,11 @@ def attend(c: Paged, q: torch.Tensor, spans, scale=None, softcap=0.0, window=0, 
     scale * sum |q k| of the row, which is a relative error of p, entering
     numerator and sum: 2 (d + 8) 2^-24 S A.  exp2 and the sigmoid on the special
     function unit, the sum of p and the merge: 2^-16 A.  The soft cap's tanh adds
-    an absolute 2^-19 cap to a score."""
+    an absolute 2^-19 cap to a score.  Over E4M3 pages the chunk call takes a query
+    as the sum of two E4M3 numbers per element: exact, or below 2^-10 of the row's
+    largest within 2^-17 of that, which adds 2^-17 max|q| scale sum |k| to a score;
+    and V values with a scale below 2^-40 are multiples of 2^-64 (2^-65 of output).
+    The weights' rounding to f16 there is finer than bf16's."""
     T, H, d = q.shape
     KV = c.k.shape[1]
     G = H // KV
@@ -153,6 +146,8 @@ def attend(c: Paged, q: torch.Tensor, spans, scale=None, softcap=0.0, window=0, 
             qi = q[row + i].double().view(KV, G, d)
             s = torch.einsum("kgd,knd->kgn", qi, k1) * sc
             eps = (d + 8) * 2.0 ** -24 * sc * torch.einsum("kgd,knd->kgn", qi.abs(), k1.abs()).amax(-1)
+            if c.k_scale is not None:
+                eps = eps + 2.0 ** -17 * sc * qi.abs().amax(-1) * k1.abs().sum(-1).amax(-1)[:, None]
             if softcap > 0:
                 s = softcap * torch.tanh(s / softcap)
                 eps = eps + 2.0 ** -19 * softcap
@@ -161,6 +156,8 @@ def attend(c: Paged, q: torch.Tensor, spans, scale=None, softcap=0.0, window=0, 
             a = torch.einsum("kgn,knd->kgd", p, v1.abs())
             rel = (2 * eps + 2.0 ** -16)[..., None]
             t = 2.0 ** -8 * o.abs() + a * (2.0 ** -8 + rel)
+            if c.v_scale is not None:
+                t = t + 2.0 ** -65
             if gate is not None:
                 g = torch.sigmoid(gate[row + i].double()).view(KV, G, d)
                 o, t = o * g, t * g

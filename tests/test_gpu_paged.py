@@ -7,8 +7,7 @@ import torch
 
 import causal_gqa_attention_rope_gb300 as na
 from harness import Guarded
-from paged_ref import (Paged, attend, bits, dequantised, exponent, make_paged, normed_rotated,
-                       v_normed, values)
+from paged_ref import (Paged, attend, bits, exponent, make_paged, normed_rotated, v_normed)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -300,6 +299,10 @@ PREFILL = [
     ("e4m3", 128, 32, 1, 1, [(4000, 64)], {}),
     ("e4m3", 128, 128, 1, 2, [(250, 300)], dict(window=260)),
     ("e4m3", 64, 16, 1, 1, [(5000, 2)], {}),
+    # several waves of units, more tiles each than any ring holds
+    ("e4m3", 128, 16, 4, 4, [(1400 + 17 * i, 1 + i % 5) for i in range(60)], {}),
+    ("bf16", 128, 32, 4, 4, [(1400 + 17 * i, 1 + i % 5) for i in range(60)], {}),
+    ("e4m3", 64, 64, 4, 2, [(2000 - 11 * i, 1 + i % 3) for i in range(45)], dict(gate=True)),
 ]
 
 
@@ -334,7 +337,7 @@ def prefill_case(case, seed):
     return cfg, cache, q, gate, prior, new, [(starts[b], p, n) for b, (p, n) in enumerate(seqs)]
 
 
-@pytest.mark.parametrize("case", PREFILL, ids=lambda c: f"{c[0]}d{c[1]}p{c[2]}g{c[4]}")
+@pytest.mark.parametrize("case", PREFILL, ids=lambda c: f"{c[0]}d{c[1]}p{c[2]}g{c[4]}b{len(c[5])}")
 def test_prefill(case):
     cfg, cache, q, gate, prior, new, spans = prefill_case(case, 31)
     out, status = run_prefill(cfg, q, cache.to(DEV), prior, new, gate)
@@ -343,16 +346,7 @@ def test_prefill(case):
     check(out, ref.out, ref.tol, "out")
 
 
-@pytest.mark.parametrize("case", [c for c in PREFILL if c[0] == "e4m3"],
-                         ids=lambda c: f"d{c[1]}p{c[2]}g{c[4]}")
-def test_prefill_e4m3_is_the_bf16_cache_it_stands_for(case):
-    cfg, cache, q, gate, prior, new, _ = prefill_case(case, 33)
-    a, _ = run_prefill(cfg, q, cache.to(DEV), prior, new, gate)
-    b, _ = run_prefill(cfg, q, dequantised(cache).to(DEV), prior, new, gate)
-    assert torch.equal(bits(a), bits(b))
-
-
-@pytest.mark.parametrize("e", [-100, -20, 8, 30, 100])
+@pytest.mark.parametrize("e", [-100, -45, -20, 8, 30, 50])
 def test_prefill_e4m3_scales_far_from_one(e):
     """V's scale far from one on every page (K's stays at unit scale)."""
     case = ("e4m3", 128, 64, 1, 2, [(300, 40)], {})
@@ -362,6 +356,37 @@ def test_prefill_e4m3_scales_far_from_one(e):
     out, status = run_prefill(cfg, q, cache.to(DEV), prior, new)
     assert status == 0
     ref = attend(cache, q, spans)
+    check(out, ref.out, ref.tol, "out")
+
+
+def test_v_scale_above_the_largest_is_reported():
+    cache = make_paged([40], 1, 64, 16, "e4m3", 36)
+    cache.v_scale[cache.v_scale != 255] = 127 + 48
+    g = torch.Generator().manual_seed(37)
+    cfg, q = na.AttnConfig(2, 1, 64), rnd(g, 1, 2, 64)
+    assert run_decode(cfg, q, cache.to(DEV), [40])[2] == na.NA_ERR_UNSUPPORTED
+    assert run_prefill(cfg, q, cache.to(DEV), [39], [1])[1] == na.NA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", ["decode", "prefill"])
+def test_pages_of_zeros(call):
+    """Pages whose K or V is all zero have scale byte 0 (2^-127): they still weigh in
+    the softmax, alone or beside other pages."""
+    lens, KV, d, page = [100, 32, 200], 2, 64, 16
+    cache = make_paged(lens, KV, d, page, "e4m3", 38)
+    for b, pages in ((0, [1, 3]), (1, [0, 1]), (2, [12])):
+        for i in pages:
+            pid = int(cache.table[b, i])
+            for pool, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+                pool.view(torch.uint8)[pid], scale[pid] = 0, 0
+    g = torch.Generator().manual_seed(39)
+    cfg, q = na.AttnConfig(4, KV, d), rnd(g, 3, 4, d)
+    if call == "decode":
+        out, _, status = run_decode(cfg, q, cache.to(DEV), lens)
+    else:
+        out, status = run_prefill(cfg, q, cache.to(DEV), [n - 1 for n in lens], [1] * 3)
+    assert status == 0
+    ref = attend(cache, q, [(b, n - 1, 1) for b, n in enumerate(lens)])
     check(out, ref.out, ref.tol, "out")
 
 
