@@ -592,10 +592,18 @@ __global__ void __launch_bounds__(kCombThreads) decode_combine_kernel(const Deco
         for (int u = 0; u < PO; u++)
             if (mo[u] != -INFINITY)
                 o += xo[u] * exp2f(mo[u] - M);
-        for (int s = PO; s < ns; s++) {
-            const float m = ml[2 * hpc * s];
-            if (m != -INFINITY)
-                o += po[(size_t)s * hpc * D + e0] * exp2f(m - M);
+        for (int s0 = PO; s0 < ns; s0 += 8) {  // eight pieces' loads in flight, added in order
+            float m[8], x[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const int s = min(s0 + u, ns - 1);
+                m[u] = ml[2 * hpc * s];
+                x[u] = po[(size_t)s * hpc * D + e0];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                if (s0 + u < ns && m[u] != -INFINITY)
+                    o += x[u] * exp2f(m[u] - M);
         }
         o *= inv_l;
         if ((p.flags & NA_OUT_GATE) && p.gate)

@@ -8,10 +8,9 @@
 // HPC <= 8 query heads at a time: the pass is bound by HBM, and what it has to
 // avoid is spending more time on instructions than the bytes take.
 //
-// The producer warp keeps the page ids (and scales) of the next 64 pages in
-// registers, one page per lane and batch, the second batch loading while the
-// first is used; each lane then issues one box of a tile: a page's rows, or 64
-// of them, by 128 bytes.  A tile is 64 keys aligned to 64 positions, so a box
+// The producer warp keeps the page ids (and scales) of 32 pages at a time in
+// registers, one page per lane, the next windows' loading meanwhile; each lane
+// then issues one box of a tile: a page's rows, or 64 of them, by 128 bytes.  A tile is 64 keys aligned to 64 positions, so a box
 // never leaves its page and the 16 keys of a consumer warp always share one
 // page, hence one scale pair, which the producer hands over with the tile.
 //
@@ -51,9 +50,8 @@ struct __align__(1024) PagedSmem {
     static constexpr uint32_t TILE_BYTES = TILE * ROW;
     uint8_t k[ST][TILE_BYTES];
     uint8_t v[ST][TILE_BYTES];
-    float obuf[MAX_HPC][D];  // the warps' partial outputs, added in warp order
-    float merge_m[CWARPS][MAX_HPC];
-    float merge_l[CWARPS][MAX_HPC];
+    // partial results on their way to another warp: [output quads, (max, sum)][lane]
+    float4 merge[CWARPS - 1][D / 16 + 1][32];
     uint16_t scales[ST][CWARPS];  // a warp's K | V << 8 scale bytes in each stage (E4M3)
     uint64_t full[ST];
     uint64_t empty[ST];
@@ -73,33 +71,73 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c)
         return (uint32_t)((c >> 3) * (TILE * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// One page as the producer keeps it: its id (-1: holds no key of the piece)
-// and the scale bytes of its K and V.
-struct PageEntry {
-    int id;
-    uint32_t scales;  // K's byte | V's byte << 8
+// The page windows that the producer walks: 32 consecutive pages of a piece,
+// one per lane, piece after piece.  A second walker runs ahead of the tiles, so
+// that a window's ids are requested two windows early and its scales one: the
+// producer never waits for a load it has just issued, but at its start.
+struct WindowIds {
+    int id;       // this lane's page, as the table has it (in flight)
+    bool wanted;  // the page holds keys of the piece
+    int wb, kvh;  // the window's first page; the piece's kv head
 };
 
+struct Window {
+    int id;           // this lane's page (-1: not wanted)
+    uint32_t ks, vs;  // the scale bytes of its K and V (in flight at first)
+    int wb;
+};
+
+struct WindowIter {
+    Walker walk;
+    Piece pc;
+    int wb, p_lo, p_hi;  // the window's first page, the piece's first and last
+    bool valid;
+
+    __device__ __forceinline__ void start(const Slice &sl, const DecodeParams &p)
+    {
+        walk.init(sl, p);
+        wb = 0;
+        p_hi = -1;
+        valid = true;
+    }
+
+    template <int TILE>
+    __device__ __forceinline__ WindowIds next(const DecodeParams &p, const PagedView &pg, int lane)
+    {
+        wb += 32;
+        if (valid && wb > p_hi && (valid = walk.next(p, pc))) {
+            const int lo = pc.kf + pc.k0;
+            wb = (lo / TILE * TILE) >> pg.page_log;
+            p_lo = lo >> pg.page_log;
+            p_hi = (pc.kf + pc.k1 - 1) >> pg.page_log;
+        }
+        const int i = wb + lane;
+        WindowIds w{0, valid && i >= p_lo && i <= p_hi, wb, pc.kvh};
+        if (w.wanted)
+            w.id = __ldcg(pg.table + (size_t)pc.b * pg.pages_per_seq + i);
+        return w;
+    }
+};
+
+// A window's ids checked (one outside the cache is reported, and page 0 read
+// instead) and its scales requested.
 template <bool E4M3>
-__device__ __forceinline__ PageEntry page_entry(const DecodeParams &p, const PagedView &pg,
-                                                const int32_t *row, int i, int lo, int hi, int kvh)
+__device__ __forceinline__ Window open_window(const DecodeParams &p, const PagedView &pg,
+                                              const WindowIds &ids)
 {
-    PageEntry e{-1, 0x7f7fu};
-    if (i >= lo && i <= hi) {
-        e.id = __ldcg(row + i);
-        if ((unsigned)e.id >= (unsigned)pg.num_pages) {  // reported; read page 0 instead
+    Window w{-1, 127u, 127u, ids.wb};
+    if (ids.wanted) {
+        w.id = ids.id;
+        if ((unsigned)w.id >= (unsigned)pg.num_pages) {
             na_report(p.status, NA_ERR_PAGE);
-            e.id = 0;
+            w.id = 0;
         }
         if constexpr (E4M3) {
-            const size_t at = (size_t)e.id * p.KV + kvh;
-            const uint32_t vs = __ldcg(pg.v_scale + at);
-            if ((int)vs - 127 > kTopVExp)
-                na_report(p.status, NA_ERR_UNSUPPORTED);
-            e.scales = (uint32_t)__ldcg(pg.k_scale + at) | (vs << 8);
+            w.ks = __ldcg(pg.k_scale + (size_t)w.id * p.KV + ids.kvh);
+            w.vs = __ldcg(pg.v_scale + (size_t)w.id * p.KV + ids.kvh);
         }
     }
-    return e;
+    return w;
 }
 
 template <int D, bool E4M3, bool CAPPED>
@@ -151,22 +189,30 @@ __global__ void __launch_bounds__(THREADS, 2)
         // this lane's box of a tile: rows [bi << box_log, ...), column block bc, of K or of V
         const int bi = lane & (nbox - 1), bc = (lane / nbox) % COLS, bt = lane / (nbox * COLS);
         const uint32_t box_bytes = Smem::BOX << box_log;
+        WindowIter iter;
+        iter.start(sm.slice, p);
+        WindowIds ids = iter.next<TILE>(p, pg, lane);
+        WindowIds ids1 = iter.next<TILE>(p, pg, lane);
+        Window nxt = open_window<E4M3>(p, pg, ids), cur = nxt;
+        ids = ids1;
+        ids1 = iter.next<TILE>(p, pg, lane);
+        auto advance = [&]() {
+            cur = nxt;
+            nxt = open_window<E4M3>(p, pg, ids);
+            ids = ids1;
+            ids1 = iter.next<TILE>(p, pg, lane);
+            if (E4M3 && (int)cur.vs - 127 > kTopVExp)
+                na_report(p.status, NA_ERR_UNSUPPORTED);
+        };
         uint32_t it = 0;
         bool ok = true;
         while (ok && walk.next(p, pc)) {
             const int lo = pc.kf + pc.k0, hi = pc.kf + pc.k1;
-            const int p_lo = lo >> pg.page_log, p_hi = (hi - 1) >> pg.page_log;
-            const int32_t *row = pg.table + (size_t)pc.b * pg.pages_per_seq;
-            int wb = (lo / TILE * TILE) >> pg.page_log;  // page of lane 0's entry
-            PageEntry cur = page_entry<E4M3>(p, pg, row, wb + lane, p_lo, p_hi, pc.kvh);
-            PageEntry nxt = page_entry<E4M3>(p, pg, row, wb + 32 + lane, p_lo, p_hi, pc.kvh);
+            advance();
             for (int t0 = lo / TILE * TILE; t0 < hi; t0 += TILE, it++) {
                 const int stage = it % ST;
-                if ((t0 >> pg.page_log) - wb >= 32) {
-                    cur = nxt;
-                    wb += 32;
-                    nxt = page_entry<E4M3>(p, pg, row, wb + 32 + lane, p_lo, p_hi, pc.kvh);
-                }
+                if ((t0 >> pg.page_log) - cur.wb >= 32)
+                    advance();
                 const bool free = mbar_wait_bounded(&sm.empty[stage], ((it / ST) & 1) ^ 1) &&
                                   !*(volatile int *)&sm.abort_flag;
                 if (!__all_sync(FULL, free)) {
@@ -178,12 +224,13 @@ __global__ void __launch_bounds__(THREADS, 2)
                     break;
                 }
                 const int pos = t0 + (bi << box_log);
-                const int id = __shfl_sync(FULL, cur.id, ((pos >> pg.page_log) - wb) & 31);
+                const int id = __shfl_sync(FULL, cur.id, ((pos >> pg.page_log) - cur.wb) & 31);
                 const bool mine = bt < 2 && id >= 0;
                 const uint32_t n = __popc(__ballot_sync(FULL, mine));
                 if constexpr (E4M3) {
                     const int kp = t0 + 16 * (lane & 3);
-                    const uint32_t sc = __shfl_sync(FULL, cur.scales, ((kp >> pg.page_log) - wb) & 31);
+                    const uint32_t sc = __shfl_sync(FULL, cur.ks | (cur.vs << 8),
+                                                    ((kp >> pg.page_log) - cur.wb) & 31);
                     if (lane < CWARPS)
                         sm.scales[stage][lane] = (uint16_t)sc;
                 }
@@ -383,18 +430,18 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (inb)
                     prow1[pb] = sc[3];
             }
-            // Tile maximum per head (over the 8 lanes sharing the column), then
-            // (rarely) raise the reference maximum.  E4M3: of score + V's exponent,
-            // and the reference stays kF16Top below it.
-            float mx0 = fmaxf(sc[0], sc[2]) + v_off, mx1 = fmaxf(sc[1], sc[3]) + v_off;
-#pragma unroll
-            for (int m = 4; m < 32; m <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(FULL, mx0, m));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(FULL, mx1, m));
-            }
+            // When a score exceeds its head's reference by too much (rarely) the
+            // reference is raised to the tile's maximum, over the 8 lanes sharing the
+            // column.  E4M3: of score + V's exponent, and the reference stays kF16Top
+            // below it.
             constexpr float TOP = E4M3 ? kF16Top : 0.f, LIMIT = E4M3 ? kF16Limit : kRescaleThreshold;
-            const bool raise = mx0 > m_ref[0] + LIMIT || mx1 > m_ref[1] + LIMIT;
-            if (__any_sync(FULL, raise)) {  // warp-uniform
+            float mx0 = fmaxf(sc[0], sc[2]) + v_off, mx1 = fmaxf(sc[1], sc[3]) + v_off;
+            if (__any_sync(FULL, mx0 > m_ref[0] + LIMIT || mx1 > m_ref[1] + LIMIT)) {
+#pragma unroll
+                for (int m = 4; m < 32; m <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(FULL, mx0, m));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(FULL, mx1, m));
+                }
                 const float n0 = fmaxf(m_ref[0], mx0 - TOP), n1 = fmaxf(m_ref[1], mx1 - TOP);
                 const float a0 = (m_ref[0] == -INFINITY) ? 0.f : exp2f(m_ref[0] - n0);
                 const float a1 = (m_ref[1] == -INFINITY) ? 0.f : exp2f(m_ref[1] - n1);
@@ -463,88 +510,84 @@ __global__ void __launch_bounds__(THREADS, 2)
             if (lane == 0)
                 mbar_arrive(&sm.empty[stage]);
         }
-        // Sums over the 8 lanes of each column; then the warps' partials are
-        // merged in warp order.
+        // Sums over the 8 lanes of each column; then the warps' partials are merged
+        // pairwise, 1 into 0 and 3 into 2, 2 into 0.  Lane l of every warp holds the
+        // same heads and d, so a partial crosses as one float4 per lane and step,
+        // and the order of the additions is fixed.  (Adding warp after warp into
+        // one buffer of rows, as the contiguous pass does, took ~10 us a piece.)
 #pragma unroll
         for (int m = 4; m < 32; m <<= 1) {
             l_sum[0] += __shfl_xor_sync(FULL, l_sum[0], m);
             l_sum[1] += __shfl_xor_sync(FULL, l_sum[1], m);
         }
-        if (g == 0) {
-            if (v0) {
-                sm.merge_m[warp][h0] = m_ref[0];
-                sm.merge_l[warp][h0] = l_sum[0];
+        auto give = [&](float4 (*buf)[32]) {
+#pragma unroll
+            for (int s = 0; s < KS; s++)
+                buf[s][lane] = make_float4(acc[s][0], acc[s][1], acc[s][2], acc[s][3]);
+            buf[KS][lane] = make_float4(m_ref[0], m_ref[1], l_sum[0], l_sum[1]);
+        };
+        auto take = [&](const float4 (*buf)[32]) {
+            const float4 o = buf[KS][lane];
+            const float om[2] = {o.x, o.y}, ol[2] = {o.z, o.w};
+            float fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const float m = fmaxf(m_ref[i], om[i]);
+                fa[i] = m_ref[i] == -INFINITY ? 0.f : exp2f(m_ref[i] - m);
+                fb[i] = om[i] == -INFINITY ? 0.f : exp2f(om[i] - m);
+                m_ref[i] = m;
+                l_sum[i] = l_sum[i] * fa[i] + ol[i] * fb[i];
             }
-            if (v1) {
-                sm.merge_m[warp][h1] = m_ref[1];
-                sm.merge_l[warp][h1] = l_sum[1];
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                const float4 x = buf[s][lane];
+                acc[s][0] = acc[s][0] * fa[0] + x.x * fb[0];
+                acc[s][1] = acc[s][1] * fa[1] + x.y * fb[1];
+                acc[s][2] = acc[s][2] * fa[0] + x.z * fb[0];
+                acc[s][3] = acc[s][3] * fa[1] + x.w * fb[1];
             }
-        }
+        };
+        if (warp & 1)
+            give(sm.merge[warp >> 1]);
         named_barrier_sync(1, CWARPS * 32);
-        float M0 = -INFINITY, M1 = -INFINITY;
-        if (v0)
-#pragma unroll
-            for (int ww = 0; ww < CWARPS; ww++)
-                M0 = fmaxf(M0, sm.merge_m[ww][h0]);
-        if (v1)
-#pragma unroll
-            for (int ww = 0; ww < CWARPS; ww++)
-                M1 = fmaxf(M1, sm.merge_m[ww][h1]);
-        const float f0 = (m_ref[0] == -INFINITY) ? 0.f : exp2f(m_ref[0] - M0);
-        const float f1 = (m_ref[1] == -INFINITY) ? 0.f : exp2f(m_ref[1] - M1);
-        // acc row l/4 is d = 16 s + l/4 and row l/4 + 8 is 8 further on (bf16),
-        // or d = 16 s + 2 (l/4) and the next one (E4M3).
-        const int e0 = E4M3 ? 2 * g : g;
-        constexpr int E1 = E4M3 ? 1 : 8;
-        for (int ww = 0; ww < CWARPS; ww++) {
-            if (warp == ww) {
-#pragma unroll
-                for (int s = 0; s < KS; s++) {
-                    const int e = 16 * s + e0;
-                    if (v0) {
-                        float *o0 = &sm.obuf[h0][e];
-                        o0[0] = ww == 0 ? acc[s][0] * f0 : o0[0] + acc[s][0] * f0;
-                        o0[E1] = ww == 0 ? acc[s][2] * f0 : o0[E1] + acc[s][2] * f0;
-                    }
-                    if (v1) {
-                        float *o1 = &sm.obuf[h1][e];
-                        o1[0] = ww == 0 ? acc[s][1] * f1 : o1[0] + acc[s][1] * f1;
-                        o1[E1] = ww == 0 ? acc[s][3] * f1 : o1[E1] + acc[s][3] * f1;
-                    }
-                }
-            }
-            named_barrier_sync(1, CWARPS * 32);
-        }
+        if (!(warp & 1))
+            take(sm.merge[warp >> 1]);
+        if (warp == 2)
+            give(sm.merge[2]);
+        named_barrier_sync(1, CWARPS * 32);
+        // (Warps 1 and 3 write again after this barrier, which the readers of their
+        // buffers have passed; warp 2 after the next piece's first one.)
+        if (warp != 0)
+            continue;
+        take(sm.merge[2]);
         // Every consumer warp has finished this piece's tiles (or given up): the
         // abort flag is final for the piece, and a piece of a CTA whose wait gave
         // up is written as the marker (max -inf, sum -1) that the merge pass reports.
         const bool bad = *(volatile int *)&sm.abort_flag != 0;
-        for (int idx = threadIdx.x; idx < hpc * D; idx += CWARPS * 32) {
-            const int h = idx / D, e = idx - h * D;
-            const size_t row = (size_t)pc.id * hpc + h;
-            if (bad) {
-                if (e == 0) {
-                    p.part_ml[row * 2] = -INFINITY;
-                    p.part_ml[row * 2 + 1] = -1.0f;
-                }
-                continue;
-            }
-            p.part_o[row * D + e] = sm.obuf[h][e];
-            if (e == 0) {
-                float M = -INFINITY;
+        // acc row l/4 is d = 16 s + l/4 and row l/4 + 8 is 8 further on (bf16),
+        // or d = 16 s + 2 (l/4) and the next one (E4M3).
+        float *po = p.part_o + (size_t)pc.id * hpc * D;
+        float *ml = p.part_ml + (size_t)pc.id * hpc * 2;
 #pragma unroll
-                for (int ww = 0; ww < CWARPS; ww++)
-                    M = fmaxf(M, sm.merge_m[ww][h]);
-                float l = 0.f;
+        for (int i = 0; i < 2; i++) {
+            const int h = h0 + i;
+            if (h >= hpc)
+                break;
+            if (!bad) {
 #pragma unroll
-                for (int ww = 0; ww < CWARPS; ww++) {
-                    const float mw = sm.merge_m[ww][h];
-                    if (mw != -INFINITY)
-                        l += sm.merge_l[ww][h] * exp2f(mw - M);
+                for (int s = 0; s < KS; s++) {
+                    float *o = po + h * D + 16 * s + (E4M3 ? 2 * g : g);
+                    if constexpr (E4M3) {
+                        *reinterpret_cast<float2 *>(o) = make_float2(acc[s][i], acc[s][2 + i]);
+                    } else {
+                        o[0] = acc[s][i];
+                        o[8] = acc[s][2 + i];
+                    }
                 }
-                p.part_ml[row * 2] = M;
-                p.part_ml[row * 2 + 1] = l;
             }
+            if (g == 0)
+                *reinterpret_cast<float2 *>(ml + 2 * h) =
+                    bad ? make_float2(-INFINITY, -1.0f) : make_float2(m_ref[i], l_sum[i]);
         }
         if (threadIdx.x == 0) {  // the span follows from the slicing alone: always written
             const int stream = pc.id - blockIdx.x;
@@ -553,7 +596,6 @@ __global__ void __launch_bounds__(THREADS, 2)
             if (pc.last)
                 p.piece_span[2 * stream + 1] = pc.id;
         }
-        named_barrier_sync(1, CWARPS * 32);
     }
 }
 
