@@ -209,10 +209,11 @@ class PagedKVCache:
     v_scale: "object" = None
 
     def c(self) -> na_paged_kv_cache:
+        num_pages, _, page_size, _ = self.k.shape
+        batch, pages_per_seq = self.page_table.shape
         return na_paged_kv_cache(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
-                                 _ptr(self.v_scale), _ptr(self.page_table), int(self.k.shape[0]),
-                                 int(self.k.shape[2]), int(self.page_table.shape[0]),
-                                 int(self.page_table.shape[1]),
+                                 _ptr(self.v_scale), _ptr(self.page_table), num_pages, page_size,
+                                 batch, pages_per_seq,
                                  NA_KV_BF16 if self.k_scale is None else NA_KV_E4M3)
 
 
@@ -229,21 +230,48 @@ def _ptr(t) -> Optional[int]:
 
 
 _current_stream = None
+_current_device = None
+
+
+def _find_current():
+    """Set the lookups of the current device and of its current stream."""
+    global _current_stream, _current_device
+    import torch
+    torch.cuda.current_device()  # initialises CUDA
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:  # the handle alone, without building a Stream object
+        _current_stream = lambda: raw(_current_device())
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream
 
 
 def _stream(stream) -> Optional[int]:
     """Raw handle of `stream`, or of the current device's current stream."""
-    global _current_stream
     if stream is not None:
         return stream.cuda_stream
     if _current_stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:  # the handle alone, without building a Stream object
-            _current_stream = lambda: raw(torch.cuda.current_device())
-        else:
-            _current_stream = lambda: torch.cuda.current_stream().cuda_stream
+        _find_current()
     return _current_stream()
+
+
+def _stream_for(t, stream) -> Optional[int]:
+    """The same for a call whose tensors have to be on the current device, as t is."""
+    if _current_device is None:
+        _find_current()
+    if t.get_device() != _current_device():
+        raise ValueError(f"tensors on cuda:{t.get_device()}, but the current device is "
+                         f"cuda:{_current_device()}")
+    return _current_stream() if stream is None else stream.cuda_stream
+
+
+_dtypes = {}  # torch's dtype objects by name
+
+
+def _dtype(name: str):
+    import torch
+    _dtypes[name] = getattr(torch, name)
+    return _dtypes[name]
 
 
 def _want(t, name: str, dtype: str, shape=None, min_rows: int = 0):
@@ -253,17 +281,21 @@ def _want(t, name: str, dtype: str, shape=None, min_rows: int = 0):
     size; the first dimension must also hold at least `min_rows`."""
     if t is None:
         return
-    import torch
-    if t.dtype != getattr(torch, dtype):
+    if t.dtype is not (_dtypes.get(dtype) or _dtype(dtype)):
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if shape is not None:
-        ok = t.dim() == len(shape) and all(w is None or int(t.shape[i]) == w
-                                           for i, w in enumerate(shape))
-        if not ok:
-            want = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
-            raise ValueError(f"{name}: expected shape {want}, got {list(t.shape)}")
-        if int(t.shape[0]) < min_rows:
-            raise ValueError(f"{name}: {int(t.shape[0])} rows, at least {min_rows} needed")
+        got = t.shape
+        if got != shape:  # not the very sizes: None matches any
+            ok = len(got) == len(shape)
+            if ok:
+                for w, g in zip(shape, got):
+                    if w != g and w is not None:
+                        ok = False
+            if not ok:
+                want = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
+                raise ValueError(f"{name}: expected shape {want}, got {list(got)}")
+        if got[0] < min_rows:
+            raise ValueError(f"{name}: {int(got[0])} rows, at least {min_rows} needed")
 
 
 def _want_cache(cache: "KVCache", cfg: "AttnConfig", batch: int):
@@ -336,7 +368,7 @@ def na_rope_append_kv_paged(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache
     rc = lib.na_rope_append_kv_paged(ctypes.byref(c), ctypes.byref(r), batch, _ptr(cu_seqlens),
                                      _ptr(cache_lens), T, _ptr(q), _ptr(k), _ptr(v),
                                      _ptr(q_norm_w), _ptr(k_norm_w), _ptr(q_out), ctypes.byref(kc),
-                                     _ptr(status), _stream(stream))
+                                     _ptr(status), _stream_for(q, stream))
     _check("na_rope_append_kv_paged", rc)
 
 
@@ -416,7 +448,7 @@ def na_attn_prefill_chunk_paged(cfg: AttnConfig, cu_seqlens, cache_lens, max_new
     rc = lib.na_attn_prefill_chunk_paged(ctypes.byref(c), batch, _ptr(cu_seqlens),
                                          _ptr(cache_lens), T, int(max_new_len), int(max_total_len),
                                          _ptr(q_rot), ctypes.byref(kc), _ptr(gate), _ptr(out),
-                                         _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+                                         _ptr(workspace), ws_bytes, _ptr(status), _stream_for(q_rot, stream))
     _check("na_attn_prefill_chunk_paged", rc)
 
 
@@ -461,7 +493,7 @@ def na_attn_decode_paged(cfg: AttnConfig, q_rot, cache: PagedKVCache, kv_lens, m
     rc = lib.na_attn_decode_paged(ctypes.byref(c), batch, _ptr(q_rot), ctypes.byref(kc),
                                   _ptr(kv_lens), int(max_kv_len), _ptr(gate), _ptr(out),
                                   _ptr(probs), stride, int(num_splits), _ptr(workspace), ws_bytes,
-                                  _ptr(status), _stream(stream))
+                                  _ptr(status), _stream_for(q_rot, stream))
     _check("na_attn_decode_paged", rc)
 
 

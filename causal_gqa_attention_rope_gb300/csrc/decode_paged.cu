@@ -38,13 +38,16 @@ constexpr int CWARPS = 4;  // consumer warps
 constexpr int THREADS = (CWARPS + 1) * 32;
 constexpr int MAX_HPC = 8;
 
-// Both page types keep 96 KB of tiles in flight per CTA at d = 128.
+// Tiles in flight and CTAs per SM.  An E4M3 tile is half as large, and what its
+// pass lacks first is warps (64 sequences of 512 .. 8192 keys, 32/8 heads: two
+// CTAs of four or six tiles 106 us, three of three 100 us).
+constexpr int kStages = 3;
 template <bool E4M3>
-constexpr int kStages = E4M3 ? 6 : 3;
+constexpr int kCtasPerSm = E4M3 ? 3 : 2;
 
 template <int D, bool E4M3>
 struct __align__(1024) PagedSmem {
-    static constexpr int ST = kStages<E4M3>;
+    static constexpr int ST = kStages;
     static constexpr uint32_t ROW = D * (E4M3 ? 1 : 2);           // bytes of a row
     static constexpr uint32_t BOX = ROW < 128 ? ROW : 128;        // of a row in one box
     static constexpr uint32_t TILE_BYTES = TILE * ROW;
@@ -141,7 +144,7 @@ __device__ __forceinline__ Window open_window(const DecodeParams &p, const Paged
 }
 
 template <int D, bool E4M3, bool CAPPED>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     decode_paged_kernel(const DecodeParams p, const PagedView pg,
                         const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v)
@@ -643,7 +646,7 @@ cudaError_t launch_paged_t(const DecodeParams &p, const PagedView &pg, cudaStrea
 
 }  // namespace
 
-int decode_paged_ctas_per_sm() { return 2; }
+int decode_paged_ctas_per_sm(bool e4m3) { return e4m3 ? kCtasPerSm<true> : kCtasPerSm<false>; }
 
 cudaError_t launch_decode_paged(const DecodeParams &p, const PagedView &pg, bool e4m3, int d,
                                 cudaStream_t stream)

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "na_internal.cuh"
@@ -254,8 +255,10 @@ struct DecodePlan {
 // cuts the concatenated key streams into one equal slice per CTA (at least
 // min_slice keys), so the workspace holds one partial row group per piece:
 // streams + grid pieces at most, whatever the lengths.
+// A paged cache passes its CTAs per SM, and takes any divisor of the group up
+// to 8 as the heads scored together.
 DecodePlan plan_decode(const na_attn_cfg *c, int batch, int max_kv_len, int num_splits,
-                       bool paged = false)
+                       int paged_ctas_per_sm = 0)
 {
     DecodePlan pl{};
     const int tile = decode_key_tile();
@@ -263,7 +266,7 @@ DecodePlan plan_decode(const na_attn_cfg *c, int batch, int max_kv_len, int num_
     // query heads scored together (the MMA takes up to 8): each stream of
     // K/V is read once for them
     pl.heads_per_cta = (group % 8 == 0) ? 8 : (group % 4 == 0) ? 4 : ((group % 2 == 0) ? 2 : 1);
-    if (paged)  // any divisor of the group
+    if (paged_ctas_per_sm)
         for (pl.heads_per_cta = 8; group % pl.heads_per_cta != 0;)
             pl.heads_per_cta--;
     const int len = max_kv_len > 0 ? max_kv_len : 1;
@@ -271,7 +274,7 @@ DecodePlan plan_decode(const na_attn_cfg *c, int batch, int max_kv_len, int num_
     if (min_slice < 1)
         min_slice = 1;
     pl.min_slice = min_slice;
-    pl.grid = (paged ? decode_paged_ctas_per_sm() : decode_ctas_per_sm()) * sm_count();
+    pl.grid = (paged_ctas_per_sm ? paged_ctas_per_sm : decode_ctas_per_sm()) * sm_count();
     pl.streams = batch * c->num_kv_heads * (group / pl.heads_per_cta);
     pl.max_pieces = pl.streams + pl.grid;
     const size_t rows = (size_t)pl.max_pieces * pl.heads_per_cta;
@@ -692,7 +695,9 @@ int na_decode_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_
         return rc;
     if (!bytes || batch <= 0 || max_kv_len < 0 || num_splits < 0)
         return NA_ERR_INVALID_ARG;
-    *bytes = plan_decode(cfg, batch, max_kv_len, num_splits, true).ws_bytes;
+    // for either page type
+    const int ctas = std::max(decode_paged_ctas_per_sm(false), decode_paged_ctas_per_sm(true));
+    *bytes = plan_decode(cfg, batch, max_kv_len, num_splits, ctas).ws_bytes;
     return NA_OK;
 }
 
@@ -718,7 +723,8 @@ int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_ro
         return NA_ERR_CAPACITY;
     if ((cfg->flags & NA_OUT_GATE) && !gate)
         return NA_ERR_INVALID_ARG;
-    const DecodePlan pl = plan_decode(cfg, batch, max_kv_len, num_splits, true);
+    const DecodePlan pl =
+        plan_decode(cfg, batch, max_kv_len, num_splits, decode_paged_ctas_per_sm(e4m3));
     if (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace))
         return NA_ERR_WORKSPACE;
     DecodeParams p = decode_params(cfg, pl, batch, q_rot, kv_lens, max_kv_len, gate, out, probs,

@@ -385,6 +385,6 @@ cudaError_t launch_prefill_paged(const PrefillParams &p, const PagedView &pg, bo
 size_t rope_append_smem_bytes(int H, int KV, int d, int rd);
 int decode_key_tile();
 int decode_ctas_per_sm();
-int decode_paged_ctas_per_sm();
+int decode_paged_ctas_per_sm(bool e4m3);
 int prefill_key_tile();
 int prefill_q_tile();
