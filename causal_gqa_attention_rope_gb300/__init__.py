@@ -304,16 +304,18 @@ def _want_cache(cache: "KVCache", cfg: "AttnConfig", batch: int):
 
 
 def _want_paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int):
-    kind = "bfloat16" if cache.k_scale is None and cache.v_scale is None else "float8_e4m3fn"
+    k_scale, v_scale = cache.k_scale, cache.v_scale
+    kind = "bfloat16" if k_scale is None and v_scale is None else "float8_e4m3fn"
+    shape = cache.k.shape
     _want(cache.k, "cache.k", kind, (None, cfg.num_kv_heads, None, cfg.head_dim))
-    _want(cache.v, "cache.v", kind, tuple(cache.k.shape))
+    _want(cache.v, "cache.v", kind, shape)
     _want(cache.page_table, "cache.page_table", "int32", (None, None), batch)
     if kind != "bfloat16":
-        scales = (int(cache.k.shape[0]), cfg.num_kv_heads)
-        for t, name in ((cache.k_scale, "cache.k_scale"), (cache.v_scale, "cache.v_scale")):
-            if t is None:
-                raise ValueError(f"{name}: missing")
-            _want(t, name, "uint8", scales)
+        if k_scale is None or v_scale is None:
+            raise ValueError(f"cache.{'k' if k_scale is None else 'v'}_scale: missing")
+        scales = (shape[0], cfg.num_kv_heads)
+        _want(k_scale, "cache.k_scale", "uint8", scales)
+        _want(v_scale, "cache.v_scale", "uint8", scales)
 
 
 def _check(fn: str, rc: int):
@@ -331,10 +333,15 @@ def _append_args(cfg, cu_seqlens, cache_lens, q, k, v, q_out, q_norm_w, k_norm_w
     H, KV, d = cfg.num_heads, cfg.num_kv_heads, cfg.head_dim
     _want(cu_seqlens, "cu_seqlens", "int32", (None,))
     _want(cache_lens, "cache_lens", "int32", (None,), batch)
-    _want(q, "q", "bfloat16", (None, H, d), T)
-    _want(q_out, "q_out", "bfloat16", (None, H, d), T)
-    _want(k, "k", "bfloat16", (None, KV, d), T)
-    _want(v, "v", "bfloat16", (None, KV, d), T)
+    bf16, kv = q.dtype, (T, KV, d)
+    # the usual sizes, checked at once; anything else one by one
+    if not (bf16 is _dtypes.get("bfloat16") and q_out.dtype is bf16 and k.dtype is bf16
+            and v.dtype is bf16 and q.shape == (T, H, d) and q_out.shape == (T, H, d)
+            and k.shape == kv and v.shape == kv):
+        _want(q, "q", "bfloat16", (None, H, d), T)
+        _want(q_out, "q_out", "bfloat16", (None, H, d), T)
+        _want(k, "k", "bfloat16", (None, KV, d), T)
+        _want(v, "v", "bfloat16", (None, KV, d), T)
     _want(q_norm_w, "q_norm_w", "bfloat16", (d,))
     _want(k_norm_w, "k_norm_w", "bfloat16", (d,))
     _want(status, "status", "int32", (None,), 1)
@@ -412,8 +419,10 @@ def _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status, total_t
     H, d = cfg.num_heads, cfg.head_dim
     _want(cu_seqlens, "cu_seqlens", "int32", (None,))
     _want(cache_lens, "cache_lens", "int32", (None,), batch)
-    _want(q_rot, "q_rot", "bfloat16", (None, H, d), T)
-    _want(out, "out", "bfloat16", (None, H, d), T)
+    if not (q_rot.dtype is _dtypes.get("bfloat16") and out.dtype is q_rot.dtype
+            and q_rot.shape == (T, H, d) and out.shape == (T, H, d)):
+        _want(q_rot, "q_rot", "bfloat16", (None, H, d), T)
+        _want(out, "out", "bfloat16", (None, H, d), T)
     _want(gate, "gate", "bfloat16", (None, H, d), T)
     _want(status, "status", "int32", (None,), 1)
     return batch, T

@@ -1,0 +1,632 @@
+// append_paged.cu -- a chunk's queries, keys and values into a paged cache, in
+// one launch (na_rope_append_kv_paged).  Two kinds of CTA share the grid.
+//
+// Rows: q (and with bf16 pages k and v), arithmetic as in rope_append.cu.  A CTA
+// takes NT / 64 tokens: its threads request 16 elements of up to P rows each
+// before anything else, find the tokens' sequences and pages, compute one cos
+// and sin each (all pairs of all tokens of the CTA) into shared memory, and
+// rotate.  The rows of a token are then served by one cos and sin per pair
+// instead of one per pair and 8 rows, and the loads of P rows are in flight at
+// once.  Few tokens take P = 1 and one token per CTA, for more CTAs.
+// (2048 tokens of 40 query heads, d 128: ROWS_TIME us with the E4M3 pages of 8
+// kv heads, against 17.7 + 9.1 us as two launches with 64-thread CTAs per row
+// group.)
+//
+// E4M3 pages.  A page's scale is 2^e with the smallest e such that max |x| <=
+// 448 * 2^e over its tokens (448 is E4M3's largest value), so it is known only
+// when all of the page's tokens are: one CTA takes one page that the call
+// touches, one kv head, and K or V.  Its threads hold the page's new rows in
+// registers -- normed and rotated in fp32, 16 elements of a row per thread --
+// agree on the largest magnitude, and round once to E4M3.  When the page holds
+// earlier tokens of the sequence its scale never shrinks, and when it grows
+// those tokens are rounded to the new one: a power of two, so only values that
+// leave E4M3's normal range (2^-15 of the page's largest, and below) change.
+//
+// Both move a few bytes per element and are bound by latency: bounds, page id
+// and rows are one dependent load apart each, so the rows are requested before
+// the others are looked at.
+//
+// Page slots.  Sequence b touches at most new_b / page + 2 pages; it owns the
+// slots [F(b), F(b + 1)) with F(b) = cu_seqlens[b] / page + 2 b, which hold that
+// many, and a CTA finds its sequence by a 32-way search for the last b with
+// F(b) <= slot (one round of loads up to 32 sequences, two up to 1024).
+#include <cuda_fp16.h>
+
+#include "na_internal.cuh"
+#include "rope_math.cuh"
+
+namespace {
+
+using namespace rope;
+
+// cos and sin of 2 pi pos f, f in turns as a 64-bit fraction: the phase is
+// exact modulo one turn to 2^-32, its cosine and sine are within ~2e-7, far
+// below the 2^-4 of the rounding to E4M3.
+__device__ __forceinline__ void cos_sin_phase(int pos, unsigned long long f, float &c, float &s)
+{
+    const int phase = (int)(((unsigned long long)(unsigned)pos * f) >> 32);
+    sincospif((float)phase * 0x1p-31f, &s, &c);
+}
+
+// Two fp32 values to E4M3, round to nearest even, saturating; lo in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float4 y, float mul)
+{
+    return pack_e4m3x2(y.x * mul, y.y * mul) | (pack_e4m3x2(y.z * mul, y.w * mul) << 16);
+}
+
+// Four E4M3 bytes times `mul`, rounded again.
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float mul)
+{
+    uint32_t lo, hi;
+    e4m3x4_to_f16(w, lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return pack_e4m3x4(make_float4(a.x, a.y, b.x, b.y), mul);
+}
+
+// E8M0 byte of the smallest power of two 2^e with amax <= 448 * 2^e
+// (448 = 1.75 * 2^8); 0 for a zero or tiny amax.
+__device__ __forceinline__ int scale_byte(float amax)
+{
+    const uint32_t u = __float_as_uint(fminf(amax, 3.4028235e38f));
+    const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return max(e, 0);
+}
+
+// The page of one CTA: tokens [tok0, tok0 + rows) at positions pos0 ..
+struct PageWork {
+    int b, page, tok0, pos0, rows;
+};
+
+// Finds this slot's work; every warp does so by itself.  False: nothing to do
+// (errors reported by one thread of the grid row).
+__device__ __forceinline__ bool find_page(const RopeAppendParams &p, const PagedView &pg, int slot,
+                                          bool reporter, PageWork &w)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = p.batch, step;
+    int c0 = 0, c1 = 0, prior = 0;
+    do {
+        step = (n + 31) / 32;
+        const int off = lane * step;
+        int a0 = 0, a1 = 0, pl = 0;
+        bool below = false;
+        if (off < n) {
+            a0 = __ldg(p.cu_seqlens + lo + off);
+            a1 = __ldg(p.cu_seqlens + lo + off + 1);
+            pl = __ldg(p.cache_lens + lo + off);
+            below = (a0 >> pg.page_log) + 2 * (lo + off) <= slot;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, below);
+        const int src = m ? 31 - __clz(m) : 0;
+        c0 = __shfl_sync(0xffffffffu, a0, src);
+        c1 = __shfl_sync(0xffffffffu, a1, src);
+        prior = __shfl_sync(0xffffffffu, pl, src);
+        lo += src * step;
+        n = min(step, n - src * step);
+    } while (step > 1);
+    const int j = slot - ((c0 >> pg.page_log) + 2 * lo);  // page ordinal within the sequence
+    if (c1 <= c0 || j < 0)
+        return false;
+    if (c0 < 0 || c1 > p.total_tokens) {  // a sequence outside the call's tokens
+        if (reporter)
+            na_report(p.status, NA_ERR_INVALID_ARG);
+        return false;
+    }
+    if (prior < 0) {
+        if (reporter)
+            na_report(p.status, NA_ERR_CAPACITY);
+        return false;
+    }
+    const long long page = (prior >> pg.page_log) + (long long)j;
+    const long long first = max((long long)prior, page << pg.page_log);
+    const long long last = min((long long)prior + (c1 - c0), (page + 1) << pg.page_log);
+    if (first >= last)
+        return false;
+    if (page >= pg.pages_per_seq) {
+        if (reporter)
+            na_report(p.status, NA_ERR_CAPACITY);
+        return false;
+    }
+    w.b = lo;
+    w.page = (int)page;
+    w.pos0 = (int)first;
+    w.rows = (int)(last - first);
+    w.tok0 = c0 + (int)(first - prior);
+    return true;
+}
+
+// R rows' units of 16 elements per thread: R * NT / (D / 16) rows >= the page.
+// Unit k of a rotated row holds the eight pairs 8k .. 8k + 7, then the tail two
+// elements per pair slot; GENERIC is the same with rotary_dim not a multiple of
+// 16, element by element.
+template <int D, int R, int NT, bool GENERIC>
+__device__ __forceinline__ void append_page(const RopeAppendParams &p, const PagedView &pg,
+                                            const RopeTurns &turns, int slot, int g, bool is_v)
+{
+    constexpr int UPR = D / 16;  // units per row: the row's lanes, aligned in a warp
+    __shared__ float warp_max[NT / 32];
+    const int half = p.rd / 2;
+    const int k = threadIdx.x % UPR, row0 = threadIdx.x / UPR;
+    const bool normed = (p.flags & (is_v ? NA_V_NORM : NA_QK_NORM)) != 0;
+    // element of pair slot i: its first and its second
+    auto first_of = [&](int i) { return is_v || i >= half ? (is_v ? 2 * i : p.rd + 2 * (i - half)) : i; };
+    auto second_of = [&](int i) { return !is_v && i < half ? i + half : first_of(i) + 1; };
+    const bool rot = !is_v && 8 * k < half;  // (GENERIC: some slots of the unit may not be)
+    unsigned long long f[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        f[i] = rot ? turns.hi[8 * k + i] : 0ull;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    PageWork w;
+    if (!find_page(p, pg, slot, threadIdx.x == 0 && g == 0 && !is_v, w))
+        return;
+
+    // The rows first, then the page id: both loads in flight together.
+    const bf16 *src = (is_v ? p.v : p.k) + ((size_t)w.tok0 * p.KV + g) * D;
+    const size_t src_stride = (size_t)p.KV * D;
+    // two 8-element chunks of a unit (not GENERIC)
+    const int ca = rot ? k : 2 * k, cb = rot ? half / 8 + k : 2 * k + 1;
+    uint4 xa[R], xb[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const int row = row0 + r * (NT / UPR);
+        xa[r] = xb[r] = make_uint4(0, 0, 0, 0);
+        if (row < w.rows) {
+            const bf16 *x = src + row * src_stride;
+            if constexpr (GENERIC) {
+                uint16_t h[16];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    h[i] = reinterpret_cast<const uint16_t *>(x)[first_of(8 * k + i)];
+                    h[8 + i] = reinterpret_cast<const uint16_t *>(x)[second_of(8 * k + i)];
+                }
+                auto two = [&](int i) { return (uint32_t)h[i] | ((uint32_t)h[i + 1] << 16); };
+                xa[r] = make_uint4(two(0), two(2), two(4), two(6));
+                xb[r] = make_uint4(two(8), two(10), two(12), two(14));
+            } else {
+                xa[r] = __ldg(reinterpret_cast<const uint4 *>(x) + ca);
+                xb[r] = __ldg(reinterpret_cast<const uint4 *>(x) + cb);
+            }
+        }
+    }
+    const int id = __ldcg(pg.table + (size_t)w.b * pg.pages_per_seq + w.page);
+    float wa[8], wb[8];  // norm weights of the unit (K)
+    if (!is_v && normed) {
+        if constexpr (GENERIC) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                wa[i] = __bfloat162float(p.kw[first_of(8 * k + i)]);
+                wb[i] = __bfloat162float(p.kw[second_of(8 * k + i)]);
+            }
+        } else {
+            bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p.kw) + ca), wa);
+            bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p.kw) + cb), wb);
+        }
+        if (p.flags & NA_QK_NORM_ZERO_CENTERED) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                wa[i] += 1.0f;
+                wb[i] += 1.0f;
+            }
+        }
+    }
+    if ((unsigned)id >= (unsigned)pg.num_pages) {
+        if (threadIdx.x == 0)
+            na_report(p.status, NA_ERR_PAGE);
+        return;
+    }
+    uint8_t *scale = const_cast<uint8_t *>(is_v ? pg.v_scale : pg.k_scale) + (size_t)id * p.KV + g;
+    const int held = w.pos0 & ((1 << pg.page_log) - 1);  // earlier tokens of the page
+    const int old = held ? (int)__ldcg(scale) : 0;
+
+    // The values wait in shared memory for the page's scale (in registers they
+    // would cost the row CTAs of the launch their occupancy): [unit's quad][thread].
+    extern __shared__ float4 vals[];
+    auto at = [&](int r, int q) -> float4 & { return vals[(r * 4 + q) * NT + threadIdx.x]; };
+    float amax = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const int row = row0 + r * (NT / UPR);
+        if (r * (NT / UPR) >= w.rows)  // uniform: no thread has a row left
+            break;
+        float ya[8], yb[8];
+        bf16x8_to_f32(xa[r], ya);
+        bf16x8_to_f32(xb[r], yb);
+        float fr = 1.0f;
+        if (normed) {  // every lane shuffles; rows are aligned to UPR lanes
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                ss = fmaf(ya[i], ya[i], fmaf(yb[i], yb[i], ss));
+#pragma unroll
+            for (int o = UPR / 2; o; o >>= 1)
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            fr = 1.0f / sqrtf(ss / (float)D + p.eps);
+            if (!is_v) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    ya[i] *= wa[i];
+                    yb[i] *= wb[i];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            float a = ya[i] * fr, b = yb[i] * fr;
+            if (rot && (!GENERIC || 8 * k + i < half)) {
+                float c, s;
+                cos_sin_phase(w.pos0 + row, f[i], c, s);
+                const float a0 = a, b0 = b;
+                a = (a0 * c - b0 * s) * p.rope_scale;
+                b = (a0 * s + b0 * c) * p.rope_scale;
+            }
+            ya[i] = a;
+            yb[i] = b;
+            amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));  // rows past the page's: zeros
+        }
+        at(r, 0) = make_float4(ya[0], ya[1], ya[2], ya[3]);
+        at(r, 1) = make_float4(ya[4], ya[5], ya[6], ya[7]);
+        at(r, 2) = make_float4(yb[0], yb[1], yb[2], yb[3]);
+        at(r, 3) = make_float4(yb[4], yb[5], yb[6], yb[7]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((threadIdx.x & 31) == 0)
+        warp_max[threadIdx.x >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 32; i++)
+        amax = fmaxf(amax, warp_max[i]);
+    const int now = max(old, scale_byte(amax));
+
+    uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? p.cache_v : p.cache_k);
+    uint8_t *page = pool + (((size_t)id * p.KV + g) << pg.page_log) * D;
+    if (held && now > old) {
+        const int e = 127 + old - now;
+        const float shrink = e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
+        uint4 *rows = reinterpret_cast<uint4 *>(page);
+        for (int i = threadIdx.x; i < held * D / 16; i += NT) {
+            uint4 u = __ldcg(rows + i);
+            u.x = rescale_e4m3x4(u.x, shrink);
+            u.y = rescale_e4m3x4(u.y, shrink);
+            u.z = rescale_e4m3x4(u.z, shrink);
+            u.w = rescale_e4m3x4(u.w, shrink);
+            rows[i] = u;
+        }
+    }
+    const float mul = e8m0_value(254 - now);  // 2^-e
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const int row = row0 + r * (NT / UPR);
+        if (row >= w.rows)
+            break;
+        uint8_t *dst = page + (size_t)(held + row) * D;
+        const uint2 a = make_uint2(pack_e4m3x4(at(r, 0), mul), pack_e4m3x4(at(r, 1), mul));
+        const uint2 b = make_uint2(pack_e4m3x4(at(r, 2), mul), pack_e4m3x4(at(r, 3), mul));
+        if constexpr (GENERIC) {
+            const uint32_t q[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                dst[first_of(8 * k + i)] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+                dst[second_of(8 * k + i)] = (uint8_t)(q[2 + i / 4] >> (8 * (i % 4)));
+            }
+        } else {
+            *reinterpret_cast<uint2 *>(dst + 8 * ca) = a;
+            *reinterpret_cast<uint2 *>(dst + 8 * cb) = b;
+        }
+    }
+    if (threadIdx.x == 0)
+        *scale = (uint8_t)now;
+}
+
+constexpr int kManyRowCtas = 608;  // four per SM
+
+// Page CTAs of a call: (slot, kv head, K or V).
+long long page_ctas(const RopeAppendParams &p, const PagedView &pg)
+{
+    return ((p.total_tokens >> pg.page_log) + 2ll * p.batch) * p.KV * 2;
+}
+
+template <int D, int R, int NT, bool GENERIC>
+__device__ __forceinline__ void append_page_cta(const RopeAppendParams &p, const PagedView &pg,
+                                                const RopeTurns &turns, int i)
+{
+    const int per = 2 * p.KV, slot = i / per, rest = i - slot * per;
+    append_page<D, R, NT, GENERIC>(p, pg, turns, slot, rest >> 1, rest & 1);
+}
+
+// The rows of TK tokens from token t0 on: P of them per thread group from row
+// slot first on (row slots run token after token).
+struct RowPlace {
+    int pos;        // < 0: the token is skipped
+    int id, slot;   // bf16 pages: its page and slot there
+};
+
+template <int D, int NT, int P, int TK, bool E4M3>
+__device__ __forceinline__ void append_rows(const RopeAppendParams &p, const PagedView &pg,
+                                            const RopeTurns &turns, int t0, int first)
+{
+    constexpr int UPR = D / 16, RP = NT / UPR;  // 32-byte units per row, rows per pass
+    __shared__ float4 cs[TK][64];
+    __shared__ RowPlace place[TK];
+    const int H = p.H, KV = E4M3 ? 0 : p.KV, rows = H + 2 * KV;
+    const int half = p.rd / 2, lane = threadIdx.x & 31;
+    const int k = threadIdx.x % UPR;
+    const bool qk_norm = (p.flags & NA_QK_NORM) != 0;
+    const bool zero_centered = (p.flags & NA_QK_NORM_ZERO_CENTERED) != 0;
+    const bool v_norm = !E4M3 && (p.flags & NA_V_NORM) != 0;
+    const int ntok = min(TK, p.total_tokens - t0);
+    const bool rot = k < p.rd / 16;
+    // 16-byte chunks of a unit: of a rotated row, and of a V row
+    const int qa = rot ? k : 2 * k, qb = rot ? half / 8 + k : 2 * k + 1;
+
+    // this thread's cos and sin: pair `pair` of token `tk`
+    const int tk = TK == 1 ? 0 : threadIdx.x / 64, pair = threadIdx.x & 63;
+    const bool trig = (TK > 1 || threadIdx.x < 64) && pair < half;
+    const unsigned long long fhi = trig ? turns.hi[pair] : 0ull;
+    const unsigned int flo = trig ? turns.lo[pair] : 0u;
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    // Row slot first + i RP + thread / UPR: its token (of the CTA) and row.
+    auto row_at = [&](int i, int &t, int &r) {
+        const int s = first + i * RP + threadIdx.x / UPR;
+        t = TK == 1 ? 0 : s / rows;
+        r = TK == 1 ? s : s - t * rows;
+        return t < ntok && r < rows;
+    };
+    uint4 xa[P], xb[P];
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        int t, r;
+        xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
+        if (row_at(i, t, r)) {
+            const size_t tok = (size_t)(t0 + t);
+            const bf16 *src;
+            const bool is_v = !E4M3 && r >= H + KV;
+            if (E4M3 || r < H)
+                src = p.q + (tok * H + r) * D;
+            else
+                src = is_v ? p.v + (tok * KV + (r - H - KV)) * D : p.k + (tok * KV + (r - H)) * D;
+            xa[i] = ldg_early(reinterpret_cast<const uint4 *>(src) + (is_v ? 2 * k : qa));
+            xb[i] = ldg_early(reinterpret_cast<const uint4 *>(src) + (is_v ? 2 * k + 1 : qb));
+        }
+    }
+    int pos = -1;
+    if (tk < ntok) {  // a warp's threads share tk
+        int b;
+        owner_of(p, t0 + tk, lane, b, pos);
+        int id = 0;
+        if (pos < 0 || pos >= p.capacity) {
+            if (lane == 0)
+                na_report(p.status, NA_ERR_CAPACITY);
+            pos = -1;
+        } else if constexpr (!E4M3) {
+            id = __ldcg(pg.table + (size_t)b * pg.pages_per_seq + (pos >> pg.page_log));
+            if ((unsigned)id >= (unsigned)pg.num_pages) {
+                if (lane == 0)
+                    na_report(p.status, NA_ERR_PAGE);
+                pos = -1;
+            }
+        }
+        if (pair == 0)
+            place[tk] = RowPlace{pos, id, pos & ((1 << pg.page_log) - 1)};
+        if (trig && pos >= 0)  // [i][k] for pair 8k + i: a row's lanes read adjacent entries
+            cs[tk][(pair & 7) * 8 + (pair >> 3)] = cos_sin_turns((unsigned)pos, fhi, flo, kTrig.e);
+    }
+    __syncthreads();
+
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        int t, r;
+        const bool active = row_at(i, t, r);
+        const bool is_v = !E4M3 && r >= H + KV;
+        float a[8], c[8];
+        bf16x8_to_f32(xa[i], a);
+        bf16x8_to_f32(xb[i], c);
+        float f = 1.0f;
+        if (qk_norm || v_norm) {  // every lane shuffles; rows are aligned to UPR lanes
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                ss = fmaf(a[e], a[e], fmaf(c[e], c[e], ss));
+#pragma unroll
+            for (int o = UPR / 2; o; o >>= 1)
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (is_v ? v_norm : qk_norm)
+                f = 1.0f / sqrtf(ss / (float)D + p.eps);
+        }
+        if (!active)
+            continue;
+        const RowPlace pl = place[t];
+        if (pl.pos < 0)
+            continue;
+        float ya[8], yb[8];
+        if (is_v) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                ya[e] = a[e] * f;
+                yb[e] = c[e] * f;
+            }
+        } else {
+            const float4 *trig_row = cs[t];
+            const float fr = f * p.rope_scale;  // the attention factor scales rotated dims only
+            if (qk_norm) {
+                const uint4 *w = reinterpret_cast<const uint4 *>(E4M3 || r < H ? p.qw : p.kw);
+                float wa[8], wb[8];
+                bf16x8_to_f32(__ldg(w + qa), wa);
+                bf16x8_to_f32(__ldg(w + qb), wb);
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const F2 x0 = weighted(a[e], wa[e], zero_centered);
+                    const F2 x1 = weighted(c[e], wb[e], zero_centered);
+                    if (!rot) {
+                        ya[e] = fmaf(x0.hi, f, x0.lo * f);
+                        yb[e] = fmaf(x1.hi, f, x1.lo * f);
+                    } else if (zero_centered) {
+                        rotate(x0, x1, trig_row[e * 8 + k], fr, ya[e], yb[e]);
+                    } else {  // x * w of two bf16 values is exact in fp32
+                        rotate_exact(x0.hi, x1.hi, trig_row[e * 8 + k], fr, ya[e], yb[e]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    ya[e] = a[e];
+                    yb[e] = c[e];
+                    if (rot)
+                        rotate_exact(a[e], c[e], trig_row[e * 8 + k], fr, ya[e], yb[e]);
+                }
+            }
+        }
+        bf16 *dst;
+        if (E4M3 || r < H)
+            dst = p.q_out + ((size_t)(t0 + t) * H + r) * D;
+        else
+            dst = (is_v ? p.cache_v : p.cache_k) +
+                  ((((size_t)pl.id * KV + (is_v ? r - H - KV : r - H)) << pg.page_log) + pl.slot) * D;
+        reinterpret_cast<uint4 *>(dst)[is_v ? 2 * k : qa] = f32_to_bf16x8(ya);
+        reinterpret_cast<uint4 *>(dst)[is_v ? 2 * k + 1 : qb] = f32_to_bf16x8(yb);
+    }
+}
+
+// Page CTAs first (E4M3): theirs is the longer chain of dependent loads.
+template <int D, bool E4M3, int R, int NT, int P>
+__global__ void __launch_bounds__(NT, 768 / NT) append_paged_kernel(const RopeAppendParams p,
+                                                          const PagedView pg, const RopeTurns turns,
+                                                          const int n_page_ctas,
+                                                          const int ctas_per_group)
+{
+    constexpr int TK = P == 1 ? 1 : NT / 64, RP = NT / (D / 16);
+    int i = blockIdx.x;
+    if constexpr (E4M3) {
+        if (i < n_page_ctas) {
+            append_page_cta<D, R, NT, false>(p, pg, turns, i);
+            return;
+        }
+        i -= n_page_ctas;
+    }
+    const int group = i / ctas_per_group, part = i - group * ctas_per_group;
+    append_rows<D, NT, P, TK, E4M3>(p, pg, turns, group * TK, part * P * RP);
+}
+
+template <int D, int R, int NT>
+__global__ void __launch_bounds__(NT, 768 / NT) append_pages_kernel(const RopeAppendParams p,
+                                                          const PagedView pg, const RopeTurns turns)
+{
+    append_page_cta<D, R, NT, true>(p, pg, turns, blockIdx.x);
+}
+
+// Shared memory of the page CTAs, granted to `kernel` once per device where it
+// is more than the default.
+template <int R, int NT, typename Kernel>
+cudaError_t grant_smem(Kernel kernel, std::atomic<unsigned long long> &done)
+{
+    constexpr int bytes = R * NT * 64;
+    if (bytes <= 48 * 1024)
+        return cudaSuccess;
+    return once_per_device(done, [kernel] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+}
+
+template <int D, bool E4M3, int R, int NT, int P>
+cudaError_t launch_fused(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
+                         cudaStream_t stream)
+{
+    constexpr int TK = P == 1 ? 1 : NT / 64, RP = NT / (D / 16);
+    const int rows = p.H + (E4M3 ? 0 : 2 * p.KV);
+    const long long groups = (p.total_tokens + TK - 1) / TK;
+    const int per = (TK * rows + P * RP - 1) / (P * RP);
+    const long long pages = E4M3 ? page_ctas(p, pg) : 0;
+    if (pages + groups * per > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    static std::atomic<unsigned long long> granted{0};
+    const size_t smem = E4M3 ? R * NT * 64 : 0;
+    const cudaError_t e = grant_smem<E4M3 ? R : 0, NT>(append_paged_kernel<D, E4M3, R, NT, P>, granted);
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(append_paged_kernel<D, E4M3, R, NT, P>, dim3((unsigned)(pages + groups * per)),
+                         dim3(NT), smem, stream, p, pg, turns, (int)pages, per);
+}
+
+// P = 2 row units per thread when that still gives every SM a few CTAs.
+template <int D, bool E4M3, int R, int NT>
+cudaError_t launch_p(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
+                     cudaStream_t stream)
+{
+    const long long units = (long long)p.total_tokens * (p.H + (E4M3 ? 0 : 2 * p.KV)) * (D / 16);
+    if (units >= 2ll * NT * kManyRowCtas)
+        return launch_fused<D, E4M3, R, NT, 2>(p, pg, turns, stream);
+    return launch_fused<D, E4M3, R, NT, 1>(p, pg, turns, stream);
+}
+
+template <int D, int R, int NT>
+cudaError_t launch_generic(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
+                           cudaStream_t stream)
+{
+    const long long pages = page_ctas(p, pg);
+    if (pages > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    static std::atomic<unsigned long long> granted{0};
+    const cudaError_t e = grant_smem<R, NT>(append_pages_kernel<D, R, NT>, granted);
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(append_pages_kernel<D, R, NT>, dim3((unsigned)pages), dim3(NT), R * NT * 64,
+                         stream, p, pg, turns);
+}
+
+}  // namespace
+
+cudaError_t launch_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
+                                const RopeTurns &turns, cudaStream_t stream)
+{
+    if (p.d == 128) {
+        if (!e4m3)
+            return launch_p<128, false, 1, 128>(p, pg, turns, stream);
+        switch (pg.page_log) {
+        case 4: return launch_p<128, true, 1, 128>(p, pg, turns, stream);
+        case 5: return launch_p<128, true, 2, 128>(p, pg, turns, stream);
+        case 6: return launch_p<128, true, 4, 128>(p, pg, turns, stream);
+        default: return launch_p<128, true, 4, 256>(p, pg, turns, stream);
+        }
+    }
+    if (!e4m3)
+        return launch_p<64, false, 1, 128>(p, pg, turns, stream);
+    switch (pg.page_log) {
+    case 4:
+    case 5: return launch_p<64, true, 1, 128>(p, pg, turns, stream);
+    case 6: return launch_p<64, true, 2, 128>(p, pg, turns, stream);
+    default: return launch_p<64, true, 4, 128>(p, pg, turns, stream);
+    }
+}
+
+// The page CTAs alone, for any even rotary dimension.
+cudaError_t launch_append_pages(const RopeAppendParams &p, const PagedView &pg,
+                                const RopeTurns &turns, cudaStream_t stream)
+{
+    if (p.d == 128) {
+        switch (pg.page_log) {
+        case 4: return launch_generic<128, 1, 128>(p, pg, turns, stream);
+        case 5: return launch_generic<128, 2, 128>(p, pg, turns, stream);
+        case 6: return launch_generic<128, 4, 128>(p, pg, turns, stream);
+        default: return launch_generic<128, 4, 256>(p, pg, turns, stream);
+        }
+    }
+    switch (pg.page_log) {
+    case 4:
+    case 5: return launch_generic<64, 1, 128>(p, pg, turns, stream);
+    case 6: return launch_generic<64, 2, 128>(p, pg, turns, stream);
+    default: return launch_generic<64, 4, 128>(p, pg, turns, stream);
+    }
+}

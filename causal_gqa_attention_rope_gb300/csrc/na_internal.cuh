@@ -378,8 +378,10 @@ cudaError_t launch_decode_combine(const DecodeParams &p, int d, cudaStream_t str
 cudaError_t launch_importance(const ImportanceParams &p, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillParams &p, int d, int total_tokens, int cache_batch,
                            cudaStream_t stream);
-cudaError_t launch_kv_append_e4m3(const RopeAppendParams &p, const PagedView &pg,
-                                  const RopeTurns &turns, cudaStream_t stream);
+cudaError_t launch_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
+                                const RopeTurns &turns, cudaStream_t stream);
+cudaError_t launch_append_pages(const RopeAppendParams &p, const PagedView &pg,
+                                const RopeTurns &turns, cudaStream_t stream);
 cudaError_t launch_prefill_paged(const PrefillParams &p, const PagedView &pg, bool e4m3, int d,
                                  int total_tokens, cudaStream_t stream);
 size_t rope_append_smem_bytes(int H, int KV, int d, int rd);
