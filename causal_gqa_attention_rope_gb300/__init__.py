@@ -211,10 +211,9 @@ class PagedKVCache:
     def c(self) -> na_paged_kv_cache:
         num_pages, _, page_size, _ = self.k.shape
         batch, pages_per_seq = self.page_table.shape
-        return na_paged_kv_cache(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
-                                 _ptr(self.v_scale), _ptr(self.page_table), num_pages, page_size,
-                                 batch, pages_per_seq,
-                                 NA_KV_BF16 if self.k_scale is None else NA_KV_E4M3)
+        return na_paged_kv_cache(
+            *_ptrs(self.k, self.v, self.k_scale, self.v_scale, self.page_table), num_pages,
+            page_size, batch, pages_per_seq, NA_KV_BF16 if self.k_scale is None else NA_KV_E4M3)
 
 
 # ---------------------------------------------------------------- helpers --
@@ -227,6 +226,14 @@ def _ptr(t) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError("libna needs contiguous tensors")
     return t.data_ptr()
+
+
+def _ptrs(*tensors) -> list:
+    """_ptr of each."""
+    out = []
+    for t in tensors:
+        out.append(t.data_ptr() if t is not None and t.is_cuda and t.is_contiguous() else _ptr(t))
+    return out
 
 
 _current_stream = None
@@ -372,10 +379,9 @@ def na_rope_append_kv_paged(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache
                             status, total_tokens)
     _want_paged(cache, cfg, batch)
     c, r, kc = cfg.c(), rope.c(), cache.c()
-    rc = lib.na_rope_append_kv_paged(ctypes.byref(c), ctypes.byref(r), batch, _ptr(cu_seqlens),
-                                     _ptr(cache_lens), T, _ptr(q), _ptr(k), _ptr(v),
-                                     _ptr(q_norm_w), _ptr(k_norm_w), _ptr(q_out), ctypes.byref(kc),
-                                     _ptr(status), _stream_for(q, stream))
+    cu, lens, *rows, st = _ptrs(cu_seqlens, cache_lens, q, k, v, q_norm_w, k_norm_w, q_out, status)
+    rc = lib.na_rope_append_kv_paged(ctypes.byref(c), ctypes.byref(r), batch, cu, lens, T, *rows,
+                                     ctypes.byref(kc), st, _stream_for(q, stream))
     _check("na_rope_append_kv_paged", rc)
 
 
@@ -454,18 +460,21 @@ def na_attn_prefill_chunk_paged(cfg: AttnConfig, cu_seqlens, cache_lens, max_new
     _want_paged(cache, cfg, batch)
     c, kc = cfg.c(), cache.c()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = lib.na_attn_prefill_chunk_paged(ctypes.byref(c), batch, _ptr(cu_seqlens),
-                                         _ptr(cache_lens), T, int(max_new_len), int(max_total_len),
-                                         _ptr(q_rot), ctypes.byref(kc), _ptr(gate), _ptr(out),
-                                         _ptr(workspace), ws_bytes, _ptr(status), _stream_for(q_rot, stream))
+    cu, lens, pq, pgate, po, ws, st = _ptrs(cu_seqlens, cache_lens, q_rot, gate, out, workspace,
+                                            status)
+    rc = lib.na_attn_prefill_chunk_paged(ctypes.byref(c), batch, cu, lens, T, int(max_new_len),
+                                         int(max_total_len), pq, ctypes.byref(kc), pgate, po, ws,
+                                         ws_bytes, st, _stream_for(q_rot, stream))
     _check("na_attn_prefill_chunk_paged", rc)
 
 
 def _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status):
     H, d = cfg.num_heads, cfg.head_dim
-    _want(q_rot, "q_rot", "bfloat16", (None, H, d))
     B = int(q_rot.shape[0])
-    _want(out, "out", "bfloat16", (B, H, d))
+    rows = (B, H, d)
+    if not (q_rot.dtype is _dtypes.get("bfloat16") and q_rot.shape == rows):
+        _want(q_rot, "q_rot", "bfloat16", (None, H, d))
+    _want(out, "out", "bfloat16", rows)
     _want(gate, "gate", "bfloat16", (B, H, d))
     _want(kv_lens, "kv_lens", "int32", (None,), B)
     _want(probs, "probs", "float32", (B, H, None))
@@ -499,10 +508,10 @@ def na_attn_decode_paged(cfg: AttnConfig, q_rot, cache: PagedKVCache, kv_lens, m
     c, kc = cfg.c(), cache.c()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     stride = int(probs.shape[-1]) if probs is not None else 0
-    rc = lib.na_attn_decode_paged(ctypes.byref(c), batch, _ptr(q_rot), ctypes.byref(kc),
-                                  _ptr(kv_lens), int(max_kv_len), _ptr(gate), _ptr(out),
-                                  _ptr(probs), stride, int(num_splits), _ptr(workspace), ws_bytes,
-                                  _ptr(status), _stream_for(q_rot, stream))
+    pq, lens, pgate, po, pp, ws, st = _ptrs(q_rot, kv_lens, gate, out, probs, workspace, status)
+    rc = lib.na_attn_decode_paged(ctypes.byref(c), batch, pq, ctypes.byref(kc), lens,
+                                  int(max_kv_len), pgate, po, pp, stride, int(num_splits), ws,
+                                  ws_bytes, st, _stream_for(q_rot, stream))
     _check("na_attn_decode_paged", rc)
 
 

@@ -352,11 +352,37 @@ struct RowPlace {
     int id, slot;   // bf16 pages: its page and slot there
 };
 
+// rotate_exact (rope_math.cuh) of two pairs at a time on packed fp32 operations:
+// the same products, sums and roundings, -a1 standing in for the subtractions.
+// c: cos hi, hi, lo, lo of the two pairs; s: sin likewise.
+__device__ __forceinline__ void rotate_exact2(float2 a0, float2 a1, float4 c, float4 s, float2 fr,
+                                              float2 &y0, float2 &y1)
+{
+    const float2 na1 = make_float2(-a1.x, -a1.y);
+    const float2 ch = make_float2(c.x, c.y), cl = make_float2(c.z, c.w);
+    const float2 sh = make_float2(s.x, s.y), sl = make_float2(s.z, s.w);
+    {
+        const float2 t = __fmul2_rn(a1, sh), nt = __fmul2_rn(na1, sh);
+        const float2 ne = __ffma2_rn(na1, sh, t);  // minus the rounding error of t
+        const float2 h = __ffma2_rn(a0, ch, nt);
+        const float2 lo = __fadd2_rn(__ffma2_rn(a0, cl, __fmul2_rn(na1, sl)), ne);
+        y0 = __ffma2_rn(h, fr, __fmul2_rn(lo, fr));
+    }
+    {
+        const float2 t = __fmul2_rn(a1, ch), nt = __fmul2_rn(na1, ch);
+        const float2 e = __ffma2_rn(a1, ch, nt);
+        const float2 h = __ffma2_rn(a0, sh, t);
+        const float2 lo = __fadd2_rn(__ffma2_rn(a0, sl, __fmul2_rn(a1, cl)), e);
+        y1 = __ffma2_rn(h, fr, __fmul2_rn(lo, fr));
+    }
+}
+
 template <int D, int NT, int P, int TK, bool E4M3>
 __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const PagedView &pg,
                                             const RopeTurns &turns, int t0, int first)
 {
     constexpr int UPR = D / 16, RP = NT / UPR;  // 32-byte units per row, rows per pass
+    // cos (and sin) hi, hi, lo, lo of pairs 8 k + 2 j and the next: [2 j (+ 1)][k]
     __shared__ float4 cs[TK][64];
     __shared__ RowPlace place[TK];
     const int H = p.H, KV = E4M3 ? 0 : p.KV, rows = H + 2 * KV;
@@ -380,9 +406,14 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
 
     // Row slot first + i RP + thread / UPR: its token (of the CTA) and row.
     auto row_at = [&](int i, int &t, int &r) {
-        const int s = first + i * RP + threadIdx.x / UPR;
-        t = TK == 1 ? 0 : s / rows;
-        r = TK == 1 ? s : s - t * rows;
+        r = first + i * RP + threadIdx.x / UPR;
+        t = 0;
+#pragma unroll
+        for (int u = 1; u < TK; u++)
+            if (r >= rows) {
+                r -= rows;
+                t = u;
+            }
         return t < ntok && r < rows;
     };
     uint4 xa[P], xb[P];
@@ -421,8 +452,14 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
         }
         if (pair == 0)
             place[tk] = RowPlace{pos, id, pos & ((1 << pg.page_log) - 1)};
-        if (trig && pos >= 0)  // [i][k] for pair 8k + i: a row's lanes read adjacent entries
-            cs[tk][(pair & 7) * 8 + (pair >> 3)] = cos_sin_turns((unsigned)pos, fhi, flo, kTrig.e);
+        if (trig && pos >= 0) {
+            const float4 x = cos_sin_turns((unsigned)pos, fhi, flo, kTrig.e);
+            float *c = reinterpret_cast<float *>(&cs[tk][(pair & 6) * 8 + (pair >> 3)]) + (pair & 1);
+            c[0] = x.x;
+            c[2] = x.y;
+            c[32] = x.z;
+            c[34] = x.w;
+        }
     }
     __syncthreads();
 
@@ -459,33 +496,52 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
                 yb[e] = c[e] * f;
             }
         } else {
-            const float4 *trig_row = cs[t];
+            const float4 *trig_row = cs[t] + k;
             const float fr = f * p.rope_scale;  // the attention factor scales rotated dims only
+            float wa[8], wb[8];
             if (qk_norm) {
                 const uint4 *w = reinterpret_cast<const uint4 *>(E4M3 || r < H ? p.qw : p.kw);
-                float wa[8], wb[8];
                 bf16x8_to_f32(__ldg(w + qa), wa);
                 bf16x8_to_f32(__ldg(w + qb), wb);
+            }
+            if (qk_norm && zero_centered) {
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    const F2 x0 = weighted(a[e], wa[e], zero_centered);
-                    const F2 x1 = weighted(c[e], wb[e], zero_centered);
-                    if (!rot) {
+                    const F2 x0 = weighted(a[e], wa[e], true), x1 = weighted(c[e], wb[e], true);
+                    if (rot) {
+                        const float *tr = reinterpret_cast<const float *>(trig_row + (e & 6) * 8) + (e & 1);
+                        rotate(x0, x1, make_float4(tr[0], tr[2], tr[32], tr[34]), fr, ya[e], yb[e]);
+                    } else {
                         ya[e] = fmaf(x0.hi, f, x0.lo * f);
                         yb[e] = fmaf(x1.hi, f, x1.lo * f);
-                    } else if (zero_centered) {
-                        rotate(x0, x1, trig_row[e * 8 + k], fr, ya[e], yb[e]);
-                    } else {  // x * w of two bf16 values is exact in fp32
-                        rotate_exact(x0.hi, x1.hi, trig_row[e * 8 + k], fr, ya[e], yb[e]);
                     }
                 }
             } else {
+                if (qk_norm) {  // x * w of two bf16 values is exact in fp32
 #pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    ya[e] = a[e];
-                    yb[e] = c[e];
-                    if (rot)
-                        rotate_exact(a[e], c[e], trig_row[e * 8 + k], fr, ya[e], yb[e]);
+                    for (int e = 0; e < 8; e++) {
+                        a[e] *= wa[e];
+                        c[e] *= wb[e];
+                    }
+                }
+                if (rot) {
+                    const float2 fr2 = make_float2(fr, fr);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        float2 y0, y1;
+                        rotate_exact2(make_float2(a[e], a[e + 1]), make_float2(c[e], c[e + 1]),
+                                      trig_row[e * 8], trig_row[e * 8 + 8], fr2, y0, y1);
+                        ya[e] = y0.x;
+                        ya[e + 1] = y0.y;
+                        yb[e] = y1.x;
+                        yb[e + 1] = y1.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        ya[e] = a[e] * f;
+                        yb[e] = c[e] * f;
+                    }
                 }
             }
         }

@@ -58,6 +58,7 @@ struct __align__(1024) PagedSmem {
     uint16_t scales[ST][CWARPS];  // a warp's K | V << 8 scale bytes in each stage (E4M3)
     uint64_t full[ST];
     uint64_t empty[ST];
+    float2 fin[MAX_HPC];  // a finished stream's reference and 1 / sum, per head
     Slice slice;
     int abort_flag;
 };
@@ -143,7 +144,64 @@ __device__ __forceinline__ Window open_window(const DecodeParams &p, const Paged
     return w;
 }
 
-template <int D, bool E4M3, bool CAPPED>
+// A stream that one CTA has read whole, by its NT consumer threads: warp 0 holds
+// the merged rows and writes them (gated), then the raw scores become
+// probabilities.  `bad`: a wait gave up; the rows are zero.
+template <int D, bool E4M3, int NT>
+__device__ __forceinline__ void finish_stream(const DecodeParams &p, const Piece &pc, float2 *fin,
+                                              int head0, int hpc, const float (&acc)[D / 16][4],
+                                              const float (&m_ref)[2], const float (&l_sum)[2],
+                                              bool bad)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const size_t row0 = (size_t)pc.b * p.H + head0;
+    if (threadIdx.x < 32) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int h = 2 * t + i;
+            if (h >= hpc)
+                break;
+            const float inv = l_sum[i] > 0.f && !bad ? 1.0f / l_sum[i] : 0.f;
+            if (g == 0)
+                fin[h] = make_float2(m_ref[i], inv);
+            const bf16 *gate = p.gate ? p.gate + (row0 + h) * D : nullptr;
+            bf16 *out = p.out + (row0 + h) * D;
+            auto value = [&](float o, int e) {
+                o = bad ? 0.f : o * inv;
+                return gate ? o * (1.0f / (1.0f + __expf(-__bfloat162float(gate[e])))) : o;
+            };
+#pragma unroll
+            for (int s = 0; s < D / 16; s++) {
+                if constexpr (E4M3) {
+                    const int e = 16 * s + 2 * g;
+                    *reinterpret_cast<uint32_t *>(out + e) =
+                        pack_bf16x2(value(acc[s][i], e), value(acc[s][2 + i], e + 1));
+                } else {
+                    const int e = 16 * s + g;
+                    out[e] = __float2bfloat16_rn(value(acc[s][i], e));
+                    out[e + 8] = __float2bfloat16_rn(value(acc[s][2 + i], e + 8));
+                }
+            }
+        }
+    }
+    if (!p.probs)
+        return;
+    named_barrier_sync(1, NT);
+    if (bad)
+        return;
+    const int n = pc.kf + pc.k1;  // keys before the window (none without one) get 0
+    for (int h = 0; h < hpc; h++) {
+        float *row = p.probs + (row0 + h) * p.probs_stride;
+        const float2 f = fin[h];
+        for (int j = threadIdx.x; j < n; j += NT)
+            row[j] = j < pc.kf ? 0.f : ex2_mufu(row[j] - f.x) * f.y;
+    }
+}
+
+// DIRECT: one CTA per stream instead of a slice of the concatenation, for calls
+// of short sequences: no partial results and no merge pass (one sequence of 333
+// keys, 4/2 heads: DIRECT_SPLIT us with the merge pass, DIRECT_ONE us so).
+template <int D, bool E4M3, bool CAPPED, bool DIRECT>
 __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     decode_paged_kernel(const DecodeParams p, const PagedView pg,
                         const __grid_constant__ CUtensorMap map_k,
@@ -173,8 +231,15 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    if (warp == CWARPS)
+    if constexpr (DIRECT) {  // this CTA's stream, all of it
+        if (threadIdx.x == 0) {
+            const int spb = p.KV * p.head_chunks, b = blockIdx.x / spb;
+            const int len = valid_len(p, b);
+            sm.slice = Slice{0, len, 0, b, (int)blockIdx.x - b * spb, len == 0};
+        }
+    } else if (warp == CWARPS) {
         locate_slice(p, lane, sm.slice);
+    }
     __syncthreads();
     Walker walk;
     walk.init(sm.slice, p);
@@ -267,6 +332,20 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     // 2(l%4) and 2(l%4) + 1, and their probabilities, transposed in registers,
     // are the B operand of O^T += V^T P^T.
     const int hpc = p.group / p.head_chunks;
+    if constexpr (DIRECT) {  // a stream without keys: zero rows, as the merge pass gives
+        if (walk.done) {
+            const Slice sl = sm.slice;
+            const int n = __ldg(p.kv_lens + sl.b);
+            if (threadIdx.x == 0 && (n < 0 || n > p.capacity || n > p.max_kv_len))
+                na_report(p.status, NA_ERR_CAPACITY);
+            const int kvh = sl.si / p.head_chunks, hc = sl.si - kvh * p.head_chunks;
+            uint32_t *out = reinterpret_cast<uint32_t *>(
+                p.out + ((size_t)sl.b * p.H + kvh * p.group + hc * hpc) * D);
+            for (int e = threadIdx.x; e < hpc * D / 2; e += CWARPS * 32)
+                out[e] = 0u;
+            return;
+        }
+    }
     const int g = lane >> 2, t = lane & 3;
     const int h0 = 2 * t, h1 = 2 * t + 1;  // this lane's heads (columns)
     const bool v0 = h0 < hpc, v1 = h1 < hpc;
@@ -560,9 +639,15 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
         named_barrier_sync(1, CWARPS * 32);
         // (Warps 1 and 3 write again after this barrier, which the readers of their
         // buffers have passed; warp 2 after the next piece's first one.)
+        if (warp == 0)
+            take(sm.merge[2]);
+        if constexpr (DIRECT) {  // the whole stream: its rows and probabilities
+            finish_stream<D, E4M3, THREADS - 32>(p, pc, sm.fin, head0, hpc, acc, m_ref, l_sum,
+                                                 *(volatile int *)&sm.abort_flag != 0);
+            continue;
+        }
         if (warp != 0)
             continue;
-        take(sm.merge[2]);
         // Every consumer warp has finished this piece's tiles (or given up): the
         // abort flag is final for the piece, and a piece of a CTA whose wait gave
         // up is written as the marker (max -inf, sum -1) that the merge pass reports.
@@ -602,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     }
 }
 
-template <int D, bool E4M3, bool CAPPED>
+template <int D, bool E4M3, bool CAPPED, bool DIRECT>
 cudaError_t launch_paged_split(const DecodeParams &p, const PagedView &pg, cudaStream_t stream)
 {
     typedef PagedSmem<D, E4M3> Smem;
@@ -623,28 +708,33 @@ cudaError_t launch_paged_split(const DecodeParams &p, const PagedView &pg, cudaS
     const size_t smem = sizeof(Smem) + 1024;  // + alignment slack
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = once_per_device(configured, [smem] {
-        cudaError_t r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED>,
+        cudaError_t r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED, DIRECT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED>,
+            r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED, DIRECT>,
                                      cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         return r;
     });
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(decode_paged_kernel<D, E4M3, CAPPED>, dim3(p.grid), dim3(THREADS), smem,
+    return launch_kernel(decode_paged_kernel<D, E4M3, CAPPED, DIRECT>, dim3(p.grid), dim3(THREADS), smem,
                          stream, p, pg, mk, mv);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_paged_t(const DecodeParams &p, const PagedView &pg, cudaStream_t stream)
 {
-    const cudaError_t e = p.cap_out > 0.f ? launch_paged_split<D, E4M3, true>(p, pg, stream)
-                                          : launch_paged_split<D, E4M3, false>(p, pg, stream);
+    if (p.direct)
+        return p.cap_out > 0.f ? launch_paged_split<D, E4M3, true, true>(p, pg, stream)
+                               : launch_paged_split<D, E4M3, false, true>(p, pg, stream);
+    const cudaError_t e = p.cap_out > 0.f ? launch_paged_split<D, E4M3, true, false>(p, pg, stream)
+                                          : launch_paged_split<D, E4M3, false, false>(p, pg, stream);
     return e != cudaSuccess ? e : launch_decode_combine(p, D, stream);
 }
 
 }  // namespace
+
+int decode_paged_direct_keys() { return 512; }
 
 int decode_paged_ctas_per_sm(bool e4m3) { return e4m3 ? kCtasPerSm<true> : kCtasPerSm<false>; }
 

@@ -135,6 +135,41 @@ double rope_attention_factor(const na_rope_params *r)
     return 1.0;
 }
 
+// The frequencies in turns, and the multiplier.  A step calls this with the same
+// few parameters layer after layer, and 64 powers and divisions take longer than
+// the launch (5 us of a call): each thread keeps its last table, by the values
+// that determine it.
+struct RopeTable {
+    RopeTurns turns;
+    float scale;
+};
+
+const RopeTable &rope_table(const na_rope_params *r, int rd)
+{
+    struct Kept {
+        bool valid = false;
+        na_rope_params r{};
+        int rd = 0;
+        RopeTable table{};
+    };
+    static thread_local Kept kept;
+    const na_rope_params &k = kept.r;
+    const bool same = kept.valid && kept.rd == rd && k.base == r->base && k.yarn == r->yarn &&
+                      k.factor == r->factor && k.orig_max_pos == r->orig_max_pos &&
+                      k.beta_fast == r->beta_fast && k.beta_slow == r->beta_slow &&
+                      k.attn_factor == r->attn_factor;
+    if (!same) {
+        double inv_freq[64];
+        rope_frequencies(r, rd, inv_freq);
+        kept.table.turns = rope_turns_of(inv_freq, rd / 2);
+        kept.table.scale = (float)rope_attention_factor(r);
+        kept.r = *r;
+        kept.rd = rd;
+        kept.valid = true;
+    }
+    return kept.table;
+}
+
 int check_rope(const na_rope_params *r)
 {
     if (!r || !(r->base > 1.0))
@@ -296,7 +331,7 @@ int check_append(const na_attn_cfg *cfg, const na_rope_params *rope, int batch, 
 }
 
 // ... and after it, with the kernel's parameters that do not depend on it.
-int fill_append(const na_attn_cfg *cfg, const na_rope_params *rope, int batch,
+int fill_append(const na_attn_cfg *cfg, int batch,
                 const int32_t *cu_seqlens, const int32_t *cache_lens, int total_tokens,
                 const void *q, const void *k, const void *v, const void *q_norm_w,
                 const void *k_norm_w, void *q_out, int32_t *status, RopeAppendParams *p)
@@ -317,7 +352,6 @@ int fill_append(const na_attn_cfg *cfg, const na_rope_params *rope, int batch,
     p->rd = cfg->rotary_dim;
     p->flags = cfg->flags;
     p->eps = cfg->rms_eps;
-    p->rope_scale = (float)rope_attention_factor(rope);
     p->batch = batch;
     p->total_tokens = total_tokens;
     p->cu_seqlens = cu_seqlens;
@@ -443,16 +477,15 @@ int na_rope_append_kv(const na_attn_cfg *cfg, const na_rope_params *rope, int32_
     if (total_tokens == 0)
         return NA_OK;
     RopeAppendParams p{};
-    if ((rc = fill_append(cfg, rope, batch, cu_seqlens, cache_lens, total_tokens, q, k, v, q_norm_w,
+    if ((rc = fill_append(cfg, batch, cu_seqlens, cache_lens, total_tokens, q, k, v, q_norm_w,
                           k_norm_w, q_out, status, &p)) != NA_OK)
         return rc;
-    double inv_freq[64];
-    rope_frequencies(rope, cfg->rotary_dim, inv_freq);
+    const RopeTable &table = rope_table(rope, cfg->rotary_dim);
+    p.rope_scale = table.scale;
     p.capacity = cache->capacity;
     p.cache_k = static_cast<bf16 *>(cache->k);
     p.cache_v = static_cast<bf16 *>(cache->v);
-    return launch_rope_append(p, inv_freq, cfg->rotary_dim / 2,
-                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_rope_append(p, table.turns, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? NA_OK
                : NA_ERR_CUDA;
 }
@@ -473,17 +506,15 @@ int na_rope_append_kv_paged(const na_attn_cfg *cfg, const na_rope_params *rope, 
     if (total_tokens == 0)
         return NA_OK;
     RopeAppendParams p{};
-    if ((rc = fill_append(cfg, rope, batch, cu_seqlens, cache_lens, total_tokens, q, k, v, q_norm_w,
+    if ((rc = fill_append(cfg, batch, cu_seqlens, cache_lens, total_tokens, q, k, v, q_norm_w,
                           k_norm_w, q_out, status, &p)) != NA_OK)
         return rc;
-    if (e4m3 && cfg->num_kv_heads > 65535)  // one grid row per kv head
-        return NA_ERR_UNSUPPORTED;
-    double inv_freq[64];
-    rope_frequencies(rope, cfg->rotary_dim, inv_freq);
+    const RopeTable &table = rope_table(rope, cfg->rotary_dim);
+    p.rope_scale = table.scale;
     p.capacity = cache->pages_per_seq * cache->page_size;
     p.cache_k = static_cast<bf16 *>(cache->k);
     p.cache_v = static_cast<bf16 *>(cache->v);
-    return launch_rope_append_paged(p, pg, e4m3, inv_freq, cfg->rotary_dim / 2,
+    return launch_rope_append_paged(p, pg, e4m3, table.turns,
                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? NA_OK
                : NA_ERR_CUDA;
@@ -729,6 +760,10 @@ int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_ro
         return NA_ERR_WORKSPACE;
     DecodeParams p = decode_params(cfg, pl, batch, q_rot, kv_lens, max_kv_len, gate, out, probs,
                                    probs_stride, workspace, status);
+    if (num_splits == 0 && max_kv_len <= decode_paged_direct_keys()) {
+        p.direct = 1;
+        p.grid = pl.streams;
+    }
     p.capacity = capacity;
     p.cache_batch = cache->batch;
     p.cache_k = static_cast<const bf16 *>(cache->k);

@@ -326,6 +326,7 @@ struct DecodeParams {
     float *part_o;             // [max_pieces][heads-per-CTA][d]
     float *part_ml;            // [max_pieces][heads-per-CTA][2]  (max, sum) in the log2 domain
     int32_t *piece_span;       // [streams][2]  first and last piece id of each stream
+    int direct;                // paged: one CTA per stream, no merge pass
     int32_t *status;
 };
 
@@ -367,10 +368,11 @@ struct ImportanceParams {
 };
 
 // Kernel launchers (one translation unit each).
-cudaError_t launch_rope_append(const RopeAppendParams &p, const double *inv_freq, int half,
+RopeTurns rope_turns_of(const double *inv_freq, int half);
+cudaError_t launch_rope_append(const RopeAppendParams &p, const RopeTurns &turns,
                                cudaStream_t stream);
 cudaError_t launch_rope_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
-                                     const double *inv_freq, int half, cudaStream_t stream);
+                                     const RopeTurns &turns, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams &p, int d, int heads_per_cta, cudaStream_t stream);
 cudaError_t launch_decode_paged(const DecodeParams &p, const PagedView &pg, bool e4m3, int d,
                                 cudaStream_t stream);
@@ -388,5 +390,6 @@ size_t rope_append_smem_bytes(int H, int KV, int d, int rd);
 int decode_key_tile();
 int decode_ctas_per_sm();
 int decode_paged_ctas_per_sm(bool e4m3);
+int decode_paged_direct_keys();
 int prefill_key_tile();
 int prefill_q_tile();

@@ -387,14 +387,6 @@ void turns_fixed_point(double inv_freq, unsigned long long &hi, unsigned int &lo
     lo = (unsigned int)(x & 0xffffffff);
 }
 
-RopeTurns turns_of(const double *inv_freq, int half)
-{
-    RopeTurns turns{};
-    for (int i = 0; i < half && i < 64; i++)
-        turns_fixed_point(inv_freq[i], turns.hi[i], turns.lo[i]);
-    return turns;
-}
-
 template <bool PAGED>
 cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
                           cudaStream_t stream)
@@ -421,10 +413,17 @@ cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const 
 
 }  // namespace
 
-cudaError_t launch_rope_append(const RopeAppendParams &p, const double *inv_freq, int half,
+RopeTurns rope_turns_of(const double *inv_freq, int half)
+{
+    RopeTurns turns{};
+    for (int i = 0; i < half && i < 64; i++)
+        turns_fixed_point(inv_freq[i], turns.hi[i], turns.lo[i]);
+    return turns;
+}
+
+cudaError_t launch_rope_append(const RopeAppendParams &p, const RopeTurns &turns,
                                cudaStream_t stream)
 {
-    const RopeTurns turns = turns_of(inv_freq, half);
     if (p.rd % 16 == 0) {
         const int rows_per_cta = kAppendThreads / (p.d / 16);
         const dim3 grid(p.total_tokens, (p.H + 2 * p.KV + rows_per_cta - 1) / rows_per_cta);
@@ -439,9 +438,8 @@ cudaError_t launch_rope_append(const RopeAppendParams &p, const double *inv_freq
 // Into pages: one launch when the rotary dimension fits the register kernels;
 // otherwise the staged rows, then (E4M3) keys and values by page.
 cudaError_t launch_rope_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
-                                     const double *inv_freq, int half, cudaStream_t stream)
+                                     const RopeTurns &turns, cudaStream_t stream)
 {
-    const RopeTurns turns = turns_of(inv_freq, half);
     if (p.rd % 16 == 0)
         return launch_append_paged(p, pg, e4m3, turns, stream);
     if (!e4m3)
