@@ -14,8 +14,7 @@ Entry points (same names as the C ABI):
   na_attn_decode_static_ws  na_attn_decode with library-owned scratch
   na_rope_append_kv_paged, na_attn_prefill_chunk_paged, na_attn_decode_paged
                          the same over a paged cache of bf16 or 8-bit (E4M3) pages
-  na_prefill_workspace_size / na_decode_workspace_size / na_decode_paged_workspace_size /
-  na_status_string
+  na_prefill_workspace_size / na_decode_workspace_size, the same with _paged, na_status_string
 """
 from __future__ import annotations
 
@@ -50,7 +49,8 @@ EXPORTED = ("na_rope_append_kv", "na_attn_prefill_chunk", "na_attn_decode",
             "na_attn_decode_static_ws", "na_decode_importance",
             "na_prefill_workspace_size", "na_decode_workspace_size", "na_status_string",
             "na_selftest_wait_timeout", "na_rope_append_kv_paged", "na_attn_prefill_chunk_paged",
-            "na_attn_decode_paged", "na_decode_paged_workspace_size")
+            "na_attn_decode_paged", "na_prefill_paged_workspace_size",
+            "na_decode_paged_workspace_size")
 
 
 class na_attn_cfg(ctypes.Structure):
@@ -118,6 +118,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                 SZ, P, P]
     lib.na_attn_decode_paged.argtypes = [cfgp, I32, P, pagedp, P, I32, P, P, P, I32, I32, P, SZ, P,
                                          P]
+    lib.na_prefill_paged_workspace_size.argtypes = [cfgp, I32, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.na_decode_paged_workspace_size.argtypes = [cfgp, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.na_selftest_wait_timeout.argtypes = [P, P]
     lib.na_status_string.argtypes = [ctypes.c_int]
@@ -127,7 +128,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "na_prefill_workspace_size", "na_decode_workspace_size",
                  "na_selftest_wait_timeout", "na_rope_append_kv_paged",
                  "na_attn_prefill_chunk_paged", "na_attn_decode_paged",
-                 "na_decode_paged_workspace_size"):
+                 "na_prefill_paged_workspace_size", "na_decode_paged_workspace_size"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -407,6 +408,17 @@ def na_decode_workspace_size(cfg: AttnConfig, batch: int, max_kv_len: int,
     return int(out.value)
 
 
+def na_prefill_paged_workspace_size(cfg: AttnConfig, batch: int, total_tokens: int,
+                                    max_new_len: int, max_total_len: int) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    c = cfg.c()
+    _check("na_prefill_paged_workspace_size",
+           lib.na_prefill_paged_workspace_size(ctypes.byref(c), batch, total_tokens, max_new_len,
+                                               max_total_len, ctypes.byref(out)))
+    return int(out.value)
+
+
 def na_decode_paged_workspace_size(cfg: AttnConfig, batch: int, max_kv_len: int,
                                    num_splits: int = 0) -> int:
     lib = load_library()
@@ -454,7 +466,8 @@ def na_attn_prefill_chunk_paged(cfg: AttnConfig, cu_seqlens, cache_lens, max_new
                                 max_total_len: int, q_rot, cache: PagedKVCache, out, gate=None,
                                 workspace=None, status=None, total_tokens: Optional[int] = None,
                                 stream=None):
-    """na_attn_prefill_chunk against bf16 or E4M3 pages (workspace: na_prefill_workspace_size)."""
+    """na_attn_prefill_chunk against bf16 or E4M3 pages (workspace:
+    na_prefill_paged_workspace_size)."""
     lib = load_library()
     batch, T = _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status, total_tokens)
     _want_paged(cache, cfg, batch)

@@ -210,7 +210,7 @@ int check_paged_cache(const na_attn_cfg *cfg, const na_paged_kv_cache *c, int ba
 }
 
 struct PrefillPlan {
-    int pack, tile_tokens, q_tiles, full_units, tail_units, num_splits, split_len, grid;
+    int pack, rep, tile_tokens, q_tiles, full_units, tail_units, num_splits, split_len, grid;
     size_t ws_bytes;
 };
 
@@ -224,7 +224,7 @@ struct PrefillPlan {
 // context chunk on 152 SMs left 120 SMs idle for most of a fifth wave); a
 // merge pass combines the pieces of those units.
 PrefillPlan plan_prefill(const na_attn_cfg *c, int batch, int total_tokens, int max_new_len,
-                         int max_total_len)
+                         int max_total_len, bool paged = false)
 {
     PrefillPlan pl{};
     const int bm = prefill_q_tile(), bn = prefill_key_tile();
@@ -235,10 +235,13 @@ PrefillPlan plan_prefill(const na_attn_cfg *c, int batch, int total_tokens, int 
     // A single sequence whose tokens fill whole tiles gains nothing (measured
     // 3% slower packed on 128-token chunks, group 4), so it stays unpacked.
     const int group = c->num_heads / c->num_kv_heads;
-    pl.pack = (group > 1 && bm % group == 0) ? group : 1;
+    // A paged call packs any group that fits, and lays tiles of few rows over the
+    // lanes several times (prefill.cu, REP).
+    pl.pack = (group > 1 && (paged ? group <= bm : bm % group == 0)) ? group : 1;
     if (batch == 1 && total_tokens % bm == 0)
         pl.pack = 1;
-    pl.tile_tokens = bm / pl.pack;
+    pl.rep = paged && (long long)max_new_len * pl.pack <= bm / kPrefillRep ? kPrefillRep : 1;
+    pl.tile_tokens = bm / pl.rep / pl.pack;
     pl.q_tiles = (max_new_len + pl.tile_tokens - 1) / pl.tile_tokens;
     const long long units = (long long)batch * pl.q_tiles * (c->num_heads / pl.pack);
     const long long sms = sm_count();
@@ -422,6 +425,8 @@ PrefillParams prefill_params(const na_attn_cfg *cfg, const PrefillPlan &pl, int 
     p.softcap = cfg->softcap;
     p.window = cfg->window;
     p.pack = pl.pack;
+    p.pack_inv = 65536 / pl.pack + 1;
+    p.rep = pl.rep;
     p.tile_tokens = pl.tile_tokens;
     p.q_tiles = pl.q_tiles;
     p.HG = p.H / pl.pack;
@@ -614,7 +619,7 @@ int na_attn_prefill_chunk_paged(const na_attn_cfg *cfg, int32_t batch, const int
         return NA_ERR_INVALID_ARG;
     if ((cfg->flags & NA_OUT_GATE) && (!gate || !aligned16(gate)))
         return NA_ERR_INVALID_ARG;
-    const PrefillPlan pl = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len);
+    const PrefillPlan pl = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len, true);
     if (pl.ws_bytes > 0 && (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace)))
         return NA_ERR_WORKSPACE;
     PrefillParams p = prefill_params(cfg, pl, batch, cu_seqlens, cache_lens, total_tokens,
@@ -716,6 +721,18 @@ int na_attn_decode(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
                    cudaSuccess
                ? NA_OK
                : NA_ERR_CUDA;
+}
+
+int na_prefill_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t total_tokens,
+                                    int32_t max_new_len, int32_t max_total_len, size_t *bytes)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if (!bytes || batch <= 0 || total_tokens < 0 || max_new_len < 0 || max_total_len < 0)
+        return NA_ERR_INVALID_ARG;
+    *bytes = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len, true).ws_bytes;
+    return NA_OK;
 }
 
 int na_decode_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_kv_len,

@@ -338,8 +338,10 @@ struct PrefillParams {
     int total_tokens;          // host copy of cu_seqlens[batch]
     float softcap;             // > 0: scores capped to softcap * tanh(s / softcap)
     int window;                // > 0: keys pos - window + 1 .. pos only
-    int pack;                  // query heads of one kv group per tile (a power of two)
-    int tile_tokens;           // tokens per tile: 128 / pack
+    int pack;                  // query heads of one kv group per tile (a power of two but for pages)
+    int tile_tokens;           // tokens per tile: 128 / (pack rep)
+    int pack_inv;              // pages: r / pack = r pack_inv >> 16 for a row r < 128
+    int rep;                   // pages: times the tile's rows are laid over the 128 lanes
     int q_tiles;               // ceil(max_new_len / tile_tokens)
     int HG;                    // head groups per sequence: H / pack
     int full_units;            // units (query tile, head group, sequence) run whole, one CTA each
@@ -366,6 +368,8 @@ struct ImportanceParams {
     float *imp;
     int32_t *status;
 };
+
+constexpr int kPrefillRep = 4;  // PrefillParams.rep of a call whose tiles have few rows
 
 // Kernel launchers (one translation unit each).
 RopeTurns rope_turns_of(const double *inv_freq, int half);

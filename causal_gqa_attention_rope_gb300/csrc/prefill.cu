@@ -52,6 +52,15 @@
 // it took 1595 us, with K converted the same way too 2217 us, and with the tiles
 // left unconverted it would take 920 us.
 //
+// Few rows (REP = 4).  A tile of a paged call with at most 32 rows -- drafted
+// tokens, single tokens of a mixed batch -- is loaded four times over, so that
+// each softmax warp has all the rows in its 32 lanes and takes a quarter of the
+// keys: it exponentiates 32 columns instead of 128 and writes zeros for the
+// others, and the four partial rows of a query are merged at the end like split
+// pieces.  With one warp working on every key and three on padding the softmax
+// held the tile loop up (64 sequences of 512 .. 8192 keys, 2 .. 8 tokens: 156 us
+// against REP_TIME us).
+//
 #include <climits>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -345,7 +354,8 @@ __device__ __forceinline__ void rank_sequences(const PrefillParams &p, RankScrat
     prior = __shfl_sync(0xffffffffu, f.w, 0);
 }
 
-template <int D, bool CAPPED, KvSource SRC>
+// REP: the tile's rows fill 128 / REP lanes, REP times over (paged calls).
+template <int D, bool CAPPED, KvSource SRC, int REP = 1>
 __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS, 1)
     prefill_tc_kernel(const PrefillParams p, const PagedView pg,
                       const __grid_constant__ CUtensorMap map_q,
@@ -421,7 +431,10 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     // ------------------------------------------------------------ the tile --
     // The 128 rows are tile_tokens tokens x pack query heads of one kv group,
     // token-major: row r is token r >> pack_shift, head h0 + (r & (pack - 1)).
+    // (Paged calls pack groups that are no power of two as well.)
     const int pack_shift = __ffs(p.pack) - 1;
+    auto tok_of = [&](int r) { return PAGED ? (r * p.pack_inv) >> 16 : r >> pack_shift; };
+    auto head_of = [&](int r) { return PAGED ? r - tok_of(r) * p.pack : r & (p.pack - 1); };
     const int h0 = hg * p.pack;
     const int kvh = h0 / p.group;
     const int r0 = qt * p.tile_tokens;  // first token of the tile within the sequence
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         prior = __ldg(p.cache_lens + b);
     }
     const int rows_tok = min(p.tile_tokens, n_new - r0);
-    const int rows = rows_tok << pack_shift;  // valid tensor-memory rows
+    const int rows = PAGED ? rows_tok * p.pack : rows_tok << pack_shift;  // valid tensor-memory rows
     const int pos_lo = prior + r0, pos_hi = prior + r0 + rows_tok - 1;
     // Keys the tile can see: from the key tile holding the first row's window
     // start (0 without a window) to the last row; splits cut that range.
@@ -557,14 +570,18 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         // wait), so these copies overlap the tensor-memory allocation and the
         // barrier itself.
         if (!early_q) {
-            mbar_arrive_expect_tx(&sm.q_full, KB * BM * 128);
+            // (a paged box holds tile_tokens x pack rows, 128 / REP of them at most)
+            mbar_arrive_expect_tx(&sm.q_full,
+                                  PAGED ? REP * KB * p.pack * p.tile_tokens * 128 : KB * BM * 128);
             for (int kb = 0; kb < KB; kb++) {
                 bf16 *dst;
                 if constexpr (E4M3)
                     dst = sm.v[0][kb];
                 else
                     dst = sm.q[kb];
-                tc::tma_load_3d(dst, &map_q, kb * 64, h0, tok0 + r0, &sm.q_full);
+                for (int i = 0; i < REP; i++)
+                    tc::tma_load_3d(dst + i * (BM / REP) * 64, &map_q, kb * 64, h0, tok0 + r0,
+                                    &sm.q_full);
             }
         }
         if constexpr (!PAGED) {
@@ -592,7 +609,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     constexpr int LDS = D + 4;   // staged row stride (floats): conflict-free row writes
     constexpr int EPL = D / 32;  // elements per lane in the row stores
     constexpr int GW = D / 64;   // 32-bit words of gate per lane and row
-    constexpr int SR = BM / 8;   // rows stored per warp
+    constexpr int SR = BM / REP / 8;  // rows stored per warp
     float *stage = reinterpret_cast<float *>(&sm.k[0]);  // the K ring (and what follows), idle by then
     const bool split_out = nsplit > 1;
     // rows of this piece in the workspace: [tail unit][split][row]
@@ -603,8 +620,8 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
 #pragma unroll
         for (int i = 0; i < SR; i++) {
             const int rr = warp * SR + i;
-            const size_t off = ((size_t)(tok0 + r0 + (rr >> pack_shift)) * p.H + h0 +
-                                (rr & (p.pack - 1))) * D + lane * 2 * GW;
+            const size_t off = ((size_t)(tok0 + r0 + tok_of(rr)) * p.H + h0 + head_of(rr)) * D +
+                               lane * 2 * GW;
             gq[i][0] = 0;
             if constexpr (GW == 2)
                 gq[i][1] = 0;
@@ -887,8 +904,12 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     } else {
         // ------------------------------------------------------- softmax --
         const int quarter = warp & 3;
-        const int r = quarter * 32 + lane;  // query row == TMEM lane
-        const int row_pos = pos_lo + (r >> pack_shift);
+        const int r = quarter * 32 + lane;  // TMEM lane
+        const int rq = r & (BM / REP - 1);  // its query row
+        const int row_pos = pos_lo + tok_of(rq);
+        // the 32-column blocks of a score tile that this warp takes
+        constexpr int NC = 4 / REP;
+        const int c0 = REP == 1 ? 0 : quarter / (4 / REP) * NC;
         const int row_lo = p.window > 0 ? row_pos - p.window + 1 : INT_MIN;  // first visible key
         constexpr bool capped = CAPPED;
         // soft-capped scores, kept in the raw score's units so the rest of the
@@ -920,10 +941,10 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 break;
             }
             tc::fence_after_sync();
-            uint32_t sr[4][32];
+            uint32_t sr[NC][32];
 #pragma unroll
-            for (int c = 0; c < 4; c++)
-                tc::tmem_ld32(s_t + c * 32, sr[c]);
+            for (int c = 0; c < NC; c++)
+                tc::tmem_ld32(s_t + (c0 + c) * 32, sr[c]);
             tc::tmem_wait_ld();
 
             // E4M3: what turns a raw score of 16 keys into the log2 domain (the soft
@@ -934,7 +955,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 if constexpr (E4M3) {
                     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                  : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                                 : "r"(smem_addr(&sm.mul_off[j % SCALE_SLOTS][c])));
+                                 : "r"(smem_addr(&sm.mul_off[j % SCALE_SLOTS][c0 + c])));
                     // positive: masked scores are -inf
                     x.x = fmaxf(x.x * sl2, 1.2e-38f);
                     x.y = fmaxf(x.y * sl2, 1.2e-38f);
@@ -944,7 +965,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             if constexpr (capped && E4M3) {
                 const float in = 2.0f / p.softcap, out = p.softcap * NA_LOG2E;
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
+                for (int c = 0; c < NC; c++) {
                     const float4 mo = mul_off(c);
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
@@ -954,7 +975,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 }
             } else if constexpr (capped) {
 #pragma unroll
-                for (int c = 0; c < 4; c++)
+                for (int c = 0; c < NC; c++)
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
                         const float e = ex2_mufu(__uint_as_float(sr[c][i]) * cap_in);
@@ -964,10 +985,10 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             const bool need_mask = (j0 + BN - 1 > pos_lo) || (j0 + BN > k_end) || (j0 < row_lo);
             if (need_mask) {
 #pragma unroll
-                for (int c = 0; c < 4; c++)
+                for (int c = 0; c < NC; c++)
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
-                        const int key = j0 + c * 32 + i;
+                        const int key = j0 + (c0 + c) * 32 + i;
                         if (key > row_pos || key >= k_end || key < row_lo)
                             sr[c][i] = __float_as_uint(-INFINITY);
                     }
@@ -976,9 +997,9 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             // keys, of score + V's exponent)
             float mxs;
             if constexpr (E4M3) {
-                float mg[8];
+                float mg[2 * NC];
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
+                for (int c = 0; c < NC; c++) {
                     const float4 mo = mul_off(c);
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
@@ -994,12 +1015,14 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                         mg[2 * c + h] = fmaf(fmaxf(m0, m1), mul, h ? mo.w : mo.z);
                     }
                 }
-                mxs = max3f(max3f(mg[0], mg[1], mg[2]), max3f(mg[3], mg[4], mg[5]),
-                            fmaxf(mg[6], mg[7]));
+                mxs = fmaxf(mg[0], mg[1]);
+#pragma unroll
+                for (int c = 1; c < NC; c++)
+                    mxs = max3f(mxs, mg[2 * c], mg[2 * c + 1]);
             } else {
             float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; c++)
+            for (int c = 0; c < NC; c++)
 #pragma unroll
                 for (int i = 0; i < 32; i += 8) {
                     mxa = max3f(mxa, __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
@@ -1022,14 +1045,14 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
+            for (int c = 0; c < NC; c++) {
                 uint32_t pk[16];
                 float4 mo = mul_off(c);
                 float2 inv;
                 if constexpr (E4M3)
                     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                                  : "=f"(inv.x), "=f"(inv.y)
-                                 : "r"(smem_addr(&sm.v_inv[j % SCALE_SLOTS][c])));
+                                 : "r"(smem_addr(&sm.v_inv[j % SCALE_SLOTS][c0 + c])));
                 if constexpr (E4M3 && capped)
                     mo.x = mo.y = 1.0f;
 #pragma unroll
@@ -1049,10 +1072,17 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                         pk[i] = pack_bf16x2(pp.x, pp.y);
                     }
                 }
-                tc::tmem_st16(s_t + c * 16, pk);
+                tc::tmem_st16(s_t + (c0 + c) * 16, pk);
             }
             const float2 acc01 = __fadd2_rn(acc[0], acc[1]), acc23 = __fadd2_rn(acc[2], acc[3]);
             const float rs = (acc01.x + acc01.y) + (acc23.x + acc23.y);
+            if constexpr (REP > 1) {  // the other warps' keys weigh nothing in these lanes
+                const uint32_t none[16] = {};
+#pragma unroll
+                for (int c = 1; c < REP; c++)
+                    tc::tmem_st16(s_t + ((c0 + c * NC) & 3) * 16, none);
+                static_assert(NC == 1, "one column block per warp");
+            }
             tc::tmem_wait_st();
 
             if (!E4M3 && (j0 + BN > k_end || (PAGED && j0 < vis_lo))) {
@@ -1113,18 +1143,38 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         // last P V product.
         if (!E4M3 && ok && gated_out)
             load_gate();
-        if (!ok) {
-            if (lane == 0)
-                set_abort(&sm.abort_flag, p.status);
-        } else if (warp_wait(&sm.o_done[(n_tiles - 1) % NUM_S], ((n_tiles - 1) / NUM_S) & 1,
-                             &sm.abort_flag)) {
+        const bool done = ok && warp_wait(&sm.o_done[(n_tiles - 1) % NUM_S],
+                                          ((n_tiles - 1) / NUM_S) & 1, &sm.abort_flag);
+        float2 *ml = reinterpret_cast<float2 *>(stage + BM * LDS);  // REP: (reference, sum) per lane
+        if constexpr (REP > 1) {  // joined by every softmax warp, whatever became of its waits
+            ml[r] = make_float2(m_ref, l);
+            named_barrier_sync(1, BM);
+        }
+        if (done) {
             // ---------------------------------------------------- epilogue --
             // Each thread writes its O row (normalised unless this is a split
             // partial) into the idle K ring, rows padded by 16 bytes so the
             // row-per-thread writes are bank-conflict free; then each warp
             // stores its 32 rows one row per instruction, coalesced.
             tc::fence_after_sync();
-            const float scale = split_out ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
+            float scale = split_out ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
+            if constexpr (REP > 1) {  // the row's partials: their weights against each other
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int i = 0; i < REP; i++)
+                    M = fmaxf(M, ml[rq + i * (BM / REP)].x);
+#pragma unroll
+                for (int i = 0; i < REP; i++) {
+                    const float2 x = ml[rq + i * (BM / REP)];
+                    if (x.x != -INFINITY)
+                        L = fmaf(x.y, ex2_mufu(x.x - M), L);
+                }
+                scale = m_ref == -INFINITY ? 0.f : ex2_mufu(m_ref - M);
+                if (!split_out)
+                    scale *= L > 0.f ? 1.0f / L : 0.f;
+                m_ref = M;
+                l = L;
+            }
             {
                 uint32_t o[D / 32][32];  // the whole row in one round of loads
 #pragma unroll
@@ -1175,6 +1225,13 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 v[0] = x.x;
                 v[1] = x.y;
             }
+            if constexpr (REP > 1) {  // the row's weighted partials
+#pragma unroll
+                for (int u = 1; u < REP; u++)
+#pragma unroll
+                    for (int e = 0; e < EPL; e++)
+                        v[e] += src[u * (BM / REP) * LDS + e];
+            }
             if (split_out) {
                 float *dst = p.part_o + (piece_row0 + rr) * D + lane * EPL;
                 if constexpr (EPL == 4)
@@ -1196,8 +1253,8 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
 #pragma unroll
             for (int e = 0; e < EPL; e += 2)
                 pk[e / 2] = pack_bf16x2(v[e], v[e + 1]);
-            const size_t tok = (size_t)(tok0 + r0 + (rr >> pack_shift));
-            const int h = h0 + (rr & (p.pack - 1));
+            const size_t tok = (size_t)(tok0 + r0 + tok_of(rr));
+            const int h = h0 + head_of(rr);
             const size_t off = (tok * p.H + h) * D + lane * EPL;
             if constexpr (EPL == 4)
                 *reinterpret_cast<uint2 *>(p.out + off) = make_uint2(pk[0], pk[1]);
@@ -1311,10 +1368,11 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillParam
     if (prior < 0 || (!ring && pos_hi >= p.capacity) || pos_hi >= p.max_total_len)
         return;
     const int pack_shift = __ffs(p.pack) - 1;
-    if (r >= (rows_tok << pack_shift))
+    if (r >= (PAGED ? rows_tok * p.pack : rows_tok << pack_shift))
         return;
-    const size_t out_row = (size_t)(tok0 + r0 + (r >> pack_shift)) * p.H + hg * p.pack +
-                           (r & (p.pack - 1));
+    const int tok = PAGED ? (r * p.pack_inv) >> 16 : r >> pack_shift;
+    const size_t out_row = (size_t)(tok0 + r0 + tok) * p.H + hg * p.pack +
+                           (PAGED ? r - tok * p.pack : r & (p.pack - 1));
     uint32_t gw[EPL / 2];  // gate words, requested before the merge arithmetic
     const bool gated = (p.flags & NA_OUT_GATE) && p.gate;
     if (gated) {
@@ -1402,7 +1460,7 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillParam
         *reinterpret_cast<uint32_t *>(dst) = packed[0];
 }
 
-template <int D, KvSource SRC>
+template <int D, KvSource SRC, int REP = 1>
 cudaError_t launch_prefill_t(const PrefillParams &p, const PagedView &pg, int total_tokens,
                              int cache_batch, cudaStream_t stream)
 {
@@ -1438,10 +1496,10 @@ cudaError_t launch_prefill_t(const PrefillParams &p, const PagedView &pg, int to
     const size_t smem = tc_smem_bytes<D, SRC>();
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = once_per_device(configured, [smem] {
-        cudaError_t r = cudaFuncSetAttribute(prefill_tc_kernel<D, false, SRC>,
+        cudaError_t r = cudaFuncSetAttribute(prefill_tc_kernel<D, false, SRC, REP>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(prefill_tc_kernel<D, true, SRC>,
+            r = cudaFuncSetAttribute(prefill_tc_kernel<D, true, SRC, REP>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return r;
     });
@@ -1449,14 +1507,23 @@ cudaError_t launch_prefill_t(const PrefillParams &p, const PagedView &pg, int to
         return e;
     const dim3 grid(p.full_units + p.tail_units * p.num_splits);
     const dim3 block(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS);
-    e = p.softcap > 0.f ? launch_kernel(prefill_tc_kernel<D, true, SRC>, grid, block, smem, stream,
+    e = p.softcap > 0.f ? launch_kernel(prefill_tc_kernel<D, true, SRC, REP>, grid, block, smem, stream,
                                         p, pg, mq, mk, mv)
-                        : launch_kernel(prefill_tc_kernel<D, false, SRC>, grid, block, smem, stream,
+                        : launch_kernel(prefill_tc_kernel<D, false, SRC, REP>, grid, block, smem, stream,
                                         p, pg, mq, mk, mv);
     if (e != cudaSuccess || p.num_splits == 1)
         return e;
     return launch_kernel(prefill_combine_kernel<D, SRC != KV_CONTIGUOUS>, dim3(p.tail_units, BM / kMergeRows), dim3(256),
                          0, stream, p);
+}
+
+// A paged call, by whether its tiles have few rows.
+template <int D, KvSource SRC>
+cudaError_t launch_paged_t(const PrefillParams &p, const PagedView &pg, int total_tokens,
+                           cudaStream_t stream)
+{
+    return p.rep == 1 ? launch_prefill_t<D, SRC, 1>(p, pg, total_tokens, 0, stream)
+                      : launch_prefill_t<D, SRC, kPrefillRep>(p, pg, total_tokens, 0, stream);
 }
 
 }  // namespace
@@ -1525,8 +1592,8 @@ cudaError_t launch_prefill_paged(const PrefillParams &p, const PagedView &pg, bo
                                  int total_tokens, cudaStream_t stream)
 {
     if (d == 128)
-        return e4m3 ? launch_prefill_t<128, KV_PAGED_E4M3>(p, pg, total_tokens, 0, stream)
-                    : launch_prefill_t<128, KV_PAGED>(p, pg, total_tokens, 0, stream);
-    return e4m3 ? launch_prefill_t<64, KV_PAGED_E4M3>(p, pg, total_tokens, 0, stream)
-                : launch_prefill_t<64, KV_PAGED>(p, pg, total_tokens, 0, stream);
+        return e4m3 ? launch_paged_t<128, KV_PAGED_E4M3>(p, pg, total_tokens, stream)
+                    : launch_paged_t<128, KV_PAGED>(p, pg, total_tokens, stream);
+    return e4m3 ? launch_paged_t<64, KV_PAGED_E4M3>(p, pg, total_tokens, stream)
+                : launch_paged_t<64, KV_PAGED>(p, pg, total_tokens, stream);
 }

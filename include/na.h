@@ -386,7 +386,7 @@ int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_ro
  *
  *   max_total_len  HOST upper bound of cache_lens[b] + new length;
  *                  <= pages_per_seq * page_size.
- *   workspace      na_prefill_workspace_size() bytes (NULL allowed when that is 0).
+ *   workspace      na_prefill_paged_workspace_size() bytes (NULL allowed when that is 0).
  *   Everything else as in na_attn_prefill_chunk.
  */
 int na_attn_prefill_chunk_paged(const na_attn_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
@@ -394,6 +394,10 @@ int na_attn_prefill_chunk_paged(const na_attn_cfg *cfg, int32_t batch, const int
                                 int32_t max_new_len, int32_t max_total_len, const void *q_rot,
                                 const na_paged_kv_cache *cache, const void *gate, void *out,
                                 void *workspace, size_t ws_bytes, int32_t *status, void *stream);
+
+/* Workspace bytes (HOST out-parameter) that na_attn_prefill_chunk_paged needs for these bounds. */
+int na_prefill_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t total_tokens,
+                                    int32_t max_new_len, int32_t max_total_len, size_t *bytes);
 
 /* Workspace bytes (HOST out-parameter) that na_attn_decode_paged needs for these bounds. */
 int na_decode_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_kv_len,

@@ -303,6 +303,16 @@ PREFILL = [
     ("e4m3", 128, 16, 4, 4, [(1400 + 17 * i, 1 + i % 5) for i in range(60)], {}),
     ("bf16", 128, 32, 4, 4, [(1400 + 17 * i, 1 + i % 5) for i in range(60)], {}),
     ("e4m3", 64, 64, 4, 2, [(2000 - 11 * i, 1 + i % 3) for i in range(45)], dict(gate=True)),
+    # groups that are no power of two; few rows (laid over the tile four times) and many
+    ("e4m3", 128, 32, 2, 5, [(900, 6), (40, 1), (0, 3), (0, 0), (127, 2)], dict(gate=True)),
+    ("e4m3", 128, 32, 2, 5, [(900, 60), (40, 7), (0, 26), (3, 25)], {}),
+    ("bf16", 64, 16, 2, 3, [(300, 10), (5000, 1), (0, 9)], dict(window=70)),
+    ("bf16", 128, 64, 1, 6, [(300, 50), (0, 129)], dict(softcap=8.0)),
+    ("e4m3", 64, 16, 1, 12, [(700, 2), (31, 1)], dict(softcap=8.0, window=500)),
+    ("e4m3", 64, 64, 3, 1, [(60, 32), (1000, 31)], dict(window=33)),
+    ("bf16", 128, 16, 1, 32, [(100, 1), (2000, 1)], {}),
+    ("e4m3", 64, 16, 1, 40, [(100, 3), (600, 4)], {}),
+    ("e4m3", 64, 16, 1, 130, [(100, 3)], {}),
 ]
 
 
@@ -311,7 +321,7 @@ def run_prefill(cfg, q, cache, prior, new, gate=None):
     top, most = max(p + n for p, n in zip(prior, new)), max(new)
     go = Guarded(q.shape, q.dtype, DEV)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
-    ws = na.workspace(na.na_prefill_workspace_size(cfg, len(new), T, most, top), DEV)
+    ws = na.workspace(na.na_prefill_paged_workspace_size(cfg, len(new), T, most, top), DEV)
     na.na_attn_prefill_chunk_paged(cfg, cu_of(new), ints(prior), most, top, q.to(DEV), cache, go.t,
                                    gate=None if gate is None else gate.to(DEV), workspace=ws,
                                    status=status)
@@ -418,7 +428,7 @@ def test_prompt_then_decode_with_importance(fmt):
                                    q_norm_w=qw, k_norm_w=kw, status=status)
         probs = None
         if max(new) > 1:
-            ws = na.workspace(na.na_prefill_workspace_size(cfg, B, T, max(new), top), DEV)
+            ws = na.workspace(na.na_prefill_paged_workspace_size(cfg, B, T, max(new), top), DEV)
             na.na_attn_prefill_chunk_paged(cfg, cu_of(new), ints(at), max(new), top, q_rot, cache,
                                            out, workspace=ws, status=status)
         else:

@@ -110,7 +110,7 @@ def test_workspaces(lib):
     assert decode(lib, c, paged(), ws_bytes=need - 1) == na.NA_ERR_WORKSPACE
     assert size(0, 512, 0) == na.NA_ERR_INVALID_ARG
     assert size(4, -1, 0) == na.NA_ERR_INVALID_ARG
-    assert lib.na_prefill_workspace_size(ctypes.byref(c), 4, 8, 2, 512 * 8, ctypes.byref(out)) == 0
+    assert lib.na_prefill_paged_workspace_size(ctypes.byref(c), 4, 8, 2, 512 * 8, ctypes.byref(out)) == 0
     assert out.value > 0
     big = paged(pages_per_seq=64)
     assert prefill(lib, c, big, top=4096) == na.NA_ERR_WORKSPACE
