@@ -312,18 +312,43 @@ def _want_cache(cache: "KVCache", cfg: "AttnConfig", batch: int):
 
 
 def _want_paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int):
-    k_scale, v_scale = cache.k_scale, cache.v_scale
-    kind = "bfloat16" if k_scale is None and v_scale is None else "float8_e4m3fn"
-    shape = cache.k.shape
+    """A paged cache's tensors, one by one."""
+    bf16 = cache.k_scale is None and cache.v_scale is None
+    kind = "bfloat16" if bf16 else "float8_e4m3fn"
     _want(cache.k, "cache.k", kind, (None, cfg.num_kv_heads, None, cfg.head_dim))
-    _want(cache.v, "cache.v", kind, shape)
+    _want(cache.v, "cache.v", kind, cache.k.shape)
     _want(cache.page_table, "cache.page_table", "int32", (None, None), batch)
-    if kind != "bfloat16":
-        if k_scale is None or v_scale is None:
-            raise ValueError(f"cache.{'k' if k_scale is None else 'v'}_scale: missing")
-        scales = (shape[0], cfg.num_kv_heads)
-        _want(k_scale, "cache.k_scale", "uint8", scales)
-        _want(v_scale, "cache.v_scale", "uint8", scales)
+    if not bf16:
+        scales = (cache.k.shape[0], cfg.num_kv_heads)
+        for t, name in ((cache.k_scale, "cache.k_scale"), (cache.v_scale, "cache.v_scale")):
+            if t is None:
+                raise ValueError(f"{name}: missing")
+            _want(t, name, "uint8", scales)
+
+
+def _paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int) -> na_paged_kv_cache:
+    """The C struct of a paged cache, its tensors checked (all at once: a decode
+    step's host time is mostly such checks)."""
+    k, v, table, k_scale, v_scale = cache.k, cache.v, cache.page_table, cache.k_scale, cache.v_scale
+    bf16 = k_scale is None and v_scale is None
+    try:
+        shape, dtype = k.shape, k.dtype
+        num_pages, kv_heads, page_size, d = shape
+        rows, pages_per_seq = table.shape
+        ok = (kv_heads == cfg.num_kv_heads and d == cfg.head_dim and rows >= batch
+              and v.shape == shape and v.dtype is dtype and table.dtype is _dtypes["int32"]
+              and dtype is _dtypes["bfloat16" if bf16 else "float8_e4m3fn"])
+        if ok and not bf16:
+            u8, scales = _dtypes["uint8"], (num_pages, kv_heads)
+            ok = (k_scale.dtype is u8 and v_scale.dtype is u8 and k_scale.shape == scales
+                  and v_scale.shape == scales)
+    except (AttributeError, KeyError, ValueError):  # no tensor, a type not met yet, another rank
+        ok = False
+    if not ok:
+        _want_paged(cache, cfg, batch)
+        return cache.c()
+    return na_paged_kv_cache(*_ptrs(k, v, k_scale, v_scale, table), num_pages, page_size, rows,
+                             pages_per_seq, NA_KV_BF16 if bf16 else NA_KV_E4M3)
 
 
 def _check(fn: str, rc: int):
@@ -378,8 +403,8 @@ def na_rope_append_kv_paged(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache
     lib = load_library()
     batch, T = _append_args(cfg, cu_seqlens, cache_lens, q, k, v, q_out, q_norm_w, k_norm_w,
                             status, total_tokens)
-    _want_paged(cache, cfg, batch)
-    c, r, kc = cfg.c(), rope.c(), cache.c()
+    kc = _paged(cache, cfg, batch)
+    c, r = cfg.c(), rope.c()
     cu, lens, *rows, st = _ptrs(cu_seqlens, cache_lens, q, k, v, q_norm_w, k_norm_w, q_out, status)
     rc = lib.na_rope_append_kv_paged(ctypes.byref(c), ctypes.byref(r), batch, cu, lens, T, *rows,
                                      ctypes.byref(kc), st, _stream_for(q, stream))
@@ -470,8 +495,8 @@ def na_attn_prefill_chunk_paged(cfg: AttnConfig, cu_seqlens, cache_lens, max_new
     na_prefill_paged_workspace_size)."""
     lib = load_library()
     batch, T = _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status, total_tokens)
-    _want_paged(cache, cfg, batch)
-    c, kc = cfg.c(), cache.c()
+    kc = _paged(cache, cfg, batch)
+    c = cfg.c()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     cu, lens, pq, pgate, po, ws, st = _ptrs(cu_seqlens, cache_lens, q_rot, gate, out, workspace,
                                             status)
@@ -483,11 +508,12 @@ def na_attn_prefill_chunk_paged(cfg: AttnConfig, cu_seqlens, cache_lens, max_new
 
 def _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status):
     H, d = cfg.num_heads, cfg.head_dim
-    B = int(q_rot.shape[0])
-    rows = (B, H, d)
-    if not (q_rot.dtype is _dtypes.get("bfloat16") and q_rot.shape == rows):
+    shape, dtype = q_rot.shape, q_rot.dtype
+    B = int(shape[0])
+    if not (dtype is _dtypes.get("bfloat16") and shape[1:] == (H, d) and out.dtype is dtype
+            and out.shape == shape):
         _want(q_rot, "q_rot", "bfloat16", (None, H, d))
-    _want(out, "out", "bfloat16", rows)
+        _want(out, "out", "bfloat16", (B, H, d))
     _want(gate, "gate", "bfloat16", (B, H, d))
     _want(kv_lens, "kv_lens", "int32", (None,), B)
     _want(probs, "probs", "float32", (B, H, None))
@@ -517,8 +543,8 @@ def na_attn_decode_paged(cfg: AttnConfig, q_rot, cache: PagedKVCache, kv_lens, m
     """na_attn_decode over bf16 or E4M3 pages (workspace: na_decode_paged_workspace_size)."""
     lib = load_library()
     batch = _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status)
-    _want_paged(cache, cfg, batch)
-    c, kc = cfg.c(), cache.c()
+    kc = _paged(cache, cfg, batch)
+    c = cfg.c()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     stride = int(probs.shape[-1]) if probs is not None else 0
     pq, lens, pgate, po, pp, ws, st = _ptrs(q_rot, kv_lens, gate, out, probs, workspace, status)
