@@ -435,10 +435,13 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
     }
     int pos = -1;
     if (tk < ntok) {  // a warp's threads share tk
+        const int end = __ldg(p.cu_seqlens + p.batch);  // rows behind it are left alone
         int b;
         owner_of(p, t0 + tk, lane, b, pos);
         int id = 0;
-        if (pos < 0 || pos >= p.capacity) {
+        if (t0 + tk >= end) {
+            pos = -1;
+        } else if (pos < 0 || pos >= p.capacity) {
             if (lane == 0)
                 na_report(p.status, NA_ERR_CAPACITY);
             pos = -1;

@@ -247,7 +247,11 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const RopeA
 
 // -------------------------------------------------------- staged path --
 
-template <bool PAGED>
+// Where the staged kernel's keys and values go; a paged call's rows behind the
+// last sequence are left alone.
+enum StagedTarget { TO_CACHE, TO_PAGES, QUERIES_ALONE };
+
+template <StagedTarget TO>
 __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(const RopeAppendParams p,
                                                                            const PagedView pg,
                                                                            const RopeTurns turns)
@@ -274,6 +278,8 @@ __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(cons
         reinterpret_cast<uint4 *>(trig)[i] = __ldg(reinterpret_cast<const uint4 *>(&kTrig) + i);
     grid_dependency_wait();
     grid_dependents_launch();
+    if (TO != TO_CACHE && t >= __ldg(p.cu_seqlens + p.batch))
+        return;
     int b, pos;
     owner_of(p, t, lane, b, pos);
     const bool ring = (p.flags & NA_RING_CACHE) != 0;  // slot = pos % capacity
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(cons
     }
     int slot;
     size_t cap;
-    if (!cache_place<PAGED>(p, pg, pos, b, slot, cap)) {
+    if (!cache_place<TO == TO_PAGES>(p, pg, pos, b, slot, cap)) {
         if (threadIdx.x == 0)
             na_report(p.status, NA_ERR_PAGE);
         return;
@@ -387,7 +393,7 @@ void turns_fixed_point(double inv_freq, unsigned long long &hi, unsigned int &lo
     lo = (unsigned int)(x & 0xffffffff);
 }
 
-template <bool PAGED>
+template <StagedTarget TO>
 cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
                           cudaStream_t stream)
 {
@@ -396,7 +402,7 @@ cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const 
     static std::atomic<size_t> configured[kMaxDevices];
     const int dev = current_device_index();
     if (smem > 48 * 1024 && (dev < 0 || smem > configured[dev].load(std::memory_order_acquire))) {
-        cudaError_t e = cudaFuncSetAttribute(rope_append_staged_kernel<PAGED>,
+        cudaError_t e = cudaFuncSetAttribute(rope_append_staged_kernel<TO>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
         if (e != cudaSuccess)
@@ -407,7 +413,7 @@ cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const 
                 ;
         }
     }
-    return launch_kernel(rope_append_staged_kernel<PAGED>, dim3(p.total_tokens),
+    return launch_kernel(rope_append_staged_kernel<TO>, dim3(p.total_tokens),
                          dim3(kStagedThreads), smem, stream, p, pg, turns);
 }
 
@@ -432,7 +438,7 @@ cudaError_t launch_rope_append(const RopeAppendParams &p, const RopeTurns &turns
                                  turns);
         return launch_kernel(rope_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, p, turns);
     }
-    return launch_staged<false>(p, PagedView{}, turns, stream);
+    return launch_staged<TO_CACHE>(p, PagedView{}, turns, stream);
 }
 
 // Into pages: one launch when the rotary dimension fits the register kernels;
@@ -443,10 +449,10 @@ cudaError_t launch_rope_append_paged(const RopeAppendParams &p, const PagedView 
     if (p.rd % 16 == 0)
         return launch_append_paged(p, pg, e4m3, turns, stream);
     if (!e4m3)
-        return launch_staged<true>(p, pg, turns, stream);
+        return launch_staged<TO_PAGES>(p, pg, turns, stream);
     RopeAppendParams q = p;
     q.KV = 0;
-    const cudaError_t e = launch_staged<false>(q, pg, turns, stream);
+    const cudaError_t e = launch_staged<QUERIES_ALONE>(q, pg, turns, stream);
     return e != cudaSuccess ? e : launch_append_pages(p, pg, turns, stream);
 }
 

@@ -127,9 +127,9 @@ typedef struct na_kv_cache {
  *     its tokens, an attention call's outputs of that sequence are unspecified.
  *   - Sequences may share pages that they only read (a common prompt).  Pages
  *     that a call appends to belong to one sequence.
- *   - Slots that hold no position of the sequence may hold any bits.  The values
- *     that are attended have to be finite: a NaN or infinity of V reaches every
- *     query row of its tile, masked or not.
+ *   - Slots that hold no position of the sequence may hold any bits.  Queries and
+ *     the keys and values of the sequence have to be finite: a NaN or infinity of
+ *     V reaches every query row of its tile, masked or not.
  *   - Sizes: page_size 16, 32, 64 or 128; num_pages * kv heads * page_size
  *     <= 2^31 - 1 (NA_ERR_UNSUPPORTED otherwise).  The capacity of a sequence is
  *     pages_per_seq * page_size.  NA_RING_CACHE is NA_ERR_UNSUPPORTED: a window
@@ -348,6 +348,8 @@ int na_decode_importance(const na_attn_cfg *cfg, int32_t batch, const float *pro
  * whose first token is appended depends on the new tokens alone, whatever the
  * page held before.  q_out is bf16 in both cases.
  *
+ *   total_tokens  HOST upper bound of cu_seqlens[batch] (a padded batch): rows of
+ *                 q_out past cu_seqlens[batch] are left as they were.
  *   status  NA_ERR_CAPACITY for a token whose position is not below
  *           pages_per_seq * page_size, NA_ERR_PAGE for one whose table entry
  *           lies outside the cache, NA_ERR_INVALID_ARG (NA_KV_E4M3) for a
@@ -386,6 +388,8 @@ int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_ro
  *
  *   max_total_len  HOST upper bound of cache_lens[b] + new length;
  *                  <= pages_per_seq * page_size.
+ *   total_tokens   HOST upper bound of cu_seqlens[batch] (a padded batch): rows of
+ *                  out past cu_seqlens[batch] are left as they were.
  *   workspace      na_prefill_paged_workspace_size() bytes (NULL allowed when that is 0).
  *   Everything else as in na_attn_prefill_chunk.
  */

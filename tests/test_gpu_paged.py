@@ -7,7 +7,8 @@ import torch
 
 import causal_gqa_attention_rope_gb300 as na
 from harness import Guarded
-from paged_ref import (Paged, attend, bits, exponent, make_paged, normed_rotated, v_normed)
+from paged_ref import (Paged, attend, bits, exponent, make_paged, normed_rotated, v_normed,
+                       values)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -208,6 +209,15 @@ DECODE = [
     ("bf16", 128, 16, 1, 12, [3000, 63], dict(window=1000, probs=True)),
     ("bf16", 64, 128, 4, 1, [127, 1, 900], dict(softcap=5.0)),
     ("bf16", 128, 32, 2, 6, [100, 31], dict(splits=2)),
+    # short sequences: one CTA per stream
+    ("e4m3", 128, 16, 2, 16, [300, 1, 0, 512], dict(window=40, probs=True)),
+    ("e4m3", 128, 64, 2, 3, [500, 64, 63], dict(softcap=9.0, gate=True, probs=True)),
+    ("bf16", 64, 32, 1, 5, [0, 400, 33], dict(window=64, probs=True, gate=True)),
+    ("bf16", 128, 128, 2, 8, [512, 129], dict(softcap=9.0, probs=True)),
+    ("bf16", 128, 128, 2, 8, [513, 129], dict(probs=True)),
+    ("e4m3", 64, 16, 2, 4, [0, 0], {}),
+    ("bf16", 64, 16, 1, 2, [i % 40 for i in range(700)], {}),
+    ("e4m3", 64, 16, 1, 2, [(i * 37) % 600 for i in range(300)], {}),
 ]
 
 
@@ -313,6 +323,9 @@ PREFILL = [
     ("bf16", 128, 16, 1, 32, [(100, 1), (2000, 1)], {}),
     ("e4m3", 64, 16, 1, 40, [(100, 3), (600, 4)], {}),
     ("e4m3", 64, 16, 1, 130, [(100, 3)], {}),
+    # more sequences than are ranked
+    ("e4m3", 64, 16, 1, 2, [(i % 50, i % 4) for i in range(270)], {}),
+    ("bf16", 64, 16, 1, 2, [(200 - i % 50, i % 30) for i in range(100)], {}),
 ]
 
 
@@ -500,6 +513,127 @@ def test_graph_replay_with_new_lengths():
     assert torch.equal(bits(a), bits(b))
     for x, y in ((ca.k, cb.k), (ca.v, cb.v), (ca.k_scale, cb.k_scale), (ca.v_scale, cb.v_scale)):
         assert torch.equal(bits(x), bits(y))
+
+
+@pytest.mark.parametrize("fmt,rd", [("bf16", 64), ("e4m3", 64), ("bf16", 18), ("e4m3", 18)])
+def test_padded_batch_leaves_the_rest_alone(fmt, rd):
+    """total_tokens above cu_seqlens[batch]: rows of q_out and out behind the last
+    sequence, and the pages, as without them."""
+    case = (64, rd, 16, 2, 4, {}, [(20, 9), (3, 40)])
+    cfg, rope, prior, new, cache, q, k, v, _, _ = append_case(case, 63, fmt)
+    q_ref, after, _ = run_append(cfg, rope, prior, new, cache, q, k, v, None, None)
+    pad = lambda t: torch.cat([t, torch.ones(15, *t.shape[1:], dtype=t.dtype)]).to(DEV)  # noqa: E731
+    dc = cache.to(DEV)
+    T = sum(new)
+    q_out = torch.full((T + 15, 4, 64), -3.0, dtype=torch.bfloat16, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    na.na_rope_append_kv_paged(cfg, rope, cu_of(new), ints(prior), pad(q), pad(k), pad(v), q_out, dc,
+                               status=status)
+    out = torch.full_like(q_out, -5.0)
+    ws = na.workspace(na.na_prefill_paged_workspace_size(cfg, 2, T + 15, 40, 43), DEV)
+    na.na_attn_prefill_chunk_paged(cfg, cu_of(new), ints(prior), 40, 43, q_out, dc, out,
+                                   workspace=ws, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(bits(q_out[:T].cpu()), bits(q_ref)) and (q_out[T:] == -3.0).all()
+    assert (out[T:] == -5.0).all()
+    got = Paged.back(dc)
+    for a, b in ((got.k, after.k), (got.v, after.v)):
+        assert torch.equal(bits(a), bits(b))
+    ref = attend(after, q_ref, [(0, 20, 9), (9, 3, 40)])
+    check(out[:T], ref.out, ref.tol, "out")
+
+
+def test_append_many_sequences():
+    """A 32-way search of three rounds: 1100 sequences of zero to two tokens."""
+    seqs = [(i % 23, i % 3) for i in range(1100)]
+    test_append_e4m3_pages((64, 64, 16, 1, 1, {}, seqs), 1.0)
+    test_append_bf16_pages_equal_the_contiguous_append((64, 64, 16, 1, 1, {}, seqs))
+
+
+def test_append_e4m3_zeros_first():
+    """A page of zeros has scale byte 0, and takes the scale of what follows."""
+    case = (64, 64, 16, 1, 1, {}, [(0, 4)])
+    cfg, rope, prior, new, cache, q, k, v, _, _ = append_case(case, 64, "e4m3")
+    cache.table = torch.zeros(1, 2, dtype=torch.int32)
+    z = torch.zeros_like(k)
+    _, after, _ = run_append(cfg, rope, [0], [4], cache, q, z, z, None, None)
+    assert int(after.k_scale[0, 0]) == 0 and int(after.v_scale[0, 0]) == 0
+    _, after, _ = run_append(cfg, rope, [4], [4], after, q, k, v, None, None)
+    e = exponent(v.double().abs().amax())
+    assert int(after.v_scale[0, 0]) == int(e) + 127
+    assert (values(after.v, after.v_scale, torch.zeros(1))[0, :4] == 0).all()
+    got = values(after.v, after.v_scale, torch.zeros(1))[0, 4:8]
+    want = v[:, 0].double()
+    check(got, want, 0.5 * e4m3_step(want / 2.0 ** e) * 2.0 ** e, "values")
+
+
+def test_two_streams_at_once():
+    """Two decodes on two streams, each with its own workspace, at the same time."""
+    cases = []
+    for seed, lens in ((81, [3000, 900, 40]), (82, [5000, 16])):
+        cache = make_paged(lens, 2, 128, 64, "e4m3", seed)
+        q = rnd(torch.Generator().manual_seed(seed), len(lens), 8, 128)
+        cfg = na.AttnConfig(8, 2, 128)
+        ref = attend(cache, q, [(b, n - 1, 1) for b, n in enumerate(lens)])
+        cases.append((cfg, q.to(DEV), cache.to(DEV), ints(lens), max(lens),
+                      torch.empty(len(lens), 8, 128, dtype=torch.bfloat16, device=DEV),
+                      na.workspace(na.na_decode_paged_workspace_size(cfg, len(lens), max(lens)), DEV),
+                      torch.cuda.Stream(), ref))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for cfg, q, cache, lens, top, out, ws, st, _ in cases:
+            na.na_attn_decode_paged(cfg, q, cache, lens, top, out, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for *_, out, _, _, ref in cases:
+        check(out, ref.out, ref.tol, "out")
+
+
+def test_first_calls_inside_a_capture():
+    """A layer's three calls captured without having run before (in a thread of
+    their own), replayed: the chunk, then the decode, match the pages."""
+    import threading
+    KV, G, d, page = 1, 3, 64, 128
+    cfg, rope = na.AttnConfig(KV * G, KV, d), na.RopeConfig()
+    host = make_paged([0, 0], KV, d, page, "e4m3", 91, room=300)
+    g = torch.Generator().manual_seed(92)
+    q, k, v = (rnd(g, 300, n, d).to(DEV) for n in (KV * G, KV, KV))
+    failed = []
+
+    def work():
+        try:
+            cache = host.to(DEV)
+            q_rot, out = torch.empty_like(q), torch.empty_like(q)
+            cu, prior, lens = cu_of([200, 100]), ints([0, 0]), ints([200, 100])
+            dec = torch.empty(2, KV * G, d, dtype=torch.bfloat16, device=DEV)
+            status = torch.zeros(1, dtype=torch.int32, device=DEV)
+            ws = na.workspace(na.na_prefill_paged_workspace_size(cfg, 2, 300, 200, 200), DEV)
+            dws = na.workspace(na.na_decode_paged_workspace_size(cfg, 2, 1000), DEV)
+            ends = torch.tensor([199, 299], device=DEV)
+            torch.cuda.synchronize()
+            s = torch.cuda.Stream()
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=s):
+                na.na_rope_append_kv_paged(cfg, rope, cu, prior, q, k, v, q_rot, cache, status=status)
+                na.na_attn_prefill_chunk_paged(cfg, cu, prior, 200, 200, q_rot, cache, out,
+                                               workspace=ws, status=status)
+                na.na_attn_decode_paged(cfg, q_rot.index_select(0, ends), cache, lens, 300, dec,
+                                        workspace=dws, status=status)
+            gr.replay()
+            torch.cuda.synchronize()
+            assert int(status.item()) == 0
+            c = Paged.back(cache)
+            ref = attend(c, q_rot.cpu(), [(0, 0, 200), (200, 0, 100)])
+            check(out, ref.out, ref.tol, "chunk")
+            check(dec, ref.out[[199, 299]], ref.tol[[199, 299]], "decode")
+        except BaseException as e:  # noqa: BLE001 - reported by the test's thread
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    if failed:
+        raise failed[0]
 
 
 # ------------------------------------------------- reported by the device --
