@@ -683,8 +683,9 @@ template <int D>
 cudaError_t launch_combine_t(const DecodeParams &p, cudaStream_t stream)
 {
     // Two shared-memory buffers that hold a row of max_kv_len keys between
-    // them (up to kCombMaxHalf groups of four keys each).
-    const int groups = (p.max_kv_len + 3) / 4;
+    // them (up to kCombMaxHalf groups of four keys each); without probabilities
+    // the smallest, so that they do not hold down the CTAs per SM.
+    const int groups = p.probs ? (p.max_kv_len + 3) / 4 : 0;
     const int half = std::min(kCombMaxHalf, std::max(32, ((groups + 1) / 2 + 31) / 32 * 32));
     return launch_kernel(decode_combine_kernel<D>, dim3(p.batch * p.H), dim3(kCombThreads),
                          (size_t)2 * half * sizeof(float4), stream, p, half);

@@ -52,6 +52,21 @@
 // it took 1595 us, with K converted the same way too 2217 us, and with the tiles
 // left unconverted it would take 920 us.
 //
+// Two softmax groups (PAIR: E4M3, REP = 1).  Without the softmax a tile of the
+// E4M3 kernel takes 0.78 us, with one warp per 32 rows 1.04: ~1900 cycles of
+// waiting, loading, taking maxima, exponentiating and storing, one after the
+// other, of which the exponentials' unit is busy 512.  Warps 4-7 take columns
+// 0 .. 63 of a tile and warps 8-11 the same rows' columns 64 .. 127.  The two warps
+// of a row swap their maxima through shared memory and one barrier of 64 threads
+// per tile (which also keeps the second's weights off columns that the first has
+// yet to load), so that both hold the same reference; sums stay apart until the
+// end.  A mixed step of 16 prompts takes 463 us so, 490 with one group; a long
+// context 1004 against 1016.  What stays is the exponentials' phase, 1036 cycles
+// for the two warps together, with the tensor cores on the same tensor memory.
+// (Groups that alternate tiles, half a tile apart: 608 and 1292 us, and with
+// accumulators and references of their own 615 and 1336: both load scores again
+// or in smaller pieces to stay within 128 registers.)
+//
 // Few rows (REP = 4).  A tile of a paged call with at most 32 rows -- drafted
 // tokens, single tokens of a mixed batch -- is loaded four times over, so that
 // each softmax warp has all the rows in its 32 lanes and takes a quarter of the
@@ -76,10 +91,16 @@ constexpr int BN = 128;      // keys per tile
 constexpr int STAGES = 3;    // K/V shared-memory ring depth (bf16 caches)
 constexpr int NUM_S = 3;     // S/P buffers in tensor memory
 constexpr int THREADS = 256; // 8 warps: producer, S issuer, PV issuer, idle, 4 softmax
-constexpr int E4M3_THREADS = THREADS + 128;  // and 4 that convert E4M3 tiles
+
+// Threads of a CTA: E4M3 pages have four more warps that convert, and, unless the
+// rows are laid over the lanes, a second softmax group.
+constexpr int cta_threads(bool e4m3, int rep)
+{
+    return THREADS + (e4m3 ? 128 : 0) + (e4m3 && rep == 1 ? 128 : 0);
+}
 constexpr int E4M3_K_STAGES = 4;  // K tiles in bytes
 constexpr int E4M3_V_STAGES = 2;  // bf16 V tiles behind a raw ring ...
-constexpr int RAW_STAGES = 4;     // ... of this many in bytes
+constexpr int RAW_STAGES = 3;     // ... of this many in bytes
 constexpr int SCALE_SLOTS = 8;    // K scales outlive their tile until its softmax (at most 7 tiles)
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL0 = 128;  // S buffer i at columns 128 (i + 1); O at column 0
@@ -114,6 +135,9 @@ struct __align__(1024) TcSmem<D, KV_PAGED_E4M3> {
     float4 mul_off[SCALE_SLOTS][4];
     float2 v_inv[SCALE_SLOTS][4];
     uint8_t v_scale[RAW_STAGES][8];  // V's E8M0 bytes
+    float row_mul[BM];               // what undoes a Q row's scaling
+    float pair_max[2][2][BM];        // the softmax groups' row maxima, by tile parity
+    int pair_failed[4];              // a wait of one of the row quarter's two warps gave up
     uint64_t raw_full[RAW_STAGES], raw_empty[RAW_STAGES];
     uint64_t q_full, q_split;
     uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST];
@@ -356,7 +380,7 @@ __device__ __forceinline__ void rank_sequences(const PrefillParams &p, RankScrat
 
 // REP: the tile's rows fill 128 / REP lanes, REP times over (paged calls).
 template <int D, bool CAPPED, KvSource SRC, int REP = 1>
-__global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS, 1)
+__global__ void __launch_bounds__(cta_threads(SRC == KV_PAGED_E4M3, REP), 1)
     prefill_tc_kernel(const PrefillParams p, const PagedView pg,
                       const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_k,
@@ -366,6 +390,8 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     constexpr int KB = D / 64;
     constexpr int KST = Smem::KST, VST = Smem::VST;
     constexpr bool PAGED = SRC != KV_CONTIGUOUS, E4M3 = SRC == KV_PAGED_E4M3;
+    constexpr bool PAIR = E4M3 && REP == 1;   // two softmax groups
+    constexpr int CONVERT0 = PAIR ? 12 : 8;   // first of the converting warps
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~uintptr_t(1023));
@@ -396,13 +422,16 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         for (int s = 0; s < NUM_S; s++) {
             mbar_init(&sm.s_full[s], 1);
             mbar_init(&sm.s_free[s], 1);
-            mbar_init(&sm.p_full[s], 4);
+            mbar_init(&sm.p_full[s], PAIR ? 8 : 4);
         }
         for (int s = 0; s < NUM_S; s++)
             mbar_init(&sm.o_done[s], 1);
         mbar_init(&sm.drain[0], 1);
         mbar_init(&sm.drain[1], 1);
         sm.abort_flag = 0;
+        if constexpr (PAIR)
+            for (int i = 0; i < 4; i++)
+                sm.pair_failed[i] = 0;
         fence_barrier_init();
     }
     // The block's unit: CTAs 0 .. full_units - 1 take whole units, the rest one
@@ -609,7 +638,8 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
     constexpr int LDS = D + 4;   // staged row stride (floats): conflict-free row writes
     constexpr int EPL = D / 32;  // elements per lane in the row stores
     constexpr int GW = D / 64;   // 32-bit words of gate per lane and row
-    constexpr int SR = BM / REP / 8;  // rows stored per warp
+    constexpr int SW = PAIR ? 16 : 8;  // storing warps
+    constexpr int SR = BM / REP / SW;  // rows stored per warp
     float *stage = reinterpret_cast<float *>(&sm.k[0]);  // the K ring (and what follows), idle by then
     const bool split_out = nsplit > 1;
     // rows of this piece in the workspace: [tail unit][split][row]
@@ -875,7 +905,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 }
             }
         }
-    } else if (E4M3 && warp >= 8) {
+    } else if (E4M3 && warp >= CONVERT0) {
         // -------------------------------------- E4M3 V tiles to f16 tiles --
         if constexpr (E4M3) {
             for (int j = 0; j < n_tiles; j++) {
@@ -891,7 +921,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                     break;
                 }
                 const int j0 = k_begin + j * BN;
-                convert_tile<D>(sm.raw[rs], sm.v_scale[rs], sm.v[st][0], warp - 8, lane,
+                convert_tile<D>(sm.raw[rs], sm.v_scale[rs], sm.v[st][0], warp - CONVERT0, lane,
                                 vis_lo - j0, k_end - j0);
                 tc::fence_proxy_async_smem();  // before the tensor core's reads
                 __syncwarp();
@@ -908,8 +938,9 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         const int rq = r & (BM / REP - 1);  // its query row
         const int row_pos = pos_lo + tok_of(rq);
         // the 32-column blocks of a score tile that this warp takes
-        constexpr int NC = 4 / REP;
-        const int c0 = REP == 1 ? 0 : quarter / (4 / REP) * NC;
+        constexpr int NC = PAIR ? 2 : 4 / REP;
+        const int group = PAIR ? (warp - 4) >> 2 : 0;
+        const int c0 = PAIR ? 2 * group : (REP == 1 ? 0 : quarter / (4 / REP) * NC);
         const int row_lo = p.window > 0 ? row_pos - p.window + 1 : INT_MIN;  // first visible key
         constexpr bool capped = CAPPED;
         // soft-capped scores, kept in the raw score's units so the rest of the
@@ -923,21 +954,36 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
         if constexpr (E4M3) {
-            ok = warp_wait(&sm.q_full, 0, &sm.abort_flag);
-            if (ok) {
-                sl2 *= split_q_row<D>(sm.v[0][0], sm.q8[0], sm.q8[1], r);
-                tc::fence_proxy_async_smem();  // before the tensor core's reads
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sm.q_split);
+            if (group == 0) {
+                ok = warp_wait(&sm.q_full, 0, &sm.abort_flag);
+                if (ok) {
+                    sm.row_mul[r] = split_q_row<D>(sm.v[0][0], sm.q8[0], sm.q8[1], r);
+                    tc::fence_proxy_async_smem();  // before the tensor core's reads
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.q_split);
+                }
+            } else {
+                ok = warp_wait(&sm.q_split, 0, &sm.abort_flag);
             }
+            if (ok)
+                sl2 *= sm.row_mul[r];
         }
-        for (int j = 0; ok && j < n_tiles; j++) {
+        for (int j = 0; (PAIR || ok) && j < n_tiles; j++) {
             const int sb = j % NUM_S;
             const int j0 = k_begin + j * BN;
             const uint32_t s_t = tmem + S_COL0 * (sb + 1) + lane_off;
-            if (!warp_wait(&sm.s_full[sb], (j / NUM_S) & 1, &sm.abort_flag)) {
+            // (PAIR: a failed wait is told at the tile's barrier, and both warps leave)
+            if (!(ok && warp_wait(&sm.s_full[sb], (j / NUM_S) & 1, &sm.abort_flag))) {
                 ok = false;
+                if constexpr (PAIR) {
+                    if (lane == 0) {
+                        *(volatile int *)&sm.pair_failed[quarter] = 1;
+                        set_abort(&sm.abort_flag, p.status);
+                    }
+                    __syncwarp();
+                    named_barrier_sync(2 + quarter, 64);
+                }
                 break;
             }
             tc::fence_after_sync();
@@ -945,28 +991,34 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
 #pragma unroll
             for (int c = 0; c < NC; c++)
                 tc::tmem_ld32(s_t + (c0 + c) * 32, sr[c]);
+            // E4M3: what turns a raw score of 16 keys into the log2 domain (the soft
+            // cap leaves it there), V's exponents in the weights, and 2^-those;
+            // requested with the scores, since shared memory answers late while the
+            // tensor cores read it.
+            float4 mul_off[NC];
+            float2 v_inv[NC];
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int c = 0; c < NC; c++) {
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(mul_off[c].x), "=f"(mul_off[c].y), "=f"(mul_off[c].z),
+                                   "=f"(mul_off[c].w)
+                                 : "r"(smem_addr(&sm.mul_off[j % SCALE_SLOTS][c0 + c])));
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                                 : "=f"(v_inv[c].x), "=f"(v_inv[c].y)
+                                 : "r"(smem_addr(&sm.v_inv[j % SCALE_SLOTS][c0 + c])));
+                    // positive: masked scores are -inf
+                    mul_off[c].x = fmaxf(mul_off[c].x * sl2, 1.2e-38f);
+                    mul_off[c].y = fmaxf(mul_off[c].y * sl2, 1.2e-38f);
+                }
+            }
             tc::tmem_wait_ld();
 
-            // E4M3: what turns a raw score of 16 keys into the log2 domain (the soft
-            // cap leaves it there) and V's exponent; read again where it is used, the
-            // registers hold the scores.
-            auto mul_off = [&](int c) {
-                float4 x;
-                if constexpr (E4M3) {
-                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                                 : "r"(smem_addr(&sm.mul_off[j % SCALE_SLOTS][c0 + c])));
-                    // positive: masked scores are -inf
-                    x.x = fmaxf(x.x * sl2, 1.2e-38f);
-                    x.y = fmaxf(x.y * sl2, 1.2e-38f);
-                }
-                return x;
-            };
             if constexpr (capped && E4M3) {
                 const float in = 2.0f / p.softcap, out = p.softcap * NA_LOG2E;
 #pragma unroll
                 for (int c = 0; c < NC; c++) {
-                    const float4 mo = mul_off(c);
+                    const float4 mo = mul_off[c];
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
                         const float e = ex2_mufu(__uint_as_float(sr[c][i]) * (i < 16 ? mo.x : mo.y) * in);
@@ -1000,7 +1052,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 float mg[2 * NC];
 #pragma unroll
                 for (int c = 0; c < NC; c++) {
-                    const float4 mo = mul_off(c);
+                    const float4 mo = mul_off[c];
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         const uint32_t *x = &sr[c][16 * h];
@@ -1033,6 +1085,15 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             const float mx = max3f(mxa, mxb, fmaxf(mxc, mxd));
             mxs = mx * sl2;
             }
+            if constexpr (PAIR) {  // the other half of the row
+                sm.pair_max[j & 1][group][r] = mxs;
+                named_barrier_sync(2 + quarter, 64);
+                if (*(volatile int *)&sm.pair_failed[quarter]) {
+                    ok = false;
+                    break;
+                }
+                mxs = fmaxf(mxs, sm.pair_max[j & 1][group ^ 1][r]);
+            }
             float alpha = 1.f;
             bool corr = false;
             constexpr float TOP = E4M3 ? kF16Top : 0.f, LIMIT = E4M3 ? kF16Limit : 8.0f;
@@ -1047,12 +1108,8 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
 #pragma unroll
             for (int c = 0; c < NC; c++) {
                 uint32_t pk[16];
-                float4 mo = mul_off(c);
-                float2 inv;
-                if constexpr (E4M3)
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                                 : "=f"(inv.x), "=f"(inv.y)
-                                 : "r"(smem_addr(&sm.v_inv[j % SCALE_SLOTS][c0 + c])));
+                float4 mo = mul_off[c];
+                const float2 inv = v_inv[c];
                 if constexpr (E4M3 && capped)
                     mo.x = mo.y = 1.0f;
 #pragma unroll
@@ -1113,9 +1170,11 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             // S buffer had to be free), and its next one, PV(j-1+NUM_S), needs a
             // P this warp has not written yet.  Waiting for PV(j-1) on every tile
             // kept PV(j) from being queued behind it.
-            if (j >= 1 && __any_sync(0xffffffffu, corr)) {
+            if (j >= 1 && group == 0 && __any_sync(0xffffffffu, corr)) {
                 if (!warp_wait(&sm.o_done[(j - 1) % NUM_S], ((j - 1) / NUM_S) & 1, &sm.abort_flag)) {
                     ok = false;
+                    if constexpr (PAIR)
+                        continue;  // to the next tile's barrier
                     break;
                 }
                 // rescale this warp's O rows (PV(j-1) has landed)
@@ -1150,6 +1209,11 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             ml[r] = make_float2(m_ref, l);
             named_barrier_sync(1, BM);
         }
+        if constexpr (PAIR) {  // the row's two sums (one reference)
+            sm.pair_max[0][group][r] = l;
+            named_barrier_sync(1, 2 * BM);
+            l += sm.pair_max[0][group ^ 1][r];
+        }
         if (done) {
             // ---------------------------------------------------- epilogue --
             // Each thread writes its O row (normalised unless this is a split
@@ -1176,14 +1240,16 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                 l = L;
             }
             {
-                uint32_t o[D / 32][32];  // the whole row in one round of loads
+                constexpr int OC = PAIR ? D / 64 : D / 32;  // column blocks of O (PAIR: half each)
+                const int oc0 = group * OC;
+                uint32_t o[OC][32];  // in one round of loads
 #pragma unroll
-                for (int c = 0; c < D / 32; c++)
-                    tc::tmem_ld32(o_t + c * 32, o[c]);
+                for (int c = 0; c < OC; c++)
+                    tc::tmem_ld32(o_t + (oc0 + c) * 32, o[c]);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < D / 32; c++) {
-                    float4 *row4 = reinterpret_cast<float4 *>(stage + r * LDS + c * 32);
+                for (int c = 0; c < OC; c++) {
+                    float4 *row4 = reinterpret_cast<float4 *>(stage + r * LDS + (oc0 + c) * 32);
 #pragma unroll
                     for (int q = 0; q < 8; q++)
                         row4[q] = make_float4(__uint_as_float(o[c][4 * q]) * scale,
@@ -1192,7 +1258,7 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
                                               __uint_as_float(o[c][4 * q + 3]) * scale);
                 }
             }
-            if (split_out && r < rows) {
+            if (split_out && group == 0 && r < rows) {
                 p.part_ml[(piece_row0 + r) * 2] = m_ref;
                 p.part_ml[(piece_row0 + r) * 2 + 1] = l;
             }
@@ -1200,12 +1266,12 @@ __global__ void __launch_bounds__(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS,
             set_abort(&sm.abort_flag, p.status);
         }
     }
-    if (E4M3 && warp < 8 && gated_out)
+    if (E4M3 && warp < SW && gated_out)
         load_gate();
 
     tc::fence_before_sync();
     __syncthreads();  // the staged rows are complete (unless a wait gave up)
-    if (!aborted(&sm.abort_flag) && warp < 8) {
+    if (!aborted(&sm.abort_flag) && warp < SW) {
         // Lanes across a row, one row per step, this warp's SR rows.
 #pragma unroll
         for (int i = 0; i < SR; i++) {
@@ -1506,7 +1572,7 @@ cudaError_t launch_prefill_t(const PrefillParams &p, const PagedView &pg, int to
     if (e != cudaSuccess)
         return e;
     const dim3 grid(p.full_units + p.tail_units * p.num_splits);
-    const dim3 block(SRC == KV_PAGED_E4M3 ? E4M3_THREADS : THREADS);
+    const dim3 block(cta_threads(SRC == KV_PAGED_E4M3, REP));
     e = p.softcap > 0.f ? launch_kernel(prefill_tc_kernel<D, true, SRC, REP>, grid, block, smem, stream,
                                         p, pg, mq, mk, mv)
                         : launch_kernel(prefill_tc_kernel<D, false, SRC, REP>, grid, block, smem, stream,
