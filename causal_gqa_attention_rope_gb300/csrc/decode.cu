@@ -483,7 +483,11 @@ __device__ __forceinline__ float prob_of(float raw, int j, int kf, float M, floa
 constexpr int kCombThreads = 128;
 constexpr int kCombMaxHalf = 1024;  // 16-byte groups per buffer (4096 keys)
 
-template <int D>
+//
+// U: pieces loaded at a time after the first four.  A stream of many pieces (few
+// long sequences: 28 pieces each for four of 50001 .. 131072 keys) takes one round
+// of loads instead of three with 32; the additions are the same.
+template <int D, int U>
 __global__ void __launch_bounds__(kCombThreads) decode_combine_kernel(const DecodeParams p,
                                                                       const int half)
 {
@@ -592,16 +596,16 @@ __global__ void __launch_bounds__(kCombThreads) decode_combine_kernel(const Deco
         for (int u = 0; u < PO; u++)
             if (mo[u] != -INFINITY)
                 o += xo[u] * exp2f(mo[u] - M);
-        for (int s0 = PO; s0 < ns; s0 += 8) {  // eight pieces' loads in flight, added in order
-            float m[8], x[8];
+        for (int s0 = PO; s0 < ns; s0 += U) {  // U pieces' loads in flight, added in order
+            float m[U], x[U];
 #pragma unroll
-            for (int u = 0; u < 8; u++) {
+            for (int u = 0; u < U; u++) {
                 const int s = min(s0 + u, ns - 1);
                 m[u] = ml[2 * hpc * s];
                 x[u] = po[(size_t)s * hpc * D + e0];
             }
 #pragma unroll
-            for (int u = 0; u < 8; u++)
+            for (int u = 0; u < U; u++)
                 if (s0 + u < ns && m[u] != -INFINITY)
                     o += x[u] * exp2f(m[u] - M);
         }
@@ -687,8 +691,12 @@ cudaError_t launch_combine_t(const DecodeParams &p, cudaStream_t stream)
     // the smallest, so that they do not hold down the CTAs per SM.
     const int groups = p.probs ? (p.max_kv_len + 3) / 4 : 0;
     const int half = std::min(kCombMaxHalf, std::max(32, ((groups + 1) / 2 + 31) / 32 * 32));
-    return launch_kernel(decode_combine_kernel<D>, dim3(p.batch * p.H), dim3(kCombThreads),
-                         (size_t)2 * half * sizeof(float4), stream, p, half);
+    const int streams = p.batch * p.KV * p.head_chunks;
+    return p.grid > 8 * streams
+               ? launch_kernel(decode_combine_kernel<D, 32>, dim3(p.batch * p.H), dim3(kCombThreads),
+                               (size_t)2 * half * sizeof(float4), stream, p, half)
+               : launch_kernel(decode_combine_kernel<D, 8>, dim3(p.batch * p.H), dim3(kCombThreads),
+                               (size_t)2 * half * sizeof(float4), stream, p, half);
 }
 
 template <int D, int HPC>
