@@ -82,13 +82,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     uint32_t r;
@@ -125,8 +118,8 @@ __device__ __forceinline__ uint32_t v_rest_f16x2(uint32_t byte)
 __device__ __forceinline__ float exp2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
 
 // f16 weights: the largest of a row is raised to 2^kF16Top when it would exceed
-// 2^(kF16Top + kRaise), below f16's largest, so that weights down to 2^-21 of it
-// are normal numbers.
+// 2^kF16Limit, half of f16's largest, so that weights down to 2^-21 of it are
+// normal numbers.
 constexpr float kF16Top = 7.0f, kF16Limit = 15.0f;
 
 // ------------------------------------------------------ shared-memory sync --

@@ -45,12 +45,13 @@
 // sum is exact for elements down to 2^-10 of the row's largest and within 2^-17
 // of that below.)  The row's and K's powers of two multiply the scores in the
 // softmax, 16 keys at a time sharing a page.  V's boxes land as bytes in a raw
-// ring, and four more warps (8-11) turn them into the swizzled f16 tile, two
+// ring, and four more warps (the last ones) turn them into the swizzled f16 tile, two
 // conversions a word; V's scale enters the weights (na_internal.cuh), which are
-// f16 here.  A 2048-token chunk over 28672 keys, 40/8 heads, takes 1010 us (0.65
-// of the bf16 peak); with V converted to bf16, ten integer instructions a word,
-// it took 1595 us, with K converted the same way too 2217 us, and with the tiles
-// left unconverted it would take 920 us.
+// f16 here.  A 2048-token chunk over 28672 keys, 40/8 heads, takes 1004 us (0.66
+// of the bf16 peak).  With one softmax group and V converted to bf16, ten integer
+// instructions a word, it took 1595 us, with K converted the same way too 2217 us;
+// with the tiles left unconverted it would take 920 us, and without the softmax
+// 762 us.
 //
 // Two softmax groups (PAIR: E4M3, REP = 1).  Without the softmax a tile of the
 // E4M3 kernel takes 0.78 us, with one warp per 32 rows 1.04: ~1900 cycles of
@@ -74,8 +75,7 @@
 // others, and the four partial rows of a query are merged at the end like split
 // pieces.  With one warp working on every key and three on padding the softmax
 // held the tile loop up (64 sequences of 512 .. 8192 keys, 2 .. 8 tokens: 156 us
-// against REP_TIME us).
-//
+// against 126 us).
 #include <climits>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -332,7 +332,7 @@ __device__ __forceinline__ float split_q_row(const bf16 *staged, uint8_t *hi, ui
 // Up to kRankBatch sequences of a paged call go to the slots in order of
 // decreasing end position, as up to 32 do by shuffles: one thread per sequence
 // counts those ahead of it.  (64 sequences of 512 .. 8192 keys, 512 units on 152
-// SMs: 197 us in table order, RANK_TIME us so.)  Called by all threads of a CTA
+// SMs: 197 us in table order, 156 us so.)  Called by all threads of a CTA
 // of at least 256; every thread gets the sequence of `slot`.
 constexpr int kRankBatch = 256;
 
