@@ -213,8 +213,9 @@ class PagedKVCache:
         num_pages, _, page_size, _ = self.k.shape
         batch, pages_per_seq = self.page_table.shape
         return na_paged_kv_cache(
-            *_ptrs(self.k, self.v, self.k_scale, self.v_scale, self.page_table), num_pages,
-            page_size, batch, pages_per_seq, NA_KV_BF16 if self.k_scale is None else NA_KV_E4M3)
+            _ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale),
+            _ptr(self.page_table), num_pages, page_size, batch, pages_per_seq,
+            NA_KV_BF16 if self.k_scale is None else NA_KV_E4M3)
 
 
 # ---------------------------------------------------------------- helpers --
@@ -227,14 +228,6 @@ def _ptr(t) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError("libna needs contiguous tensors")
     return t.data_ptr()
-
-
-def _ptrs(*tensors) -> list:
-    """_ptr of each."""
-    out = []
-    for t in tensors:
-        out.append(t.data_ptr() if t is not None and t.is_cuda and t.is_contiguous() else _ptr(t))
-    return out
 
 
 _current_stream = None
@@ -263,14 +256,14 @@ def _stream(stream) -> Optional[int]:
     return _current_stream()
 
 
-def _stream_for(t, stream) -> Optional[int]:
-    """The same for a call whose tensors have to be on the current device, as t is."""
+def _on_current(*tensors):
+    """Refuse tensors of another device than the current one."""
     if _current_device is None:
         _find_current()
-    if t.get_device() != _current_device():
-        raise ValueError(f"tensors on cuda:{t.get_device()}, but the current device is "
-                         f"cuda:{_current_device()}")
-    return _current_stream() if stream is None else stream.cuda_stream
+    for t in tensors:
+        if t is not None and t.get_device() != _current_device():
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, but the current device is "
+                             f"cuda:{_current_device()}")
 
 
 _dtypes = {}  # torch's dtype objects by name
@@ -311,8 +304,8 @@ def _want_cache(cache: "KVCache", cfg: "AttnConfig", batch: int):
     _want(cache.v, "cache.v", "bfloat16", tuple(cache.k.shape))
 
 
-def _want_paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int):
-    """A paged cache's tensors, one by one."""
+def _paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int) -> na_paged_kv_cache:
+    """The C struct of a paged cache, its tensors checked."""
     bf16 = cache.k_scale is None and cache.v_scale is None
     kind = "bfloat16" if bf16 else "float8_e4m3fn"
     _want(cache.k, "cache.k", kind, (None, cfg.num_kv_heads, None, cfg.head_dim))
@@ -324,31 +317,29 @@ def _want_paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int):
             if t is None:
                 raise ValueError(f"{name}: missing")
             _want(t, name, "uint8", scales)
+    return cache.c()
 
 
-def _paged(cache: "PagedKVCache", cfg: "AttnConfig", batch: int) -> na_paged_kv_cache:
-    """The C struct of a paged cache, its tensors checked (all at once: a decode
-    step's host time is mostly such checks)."""
-    k, v, table, k_scale, v_scale = cache.k, cache.v, cache.page_table, cache.k_scale, cache.v_scale
-    bf16 = k_scale is None and v_scale is None
-    try:
-        shape, dtype = k.shape, k.dtype
-        num_pages, kv_heads, page_size, d = shape
-        rows, pages_per_seq = table.shape
-        ok = (kv_heads == cfg.num_kv_heads and d == cfg.head_dim and rows >= batch
-              and v.shape == shape and v.dtype is dtype and table.dtype is _dtypes["int32"]
-              and dtype is _dtypes["bfloat16" if bf16 else "float8_e4m3fn"])
-        if ok and not bf16:
-            u8, scales = _dtypes["uint8"], (num_pages, kv_heads)
-            ok = (k_scale.dtype is u8 and v_scale.dtype is u8 and k_scale.shape == scales
-                  and v_scale.shape == scales)
-    except (AttributeError, KeyError, ValueError):  # no tensor, a type not met yet, another rank
-        ok = False
-    if not ok:
-        _want_paged(cache, cfg, batch)
-        return cache.c()
-    return na_paged_kv_cache(*_ptrs(k, v, k_scale, v_scale, table), num_pages, page_size, rows,
-                             pages_per_seq, NA_KV_BF16 if bf16 else NA_KV_E4M3)
+_native = None
+
+
+def _calls():
+    """The compiled paged calls (csrc/paged_calls.cpp): they answer a call's status, or None,
+    without having called, for what is not plainly right; the checks here then say what."""
+    global _native
+    if _native is None:
+        lib = load_library()
+        import torch  # noqa: F401  (its libraries have to be there first)
+        try:
+            from . import _paged_calls as calls
+        except ImportError as e:
+            raise RuntimeError("the paged calls are not built; run __graft_entry__.build() or "
+                               "python -m causal_gqa_attention_rope_gb300._build") from e
+        calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                     for f in (lib.na_rope_append_kv_paged, lib.na_attn_prefill_chunk_paged,
+                               lib.na_attn_decode_paged)), AttnConfig, RopeConfig, PagedKVCache)
+        _native = calls
+    return _native
 
 
 def _check(fn: str, rc: int):
@@ -400,15 +391,22 @@ def na_rope_append_kv_paged(cfg: AttnConfig, rope: RopeConfig, cu_seqlens, cache
                             q_out, cache: PagedKVCache, q_norm_w=None, k_norm_w=None, status=None,
                             total_tokens: Optional[int] = None, stream=None):
     """na_rope_append_kv into bf16 or E4M3 pages."""
-    lib = load_library()
-    batch, T = _append_args(cfg, cu_seqlens, cache_lens, q, k, v, q_out, q_norm_w, k_norm_w,
-                            status, total_tokens)
-    kc = _paged(cache, cfg, batch)
-    c, r = cfg.c(), rope.c()
-    cu, lens, *rows, st = _ptrs(cu_seqlens, cache_lens, q, k, v, q_norm_w, k_norm_w, q_out, status)
-    rc = lib.na_rope_append_kv_paged(ctypes.byref(c), ctypes.byref(r), batch, cu, lens, T, *rows,
-                                     ctypes.byref(kc), st, _stream_for(q, stream))
-    _check("na_rope_append_kv_paged", rc)
+    rc = (_native or _calls()).append(cfg, rope, cu_seqlens, cache_lens, q, k, v, q_out,
+                                           cache, q_norm_w, k_norm_w, status, total_tokens, stream)
+    if rc is None:
+        batch, T = _append_args(cfg, cu_seqlens, cache_lens, q, k, v, q_out, q_norm_w, k_norm_w,
+                                status, total_tokens)
+        kc = _paged(cache, cfg, batch)
+        c, r = cfg.c(), rope.c()
+        args = [_ptr(t) for t in (q, k, v, q_norm_w, k_norm_w, q_out)]
+        cu, lens, st = _ptr(cu_seqlens), _ptr(cache_lens), _ptr(status)
+        _on_current(cu_seqlens, cache_lens, q, k, v, q_norm_w, k_norm_w, q_out, status, cache.k,
+                    cache.v, cache.k_scale, cache.v_scale, cache.page_table)
+        rc = load_library().na_rope_append_kv_paged(
+            ctypes.byref(c), ctypes.byref(r), batch, cu, lens, T, *args, ctypes.byref(kc), st,
+            _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_rope_append_kv_paged", rc)
 
 
 def na_prefill_workspace_size(cfg: AttnConfig, batch: int, total_tokens: int, max_new_len: int,
@@ -493,17 +491,24 @@ def na_attn_prefill_chunk_paged(cfg: AttnConfig, cu_seqlens, cache_lens, max_new
                                 stream=None):
     """na_attn_prefill_chunk against bf16 or E4M3 pages (workspace:
     na_prefill_paged_workspace_size)."""
-    lib = load_library()
-    batch, T = _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status, total_tokens)
-    kc = _paged(cache, cfg, batch)
-    c = cfg.c()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    cu, lens, pq, pgate, po, ws, st = _ptrs(cu_seqlens, cache_lens, q_rot, gate, out, workspace,
-                                            status)
-    rc = lib.na_attn_prefill_chunk_paged(ctypes.byref(c), batch, cu, lens, T, int(max_new_len),
-                                         int(max_total_len), pq, ctypes.byref(kc), pgate, po, ws,
-                                         ws_bytes, st, _stream_for(q_rot, stream))
-    _check("na_attn_prefill_chunk_paged", rc)
+    rc = (_native or _calls()).prefill(cfg, cu_seqlens, cache_lens, max_new_len,
+                                            max_total_len, q_rot, cache, out, gate, workspace,
+                                            status, total_tokens, stream)
+    if rc is None:
+        batch, T = _prefill_args(cfg, cu_seqlens, cache_lens, q_rot, out, gate, status,
+                                 total_tokens)
+        kc = _paged(cache, cfg, batch)
+        c = cfg.c()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        cu, lens, pq, pgate, po, ws, st = [
+            _ptr(t) for t in (cu_seqlens, cache_lens, q_rot, gate, out, workspace, status)]
+        _on_current(cu_seqlens, cache_lens, q_rot, gate, out, workspace, status, cache.k, cache.v,
+                    cache.k_scale, cache.v_scale, cache.page_table)
+        rc = load_library().na_attn_prefill_chunk_paged(
+            ctypes.byref(c), batch, cu, lens, T, int(max_new_len), int(max_total_len), pq,
+            ctypes.byref(kc), pgate, po, ws, ws_bytes, st, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_attn_prefill_chunk_paged", rc)
 
 
 def _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status):
@@ -541,17 +546,23 @@ def na_attn_decode_paged(cfg: AttnConfig, q_rot, cache: PagedKVCache, kv_lens, m
                          out, probs=None, gate=None, workspace=None, num_splits: int = 0,
                          status=None, stream=None):
     """na_attn_decode over bf16 or E4M3 pages (workspace: na_decode_paged_workspace_size)."""
-    lib = load_library()
-    batch = _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status)
-    kc = _paged(cache, cfg, batch)
-    c = cfg.c()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    stride = int(probs.shape[-1]) if probs is not None else 0
-    pq, lens, pgate, po, pp, ws, st = _ptrs(q_rot, kv_lens, gate, out, probs, workspace, status)
-    rc = lib.na_attn_decode_paged(ctypes.byref(c), batch, pq, ctypes.byref(kc), lens,
-                                  int(max_kv_len), pgate, po, pp, stride, int(num_splits), ws,
-                                  ws_bytes, st, _stream_for(q_rot, stream))
-    _check("na_attn_decode_paged", rc)
+    rc = (_native or _calls()).decode(cfg, q_rot, cache, kv_lens, max_kv_len, out, probs,
+                                           gate, workspace, num_splits, status, stream)
+    if rc is None:
+        batch = _want_decode(cfg, q_rot, kv_lens, out, probs, gate, status)
+        kc = _paged(cache, cfg, batch)
+        c = cfg.c()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        stride = int(probs.shape[-1]) if probs is not None else 0
+        pq, lens, pgate, po, pp, ws, st = [
+            _ptr(t) for t in (q_rot, kv_lens, gate, out, probs, workspace, status)]
+        _on_current(q_rot, kv_lens, gate, out, probs, workspace, status, cache.k, cache.v,
+                    cache.k_scale, cache.v_scale, cache.page_table)
+        rc = load_library().na_attn_decode_paged(
+            ctypes.byref(c), batch, pq, ctypes.byref(kc), lens, int(max_kv_len), pgate, po, pp,
+            stride, int(num_splits), ws, ws_bytes, st, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_attn_decode_paged", rc)
 
 
 def na_attn_decode_static_ws(cfg: AttnConfig, q_rot, cache: KVCache, kv_lens, max_kv_len: int,

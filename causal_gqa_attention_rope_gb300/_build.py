@@ -1,16 +1,20 @@
 """Build the CUDA library ``libna.so`` in-tree with nvcc for sm_103a.
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked into
-one shared library with a C ABI (``include/na.h``).  The output sits beside
-this file so the Python binding finds it without installation.
+one shared library with a C ABI (``include/na.h``).  ``csrc/paged_calls.cpp``,
+compiled meanwhile with the host compiler against torch's headers, becomes the
+extension module ``_paged_calls``.  Both outputs sit beside this file so the
+Python binding finds them without installation.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libna.so")
+CALLS = os.path.join(PKG, "_paged_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -36,6 +41,23 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_calls(cuda: str) -> str:
+    """Compile (if stale) and return the path of the extension module _paged_calls."""
+    src = os.path.join(CSRC, "paged_calls.cpp")
+    if _stale(CALLS, [src, __file__, os.path.join(INCLUDE, "na.h")]):
+        torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+        tmp = CALLS + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o",
+               tmp, "-I", INCLUDE, "-I", os.path.join(torch, "include"), "-I",
+               os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], "-L",
+               os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"compiling {src} failed:\n{res.stderr}")
+        os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(verbose: bool = False, extra_flags=None) -> str:
@@ -59,8 +81,10 @@ def build(verbose: bool = False, extra_flags=None) -> str:
                 print(res.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(sources))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
+        calls = ex.submit(build_calls, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
         objs = list(ex.map(compile_one, sources))
+        calls.result()
     if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs

@@ -146,3 +146,19 @@ def test_binding_checks_shapes_and_types(lib):
             decode_with(replaced(**kw))
     with pytest.raises(ValueError, match="CUDA"):  # right shapes, but on the host
         decode_with(good)
+
+
+def test_compiled_calls_answer_none_for_what_is_not_plain(lib):
+    """Nothing but the plain call is made: no tensors, host tensors, another number of arguments."""
+    calls = na._calls()
+    host = make_paged([5, 9], 2, 64, 16, "e4m3", 1)
+    cache = na.PagedKVCache(host.k, host.v, host.table, host.k_scale, host.v_scale)
+    conf, t = na.AttnConfig(4, 2, 64), torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    for f, n, at, plain in ((calls.append, 14, 4, (conf, na.RopeConfig())), (calls.prefill, 13, 5, (conf,)),
+                            (calls.decode, 12, 1, (conf,))):
+        for filler in (None, 0, "x", t, cache, object()):
+            args = list(plain) + [filler] * (n - len(plain))
+            assert f(*args) is None
+            args[at] = t
+            assert f(*args) is None
+            assert f(*args[:-1]) is None
