@@ -27,6 +27,8 @@
 // 2^-26 of the largest, within 2^-33 of it below); K's scale multiplies the
 // scores in fp32 and V's enters the weights (na_internal.cuh), which have f16's
 // 11 significand bits.
+#include <type_traits>
+
 #include "decode_shared.cuh"
 #include "na_internal.cuh"
 #include "tc_primitives.cuh"
@@ -39,6 +41,7 @@ constexpr int TILE = 64;   // keys per tile: CWARPS warps x 16 keys
 constexpr int CWARPS = 4;  // consumer warps
 constexpr int THREADS = (CWARPS + 1) * 32;
 constexpr int MAX_HPC = 8;
+constexpr int MAX_CLUSTER = 8;  // CTAs of a cluster, at most (the portable size)
 
 // Tiles in flight and CTAs per SM.  An E4M3 tile is half as large, and what its
 // pass lacks first is warps (64 sequences of 512 .. 8192 keys, 32/8 heads: two
@@ -62,7 +65,7 @@ struct __align__(1024) PagedSmem {
     uint64_t empty[ST];
     float2 fin[MAX_HPC];  // a finished stream's reference and 1 / sum, per head
     Slice slice;
-    int abort_flag;
+    int abort_flag, cluster_bad;
 };
 
 // Byte offset, within a tile of K or V, of 16-byte chunk c of row r, as the
@@ -146,14 +149,38 @@ __device__ __forceinline__ Window open_window(const DecodeParams &p, const Paged
     return w;
 }
 
-// A stream that one CTA has read whole, by its NT consumer threads: warp 0 holds
-// the merged rows and writes them (gated), then the raw scores become
+// This thread's lane of a partial in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 cluster_load(const float4 *p, int rank)
+{
+    uint32_t a;
+    float4 x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(a)
+                 : "memory");
+    return x;
+}
+
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A stream that a cluster of C CTAs (one, or up to MAX_CLUSTER) has read whole, by
+// the NT consumer threads of each: warp 0 holds the merged rows' d-blocks s = rank
+// mod C and writes them (gated); then the raw scores of this CTA's keys become
 // probabilities.  `bad`: a wait gave up; the rows are zero.
 template <int D, bool E4M3, int NT>
 __device__ __forceinline__ void finish_stream(const DecodeParams &p, const Piece &pc, float2 *fin,
                                               int head0, int hpc, const float (&acc)[D / 16][4],
                                               const float (&m_ref)[2], const float (&l_sum)[2],
-                                              bool bad)
+                                              bool bad, int rank, int C)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const size_t row0 = (size_t)pc.b * p.H + head0;
@@ -174,6 +201,8 @@ __device__ __forceinline__ void finish_stream(const DecodeParams &p, const Piece
             };
 #pragma unroll
             for (int s = 0; s < D / 16; s++) {
+                if ((s & (C - 1)) != rank)
+                    continue;
                 if constexpr (E4M3) {
                     const int e = 16 * s + 2 * g;
                     *reinterpret_cast<uint32_t *>(out + e) =
@@ -191,19 +220,23 @@ __device__ __forceinline__ void finish_stream(const DecodeParams &p, const Piece
     named_barrier_sync(1, NT);
     if (bad)
         return;
-    const int n = pc.kf + pc.k1;  // keys before the window (none without one) get 0
+    // keys before the window (none without one) get 0, from the first CTA
+    const int j0 = rank == 0 ? 0 : pc.kf + pc.k0, n = pc.kf + pc.k1;
     for (int h = 0; h < hpc; h++) {
         float *row = p.probs + (row0 + h) * p.probs_stride;
         const float2 f = fin[h];
-        for (int j = threadIdx.x; j < n; j += NT)
+        for (int j = j0 + threadIdx.x; j < n; j += NT)
             row[j] = j < pc.kf ? 0.f : ex2_mufu(row[j] - f.x) * f.y;
     }
 }
 
-// DIRECT: one CTA per stream instead of a slice of the concatenation, for calls
-// of short sequences: no partial results and no merge pass (one sequence of 333
-// keys, 4/2 heads: 9.8 us with the merge pass, 6.9 us so).
-template <int D, bool E4M3, bool CAPPED, bool DIRECT>
+// Short streams are not cut over the whole grid: SPLIT is the slice of the
+// concatenation and a merge pass behind it, DIRECT one CTA per stream, CLUSTER
+// p.direct CTAs per stream, neighbouring tiles each, whose partials meet through
+// shared memory: no partial results in the workspace and no merge pass.
+enum Mode { SPLIT, DIRECT, CLUSTER };
+
+template <int D, bool E4M3, bool CAPPED, Mode MODE>
 __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     decode_paged_kernel(const DecodeParams p, const PagedView pg,
                         const __grid_constant__ CUtensorMap map_k,
@@ -233,11 +266,21 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    if constexpr (DIRECT) {  // this CTA's stream, all of it
+    const int C = MODE == CLUSTER ? p.direct : 1;  // CTAs of a stream, and this one's number
+    const int rank = blockIdx.x & (C - 1);
+    if constexpr (MODE != SPLIT) {  // this CTA's stream, all of it or its share of the tiles
         if (threadIdx.x == 0) {
-            const int spb = p.KV * p.head_chunks, b = blockIdx.x / spb;
-            const int len = valid_len(p, b);
-            sm.slice = Slice{0, len, 0, b, (int)blockIdx.x - b * spb, len == 0};
+            const int spb = p.KV * p.head_chunks, st = blockIdx.x / C, b = st / spb;
+            int kf;
+            const int len = attended_keys(p, b, kf);
+            long long start = 0, end = len;
+            if constexpr (MODE == CLUSTER) {
+                const int t0 = kf / TILE, share = (kf + len - t0 * TILE + TILE * C - 1) / (TILE * C);
+                const int lo = (t0 + rank * share) * TILE - kf;
+                start = max(0, lo);
+                end = min(len, lo + share * TILE);
+            }
+            sm.slice = Slice{start, end, 0, b, st - b * spb, start >= end};
         }
     } else if (warp == CWARPS) {
         locate_slice(p, lane, sm.slice);
@@ -334,12 +377,17 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     // 2(l%4) and 2(l%4) + 1, and their probabilities, transposed in registers,
     // are the B operand of O^T += V^T P^T.
     const int hpc = p.group / p.head_chunks;
-    if constexpr (DIRECT) {  // a stream without keys: zero rows, as the merge pass gives
+    if constexpr (MODE != SPLIT) {  // a stream without keys: zero rows, as the merge pass gives
         if (walk.done) {
             const Slice sl = sm.slice;
             const int n = __ldg(p.kv_lens + sl.b);
             if (threadIdx.x == 0 && (n < 0 || n > p.capacity || n > p.max_kv_len))
                 na_report(p.status, NA_ERR_CAPACITY);
+        }
+    }
+    if constexpr (MODE == DIRECT) {
+        if (walk.done) {
+            const Slice sl = sm.slice;
             const int kvh = sl.si / p.head_chunks, hc = sl.si - kvh * p.head_chunks;
             uint32_t *out = reinterpret_cast<uint32_t *>(
                 p.out + ((size_t)sl.b * p.H + kvh * p.group + hc * hpc) * D);
@@ -363,8 +411,26 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     // A warp whose wait timed out keeps walking the pieces so that every warp
     // joins the same named barriers, but does no more waits or writes.
     bool aborted = false;
+    // A cluster's CTAs all take part in the merge, those without keys too.
+    bool once = true;
+    auto next_piece = [&]() {
+        const bool more = walk.next(p, pc);
+        if constexpr (MODE == CLUSTER) {
+            if (!more && once) {
+                const Slice sl = sm.slice;
+                pc.b = sl.b;
+                pc.kvh = sl.si / p.head_chunks;
+                pc.hc = sl.si - pc.kvh * p.head_chunks;
+                pc.k0 = pc.k1 = pc.kf = 0;
+            }
+            const bool go = once;
+            once = false;
+            return go;
+        }
+        return more;
+    };
 
-    while (walk.next(p, pc)) {
+    while (next_piece()) {
         const int lo = pc.kf + pc.k0, hi = pc.kf + pc.k1;
         if (*(volatile int *)&sm.abort_flag)
             aborted = true;
@@ -644,9 +710,74 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
         // buffers have passed; warp 2 after the next piece's first one.)
         if (warp == 0)
             take(sm.merge[2]);
-        if constexpr (DIRECT) {  // the whole stream: its rows and probabilities
+        if constexpr (MODE == CLUSTER) {
+            // The CTAs' partials: warp 0 of each offers its own (merge[0], which it has
+            // read), takes every CTA's maximum and sum, and the d-blocks that it writes,
+            // in the order of the ranks.  All consumer threads meet in both barriers
+            // whatever happened before; the second lets no CTA go whose partial is
+            // still being read.
+            bool bad = *(volatile int *)&sm.abort_flag != 0;
+            if (warp == 0) {
+                give(sm.merge[0]);
+                if (bad)
+                    sm.merge[0][KS][lane] = make_float4(-INFINITY, -INFINITY, -1.f, -1.f);
+            }
+            cluster_arrive();
+            cluster_wait();
+            if (warp == 0) {
+                float4 ml[MAX_CLUSTER];
+#pragma unroll
+                for (int c = 0; c < MAX_CLUSTER; c++)
+                    ml[c] = c < C ? cluster_load(&sm.merge[0][KS][lane], c)
+                                  : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+                m_ref[0] = m_ref[1] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < MAX_CLUSTER; c++) {
+                    bad = bad || ml[c].z < 0.f;
+                    m_ref[0] = fmaxf(m_ref[0], ml[c].x);
+                    m_ref[1] = fmaxf(m_ref[1], ml[c].y);
+                }
+                l_sum[0] = l_sum[1] = 0.f;
+#pragma unroll
+                for (int c = 0; c < MAX_CLUSTER; c++) {  // the factors replace the maxima
+                    ml[c].x = ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - m_ref[0]);
+                    ml[c].y = ml[c].y == -INFINITY ? 0.f : exp2f(ml[c].y - m_ref[1]);
+                    l_sum[0] += ml[c].z * ml[c].x;
+                    l_sum[1] += ml[c].w * ml[c].y;
+                }
+#pragma unroll
+                for (int s = 0; s < KS; s++) {
+                    if ((s & (C - 1)) != rank)
+                        continue;
+                    float4 x[MAX_CLUSTER];
+#pragma unroll
+                    for (int c = 0; c < MAX_CLUSTER; c++)
+                        x[c] = c < C ? cluster_load(&sm.merge[0][s][lane], c)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    acc[s][0] = acc[s][1] = acc[s][2] = acc[s][3] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < MAX_CLUSTER; c++) {
+                        acc[s][0] += x[c].x * ml[c].x;
+                        acc[s][1] += x[c].y * ml[c].y;
+                        acc[s][2] += x[c].z * ml[c].x;
+                        acc[s][3] += x[c].w * ml[c].y;
+                    }
+                }
+                if (lane == 0)
+                    sm.cluster_bad = bad;
+            }
+            __syncwarp();
+            cluster_arrive();
+            named_barrier_sync(1, THREADS - 32);  // cluster_bad
             finish_stream<D, E4M3, THREADS - 32>(p, pc, sm.fin, head0, hpc, acc, m_ref, l_sum,
-                                                 *(volatile int *)&sm.abort_flag != 0);
+                                                 sm.cluster_bad != 0, rank, C);
+            __syncwarp();
+            cluster_wait();
+            continue;
+        }
+        if constexpr (MODE == DIRECT) {  // the whole stream: its rows and probabilities
+            finish_stream<D, E4M3, THREADS - 32>(p, pc, sm.fin, head0, hpc, acc, m_ref, l_sum,
+                                                 *(volatile int *)&sm.abort_flag != 0, 0, 1);
             continue;
         }
         if (warp != 0)
@@ -690,7 +821,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
     }
 }
 
-template <int D, bool E4M3, bool CAPPED, bool DIRECT>
+template <int D, bool E4M3, bool CAPPED, Mode MODE>
 cudaError_t launch_paged_split(const DecodeParams &p, const PagedView &pg, cudaStream_t stream)
 {
     typedef PagedSmem<D, E4M3> Smem;
@@ -711,35 +842,61 @@ cudaError_t launch_paged_split(const DecodeParams &p, const PagedView &pg, cudaS
     const size_t smem = sizeof(Smem) + 1024;  // + alignment slack
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = once_per_device(configured, [smem] {
-        cudaError_t r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED, DIRECT>,
+        cudaError_t r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED, MODE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED, DIRECT>,
+            r = cudaFuncSetAttribute(decode_paged_kernel<D, E4M3, CAPPED, MODE>,
                                      cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         return r;
     });
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(decode_paged_kernel<D, E4M3, CAPPED, DIRECT>, dim3(p.grid), dim3(THREADS), smem,
-                         stream, p, pg, mk, mv);
+    return launch_kernel_cluster(decode_paged_kernel<D, E4M3, CAPPED, MODE>, dim3(p.grid),
+                                 dim3(THREADS), smem, MODE == CLUSTER ? p.direct : 0, stream, p, pg,
+                                 mk, mv);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_paged_t(const DecodeParams &p, const PagedView &pg, cudaStream_t stream)
 {
-    if (p.direct)
-        return p.cap_out > 0.f ? launch_paged_split<D, E4M3, true, true>(p, pg, stream)
-                               : launch_paged_split<D, E4M3, false, true>(p, pg, stream);
-    const cudaError_t e = p.cap_out > 0.f ? launch_paged_split<D, E4M3, true, false>(p, pg, stream)
-                                          : launch_paged_split<D, E4M3, false, false>(p, pg, stream);
-    return e != cudaSuccess ? e : launch_decode_combine(p, D, stream);
+    auto split = [&](auto capped) {
+        constexpr bool CAP = decltype(capped)::value;
+        if (p.direct > 1)
+            return launch_paged_split<D, E4M3, CAP, CLUSTER>(p, pg, stream);
+        if (p.direct)
+            return launch_paged_split<D, E4M3, CAP, DIRECT>(p, pg, stream);
+        const cudaError_t e = launch_paged_split<D, E4M3, CAP, SPLIT>(p, pg, stream);
+        return e != cudaSuccess ? e : launch_decode_combine(p, D, stream);
+    };
+    return p.cap_out > 0.f ? split(std::true_type()) : split(std::false_type());
 }
 
 }  // namespace
 
-int decode_paged_direct_keys() { return 512; }
-
 int decode_paged_ctas_per_sm(bool e4m3) { return e4m3 ? kCtasPerSm<true> : kCtasPerSm<false>; }
+
+// CTAs per stream of a call that is not cut over the whole grid, or 0.  A tile
+// takes a CTA 0.45 us (bf16) or 0.6 us (E4M3), the meeting in shared memory 1 us,
+// the merge pass 3 us: 128 keys per CTA while every CTA has an SM of its own, then
+// 256 while all are resident, and the whole grid once that leaves a CTA more than
+// 512 (or 256 with so few streams that the grid cuts them finer).  Measured, d 128,
+// one kv head per stream, split against this, bf16 / E4M3 in us: 16 streams of 1024
+// keys 8.3 / 9.1 against 8.2 / 8.7, of 2048 11.0 / 11.3 against 9.1 / 9.9; 64 of 2048
+// 16.3 / 15.8 against 12.0 / 14.1; 16 of 512 8.7 / 10.0 with one CTA each, 7.7 / 8.1
+// with four.  Beyond: 2 streams of 4096 keys 9.7 / 10.8 against 10.3 / 11.6; 128 of 512
+// with two CTAs each, two per SM, 10.1 / 11.1 against 9.3 / 10.6 with one.
+int decode_paged_cluster(bool e4m3, int sms, long long streams, int max_kv_len)
+{
+    int C = 1;
+    if (max_kv_len > 256)
+        while (C < MAX_CLUSTER && max_kv_len > 128 * C && streams * 2 * C <= sms)
+            C *= 2;
+    if (max_kv_len > 512)
+        while (C < MAX_CLUSTER && max_kv_len > 256 * C &&
+               streams * 2 * C <= (long long)sms * decode_paged_ctas_per_sm(e4m3))
+            C *= 2;
+    return max_kv_len <= (streams < 8 ? 256 : 512) * C ? C : 0;
+}
 
 cudaError_t launch_decode_paged(const DecodeParams &p, const PagedView &pg, bool e4m3, int d,
                                 cudaStream_t stream)

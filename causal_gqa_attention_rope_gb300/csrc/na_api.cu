@@ -777,10 +777,10 @@ int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_ro
         return NA_ERR_WORKSPACE;
     DecodeParams p = decode_params(cfg, pl, batch, q_rot, kv_lens, max_kv_len, gate, out, probs,
                                    probs_stride, workspace, status);
-    if (num_splits == 0 && max_kv_len <= decode_paged_direct_keys()) {
-        p.direct = 1;
-        p.grid = pl.streams;
-    }
+    if (num_splits == 0)
+        p.direct = decode_paged_cluster(e4m3, sm_count(), pl.streams, max_kv_len);
+    if (p.direct)
+        p.grid = pl.streams * p.direct;
     p.capacity = capacity;
     p.cache_batch = cache->batch;
     p.cache_k = static_cast<const bf16 *>(cache->k);

@@ -232,21 +232,32 @@ __device__ __forceinline__ void grid_dependents_launch()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// `cluster`: CTAs per thread-block cluster along x (0: no clusters).
 template <typename... Params, typename... Args>
-cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t stream, Args... args)
+cudaError_t launch_kernel_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                  int cluster, cudaStream_t stream, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, Args... args)
+{
+    return launch_kernel_cluster(kernel, grid, block, smem, 0, stream, args...);
 }
 
 // Host setup that must run once per device (kernel attributes): `setup`
@@ -326,7 +337,7 @@ struct DecodeParams {
     float *part_o;             // [max_pieces][heads-per-CTA][d]
     float *part_ml;            // [max_pieces][heads-per-CTA][2]  (max, sum) in the log2 domain
     int32_t *piece_span;       // [streams][2]  first and last piece id of each stream
-    int direct;                // paged: one CTA per stream, no merge pass
+    int direct;                // paged: CTAs per stream when there is no merge pass, else 0
     int32_t *status;
 };
 
@@ -394,6 +405,6 @@ size_t rope_append_smem_bytes(int H, int KV, int d, int rd);
 int decode_key_tile();
 int decode_ctas_per_sm();
 int decode_paged_ctas_per_sm(bool e4m3);
-int decode_paged_direct_keys();
+int decode_paged_cluster(bool e4m3, int sms, long long streams, int max_kv_len);
 int prefill_key_tile();
 int prefill_q_tile();

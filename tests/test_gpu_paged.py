@@ -266,6 +266,37 @@ def test_decode(case):
             assert (probs[b, :, n:] == -7.0).all()
 
 
+@pytest.mark.parametrize("case", [c for c in DECODE if "splits" not in c[6] and len(c[5]) < 10],
+                         ids=lambda c: f"{c[0]}d{c[1]}p{c[2]}g{c[4]}")
+def test_decode_cut_over_the_grid(case):
+    """The calls that take one CTA or one cluster per stream, through the merge pass instead."""
+    test_decode(case[:6] + (dict(case[6], splits=4),))
+
+
+# streams of a few CTAs each: the first, the last or every CTA but one without keys, windows
+# that start inside a CTA's share, and the lengths at which the number of CTAs changes
+CLUSTERS = [
+    ("bf16", 128, 64, 1, 4, [257, 0, 1, 64, 65], dict(probs=True)),
+    ("e4m3", 128, 64, 1, 4, [257, 0, 1, 64, 65], dict(probs=True, gate=True)),
+    ("bf16", 64, 16, 2, 8, [1024, 449, 448, 1023], dict(probs=True)),
+    ("e4m3", 64, 16, 2, 8, [1025, 449, 448, 129], dict(probs=True)),
+    ("bf16", 128, 128, 2, 3, [2048, 1, 0, 1500, 77], dict(window=130, probs=True, gate=True)),
+    ("e4m3", 128, 128, 2, 3, [2048, 1, 0, 1500, 77], dict(window=130, probs=True)),
+    ("bf16", 64, 32, 3, 1, [900, 65], dict(window=1, probs=True)),
+    ("e4m3", 64, 32, 3, 1, [900, 65], dict(window=1, softcap=3.0, probs=True)),
+    ("e4m3", 128, 16, 8, 2, [4096, 3999, 7], dict(softcap=30.0)),
+    ("bf16", 128, 64, 4, 2, [4096, 4095], dict(probs=True)),
+    ("bf16", 64, 64, 8, 1, [600] * 8, dict(probs=True)),
+    ("e4m3", 64, 64, 16, 1, [600 - 31 * i for i in range(16)], {}),
+    ("e4m3", 128, 64, 1, 40, [2000, 511], dict(probs=True)),
+]
+
+
+@pytest.mark.parametrize("case", CLUSTERS, ids=lambda c: f"{c[0]}d{c[1]}p{c[2]}g{c[4]}n{max(c[5])}")
+def test_decode_clusters(case):
+    test_decode(case)
+
+
 @pytest.mark.parametrize("mag", [2.0 ** 30, 2.0 ** -40])
 def test_decode_e4m3_scales_far_from_one(mag):
     """V of any magnitude, and page scales that differ by 2^10 within a sequence."""
