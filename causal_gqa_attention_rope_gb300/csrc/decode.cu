@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2)
     if (warp == DEC_CWARPS)
         locate_slice(p, lane, sm.slice);
     __syncthreads();
-    Walker walk;
+    Walker<> walk;
     walk.init(sm.slice, p);
     Piece pc;
     const bool ring = (p.flags & NA_RING_CACHE) != 0;  // capacity a multiple of DEC_TILE

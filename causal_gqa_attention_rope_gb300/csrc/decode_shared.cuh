@@ -35,6 +35,14 @@ __device__ __forceinline__ int valid_len(const DecodeParams &p, int b)
     return attended_keys(p, b, first);
 }
 
+// What a stream counts for in the cut into equal slices: its keys, and COST more
+// ahead of them for the time that a CTA spends on a piece besides its keys.
+template <int COST>
+__device__ __forceinline__ int stream_weight(int n)
+{
+    return n > 0 ? n + COST : 0;
+}
+
 // Where this CTA's key slice starts: computed by one full warp, then shared.
 struct Slice {
     long long start, end;  // [start, end) in the concatenation of all streams
@@ -50,13 +58,14 @@ struct Piece {
     bool first, last;  // holds the stream's first / last key
 };
 
+template <int COST = 0>
 __device__ __forceinline__ void locate_slice(const DecodeParams &p, int lane, Slice &out)
 {
     const unsigned FULL = 0xffffffffu;
     const int spb = p.KV * p.head_chunks;  // streams per sequence
     long long t = 0;
     for (int b = lane; b < p.batch; b += 32)
-        t += valid_len(p, b);
+        t += stream_weight<COST>(valid_len(p, b));
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1)
         t += __shfl_xor_sync(FULL, t, m);
@@ -74,7 +83,7 @@ __device__ __forceinline__ void locate_slice(const DecodeParams &p, int lane, Sl
         long long base = 0;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
             const int b = b0 + lane;
-            const int n = b < p.batch ? valid_len(p, b) : 0;
+            const int n = b < p.batch ? stream_weight<COST>(valid_len(p, b)) : 0;
             const long long w = (long long)n * spb;
             long long incl = w;
 #pragma unroll
@@ -102,6 +111,7 @@ __device__ __forceinline__ void locate_slice(const DecodeParams &p, int lane, Sl
 }
 
 // Walks this CTA's pieces in order; every thread of the CTA walks the same way.
+template <int COST = 0>
 struct Walker {
     long long start, end, off;
     int b, si, len, kfirst, spb, c;
@@ -126,14 +136,15 @@ struct Walker {
         while (!done && b < p.batch && off < end) {
             const long long s_off = off;
             const int n = len, sb = b, ssi = si, kfs = kfirst;
-            off += n;
+            off += stream_weight<COST>(n);
             if (++si == spb) {
                 si = 0;
                 if (++b < p.batch)
                     len = attended_keys(p, b, kfirst);
             }
-            const long long lo = start > s_off ? start - s_off : 0;
-            const long long hi = end - s_off < n ? end - s_off : n;
+            const long long k_off = s_off + COST;  // of the stream's first key
+            const long long lo = start > k_off ? start - k_off : 0;
+            const long long hi = end - k_off < n ? end - k_off : n;
             if (lo < hi) {
                 pc.b = sb;
                 pc.kvh = ssi / p.head_chunks;
