@@ -1,5 +1,8 @@
 """The compiled route of the three paged calls (csrc/paged_calls.cpp): it takes the plain
 call, leaves anything else to the Python checks, and both give the same bits."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -186,3 +189,20 @@ def test_the_library_refuses_through_the_compiled_route(monkeypatch):
     with pytest.raises(na.NAError) as e:
         steps("bf16", max_total=lambda a: 10 ** 6)  # past the table
     assert e.value.code == na.NA_ERR_CAPACITY and spy.answers == [na.NA_OK, na.NA_ERR_CAPACITY]
+
+
+def test_readme_examples_run():
+    """The README's examples one after the other, the contiguous cache and the paged one."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    with open(path) as fh:
+        blocks = re.findall(r"```python\n(.*?)```", fh.read(), re.S)
+    assert len(blocks) == 2
+    names = {}
+    for block in blocks:
+        exec(block, names)
+    torch.cuda.synchronize()
+    assert int(names["status"].item()) == 0
+    for out in (names["out"], names["out1"]):
+        assert torch.isfinite(out.float()).all() and out.abs().max() > 0
+    total = names["probs"][0, :, :129].double().sum(-1)
+    assert (total - 1).abs().max() < 129 * 2.0 ** -16
