@@ -46,8 +46,9 @@ def _stale(target: str, deps) -> bool:
 def build_calls(cuda: str) -> str:
     """Compile (if stale) and return the path of the extension module _paged_calls."""
     src = os.path.join(CSRC, "paged_calls.cpp")
-    if _stale(CALLS, [src, __file__, os.path.join(INCLUDE, "na.h")]):
-        torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    deps = [src, __file__, os.path.join(INCLUDE, "na.h"), os.path.join(torch, "version.py")]
+    if _stale(CALLS, deps):
         tmp = CALLS + f".tmp{os.getpid()}"
         cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o",
                tmp, "-I", INCLUDE, "-I", os.path.join(torch, "include"), "-I",

@@ -227,6 +227,12 @@ void start(Reader &r, PyObject *q)
         r.device = c10::cuda::current_device();
 }
 
+PyObject *declined()
+{
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
 template <class F>
 PyObject *answer(const Reader &r, F call)
 {
@@ -275,7 +281,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
                             &cache, status, stream);
         });
     } catch (...) {  // a tensor without storage: Python's checks say so
-        Py_RETURN_NONE;
+        return declined();
     }
 }
 
@@ -311,7 +317,7 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n)
                              gate, out, ws, ws_bytes, status, stream);
         });
     } catch (...) {
-        Py_RETURN_NONE;
+        return declined();
     }
 }
 
@@ -354,7 +360,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
                             (int32_t)stride, splits, ws, ws_bytes, status, stream);
         });
     } catch (...) {
-        Py_RETURN_NONE;
+        return declined();
     }
 }
 

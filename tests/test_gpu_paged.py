@@ -195,6 +195,23 @@ def test_append_e4m3_token_by_token_is_the_chunk():
 
 # ----------------------------------------------------------------- decode --
 
+# calls with enough rows for four per thread, and next to it
+MANY = [
+    (128, 128, 16, 4, 32, dict(qk_norm=True), [(0, 700), (3, 517), (40, 231)]),
+    (128, 64, 64, 8, 16, {}, [(100, 2500)]),
+    (64, 64, 32, 2, 64, {}, [(31, 1301), (0, 64), (5, 1)]),
+    (64, 32, 128, 8, 48, dict(qk_norm=True, zero=True, v_norm=True), [(7, 1500)]),
+    (128, 128, 128, 1, 40, {}, [(127, 1300)]),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"d{c[0]}rd{c[1]}p{c[2]}")
+def test_append_many_rows(case):
+    test_append_bf16_pages_equal_the_contiguous_append(case)
+    test_append_e4m3_pages(case, 1.0)
+
+
+
 DECODE = [
     # fmt, d, page, KV, G, lens, options
     ("e4m3", 128, 64, 8, 4, [1, 64, 65, 700], dict(probs=True)),
