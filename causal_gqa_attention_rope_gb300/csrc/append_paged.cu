@@ -80,6 +80,41 @@ __device__ __forceinline__ int scale_byte(float amax)
     return max(e, 0);
 }
 
+// Rows of a GENERIC call (rotary_dim no multiple of 16) pass through shared memory
+// between the 16 consecutive elements that a lane loads or stores and the eight
+// pairs, rd / 2 apart, that it rotates: a row's UPR lanes sit in one warp, and a
+// row is an odd number of words, so that the four rows of a warp miss each other's
+// banks.  (2048 tokens of 40/8 heads, E4M3 pages, rotary_dim 34: 23 us; 48 with
+// the queries staged by rope_append.cu and the pages element by element from global
+// memory; rotary_dim 64 takes 15.)
+template <int D, int NT>
+struct RowStage {
+    uint32_t words[NT / (D / 16)][D / 2 + 1];
+};
+
+// Element of pair slot i, its first and its second: (i, i + half) of the rotated
+// ones, then the tail two by two.
+__device__ __forceinline__ int slot_first(int i, int half) { return i < half ? i : 2 * i; }
+__device__ __forceinline__ int slot_second(int i, int half) { return i < half ? i + half : 2 * i + 1; }
+
+// A lane's chunks 2 k and 2 k + 1 in, its eight slots out (called by whole warps).
+__device__ __forceinline__ void stage_in(uint32_t *row, int k, int half, uint4 xa, uint4 xb,
+                                         float (&a)[8], float (&c)[8])
+{
+    __syncwarp();  // the reads of what was here
+    const uint32_t x[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        row[8 * k + j] = x[j];
+    __syncwarp();
+    const bf16 *el = reinterpret_cast<const bf16 *>(row);
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        a[e] = __bfloat162float(el[slot_first(8 * k + e, half)]);
+        c[e] = __bfloat162float(el[slot_second(8 * k + e, half)]);
+    }
+}
+
 // The page of one CTA: tokens [tok0, tok0 + rows) at positions pos0 ..
 struct PageWork {
     int b, page, tok0, pos0, rows;
@@ -145,20 +180,18 @@ __device__ __forceinline__ bool find_page(const RopeAppendParams &p, const Paged
 
 // R rows' units of 16 elements per thread: R * NT / (D / 16) rows >= the page.
 // Unit k of a rotated row holds the eight pairs 8k .. 8k + 7, then the tail two
-// elements per pair slot; GENERIC is the same with rotary_dim not a multiple of
-// 16, element by element.
+// elements per pair slot.
 template <int D, int R, int NT, bool GENERIC>
 __device__ __forceinline__ void append_page(const RopeAppendParams &p, const PagedView &pg,
-                                            const RopeTurns &turns, int slot, int g, bool is_v)
+                                            const RopeTurns &turns, RowStage<D, NT> *stage,
+                                            int slot, int g, bool is_v)
 {
     constexpr int UPR = D / 16;  // units per row: the row's lanes, aligned in a warp
     __shared__ float warp_max[NT / 32];
     const int half = p.rd / 2;
     const int k = threadIdx.x % UPR, row0 = threadIdx.x / UPR;
     const bool normed = (p.flags & (is_v ? NA_V_NORM : NA_QK_NORM)) != 0;
-    // element of pair slot i: its first and its second
-    auto first_of = [&](int i) { return is_v || i >= half ? (is_v ? 2 * i : p.rd + 2 * (i - half)) : i; };
-    auto second_of = [&](int i) { return !is_v && i < half ? i + half : first_of(i) + 1; };
+    const int pairs = is_v ? 0 : half;  // a V row's slots are all tail
     const bool rot = !is_v && 8 * k < half;  // (GENERIC: some slots of the unit may not be)
     unsigned long long f[8];
 #pragma unroll
@@ -173,8 +206,8 @@ __device__ __forceinline__ void append_page(const RopeAppendParams &p, const Pag
     // The rows first, then the page id: both loads in flight together.
     const bf16 *src = (is_v ? p.v : p.k) + ((size_t)w.tok0 * p.KV + g) * D;
     const size_t src_stride = (size_t)p.KV * D;
-    // two 8-element chunks of a unit (not GENERIC)
-    const int ca = rot ? k : 2 * k, cb = rot ? half / 8 + k : 2 * k + 1;
+    // two 8-element chunks of a unit
+    const int ca = rot && !GENERIC ? k : 2 * k, cb = rot && !GENERIC ? half / 8 + k : 2 * k + 1;
     uint4 xa[R], xb[R];
 #pragma unroll
     for (int r = 0; r < R; r++) {
@@ -182,20 +215,8 @@ __device__ __forceinline__ void append_page(const RopeAppendParams &p, const Pag
         xa[r] = xb[r] = make_uint4(0, 0, 0, 0);
         if (row < w.rows) {
             const bf16 *x = src + row * src_stride;
-            if constexpr (GENERIC) {
-                uint16_t h[16];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    h[i] = reinterpret_cast<const uint16_t *>(x)[first_of(8 * k + i)];
-                    h[8 + i] = reinterpret_cast<const uint16_t *>(x)[second_of(8 * k + i)];
-                }
-                auto two = [&](int i) { return (uint32_t)h[i] | ((uint32_t)h[i + 1] << 16); };
-                xa[r] = make_uint4(two(0), two(2), two(4), two(6));
-                xb[r] = make_uint4(two(8), two(10), two(12), two(14));
-            } else {
-                xa[r] = __ldg(reinterpret_cast<const uint4 *>(x) + ca);
-                xb[r] = __ldg(reinterpret_cast<const uint4 *>(x) + cb);
-            }
+            xa[r] = __ldg(reinterpret_cast<const uint4 *>(x) + ca);
+            xb[r] = __ldg(reinterpret_cast<const uint4 *>(x) + cb);
         }
     }
     const int id = __ldcg(pg.table + (size_t)w.b * pg.pages_per_seq + w.page);
@@ -204,8 +225,8 @@ __device__ __forceinline__ void append_page(const RopeAppendParams &p, const Pag
         if constexpr (GENERIC) {
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                wa[i] = __bfloat162float(p.kw[first_of(8 * k + i)]);
-                wb[i] = __bfloat162float(p.kw[second_of(8 * k + i)]);
+                wa[i] = __bfloat162float(p.kw[slot_first(8 * k + i, half)]);
+                wb[i] = __bfloat162float(p.kw[slot_second(8 * k + i, half)]);
             }
         } else {
             bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p.kw) + ca), wa);
@@ -239,8 +260,12 @@ __device__ __forceinline__ void append_page(const RopeAppendParams &p, const Pag
         if (r * (NT / UPR) >= w.rows)  // uniform: no thread has a row left
             break;
         float ya[8], yb[8];
-        bf16x8_to_f32(xa[r], ya);
-        bf16x8_to_f32(xb[r], yb);
+        if constexpr (GENERIC) {
+            stage_in(stage->words[row0], k, pairs, xa[r], xb[r], ya, yb);
+        } else {
+            bf16x8_to_f32(xa[r], ya);
+            bf16x8_to_f32(xb[r], yb);
+        }
         float fr = 1.0f;
         if (normed) {  // every lane shuffles; rows are aligned to UPR lanes
             float ss = 0.f;
@@ -308,18 +333,25 @@ __device__ __forceinline__ void append_page(const RopeAppendParams &p, const Pag
 #pragma unroll
     for (int r = 0; r < R; r++) {
         const int row = row0 + r * (NT / UPR);
-        if (row >= w.rows)
+        if (GENERIC ? r * (NT / UPR) >= w.rows : row >= w.rows)  // (GENERIC: whole warps go on)
             break;
         uint8_t *dst = page + (size_t)(held + row) * D;
         const uint2 a = make_uint2(pack_e4m3x4(at(r, 0), mul), pack_e4m3x4(at(r, 1), mul));
         const uint2 b = make_uint2(pack_e4m3x4(at(r, 2), mul), pack_e4m3x4(at(r, 3), mul));
         if constexpr (GENERIC) {
+            __syncwarp();
+            uint32_t *words = stage->words[row0];
+            uint8_t *bytes = reinterpret_cast<uint8_t *>(words);
             const uint32_t q[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                dst[first_of(8 * k + i)] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
-                dst[second_of(8 * k + i)] = (uint8_t)(q[2 + i / 4] >> (8 * (i % 4)));
+                bytes[slot_first(8 * k + i, pairs)] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+                bytes[slot_second(8 * k + i, pairs)] = (uint8_t)(q[2 + i / 4] >> (8 * (i % 4)));
             }
+            __syncwarp();
+            if (row < w.rows)
+                *reinterpret_cast<uint4 *>(dst + 16 * k) =
+                    make_uint4(words[4 * k], words[4 * k + 1], words[4 * k + 2], words[4 * k + 3]);
         } else {
             *reinterpret_cast<uint2 *>(dst + 8 * ca) = a;
             *reinterpret_cast<uint2 *>(dst + 8 * cb) = b;
@@ -339,10 +371,11 @@ long long page_ctas(const RopeAppendParams &p, const PagedView &pg)
 
 template <int D, int R, int NT, bool GENERIC>
 __device__ __forceinline__ void append_page_cta(const RopeAppendParams &p, const PagedView &pg,
-                                                const RopeTurns &turns, int i)
+                                                const RopeTurns &turns, RowStage<D, NT> *stage,
+                                                int i)
 {
     const int per = 2 * p.KV, slot = i / per, rest = i - slot * per;
-    append_page<D, R, NT, GENERIC>(p, pg, turns, slot, rest >> 1, rest & 1);
+    append_page<D, R, NT, GENERIC>(p, pg, turns, stage, slot, rest >> 1, rest & 1);
 }
 
 // The rows of TK tokens from token t0 on: P of them per thread group from row
@@ -377,9 +410,10 @@ __device__ __forceinline__ void rotate_exact2(float2 a0, float2 a1, float4 c, fl
     }
 }
 
-template <int D, int NT, int P, int TK, bool E4M3>
+template <int D, int NT, int P, int TK, bool E4M3, bool GENERIC>
 __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const PagedView &pg,
-                                            const RopeTurns &turns, int t0, int first)
+                                            const RopeTurns &turns, RowStage<D, NT> *stage, int t0,
+                                            int first)
 {
     constexpr int UPR = D / 16, RP = NT / UPR;  // 32-byte units per row, rows per pass
     // cos (and sin) hi, hi, lo, lo of pairs 8 k + 2 j and the next: [2 j (+ 1)][k]
@@ -392,9 +426,9 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
     const bool zero_centered = (p.flags & NA_QK_NORM_ZERO_CENTERED) != 0;
     const bool v_norm = !E4M3 && (p.flags & NA_V_NORM) != 0;
     const int ntok = min(TK, p.total_tokens - t0);
-    const bool rot = k < p.rd / 16;
+    const bool rot = GENERIC ? 8 * k < half : k < p.rd / 16;
     // 16-byte chunks of a unit: of a rotated row, and of a V row
-    const int qa = rot ? k : 2 * k, qb = rot ? half / 8 + k : 2 * k + 1;
+    const int qa = rot && !GENERIC ? k : 2 * k, qb = rot && !GENERIC ? half / 8 + k : 2 * k + 1;
 
     // this thread's cos and sin: pair `pair` of token `tk`
     const int tk = TK == 1 ? 0 : threadIdx.x / 64, pair = threadIdx.x & 63;
@@ -472,8 +506,14 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
         const bool active = row_at(i, t, r);
         const bool is_v = !E4M3 && r >= H + KV;
         float a[8], c[8];
-        bf16x8_to_f32(xa[i], a);
-        bf16x8_to_f32(xb[i], c);
+        if constexpr (GENERIC) {
+            stage_in(stage->words[threadIdx.x / UPR], k, is_v ? 0 : half, xa[i], xb[i], a, c);
+        } else {
+            bf16x8_to_f32(xa[i], a);
+            bf16x8_to_f32(xb[i], c);
+        }
+        // (GENERIC: a rotated unit's slots from `half` on are plain)
+        auto turned = [&](int e) { return rot && (!GENERIC || 8 * k + e < half); };
         float f = 1.0f;
         if (qk_norm || v_norm) {  // every lane shuffles; rows are aligned to UPR lanes
             float ss = 0.f;
@@ -486,11 +526,10 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
             if (is_v ? v_norm : qk_norm)
                 f = 1.0f / sqrtf(ss / (float)D + p.eps);
         }
-        if (!active)
-            continue;
         const RowPlace pl = place[t];
-        if (pl.pos < 0)
-            continue;
+        const bool written = active && pl.pos >= 0;
+        if (!GENERIC && !written)
+            continue;  // (GENERIC: whole warps go on)
         float ya[8], yb[8];
         if (is_v) {
 #pragma unroll
@@ -504,14 +543,29 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
             float wa[8], wb[8];
             if (qk_norm) {
                 const uint4 *w = reinterpret_cast<const uint4 *>(E4M3 || r < H ? p.qw : p.kw);
-                bf16x8_to_f32(__ldg(w + qa), wa);
-                bf16x8_to_f32(__ldg(w + qb), wb);
+                if constexpr (GENERIC) {
+                    const bf16 *el = reinterpret_cast<const bf16 *>(w);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        wa[e] = __bfloat162float(el[slot_first(8 * k + e, half)]);
+                        wb[e] = __bfloat162float(el[slot_second(8 * k + e, half)]);
+                    }
+                } else {
+                    bf16x8_to_f32(__ldg(w + qa), wa);
+                    bf16x8_to_f32(__ldg(w + qb), wb);
+                }
             }
-            if (qk_norm && zero_centered) {
+            // (GENERIC bf16 rows take this way too, without weights: it has the bits of the
+            // contiguous call's staged rows)
+            if ((qk_norm && zero_centered) || (GENERIC && !E4M3)) {
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    const F2 x0 = weighted(a[e], wa[e], true), x1 = weighted(c[e], wb[e], true);
-                    if (rot) {
+                    F2 x0{a[e], 0.f}, x1{c[e], 0.f};
+                    if (qk_norm) {
+                        x0 = weighted(a[e], wa[e], zero_centered);
+                        x1 = weighted(c[e], wb[e], zero_centered);
+                    }
+                    if (turned(e)) {
                         const float *tr = reinterpret_cast<const float *>(trig_row + (e & 6) * 8) + (e & 1);
                         rotate(x0, x1, make_float4(tr[0], tr[2], tr[32], tr[34]), fr, ya[e], yb[e]);
                     } else {
@@ -534,10 +588,10 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
                         float2 y0, y1;
                         rotate_exact2(make_float2(a[e], a[e + 1]), make_float2(c[e], c[e + 1]),
                                       trig_row[e * 8], trig_row[e * 8 + 8], fr2, y0, y1);
-                        ya[e] = y0.x;
-                        ya[e + 1] = y0.y;
-                        yb[e] = y1.x;
-                        yb[e + 1] = y1.y;
+                        ya[e] = turned(e) ? y0.x : a[e] * f;
+                        ya[e + 1] = turned(e + 1) ? y0.y : a[e + 1] * f;
+                        yb[e] = turned(e) ? y1.x : c[e] * f;
+                        yb[e + 1] = turned(e + 1) ? y1.y : c[e + 1] * f;
                     }
                 } else {
 #pragma unroll
@@ -554,13 +608,30 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
         else
             dst = (is_v ? p.cache_v : p.cache_k) +
                   ((((size_t)pl.id * KV + (is_v ? r - H - KV : r - H)) << pg.page_log) + pl.slot) * D;
-        reinterpret_cast<uint4 *>(dst)[is_v ? 2 * k : qa] = f32_to_bf16x8(ya);
-        reinterpret_cast<uint4 *>(dst)[is_v ? 2 * k + 1 : qb] = f32_to_bf16x8(yb);
+        if constexpr (GENERIC) {
+            __syncwarp();
+            uint32_t *words = stage->words[threadIdx.x / UPR];
+            bf16 *el = reinterpret_cast<bf16 *>(words);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                el[slot_first(8 * k + e, is_v ? 0 : half)] = __float2bfloat16_rn(ya[e]);
+                el[slot_second(8 * k + e, is_v ? 0 : half)] = __float2bfloat16_rn(yb[e]);
+            }
+            __syncwarp();
+            const uint32_t *x = words + 8 * k;
+            if (written) {
+                reinterpret_cast<uint4 *>(dst)[2 * k] = make_uint4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<uint4 *>(dst)[2 * k + 1] = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+        } else {
+            reinterpret_cast<uint4 *>(dst)[is_v ? 2 * k : qa] = f32_to_bf16x8(ya);
+            reinterpret_cast<uint4 *>(dst)[is_v ? 2 * k + 1 : qb] = f32_to_bf16x8(yb);
+        }
     }
 }
 
 // Page CTAs first (E4M3): theirs is the longer chain of dependent loads.
-template <int D, bool E4M3, int R, int NT, int P>
+template <int D, bool E4M3, int R, int NT, int P, bool GENERIC>
 __global__ void __launch_bounds__(NT, 768 / NT) append_paged_kernel(const RopeAppendParams p,
                                                           const PagedView pg, const RopeTurns turns,
                                                           const int n_page_ctas,
@@ -568,22 +639,20 @@ __global__ void __launch_bounds__(NT, 768 / NT) append_paged_kernel(const RopeAp
 {
     constexpr int TK = P == 1 ? 1 : NT / 64, RP = NT / (D / 16);
     int i = blockIdx.x;
+    RowStage<D, NT> *stage = nullptr;
+    if constexpr (GENERIC) {
+        __shared__ RowStage<D, NT> rows;
+        stage = &rows;
+    }
     if constexpr (E4M3) {
         if (i < n_page_ctas) {
-            append_page_cta<D, R, NT, false>(p, pg, turns, i);
+            append_page_cta<D, R, NT, GENERIC>(p, pg, turns, stage, i);
             return;
         }
         i -= n_page_ctas;
     }
     const int group = i / ctas_per_group, part = i - group * ctas_per_group;
-    append_rows<D, NT, P, TK, E4M3>(p, pg, turns, group * TK, part * P * RP);
-}
-
-template <int D, int R, int NT>
-__global__ void __launch_bounds__(NT, 768 / NT) append_pages_kernel(const RopeAppendParams p,
-                                                          const PagedView pg, const RopeTurns turns)
-{
-    append_page_cta<D, R, NT, true>(p, pg, turns, blockIdx.x);
+    append_rows<D, NT, P, TK, E4M3, GENERIC>(p, pg, turns, stage, group * TK, part * P * RP);
 }
 
 // Shared memory of the page CTAs, granted to `kernel` once per device where it
@@ -599,7 +668,7 @@ cudaError_t grant_smem(Kernel kernel, std::atomic<unsigned long long> &done)
     });
 }
 
-template <int D, bool E4M3, int R, int NT, int P>
+template <int D, bool E4M3, int R, int NT, int P, bool GENERIC>
 cudaError_t launch_fused(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
                          cudaStream_t stream)
 {
@@ -612,10 +681,10 @@ cudaError_t launch_fused(const RopeAppendParams &p, const PagedView &pg, const R
         return cudaErrorInvalidConfiguration;
     static std::atomic<unsigned long long> granted{0};
     const size_t smem = E4M3 ? R * NT * 64 : 0;
-    const cudaError_t e = grant_smem<E4M3 ? R : 0, NT>(append_paged_kernel<D, E4M3, R, NT, P>, granted);
+    const cudaError_t e = grant_smem<E4M3 ? R : 0, NT>(append_paged_kernel<D, E4M3, R, NT, P, GENERIC>, granted);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(append_paged_kernel<D, E4M3, R, NT, P>, dim3((unsigned)(pages + groups * per)),
+    return launch_kernel(append_paged_kernel<D, E4M3, R, NT, P, GENERIC>, dim3((unsigned)(pages + groups * per)),
                          dim3(NT), smem, stream, p, pg, turns, (int)pages, per);
 }
 
@@ -629,26 +698,14 @@ cudaError_t launch_p(const RopeAppendParams &p, const PagedView &pg, const RopeT
 {
     const int rows = p.H + (E4M3 ? 0 : 2 * p.KV);
     const long long units = (long long)p.total_tokens * rows * (D / 16);
+    if (p.rd % 16 != 0)
+        return units >= 2ll * NT * kManyRowCtas ? launch_fused<D, E4M3, R, NT, 2, true>(p, pg, turns, stream)
+                                                : launch_fused<D, E4M3, R, NT, 1, true>(p, pg, turns, stream);
     if (units >= 4ll * NT * kManyRowCtas && NT / 64 * rows % (4 * NT / (D / 16)) == 0)
-        return launch_fused<D, E4M3, R, NT, 4>(p, pg, turns, stream);
+        return launch_fused<D, E4M3, R, NT, 4, false>(p, pg, turns, stream);
     if (units >= 2ll * NT * kManyRowCtas)
-        return launch_fused<D, E4M3, R, NT, 2>(p, pg, turns, stream);
-    return launch_fused<D, E4M3, R, NT, 1>(p, pg, turns, stream);
-}
-
-template <int D, int R, int NT>
-cudaError_t launch_generic(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
-                           cudaStream_t stream)
-{
-    const long long pages = page_ctas(p, pg);
-    if (pages > 0x7fffffffLL)
-        return cudaErrorInvalidConfiguration;
-    static std::atomic<unsigned long long> granted{0};
-    const cudaError_t e = grant_smem<R, NT>(append_pages_kernel<D, R, NT>, granted);
-    if (e != cudaSuccess)
-        return e;
-    return launch_kernel(append_pages_kernel<D, R, NT>, dim3((unsigned)pages), dim3(NT), R * NT * 64,
-                         stream, p, pg, turns);
+        return launch_fused<D, E4M3, R, NT, 2, false>(p, pg, turns, stream);
+    return launch_fused<D, E4M3, R, NT, 1, false>(p, pg, turns, stream);
 }
 
 }  // namespace
@@ -673,25 +730,5 @@ cudaError_t launch_append_paged(const RopeAppendParams &p, const PagedView &pg, 
     case 5: return launch_p<64, true, 1, 128>(p, pg, turns, stream);
     case 6: return launch_p<64, true, 2, 128>(p, pg, turns, stream);
     default: return launch_p<64, true, 4, 128>(p, pg, turns, stream);
-    }
-}
-
-// The page CTAs alone, for any even rotary dimension.
-cudaError_t launch_append_pages(const RopeAppendParams &p, const PagedView &pg,
-                                const RopeTurns &turns, cudaStream_t stream)
-{
-    if (p.d == 128) {
-        switch (pg.page_log) {
-        case 4: return launch_generic<128, 1, 128>(p, pg, turns, stream);
-        case 5: return launch_generic<128, 2, 128>(p, pg, turns, stream);
-        case 6: return launch_generic<128, 4, 128>(p, pg, turns, stream);
-        default: return launch_generic<128, 4, 256>(p, pg, turns, stream);
-        }
-    }
-    switch (pg.page_log) {
-    case 4:
-    case 5: return launch_generic<64, 1, 128>(p, pg, turns, stream);
-    case 6: return launch_generic<64, 2, 128>(p, pg, turns, stream);
-    default: return launch_generic<64, 4, 128>(p, pg, turns, stream);
     }
 }

@@ -397,8 +397,6 @@ cudaError_t launch_prefill(const PrefillParams &p, int d, int total_tokens, int 
                            cudaStream_t stream);
 cudaError_t launch_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
                                 const RopeTurns &turns, cudaStream_t stream);
-cudaError_t launch_append_pages(const RopeAppendParams &p, const PagedView &pg,
-                                const RopeTurns &turns, cudaStream_t stream);
 cudaError_t launch_prefill_paged(const PrefillParams &p, const PagedView &pg, bool e4m3, int d,
                                  int total_tokens, cudaStream_t stream);
 size_t rope_append_smem_bytes(int H, int KV, int d, int rd);

@@ -247,11 +247,9 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const RopeA
 
 // -------------------------------------------------------- staged path --
 
-// Where the staged kernel's keys and values go; a paged call's rows behind the
-// last sequence are left alone.
-enum StagedTarget { TO_CACHE, TO_PAGES, QUERIES_ALONE };
-
-template <StagedTarget TO>
+// PAGED: keys and values go to pages, and rows behind the last sequence are left
+// alone.
+template <bool PAGED>
 __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(const RopeAppendParams p,
                                                                            const PagedView pg,
                                                                            const RopeTurns turns)
@@ -278,7 +276,7 @@ __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(cons
         reinterpret_cast<uint4 *>(trig)[i] = __ldg(reinterpret_cast<const uint4 *>(&kTrig) + i);
     grid_dependency_wait();
     grid_dependents_launch();
-    if (TO != TO_CACHE && t >= __ldg(p.cu_seqlens + p.batch))
+    if (PAGED && t >= __ldg(p.cu_seqlens + p.batch))
         return;
     int b, pos;
     owner_of(p, t, lane, b, pos);
@@ -290,7 +288,7 @@ __global__ void __launch_bounds__(kStagedThreads) rope_append_staged_kernel(cons
     }
     int slot;
     size_t cap;
-    if (!cache_place<TO == TO_PAGES>(p, pg, pos, b, slot, cap)) {
+    if (!cache_place<PAGED>(p, pg, pos, b, slot, cap)) {
         if (threadIdx.x == 0)
             na_report(p.status, NA_ERR_PAGE);
         return;
@@ -393,7 +391,7 @@ void turns_fixed_point(double inv_freq, unsigned long long &hi, unsigned int &lo
     lo = (unsigned int)(x & 0xffffffff);
 }
 
-template <StagedTarget TO>
+template <bool PAGED>
 cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
                           cudaStream_t stream)
 {
@@ -402,7 +400,7 @@ cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const 
     static std::atomic<size_t> configured[kMaxDevices];
     const int dev = current_device_index();
     if (smem > 48 * 1024 && (dev < 0 || smem > configured[dev].load(std::memory_order_acquire))) {
-        cudaError_t e = cudaFuncSetAttribute(rope_append_staged_kernel<TO>,
+        cudaError_t e = cudaFuncSetAttribute(rope_append_staged_kernel<PAGED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
         if (e != cudaSuccess)
@@ -413,7 +411,7 @@ cudaError_t launch_staged(const RopeAppendParams &p, const PagedView &pg, const 
                 ;
         }
     }
-    return launch_kernel(rope_append_staged_kernel<TO>, dim3(p.total_tokens),
+    return launch_kernel(rope_append_staged_kernel<PAGED>, dim3(p.total_tokens),
                          dim3(kStagedThreads), smem, stream, p, pg, turns);
 }
 
@@ -438,22 +436,18 @@ cudaError_t launch_rope_append(const RopeAppendParams &p, const RopeTurns &turns
                                  turns);
         return launch_kernel(rope_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, p, turns);
     }
-    return launch_staged<TO_CACHE>(p, PagedView{}, turns, stream);
+    return launch_staged<false>(p, PagedView{}, turns, stream);
 }
 
-// Into pages: one launch when the rotary dimension fits the register kernels;
-// otherwise the staged rows, then (E4M3) keys and values by page.
+// Into pages.  The staged rows stay for bf16 pages with norms at a rotary dimension
+// that is no multiple of 16: their sums run in another order than the register
+// kernels', and bf16 pages hold the bits of the contiguous call.
 cudaError_t launch_rope_append_paged(const RopeAppendParams &p, const PagedView &pg, bool e4m3,
                                      const RopeTurns &turns, cudaStream_t stream)
 {
-    if (p.rd % 16 == 0)
-        return launch_append_paged(p, pg, e4m3, turns, stream);
-    if (!e4m3)
-        return launch_staged<TO_PAGES>(p, pg, turns, stream);
-    RopeAppendParams q = p;
-    q.KV = 0;
-    const cudaError_t e = launch_staged<QUERIES_ALONE>(q, pg, turns, stream);
-    return e != cudaSuccess ? e : launch_append_pages(p, pg, turns, stream);
+    if (p.rd % 16 != 0 && !e4m3 && (p.flags & (NA_QK_NORM | NA_V_NORM)))
+        return launch_staged<true>(p, pg, turns, stream);
+    return launch_append_paged(p, pg, e4m3, turns, stream);
 }
 
 size_t rope_append_smem_bytes(int H, int KV, int d, int rd)

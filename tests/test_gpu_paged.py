@@ -205,6 +205,25 @@ MANY = [
 ]
 
 
+# rotary dimensions that are no multiple of 16, with and without norms, few rows and many
+ODD = [
+    (128, 34, 64, 8, 40, {}, [(100, 700), (0, 1), (63, 2)]),
+    (128, 34, 16, 2, 8, dict(yarn=True), [(5, 40), (0, 0), (16, 16), (31, 1), (0, 17)]),
+    (64, 18, 32, 2, 6, {}, [(10, 60), (100, 1), (0, 33)]),
+    (64, 18, 128, 2, 16, dict(qk_norm=True), [(0, 128), (127, 900)]),
+    (128, 2, 128, 1, 3, dict(qk_norm=True, zero=True), [(120, 20), (0, 260)]),
+    (128, 126, 16, 1, 5, dict(v_norm=True), [(3, 50), (0, 7)]),
+    (64, 62, 64, 3, 3, {}, [(i % 70, 1 + i % 3) for i in range(75)]),
+]
+
+
+@pytest.mark.parametrize("mag", [1.0, 2.0 ** -30])
+@pytest.mark.parametrize("case", ODD, ids=lambda c: f"d{c[0]}rd{c[1]}p{c[2]}")
+def test_append_odd_rotary_dimensions(case, mag):
+    test_append_bf16_pages_equal_the_contiguous_append(case)
+    test_append_e4m3_pages(case, mag)
+
+
 @pytest.mark.parametrize("case", MANY, ids=lambda c: f"d{c[0]}rd{c[1]}p{c[2]}")
 def test_append_many_rows(case):
     test_append_bf16_pages_equal_the_contiguous_append(case)
