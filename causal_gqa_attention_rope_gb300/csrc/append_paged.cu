@@ -178,6 +178,164 @@ __device__ __forceinline__ bool find_page(const RopeAppendParams &p, const Paged
     return true;
 }
 
+// One unit of a row at position pos, normed and rotated in place; its largest
+// magnitude.  The row's other lanes run with it.  (GENERIC: the unit's first `pairs`
+// slots are rotated.)
+template <int D, bool GENERIC>
+__device__ __forceinline__ float unit_values(const RopeAppendParams &p, float (&ya)[8], float (&yb)[8],
+                                             const float (&wa)[8], const float (&wb)[8],
+                                             const unsigned long long (&f)[8], int pos, bool is_v,
+                                             bool normed, bool rot, int pairs)
+{
+    float fr = 1.0f, amax = 0.f;
+    if (normed) {  // every lane shuffles; rows are aligned to their lanes
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            ss = fmaf(ya[i], ya[i], fmaf(yb[i], yb[i], ss));
+#pragma unroll
+        for (int o = D / 32; o; o >>= 1)
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        fr = 1.0f / sqrtf(ss / (float)D + p.eps);
+        if (!is_v) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                ya[i] *= wa[i];
+                yb[i] *= wb[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        float a = ya[i] * fr, b = yb[i] * fr;
+        if (rot && (!GENERIC || i < pairs)) {
+            float c, s;
+            cos_sin_phase(pos, f[i], c, s);
+            const float a0 = a, b0 = b;
+            a = (a0 * c - b0 * s) * p.rope_scale;
+            b = (a0 * s + b0 * c) * p.rope_scale;
+        }
+        ya[i] = a;
+        yb[i] = b;
+        amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+    }
+    return amax;
+}
+
+// Earlier tokens of a page, rounded to its new scale: 16 bytes a thread.
+__device__ __forceinline__ void rescale_held(uint8_t *page, int bytes, int old, int now, int thread,
+                                             int threads)
+{
+    const int e = 127 + old - now;
+    const float shrink = e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
+    uint4 *rows = reinterpret_cast<uint4 *>(page);
+    for (int i = thread; i < bytes / 16; i += threads) {
+        uint4 u = __ldcg(rows + i);
+        u.x = rescale_e4m3x4(u.x, shrink);
+        u.y = rescale_e4m3x4(u.y, shrink);
+        u.z = rescale_e4m3x4(u.z, shrink);
+        u.w = rescale_e4m3x4(u.w, shrink);
+        rows[i] = u;
+    }
+}
+
+// The work of a page CTA (below) by one warp, for calls of a token or two per
+// sequence: four pages to a CTA instead of one CTA of which one row's lanes have
+// work (64 single tokens, 8 kv heads, d 128, pages of 64: 4.4 us, 8.5 by CTAs).  The
+// first 32 / (D / 16) rows stay in registers; should a page get more they are
+// computed twice, for the scale and for the bytes.
+template <int D>
+__device__ __forceinline__ void append_page_warp(const RopeAppendParams &p, const PagedView &pg,
+                                                 const RopeTurns &turns, int slot, int g, bool is_v)
+{
+    constexpr int UPR = D / 16, RP = 32 / UPR;
+    const int lane = threadIdx.x & 31, half = p.rd / 2;
+    const int k = lane % UPR, row0 = lane / UPR;
+    const bool normed = (p.flags & (is_v ? NA_V_NORM : NA_QK_NORM)) != 0;
+    const bool rot = !is_v && 8 * k < half;
+    unsigned long long f[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        f[i] = rot ? turns.hi[8 * k + i] : 0ull;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    PageWork w;
+    if (!find_page(p, pg, slot, lane == 0 && g == 0 && !is_v, w))
+        return;
+    const bf16 *src = (is_v ? p.v : p.k) + ((size_t)w.tok0 * p.KV + g) * D;
+    const int ca = rot ? k : 2 * k, cb = rot ? half / 8 + k : 2 * k + 1;
+    auto load = [&](int row, float (&ya)[8], float (&yb)[8]) {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (row < w.rows) {
+            const uint4 *x = reinterpret_cast<const uint4 *>(src + (size_t)row * p.KV * D);
+            a = __ldg(x + ca);
+            b = __ldg(x + cb);
+        }
+        bf16x8_to_f32(a, ya);
+        bf16x8_to_f32(b, yb);
+    };
+    const int id = __ldcg(pg.table + (size_t)w.b * pg.pages_per_seq + w.page);
+    float ya[8], yb[8], wa[8], wb[8];
+    load(row0, ya, yb);
+    if (!is_v && normed) {
+        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p.kw) + ca), wa);
+        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p.kw) + cb), wb);
+        if (p.flags & NA_QK_NORM_ZERO_CENTERED) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                wa[i] += 1.0f;
+                wb[i] += 1.0f;
+            }
+        }
+    }
+    if ((unsigned)id >= (unsigned)pg.num_pages) {
+        if (lane == 0)
+            na_report(p.status, NA_ERR_PAGE);
+        return;
+    }
+    uint8_t *scale = const_cast<uint8_t *>(is_v ? pg.v_scale : pg.k_scale) + (size_t)id * p.KV + g;
+    const int held = w.pos0 & ((1 << pg.page_log) - 1);  // earlier tokens of the page
+    const int old = held ? (int)__ldcg(scale) : 0;
+    auto values = [&](int row, float (&a)[8], float (&b)[8]) {
+        return unit_values<D, false>(p, a, b, wa, wb, f, w.pos0 + row, is_v, normed, rot, 8);
+    };
+    float amax = values(row0, ya, yb);
+    for (int r = RP; r < w.rows; r += RP) {
+        float ta[8], tb[8];
+        load(r + row0, ta, tb);
+        amax = fmaxf(amax, values(r + row0, ta, tb));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int now = max(old, scale_byte(amax));
+    uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? p.cache_v : p.cache_k);
+    uint8_t *page = pool + (((size_t)id * p.KV + g) << pg.page_log) * D;
+    if (held && now > old)
+        rescale_held(page, held * D, old, now, lane, 32);
+    const float mul = e8m0_value(254 - now);  // 2^-e
+    auto store = [&](int row, const float (&a)[8], const float (&b)[8]) {
+        if (row >= w.rows)
+            return;
+        uint8_t *dst = page + (size_t)(held + row) * D;
+        *reinterpret_cast<uint2 *>(dst + 8 * ca) =
+            make_uint2(pack_e4m3x4(make_float4(a[0], a[1], a[2], a[3]), mul),
+                       pack_e4m3x4(make_float4(a[4], a[5], a[6], a[7]), mul));
+        *reinterpret_cast<uint2 *>(dst + 8 * cb) =
+            make_uint2(pack_e4m3x4(make_float4(b[0], b[1], b[2], b[3]), mul),
+                       pack_e4m3x4(make_float4(b[4], b[5], b[6], b[7]), mul));
+    };
+    store(row0, ya, yb);
+    for (int r = RP; r < w.rows; r += RP) {
+        float ta[8], tb[8];
+        load(r + row0, ta, tb);
+        values(r + row0, ta, tb);
+        store(r + row0, ta, tb);
+    }
+    if (lane == 0)
+        *scale = (uint8_t)now;
+}
+
 // R rows' units of 16 elements per thread: R * NT / (D / 16) rows >= the page.
 // Unit k of a rotated row holds the eight pairs 8k .. 8k + 7, then the tail two
 // elements per pair slot.
@@ -266,38 +424,8 @@ __device__ __forceinline__ void append_page(const RopeAppendParams &p, const Pag
             bf16x8_to_f32(xa[r], ya);
             bf16x8_to_f32(xb[r], yb);
         }
-        float fr = 1.0f;
-        if (normed) {  // every lane shuffles; rows are aligned to UPR lanes
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                ss = fmaf(ya[i], ya[i], fmaf(yb[i], yb[i], ss));
-#pragma unroll
-            for (int o = UPR / 2; o; o >>= 1)
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            fr = 1.0f / sqrtf(ss / (float)D + p.eps);
-            if (!is_v) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    ya[i] *= wa[i];
-                    yb[i] *= wb[i];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            float a = ya[i] * fr, b = yb[i] * fr;
-            if (rot && (!GENERIC || 8 * k + i < half)) {
-                float c, s;
-                cos_sin_phase(w.pos0 + row, f[i], c, s);
-                const float a0 = a, b0 = b;
-                a = (a0 * c - b0 * s) * p.rope_scale;
-                b = (a0 * s + b0 * c) * p.rope_scale;
-            }
-            ya[i] = a;
-            yb[i] = b;
-            amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));  // rows past the page's: zeros
-        }
+        amax = fmaxf(amax, unit_values<D, GENERIC>(p, ya, yb, wa, wb, f, w.pos0 + row, is_v, normed, rot,
+                                                  half - 8 * k));
         at(r, 0) = make_float4(ya[0], ya[1], ya[2], ya[3]);
         at(r, 1) = make_float4(ya[4], ya[5], ya[6], ya[7]);
         at(r, 2) = make_float4(yb[0], yb[1], yb[2], yb[3]);
@@ -316,19 +444,8 @@ __device__ __forceinline__ void append_page(const RopeAppendParams &p, const Pag
 
     uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? p.cache_v : p.cache_k);
     uint8_t *page = pool + (((size_t)id * p.KV + g) << pg.page_log) * D;
-    if (held && now > old) {
-        const int e = 127 + old - now;
-        const float shrink = e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
-        uint4 *rows = reinterpret_cast<uint4 *>(page);
-        for (int i = threadIdx.x; i < held * D / 16; i += NT) {
-            uint4 u = __ldcg(rows + i);
-            u.x = rescale_e4m3x4(u.x, shrink);
-            u.y = rescale_e4m3x4(u.y, shrink);
-            u.z = rescale_e4m3x4(u.z, shrink);
-            u.w = rescale_e4m3x4(u.w, shrink);
-            rows[i] = u;
-        }
-    }
+    if (held && now > old)
+        rescale_held(page, held * D, old, now, threadIdx.x, NT);
     const float mul = e8m0_value(254 - now);  // 2^-e
 #pragma unroll
     for (int r = 0; r < R; r++) {
@@ -631,7 +748,8 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
 }
 
 // Page CTAs first (E4M3): theirs is the longer chain of dependent loads.
-template <int D, bool E4M3, int R, int NT, int P, bool GENERIC>
+// FEW: a warp each.
+template <int D, bool E4M3, int R, int NT, int P, bool GENERIC, bool FEW>
 __global__ void __launch_bounds__(NT, 768 / NT) append_paged_kernel(const RopeAppendParams p,
                                                           const PagedView pg, const RopeTurns turns,
                                                           const int n_page_ctas,
@@ -646,7 +764,13 @@ __global__ void __launch_bounds__(NT, 768 / NT) append_paged_kernel(const RopeAp
     }
     if constexpr (E4M3) {
         if (i < n_page_ctas) {
-            append_page_cta<D, R, NT, GENERIC>(p, pg, turns, stage, i);
+            if constexpr (FEW) {
+                const int per = 2 * p.KV, item = i * (NT / 32) + threadIdx.x / 32;
+                const int slot = item / per, rest = item - slot * per;
+                append_page_warp<D>(p, pg, turns, slot, rest >> 1, rest & 1);
+            } else {
+                append_page_cta<D, R, NT, GENERIC>(p, pg, turns, stage, i);
+            }
             return;
         }
         i -= n_page_ctas;
@@ -668,7 +792,7 @@ cudaError_t grant_smem(Kernel kernel, std::atomic<unsigned long long> &done)
     });
 }
 
-template <int D, bool E4M3, int R, int NT, int P, bool GENERIC>
+template <int D, bool E4M3, int R, int NT, int P, bool GENERIC, bool FEW = false>
 cudaError_t launch_fused(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
                          cudaStream_t stream)
 {
@@ -676,15 +800,17 @@ cudaError_t launch_fused(const RopeAppendParams &p, const PagedView &pg, const R
     const int rows = p.H + (E4M3 ? 0 : 2 * p.KV);
     const long long groups = (p.total_tokens + TK - 1) / TK;
     const int per = (TK * rows + P * RP - 1) / (P * RP);
-    const long long pages = E4M3 ? page_ctas(p, pg) : 0;
+    long long pages = E4M3 ? page_ctas(p, pg) : 0;
+    if (FEW)  // (a last warp without a slot finds no work)
+        pages = (pages + NT / 32 - 1) / (NT / 32);
     if (pages + groups * per > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     static std::atomic<unsigned long long> granted{0};
-    const size_t smem = E4M3 ? R * NT * 64 : 0;
-    const cudaError_t e = grant_smem<E4M3 ? R : 0, NT>(append_paged_kernel<D, E4M3, R, NT, P, GENERIC>, granted);
+    const size_t smem = E4M3 && !FEW ? R * NT * 64 : 0;
+    const cudaError_t e = grant_smem<E4M3 && !FEW ? R : 0, NT>(append_paged_kernel<D, E4M3, R, NT, P, GENERIC, FEW>, granted);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(append_paged_kernel<D, E4M3, R, NT, P, GENERIC>, dim3((unsigned)(pages + groups * per)),
+    return launch_kernel(append_paged_kernel<D, E4M3, R, NT, P, GENERIC, FEW>, dim3((unsigned)(pages + groups * per)),
                          dim3(NT), smem, stream, p, pg, turns, (int)pages, per);
 }
 
@@ -692,6 +818,7 @@ cudaError_t launch_fused(const RopeAppendParams &p, const PagedView &pg, const R
 // rows of a CTA's tokens come out even, else 2.  (16 sequences of 1 .. 512 tokens, 32
 // query heads, E4M3 pages of 16: 23.8 us at 2, 22.0 at 4; 2048 tokens of 40 heads,
 // where 4 leaves three of eight slots empty: 18.5 at 2, 20.9 at 4.)
+// E4M3 pages of a call of two tokens per sequence or fewer get a warp each.
 template <int D, bool E4M3, int R, int NT>
 cudaError_t launch_p(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
                      cudaStream_t stream)
@@ -701,6 +828,10 @@ cudaError_t launch_p(const RopeAppendParams &p, const PagedView &pg, const RopeT
     if (p.rd % 16 != 0)
         return units >= 2ll * NT * kManyRowCtas ? launch_fused<D, E4M3, R, NT, 2, true>(p, pg, turns, stream)
                                                 : launch_fused<D, E4M3, R, NT, 1, true>(p, pg, turns, stream);
+    if constexpr (E4M3) {
+        if (p.total_tokens <= 2ll * p.batch && units < 2ll * NT * kManyRowCtas)
+            return launch_fused<D, true, 1, 128, 1, false, true>(p, pg, turns, stream);
+    }
     if (units >= 4ll * NT * kManyRowCtas && NT / 64 * rows % (4 * NT / (D / 16)) == 0)
         return launch_fused<D, E4M3, R, NT, 4, false>(p, pg, turns, stream);
     if (units >= 2ll * NT * kManyRowCtas)

@@ -217,6 +217,21 @@ ODD = [
 ]
 
 
+# two tokens per sequence or fewer on the average, one sequence with many
+FEW = [
+    (128, 64, 64, 2, 4, dict(qk_norm=True), [(10, 70)] + [(i, 0) for i in range(40)]),
+    (64, 64, 128, 3, 3, dict(v_norm=True), [(100, 60)] + [(5, 0)] * 30 + [(127, 2)]),
+    (128, 128, 16, 1, 2, dict(qk_norm=True, zero=True), [(3, 30), (0, 0), (15, 2)] + [(7, 1)] * 60),
+    (64, 32, 32, 8, 8, {}, [(i, 1) for i in range(64)]),
+]
+
+
+@pytest.mark.parametrize("mag", [1.0, 2.0 ** 20])
+@pytest.mark.parametrize("case", FEW, ids=lambda c: f"d{c[0]}rd{c[1]}p{c[2]}")
+def test_append_few_tokens(case, mag):
+    test_append_e4m3_pages(case, mag)
+
+
 @pytest.mark.parametrize("mag", [1.0, 2.0 ** -30])
 @pytest.mark.parametrize("case", ODD, ids=lambda c: f"d{c[0]}rd{c[1]}p{c[2]}")
 def test_append_odd_rotary_dimensions(case, mag):
