@@ -240,7 +240,9 @@ PrefillPlan plan_prefill(const na_attn_cfg *c, int batch, int total_tokens, int 
     pl.pack = (group > 1 && (paged ? group <= bm : bm % group == 0)) ? group : 1;
     if (batch == 1 && total_tokens % bm == 0)
         pl.pack = 1;
-    pl.rep = paged && (long long)max_new_len * pl.pack <= bm / kPrefillRep ? kPrefillRep : 1;
+    // (a tile holds one token at least, also where the bound is of no new tokens)
+    pl.rep = paged && std::max(max_new_len, 1) * (long long)pl.pack <= bm / kPrefillRep ? kPrefillRep
+                                                                                        : 1;
     pl.tile_tokens = bm / pl.rep / pl.pack;
     pl.q_tiles = (max_new_len + pl.tile_tokens - 1) / pl.tile_tokens;
     const long long units = (long long)batch * pl.q_tiles * (c->num_heads / pl.pack);

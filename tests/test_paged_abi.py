@@ -162,3 +162,14 @@ def test_compiled_calls_answer_none_for_what_is_not_plain(lib):
             args[at] = t
             assert f(*args) is None
             assert f(*args[:-1]) is None
+
+
+@pytest.mark.parametrize("batch", [1, 2])
+@pytest.mark.parametrize("group", [1, 32, 33, 40, 128, 130])
+def test_prefill_workspace_of_a_step_without_new_tokens(lib, group, batch):
+    """max_new_len 0, whatever the group: nothing is needed, as in the contiguous query."""
+    c = na.AttnConfig(group, 1, 64)
+    for total in (0, 1, 5):
+        for top in (0, 100, 100000):
+            assert na.na_prefill_paged_workspace_size(c, batch, total, 0, top) == 0
+            assert na.na_prefill_workspace_size(c, batch, total, 0, top) == 0
