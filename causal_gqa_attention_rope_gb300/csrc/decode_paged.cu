@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
             // O^T += V^T P^T, one 16-row block of d at a time.
             if constexpr (E4M3) {
                 const bool extreme = abs((int)v_byte - 127) > kMaxVExp;  // warp-uniform
-                const uint32_t rest = v_rest_f16x2(v_byte);
+                const uint32_t rest = v_rest_f16x2(v_byte), rest2 = v_rest_f16x2_second(v_byte);
 #pragma unroll
                 for (int s = 0; s < KS / 2; s++) {
                     uint32_t w[4], a0[4], a1[4];
@@ -649,8 +649,8 @@ __global__ void __launch_bounds__(THREADS, kCtasPerSm<E4M3>)
                     if (extreme) {
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            a0[i] = mul_f16x2(a0[i], rest);
-                            a1[i] = mul_f16x2(a1[i], rest);
+                            a0[i] = mul_f16x2(mul_f16x2(a0[i], rest), rest2);
+                            a1[i] = mul_f16x2(mul_f16x2(a1[i], rest), rest2);
                         }
                     }
                     mma_f16_16816(acc[2 * s], a0, b0, b1);

@@ -106,12 +106,30 @@ __device__ __forceinline__ int v_weight_exp(uint32_t byte)
     return min(max((int)byte - 127, -kMaxVExp), kMaxVExp);
 }
 
-// The rest 2^(e - b) as an f16 pair (1 for all but extreme pages).
-__device__ __forceinline__ uint32_t v_rest_f16x2(uint32_t byte)
+// 2^r as an f16 pair, r <= 15; 0 below f16's smallest number.
+__device__ __forceinline__ uint32_t exp2_f16x2(int r)
 {
-    const int r = min((int)byte - 127 - v_weight_exp(byte), kTopVExp - kMaxVExp);
     const uint32_t h = r >= -14 ? (uint32_t)(r + 15) << 10 : (r >= -24 ? 1u << (r + 24) : 0u);
     return h | (h << 16);
+}
+
+// The rest 2^(e - b) (1 for all but extreme pages) as two f16 pairs to multiply by
+// in turn, since it passes f16's range before the values do: the first keeps every
+// E4M3 value exact (2^-9 * 2^-15 is f16's last place), the second, 1 but for pages
+// below 2^(-kMaxVExp - 15), rounds once.
+__device__ __forceinline__ int v_rest_exp(uint32_t byte)
+{
+    return min((int)byte - 127 - v_weight_exp(byte), kTopVExp - kMaxVExp);
+}
+
+__device__ __forceinline__ uint32_t v_rest_f16x2(uint32_t byte)
+{
+    return exp2_f16x2(max(v_rest_exp(byte), -15));
+}
+
+__device__ __forceinline__ uint32_t v_rest_f16x2_second(uint32_t byte)
+{
+    return exp2_f16x2(min(v_rest_exp(byte) + 15, 0));
 }
 
 // 2^x for an integer |x| <= 126.

@@ -236,10 +236,11 @@ __device__ __forceinline__ void convert_rows(const uint8_t *raw, const uint8_t *
         e4m3x4_to_f16(u[i].w, o[6], o[7]);
         if constexpr (EDGE) {
             const uint32_t rest = v_rest_f16x2(scale[r >> 4]);
+            const uint32_t rest2 = v_rest_f16x2_second(scale[r >> 4]);
             const bool seen = r >= lo && r < hi;
 #pragma unroll
             for (int q = 0; q < 8; q++)
-                o[q] = seen ? mul_f16x2(o[q], rest) : 0u;
+                o[q] = seen ? mul_f16x2(mul_f16x2(o[q], rest), rest2) : 0u;
         }
         uint8_t *row = out + r * 128;
         *reinterpret_cast<uint4 *>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);

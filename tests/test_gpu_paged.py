@@ -473,6 +473,29 @@ def test_v_scale_above_the_largest_is_reported():
     assert run_prefill(cfg, q, cache.to(DEV), [39], [1])[1] == na.NA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("e", [-73, -66, -65, -64, -63, -56, -55, -54, -49])
+@pytest.mark.parametrize("call", ["decode", "prefill"])
+def test_v_scales_around_the_last_multiple(call, e, d, page):
+    """Scales 2^e of V where E4M3 values reach the multiples of 2^-64 that they are rounded
+    to (the largest value is 2^(e + 8.8)): page scales of one sequence lie around e."""
+    lens, KV = [300, 45], 2
+    cache = make_paged(lens, KV, d, page, "e4m3", 33)
+    live = cache.v_scale != 255
+    mid = int(cache.v_scale[live].int().median())
+    cache.v_scale[live] = (cache.v_scale[live].int() - mid + e + 127).to(torch.uint8)
+    g = torch.Generator().manual_seed(34)
+    cfg = na.AttnConfig(2 * KV, KV, d)
+    q = rnd(g, 2, 2 * KV, d)
+    if call == "decode":
+        out, _, status = run_decode(cfg, q, cache.to(DEV), lens)
+    else:
+        out, status = run_prefill(cfg, q, cache.to(DEV), [n - 1 for n in lens], [1, 1])
+    assert status == 0
+    ref = attend(cache, q, [(0, 299, 1), (1, 44, 1)])
+    check(out, ref.out, ref.tol, "out")
+
+
 @pytest.mark.parametrize("call", ["decode", "prefill"])
 def test_pages_of_zeros(call):
     """Pages whose K or V is all zero have scale byte 0 (2^-127): they still weigh in
