@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "na_internal.cuh"
@@ -210,6 +211,7 @@ int check_paged_cache(const na_attn_cfg *cfg, const na_paged_kv_cache *c, int ba
 }
 
 struct PrefillPlan {
+    bool fits;  // the units can be counted and launched
     int pack, rep, tile_tokens, q_tiles, full_units, tail_units, num_splits, split_len, grid;
     size_t ws_bytes;
 };
@@ -244,9 +246,15 @@ PrefillPlan plan_prefill(const na_attn_cfg *c, int batch, int total_tokens, int 
     pl.rep = paged && std::max(max_new_len, 1) * (long long)pl.pack <= bm / kPrefillRep ? kPrefillRep
                                                                                         : 1;
     pl.tile_tokens = bm / pl.rep / pl.pack;
-    pl.q_tiles = (max_new_len + pl.tile_tokens - 1) / pl.tile_tokens;
-    const long long units = (long long)batch * pl.q_tiles * (c->num_heads / pl.pack);
+    pl.q_tiles = (int)(((long long)max_new_len + pl.tile_tokens - 1) / pl.tile_tokens);
+    const long long per_tile = (long long)batch * (c->num_heads / pl.pack);
     const long long sms = sm_count();
+    // (the grid exceeds the units by the pieces of the cut ones, fewer than the SMs; a
+    // bound that is far too loose ends here instead of in a grid cut off to 32 bits)
+    pl.fits = per_tile <= INT_MAX && per_tile * pl.q_tiles <= INT_MAX - sms;
+    if (!pl.fits)
+        return pl;
+    const long long units = per_tile * pl.q_tiles;
     // With ragged lengths the unit count is only a bound (the shortest
     // sequences' trailing units are empty), so the leftover units after the
     // last whole wave are known to be real only when every sequence has
@@ -535,8 +543,9 @@ int na_prefill_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t tot
         return rc;
     if (!bytes || batch <= 0 || total_tokens < 0 || max_new_len < 0 || max_total_len < 0)
         return NA_ERR_INVALID_ARG;
-    *bytes = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len).ws_bytes;
-    return NA_OK;
+    const PrefillPlan pl = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len);
+    *bytes = pl.ws_bytes;
+    return pl.fits ? NA_OK : NA_ERR_UNSUPPORTED;
 }
 
 int na_attn_prefill_chunk(const na_attn_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
@@ -575,6 +584,8 @@ int na_attn_prefill_chunk(const na_attn_cfg *cfg, int32_t batch, const int32_t *
     if (gated && (!gate || !aligned16(gate)))
         return NA_ERR_INVALID_ARG;
     const PrefillPlan pl = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len);
+    if (!pl.fits)
+        return NA_ERR_UNSUPPORTED;
     if (pl.ws_bytes > 0 && (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace)))
         return NA_ERR_WORKSPACE;
 
@@ -622,6 +633,8 @@ int na_attn_prefill_chunk_paged(const na_attn_cfg *cfg, int32_t batch, const int
     if ((cfg->flags & NA_OUT_GATE) && (!gate || !aligned16(gate)))
         return NA_ERR_INVALID_ARG;
     const PrefillPlan pl = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len, true);
+    if (!pl.fits)
+        return NA_ERR_UNSUPPORTED;
     if (pl.ws_bytes > 0 && (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace)))
         return NA_ERR_WORKSPACE;
     PrefillParams p = prefill_params(cfg, pl, batch, cu_seqlens, cache_lens, total_tokens,
@@ -733,8 +746,9 @@ int na_prefill_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32
         return rc;
     if (!bytes || batch <= 0 || total_tokens < 0 || max_new_len < 0 || max_total_len < 0)
         return NA_ERR_INVALID_ARG;
-    *bytes = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len, true).ws_bytes;
-    return NA_OK;
+    const PrefillPlan pl = plan_prefill(cfg, batch, total_tokens, max_new_len, max_total_len, true);
+    *bytes = pl.ws_bytes;
+    return pl.fits ? NA_OK : NA_ERR_UNSUPPORTED;
 }
 
 int na_decode_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_kv_len,

@@ -220,9 +220,11 @@ int na_rope_append_kv(const na_attn_cfg *cfg, const na_rope_params *rope, int32_
  *                 reaches max_total_len or the capacity (those rows are not written).
  * Errors (before anything is enqueued): NA_ERR_INVALID_ARG for null or misaligned
  * buffers and negative sizes, NA_ERR_UNSUPPORTED for a ring whose capacity is not
- * a multiple of 128 or a cache of more than 2^31 - 1 rows (batch x kv heads x
- * capacity), NA_ERR_CAPACITY when the ring cannot hold a window plus a chunk,
- * NA_ERR_WORKSPACE for a missing or short workspace.
+ * a multiple of 128, a cache of more than 2^31 - 1 rows (batch x kv heads x
+ * capacity) or bounds so loose that the tiles of query rows (batch x heads x
+ * max_new_len / rows of a tile) do not fit a grid, NA_ERR_CAPACITY when the ring
+ * cannot hold a window plus a chunk, NA_ERR_WORKSPACE for a missing or short
+ * workspace.
  */
 int na_attn_prefill_chunk(const na_attn_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
                           const int32_t *cache_lens, int32_t total_tokens, int32_t max_new_len,

@@ -173,3 +173,21 @@ def test_prefill_workspace_of_a_step_without_new_tokens(lib, group, batch):
         for top in (0, 100, 100000):
             assert na.na_prefill_paged_workspace_size(c, batch, total, 0, top) == 0
             assert na.na_prefill_workspace_size(c, batch, total, 0, top) == 0
+
+
+@pytest.mark.parametrize("batch,most", [(1 << 16, 1 << 20), (64, 2 ** 31 - 1), (2 ** 31 - 1, 4)])
+def test_prefill_bounds_with_too_many_units(lib, batch, most):
+    """Bounds so loose that the units (query tile, kv head, sequence) exceed a grid are refused by
+    the queries and the calls, over pages and not."""
+    c, out = cfg(), ctypes.c_size_t(0)
+    for query in (lib.na_prefill_paged_workspace_size, lib.na_prefill_workspace_size):
+        assert query(ctypes.byref(c), batch, 8, most, 512, ctypes.byref(out)) == na.NA_ERR_UNSUPPORTED
+    assert prefill(lib, c, paged(batch=batch), batch=batch, most=most) == na.NA_ERR_UNSUPPORTED
+    flat = na.na_kv_cache(16, 16, 64, 512)
+    if batch <= 64:  # (a contiguous cache has the rows of its batch)
+        assert lib.na_attn_prefill_chunk(ctypes.byref(c), batch, 16, 16, 8, most, 512, 16,
+                                         ctypes.byref(flat), None, 16, 16, 1 << 30, None,
+                                         None) == na.NA_ERR_UNSUPPORTED
+    # loose, but countable
+    for query in (lib.na_prefill_paged_workspace_size, lib.na_prefill_workspace_size):
+        assert query(ctypes.byref(c), 1, 8, 2 ** 31 - 1, 512, ctypes.byref(out)) == na.NA_OK
