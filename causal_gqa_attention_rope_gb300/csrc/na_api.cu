@@ -295,6 +295,7 @@ PrefillPlan plan_prefill(const na_attn_cfg *c, int batch, int total_tokens, int 
 }
 
 struct DecodePlan {
+    bool fits;  // the pieces can be counted
     int heads_per_cta, grid, min_slice, max_pieces, streams;
     size_t ws_bytes;
 };
@@ -318,12 +319,16 @@ DecodePlan plan_decode(const na_attn_cfg *c, int batch, int max_kv_len, int num_
         for (pl.heads_per_cta = 8; group % pl.heads_per_cta != 0;)
             pl.heads_per_cta--;
     const int len = max_kv_len > 0 ? max_kv_len : 1;
-    int min_slice = num_splits > 0 ? (len + num_splits - 1) / num_splits : 4 * tile;
+    int min_slice = num_splits > 0 ? (int)(((long long)len + num_splits - 1) / num_splits) : 4 * tile;
     if (min_slice < 1)
         min_slice = 1;
     pl.min_slice = min_slice;
     pl.grid = (paged_ctas_per_sm ? paged_ctas_per_sm : decode_ctas_per_sm()) * sm_count();
-    pl.streams = batch * c->num_kv_heads * (group / pl.heads_per_cta);
+    const long long streams = (long long)batch * (c->num_heads / pl.heads_per_cta);
+    pl.fits = streams <= INT_MAX - pl.grid;
+    if (!pl.fits)
+        return pl;
+    pl.streams = (int)streams;
     pl.max_pieces = pl.streams + pl.grid;
     const size_t rows = (size_t)pl.max_pieces * pl.heads_per_cta;
     pl.ws_bytes = rows * (c->head_dim + 2) * 4 + (size_t)pl.streams * 2 * 4;
@@ -689,8 +694,9 @@ int na_decode_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_
         return rc;
     if (!bytes || batch <= 0 || max_kv_len < 0 || num_splits < 0)
         return NA_ERR_INVALID_ARG;
-    *bytes = plan_decode(cfg, batch, max_kv_len, num_splits).ws_bytes;
-    return NA_OK;
+    const DecodePlan pl = plan_decode(cfg, batch, max_kv_len, num_splits);
+    *bytes = pl.ws_bytes;
+    return pl.fits ? NA_OK : NA_ERR_UNSUPPORTED;
 }
 
 int na_attn_decode(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
@@ -721,6 +727,8 @@ int na_attn_decode(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
     if (gated && !gate)
         return NA_ERR_INVALID_ARG;
     const DecodePlan pl = plan_decode(cfg, batch, max_kv_len, num_splits);
+    if (!pl.fits)
+        return NA_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace))
         return NA_ERR_WORKSPACE;
 
@@ -761,8 +769,9 @@ int na_decode_paged_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_
         return NA_ERR_INVALID_ARG;
     // for either page type
     const int ctas = std::max(decode_paged_ctas_per_sm(false), decode_paged_ctas_per_sm(true));
-    *bytes = plan_decode(cfg, batch, max_kv_len, num_splits, ctas).ws_bytes;
-    return NA_OK;
+    const DecodePlan pl = plan_decode(cfg, batch, max_kv_len, num_splits, ctas);
+    *bytes = pl.ws_bytes;
+    return pl.fits ? NA_OK : NA_ERR_UNSUPPORTED;
 }
 
 int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
@@ -789,6 +798,8 @@ int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_ro
         return NA_ERR_INVALID_ARG;
     const DecodePlan pl =
         plan_decode(cfg, batch, max_kv_len, num_splits, decode_paged_ctas_per_sm(e4m3));
+    if (!pl.fits)
+        return NA_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace))
         return NA_ERR_WORKSPACE;
     DecodeParams p = decode_params(cfg, pl, batch, q_rot, kv_lens, max_kv_len, gate, out, probs,

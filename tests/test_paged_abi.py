@@ -191,3 +191,18 @@ def test_prefill_bounds_with_too_many_units(lib, batch, most):
     # loose, but countable
     for query in (lib.na_prefill_paged_workspace_size, lib.na_prefill_workspace_size):
         assert query(ctypes.byref(c), 1, 8, 2 ** 31 - 1, 512, ctypes.byref(out)) == na.NA_OK
+
+
+@pytest.mark.parametrize("batch", [1 << 28, 1 << 29, 2 ** 31 - 1])
+def test_decode_batches_with_too_many_streams(lib, batch):
+    """The workspace holds partial results of every stream (sequence, kv head): a batch whose streams
+    pass 32 bits is refused, not sized by what is left of their number."""
+    c, out = cfg(), ctypes.c_size_t(0)
+    for query in (lib.na_decode_paged_workspace_size, lib.na_decode_workspace_size):
+        assert query(ctypes.byref(c), batch, 512, 0, ctypes.byref(out)) == na.NA_ERR_UNSUPPORTED
+        assert query(ctypes.byref(c), 1 << 27, 512, 0, ctypes.byref(out)) == na.NA_OK
+        assert out.value > (1 << 27) * 32 * 128 * 4
+        small = out.value
+        assert query(ctypes.byref(c), 1 << 27, 512, 2 ** 31 - 1, ctypes.byref(out)) == na.NA_OK
+        assert out.value == small
+    assert decode(lib, c, paged(batch=batch), batch=batch) == na.NA_ERR_UNSUPPORTED
