@@ -4,7 +4,9 @@ Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked into
 one shared library with a C ABI (``include/na.h``).  ``csrc/paged_calls.cpp``,
 compiled meanwhile with the host compiler against torch's headers, becomes the
 extension module ``_paged_calls``.  Both outputs sit beside this file so the
-Python binding finds them without installation.
+Python binding finds them without installation.  ``libna.so`` needs neither
+torch nor Python and is linked whatever becomes of the extension module, which
+is left out, with a warning, where torch or a header that it needs is missing.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -43,17 +46,36 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_calls(cuda: str) -> str:
-    """Compile (if stale) and return the path of the extension module _paged_calls."""
+def _calls_missing(torch, include) -> str:
+    """What the extension module needs and this machine has not, or ''."""
+    if torch is None:
+        return "torch"
+    for path in (os.path.join(include, "Python.h"),
+                 os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h"),
+                 os.path.join(torch, "lib", "libc10_cuda.so")):
+        if not os.path.exists(path):
+            return path
+    return ""
+
+
+def build_calls(cuda: str) -> str | None:
+    """Compile (if stale) and return the path of the extension module _paged_calls; None, with a
+    warning, where something that it needs is missing."""
     src = os.path.join(CSRC, "paged_calls.cpp")
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    spec = importlib.util.find_spec("torch")
+    torch = list(spec.submodule_search_locations)[0] if spec else None
+    include = sysconfig.get_paths()["include"]
+    missing = _calls_missing(torch, include)
+    if missing:
+        warnings.warn(f"the paged calls (csrc/paged_calls.cpp) are not built: {missing} is missing")
+        return None
     deps = [src, __file__, os.path.join(INCLUDE, "na.h"), os.path.join(torch, "version.py")]
     if _stale(CALLS, deps):
         tmp = CALLS + f".tmp{os.getpid()}"
         cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o",
                tmp, "-I", INCLUDE, "-I", os.path.join(torch, "include"), "-I",
-               os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], "-L",
-               os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+               os.path.join(cuda, "include"), "-I", include, "-L", os.path.join(torch, "lib"),
+               "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"compiling {src} failed:\n{res.stderr}")
@@ -85,7 +107,6 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
         calls = ex.submit(build_calls, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
         objs = list(ex.map(compile_one, sources))
-        calls.result()
     if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs
@@ -93,6 +114,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp, LIB)
+    calls.result()  # an error of its compiler is raised with the library in place
     return LIB
 
 
