@@ -329,12 +329,15 @@ def _calls():
     global _native
     if _native is None:
         lib = load_library()
-        import torch  # noqa: F401  (its libraries have to be there first)
+        import torch  # its libraries have to be there first
+        how = "run __graft_entry__.build() or python -m causal_gqa_attention_rope_gb300._build"
         try:
             from . import _paged_calls as calls
         except ImportError as e:
-            raise RuntimeError("the paged calls are not built; run __graft_entry__.build() or "
-                               "python -m causal_gqa_attention_rope_gb300._build") from e
+            raise RuntimeError(f"the paged calls are not built; {how}") from e
+        here = f"{torch.__version__} {torch.version.git_version}"
+        if getattr(calls, "torch", "") != here:  # it reads tensors through that torch's layout
+            raise RuntimeError(f"the paged calls were built for another torch than {here}; {how}")
         calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                      for f in (lib.na_rope_append_kv_paged, lib.na_attn_prefill_chunk_paged,
                                lib.na_attn_decode_paged)), AttnConfig, RopeConfig, PagedKVCache)

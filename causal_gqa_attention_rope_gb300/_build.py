@@ -14,6 +14,7 @@ import concurrent.futures
 import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sysconfig
@@ -25,7 +26,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libna.so")
-CALLS = os.path.join(PKG, "_paged_calls.so")
+# named for the Python whose ABI it has: another one does not take it for its own
+CALLS = os.path.join(PKG, "_paged_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
+# the torch that it was compiled against, whose classes it reads through inline code
+BUILT_FOR = os.path.join(BUILD, "paged_calls.torch")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -44,6 +48,19 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _torch_identity(torch) -> str:
+    """Version and commit of the torch in directory `torch`, without importing it."""
+    v = runpy.run_path(os.path.join(torch, "version.py"))
+    return f"{v['__version__']} {v['git_version']}"
+
+
+def _built_for() -> str:
+    if not os.path.exists(BUILT_FOR):
+        return ""
+    with open(BUILT_FOR) as f:
+        return f.read()
 
 
 def _calls_missing(torch, include) -> str:
@@ -69,17 +86,20 @@ def build_calls(cuda: str) -> str | None:
     if missing:
         warnings.warn(f"the paged calls (csrc/paged_calls.cpp) are not built: {missing} is missing")
         return None
-    deps = [src, __file__, os.path.join(INCLUDE, "na.h"), os.path.join(torch, "version.py")]
-    if _stale(CALLS, deps):
+    identity = _torch_identity(torch)
+    # (file times do not tell one torch from another: an older one may be installed later)
+    if _stale(CALLS, [src, __file__, os.path.join(INCLUDE, "na.h")]) or _built_for() != identity:
         tmp = CALLS + f".tmp{os.getpid()}"
         cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o",
-               tmp, "-I", INCLUDE, "-I", os.path.join(torch, "include"), "-I",
+               tmp, f'-DNA_TORCH="{identity}"', "-I", INCLUDE, "-I", os.path.join(torch, "include"), "-I",
                os.path.join(cuda, "include"), "-I", include, "-L", os.path.join(torch, "lib"),
                "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"compiling {src} failed:\n{res.stderr}")
         os.replace(tmp, CALLS)
+        with open(BUILT_FOR, "w") as f:
+            f.write(identity)
     return CALLS
 
 

@@ -402,5 +402,9 @@ PyMODINIT_FUNC PyInit__paged_calls()
         return nullptr;
     NAMES(INTERN)
 #undef INTERN
-    return PyModule_Create(&kModule);
+    PyObject *m = PyModule_Create(&kModule);
+    // the torch it reads tensors of (NA_TORCH: version and commit, by the build)
+    if (m && PyModule_AddStringConstant(m, "torch", NA_TORCH) < 0)
+        Py_CLEAR(m);
+    return m;
 }

@@ -1,10 +1,13 @@
 """What the build leaves where parts of its surroundings are missing (no GPU needed)."""
 import ctypes
 import os
+import sysconfig
 import types
 
 import pytest
+import torch
 
+import causal_gqa_attention_rope_gb300 as na
 from causal_gqa_attention_rope_gb300 import _build
 
 
@@ -46,3 +49,33 @@ def test_library_with_a_compiler_that_fails(outputs, monkeypatch):
     with pytest.raises(RuntimeError, match="paged_calls"):
         _build.build()
     check_library(outputs)
+
+
+def test_another_torch_with_older_files(monkeypatch, tmp_path):
+    """The module reads tensors through torch's inline code: with another torch installed it is
+    compiled again, whatever the times of the files."""
+    _build.build()
+    real, other = os.path.dirname(torch.__file__), tmp_path / "torch"
+    other.mkdir()
+    for part in ("include", "lib"):
+        (other / part).symlink_to(os.path.join(real, part))
+    version = other / "version.py"
+    version.write_text("__version__ = '1.0.0'\ngit_version = 'another'\n")
+    os.utime(version, (1e9, 1e9))
+    calls = types.SimpleNamespace(submodule_search_locations=[str(other)])
+    monkeypatch.setattr(_build.importlib.util, "find_spec", lambda name: calls)
+    monkeypatch.setenv("CXX", "false")
+    with pytest.raises(RuntimeError, match="paged_calls"):  # it tries to
+        _build.build()
+
+
+def test_module_of_another_torch_is_refused(monkeypatch):
+    _build.build()
+    monkeypatch.setattr(na, "_native", None)
+    monkeypatch.setattr(torch.version, "git_version", "another")
+    with pytest.raises(RuntimeError, match="another torch"):
+        na._calls()
+
+
+def test_module_is_named_for_its_python():
+    assert os.path.basename(_build.CALLS) == "_paged_calls" + sysconfig.get_config_var("EXT_SUFFIX")
