@@ -495,8 +495,7 @@ __device__ __forceinline__ void append_page_cta(const RopeAppendParams &p, const
     append_page<D, R, NT, GENERIC>(p, pg, turns, stage, slot, rest >> 1, rest & 1);
 }
 
-// The rows of TK tokens from token t0 on: P of them per thread group from row
-// slot first on (row slots run token after token).
+// Where a token's rows go.
 struct RowPlace {
     int pos;        // < 0: the token is skipped
     int id, slot;   // bf16 pages: its page and slot there
@@ -527,6 +526,8 @@ __device__ __forceinline__ void rotate_exact2(float2 a0, float2 a1, float4 c, fl
     }
 }
 
+// The rows of TK tokens from token t0 on: P of them per thread group from row
+// slot first on (row slots run token after token).
 template <int D, int NT, int P, int TK, bool E4M3, bool GENERIC>
 __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const PagedView &pg,
                                             const RopeTurns &turns, RowStage<D, NT> *stage, int t0,
@@ -539,9 +540,12 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
     const int H = p.H, KV = E4M3 ? 0 : p.KV, rows = H + 2 * KV;
     const int half = p.rd / 2, lane = threadIdx.x & 31;
     const int k = threadIdx.x % UPR;
-    const bool qk_norm = (p.flags & NA_QK_NORM) != 0;
+    // GENERIC rows of bf16 pages come without norms (launch_rope_append_paged sends those
+    // with norms to the staged kernel)
+    constexpr bool NORMS = !GENERIC || E4M3;
+    const bool qk_norm = NORMS && (p.flags & NA_QK_NORM) != 0;
     const bool zero_centered = (p.flags & NA_QK_NORM_ZERO_CENTERED) != 0;
-    const bool v_norm = !E4M3 && (p.flags & NA_V_NORM) != 0;
+    const bool v_norm = NORMS && !E4M3 && (p.flags & NA_V_NORM) != 0;
     const int ntok = min(TK, p.total_tokens - t0);
     const bool rot = GENERIC ? 8 * k < half : k < p.rd / 16;
     // 16-byte chunks of a unit: of a rotated row, and of a V row
@@ -672,9 +676,9 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
                     bf16x8_to_f32(__ldg(w + qb), wb);
                 }
             }
-            // (GENERIC bf16 rows take this way too, without weights: it has the bits of the
-            // contiguous call's staged rows)
-            if ((qk_norm && zero_centered) || (GENERIC && !E4M3)) {
+            // (rows that never have norms take this way too, without weights: it has the bits
+            // of the contiguous call's staged rows)
+            if ((qk_norm && zero_centered) || !NORMS) {
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
                     F2 x0{a[e], 0.f}, x1{c[e], 0.f};
