@@ -15,9 +15,10 @@
 // E4M3 pages.  A page's scale is 2^e with the smallest e such that max |x| <=
 // 448 * 2^e over its tokens (448 is E4M3's largest value), so it is known only
 // when all of the page's tokens are: one CTA takes one page that the call
-// touches, one kv head, and K or V.  Its threads hold the page's new rows in
-// registers -- normed and rotated in fp32, 16 elements of a row per thread --
-// agree on the largest magnitude, and round once to E4M3.  When the page holds
+// touches, one kv head, and K or V.  Its threads norm and rotate the page's new
+// rows in fp32, 16 elements of a row per thread, leave them in shared memory, agree
+// on the largest magnitude, and round once to E4M3.  (In a call of a token or two
+// per sequence a warp does this, its rows in registers.)  When the page holds
 // earlier tokens of the sequence its scale never shrinks, and when it grows
 // those tokens are rounded to the new one: a power of two, so only values that
 // leave E4M3's normal range (2^-15 of the page's largest, and below) change.
@@ -753,6 +754,10 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams &p, const Pag
 
 // Page CTAs first (E4M3): theirs is the longer chain of dependent loads.
 // FEW: a warp each.
+// 768 threads per SM hold a thread to 80 registers, where the instances with most to
+// hold spill (-Xptxas -v, bytes of stores / loads): R = 4 page rows 52 / 172 with
+// P = 2 row units, 72 / 184 with four; P = 4 alone 16 / 20 to 24 / 28; a warp per page
+// 64 / 72; GENERIC up to 20 / 68; R and P up to two, and bf16 pages up to P = 2, none.
 template <int D, bool E4M3, int R, int NT, int P, bool GENERIC, bool FEW>
 __global__ void __launch_bounds__(NT, 768 / NT) append_paged_kernel(const RopeAppendParams p,
                                                           const PagedView pg, const RopeTurns turns,
@@ -822,7 +827,9 @@ cudaError_t launch_fused(const RopeAppendParams &p, const PagedView &pg, const R
 // rows of a CTA's tokens come out even, else 2.  (16 sequences of 1 .. 512 tokens, 32
 // query heads, E4M3 pages of 16: 23.8 us at 2, 22.0 at 4; 2048 tokens of 40 heads,
 // where 4 leaves three of eight slots empty: 18.5 at 2, 20.9 at 4.)
-// E4M3 pages of a call of two tokens per sequence or fewer get a warp each.
+// E4M3 pages of a call of two tokens per sequence or fewer, on the average, get a
+// warp each (what the host knows of the lengths; a long sequence among many without
+// new tokens is right but walks its pages by single warps, twice).
 template <int D, bool E4M3, int R, int NT>
 cudaError_t launch_p(const RopeAppendParams &p, const PagedView &pg, const RopeTurns &turns,
                      cudaStream_t stream)

@@ -300,7 +300,8 @@ struct DecodePlan {
     size_t ws_bytes;
 };
 
-// Decode split plan.  The split pass runs a fixed grid (two CTAs per SM) and
+// Decode split plan.  The split pass runs a fixed grid (two CTAs per SM, three
+// over E4M3 pages) and
 // cuts the concatenated key streams into one equal slice per CTA (at least
 // min_slice keys), so the workspace holds one partial row group per piece:
 // streams + grid pieces at most, whatever the lengths.

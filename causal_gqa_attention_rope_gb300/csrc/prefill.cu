@@ -99,7 +99,7 @@ constexpr int cta_threads(bool e4m3, int rep)
     return THREADS + (e4m3 ? 128 : 0) + (e4m3 && rep == 1 ? 128 : 0);
 }
 constexpr int E4M3_K_STAGES = 4;  // K tiles in bytes
-constexpr int E4M3_V_STAGES = 2;  // bf16 V tiles behind a raw ring ...
+constexpr int E4M3_V_STAGES = 2;  // f16 V tiles behind a raw ring ...
 constexpr int RAW_STAGES = 3;     // ... of this many in bytes
 constexpr int SCALE_SLOTS = 8;    // K scales outlive their tile until its softmax (at most 7 tiles)
 constexpr uint32_t TMEM_COLS = 512;

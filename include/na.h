@@ -366,14 +366,17 @@ int na_rope_append_kv_paged(const na_attn_cfg *cfg, const na_rope_params *rope, 
 
 /*
  * na_attn_decode over a paged cache: one query per sequence, the same arithmetic
- * (E4M3 values are f16 numbers exactly, and so, but for elements below 2^-33 of
- * its largest, is a query scaled by a power of two; K's scale is applied to the
- * scores in fp32, V's in the exponent of the weights, which are rounded to f16),
- * the same outputs and probabilities.
+ * (E4M3 values are f16 numbers exactly; so is a query scaled by a power of two, for
+ * elements down to 2^-26 of its largest, and within 2^-33 of that below; K's scale is
+ * applied to the scores in fp32, V's in the exponent of the weights, which are
+ * rounded to f16), the same outputs and probabilities.
  *
  *   max_kv_len  HOST upper bound of kv_lens; <= pages_per_seq * page_size.
- *   num_splits, workspace, probs, gate, status: as in na_attn_decode, with
- *               na_decode_paged_workspace_size() bytes of workspace.
+ *   num_splits, workspace, probs, gate, status: as in na_attn_decode (the split
+ *               pass has three CTAs per SM over E4M3 pages), with
+ *               na_decode_paged_workspace_size() bytes of workspace.  With
+ *               num_splits 0 sequences of few keys are not cut over the grid: up to
+ *               8 CTAs share a sequence's kv head, without partial results.
  */
 int na_attn_decode_paged(const na_attn_cfg *cfg, int32_t batch, const void *q_rot,
                          const na_paged_kv_cache *cache, const int32_t *kv_lens,
@@ -419,9 +422,11 @@ int na_decode_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_
 
 /*
  * Self-test of the device-side failure detection (an addition of this
- * library).  Every wait inside the library's kernels gives up after about a
- * second (2^31 SM cycles) and writes NA_ERR_DEVICE_TIMEOUT into the caller's
- * status word instead of hanging.  This call runs that same bounded wait, in a
+ * library).  Every wait of the library's kernels for a copy or a tensor-core
+ * operation gives up after about a second (2^31 SM cycles) and writes
+ * NA_ERR_DEVICE_TIMEOUT into the caller's status word instead of hanging.  (The
+ * CTAs of a cluster in na_attn_decode_paged also meet in hardware barriers, which
+ * every thread reaches whatever its own waits said.)  This call runs that same bounded wait, in a
  * one-CTA kernel, on a barrier that nothing ever completes: after about a
  * second *status holds NA_ERR_DEVICE_TIMEOUT (unless it already held an error),
  * the kernel returns normally and the context stays usable.
