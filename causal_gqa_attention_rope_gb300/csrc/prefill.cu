@@ -80,6 +80,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <mutex>
+#include <type_traits>
 
 #include "na_internal.cuh"
 #include "tc_primitives.cuh"
@@ -387,13 +388,12 @@ __device__ __forceinline__ void rank_sequences(const PrefillParams &p, RankScrat
     prior = __shfl_sync(0xffffffffu, f.w, 0);
 }
 
-// REP: the tile's rows fill 128 / REP lanes, REP times over (paged calls).
-template <int D, bool CAPPED, KvSource SRC, int REP = 1>
-__global__ void __launch_bounds__(cta_threads(SRC == KV_PAGED_E4M3, REP), 1)
-    prefill_tc_kernel(const PrefillParams p, const PagedView pg,
-                      const __grid_constant__ CUtensorMap map_q,
-                      const __grid_constant__ CUtensorMap map_k,
-                      const __grid_constant__ CUtensorMap map_v)
+// The work of a CTA.  REP: the tile's rows fill 128 / REP lanes, REP times over
+// (paged calls).
+template <int D, bool CAPPED, KvSource SRC, int REP>
+__device__ __forceinline__ void prefill_tile(const PrefillParams &p, const PagedView &pg,
+                                             const CUtensorMap &map_q, const CUtensorMap &map_k,
+                                             const CUtensorMap &map_v)
 {
     typedef TcSmem<D, SRC> Smem;
     constexpr int KB = D / 64;
@@ -678,269 +678,7 @@ __global__ void __launch_bounds__(cta_threads(SRC == KV_PAGED_E4M3, REP), 1)
     if (!E4M3 && warp < 4 && gated_out)  // (E4M3: the registers are needed, all load at the end)
         load_gate();
 
-    if (warp < 4) {
-        if (PAGED && warp == 0) {
-            // ------------------------------------------------ producer, pages --
-            const int page_log = pg.page_log, nbox = BN >> page_log;  // 8 .. 1 boxes of rows per tile
-            constexpr int COLS = E4M3 ? 1 : KB;
-            constexpr uint32_t BOX_ROW = E4M3 ? D : 128;
-            const int bi = lane & (nbox - 1), bc = lane / nbox;  // this lane's box: rows, columns
-            const int p_lo = vis_lo >> page_log, p_hi = (k_end - 1) >> page_log;
-            const int32_t *row = pg.table + (size_t)b * pg.pages_per_seq;
-            struct Entry {
-                int id;
-                uint32_t scales;  // K's byte | V's byte << 8
-            };
-            auto entry = [&](int i) {
-                Entry e{-1, 0x7f7fu};
-                if (i >= p_lo && i <= p_hi) {
-                    e.id = __ldcg(row + i);
-                    if ((unsigned)e.id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
-                        na_report(p.status, NA_ERR_PAGE);
-                        e.id = 0;
-                    }
-                    if constexpr (E4M3) {
-                        const size_t at = (size_t)e.id * p.KV + kvh;
-                        const uint32_t vs = __ldcg(pg.v_scale + at);
-                        if ((int)vs - 127 > kTopVExp)
-                            na_report(p.status, NA_ERR_UNSUPPORTED);
-                        e.scales = (uint32_t)__ldcg(pg.k_scale + at) | (vs << 8);
-                    }
-                }
-                return e;
-            };
-            int wb = k_begin >> page_log;  // page of lane 0's current entry
-            Entry cur = entry(wb + lane), nxt = entry(wb + 32 + lane);
-            bool ok = true;
-            auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-                const bool got = mbar_wait_bounded(bar, parity) && !aborted(&sm.abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
-                    if (lane == 0)
-                        set_abort(&sm.abort_flag, p.status);
-                    return false;
-                }
-                return true;
-            };
-            // One tile's boxes into dst, completing on bar.
-            auto load_tile = [&](const CUtensorMap *map, int id, int n, uint8_t *dst, uint64_t *bar) {
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar, n * (BOX_ROW << page_log));
-                __syncwarp();
-                if (id >= 0)
-                    load_kv(dst + bc * (BN * 128) + (bi << page_log) * BOX_ROW, map, bc * 64,
-                            (id * p.KV + kvh) << page_log, bar);
-            };
-            int k_issued = 0, v_issued = 0;
-            for (int j = 0; ok && j < n_tiles; j++) {
-                const int j0 = k_begin + j * BN;
-                if ((j0 >> page_log) - wb >= 32) {
-                    cur = nxt;
-                    wb += 32;
-                    nxt = entry(wb + 32 + lane);
-                }
-                int id = __shfl_sync(0xffffffffu, cur.id, ((j0 >> page_log) - wb + bi) & 31);
-                if (bc >= COLS)
-                    id = -1;
-                const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
-                const uint32_t scales = __shfl_sync(0xffffffffu, cur.scales,
-                                                    (((j0 + 16 * (lane & 7)) >> page_log) - wb) & 31);
-                const int ks = j % KST;
-                if (!(ok = wait_all(&sm.k_empty[ks], ((j / KST) & 1) ^ 1)))
-                    break;
-                if constexpr (E4M3) {
-                    if (lane < 8) {
-                        const int slot = j % SCALE_SLOTS, e = v_weight_exp(scales >> 8);
-                        float *mo = reinterpret_cast<float *>(&sm.mul_off[slot][lane >> 1]);
-                        mo[lane & 1] = e8m0_value(scales & 255u);
-                        mo[2 + (lane & 1)] = (float)e;
-                        reinterpret_cast<float *>(&sm.v_inv[slot][lane >> 1])[lane & 1] = exp2i(-e);
-                    }
-                }
-                load_tile(&map_k, id, n, reinterpret_cast<uint8_t *>(sm.k[ks]), &sm.k_full[ks]);
-                k_issued = j + 1;
-                if constexpr (E4M3) {
-                    const int rs = j % RAW_STAGES;
-                    if (!(ok = wait_all(&sm.raw_empty[rs], ((j / RAW_STAGES) & 1) ^ 1)))
-                        break;
-                    if (lane < 8)
-                        sm.v_scale[rs][lane] = (uint8_t)(scales >> 8);
-                    load_tile(&map_v, id, n, sm.raw[rs], &sm.raw_full[rs]);
-                } else {
-                    const int vs = j % VST;
-                    if (!(ok = wait_all(&sm.v_empty[vs], ((j / VST) & 1) ^ 1)))
-                        break;
-                    load_tile(&map_v, id, n, reinterpret_cast<uint8_t *>(sm.v[vs]), &sm.v_full[vs]);
-                }
-                v_issued = j + 1;
-            }
-            // every copy issued lands before the CTA can exit
-            if (lane == 0) {
-                drain_wait(&sm.q_full, 0, p.status);
-                for (int j = k_issued - 1; j >= 0 && j >= k_issued - KST; j--)
-                    drain_wait(&sm.k_full[j % KST], (j / KST) & 1, p.status);
-                constexpr int VR = E4M3 ? RAW_STAGES : VST;
-                for (int j = v_issued - 1; j >= 0 && j >= v_issued - VR; j--) {
-                    uint64_t *bar;
-                    if constexpr (E4M3)
-                        bar = &sm.raw_full[j % VR];
-                    else
-                        bar = &sm.v_full[j % VR];
-                    drain_wait(bar, (j / VR) & 1, p.status);
-                }
-            }
-        } else if (warp == 0) {
-            // ------------------------------------------------------ producer --
-            if constexpr (!PAGED) {
-                if (lane == 0) {
-                    int issued = pre;
-                    for (int j = pre; j < n_tiles; j++) {
-                        const int st = j % STAGES;
-                        const uint32_t par = ((j / STAGES) & 1) ^ 1;
-                        if (!mbar_wait_bounded(&sm.k_empty[st], par) || aborted(&sm.abort_flag)) {
-                            set_abort(&sm.abort_flag, p.status);
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&sm.k_full[st], KB * BN * 128);
-                        for (int kb = 0; kb < KB; kb++)
-                            load_kv(sm.k[st][kb], &map_k, kb * 64, tile_row(j), &sm.k_full[st]);
-                        if (!mbar_wait_bounded(&sm.v_empty[st], par) || aborted(&sm.abort_flag)) {
-                            set_abort(&sm.abort_flag, p.status);
-                            drain_wait(&sm.k_full[st], (j / STAGES) & 1, p.status);
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&sm.v_full[st], KB * BN * 128);
-                        for (int kb = 0; kb < KB; kb++)
-                            load_kv(sm.v[st][kb], &map_v, kb * 64, tile_row(j), &sm.v_full[st]);
-                        issued = j + 1;
-                    }
-                    // every copy issued lands before the CTA can exit
-                    drain_wait(&sm.q_full, 0, p.status);
-                    for (int j = issued - 1; j >= 0 && j >= issued - STAGES; j--) {
-                        drain_wait(&sm.k_full[j % STAGES], (j / STAGES) & 1, p.status);
-                        drain_wait(&sm.v_full[j % STAGES], (j / STAGES) & 1, p.status);
-                    }
-                }
-            }
-        } else if (warp == 1) {
-            // ---------------------------------------------------- S = Q K^T issue --
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = E4M3 ? tc::idesc_e4m3_f32(BM, BN)
-                                                  : tc::idesc_bf16_f32(BM, BN, false, false);
-                // Descriptors of the Q tile and of K stage 0; a 64-wide column block
-                // (BM = BN rows of 128 B) is BLK16 16-byte units, a K stage K_STAGE16.
-                constexpr uint32_t BLK16 = (BM * 128) >> 4;
-                constexpr uint32_t K_STAGE16 = (E4M3 ? BN * D : KB * BN * 128) >> 4;
-                constexpr uint32_t Q_PART16 = (BM * D) >> 4;  // from the high to the low part (E4M3)
-                static_assert(BM == BN, "one column-block stride for Q and K");
-                uint64_t qd0, kd0;
-                bool ok;
-                if constexpr (E4M3) {
-                    qd0 = tc::desc_kmajor_bytes<D>(smem_addr(sm.q8[0]));
-                    kd0 = tc::desc_kmajor_bytes<D>(smem_addr(sm.k[0]));
-                    ok = mbar_wait_bounded(&sm.q_split, 0);
-                } else {
-                    qd0 = tc::desc_kmajor_sw128(smem_addr(sm.q[0]));
-                    kd0 = tc::desc_kmajor_sw128(smem_addr(sm.k[0][0]));
-                    ok = mbar_wait_bounded(&sm.q_full, 0);
-                }
-                bool any = false;
-                for (int j = 0; ok && j < n_tiles; j++) {
-                    const int st = j % KST, sb = j % NUM_S;
-                    ok = mbar_wait_bounded(&sm.k_full[st], (j / KST) & 1);
-                    if (ok && j >= NUM_S)
-                        ok = mbar_wait_bounded(&sm.s_free[sb], ((j / NUM_S) - 1) & 1);
-                    if (!ok || aborted(&sm.abort_flag))
-                        break;
-                    tc::fence_after_sync();
-                    const uint32_t s_t = tmem + S_COL0 * (sb + 1);
-                    const uint64_t kd = kd0 + (uint64_t)(st * K_STAGE16);
-                    if constexpr (E4M3) {
-#pragma unroll
-                        for (int k = 0; k < D / 32; k++)  // 32 bytes of d per step
-                            tc::mma_ss_bytes(s_t, qd0 + k * 2, kd + k * 2, idesc_s, k > 0);
-#pragma unroll
-                        for (int k = 0; k < D / 32; k++)
-                            tc::mma_ss_bytes(s_t, qd0 + Q_PART16 + k * 2, kd + k * 2, idesc_s, true);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < D / 16; k++) {  // descriptor start addresses advance in 16-byte units
-                            const uint32_t off = (k >> 2) * BLK16 + (k & 3) * 2;
-                            tc::mma_ss(s_t, qd0 + off, kd + off, idesc_s, k > 0);
-                        }
-                    }
-                    tc::mma_commit(&sm.s_full[sb]);
-                    tc::mma_commit(&sm.k_empty[st]);
-                    any = true;
-                }
-                if (!ok)
-                    set_abort(&sm.abort_flag, p.status);
-                if (any) {  // all issued MMAs complete before tensor memory is released
-                    tc::mma_commit(&sm.drain[0]);
-                    drain_wait(&sm.drain[0], 0, p.status);
-                }
-            }
-        } else if (warp == 2) {
-            // --------------------------------------------------- O += P V issue --
-            if (lane == 0) {
-                constexpr uint32_t idesc_o = E4M3 ? tc::idesc_f16_f32(BM, D, false, true)
-                                                  : tc::idesc_bf16_f32(BM, D, false, true);
-                constexpr uint32_t V_STAGE16 = (KB * BN * 128) >> 4;  // a V stage in 16-byte units
-                const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_addr(sm.v[0][0]), BN * 128);
-                bool ok = true, any = false;
-                for (int j = 0; ok && j < n_tiles; j++) {
-                    const int st = j % VST, sb = j % NUM_S;
-                    ok = mbar_wait_bounded(&sm.p_full[sb], (j / NUM_S) & 1);
-                    if (ok)
-                        ok = mbar_wait_bounded(&sm.v_full[st], (j / VST) & 1);
-                    if (!ok || aborted(&sm.abort_flag))
-                        break;
-                    tc::fence_after_sync();
-                    const uint32_t p_t = tmem + S_COL0 * (sb + 1);
-                    const uint64_t vd = vd0 + (uint64_t)(st * V_STAGE16);
-#pragma unroll
-                    for (int k = 0; k < BN / 16; k++)  // 16 keys = 16 rows of 128 B per step
-                        tc::mma_ts(tmem, p_t + k * 8, vd + (uint64_t)(k * 128), idesc_o, j > 0 || k > 0);
-                    tc::mma_commit(&sm.s_free[sb]);
-                    tc::mma_commit(&sm.v_empty[st]);
-                    tc::mma_commit(&sm.o_done[sb]);
-                    any = true;
-                }
-                if (!ok)
-                    set_abort(&sm.abort_flag, p.status);
-                if (any) {
-                    tc::mma_commit(&sm.drain[1]);
-                    drain_wait(&sm.drain[1], 0, p.status);
-                }
-            }
-        }
-    } else if (E4M3 && warp >= CONVERT0) {
-        // -------------------------------------- E4M3 V tiles to f16 tiles --
-        if constexpr (E4M3) {
-            for (int j = 0; j < n_tiles; j++) {
-                const int rs = j % RAW_STAGES, st = j % VST;
-                bool ok = warp_wait(&sm.raw_full[rs], (j / RAW_STAGES) & 1, &sm.abort_flag);
-                if (ok && j == 0)  // the first V stage holds Q until it is split
-                    ok = warp_wait(&sm.q_split, 0, &sm.abort_flag);
-                if (ok)
-                    ok = warp_wait(&sm.v_empty[st], ((j / VST) & 1) ^ 1, &sm.abort_flag);
-                if (!ok) {
-                    if (lane == 0)
-                        set_abort(&sm.abort_flag, p.status);
-                    break;
-                }
-                const int j0 = k_begin + j * BN;
-                convert_tile<D>(sm.raw[rs], sm.v_scale[rs], sm.v[st][0], warp - CONVERT0, lane,
-                                vis_lo - j0, k_end - j0);
-                tc::fence_proxy_async_smem();  // before the tensor core's reads
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.v_full[st]);
-                    mbar_arrive(&sm.raw_empty[rs]);
-                }
-            }
-        }
-    } else {
+    auto softmax = [&]() {
         // ------------------------------------------------------- softmax --
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;  // TMEM lane
@@ -1271,6 +1009,278 @@ __global__ void __launch_bounds__(cta_threads(SRC == KV_PAGED_E4M3, REP), 1)
         } else if (lane == 0) {
             set_abort(&sm.abort_flag, p.status);
         }
+    };
+    // (The order of the roles is measured, for each source its own: drafted tokens over
+    // E4M3 pages take 124.0 us so and 125.5 in the contiguous order; the other way round
+    // below.)
+    if (!PAGED || warp < 4) {
+        if (PAGED && warp == 0) {
+            // ------------------------------------------------ producer, pages --
+            const int page_log = pg.page_log, nbox = BN >> page_log;  // 8 .. 1 boxes of rows per tile
+            constexpr int COLS = E4M3 ? 1 : KB;
+            constexpr uint32_t BOX_ROW = E4M3 ? D : 128;
+            const int bi = lane & (nbox - 1), bc = lane / nbox;  // this lane's box: rows, columns
+            const int p_lo = vis_lo >> page_log, p_hi = (k_end - 1) >> page_log;
+            const int32_t *row = pg.table + (size_t)b * pg.pages_per_seq;
+            struct Entry {
+                int id;
+                uint32_t scales;  // K's byte | V's byte << 8
+            };
+            auto entry = [&](int i) {
+                Entry e{-1, 0x7f7fu};
+                if (i >= p_lo && i <= p_hi) {
+                    e.id = __ldcg(row + i);
+                    if ((unsigned)e.id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
+                        na_report(p.status, NA_ERR_PAGE);
+                        e.id = 0;
+                    }
+                    if constexpr (E4M3) {
+                        const size_t at = (size_t)e.id * p.KV + kvh;
+                        const uint32_t vs = __ldcg(pg.v_scale + at);
+                        if ((int)vs - 127 > kTopVExp)
+                            na_report(p.status, NA_ERR_UNSUPPORTED);
+                        e.scales = (uint32_t)__ldcg(pg.k_scale + at) | (vs << 8);
+                    }
+                }
+                return e;
+            };
+            int wb = k_begin >> page_log;  // page of lane 0's current entry
+            Entry cur = entry(wb + lane), nxt = entry(wb + 32 + lane);
+            bool ok = true;
+            auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+                const bool got = mbar_wait_bounded(bar, parity) && !aborted(&sm.abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    if (lane == 0)
+                        set_abort(&sm.abort_flag, p.status);
+                    return false;
+                }
+                return true;
+            };
+            // One tile's boxes into dst, completing on bar.
+            auto load_tile = [&](const CUtensorMap *map, int id, int n, uint8_t *dst, uint64_t *bar) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, n * (BOX_ROW << page_log));
+                __syncwarp();
+                if (id >= 0)
+                    load_kv(dst + bc * (BN * 128) + (bi << page_log) * BOX_ROW, map, bc * 64,
+                            (id * p.KV + kvh) << page_log, bar);
+            };
+            int k_issued = 0, v_issued = 0;
+            for (int j = 0; ok && j < n_tiles; j++) {
+                const int j0 = k_begin + j * BN;
+                if ((j0 >> page_log) - wb >= 32) {
+                    cur = nxt;
+                    wb += 32;
+                    nxt = entry(wb + 32 + lane);
+                }
+                int id = __shfl_sync(0xffffffffu, cur.id, ((j0 >> page_log) - wb + bi) & 31);
+                if (bc >= COLS)
+                    id = -1;
+                const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                const uint32_t scales = __shfl_sync(0xffffffffu, cur.scales,
+                                                    (((j0 + 16 * (lane & 7)) >> page_log) - wb) & 31);
+                const int ks = j % KST;
+                if (!(ok = wait_all(&sm.k_empty[ks], ((j / KST) & 1) ^ 1)))
+                    break;
+                if constexpr (E4M3) {
+                    if (lane < 8) {
+                        const int slot = j % SCALE_SLOTS, e = v_weight_exp(scales >> 8);
+                        float *mo = reinterpret_cast<float *>(&sm.mul_off[slot][lane >> 1]);
+                        mo[lane & 1] = e8m0_value(scales & 255u);
+                        mo[2 + (lane & 1)] = (float)e;
+                        reinterpret_cast<float *>(&sm.v_inv[slot][lane >> 1])[lane & 1] = exp2i(-e);
+                    }
+                }
+                load_tile(&map_k, id, n, reinterpret_cast<uint8_t *>(sm.k[ks]), &sm.k_full[ks]);
+                k_issued = j + 1;
+                if constexpr (E4M3) {
+                    const int rs = j % RAW_STAGES;
+                    if (!(ok = wait_all(&sm.raw_empty[rs], ((j / RAW_STAGES) & 1) ^ 1)))
+                        break;
+                    if (lane < 8)
+                        sm.v_scale[rs][lane] = (uint8_t)(scales >> 8);
+                    load_tile(&map_v, id, n, sm.raw[rs], &sm.raw_full[rs]);
+                } else {
+                    const int vs = j % VST;
+                    if (!(ok = wait_all(&sm.v_empty[vs], ((j / VST) & 1) ^ 1)))
+                        break;
+                    load_tile(&map_v, id, n, reinterpret_cast<uint8_t *>(sm.v[vs]), &sm.v_full[vs]);
+                }
+                v_issued = j + 1;
+            }
+            // every copy issued lands before the CTA can exit
+            if (lane == 0) {
+                drain_wait(&sm.q_full, 0, p.status);
+                for (int j = k_issued - 1; j >= 0 && j >= k_issued - KST; j--)
+                    drain_wait(&sm.k_full[j % KST], (j / KST) & 1, p.status);
+                constexpr int VR = E4M3 ? RAW_STAGES : VST;
+                for (int j = v_issued - 1; j >= 0 && j >= v_issued - VR; j--) {
+                    uint64_t *bar;
+                    if constexpr (E4M3)
+                        bar = &sm.raw_full[j % VR];
+                    else
+                        bar = &sm.v_full[j % VR];
+                    drain_wait(bar, (j / VR) & 1, p.status);
+                }
+            }
+        } else if (warp == 0) {
+            // ------------------------------------------------------ producer --
+            if constexpr (!PAGED) {
+                if (lane == 0) {
+                    int issued = pre;
+                    for (int j = pre; j < n_tiles; j++) {
+                        const int st = j % STAGES;
+                        const uint32_t par = ((j / STAGES) & 1) ^ 1;
+                        if (!mbar_wait_bounded(&sm.k_empty[st], par) || aborted(&sm.abort_flag)) {
+                            set_abort(&sm.abort_flag, p.status);
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&sm.k_full[st], KB * BN * 128);
+                        for (int kb = 0; kb < KB; kb++)
+                            load_kv(sm.k[st][kb], &map_k, kb * 64, tile_row(j), &sm.k_full[st]);
+                        if (!mbar_wait_bounded(&sm.v_empty[st], par) || aborted(&sm.abort_flag)) {
+                            set_abort(&sm.abort_flag, p.status);
+                            drain_wait(&sm.k_full[st], (j / STAGES) & 1, p.status);
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&sm.v_full[st], KB * BN * 128);
+                        for (int kb = 0; kb < KB; kb++)
+                            load_kv(sm.v[st][kb], &map_v, kb * 64, tile_row(j), &sm.v_full[st]);
+                        issued = j + 1;
+                    }
+                    // every copy issued lands before the CTA can exit
+                    drain_wait(&sm.q_full, 0, p.status);
+                    for (int j = issued - 1; j >= 0 && j >= issued - STAGES; j--) {
+                        drain_wait(&sm.k_full[j % STAGES], (j / STAGES) & 1, p.status);
+                        drain_wait(&sm.v_full[j % STAGES], (j / STAGES) & 1, p.status);
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // ---------------------------------------------------- S = Q K^T issue --
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = E4M3 ? tc::idesc_e4m3_f32(BM, BN)
+                                                  : tc::idesc_bf16_f32(BM, BN, false, false);
+                // Descriptors of the Q tile and of K stage 0; a 64-wide column block
+                // (BM = BN rows of 128 B) is BLK16 16-byte units, a K stage K_STAGE16.
+                constexpr uint32_t BLK16 = (BM * 128) >> 4;
+                constexpr uint32_t K_STAGE16 = (E4M3 ? BN * D : KB * BN * 128) >> 4;
+                constexpr uint32_t Q_PART16 = (BM * D) >> 4;  // from the high to the low part (E4M3)
+                static_assert(BM == BN, "one column-block stride for Q and K");
+                uint64_t qd0, kd0;
+                bool ok;
+                if constexpr (E4M3) {
+                    qd0 = tc::desc_kmajor_bytes<D>(smem_addr(sm.q8[0]));
+                    kd0 = tc::desc_kmajor_bytes<D>(smem_addr(sm.k[0]));
+                    ok = mbar_wait_bounded(&sm.q_split, 0);
+                } else {
+                    qd0 = tc::desc_kmajor_sw128(smem_addr(sm.q[0]));
+                    kd0 = tc::desc_kmajor_sw128(smem_addr(sm.k[0][0]));
+                    ok = mbar_wait_bounded(&sm.q_full, 0);
+                }
+                bool any = false;
+                for (int j = 0; ok && j < n_tiles; j++) {
+                    const int st = j % KST, sb = j % NUM_S;
+                    ok = mbar_wait_bounded(&sm.k_full[st], (j / KST) & 1);
+                    if (ok && j >= NUM_S)
+                        ok = mbar_wait_bounded(&sm.s_free[sb], ((j / NUM_S) - 1) & 1);
+                    if (!ok || aborted(&sm.abort_flag))
+                        break;
+                    tc::fence_after_sync();
+                    const uint32_t s_t = tmem + S_COL0 * (sb + 1);
+                    const uint64_t kd = kd0 + (uint64_t)(st * K_STAGE16);
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int k = 0; k < D / 32; k++)  // 32 bytes of d per step
+                            tc::mma_ss_bytes(s_t, qd0 + k * 2, kd + k * 2, idesc_s, k > 0);
+#pragma unroll
+                        for (int k = 0; k < D / 32; k++)
+                            tc::mma_ss_bytes(s_t, qd0 + Q_PART16 + k * 2, kd + k * 2, idesc_s, true);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 16; k++) {  // descriptor start addresses advance in 16-byte units
+                            const uint32_t off = (k >> 2) * BLK16 + (k & 3) * 2;
+                            tc::mma_ss(s_t, qd0 + off, kd + off, idesc_s, k > 0);
+                        }
+                    }
+                    tc::mma_commit(&sm.s_full[sb]);
+                    tc::mma_commit(&sm.k_empty[st]);
+                    any = true;
+                }
+                if (!ok)
+                    set_abort(&sm.abort_flag, p.status);
+                if (any) {  // all issued MMAs complete before tensor memory is released
+                    tc::mma_commit(&sm.drain[0]);
+                    drain_wait(&sm.drain[0], 0, p.status);
+                }
+            }
+        } else if (warp == 2) {
+            // --------------------------------------------------- O += P V issue --
+            if (lane == 0) {
+                constexpr uint32_t idesc_o = E4M3 ? tc::idesc_f16_f32(BM, D, false, true)
+                                                  : tc::idesc_bf16_f32(BM, D, false, true);
+                constexpr uint32_t V_STAGE16 = (KB * BN * 128) >> 4;  // a V stage in 16-byte units
+                const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_addr(sm.v[0][0]), BN * 128);
+                bool ok = true, any = false;
+                for (int j = 0; ok && j < n_tiles; j++) {
+                    const int st = j % VST, sb = j % NUM_S;
+                    ok = mbar_wait_bounded(&sm.p_full[sb], (j / NUM_S) & 1);
+                    if (ok)
+                        ok = mbar_wait_bounded(&sm.v_full[st], (j / VST) & 1);
+                    if (!ok || aborted(&sm.abort_flag))
+                        break;
+                    tc::fence_after_sync();
+                    const uint32_t p_t = tmem + S_COL0 * (sb + 1);
+                    const uint64_t vd = vd0 + (uint64_t)(st * V_STAGE16);
+#pragma unroll
+                    for (int k = 0; k < BN / 16; k++)  // 16 keys = 16 rows of 128 B per step
+                        tc::mma_ts(tmem, p_t + k * 8, vd + (uint64_t)(k * 128), idesc_o, j > 0 || k > 0);
+                    tc::mma_commit(&sm.s_free[sb]);
+                    tc::mma_commit(&sm.v_empty[st]);
+                    tc::mma_commit(&sm.o_done[sb]);
+                    any = true;
+                }
+                if (!ok)
+                    set_abort(&sm.abort_flag, p.status);
+                if (any) {
+                    tc::mma_commit(&sm.drain[1]);
+                    drain_wait(&sm.drain[1], 0, p.status);
+                }
+            }
+        } else if (warp >= 4) {
+            if constexpr (!PAGED)
+                softmax();
+        }
+    } else if (E4M3 && warp >= CONVERT0) {
+        // -------------------------------------- E4M3 V tiles to f16 tiles --
+        if constexpr (E4M3) {
+            for (int j = 0; j < n_tiles; j++) {
+                const int rs = j % RAW_STAGES, st = j % VST;
+                bool ok = warp_wait(&sm.raw_full[rs], (j / RAW_STAGES) & 1, &sm.abort_flag);
+                if (ok && j == 0)  // the first V stage holds Q until it is split
+                    ok = warp_wait(&sm.q_split, 0, &sm.abort_flag);
+                if (ok)
+                    ok = warp_wait(&sm.v_empty[st], ((j / VST) & 1) ^ 1, &sm.abort_flag);
+                if (!ok) {
+                    if (lane == 0)
+                        set_abort(&sm.abort_flag, p.status);
+                    break;
+                }
+                const int j0 = k_begin + j * BN;
+                convert_tile<D>(sm.raw[rs], sm.v_scale[rs], sm.v[st][0], warp - CONVERT0, lane,
+                                vis_lo - j0, k_end - j0);
+                tc::fence_proxy_async_smem();  // before the tensor core's reads
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.v_full[st]);
+                    mbar_arrive(&sm.raw_empty[rs]);
+                }
+            }
+        }
+    } else {
+        if constexpr (PAGED)
+            softmax();
     }
     if (E4M3 && warp < SW && gated_out)
         load_gate();
@@ -1339,6 +1349,31 @@ __global__ void __launch_bounds__(cta_threads(SRC == KV_PAGED_E4M3, REP), 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, TMEM_COLS);
     }
+}
+
+// A contiguous cache's kernel has no page view among its parameters, and its roles
+// in an order of their own: 16 chunks of 2048 tokens, 40/8 heads, with their appends
+// take 7.51 ms, and took 7.64 as one more instance of the paged kernel (7.57 before
+// there was one).  Registers and arithmetic are the same.
+template <int D, bool CAPPED>
+__global__ void __launch_bounds__(THREADS, 1)
+    prefill_tc_kernel(const __grid_constant__ PrefillParams p,
+                      const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v)
+{
+    prefill_tile<D, CAPPED, KV_CONTIGUOUS, 1>(p, PagedView{}, map_q, map_k, map_v);
+}
+
+template <int D, bool CAPPED, KvSource SRC, int REP>
+__global__ void __launch_bounds__(cta_threads(SRC == KV_PAGED_E4M3, REP), 1)
+    prefill_tc_paged_kernel(const __grid_constant__ PrefillParams p,
+                            const __grid_constant__ PagedView pg,
+                            const __grid_constant__ CUtensorMap map_q,
+                            const __grid_constant__ CUtensorMap map_k,
+                            const __grid_constant__ CUtensorMap map_v)
+{
+    prefill_tile<D, CAPPED, SRC, REP>(p, pg, map_q, map_k, map_v);
 }
 
 // The sequence that grid slot `slot` serves, and its bounds: with 2 to 32
@@ -1567,22 +1602,30 @@ cudaError_t launch_prefill_t(const PrefillParams &p, const PagedView &pg, int to
     }
     const size_t smem = tc_smem_bytes<D, SRC>();
     static std::atomic<unsigned long long> configured{0};
-    cudaError_t e = once_per_device(configured, [smem] {
-        cudaError_t r = cudaFuncSetAttribute(prefill_tc_kernel<D, false, SRC, REP>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto kernel_of = [](auto capped) {
+        constexpr bool CAPPED = decltype(capped)::value;
+        if constexpr (SRC == KV_CONTIGUOUS)
+            return prefill_tc_kernel<D, CAPPED>;
+        else
+            return prefill_tc_paged_kernel<D, CAPPED, SRC, REP>;
+    };
+    const auto plain = kernel_of(std::false_type()), capped = kernel_of(std::true_type());
+    cudaError_t e = once_per_device(configured, [=] {
+        cudaError_t r = cudaFuncSetAttribute(plain, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(prefill_tc_kernel<D, true, SRC, REP>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            r = cudaFuncSetAttribute(capped, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return r;
     });
     if (e != cudaSuccess)
         return e;
     const dim3 grid(p.full_units + p.tail_units * p.num_splits);
     const dim3 block(cta_threads(SRC == KV_PAGED_E4M3, REP));
-    e = p.softcap > 0.f ? launch_kernel(prefill_tc_kernel<D, true, SRC, REP>, grid, block, smem, stream,
-                                        p, pg, mq, mk, mv)
-                        : launch_kernel(prefill_tc_kernel<D, false, SRC, REP>, grid, block, smem, stream,
-                                        p, pg, mq, mk, mv);
+    const auto kernel = p.softcap > 0.f ? capped : plain;
+    if constexpr (SRC == KV_CONTIGUOUS)
+        e = launch_kernel(kernel, grid, block, smem, stream, p, mq, mk, mv);
+    else
+        e = launch_kernel(kernel, grid, block, smem, stream, p, pg, mq, mk, mv);
     if (e != cudaSuccess || p.num_splits == 1)
         return e;
     return launch_kernel(prefill_combine_kernel<D, SRC != KV_CONTIGUOUS>, dim3(p.tail_units, BM / kMergeRows), dim3(256),
