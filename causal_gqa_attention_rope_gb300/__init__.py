@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
   na_attn_decode_static_ws  na_attn_decode with library-owned scratch
   na_rope_append_kv_paged, na_attn_prefill_chunk_paged, na_attn_decode_paged
                          the same over a paged cache of bf16 or 8-bit (E4M3) pages
+  na_pages_fork          page tables of a step: sequences forked, ended, begun, given room
+  na_pages_copy          whole pages copied
+  na_pages_compact       kept tokens to the front of new pages, keys turned to their new positions
   na_prefill_workspace_size / na_decode_workspace_size, the same with _paged, na_status_string
 """
 from __future__ import annotations
@@ -41,6 +44,8 @@ NA_V_NORM = 4
 NA_OUT_GATE = 8
 NA_RING_CACHE = 16
 
+NA_ROPE_INTERLEAVED = 2
+
 NA_KV_BF16 = 0
 NA_KV_E4M3 = 1
 
@@ -50,7 +55,8 @@ EXPORTED = ("na_rope_append_kv", "na_attn_prefill_chunk", "na_attn_decode",
             "na_prefill_workspace_size", "na_decode_workspace_size", "na_status_string",
             "na_selftest_wait_timeout", "na_rope_append_kv_paged", "na_attn_prefill_chunk_paged",
             "na_attn_decode_paged", "na_prefill_paged_workspace_size",
-            "na_decode_paged_workspace_size")
+            "na_decode_paged_workspace_size", "na_pages_fork", "na_pages_copy",
+            "na_pages_compact")
 
 
 class na_attn_cfg(ctypes.Structure):
@@ -120,6 +126,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                          P]
     lib.na_prefill_paged_workspace_size.argtypes = [cfgp, I32, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.na_decode_paged_workspace_size.argtypes = [cfgp, I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.na_pages_fork.argtypes = [I32, I32, P, P, P, P, I32, I32, P, I32, P, P, P, P, P, P, P]
+    lib.na_pages_copy.argtypes = [I32, I32, pagedp, I32, P, P, P, P]
+    lib.na_pages_compact.argtypes = [I32, I32, I32, pagedp, pagedp, P, P, I32, ropep, I32, I32,
+                                     ctypes.c_uint32, P, P]
     lib.na_selftest_wait_timeout.argtypes = [P, P]
     lib.na_status_string.argtypes = [ctypes.c_int]
     lib.na_status_string.restype = ctypes.c_char_p
@@ -128,7 +138,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "na_prefill_workspace_size", "na_decode_workspace_size",
                  "na_selftest_wait_timeout", "na_rope_append_kv_paged",
                  "na_attn_prefill_chunk_paged", "na_attn_decode_paged",
-                 "na_prefill_paged_workspace_size", "na_decode_paged_workspace_size"):
+                 "na_prefill_paged_workspace_size", "na_decode_paged_workspace_size",
+                 "na_pages_fork", "na_pages_copy", "na_pages_compact"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -216,6 +227,17 @@ class PagedKVCache:
             _ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale),
             _ptr(self.page_table), num_pages, page_size, batch, pages_per_seq,
             NA_KV_BF16 if self.k_scale is None else NA_KV_E4M3)
+
+
+@dataclass
+class PagedLatentCache:
+    """Caller-owned pages of latent rows and page table.
+
+    kv          bfloat16 [num_pages, page_size, row]: one row a token for all heads
+    page_table  int32 [batch, pages_per_seq], as PagedKVCache's
+    """
+    kv: "object"
+    page_table: "object"
 
 
 # ---------------------------------------------------------------- helpers --
@@ -602,6 +624,101 @@ def na_decode_importance(cfg: AttnConfig, probs, kv_lens, max_kv_len: int, imp,
                                   int(imp.shape[-1]), 1 if accumulate else 0, _ptr(status),
                                   _stream(stream))
     _check("na_decode_importance", rc)
+
+
+def na_pages_fork(parents, lens, table, ref, page_size: int, new_table, new_ref, new_lens, copy_src,
+                  copy_dst, grow=None, status=None, stream=None):
+    """One step of a batch's page tables: sequence b continues parents[b] (< 0: starts empty) and
+    gets room for grow[b] more tokens; the page copies that this needs are copy_src -> copy_dst
+    (na_pages_copy)."""
+    lib = load_library()
+    _want(parents, "parents", "int32", (None,))
+    _want(table, "table", "int32", (None, None))
+    batch, (old, P) = int(parents.shape[0]), table.shape
+    _want(lens, "lens", "int32", (old,))
+    _want(ref, "ref", "int32", (None,))
+    _want(new_table, "new_table", "int32", (batch, P))
+    _want(new_ref, "new_ref", "int32", ref.shape)
+    for t, name in ((new_lens, "new_lens"), (copy_src, "copy_src"), (copy_dst, "copy_dst"),
+                    (grow, "grow")):
+        _want(t, name, "int32", (batch,))
+    _want(status, "status", "int32", (None,), 1)
+    args = [_ptr(t) for t in (parents, grow, lens, table)]
+    outs = [_ptr(t) for t in (new_table, new_ref, new_lens, copy_src, copy_dst, status)]
+    pref = _ptr(ref)
+    _on_current(parents, grow, lens, table, ref, new_table, new_ref, new_lens, copy_src, copy_dst,
+                status)
+    _check("na_pages_fork",
+           lib.na_pages_fork(batch, old, *args, P, int(page_size), pref, int(ref.shape[0]), *outs,
+                             _stream(stream)))
+
+
+def _pages(cache, name: str):
+    """The C struct of a cache's pages (with its table where it has one), its tensors checked, and
+    (kv heads, row width)."""
+    if isinstance(cache, PagedLatentCache):
+        _want(cache.kv, f"{name}.kv", "bfloat16", (None, None, None))
+        pages, page, d = cache.kv.shape
+        heads, tensors = 1, (cache.kv, None, None, None)
+    else:
+        kind = "bfloat16" if cache.k_scale is None and cache.v_scale is None else "float8_e4m3fn"
+        _want(cache.k, f"{name}.k", kind, (None, None, None, None))
+        _want(cache.v, f"{name}.v", kind, cache.k.shape)
+        pages, heads, page, d = cache.k.shape
+        tensors = (cache.k, cache.v, cache.k_scale, cache.v_scale)
+        if kind != "bfloat16":
+            for t, which in ((cache.k_scale, "k_scale"), (cache.v_scale, "v_scale")):
+                if t is None:
+                    raise ValueError(f"{name}.{which}: missing")
+                _want(t, f"{name}.{which}", "uint8", (pages, heads))
+    _want(cache.page_table, f"{name}.page_table", "int32", (None, None))
+    batch, per = (0, 0) if cache.page_table is None else cache.page_table.shape
+    c = na_paged_kv_cache(*(_ptr(t) for t in tensors), _ptr(cache.page_table), pages, page, batch,
+                          per, NA_KV_BF16 if tensors[2] is None else NA_KV_E4M3)
+    _on_current(*tensors, cache.page_table)
+    return c, int(heads), int(d)
+
+
+def na_pages_copy(cache, src, dst, status=None, stream=None):
+    """Copy whole pages src[i] -> dst[i] of a PagedKVCache or PagedLatentCache (a negative entry:
+    nothing)."""
+    lib = load_library()
+    c, heads, d = _pages(cache, "cache")
+    _want(src, "src", "int32", (None,))
+    _want(dst, "dst", "int32", src.shape)
+    _want(status, "status", "int32", (None,), 1)
+    ps, pd, st = _ptr(src), _ptr(dst), _ptr(status)
+    _on_current(src, dst, status)
+    _check("na_pages_copy", lib.na_pages_copy(heads, d, ctypes.byref(c), int(src.shape[0]), ps, pd,
+                                              st, _stream(stream)))
+
+
+def na_pages_compact(cache, new_cache, keep_lens, max_keep: int, keep=None,
+                     rope: Optional[RopeConfig] = None, rotary_start: int = 0,
+                     rotary_dim: Optional[int] = None, interleaved: bool = False, status=None,
+                     stream=None):
+    """Move the rows at positions keep[b] of each sequence of `cache` (all in order with keep None)
+    to the front of `new_cache`'s pages, keys turned to their new positions where rope is given
+    (rotary_dim: by default from rotary_start to the row's end)."""
+    lib = load_library()
+    _want(keep_lens, "keep_lens", "int32", (None,))
+    batch, max_keep = int(keep_lens.shape[0]), int(max_keep)
+    a, heads, d = _pages(cache, "cache")
+    z, new_heads, new_d = _pages(new_cache, "new_cache")
+    if (heads, d) != (new_heads, new_d):
+        raise ValueError(f"new_cache: rows of {new_heads} x {new_d}, the cache's are {heads} x {d}")
+    if cache.page_table is None or new_cache.page_table is None:
+        raise ValueError("both caches need a page table")
+    _want(keep, "keep", "int32", (batch, max_keep))
+    _want(status, "status", "int32", (None,), 1)
+    pk, pl, st = _ptr(keep), _ptr(keep_lens), _ptr(status)
+    _on_current(keep, keep_lens, status)
+    r = None if rope is None else ctypes.byref(rope.c())
+    rd = d - rotary_start if rotary_dim is None else rotary_dim
+    _check("na_pages_compact",
+           lib.na_pages_compact(heads, d, batch, ctypes.byref(a), ctypes.byref(z), pk, pl, max_keep,
+                                r, int(rotary_start), 0 if r is None else int(rd),
+                                NA_ROPE_INTERLEAVED if interleaved else 0, st, _stream(stream)))
 
 
 def na_selftest_wait_timeout(status, stream=None):

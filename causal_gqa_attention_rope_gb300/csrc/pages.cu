@@ -1,0 +1,643 @@
+// pages.cu -- the pages of a cache between attention calls: a step of the page
+// tables (na_pages_fork), whole pages copied (na_pages_copy), kept tokens moved to
+// the front of new pages (na_pages_compact).
+#include <climits>
+#include <cuda_fp16.h>
+
+#include "pages.cuh"
+#include "rope_math.cuh"
+
+namespace {
+
+using namespace rope;
+
+// ------------------------------------------------------------------- fork --
+//
+// One CTA: a step's tables are a few thousand entries, and every phase needs what
+// the phase before found about all sequences.  Counts of references change by
+// atomics on integers, whose order does not show, and only for parents that have
+// not exactly one child (kids - 1 for a shared page, -1 for an ended sequence's).
+// Free pages are then found in index order by a scan, page rank k going to the
+// sequence whose range of missing pages holds k.
+
+constexpr int FORK_THREADS = 1024;
+
+// Exclusive prefix sum of one value per thread over the CTA; `total` gets the sum.
+__device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();  // the sums of an earlier call have been read
+    if (lane == 31)
+        warp_sums[warp] = x;
+    __syncthreads();
+    const int w = warp_sums[lane];  // FORK_THREADS / 32 = 32 warps
+    int before = lane < warp ? w : 0, all = w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    total = all;
+    return before + x - v;
+}
+
+__global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkParams p)
+{
+    extern __shared__ int fork_smem[];
+    int *kids = fork_smem;              // [old_batch]
+    int *first = kids + p.old_batch;    // [old_batch]  lowest child
+    int *held = first + p.old_batch;    // [old_batch]  pages of the row
+    int *start = held + p.old_batch;    // [batch]  first missing entry
+    int *offs = start + p.batch;        // [batch + 1]  missing entries before sequence b
+    __shared__ int warp_sums[32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int P = p.pages_per_seq;
+
+    for (int i = tid; i < p.old_batch; i += FORK_THREADS) {
+        kids[i] = 0;
+        first[i] = INT_MAX;
+    }
+    for (int i = tid; i < p.num_pages; i += FORK_THREADS)
+        p.new_ref[i] = __ldg(p.ref + i);
+    __syncthreads();
+    for (int b = tid; b < p.batch; b += FORK_THREADS) {
+        const int par = __ldg(p.parents + b);
+        if (par >= p.old_batch) {
+            na_report(p.status, NA_ERR_INVALID_ARG);
+        } else if (par >= 0) {
+            atomicAdd(&kids[par], 1);
+            atomicMin(&first[par], b);
+        }
+    }
+    __syncthreads();
+
+    // Old rows: a warp each.  How many pages a row holds, and what becomes of their counts.
+    for (int r = warp; r < p.old_batch; r += FORK_THREADS / 32) {
+        const int32_t *row = p.table + (size_t)r * P;
+        const int full = max(__ldg(p.lens + r), 0) >> p.page_log;
+        const int k = kids[r];
+        int n = P;
+        for (int base = 0; base < P; base += 128) {
+            int e[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int j = base + i * 32 + lane;
+                e[i] = j < P ? __ldg(row + j) : -1;
+            }
+            bool end = false;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const unsigned bad = __ballot_sync(0xffffffffu, (unsigned)e[i] >= (unsigned)p.num_pages);
+                if (end)
+                    continue;
+                const int good = bad ? __ffs(bad) - 1 : 32;
+                const int j = base + i * 32 + lane;
+                if (lane < good) {
+                    const int delta = k == 0 ? -1 : (j < full ? k - 1 : 0);
+                    if (delta != 0)
+                        atomicAdd(p.new_ref + e[i], delta);
+                }
+                if (bad) {
+                    end = true;
+                    n = min(base + i * 32 + good, P);
+                    if (lane == good && e[i] >= 0)
+                        na_report(p.status, NA_ERR_PAGE);
+                }
+            }
+            if (end)
+                break;
+        }
+        if (lane == 0)
+            held[r] = n;
+    }
+    __syncthreads();
+
+    // New rows: a warp each.
+    for (int b = warp; b < p.batch; b += FORK_THREADS / 32) {
+        int par = __ldg(p.parents + b);
+        if (par >= p.old_batch)
+            par = -1;
+        const int n = par >= 0 ? max(__ldg(p.lens + par), 0) : 0;
+        int grow = p.grow ? __ldg(p.grow + b) : 0;
+        const int have = par >= 0 ? held[par] : 0;
+        const bool elder = par >= 0 && first[par] == b;
+        const int mine = elder ? have : min(n >> p.page_log, have);
+        if (lane == 0) {
+            if (grow < 0)
+                na_report(p.status, NA_ERR_INVALID_ARG);
+            if (((long long)have << p.page_log) < n)
+                na_report(p.status, NA_ERR_PAGE);
+        }
+        grow = max(grow, 0);
+        const long long pages = ((long long)n + grow + (1 << p.page_log) - 1) >> p.page_log;
+        if (pages > P && lane == 0)
+            na_report(p.status, NA_ERR_CAPACITY);
+        const int32_t *from = p.table + (size_t)max(par, 0) * P;
+        int32_t *to = p.new_table + (size_t)b * P;
+        for (int j = lane; j < P; j += 32)
+            to[j] = j < mine ? __ldg(from + j) : -1;
+        if (lane == 0) {
+            start[b] = mine;
+            offs[b] = max((int)min(pages, (long long)P) - mine, 0);
+            p.new_lens[b] = n;
+        }
+    }
+    __syncthreads();
+
+    // Missing pages before each sequence's.
+    int missing = 0;
+    for (int base = 0; base < p.batch; base += FORK_THREADS) {
+        const int b = base + tid;
+        int sum;
+        const int before = block_prefix(b < p.batch ? offs[b] : 0, warp_sums, sum);
+        if (b < p.batch)
+            offs[b] = missing + before;
+        missing += sum;
+    }
+    if (tid == 0)
+        offs[p.batch] = missing;
+    __syncthreads();
+
+    // Free pages in order, four to a thread and round.
+    int found = 0;
+    for (int base = 0; base < p.num_pages && found < missing; base += 4 * FORK_THREADS) {
+        const int i0 = base + 4 * tid;
+        unsigned free = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (i0 + i < p.num_pages && __ldcg(p.new_ref + i0 + i) == 0)
+                free |= 1u << i;
+        int sum;
+        int rank = found + block_prefix(__popc(free), warp_sums, sum);
+        found += sum;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (!(free >> i & 1) || rank >= missing)
+                continue;
+            int lo = 0, hi = p.batch - 1;  // the last b with offs[b] <= rank
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (offs[mid] <= rank)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            p.new_table[(size_t)lo * P + start[lo] + (rank - offs[lo])] = i0 + i;
+            p.new_ref[i0 + i] = 1;
+            rank++;
+        }
+    }
+    if (found < missing && tid == 0)
+        na_report(p.status, NA_ERR_CAPACITY);
+    __syncthreads();
+
+    for (int b = tid; b < p.batch; b += FORK_THREADS) {
+        const int par = __ldg(p.parents + b);
+        int src = -1, dst = -1;
+        if (par >= 0 && par < p.old_batch && first[par] != b) {
+            const int n = max(__ldg(p.lens + par), 0), j = n >> p.page_log;
+            if ((n & ((1 << p.page_log) - 1)) && j < held[par]) {
+                dst = __ldcg(p.new_table + (size_t)b * P + j);
+                src = dst >= 0 ? __ldg(p.table + (size_t)par * P + j) : -1;
+            }
+        }
+        p.copy_src[b] = src;
+        p.copy_dst[b] = dst;
+    }
+}
+
+// ------------------------------------------------------------------- copy --
+//
+// Bound by memory: a CTA moves COPY_BYTES of one page, every thread's four
+// 16-byte loads in flight before its first store.
+
+constexpr int COPY_THREADS = 256;
+constexpr int COPY_BYTES = COPY_THREADS * 16 * 4;
+
+__global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PageCopyParams p)
+{
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int per = p.v ? 2 * p.chunks : p.chunks;
+    const int pair = blockIdx.x / per, part = blockIdx.x - pair * per;
+    const int src = __ldg(p.src + pair), dst = __ldg(p.dst + pair);
+    if (src < 0 || dst < 0)
+        return;
+    if (src >= p.num_pages || dst >= p.num_pages) {
+        if (part == 0 && threadIdx.x == 0)
+            na_report(p.status, NA_ERR_PAGE);
+        return;
+    }
+    const bool is_v = part >= p.chunks;
+    uint8_t *pool = is_v ? p.v : p.k;
+    const long long at = (long long)(is_v ? part - p.chunks : part) * COPY_BYTES + threadIdx.x * 16;
+    const uint8_t *from = pool + src * p.page_bytes;
+    uint8_t *to = pool + dst * p.page_bytes;
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const long long x = at + i * COPY_THREADS * 16;
+        if (x < p.page_bytes)
+            u[i] = *reinterpret_cast<const uint4 *>(from + x);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const long long x = at + i * COPY_THREADS * 16;
+        if (x < p.page_bytes)
+            *reinterpret_cast<uint4 *>(to + x) = u[i];
+    }
+    if (p.k_scale && (part == 0 || part == p.chunks)) {
+        uint8_t *scale = is_v ? p.v_scale : p.k_scale;
+        for (int g = threadIdx.x; g < p.kv_heads; g += COPY_THREADS)
+            scale[(size_t)dst * p.kv_heads + g] = scale[(size_t)src * p.kv_heads + g];
+    }
+}
+
+// ---------------------------------------------------------------- compact --
+//
+// A row's elements in units of W (8, one 16-byte word of bf16, or 1 where the
+// turned dimensions have no such multiple): units of W pairs that turn together,
+// then the others.
+
+// Elements e0 .. and e1 .. (both W long) of pair unit u: the two halves, or with
+// interleaved pairs 2 W consecutive elements.
+template <int W>
+__device__ __forceinline__ void pair_unit(const CompactParams &p, int u, int &e0, int &e1)
+{
+    e0 = p.rot_start + (p.interleaved ? 2 * u * W : u * W);
+    e1 = e0 + (p.interleaved ? W : p.rd / 2);
+}
+
+// Element of unit u of those that do not turn.
+template <int W>
+__device__ __forceinline__ int plain_unit(const CompactParams &p, int u)
+{
+    const int e = u * W;
+    return e >= p.rot_start ? e + p.rd : e;
+}
+
+// Where row j of sequence b comes from and goes to: rows of one kv head's pages as
+// (page, slot); false (with a report) where there is no such place.
+struct Move {
+    int src, src_slot, dst, dst_slot, shift;  // shift: old position - new position
+};
+
+__device__ __forceinline__ bool find_move(const CompactParams &p, int b, int j, Move &m)
+{
+    const int old = p.keep ? __ldg(p.keep + (size_t)b * p.max_keep + j) : j;
+    const int old_page = old >> p.from.page_log, new_page = j >> p.to.page_log;
+    if (old < 0 || old_page >= p.from.pages_per_seq) {
+        na_report(p.status, NA_ERR_CAPACITY);
+        return false;
+    }
+    m.src = __ldg(p.from.table + (size_t)b * p.from.pages_per_seq + old_page);
+    m.dst = __ldg(p.to.table + (size_t)b * p.to.pages_per_seq + new_page);
+    if ((unsigned)m.src >= (unsigned)p.from.num_pages || (unsigned)m.dst >= (unsigned)p.to.num_pages) {
+        na_report(p.status, NA_ERR_PAGE);
+        return false;
+    }
+    m.src_slot = old & ((1 << p.from.page_log) - 1);
+    m.dst_slot = j & ((1 << p.to.page_log) - 1);
+    m.shift = old - j;
+    return true;
+}
+
+// Rows to move of sequence b (0, with a report, for a length that has no room).
+__device__ __forceinline__ int kept_rows(const CompactParams &p, int b)
+{
+    const int n = __ldg(p.keep_lens + b);
+    if (n > p.max_keep || n > p.to_positions) {
+        if (threadIdx.x == 0)
+            na_report(p.status, NA_ERR_CAPACITY);
+        return 0;
+    }
+    return n;
+}
+
+// cos and sin of pair i turned back by `shift` positions (forward for a negative one).
+__device__ __forceinline__ float4 turn_back(const RopeTurns &t, int i, int shift)
+{
+    float4 c = cos_sin_turns((unsigned)abs(shift), t.hi[i], t.lo[i], kTrig.e);
+    if (shift > 0) {
+        c.z = -c.z;
+        c.w = -c.w;
+    }
+    return c;
+}
+
+template <int W>
+struct Words;
+template <>
+struct Words<8> {
+    typedef uint4 T;
+    static __device__ __forceinline__ void widen(const uint4 &u, float *f) { bf16x8_to_f32(u, f); }
+    static __device__ __forceinline__ uint4 round(const float *f) { return f32_to_bf16x8(f); }
+};
+template <>
+struct Words<1> {
+    typedef uint16_t T;
+    static __device__ __forceinline__ void widen(uint16_t u, float *f)
+    {
+        f[0] = __uint_as_float((uint32_t)u << 16);
+    }
+    static __device__ __forceinline__ uint16_t round(const float *f)
+    {
+        return (uint16_t)(pack_bf16x2(f[0], 0.f) & 0xffffu);
+    }
+};
+
+constexpr int COMPACT_THREADS = 256;
+constexpr int COMPACT_ROWS = 16;
+constexpr int COMPACT_HEADS = 4;  // heads whose loads are in flight together
+
+// bf16: a CTA moves COMPACT_ROWS rows of one sequence.  A thread takes one unit of a
+// row for every kv head, so that cos and sin are computed once for all heads.
+template <int W>
+__global__ void __launch_bounds__(COMPACT_THREADS)
+    pages_compact_kernel(const __grid_constant__ CompactParams p,
+                         const __grid_constant__ RopeTurns turns, int row_blocks)
+{
+    typedef typename Words<W>::T Word;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int b = blockIdx.x / row_blocks, j0 = (blockIdx.x - b * row_blocks) * COMPACT_ROWS;
+    const int n = min(kept_rows(p, b) - j0, COMPACT_ROWS);
+    const int pairs = p.turn ? p.rd / 2 / W : 0;
+    const int k_units = pairs + (p.d - (p.turn ? p.rd : 0)) / W;
+    const int units = k_units + (p.to_v ? p.d / W : 0);
+    for (int i = threadIdx.x; i < n * units; i += COMPACT_THREADS) {
+        const int r = i / units;
+        int u = i - r * units;
+        Move m;
+        if (!find_move(p, b, j0 + r, m))
+            continue;
+        const bool is_v = u >= k_units;
+        if (is_v)
+            u -= k_units;
+        const size_t src_head = (size_t)p.d << p.from.page_log, dst_head = (size_t)p.d << p.to.page_log;
+        const bf16 *from = reinterpret_cast<const bf16 *>(is_v ? p.from_v : p.from_k) +
+                           (size_t)m.src * p.KV * src_head + (size_t)m.src_slot * p.d;
+        bf16 *to = reinterpret_cast<bf16 *>(is_v ? p.to_v : p.to_k) + (size_t)m.dst * p.KV * dst_head +
+                   (size_t)m.dst_slot * p.d;
+        if (is_v || u >= pairs) {
+            const int e = is_v ? u * W : (p.turn ? plain_unit<W>(p, u - pairs) : (u - pairs) * W);
+            for (int g = 0; g < p.KV; g += COMPACT_HEADS) {
+                Word x[COMPACT_HEADS];
+#pragma unroll
+                for (int h = 0; h < COMPACT_HEADS; h++)
+                    if (g + h < p.KV)
+                        x[h] = *reinterpret_cast<const Word *>(from + (g + h) * src_head + e);
+#pragma unroll
+                for (int h = 0; h < COMPACT_HEADS; h++)
+                    if (g + h < p.KV)
+                        *reinterpret_cast<Word *>(to + (g + h) * dst_head + e) = x[h];
+            }
+            continue;
+        }
+        int e0, e1;
+        pair_unit<W>(p, u, e0, e1);
+        float4 cs[W];
+        for (int g = 0; g < p.KV; g += COMPACT_HEADS) {
+            Word x0[COMPACT_HEADS], x1[COMPACT_HEADS];
+#pragma unroll
+            for (int h = 0; h < COMPACT_HEADS; h++)
+                if (g + h < p.KV) {
+                    x0[h] = *reinterpret_cast<const Word *>(from + (g + h) * src_head + e0);
+                    x1[h] = *reinterpret_cast<const Word *>(from + (g + h) * src_head + e1);
+                }
+            if (g == 0) {
+#pragma unroll
+                for (int w = 0; w < W; w++)
+                    cs[w] = turn_back(turns, u * W + w, m.shift);
+            }
+#pragma unroll
+            for (int h = 0; h < COMPACT_HEADS; h++) {
+                if (g + h >= p.KV)
+                    continue;
+                float a[2 * W], y[2 * W];
+                Words<W>::widen(x0[h], a);
+                Words<W>::widen(x1[h], a + W);
+                if (p.interleaved) {
+#pragma unroll
+                    for (int w = 0; w < W; w++)
+                        rotate_exact(a[2 * w], a[2 * w + 1], cs[w], 1.0f, y[2 * w], y[2 * w + 1]);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < W; w++)
+                        rotate_exact(a[w], a[W + w], cs[w], 1.0f, y[w], y[W + w]);
+                }
+                if (m.shift != 0) {  // (a row that stays keeps its bits, NaN's too)
+                    x0[h] = Words<W>::round(y);
+                    x1[h] = Words<W>::round(y + W);
+                }
+                *reinterpret_cast<Word *>(to + (g + h) * dst_head + e0) = x0[h];
+                *reinterpret_cast<Word *>(to + (g + h) * dst_head + e1) = x1[h];
+            }
+        }
+    }
+}
+
+// E4M3: a CTA fills one page of one kv head, of K or V: the rows in fp32 into shared
+// memory, their largest magnitude, then the bytes.
+__device__ __forceinline__ float e4m3_value(uint32_t byte)
+{
+    uint32_t lo, hi;
+    e4m3x4_to_f16(byte, lo, hi);
+    return __half2float(__ushort_as_half((unsigned short)(lo & 0xffffu)));
+}
+
+__device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// E8M0 byte of the smallest 2^e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), e >= -127.
+__device__ __forceinline__ int scale_byte(float amax)
+{
+    const uint32_t x = __float_as_uint(amax);
+    return max((int)(x >> 23) - 8 + ((x & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+}
+
+template <int W>
+__global__ void __launch_bounds__(COMPACT_THREADS)
+    pages_compact_e4m3_kernel(const __grid_constant__ CompactParams p,
+                              const __grid_constant__ RopeTurns turns, int page_blocks)
+{
+    extern __shared__ float rows[];  // [page][d]
+    __shared__ float amax_of[COMPACT_THREADS / 32];
+    __shared__ int moved[128];       // row r of the page is among those to write
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int b = blockIdx.x / page_blocks, pg = blockIdx.x - b * page_blocks;
+    const bool is_v = blockIdx.y >= p.KV;
+    const int g = is_v ? blockIdx.y - p.KV : blockIdx.y;
+    const int j0 = pg << p.to.page_log;
+    const int n = min(kept_rows(p, b) - j0, 1 << p.to.page_log);
+    if (n <= 0)
+        return;
+    const int32_t dst = __ldg(p.to.table + (size_t)b * p.to.pages_per_seq + pg);
+    const bool turn = p.turn && !is_v;
+    const int pairs = turn ? p.rd / 2 / W : 0;
+    const int units = pairs + (p.d - (turn ? p.rd : 0)) / W;
+    float amax = 0.f;
+    for (int i = threadIdx.x; i < n * units; i += COMPACT_THREADS) {
+        const int r = i / units, u = i - r * units;
+        Move m;
+        const bool there = find_move(p, b, j0 + r, m);
+        if (u == 0)
+            moved[r] = there;
+        if (!there)
+            continue;
+        const uint8_t *from = (is_v ? p.from_v : p.from_k) +
+                              ((((size_t)m.src * p.KV + g) << p.from.page_log) + m.src_slot) * p.d;
+        uint32_t s = __ldg((is_v ? p.from.v_scale : p.from.k_scale) + (size_t)m.src * p.KV + g);
+        if (s == 255) {
+            na_report(p.status, NA_ERR_UNSUPPORTED);
+            s = 254;
+        }
+        const float mul = e8m0_value(s);
+        float *row = rows + r * p.d;
+        auto load = [&](int e, float (&x)[W]) {
+            if constexpr (W == 8) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(from + e);
+                uint32_t h[4];
+                e4m3x4_to_f16(w.x, h[0], h[1]);
+                e4m3x4_to_f16(w.y, h[2], h[3]);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                    x[2 * k] = f.x * mul;
+                    x[2 * k + 1] = f.y * mul;
+                }
+            } else {
+                x[0] = e4m3_value(from[e]) * mul;
+            }
+        };
+        if (u >= pairs) {
+            const int e = turn ? plain_unit<W>(p, u - pairs) : u * W;
+            float x[W];
+            load(e, x);
+#pragma unroll
+            for (int w = 0; w < W; w++) {
+                row[e + w] = x[w];
+                amax = fmaxf(amax, fabsf(x[w]));
+            }
+            continue;
+        }
+        int e0, e1;
+        pair_unit<W>(p, u, e0, e1);
+        float x[2][W];
+        load(e0, x[0]);
+        load(e1, x[1]);
+#pragma unroll
+        for (int w = 0; w < W; w++) {
+            const float4 c = turn_back(turns, u * W + w, m.shift);
+            // the pair's places: its halves, or two neighbours of the 2 W elements
+            const int i0 = p.interleaved ? 2 * w : w, i1 = p.interleaved ? 2 * w + 1 : W + w;
+            const float a0 = x[i0 / W][i0 % W], a1 = x[i1 / W][i1 % W];
+            const float y0 = fmaf(a0, c.x, -a1 * c.z), y1 = fmaf(a1, c.x, a0 * c.z);
+            row[(i0 < W ? e0 : e1) + i0 % W] = y0;
+            row[(i1 < W ? e0 : e1) + i1 % W] = y1;
+            amax = fmaxf(amax, fmaxf(fabsf(y0), fabsf(y1)));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((threadIdx.x & 31) == 0)
+        amax_of[threadIdx.x >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < COMPACT_THREADS / 32; w++)
+        amax = fmaxf(amax, amax_of[w]);
+    if ((unsigned)dst >= (unsigned)p.to.num_pages)
+        return;  // reported with the rows
+    const int s = min(scale_byte(amax), 254);
+    // 2^(127 - s) in two factors: the first of a small scale alone exceeds fp32
+    const int up = 127 - s, half = up / 2;
+    const float m0 = exp2i(half), m1 = exp2i(up - half);
+    const size_t page = (size_t)dst * p.KV + g;
+    uint8_t *to = (is_v ? p.to_v : p.to_k) + (page << p.to.page_log) * p.d;
+    if (threadIdx.x == 0)
+        (is_v ? p.to_v_scale : p.to_k_scale)[page] = (uint8_t)s;
+    for (int i = threadIdx.x; i < n * (p.d / 4); i += COMPACT_THREADS) {
+        const int r = i / (p.d / 4);
+        if (!moved[r])
+            continue;
+        const float4 x = *reinterpret_cast<const float4 *>(rows + 4 * i);
+        reinterpret_cast<uint32_t *>(to)[i] =
+            e4m3x4_of(x.x * m0 * m1, x.y * m0 * m1, x.z * m0 * m1, x.w * m0 * m1);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_fork(const ForkParams &p, cudaStream_t stream)
+{
+    const size_t smem = (3 * (size_t)p.old_batch + 2 * (size_t)p.batch + 1) * sizeof(int);
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = once_per_device(configured, [] {
+        return cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (5 * kMaxForkBatch + 1) * (int)sizeof(int));
+    });
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(pages_fork_kernel, dim3(1), dim3(FORK_THREADS), smem, stream, p);
+}
+
+cudaError_t launch_pages_copy(const PageCopyParams &p, cudaStream_t stream)
+{
+    PageCopyParams q = p;
+    q.chunks = (int)((p.page_bytes + COPY_BYTES - 1) / COPY_BYTES);
+    const long long grid = (long long)p.n * q.chunks * (p.v ? 2 : 1);
+    if (grid > INT_MAX)
+        return cudaErrorInvalidConfiguration;
+    return launch_kernel(pages_copy_kernel, dim3((unsigned)grid), dim3(COPY_THREADS), 0, stream, q);
+}
+
+cudaError_t launch_pages_compact(const CompactParams &p, bool e4m3, const RopeTurns &turns,
+                                 cudaStream_t stream)
+{
+    // words of 8 elements where pairs, their start and the rest come in such
+    const int unit = p.turn ? (p.rd | 2 * p.rot_start) & 15 : 0;
+    if (e4m3) {
+        const int page = 1 << p.to.page_log;
+        const int blocks = (p.max_keep + page - 1) / page;
+        if ((long long)blocks * p.batch > INT_MAX)
+            return cudaErrorInvalidConfiguration;
+        const dim3 grid((unsigned)(blocks * p.batch), 2 * p.KV);
+        const size_t smem = (size_t)page * p.d * sizeof(float);
+        const auto kernel = unit ? pages_compact_e4m3_kernel<1> : pages_compact_e4m3_kernel<8>;
+        static std::atomic<unsigned long long> configured{0};
+        const cudaError_t e = once_per_device(configured, [] {
+            const int most = 128 * 128 * sizeof(float);
+            const cudaError_t r = cudaFuncSetAttribute(
+                pages_compact_e4m3_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            return r != cudaSuccess ? r
+                                    : cudaFuncSetAttribute(pages_compact_e4m3_kernel<1>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                           most);
+        });
+        if (e != cudaSuccess)
+            return e;
+        return launch_kernel(kernel, grid, dim3(COMPACT_THREADS), smem, stream, p, turns, blocks);
+    }
+    const int blocks = (p.max_keep + COMPACT_ROWS - 1) / COMPACT_ROWS;
+    if ((long long)blocks * p.batch > INT_MAX)
+        return cudaErrorInvalidConfiguration;
+    return launch_kernel(unit ? pages_compact_kernel<1> : pages_compact_kernel<8>,
+                         dim3((unsigned)(blocks * p.batch)), dim3(COMPACT_THREADS), 0, stream, p,
+                         turns, blocks);
+}

@@ -420,6 +420,112 @@ int na_prefill_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t tot
 int na_decode_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_kv_len,
                              int32_t num_splits, size_t *bytes);
 
+#define NA_ROPE_INTERLEAVED 2u /* RoPE turns pairs (x[2 i], x[2 i + 1]) instead of (x[i], x[i + rd/2]) */
+
+/* ------------------------------------------------------- pages of a cache --
+ *
+ * The page tables of a serving batch, its forks and evictions.  (Additions of
+ * this library; the pages have no counterpart.)  One table serves every layer
+ * of a model, so na_pages_fork is called once a step, and na_pages_copy and
+ * na_pages_compact once per layer.  A cache of one row
+ * a token and no values (latent rows) has one kv head and v NULL.
+ */
+
+/*
+ * One step of a batch's page tables: which sequences go on, from which, and
+ * how many positions they need.
+ *
+ * The old batch is table [old_batch][pages_per_seq]: row p holds the pages of its
+ * sequence, lens[p] tokens, its entries up to the first negative one.  Sequence b
+ * of the new batch continues parents[b] (an old sequence, many may share one), or
+ * starts empty (parents[b] < 0); an old sequence that is nobody's parent ends.
+ * With n = lens[parents[b]] (or 0) tokens:
+ *   - new_table[b] gets the parent's n / page_size full pages, shared.  The child
+ *     with the lowest b gets all of the parent's other pages too (a part-filled one,
+ *     and those reserved behind it).  For any other child of a parent whose last
+ *     page is part-filled a page is taken, and the copy that it needs is
+ *     copy_src[b] -> copy_dst[b] (-1 where there is none): na_pages_copy.
+ *   - pages are taken until the row has room for n + grow[b] tokens (grow NULL: 0).
+ *   - ref[page] counts the rows that hold a page, of this batch and of others (a
+ *     prefix that is kept, a second table).  new_ref is ref without the old rows'
+ *     and with the new ones'; a page with count 0 is free.  Pages are taken in
+ *     index order from those free after that, for b in order and positions in order.
+ * The other entries of new_table are -1.  All results are functions of the
+ * inputs alone, in whatever order the device works.
+ *
+ *   batch, old_batch  1 .. 4096 sequences.
+ *   parents, grow     int32 [batch] (grow may be NULL);  lens int32 [old_batch].
+ *   table             int32 [old_batch][pages_per_seq];  ref int32 [num_pages].
+ *   new_table         int32 [batch][pages_per_seq];  new_ref int32 [num_pages];
+ *   new_lens, copy_src, copy_dst  int32 [batch].  No output may overlap an input or
+ *                     another output (callers keep two tables and take turns).
+ *   status  NA_ERR_INVALID_ARG for a parent >= old_batch (taken as none) or a
+ *           negative grow (taken as 0), NA_ERR_PAGE for an entry >= num_pages (which
+ *           ends its row) or a row with fewer pages than lens needs (the missing ones
+ *           are taken), NA_ERR_CAPACITY when no page is free or a row would need more
+ *           than pages_per_seq (the entries that are missing are -1, a copy
+ *           without a page -1 -> -1).
+ * Errors: NA_ERR_INVALID_ARG for null pointers (status and grow may be NULL) and
+ * sizes below 1, NA_ERR_UNSUPPORTED for a page size other than 16, 32, 64, 128 or
+ * more than 4096 sequences.
+ */
+int na_pages_fork(int32_t batch, int32_t old_batch, const int32_t *parents, const int32_t *grow,
+                  const int32_t *lens, const int32_t *table, int32_t pages_per_seq,
+                  int32_t page_size, const int32_t *ref, int32_t num_pages, int32_t *new_table,
+                  int32_t *new_ref, int32_t *new_lens, int32_t *copy_src, int32_t *copy_dst,
+                  int32_t *status, void *stream);
+
+/*
+ * Whole pages (K, V and their scales, every kv head) from src[i] to dst[i], i < n;
+ * a pair with a negative src or dst is skipped.  The pairs have to be independent:
+ * no page may be the dst of two, or the dst of one and the src of another.
+ *
+ *   cache   its page_table, batch and pages_per_seq are not looked at.
+ *   n       pairs; 0 is a no-op.   src, dst  int32 [n].
+ *   status  NA_ERR_PAGE for a page >= num_pages (that pair is skipped).
+ * Errors: as for a paged cache; head_dim has to be a multiple of 8 (NA_KV_E4M3: 16)
+ * and at most 1024 (NA_ERR_UNSUPPORTED).
+ */
+int na_pages_copy(int32_t num_kv_heads, int32_t head_dim, const na_paged_kv_cache *cache, int32_t n,
+                  const int32_t *src, const int32_t *dst, int32_t *status, void *stream);
+
+/*
+ * The kept tokens of each sequence, in a cache's pages, to the front of others: row
+ * j < keep_lens[b] of sequence b in `to` becomes the row at position keep[b][j]
+ * (j itself with keep NULL) of sequence b in `from`.  With rope, K's dimensions
+ * [rotary_start, rotary_start + rotary_dim) are turned by (j - keep[b][j]) positions,
+ * so that a key stands as if it had been appended at its new position (cos and sin
+ * are not multiplied by an attention factor again).  This is what eviction by
+ * na_decode_importance needs: positions then follow from the new lengths, in the
+ * attention calls and for the tokens to come.  With keep NULL, no rope and a
+ * contiguous `to` it gathers sequences out of their pages.
+ * bf16: an unturned row is moved bit for bit; a turned value is rounded once to
+ * bf16 (within one ulp, correctly but for ~2^-23 next to a rounding border).
+ * E4M3: a new page's scale is the smallest power of two 2^e with max |x| <= 448 * 2^e
+ * over the rows moved into it, x the stored values turned in fp32 (within 2^-20 of
+ * the row's largest), and every x is rounded once to x * 2^-e.
+ *
+ *   from, to   caches of one dtype; their page sizes may differ, and they may be
+ *              the same pools.  No page that `to` writes may be one that `from`
+ *              reads, or belong to two sequences.  Slots of `to` behind a sequence's
+ *              rows are left as they were.
+ *   rope       HOST, or NULL: nothing is turned.  rotary_dim even, rotary_start +
+ *              rotary_dim <= head_dim.  flags: 0 or NA_ROPE_INTERLEAVED.
+ *   max_keep   HOST upper bound of keep_lens, and keep's row stride; 0 is a no-op.
+ *   status     NA_ERR_CAPACITY for a length above max_keep or `to`'s positions or a
+ *              kept position outside `from`'s (the row is skipped, a sequence
+ *              altogether for its length), NA_ERR_PAGE for a table entry outside its
+ *              pool (its rows are skipped), NA_ERR_UNSUPPORTED for an E8M0 byte 255
+ *              (taken as 2^127).
+ * Errors: as for paged caches; NA_ERR_UNSUPPORTED for a head_dim that is no multiple
+ * of 8 (E4M3: 16) or above 1024 (E4M3: 128) or a rotary_dim above 128.
+ */
+int na_pages_compact(int32_t num_kv_heads, int32_t head_dim, int32_t batch,
+                     const na_paged_kv_cache *from, const na_paged_kv_cache *to, const int32_t *keep,
+                     const int32_t *keep_lens, int32_t max_keep, const na_rope_params *rope,
+                     int32_t rotary_start, int32_t rotary_dim, uint32_t flags, int32_t *status,
+                     void *stream);
+
 /*
  * Self-test of the device-side failure detection (an addition of this
  * library).  Every wait of the library's kernels for a copy or a tensor-core
