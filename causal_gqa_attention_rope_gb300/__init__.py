@@ -14,10 +14,14 @@ Entry points (same names as the C ABI):
   na_attn_decode_static_ws  na_attn_decode with library-owned scratch
   na_rope_append_kv_paged, na_attn_prefill_chunk_paged, na_attn_decode_paged
                          the same over a paged cache of bf16 or 8-bit (E4M3) pages
+  na_latent_append_paged, na_attn_latent_paged, na_attn_latent_expanded
+                         latent attention: fused append of latent rows, the absorbed form over
+                         pages, the expanded form
   na_pages_fork          page tables of a step: sequences forked, ended, begun, given room
   na_pages_copy          whole pages copied
   na_pages_compact       kept tokens to the front of new pages, keys turned to their new positions
-  na_prefill_workspace_size / na_decode_workspace_size, the same with _paged, na_status_string
+  na_prefill_workspace_size / na_decode_workspace_size, the same with _paged,
+  na_latent_paged_workspace_size, na_status_string
 """
 from __future__ import annotations
 
@@ -44,6 +48,7 @@ NA_V_NORM = 4
 NA_OUT_GATE = 8
 NA_RING_CACHE = 16
 
+NA_LATENT_NORM = 1
 NA_ROPE_INTERLEAVED = 2
 
 NA_KV_BF16 = 0
@@ -56,7 +61,8 @@ EXPORTED = ("na_rope_append_kv", "na_attn_prefill_chunk", "na_attn_decode",
             "na_selftest_wait_timeout", "na_rope_append_kv_paged", "na_attn_prefill_chunk_paged",
             "na_attn_decode_paged", "na_prefill_paged_workspace_size",
             "na_decode_paged_workspace_size", "na_pages_fork", "na_pages_copy",
-            "na_pages_compact")
+            "na_pages_compact", "na_latent_append_paged", "na_attn_latent_paged",
+            "na_latent_paged_workspace_size", "na_attn_latent_expanded")
 
 
 class na_attn_cfg(ctypes.Structure):
@@ -84,6 +90,19 @@ class na_paged_kv_cache(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("batch", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class na_latent_cfg(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("kv_rank", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("nope_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+                ("rms_eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class na_paged_latent_cache(ctypes.Structure):
+    _fields_ = [("kv", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32)]
 
 
 class NAError(RuntimeError):
@@ -130,6 +149,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.na_pages_copy.argtypes = [I32, I32, pagedp, I32, P, P, P, P]
     lib.na_pages_compact.argtypes = [I32, I32, I32, pagedp, pagedp, P, P, I32, ropep, I32, I32,
                                      ctypes.c_uint32, P, P]
+    latp, lcachep, I64 = ctypes.POINTER(na_latent_cfg), ctypes.POINTER(na_paged_latent_cache), ctypes.c_int64
+    lib.na_latent_append_paged.argtypes = [latp, ropep, I32, P, P, I32, P, I64, P, I64, P, I64, P,
+                                           lcachep, P, P]
+    lib.na_attn_latent_paged.argtypes = [latp, I32, P, P, I32, I32, I32, P, lcachep, P, P, SZ, P, P]
+    lib.na_latent_paged_workspace_size.argtypes = [latp, I32, I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.na_attn_latent_expanded.argtypes = [latp, I32, P, P, P, I32, I32, I32, I32, P, P, P, I64, P, P,
+                                            P]
     lib.na_selftest_wait_timeout.argtypes = [P, P]
     lib.na_status_string.argtypes = [ctypes.c_int]
     lib.na_status_string.restype = ctypes.c_char_p
@@ -139,7 +165,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "na_selftest_wait_timeout", "na_rope_append_kv_paged",
                  "na_attn_prefill_chunk_paged", "na_attn_decode_paged",
                  "na_prefill_paged_workspace_size", "na_decode_paged_workspace_size",
-                 "na_pages_fork", "na_pages_copy", "na_pages_compact"):
+                 "na_pages_fork", "na_pages_copy", "na_pages_compact", "na_latent_append_paged",
+                 "na_attn_latent_paged", "na_latent_paged_workspace_size", "na_attn_latent_expanded"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -196,6 +223,26 @@ class RopeConfig:
 
 
 @dataclass
+class LatentConfig:
+    """Latent attention: num_heads heads over rows of kv_rank + rope_dim numbers a token."""
+    num_heads: int
+    kv_rank: int = 512
+    rope_dim: int = 64
+    nope_dim: int = 128
+    v_dim: int = 128
+    sm_scale: float = 0.0
+    rms_eps: float = 1e-6
+    kv_norm: bool = True
+    rope_interleaved: bool = False
+
+    def c(self) -> na_latent_cfg:
+        flags = ((NA_LATENT_NORM if self.kv_norm else 0)
+                 | (NA_ROPE_INTERLEAVED if self.rope_interleaved else 0))
+        return na_latent_cfg(self.num_heads, self.kv_rank, self.rope_dim, self.nope_dim, self.v_dim,
+                             self.sm_scale, self.rms_eps, flags)
+
+
+@dataclass
 class KVCache:
     """Caller-owned bf16 cache tensors [batch, num_kv_heads, capacity, head_dim]."""
     k: "object"
@@ -233,11 +280,17 @@ class PagedKVCache:
 class PagedLatentCache:
     """Caller-owned pages of latent rows and page table.
 
-    kv          bfloat16 [num_pages, page_size, row]: one row a token for all heads
+    kv          bfloat16 [num_pages, page_size, kv_rank + rope_dim]: one row a token for all heads
     page_table  int32 [batch, pages_per_seq], as PagedKVCache's
     """
     kv: "object"
     page_table: "object"
+
+    def c(self) -> na_paged_latent_cache:
+        num_pages, page_size, _ = self.kv.shape
+        batch, pages_per_seq = self.page_table.shape
+        return na_paged_latent_cache(_ptr(self.kv), _ptr(self.page_table), num_pages, page_size, batch,
+                                     pages_per_seq)
 
 
 # ---------------------------------------------------------------- helpers --
@@ -719,6 +772,130 @@ def na_pages_compact(cache, new_cache, keep_lens, max_keep: int, keep=None,
            lib.na_pages_compact(heads, d, batch, ctypes.byref(a), ctypes.byref(z), pk, pl, max_keep,
                                 r, int(rotary_start), 0 if r is None else int(rd),
                                 NA_ROPE_INTERLEAVED if interleaved else 0, st, _stream(stream)))
+
+
+def _latent_cache(cache: PagedLatentCache, cfg: LatentConfig, batch: int) -> na_paged_latent_cache:
+    """The C struct of a latent cache, its tensors checked."""
+    _want(cache.kv, "cache.kv", "bfloat16", (None, None, cfg.kv_rank + cfg.rope_dim))
+    _want(cache.page_table, "cache.page_table", "int32", (None, None), batch)
+    return cache.c()
+
+
+def _rows(t, name: str, width: int):
+    """Pointer and stride of rows of `width` bfloat16 elements, one behind the other at any distance
+    (the last part of wider rows, say); (None, 0) for None."""
+    if t is None:
+        return None, 0
+    _want(t, name, "bfloat16", (None,) * (t.dim() - 1) + (width,))
+    if not t.is_cuda:
+        raise ValueError("libna operates on CUDA tensors only")
+    if t.numel() == 0:
+        return None, width
+    lead = t.dim() - 2  # the dimension of the rows; those before it have to follow one another
+    if t.stride(-1) != 1 or any(t.shape[i] > 1 and t.stride(i) != t.stride(i + 1) * t.shape[i + 1]
+                                for i in range(lead)):
+        raise ValueError(f"{name}: rows have to be contiguous and equally far apart")
+    if t.shape[lead] > 1:
+        return t.data_ptr(), t.stride(lead)
+    # one row in the last such dimension: the next one's stride is the distance
+    for i in range(lead - 1, -1, -1):
+        if t.shape[i] > 1:
+            return t.data_ptr(), t.stride(i)
+    return t.data_ptr(), max(t.stride(lead), width)
+
+
+def na_latent_append_paged(cfg: LatentConfig, rope: RopeConfig, cu_seqlens, cache_lens, kv, q, q_out,
+                           cache: PagedLatentCache, kv_norm_w=None, status=None,
+                           total_tokens: Optional[int] = None, stream=None):
+    """New tokens' latent rows kv [T, kv_rank + rope_dim] into their pages (normed, their rotated part
+    turned), and q_out = RoPE(q), both [T, H, rope_dim] and views of wider rows where wanted (or
+    None)."""
+    lib = load_library()
+    T = int(kv.shape[0]) if total_tokens is None else int(total_tokens)
+    batch = int(cu_seqlens.numel()) - 1
+    _want(cu_seqlens, "cu_seqlens", "int32", (None,))
+    _want(cache_lens, "cache_lens", "int32", (None,), batch)
+    _want(kv, "kv", "bfloat16", (None, None), T)
+    for t, name in ((q, "q"), (q_out, "q_out")):
+        _want(t, name, "bfloat16", (None, cfg.num_heads, cfg.rope_dim), T)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    _want(kv_norm_w, "kv_norm_w", "bfloat16", (cfg.kv_rank,))
+    _want(status, "status", "int32", (None,), 1)
+    kc = _latent_cache(cache, cfg, batch)
+    pkv, kv_stride = _rows(kv, "kv", cfg.kv_rank + cfg.rope_dim)
+    pq, q_stride = _rows(q, "q", cfg.rope_dim)
+    po, out_stride = _rows(q_out, "q_out", cfg.rope_dim)
+    c, r = cfg.c(), rope.c()
+    cu, lens, w, st = [_ptr(t) for t in (cu_seqlens, cache_lens, kv_norm_w, status)]
+    _on_current(cu_seqlens, cache_lens, kv, q, q_out, kv_norm_w, status, cache.kv, cache.page_table)
+    _check("na_latent_append_paged",
+           lib.na_latent_append_paged(ctypes.byref(c), ctypes.byref(r), batch, cu, lens, T, pkv,
+                                      kv_stride, pq, q_stride, po, out_stride, w, ctypes.byref(kc),
+                                      st, _stream(stream)))
+
+
+def na_latent_paged_workspace_size(cfg: LatentConfig, batch: int, total_tokens: int, max_new_len: int,
+                                   max_total_len: int) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    c = cfg.c()
+    _check("na_latent_paged_workspace_size",
+           lib.na_latent_paged_workspace_size(ctypes.byref(c), batch, total_tokens, max_new_len,
+                                              max_total_len, ctypes.byref(out)))
+    return int(out.value)
+
+
+def na_attn_latent_paged(cfg: LatentConfig, cu_seqlens, cache_lens, max_new_len: int,
+                         max_total_len: int, q_lat, cache: PagedLatentCache, out, workspace=None,
+                         status=None, total_tokens: Optional[int] = None, stream=None):
+    """Absorbed latent attention of new tokens (single ones or chunks) against the pages: q_lat
+    [T, H, kv_rank + rope_dim], out [T, H, kv_rank] (workspace: na_latent_paged_workspace_size)."""
+    lib = load_library()
+    T = int(q_lat.shape[0]) if total_tokens is None else int(total_tokens)
+    batch, H = int(cu_seqlens.numel()) - 1, cfg.num_heads
+    _want(cu_seqlens, "cu_seqlens", "int32", (None,))
+    _want(cache_lens, "cache_lens", "int32", (None,), batch)
+    _want(q_lat, "q_lat", "bfloat16", (None, H, cfg.kv_rank + cfg.rope_dim), T)
+    _want(out, "out", "bfloat16", (None, H, cfg.kv_rank), T)
+    _want(status, "status", "int32", (None,), 1)
+    kc = _latent_cache(cache, cfg, batch)
+    c = cfg.c()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    cu, lens, pq, po, ws, st = [_ptr(t) for t in (cu_seqlens, cache_lens, q_lat, out, workspace, status)]
+    _on_current(cu_seqlens, cache_lens, q_lat, out, workspace, status, cache.kv, cache.page_table)
+    _check("na_attn_latent_paged",
+           lib.na_attn_latent_paged(ctypes.byref(c), batch, cu, lens, T, int(max_new_len),
+                                    int(max_total_len), pq, ctypes.byref(kc), po, ws, ws_bytes, st,
+                                    _stream(stream)))
+
+
+def na_attn_latent_expanded(cfg: LatentConfig, cu_seqlens, key_starts, key_lens, max_new_len: int,
+                            max_key_len: int, q, kv, k_pe, out, status=None,
+                            total_tokens: Optional[int] = None, stream=None):
+    """Expanded latent attention, causal: q [T, H, nope_dim + rope_dim] against kv [keys, H,
+    nope_dim + v_dim] and the shared k_pe [keys, rope_dim] (a view of wider rows where wanted); out
+    [T, H, v_dim].  Sequence b's keys are rows key_starts[b] .. + key_lens[b] - 1."""
+    lib = load_library()
+    T = int(q.shape[0]) if total_tokens is None else int(total_tokens)
+    batch, H = int(cu_seqlens.numel()) - 1, cfg.num_heads
+    _want(cu_seqlens, "cu_seqlens", "int32", (None,))
+    _want(key_starts, "key_starts", "int32", (None,), batch)
+    _want(key_lens, "key_lens", "int32", (None,), batch)
+    _want(q, "q", "bfloat16", (None, H, cfg.nope_dim + cfg.rope_dim), T)
+    _want(kv, "kv", "bfloat16", (None, H, cfg.nope_dim + cfg.v_dim))
+    _want(k_pe, "k_pe", "bfloat16", (None, None), int(kv.shape[0]))
+    _want(out, "out", "bfloat16", (None, H, cfg.v_dim), T)
+    _want(status, "status", "int32", (None,), 1)
+    pe, stride = _rows(k_pe, "k_pe", cfg.rope_dim)
+    c = cfg.c()
+    cu, starts, lens, pq, pkv, po, st = [
+        _ptr(t) for t in (cu_seqlens, key_starts, key_lens, q, kv, out, status)]
+    _on_current(cu_seqlens, key_starts, key_lens, q, kv, k_pe, out, status)
+    _check("na_attn_latent_expanded",
+           lib.na_attn_latent_expanded(ctypes.byref(c), batch, cu, starts, lens, T, int(kv.shape[0]),
+                                       int(max_new_len), int(max_key_len), pq, pkv, pe, stride, po, st,
+                                       _stream(stream)))
 
 
 def na_selftest_wait_timeout(status, stream=None):

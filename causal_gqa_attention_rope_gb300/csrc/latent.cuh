@@ -1,0 +1,51 @@
+// latent.cuh -- parameters of the latent attention kernels, filled in by the C ABI
+// (latent_api.cu).
+#pragma once
+
+#include "na_internal.cuh"
+
+struct LatentAppendParams {
+    int H, R, rd, batch, capacity, total_tokens;
+    int normed, interleaved;
+    float eps, rope_scale;
+    const int32_t *cu_seqlens, *cache_lens;
+    const bf16 *kv, *q, *norm_w;
+    bf16 *q_out, *cache;
+    long long kv_stride, q_stride, q_out_stride;  // elements
+    int32_t *status;
+};
+
+struct LatentParams {
+    int H, R, rd, batch, capacity;
+    float scale_log2;          // score scale * log2(e)
+    int total_tokens, max_new_len, max_total_len;
+    int grid;                  // CTAs, each taking an equal run of key tiles
+    const int32_t *cu_seqlens, *cache_lens;
+    const bf16 *q, *cache;
+    bf16 *out;
+    float *part_o;             // [2 grid][64][R]: rows of a cut unit, CTA c's first piece at 2 c
+    float *part_ml;            // [2 grid][64][2]: (max, sum), log2 domain
+    int4 *cut;                 // [grid]: of the unit that CTA c begins and others finish
+    int32_t *status;
+};
+
+struct ExpandedParams {
+    int H, dn, rd, dv, batch;
+    float scale_log2;
+    int total_tokens, total_keys, max_new_len, max_key_len;
+    int q_tiles;
+    const int32_t *cu_seqlens, *key_starts, *key_lens;
+    const bf16 *q, *kv, *k_pe;
+    long long k_pe_stride;     // elements
+    bf16 *out;
+    int32_t *status;
+};
+
+constexpr int kLatentRows = 64;  // query rows (token, head) of a unit
+constexpr int kLatentKeys = 64;  // keys of a tile
+constexpr int kExpandedRows = 128;  // query tokens of an expanded tile
+
+cudaError_t launch_latent_append(const LatentAppendParams &p, const PagedView &pg,
+                                 const RopeTurns &turns, cudaStream_t stream);
+cudaError_t launch_latent(const LatentParams &p, const PagedView &pg, cudaStream_t stream);
+cudaError_t launch_latent_expanded(const ExpandedParams &p, cudaStream_t stream);

@@ -1,0 +1,246 @@
+// latent_api.cu -- C ABI of latent attention: argument validation, launch planning and
+// kernel launches.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "latent.cuh"
+#include "na_host.cuh"
+
+namespace {
+
+int check_cfg(const na_latent_cfg *c)
+{
+    if (!c || c->num_heads <= 0)
+        return NA_ERR_INVALID_ARG;
+    if (c->flags & ~(NA_LATENT_NORM | NA_ROPE_INTERLEAVED))
+        return NA_ERR_INVALID_ARG;
+    if (!(c->rms_eps >= 0.f) || !std::isfinite(c->sm_scale))
+        return NA_ERR_INVALID_ARG;
+    if ((c->kv_rank != 128 && c->kv_rank != 256 && c->kv_rank != 512) ||
+        (c->nope_dim != 64 && c->nope_dim != 128) || (c->v_dim != 64 && c->v_dim != 128))
+        return NA_ERR_UNSUPPORTED;
+    if (c->rope_dim < 16 || c->rope_dim > 64 || c->rope_dim % 16 != 0)
+        return NA_ERR_UNSUPPORTED;
+    return NA_OK;
+}
+
+float score_scale_log2(const na_latent_cfg *c)
+{
+    const double s = c->sm_scale > 0.f ? (double)c->sm_scale
+                                       : 1.0 / sqrt((double)(c->nope_dim + c->rope_dim));
+    return (float)(s * 1.4426950408889634);
+}
+
+int check_cache(const na_paged_latent_cache *c, int batch, PagedView *view)
+{
+    if (!c || !c->kv || !c->page_table || c->num_pages <= 0 || c->pages_per_seq <= 0 ||
+        c->batch < batch || !aligned16(c->kv))
+        return NA_ERR_INVALID_ARG;
+    const int log = page_size_log(c->page_size);
+    if (log < 0 || c->num_pages > (0x7fffffff >> log) || c->pages_per_seq > (0x7fffffff >> log))
+        return NA_ERR_UNSUPPORTED;
+    *view = PagedView{c->page_table, c->pages_per_seq, c->num_pages, log, nullptr, nullptr};
+    return NA_OK;
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
+
+struct LatentPlan {
+    int grid;
+    size_t part_o, ws_bytes;
+};
+
+// One CTA per SM, fewer where the bounds allow no more tiles than that.
+LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int max_total_len)
+{
+    LatentPlan pl{};
+    const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
+    const double tiles = (double)batch * ceil_div((long long)max_new_len * c->num_heads, kLatentRows) *
+                         ceil_div(max_total_len, kLatentKeys);
+    pl.grid = (int)std::max(1.0, std::min((double)sm_count(), tiles));
+    pl.part_o = (size_t)2 * pl.grid * kLatentRows * c->kv_rank;
+    pl.ws_bytes = (pl.part_o + (size_t)2 * pl.grid * kLatentRows * 2) * sizeof(float) +
+                  pl.grid * sizeof(int4);
+    return pl;
+}
+
+}  // namespace
+
+extern "C" {
+
+int na_latent_append_paged(const na_latent_cfg *cfg, const na_rope_params *rope, int32_t batch,
+                           const int32_t *cu_seqlens, const int32_t *cache_lens,
+                           int32_t total_tokens, const void *kv, int64_t kv_stride, const void *q,
+                           int64_t q_stride, void *q_out, int64_t q_out_stride,
+                           const void *kv_norm_w, const na_paged_latent_cache *cache,
+                           int32_t *status, void *stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if ((rc = check_rope(rope)) != NA_OK)
+        return rc;
+    if (batch <= 0 || total_tokens < 0)
+        return NA_ERR_INVALID_ARG;
+    PagedView pg;
+    if ((rc = check_cache(cache, batch, &pg)) != NA_OK)
+        return rc;
+    if (total_tokens == 0)
+        return NA_OK;
+    if (!cu_seqlens || !cache_lens || !kv || !aligned16(kv) || !q != !q_out || !aligned16(q) ||
+        !aligned16(q_out))
+        return NA_ERR_INVALID_ARG;
+    if (kv_stride % 8 != 0 || kv_stride < cfg->kv_rank + cfg->rope_dim)
+        return NA_ERR_INVALID_ARG;
+    if (q && (q_stride % 8 != 0 || q_stride < cfg->rope_dim || q_out_stride % 8 != 0 ||
+              q_out_stride < cfg->rope_dim || (q == q_out && q_stride != q_out_stride)))
+        return NA_ERR_INVALID_ARG;
+    const bool normed = (cfg->flags & NA_LATENT_NORM) != 0;
+    if (normed && (!kv_norm_w || !aligned16(kv_norm_w)))
+        return NA_ERR_INVALID_ARG;
+    const RopeTable &table = rope_table(rope, cfg->rope_dim);
+    LatentAppendParams p{};
+    p.H = cfg->num_heads;
+    p.R = cfg->kv_rank;
+    p.rd = cfg->rope_dim;
+    p.batch = batch;
+    p.capacity = cache->pages_per_seq * cache->page_size;
+    p.total_tokens = total_tokens;
+    p.normed = normed;
+    p.interleaved = (cfg->flags & NA_ROPE_INTERLEAVED) != 0;
+    p.eps = cfg->rms_eps;
+    p.rope_scale = table.scale;
+    p.cu_seqlens = cu_seqlens;
+    p.cache_lens = cache_lens;
+    p.kv = static_cast<const bf16 *>(kv);
+    p.q = static_cast<const bf16 *>(q);
+    p.norm_w = static_cast<const bf16 *>(kv_norm_w);
+    p.q_out = static_cast<bf16 *>(q_out);
+    p.cache = static_cast<bf16 *>(cache->kv);
+    p.kv_stride = kv_stride;
+    p.q_stride = q_stride;
+    p.q_out_stride = q_out_stride;
+    p.status = status;
+    return done(launch_latent_append(p, pg, table.turns, static_cast<cudaStream_t>(stream)));
+}
+
+int na_latent_paged_workspace_size(const na_latent_cfg *cfg, int32_t batch, int32_t total_tokens,
+                                   int32_t max_new_len, int32_t max_total_len, size_t *bytes)
+{
+    const int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if (!bytes || batch <= 0 || total_tokens < 0 || max_new_len < 0 || max_total_len < 0)
+        return NA_ERR_INVALID_ARG;
+    *bytes = plan_latent(cfg, batch, max_new_len, max_total_len).ws_bytes;
+    return NA_OK;
+}
+
+int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
+                         const int32_t *cache_lens, int32_t total_tokens, int32_t max_new_len,
+                         int32_t max_total_len, const void *q_lat,
+                         const na_paged_latent_cache *cache, void *out, void *workspace,
+                         size_t ws_bytes, int32_t *status, void *stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if (batch <= 0 || total_tokens < 0 || max_new_len < 0 || max_total_len < 0)
+        return NA_ERR_INVALID_ARG;
+    PagedView pg;
+    if ((rc = check_cache(cache, batch, &pg)) != NA_OK)
+        return rc;
+    if (total_tokens == 0)
+        return NA_OK;
+    if (!cu_seqlens || !cache_lens || !q_lat || !out || max_new_len <= 0 || !aligned16(q_lat) ||
+        !aligned16(out))
+        return NA_ERR_INVALID_ARG;
+    const int capacity = cache->pages_per_seq * cache->page_size;
+    if (max_total_len > capacity)
+        return NA_ERR_CAPACITY;
+    // query rows are addressed by 32-bit tensor-map coordinates
+    if ((long long)total_tokens * cfg->num_heads > INT_MAX - kLatentRows)
+        return NA_ERR_UNSUPPORTED;
+    // (a sequence has no more new tokens than the call)
+    max_new_len = std::min(max_new_len, total_tokens);
+    const LatentPlan pl = plan_latent(cfg, batch, max_new_len, max_total_len);
+    if (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace))
+        return NA_ERR_WORKSPACE;
+    LatentParams p{};
+    p.H = cfg->num_heads;
+    p.R = cfg->kv_rank;
+    p.rd = cfg->rope_dim;
+    p.batch = batch;
+    p.capacity = capacity;
+    p.scale_log2 = score_scale_log2(cfg);
+    p.total_tokens = total_tokens;
+    p.max_new_len = max_new_len;
+    p.max_total_len = max_total_len;
+    p.grid = pl.grid;
+    p.cu_seqlens = cu_seqlens;
+    p.cache_lens = cache_lens;
+    p.q = static_cast<const bf16 *>(q_lat);
+    p.cache = static_cast<const bf16 *>(cache->kv);
+    p.out = static_cast<bf16 *>(out);
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = p.part_o + pl.part_o;
+    p.cut = reinterpret_cast<int4 *>(p.part_ml + (size_t)2 * pl.grid * kLatentRows * 2);
+    p.status = status;
+    if ((rc = bind_context()) != NA_OK)
+        return rc;
+    return done(launch_latent(p, pg, static_cast<cudaStream_t>(stream)));
+}
+
+int na_attn_latent_expanded(const na_latent_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
+                            const int32_t *key_starts, const int32_t *key_lens,
+                            int32_t total_tokens, int32_t total_keys, int32_t max_new_len,
+                            int32_t max_key_len, const void *q, const void *kv, const void *k_pe,
+                            int64_t k_pe_stride, void *out, int32_t *status, void *stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc != NA_OK)
+        return rc;
+    if (batch <= 0 || total_tokens < 0 || total_keys < 0 || max_new_len < 0 || max_key_len < 0)
+        return NA_ERR_INVALID_ARG;
+    if (total_tokens == 0)
+        return NA_OK;
+    if (!cu_seqlens || !key_starts || !key_lens || !q || !kv || !k_pe || !out || max_new_len <= 0 ||
+        total_keys == 0)
+        return NA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv) || !aligned16(k_pe) || !aligned16(out) ||
+        k_pe_stride % 8 != 0 || k_pe_stride < cfg->rope_dim)
+        return NA_ERR_INVALID_ARG;
+    if ((long long)k_pe_stride >= (1ll << 32) ||
+        (long long)std::max(total_tokens, total_keys) * cfg->num_heads >= (1ll << 40))
+        return NA_ERR_UNSUPPORTED;
+    max_new_len = std::min(max_new_len, total_tokens);
+    ExpandedParams p{};
+    p.q_tiles = (max_new_len + kExpandedRows - 1) / kExpandedRows;
+    if ((double)p.q_tiles * cfg->num_heads * batch > INT_MAX)
+        return NA_ERR_UNSUPPORTED;
+    p.H = cfg->num_heads;
+    p.dn = cfg->nope_dim;
+    p.rd = cfg->rope_dim;
+    p.dv = cfg->v_dim;
+    p.batch = batch;
+    p.scale_log2 = score_scale_log2(cfg);
+    p.total_tokens = total_tokens;
+    p.total_keys = total_keys;
+    p.max_new_len = max_new_len;
+    p.max_key_len = max_key_len;
+    p.cu_seqlens = cu_seqlens;
+    p.key_starts = key_starts;
+    p.key_lens = key_lens;
+    p.q = static_cast<const bf16 *>(q);
+    p.kv = static_cast<const bf16 *>(kv);
+    p.k_pe = static_cast<const bf16 *>(k_pe);
+    p.k_pe_stride = k_pe_stride;
+    p.out = static_cast<bf16 *>(out);
+    p.status = status;
+    if ((rc = bind_context()) != NA_OK)
+        return rc;
+    return done(launch_latent_expanded(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,801 @@
+// latent_attn.cu -- absorbed latent attention over pages (na_attn_latent_paged), on
+// the sm_100-family tensor cores (tcgen05 + TMEM + TMA).
+//
+// A unit is 64 query rows -- (token, head) pairs of one sequence, token-major -- and
+// the key tiles of 64 cached rows that they see.  For each tile
+//     S   [64 rows x 64 keys]  = Q K^T      M = 64, K = R + 64 (rope part padded by TMA's
+//                                           zeros to a whole column block)
+//     O^T [R dims x 64 rows]  += V^T P^T    M = 128 per block of dims, K = 64 keys
+// where V is the first R columns of the K tile in shared memory: K-major as K, M-major
+// as V^T.  With the rows along N the accumulators of R = 512 take 256 columns of
+// tensor memory, where rows along M would take all 512 and leave none to S, and M =
+// 128 runs at the full rate.  A row's bytes come from memory once for all heads.
+//
+// Warps: 0 producer (TMA: Q of a unit, then its tiles, a box per page and 64 columns),
+// 1 issues S into one of two buffers, 2 issues O^T, 4 .. 7 softmax, 16 rows each
+// (M = 64 puts row r into lane 32 (r / 16) + r % 16), four lanes to a row, each 16
+// of a tile's keys.  Max and sum are kept per row in fp32; the reference maximum is
+// raised only when a score exceeds it by more than 2^8, and then all four warps
+// rescale the columns of O^T by the factors in shared memory.
+//
+// Work: the key tiles of all units, one after the other, are cut into one equal run
+// per CTA (one CTA per SM), whatever the lengths.  A unit that a cut goes through is
+// left in pieces (unnormalised rows with maximum and sum) which a second pass
+// joins.  CTA c has at most two: the end of a unit that an earlier CTA began (slot 2
+// c) and the beginning of one that others finish (slot 2 c + 1).
+#include <climits>
+
+#include "latent.cuh"
+#include "tc_primitives.cuh"
+#include "tile_waits.cuh"
+
+namespace {
+
+constexpr int QR = kLatentRows, KT = kLatentKeys;
+constexpr int THREADS = 256;
+constexpr uint32_t BLOCK_BYTES = 64 * 128;  // 64 rows of 64 bf16: a column block of Q or of a tile
+
+template <int R>
+struct __align__(1024) LatentSmem {
+    static constexpr int CB = R / 64 + 1;                 // column blocks of a row
+    static constexpr int STAGES = R == 512 ? 2 : 4;
+    bf16 q[CB][QR * 64];
+    bf16 kv[STAGES][CB][KT * 64];
+    bf16 p[QR * 64];
+    float factor[2][QR];       // a tile's corrections by row, by tile parity
+    float inv[QR];             // at a piece's end: 1 / sum, or 1
+    uint64_t q_full, q_empty, kv_full[STAGES], kv_empty[STAGES], s_full[2], s_empty[2], p_full,
+        pv_done, o_empty, drain[2];
+    long long warp_tiles[THREADS / 32];
+    long long total, begin;
+    int b0, t0, tile0;         // where the CTA's run begins
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct Sequence {
+    int tok0, n, prior;
+};
+
+// Sequence b; n = 0 where it breaks the call's bounds (`code` says how).
+__device__ __forceinline__ Sequence sequence_of(const LatentParams &p, int b, int &code)
+{
+    Sequence s;
+    s.tok0 = __ldg(p.cu_seqlens + b);
+    s.n = __ldg(p.cu_seqlens + b + 1) - s.tok0;
+    s.prior = __ldg(p.cache_lens + b);
+    code = NA_OK;
+    if (s.n > p.max_new_len || s.tok0 < 0 || (b == 0 && s.tok0 != 0) ||
+        (long long)s.tok0 + s.n > p.total_tokens)
+        code = NA_ERR_INVALID_ARG;
+    else if (s.n > 0 && (s.prior < 0 || (long long)s.prior + s.n > min(p.capacity, p.max_total_len)))
+        code = NA_ERR_CAPACITY;
+    if (code != NA_OK || s.n < 0)
+        s.n = 0;
+    return s;
+}
+
+__device__ __forceinline__ int units_of(const LatentParams &p, const Sequence &s)
+{
+    return (s.n * p.H + QR - 1) / QR;
+}
+
+// Keys that the rows of unit t see, and their tiles.
+__device__ __forceinline__ int keys_of(const LatentParams &p, const Sequence &s, int t)
+{
+    return s.prior + (min(t * QR + QR, s.n * p.H) - 1) / p.H + 1;
+}
+
+__device__ __forceinline__ int tiles_of(const LatentParams &p, const Sequence &s, int t)
+{
+    return (keys_of(p, s, t) + KT - 1) / KT;
+}
+
+// Tiles of the sequences 32 `chunk` + lane, a warp at a time: each lane its own, or, where
+// one of them has many units, all lanes together one sequence after the other.
+__device__ __forceinline__ long long chunk_tiles(const LatentParams &p, int chunk, int lane)
+{
+    const int b = chunk * 32 + lane;
+    Sequence s{0, 0, 0};
+    int code = NA_OK;
+    if (b < p.batch)
+        s = sequence_of(p, b, code);
+    if (code != NA_OK && blockIdx.x == 0)
+        na_report(p.status, code);
+    const int units = units_of(p, s);
+    long long sum = 0;
+    if (!__any_sync(0xffffffffu, units > 16)) {
+        for (int t = 0; t < units; t++)
+            sum += tiles_of(p, s, t);
+        return sum;
+    }
+    for (int i = 0; i < 32; i++) {
+        const Sequence o{0, __shfl_sync(0xffffffffu, s.n, i), __shfl_sync(0xffffffffu, s.prior, i)};
+        long long x = 0;
+        for (int t = lane; t < units_of(p, o); t += 32)
+            x += tiles_of(p, o, t);
+#pragma unroll
+        for (int k = 16; k; k >>= 1)
+            x += __shfl_xor_sync(0xffffffffu, x, k);
+        if (lane == i)
+            sum = x;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ long long inclusive_sum(long long x, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    return x;
+}
+
+// CTAs that have work (all others have empty runs), and the first tile of CTA c's run; the
+// runs of `total` tiles are as equal as can be, none of them empty.
+__device__ __forceinline__ long long busy_ctas(const LatentParams &p, long long total)
+{
+    return min((long long)p.grid, total);
+}
+
+__device__ __forceinline__ long long run_begin(const LatentParams &p, long long total, int c)
+{
+    const long long busy = busy_ctas(p, total);
+    return c >= busy ? total : total * c / busy;
+}
+
+// The CTA whose run holds the tile before `end`: the last c with total c / busy < end.
+__device__ __forceinline__ int run_of(const LatentParams &p, long long total, long long end)
+{
+    return (int)((end * busy_ctas(p, total) + total - 1) / total) - 1;
+}
+
+// The CTA's run: sm.total, sm.begin and the unit and tile that it begins with.  Each warp
+// sums a range of sequences; the one whose range holds the beginning looks it up.
+template <int R>
+__device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R> &sm, int warp, int lane)
+{
+    constexpr int WARPS = THREADS / 32;
+    const int chunks = (p.batch + 31) / 32, per = (chunks + WARPS - 1) / WARPS;
+    const int c0 = min(warp * per, chunks), c1 = min(c0 + per, chunks);
+    long long mine = 0, chunk_sum = 0;  // (a single chunk's sums are kept)
+    for (int c = c0; c < c1; c++) {
+        chunk_sum = chunk_tiles(p, c, lane);
+        mine += chunk_sum;
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1)
+        mine += __shfl_xor_sync(0xffffffffu, mine, k);
+    if (lane == 0)
+        sm.warp_tiles[warp] = mine;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) {
+        before += w < warp ? sm.warp_tiles[w] : 0;
+        total += sm.warp_tiles[w];
+    }
+    const long long begin = run_begin(p, total, blockIdx.x);
+    if (threadIdx.x == 0) {
+        sm.total = total;
+        sm.begin = begin;
+    }
+    if (begin >= before && begin < before + mine) {
+        for (int c = c0; c < c1; c++) {
+            if (per > 1)
+                chunk_sum = chunk_tiles(p, c, lane);
+            const long long upto = inclusive_sum(chunk_sum, lane);
+            const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
+            if (past) {
+                const int i = __ffs(past) - 1, b = c * 32 + i;
+                before += __shfl_sync(0xffffffffu, upto - chunk_sum, i);
+                int code;
+                const Sequence s = sequence_of(p, b, code);
+                for (int t = 0;; t += 32) {
+                    const long long x = t + lane < units_of(p, s) ? tiles_of(p, s, t + lane) : 0;
+                    const long long y = inclusive_sum(x, lane);
+                    const unsigned m = __ballot_sync(0xffffffffu, before + y > begin);
+                    if (m) {
+                        const int k = __ffs(m) - 1;
+                        if (lane == k) {
+                            sm.b0 = b;
+                            sm.t0 = t + k;
+                            sm.tile0 = (int)(begin - (before + y - x));
+                        }
+                        break;
+                    }
+                    before += __shfl_sync(0xffffffffu, y, 31);
+                }
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// One after the other, the pieces of the CTA's run.  Every warp role walks them for itself.
+struct Walk {
+    int b, t, tile;       // next: sequence, unit, tile of it
+    long long left;       // tiles of the run from there
+    Sequence s;
+    bool have;
+
+    // the piece: tiles [lo, hi) of unit `unit` of sequence s
+    int unit, lo, hi, tiles, keys;
+
+    template <int R>
+    __device__ __forceinline__ Walk(const LatentParams &p, const LatentSmem<R> &sm)
+        : b(sm.b0), t(sm.t0), tile(sm.tile0),
+          left(run_begin(p, sm.total, blockIdx.x + 1) - sm.begin), have(false)
+    {
+    }
+
+    __device__ __forceinline__ bool next(const LatentParams &p)
+    {
+        if (left <= 0)
+            return false;
+        int code;
+        while (!have) {
+            s = sequence_of(p, b, code);
+            have = t < units_of(p, s);
+            if (!have) {
+                b++;
+                t = 0;
+            }
+        }
+        unit = t;
+        keys = keys_of(p, s, t);
+        tiles = (keys + KT - 1) / KT;
+        lo = tile;
+        hi = (int)min((long long)tiles, lo + left);
+        left -= hi - lo;
+        tile = 0;
+        t++;
+        have = t < units_of(p, s);
+        if (!have) {
+            b++;
+            t = 0;
+        }
+        return true;
+    }
+
+    __device__ __forceinline__ int rows(const LatentParams &p) const
+    {
+        return min(QR, s.n * p.H - unit * QR);
+    }
+    __device__ __forceinline__ long long row0(const LatentParams &p) const
+    {
+        return (long long)s.tok0 * p.H + unit * QR;
+    }
+};
+
+// 16 lanes x 64 columns of tensor memory: thread l gets columns 8 i + 2 (l % 4) + {0, 1}
+// of lane l / 4 in r[4 i], r[4 i + 1] and of lane l / 4 + 8 in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Barrier of the four softmax warps that also says whether any thread's `x` holds.
+__device__ __forceinline__ bool softmax_any(bool x)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(x ? 1u : 0u)
+        : "memory");
+    return any != 0;
+}
+
+template <int R>
+__global__ void __launch_bounds__(THREADS, 1)
+    latent_attn_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ PagedView pg,
+                       const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_kv)
+{
+    typedef LatentSmem<R> Smem;
+    constexpr int CB = Smem::CB, STAGES = Smem::STAGES;
+    constexpr int DB = R / 128;                        // blocks of 128 dims: M of O^T
+    constexpr uint32_t S_COL = DB * QR;                // O^T block d at column 64 d, then S
+    constexpr uint32_t TMEM_COLS = S_COL + 128 <= 256 ? 256 : 512;
+    extern __shared__ uint8_t smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&map_q);
+        tc::prefetch_tmap(&map_kv);
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 1);
+        for (int i = 0; i < STAGES; i++) {
+            mbar_init(&sm.kv_full[i], 1);
+            mbar_init(&sm.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_empty[i], 4);
+            mbar_init(&sm.drain[i], 1);
+        }
+        mbar_init(&sm.p_full, 4);
+        mbar_init(&sm.pv_done, 1);
+        mbar_init(&sm.o_empty, 4);
+        sm.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1)
+        tc::tmem_alloc(&sm.tmem_base, TMEM_COLS);
+    grid_dependency_wait();
+    grid_dependents_launch();
+    tc::fence_before_sync();
+    find_run<R>(p, sm, warp, lane);
+    tc::fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    Walk w(p, sm);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer --
+        const int box_log = min(pg.page_log, 6), boxes = KT >> box_log;
+        const int in_page = (1 << pg.page_log) - 1;
+        const uint64_t policy = l2_policy_evict_first();
+        const bool read_once = p.max_new_len * p.H <= QR;  // one unit a sequence
+        int g = 0, pieces = 0;
+        bool ok = true;
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+            if (!warp_wait(bar, parity, &sm.abort_flag)) {
+                if (lane == 0)
+                    set_abort(&sm.abort_flag, p.status);
+                ok = false;
+            }
+            return ok;
+        };
+        for (; ok && w.next(p); pieces++) {
+            const int32_t *row = pg.table + (size_t)(w.t ? w.b : w.b - 1) * pg.pages_per_seq;
+            // this lane's page of a tile (boxes of them), or -1
+            auto page_of = [&](int j) {
+                const int at = j * KT + (lane << box_log);
+                if (lane >= boxes || j >= w.hi || at >= w.keys)
+                    return -1;
+                int id = __ldg(row + (at >> pg.page_log));
+                if ((unsigned)id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
+                    na_report(p.status, NA_ERR_PAGE);
+                    id = 0;
+                }
+                return id;
+            };
+            int id = page_of(w.lo);
+            if (pieces > 0 && !wait_all(&sm.q_empty, (pieces - 1) & 1))
+                break;
+            if (lane == 0)
+                mbar_arrive_expect_tx(&sm.q_full, CB * BLOCK_BYTES);
+            __syncwarp();
+            if (lane < CB)
+                tc::tma_load_2d(sm.q[lane], &map_q, lane * 64, (int)w.row0(p), &sm.q_full);
+            for (int j = w.lo; j < w.hi; j++, g++) {
+                const int st = g % STAGES;
+                const int next = page_of(j + 1);
+                if (!wait_all(&sm.kv_empty[st], ((g / STAGES) & 1) ^ 1))
+                    break;
+                const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sm.kv_full[st], n * CB * (128u << box_log));
+                __syncwarp();
+                const int first = (id << pg.page_log) + (pg.page_log > 6 ? (j * KT) & in_page : 0);
+                for (int i0 = 0; i0 < boxes * CB; i0 += 32) {
+                    const int i = i0 + lane, box = i & (boxes - 1), cb = i / boxes;
+                    const int from = __shfl_sync(0xffffffffu, first, box);
+                    if (box < n && cb < CB) {
+                        bf16 *dst = sm.kv[st][cb] + (box << box_log) * 64;
+                        if (read_once)
+                            tc::tma_load_2d_hint(dst, &map_kv, cb * 64, from, &sm.kv_full[st], policy);
+                        else
+                            tc::tma_load_2d(dst, &map_kv, cb * 64, from, &sm.kv_full[st]);
+                    }
+                }
+                id = next;
+            }
+        }
+        // every copy issued lands before the CTA can exit
+        if (lane == 0) {
+            if (pieces > 0)
+                drain_wait(&sm.q_full, (pieces - 1) & 1, p.status);
+            for (int i = g - 1; i >= 0 && i >= g - STAGES; i--)
+                drain_wait(&sm.kv_full[i % STAGES], (i / STAGES) & 1, p.status);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------- S = Q K^T issue --
+        if (elect_one()) {
+            constexpr uint32_t idesc = tc::idesc_bf16_f32(QR, KT, false, false);
+            constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
+            const uint64_t qd = tc::desc_kmajor_sw128(smem_addr(sm.q[0]));
+            const uint64_t kd0 = tc::desc_kmajor_sw128(smem_addr(sm.kv[0][0]));
+            bool ok = true;
+            int g = 0;
+            for (int piece = 0; ok && w.next(p); piece++) {
+                ok = mbar_wait_bounded(&sm.q_full, piece & 1);
+                for (int j = w.lo; ok && j < w.hi; j++, g++) {
+                    const int st = g % STAGES, sb = g & 1;
+                    ok = mbar_wait_bounded(&sm.kv_full[st], (g / STAGES) & 1);
+                    if (ok && g >= 2)
+                        ok = mbar_wait_bounded(&sm.s_empty[sb], ((g >> 1) - 1) & 1);
+                    if (!ok || aborted(&sm.abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint64_t kd = kd0 + (uint64_t)(st * CB * BLOCK16);
+                    const uint32_t s_t = tmem + S_COL + sb * KT;
+#pragma unroll
+                    for (int k = 0; k < CB * 4; k++) {
+                        const uint32_t off = (k >> 2) * BLOCK16 + (k & 3) * 2;
+                        tc::mma_ss(s_t, qd + off, kd + off, idesc, k > 0);
+                    }
+                    tc::mma_commit(&sm.s_full[sb]);
+                    if (j == w.hi - 1)
+                        tc::mma_commit(&sm.q_empty);
+                }
+            }
+            if (!ok)
+                set_abort(&sm.abort_flag, p.status);
+            if (g > 0) {  // all issued MMAs complete before tensor memory is released
+                tc::mma_commit(&sm.drain[0]);
+                drain_wait(&sm.drain[0], 0, p.status);
+            }
+        }
+    } else if (warp == 2) {
+        // ----------------------------------------------------- O^T += V^T P^T issue --
+        if (elect_one()) {
+            constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
+            const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_addr(sm.kv[0][0]), BLOCK_BYTES);
+            const uint64_t pd = tc::desc_kmajor_sw128(smem_addr(sm.p));
+            bool ok = true;
+            int g = 0;
+            for (int piece = 0; ok && w.next(p); piece++) {
+                // the rows' columns in whole sixteens
+                const uint32_t idesc =
+                    tc::idesc_bf16_f32(128, (w.rows(p) + 15) / 16 * 16, true, false);
+                if (piece > 0)
+                    ok = mbar_wait_bounded(&sm.o_empty, (piece - 1) & 1);
+                for (int j = w.lo; ok && j < w.hi; j++, g++) {
+                    const int st = g % STAGES;
+                    ok = mbar_wait_bounded(&sm.p_full, g & 1) &&
+                         mbar_wait_bounded(&sm.kv_full[st], (g / STAGES) & 1);
+                    if (!ok || aborted(&sm.abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint64_t vd = vd0 + (uint64_t)(st * CB * BLOCK16);
+#pragma unroll
+                    for (int d = 0; d < DB; d++)
+#pragma unroll
+                        for (int k = 0; k < KT / 16; k++)  // 16 keys: rows of 128 B of V, 32 B of a row of P
+                            tc::mma_ss(tmem + d * QR, vd + (uint64_t)(2 * d * BLOCK16 + k * 128),
+                                       pd + (uint64_t)(k * 2), idesc, j > w.lo || k > 0);
+                    tc::mma_commit(&sm.kv_empty[st]);
+                    tc::mma_commit(&sm.pv_done);
+                }
+            }
+            if (!ok)
+                set_abort(&sm.abort_flag, p.status);
+            if (g > 0) {
+                tc::mma_commit(&sm.drain[1]);
+                drain_wait(&sm.drain[1], 0, p.status);
+            }
+        }
+    } else if (warp >= 4) {
+        // -------------------------------------------------------------- softmax --
+        const int quarter = warp & 3, tid = threadIdx.x - 128;
+        const int ra = quarter * 16 + (lane >> 2);  // this thread's rows: ra and ra + 8
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const float sl2 = p.scale_log2;
+        bool ok = true;
+        int g = 0;
+        if (tid == 0)
+            p.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
+        while (ok && w.next(p)) {
+            const int rows = w.rows(p);
+            int lim[2];  // keys that the rows see
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int r = ra + 8 * h;
+                lim[h] = r < rows ? w.s.prior + (w.unit * QR + r) / p.H + 1 : 0;
+            }
+            float m_ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+            for (int j = w.lo; j < w.hi; j++, g++) {
+                const int j0 = j * KT, sb = g & 1;
+                ok = ok && warp_wait(&sm.s_full[sb], (g >> 1) & 1, &sm.abort_flag);
+                uint32_t s[32];
+                if (ok) {
+                    tc::fence_after_sync();
+                    tmem_ld_16x64(tmem + S_COL + sb * KT + lane_off, s);
+                    tc::tmem_wait_ld();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.s_empty[sb]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        s[i] = 0;
+                }
+                if (j0 + KT > min(lim[0], lim[1])) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const int key = j0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1);
+                        if (key >= lim[(i >> 1) & 1])
+                            s[i] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float alpha[2];
+                bool raise = false;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        mx = max3f(mx, __uint_as_float(s[4 * i + 2 * h]),
+                                   __uint_as_float(s[4 * i + 2 * h + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2;
+                    alpha[h] = 1.f;
+                    if (mx > m_ref[h] + 8.0f) {
+                        alpha[h] = m_ref[h] == -INFINITY ? 0.f : ex2_mufu(m_ref[h] - mx);
+                        raise = raise || m_ref[h] != -INFINITY;
+                        m_ref[h] = mx;
+                    }
+                    if ((lane & 3) == 0)
+                        sm.factor[g & 1][ra + 8 * h] = alpha[h];
+                }
+                // (a warp whose wait gave up still comes here, so that the others go on to see it)
+                const bool rescale = softmax_any(raise || !ok);
+                if (aborted(&sm.abort_flag))
+                    ok = false;
+                uint32_t pk[16];
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float neg_m = m_ref[h] == -INFINITY ? 0.f : -m_ref[h];
+                    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float2 x = __ffma2_rn(
+                            make_float2(__uint_as_float(s[4 * i + 2 * h]),
+                                        __uint_as_float(s[4 * i + 2 * h + 1])),
+                            make_float2(sl2, sl2), make_float2(neg_m, neg_m));
+                        const float2 e = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
+                        acc = __fadd2_rn(acc, e);
+                        pk[2 * i + h] = pack_bf16x2(e.x, e.y);
+                    }
+                    sum[h] = fmaf(sum[h], alpha[h], acc.x + acc.y);
+                }
+                // P and O^T are free once the last tile's product is done
+                if (ok && g > 0)
+                    ok = warp_wait(&sm.pv_done, (g - 1) & 1, &sm.abort_flag);
+                if (ok && rescale && j > w.lo) {
+                    tc::fence_after_sync();
+                    const float *f = sm.factor[g & 1];
+#pragma unroll 1
+                    for (int c = 0; c < DB * QR; c += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tmem + lane_off + c, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f[(c & (QR - 1)) + i]);
+                        tc::tmem_st32(tmem + lane_off + c, o);
+                    }
+                    tc::tmem_wait_st();
+                }
+                if (ok && j0 + KT > w.keys)
+                    ok = warp_wait(&sm.kv_full[g % STAGES], (g / STAGES) & 1, &sm.abort_flag);
+                if (ok) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const int r = ra + 8 * (i & 1);
+                        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(sm.p) + r * 128 +
+                                                      (((i >> 1) ^ (r & 7)) << 4) + (lane & 3) * 4) = pk[i];
+                    }
+                    if (j0 + KT > w.keys) {
+                        // Rows behind the last key hold whatever was there: zeros, so that no
+                        // weight of 0 meets a NaN.  (S of this tile has been read off.)
+                        const int from = w.keys - j0;
+                        uint4 *v = reinterpret_cast<uint4 *>(sm.kv[g % STAGES][0]);
+                        for (int i = tid; i < (KT - from) * 8 * (R / 64); i += 128) {
+                            const int cb = i / ((KT - from) * 8), k = i - cb * ((KT - from) * 8);
+                            v[cb * (BLOCK_BYTES / 16) + from * 8 + k] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.p_full);
+                }
+            }
+            // ------------------------------------------------------- a piece's rows --
+            ok = ok && warp_wait(&sm.pv_done, (g - 1) & 1, &sm.abort_flag);
+            const bool whole = w.lo == 0 && w.hi == w.tiles;
+            const int slot = 2 * blockIdx.x + (w.lo == 0 ? 1 : 0);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+                if ((lane & 3) == 0) {
+                    sm.inv[ra + 8 * h] = whole ? (sum[h] > 0.f ? 1.0f / sum[h] : 0.f) : 1.f;
+                    if (!whole && ok && ra + 8 * h < rows)
+                        reinterpret_cast<float2 *>(p.part_ml)[(size_t)slot * QR + ra + 8 * h] =
+                            make_float2(m_ref[h], sum[h]);
+                }
+            }
+            if (softmax_any(!ok)) {
+                ok = false;
+                break;
+            }
+            tc::fence_after_sync();
+            const long long row0 = w.row0(p);
+#pragma unroll 1
+            for (int c = 0; c < DB * QR; c += 32) {
+                const int r0 = c & (QR - 1), dim = (c / QR) * 128 + quarter * 32 + lane;
+                if (r0 >= rows)
+                    continue;
+                uint32_t o[32];
+                tc::tmem_ld32(tmem + lane_off + c, o);
+                tc::tmem_wait_ld();
+                if (whole) {
+                    bf16 *dst = p.out + (row0 + r0) * R + dim;
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        if (r0 + i < rows)
+                            dst[(size_t)i * R] = __float2bfloat16_rn(__uint_as_float(o[i]) * sm.inv[r0 + i]);
+                } else {
+                    float *dst = p.part_o + ((size_t)slot * QR + r0) * R + dim;
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        if (r0 + i < rows)
+                            dst[(size_t)i * R] = __uint_as_float(o[i]);
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.o_empty);
+            if (w.lo == 0 && !whole && tid == 0) {
+                // the unit ends (tiles - hi) behind the end of this run
+                const long long end = run_begin(p, sm.total, blockIdx.x + 1) + (w.tiles - w.hi);
+                p.cut[blockIdx.x] = make_int4((int)row0, rows, blockIdx.x, run_of(p, sm.total, end));
+            }
+        }
+        if (!ok && lane == 0)
+            set_abort(&sm.abort_flag, p.status);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// Joins the pieces of the unit that CTA blockIdx.x of the first pass began and others
+// finished: R / 4 threads a row, MERGE_ROWS rows a CTA.
+constexpr int MERGE_ROWS = 4;
+
+template <int R>
+__global__ void __launch_bounds__(R / 4 * MERGE_ROWS)
+    latent_merge_kernel(const __grid_constant__ LatentParams p)
+{
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int4 cut = p.cut[blockIdx.x];
+    const int r = blockIdx.y * MERGE_ROWS + threadIdx.x / (R / 4), x = threadIdx.x % (R / 4);
+    const int lane = threadIdx.x & 31;
+    if (cut.w < 0 || r >= cut.y)
+        return;
+    const int pieces = cut.w - cut.z + 1;
+    // piece i in slot 2 c + 1 for the first CTA, 2 c for those after it
+    auto slot = [&](int i) { return (size_t)(2 * (cut.z + i) + (i == 0 ? 1 : 0)) * QR + r; };
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml);
+    float M = -INFINITY;
+    for (int i = lane; i < pieces; i += 32)
+        M = fmaxf(M, ml[slot(i)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+        float weight = 0.f;
+        if (i0 + lane < pieces) {
+            const float2 v = ml[slot(i0 + lane)];
+            if (v.x != -INFINITY) {
+                weight = exp2f(v.x - M);
+                L = fmaf(v.y, weight, L);
+            }
+        }
+        const int n = min(32, pieces - i0);
+        for (int i = 0; i < n; i += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                if (i + k < n)
+                    v[k] = reinterpret_cast<const float4 *>(p.part_o + slot(i0 + i + k) * R)[x];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const float wk = __shfl_sync(0xffffffffu, weight, min(i + k, 31));
+                if (i + k < n) {
+                    acc.x = fmaf(v[k].x, wk, acc.x);
+                    acc.y = fmaf(v[k].y, wk, acc.y);
+                    acc.z = fmaf(v[k].z, wk, acc.z);
+                    acc.w = fmaf(v[k].w, wk, acc.w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    uint2 u;
+    u.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    u.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2 *>(p.out + ((size_t)cut.x + r) * R)[x] = u;
+}
+
+template <int R>
+cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
+{
+    CUtensorMap mq, mkv;
+    const cuuint64_t wide = R + p.rd;
+    const cuuint64_t q_dims[2] = {wide, (cuuint64_t)p.total_tokens * p.H};
+    const cuuint64_t kv_dims[2] = {wide, (cuuint64_t)pg.num_pages << pg.page_log};
+    const cuuint64_t strides[1] = {wide * 2};
+    const cuuint32_t q_box[2] = {64, QR}, kv_box[2] = {64, 1u << (pg.page_log < 6 ? pg.page_log : 6)};
+    if (!make_bf16_tile_map(&mq, p.q, 2, q_dims, strides, q_box) ||
+        !make_bf16_tile_map(&mkv, p.cache, 2, kv_dims, strides, kv_box))
+        return cudaErrorInvalidValue;
+    constexpr size_t smem = sizeof(LatentSmem<R>) + 1024;
+    // one CTA per SM, so that its tensor memory is its own
+    static_assert(smem > (116u << 10) && smem <= 232448, "shared memory of one CTA per SM");
+    static std::atomic<unsigned long long> configured{0};
+    cudaError_t e = once_per_device(configured, [] {
+        return cudaFuncSetAttribute(latent_attn_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)smem);
+    });
+    if (e != cudaSuccess)
+        return e;
+    e = launch_kernel(latent_attn_kernel<R>, dim3(p.grid), dim3(THREADS), smem, stream, p, pg, mq, mkv);
+    if (e != cudaSuccess || p.grid == 1)
+        return e;
+    const long long rows = (long long)p.max_new_len * p.H;
+    const int most = rows < QR ? (int)rows : QR;
+    return launch_kernel(latent_merge_kernel<R>, dim3(p.grid, (most + MERGE_ROWS - 1) / MERGE_ROWS),
+                         dim3(R / 4 * MERGE_ROWS), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_latent(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
+{
+    switch (p.R) {
+    case 512: return launch_latent_t<512>(p, pg, stream);
+    case 256: return launch_latent_t<256>(p, pg, stream);
+    default: return launch_latent_t<128>(p, pg, stream);
+    }
+}

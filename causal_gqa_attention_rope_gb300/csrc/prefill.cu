@@ -84,6 +84,7 @@
 
 #include "na_internal.cuh"
 #include "tc_primitives.cuh"
+#include "tile_waits.cuh"
 
 namespace {
 
@@ -153,47 +154,6 @@ constexpr size_t tc_smem_bytes()
     // at least ~116 KB so that a single CTA owns the SM (and its tensor memory)
     return (sizeof(TcSmem<D, SRC>) + 1024) > (116u << 10) ? sizeof(TcSmem<D, SRC>) + 1024
                                                           : (116u << 10);
-}
-
-__device__ __forceinline__ bool aborted(const int *flag) { return *(volatile const int *)flag != 0; }
-
-__device__ __forceinline__ void set_abort(int *flag, int32_t *status)
-{
-    *(volatile int *)flag = 1;
-    na_report(status, NA_ERR_DEVICE_TIMEOUT);
-}
-
-// A bounded wait whose outcome is only reported: the drains before exit (copies
-// in flight, MMAs before tensor memory is released), where there is nothing
-// left to skip.  A wait that gives up writes NA_ERR_DEVICE_TIMEOUT.
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, int32_t *status)
-{
-    if (!mbar_wait_bounded(bar, parity))
-        na_report(status, NA_ERR_DEVICE_TIMEOUT);
-}
-
-// A bounded wait whose result every lane of the warp shares: the softmax warps
-// follow it with warp-collective tensor-memory loads and stores, which no lane
-// may skip while others execute them.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const int *abort_flag)
-{
-    const bool done = mbar_wait_bounded(bar, parity) && !aborted(abort_flag);
-    return __all_sync(0xffffffffu, done);
-}
-
-__device__ __forceinline__ float max3f(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// 2^x on the MUFU unit (approximate, flushes subnormal results to zero).
-__device__ __forceinline__ float ex2_mufu(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // A raw E4M3 tile (BN rows of D bytes) into a 128-byte-swizzled f16 tile, by the

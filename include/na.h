@@ -427,8 +427,8 @@ int na_decode_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_
  * The page tables of a serving batch, its forks and evictions.  (Additions of
  * this library; the pages have no counterpart.)  One table serves every layer
  * of a model, so na_pages_fork is called once a step, and na_pages_copy and
- * na_pages_compact once per layer.  A cache of one row
- * a token and no values (latent rows) has one kv head and v NULL.
+ * na_pages_compact once per layer.  A latent cache (below) has one kv head of
+ * head_dim = kv_rank + rope_dim and v NULL.
  */
 
 /*
@@ -525,6 +525,125 @@ int na_pages_compact(int32_t num_kv_heads, int32_t head_dim, int32_t batch,
                      const int32_t *keep_lens, int32_t max_keep, const na_rope_params *rope,
                      int32_t rotary_start, int32_t rotary_dim, uint32_t flags, int32_t *status,
                      void *stream);
+
+/* -------------------------------------------------------- latent attention --
+ *
+ * Attention whose keys and values come from one latent vector a token.  (An
+ * addition of this library; the pages have no counterpart.)  A token's row is
+ * [c, r]: c its kv_rank latent numbers, r a rotated key part of rope_dim that all
+ * heads share.  With the maps U_h (nope_dim x kv_rank) and W_h (v_dim x kv_rank) of
+ * head h its key is [U_h c, r] and its value W_h c, so with a query [a, s]
+ *     score = scale * (a . U_h c + s . r) = scale * ([U_h^T a, s] . [c, r]),
+ *     out   = sum_j p_j W_h c_j           = W_h (sum_j p_j c_j).
+ * Absorbed form (na_attn_latent_paged): queries [U_h^T a, s] against the cached rows,
+ * the sum of the latents out; a row is read once for all heads, which suits single
+ * tokens and short chunks.  Expanded form (na_attn_latent_expanded): [U_h c, W_h c]
+ * made first, then attention of nope_dim + rope_dim and v_dim, with fewer products
+ * per query and key: for long chunks.  The maps themselves are matrix products of
+ * the caller's.
+ */
+#define NA_LATENT_NORM 1u         /* RMS norm of the latent part before it enters the cache */
+
+typedef struct na_latent_cfg {
+    int32_t num_heads; /* H, any number */
+    int32_t kv_rank;   /* R: 128, 256 or 512 */
+    int32_t rope_dim;  /* rd: 16, 32, 48 or 64 */
+    int32_t nope_dim;  /* 64 or 128: expanded keys; with rope_dim the default score scale */
+    int32_t v_dim;     /* 64 or 128: expanded values */
+    float sm_scale;    /* score scale; <= 0 selects 1 / sqrt(nope_dim + rope_dim) */
+    float rms_eps;     /* epsilon of the latent norm */
+    uint32_t flags;    /* NA_LATENT_NORM, NA_ROPE_INTERLEAVED */
+} na_latent_cfg;
+
+/* Caller-owned pages of latent rows; the rules of na_paged_kv_cache, one row for all heads. */
+typedef struct na_paged_latent_cache {
+    void *kv;                  /* bf16 [num_pages][page_size][kv_rank + rope_dim], 16-byte aligned */
+    const int32_t *page_table; /* int32 [batch][pages_per_seq] */
+    int32_t num_pages;         /* num_pages * page_size <= 2^31 - 1 */
+    int32_t page_size;         /* 16, 32, 64 or 128 */
+    int32_t batch;
+    int32_t pages_per_seq;
+} na_paged_latent_cache;
+
+/*
+ * New tokens' latent rows into their pages, and the queries' rotated parts.
+ *
+ * For new token t of sequence b at pos = cache_lens[b] + (t - cu_seqlens[b]):
+ *   row[:R]        = norm(kv[t][:R])  (unchanged without NA_LATENT_NORM)
+ *   row[R:]        = RoPE(kv[t][R:], pos)
+ *   q_out[t][h][:] = RoPE(q[t][h][:], pos)     rope_dim elements, every h
+ * Accuracy: as na_rope_append_kv (a normed value within one bf16 ulp, correctly
+ * rounded but for ~2^-21 next to a rounding border).
+ *
+ *   kv        bf16 [total_tokens] rows of R + rd elements, kv_stride elements apart.
+ *   q, q_out  bf16: rope_dim elements of token t and head h start q_stride * (t H + h)
+ *             elements after q (q_out_stride after q_out): the rotated part of wider
+ *             query rows.  q_out may be q, with the same stride; otherwise they may not
+ *             overlap.  Both NULL: no queries.
+ *   kv_norm_w bf16 [R], required with NA_LATENT_NORM, else ignored.
+ *   total_tokens  HOST upper bound of cu_seqlens[batch]; rows past it are left alone.
+ *   status    as na_rope_append_kv_paged (NA_ERR_CAPACITY, NA_ERR_PAGE; such a token's
+ *             row is skipped, with NA_ERR_CAPACITY its queries too).
+ * Errors: NA_ERR_INVALID_ARG for pointers that are null or not 16-byte aligned, strides
+ * that are no multiple of 8 elements or smaller than a row.
+ */
+int na_latent_append_paged(const na_latent_cfg *cfg, const na_rope_params *rope, int32_t batch,
+                           const int32_t *cu_seqlens, const int32_t *cache_lens,
+                           int32_t total_tokens, const void *kv, int64_t kv_stride, const void *q,
+                           int64_t q_stride, void *q_out, int64_t q_out_stride,
+                           const void *kv_norm_w, const na_paged_latent_cache *cache,
+                           int32_t *status, void *stream);
+
+/*
+ * Absorbed latent attention of new tokens, whose rows are in the pages already:
+ *   out[t][h] = sum_j softmax_j(scale * q_lat[t][h] . row_j) row_j[:R],  j <= pos of t.
+ * One token per sequence (a decode step) and chunks are the same call.
+ * Arithmetic: bf16 tensor cores with fp32 accumulation, the softmax in fp32, weights
+ * rounded to bf16 for the second product; with unit-scale inputs within 2e-2 (max-abs)
+ * and 5e-3 (relative L2) of the exact result.
+ *
+ *   q_lat      bf16 [total_tokens][H][R + rd];  out bf16 [total_tokens][H][R].
+ *   total_tokens, max_new_len, max_total_len  HOST upper bounds, as in
+ *              na_attn_prefill_chunk_paged; rows of out past cu_seqlens[batch] are left
+ *              as they were.
+ *   workspace  na_latent_paged_workspace_size() bytes.  Any contents will do.
+ *   status     as na_attn_prefill_chunk_paged; a sequence with a bad length is skipped.
+ */
+int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
+                         const int32_t *cache_lens, int32_t total_tokens, int32_t max_new_len,
+                         int32_t max_total_len, const void *q_lat,
+                         const na_paged_latent_cache *cache, void *out, void *workspace,
+                         size_t ws_bytes, int32_t *status, void *stream);
+
+/* Workspace bytes (HOST out-parameter) that na_attn_latent_paged needs for these bounds. */
+int na_latent_paged_workspace_size(const na_latent_cfg *cfg, int32_t batch, int32_t total_tokens,
+                                   int32_t max_new_len, int32_t max_total_len, size_t *bytes);
+
+/*
+ * Expanded latent attention, causal: with n new tokens and key_lens[b] keys sequence b's
+ * i-th token sees its first key_lens[b] - n + 1 + i keys (none: a row of zeros).
+ *   out[t][h] = sum_j softmax_j(scale * (q[t][h][:dn] . kv[j][h][:dn] + q[t][h][dn:] . k_pe[j]))
+ *               kv[j][h][dn:]
+ * over its keys, rows key_starts[b] .. key_starts[b] + key_lens[b] - 1 of kv and k_pe.
+ * Arithmetic and accuracy as na_attn_prefill_chunk.
+ *
+ *   key_starts, key_lens  int32 [batch].  Sequences may share keys.
+ *   max_new_len, max_key_len  HOST upper bounds.
+ *   q     bf16 [total_tokens][H][dn + rd].
+ *   kv    bf16 [total_keys][H][dn + dv]: keys and values as the expanding product writes them.
+ *   k_pe  bf16, rd elements a key, k_pe_stride elements apart (a multiple of 8): the rotated
+ *         part of latent rows.
+ *   out   bf16 [total_tokens][H][dv].
+ *   status  NA_ERR_INVALID_ARG for a new length above max_new_len or outside the call's
+ *           tokens, NA_ERR_CAPACITY for keys above max_key_len or outside the total_keys
+ *           rows; such a sequence is skipped.
+ * Keys and values of the sequences have to be finite; other rows of kv may hold any bits.
+ */
+int na_attn_latent_expanded(const na_latent_cfg *cfg, int32_t batch, const int32_t *cu_seqlens,
+                            const int32_t *key_starts, const int32_t *key_lens,
+                            int32_t total_tokens, int32_t total_keys, int32_t max_new_len,
+                            int32_t max_key_len, const void *q, const void *kv, const void *k_pe,
+                            int64_t k_pe_stride, void *out, int32_t *status, void *stream);
 
 /*
  * Self-test of the device-side failure detection (an addition of this
