@@ -416,6 +416,10 @@ def _calls():
         calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                      for f in (lib.na_rope_append_kv_paged, lib.na_attn_prefill_chunk_paged,
                                lib.na_attn_decode_paged)), AttnConfig, RopeConfig, PagedKVCache)
+        calls.bind_latent(*(ctypes.cast(f, ctypes.c_void_p).value
+                            for f in (lib.na_latent_append_paged, lib.na_attn_latent_paged,
+                                      lib.na_attn_latent_expanded, lib.na_pages_fork, lib.na_pages_copy,
+                                      lib.na_pages_compact)), LatentConfig, PagedLatentCache)
         _native = calls
     return _native
 
@@ -684,26 +688,29 @@ def na_pages_fork(parents, lens, table, ref, page_size: int, new_table, new_ref,
     """One step of a batch's page tables: sequence b continues parents[b] (< 0: starts empty) and
     gets room for grow[b] more tokens; the page copies that this needs are copy_src -> copy_dst
     (na_pages_copy)."""
-    lib = load_library()
-    _want(parents, "parents", "int32", (None,))
-    _want(table, "table", "int32", (None, None))
-    batch, (old, P) = int(parents.shape[0]), table.shape
-    _want(lens, "lens", "int32", (old,))
-    _want(ref, "ref", "int32", (None,))
-    _want(new_table, "new_table", "int32", (batch, P))
-    _want(new_ref, "new_ref", "int32", ref.shape)
-    for t, name in ((new_lens, "new_lens"), (copy_src, "copy_src"), (copy_dst, "copy_dst"),
-                    (grow, "grow")):
-        _want(t, name, "int32", (batch,))
-    _want(status, "status", "int32", (None,), 1)
-    args = [_ptr(t) for t in (parents, grow, lens, table)]
-    outs = [_ptr(t) for t in (new_table, new_ref, new_lens, copy_src, copy_dst, status)]
-    pref = _ptr(ref)
-    _on_current(parents, grow, lens, table, ref, new_table, new_ref, new_lens, copy_src, copy_dst,
-                status)
-    _check("na_pages_fork",
-           lib.na_pages_fork(batch, old, *args, P, int(page_size), pref, int(ref.shape[0]), *outs,
-                             _stream(stream)))
+    rc = (_native or _calls()).fork(parents, lens, table, ref, page_size, new_table, new_ref,
+                                    new_lens, copy_src, copy_dst, grow, status, stream)
+    if rc is None:
+        _want(parents, "parents", "int32", (None,))
+        _want(table, "table", "int32", (None, None))
+        batch, (old, P) = int(parents.shape[0]), table.shape
+        _want(lens, "lens", "int32", (old,))
+        _want(ref, "ref", "int32", (None,))
+        _want(new_table, "new_table", "int32", (batch, P))
+        _want(new_ref, "new_ref", "int32", ref.shape)
+        for t, name in ((new_lens, "new_lens"), (copy_src, "copy_src"), (copy_dst, "copy_dst"),
+                        (grow, "grow")):
+            _want(t, name, "int32", (batch,))
+        _want(status, "status", "int32", (None,), 1)
+        args = [_ptr(t) for t in (parents, grow, lens, table)]
+        outs = [_ptr(t) for t in (new_table, new_ref, new_lens, copy_src, copy_dst, status)]
+        pref = _ptr(ref)
+        _on_current(parents, grow, lens, table, ref, new_table, new_ref, new_lens, copy_src, copy_dst,
+                    status)
+        rc = load_library().na_pages_fork(
+            batch, old, *args, P, int(page_size), pref, int(ref.shape[0]), *outs, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_pages_fork", rc)
 
 
 def _pages(cache, name: str):
@@ -735,15 +742,18 @@ def _pages(cache, name: str):
 def na_pages_copy(cache, src, dst, status=None, stream=None):
     """Copy whole pages src[i] -> dst[i] of a PagedKVCache or PagedLatentCache (a negative entry:
     nothing)."""
-    lib = load_library()
-    c, heads, d = _pages(cache, "cache")
-    _want(src, "src", "int32", (None,))
-    _want(dst, "dst", "int32", src.shape)
-    _want(status, "status", "int32", (None,), 1)
-    ps, pd, st = _ptr(src), _ptr(dst), _ptr(status)
-    _on_current(src, dst, status)
-    _check("na_pages_copy", lib.na_pages_copy(heads, d, ctypes.byref(c), int(src.shape[0]), ps, pd,
-                                              st, _stream(stream)))
+    rc = (_native or _calls()).copy(cache, src, dst, status, stream)
+    if rc is None:
+        c, heads, d = _pages(cache, "cache")
+        _want(src, "src", "int32", (None,))
+        _want(dst, "dst", "int32", src.shape)
+        _want(status, "status", "int32", (None,), 1)
+        ps, pd, st = _ptr(src), _ptr(dst), _ptr(status)
+        _on_current(src, dst, status)
+        rc = load_library().na_pages_copy(
+            heads, d, ctypes.byref(c), int(src.shape[0]), ps, pd, st, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_pages_copy", rc)
 
 
 def na_pages_compact(cache, new_cache, keep_lens, max_keep: int, keep=None,
@@ -753,25 +763,29 @@ def na_pages_compact(cache, new_cache, keep_lens, max_keep: int, keep=None,
     """Move the rows at positions keep[b] of each sequence of `cache` (all in order with keep None)
     to the front of `new_cache`'s pages, keys turned to their new positions where rope is given
     (rotary_dim: by default from rotary_start to the row's end)."""
-    lib = load_library()
-    _want(keep_lens, "keep_lens", "int32", (None,))
-    batch, max_keep = int(keep_lens.shape[0]), int(max_keep)
-    a, heads, d = _pages(cache, "cache")
-    z, new_heads, new_d = _pages(new_cache, "new_cache")
-    if (heads, d) != (new_heads, new_d):
-        raise ValueError(f"new_cache: rows of {new_heads} x {new_d}, the cache's are {heads} x {d}")
-    if cache.page_table is None or new_cache.page_table is None:
-        raise ValueError("both caches need a page table")
-    _want(keep, "keep", "int32", (batch, max_keep))
-    _want(status, "status", "int32", (None,), 1)
-    pk, pl, st = _ptr(keep), _ptr(keep_lens), _ptr(status)
-    _on_current(keep, keep_lens, status)
-    r = None if rope is None else ctypes.byref(rope.c())
-    rd = d - rotary_start if rotary_dim is None else rotary_dim
-    _check("na_pages_compact",
-           lib.na_pages_compact(heads, d, batch, ctypes.byref(a), ctypes.byref(z), pk, pl, max_keep,
-                                r, int(rotary_start), 0 if r is None else int(rd),
-                                NA_ROPE_INTERLEAVED if interleaved else 0, st, _stream(stream)))
+    rc = (_native or _calls()).compact(cache, new_cache, keep_lens, max_keep, keep, rope,
+                                       rotary_start, rotary_dim, interleaved, status, stream)
+    if rc is None:
+        _want(keep_lens, "keep_lens", "int32", (None,))
+        batch, max_keep = int(keep_lens.shape[0]), int(max_keep)
+        a, heads, d = _pages(cache, "cache")
+        z, new_heads, new_d = _pages(new_cache, "new_cache")
+        if (heads, d) != (new_heads, new_d):
+            raise ValueError(f"new_cache: rows of {new_heads} x {new_d}, the cache's are {heads} x {d}")
+        if cache.page_table is None or new_cache.page_table is None:
+            raise ValueError("both caches need a page table")
+        _want(keep, "keep", "int32", (batch, max_keep))
+        _want(status, "status", "int32", (None,), 1)
+        pk, pl, st = _ptr(keep), _ptr(keep_lens), _ptr(status)
+        _on_current(keep, keep_lens, status)
+        r = None if rope is None else ctypes.byref(rope.c())
+        rd = d - rotary_start if rotary_dim is None else rotary_dim
+        rc = load_library().na_pages_compact(
+            heads, d, batch, ctypes.byref(a), ctypes.byref(z), pk, pl, max_keep, r,
+            int(rotary_start), 0 if r is None else int(rd),
+            NA_ROPE_INTERLEAVED if interleaved else 0, st, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_pages_compact", rc)
 
 
 def _latent_cache(cache: PagedLatentCache, cfg: LatentConfig, batch: int) -> na_paged_latent_cache:
@@ -810,29 +824,32 @@ def na_latent_append_paged(cfg: LatentConfig, rope: RopeConfig, cu_seqlens, cach
     """New tokens' latent rows kv [T, kv_rank + rope_dim] into their pages (normed, their rotated part
     turned), and q_out = RoPE(q), both [T, H, rope_dim] and views of wider rows where wanted (or
     None)."""
-    lib = load_library()
-    T = int(kv.shape[0]) if total_tokens is None else int(total_tokens)
-    batch = int(cu_seqlens.numel()) - 1
-    _want(cu_seqlens, "cu_seqlens", "int32", (None,))
-    _want(cache_lens, "cache_lens", "int32", (None,), batch)
-    _want(kv, "kv", "bfloat16", (None, None), T)
-    for t, name in ((q, "q"), (q_out, "q_out")):
-        _want(t, name, "bfloat16", (None, cfg.num_heads, cfg.rope_dim), T)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    _want(kv_norm_w, "kv_norm_w", "bfloat16", (cfg.kv_rank,))
-    _want(status, "status", "int32", (None,), 1)
-    kc = _latent_cache(cache, cfg, batch)
-    pkv, kv_stride = _rows(kv, "kv", cfg.kv_rank + cfg.rope_dim)
-    pq, q_stride = _rows(q, "q", cfg.rope_dim)
-    po, out_stride = _rows(q_out, "q_out", cfg.rope_dim)
-    c, r = cfg.c(), rope.c()
-    cu, lens, w, st = [_ptr(t) for t in (cu_seqlens, cache_lens, kv_norm_w, status)]
-    _on_current(cu_seqlens, cache_lens, kv, q, q_out, kv_norm_w, status, cache.kv, cache.page_table)
-    _check("na_latent_append_paged",
-           lib.na_latent_append_paged(ctypes.byref(c), ctypes.byref(r), batch, cu, lens, T, pkv,
-                                      kv_stride, pq, q_stride, po, out_stride, w, ctypes.byref(kc),
-                                      st, _stream(stream)))
+    rc = (_native or _calls()).latent_append(cfg, rope, cu_seqlens, cache_lens, kv, q, q_out,
+                                             cache, kv_norm_w, status, total_tokens, stream)
+    if rc is None:
+        T = int(kv.shape[0]) if total_tokens is None else int(total_tokens)
+        batch = int(cu_seqlens.numel()) - 1
+        _want(cu_seqlens, "cu_seqlens", "int32", (None,))
+        _want(cache_lens, "cache_lens", "int32", (None,), batch)
+        _want(kv, "kv", "bfloat16", (None, None), T)
+        for t, name in ((q, "q"), (q_out, "q_out")):
+            _want(t, name, "bfloat16", (None, cfg.num_heads, cfg.rope_dim), T)
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out go together")
+        _want(kv_norm_w, "kv_norm_w", "bfloat16", (cfg.kv_rank,))
+        _want(status, "status", "int32", (None,), 1)
+        kc = _latent_cache(cache, cfg, batch)
+        pkv, kv_stride = _rows(kv, "kv", cfg.kv_rank + cfg.rope_dim)
+        pq, q_stride = _rows(q, "q", cfg.rope_dim)
+        po, out_stride = _rows(q_out, "q_out", cfg.rope_dim)
+        c, r = cfg.c(), rope.c()
+        cu, lens, w, st = [_ptr(t) for t in (cu_seqlens, cache_lens, kv_norm_w, status)]
+        _on_current(cu_seqlens, cache_lens, kv, q, q_out, kv_norm_w, status, cache.kv, cache.page_table)
+        rc = load_library().na_latent_append_paged(
+            ctypes.byref(c), ctypes.byref(r), batch, cu, lens, T, pkv, kv_stride, pq, q_stride,
+            po, out_stride, w, ctypes.byref(kc), st, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_latent_append_paged", rc)
 
 
 def na_latent_paged_workspace_size(cfg: LatentConfig, batch: int, total_tokens: int, max_new_len: int,
@@ -851,23 +868,26 @@ def na_attn_latent_paged(cfg: LatentConfig, cu_seqlens, cache_lens, max_new_len:
                          status=None, total_tokens: Optional[int] = None, stream=None):
     """Absorbed latent attention of new tokens (single ones or chunks) against the pages: q_lat
     [T, H, kv_rank + rope_dim], out [T, H, kv_rank] (workspace: na_latent_paged_workspace_size)."""
-    lib = load_library()
-    T = int(q_lat.shape[0]) if total_tokens is None else int(total_tokens)
-    batch, H = int(cu_seqlens.numel()) - 1, cfg.num_heads
-    _want(cu_seqlens, "cu_seqlens", "int32", (None,))
-    _want(cache_lens, "cache_lens", "int32", (None,), batch)
-    _want(q_lat, "q_lat", "bfloat16", (None, H, cfg.kv_rank + cfg.rope_dim), T)
-    _want(out, "out", "bfloat16", (None, H, cfg.kv_rank), T)
-    _want(status, "status", "int32", (None,), 1)
-    kc = _latent_cache(cache, cfg, batch)
-    c = cfg.c()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    cu, lens, pq, po, ws, st = [_ptr(t) for t in (cu_seqlens, cache_lens, q_lat, out, workspace, status)]
-    _on_current(cu_seqlens, cache_lens, q_lat, out, workspace, status, cache.kv, cache.page_table)
-    _check("na_attn_latent_paged",
-           lib.na_attn_latent_paged(ctypes.byref(c), batch, cu, lens, T, int(max_new_len),
-                                    int(max_total_len), pq, ctypes.byref(kc), po, ws, ws_bytes, st,
-                                    _stream(stream)))
+    rc = (_native or _calls()).latent(cfg, cu_seqlens, cache_lens, max_new_len, max_total_len,
+                                      q_lat, cache, out, workspace, status, total_tokens, stream)
+    if rc is None:
+        T = int(q_lat.shape[0]) if total_tokens is None else int(total_tokens)
+        batch, H = int(cu_seqlens.numel()) - 1, cfg.num_heads
+        _want(cu_seqlens, "cu_seqlens", "int32", (None,))
+        _want(cache_lens, "cache_lens", "int32", (None,), batch)
+        _want(q_lat, "q_lat", "bfloat16", (None, H, cfg.kv_rank + cfg.rope_dim), T)
+        _want(out, "out", "bfloat16", (None, H, cfg.kv_rank), T)
+        _want(status, "status", "int32", (None,), 1)
+        kc = _latent_cache(cache, cfg, batch)
+        c = cfg.c()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        cu, lens, pq, po, ws, st = [_ptr(t) for t in (cu_seqlens, cache_lens, q_lat, out, workspace, status)]
+        _on_current(cu_seqlens, cache_lens, q_lat, out, workspace, status, cache.kv, cache.page_table)
+        rc = load_library().na_attn_latent_paged(
+            ctypes.byref(c), batch, cu, lens, T, int(max_new_len), int(max_total_len), pq,
+            ctypes.byref(kc), po, ws, ws_bytes, st, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_attn_latent_paged", rc)
 
 
 def na_attn_latent_expanded(cfg: LatentConfig, cu_seqlens, key_starts, key_lens, max_new_len: int,
@@ -876,26 +896,30 @@ def na_attn_latent_expanded(cfg: LatentConfig, cu_seqlens, key_starts, key_lens,
     """Expanded latent attention, causal: q [T, H, nope_dim + rope_dim] against kv [keys, H,
     nope_dim + v_dim] and the shared k_pe [keys, rope_dim] (a view of wider rows where wanted); out
     [T, H, v_dim].  Sequence b's keys are rows key_starts[b] .. + key_lens[b] - 1."""
-    lib = load_library()
-    T = int(q.shape[0]) if total_tokens is None else int(total_tokens)
-    batch, H = int(cu_seqlens.numel()) - 1, cfg.num_heads
-    _want(cu_seqlens, "cu_seqlens", "int32", (None,))
-    _want(key_starts, "key_starts", "int32", (None,), batch)
-    _want(key_lens, "key_lens", "int32", (None,), batch)
-    _want(q, "q", "bfloat16", (None, H, cfg.nope_dim + cfg.rope_dim), T)
-    _want(kv, "kv", "bfloat16", (None, H, cfg.nope_dim + cfg.v_dim))
-    _want(k_pe, "k_pe", "bfloat16", (None, None), int(kv.shape[0]))
-    _want(out, "out", "bfloat16", (None, H, cfg.v_dim), T)
-    _want(status, "status", "int32", (None,), 1)
-    pe, stride = _rows(k_pe, "k_pe", cfg.rope_dim)
-    c = cfg.c()
-    cu, starts, lens, pq, pkv, po, st = [
-        _ptr(t) for t in (cu_seqlens, key_starts, key_lens, q, kv, out, status)]
-    _on_current(cu_seqlens, key_starts, key_lens, q, kv, k_pe, out, status)
-    _check("na_attn_latent_expanded",
-           lib.na_attn_latent_expanded(ctypes.byref(c), batch, cu, starts, lens, T, int(kv.shape[0]),
-                                       int(max_new_len), int(max_key_len), pq, pkv, pe, stride, po, st,
-                                       _stream(stream)))
+    rc = (_native or _calls()).expanded(cfg, cu_seqlens, key_starts, key_lens, max_new_len,
+                                        max_key_len, q, kv, k_pe, out, status, total_tokens,
+                                        stream)
+    if rc is None:
+        T = int(q.shape[0]) if total_tokens is None else int(total_tokens)
+        batch, H = int(cu_seqlens.numel()) - 1, cfg.num_heads
+        _want(cu_seqlens, "cu_seqlens", "int32", (None,))
+        _want(key_starts, "key_starts", "int32", (None,), batch)
+        _want(key_lens, "key_lens", "int32", (None,), batch)
+        _want(q, "q", "bfloat16", (None, H, cfg.nope_dim + cfg.rope_dim), T)
+        _want(kv, "kv", "bfloat16", (None, H, cfg.nope_dim + cfg.v_dim))
+        _want(k_pe, "k_pe", "bfloat16", (None, None), int(kv.shape[0]))
+        _want(out, "out", "bfloat16", (None, H, cfg.v_dim), T)
+        _want(status, "status", "int32", (None,), 1)
+        pe, stride = _rows(k_pe, "k_pe", cfg.rope_dim)
+        c = cfg.c()
+        cu, starts, lens, pq, pkv, po, st = [
+            _ptr(t) for t in (cu_seqlens, key_starts, key_lens, q, kv, out, status)]
+        _on_current(cu_seqlens, key_starts, key_lens, q, kv, k_pe, out, status)
+        rc = load_library().na_attn_latent_expanded(
+            ctypes.byref(c), batch, cu, starts, lens, T, int(kv.shape[0]), int(max_new_len),
+            int(max_key_len), pq, pkv, pe, stride, po, st, _stream(stream))
+    if rc != NA_OK:
+        raise NAError("na_attn_latent_expanded", rc)
 
 
 def na_selftest_wait_timeout(status, stream=None):
