@@ -19,12 +19,13 @@ struct LatentParams {
     int H, R, rd, batch, capacity;
     float scale_log2;          // score scale * log2(e)
     int total_tokens, max_new_len, max_total_len;
+    int unit_rows;             // 32 or 64
     int grid;                  // CTAs, each taking an equal run of key tiles
     const int32_t *cu_seqlens, *cache_lens;
     const bf16 *q, *cache;
     bf16 *out;
-    float *part_o;             // [2 grid][64][R]: rows of a cut unit, CTA c's first piece at 2 c
-    float *part_ml;            // [2 grid][64][2]: (max, sum), log2 domain
+    float *part_o;             // [2 grid][unit_rows][R]: rows of a cut unit, CTA c's first piece at 2 c
+    float *part_ml;            // [2 grid][unit_rows][2]: (max, sum), log2 domain
     int4 *cut;                 // [grid]: of the unit that CTA c begins and others finish
     int32_t *status;
 };
@@ -41,7 +42,8 @@ struct ExpandedParams {
     int32_t *status;
 };
 
-constexpr int kLatentRows = 64;  // query rows (token, head) of a unit
+// Query rows (token, head) of a unit: 32 where no sequence of the call has more.
+inline int latent_unit_rows(long long most_rows) { return most_rows <= 32 ? 32 : 64; }
 constexpr int kLatentKeys = 64;  // keys of a tile
 constexpr int kExpandedRows = 128;  // query tokens of an expanded tile
 

@@ -47,7 +47,7 @@ int check_cache(const na_paged_latent_cache *c, int batch, PagedView *view)
 int done(cudaError_t e) { return e == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
 
 struct LatentPlan {
-    int grid;
+    int grid, unit_rows;
     size_t part_o, ws_bytes;
 };
 
@@ -56,11 +56,12 @@ LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int m
 {
     LatentPlan pl{};
     const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
-    const double tiles = (double)batch * ceil_div((long long)max_new_len * c->num_heads, kLatentRows) *
-                         ceil_div(max_total_len, kLatentKeys);
+    const long long rows = (long long)max_new_len * c->num_heads;
+    pl.unit_rows = latent_unit_rows(rows);
+    const double tiles = (double)batch * ceil_div(rows, pl.unit_rows) * ceil_div(max_total_len, kLatentKeys);
     pl.grid = (int)std::max(1.0, std::min((double)sm_count(), tiles));
-    pl.part_o = (size_t)2 * pl.grid * kLatentRows * c->kv_rank;
-    pl.ws_bytes = (pl.part_o + (size_t)2 * pl.grid * kLatentRows * 2) * sizeof(float) +
+    pl.part_o = (size_t)2 * pl.grid * pl.unit_rows * c->kv_rank;
+    pl.ws_bytes = (pl.part_o + (size_t)2 * pl.grid * pl.unit_rows * 2) * sizeof(float) +
                   pl.grid * sizeof(int4);
     return pl;
 }
@@ -160,7 +161,7 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     if (max_total_len > capacity)
         return NA_ERR_CAPACITY;
     // query rows are addressed by 32-bit tensor-map coordinates
-    if ((long long)total_tokens * cfg->num_heads > INT_MAX - kLatentRows)
+    if ((long long)total_tokens * cfg->num_heads > INT_MAX - 64)
         return NA_ERR_UNSUPPORTED;
     // (a sequence has no more new tokens than the call)
     max_new_len = std::min(max_new_len, total_tokens);
@@ -177,6 +178,7 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     p.total_tokens = total_tokens;
     p.max_new_len = max_new_len;
     p.max_total_len = max_total_len;
+    p.unit_rows = pl.unit_rows;
     p.grid = pl.grid;
     p.cu_seqlens = cu_seqlens;
     p.cache_lens = cache_lens;
@@ -185,7 +187,7 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     p.out = static_cast<bf16 *>(out);
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = p.part_o + pl.part_o;
-    p.cut = reinterpret_cast<int4 *>(p.part_ml + (size_t)2 * pl.grid * kLatentRows * 2);
+    p.cut = reinterpret_cast<int4 *>(p.part_ml + (size_t)2 * pl.grid * pl.unit_rows * 2);
     p.status = status;
     if ((rc = bind_context()) != NA_OK)
         return rc;

@@ -1,8 +1,9 @@
 // latent_attn.cu -- absorbed latent attention over pages (na_attn_latent_paged), on
 // the sm_100-family tensor cores (tcgen05 + TMEM + TMA).
 //
-// A unit is 64 query rows -- (token, head) pairs of one sequence, token-major -- and
-// the key tiles of 64 cached rows that they see.  For each tile
+// A unit is 64 query rows (32 where a sequence has no more) -- (token, head) pairs of one
+// sequence, token-major -- and the key tiles of 64 cached rows that they see.  For each
+// tile
 //     S   [64 rows x 64 keys]  = Q K^T      M = 64, K = R + 64 (rope part padded by TMA's
 //                                           zeros to a whole column block)
 //     O^T [R dims x 64 rows]  += V^T P^T    M = 128 per block of dims, K = 64 keys
@@ -10,6 +11,13 @@
 // as V^T.  With the rows along N the accumulators of R = 512 take 256 columns of
 // tensor memory, where rows along M would take all 512 and leave none to S, and M =
 // 128 runs at the full rate.  A row's bytes come from memory once for all heads.
+//
+// A tile lies in shared memory as its rope block and R / 128 pairs of column blocks, each
+// kind in a ring of its own.  S starts on a pair when it has landed and PV gives a
+// pair back when its 128 dims are done, so that loading runs on through both: with
+// whole tiles handed over, two of them deep, a tile took 3750 cycles of which its
+// load was 3000, and 64 sequences of 512 .. 8192 keys 76.6 us.  32 query rows leave
+// room for half a tile more.
 //
 // Warps: 0 producer (TMA: Q of a unit, then its tiles, a box per page and 64 columns),
 // 1 issues S into one of two buffers, 2 issues O^T, 4 .. 7 softmax, 16 rows each
@@ -31,21 +39,27 @@
 
 namespace {
 
-constexpr int QR = kLatentRows, KT = kLatentKeys;
+constexpr int KT = kLatentKeys;
+constexpr int MAX_ROWS = 64;               // M of S, whatever a unit's rows are
 constexpr int THREADS = 256;
-constexpr uint32_t BLOCK_BYTES = 64 * 128;  // 64 rows of 64 bf16: a column block of Q or of a tile
+constexpr uint32_t BLOCK_BYTES = KT * 128;  // 64 keys of 64 bf16: a column block of a tile
 
-template <int R>
+// QR: rows of a unit.  With 32 the products' rows 32 .. 63 are whatever lies behind a block of
+// Q, and nobody looks at them.
+template <int R, int QR>
 struct __align__(1024) LatentSmem {
-    static constexpr int CB = R / 64 + 1;                 // column blocks of a row
-    static constexpr int STAGES = R == 512 ? 2 : 4;
+    static constexpr int CB = R / 64 + 1;   // column blocks of a row
+    static constexpr int DB = R / 128;      // pairs of them in V: blocks of 128 dims
+    static constexpr int PAIRS = R == 512 ? (QR == 32 ? 10 : 8) : (R == 256 ? 8 : 6);
+    static constexpr int ROPES = R == 512 ? (QR == 32 ? 3 : 2) : (R == 256 ? 4 : 6);
     bf16 q[CB][QR * 64];
-    bf16 kv[STAGES][CB][KT * 64];
+    bf16 pair[PAIRS][2][KT * 64];
+    bf16 rope[ROPES][KT * 64];
     bf16 p[QR * 64];
-    float factor[2][QR];       // a tile's corrections by row, by tile parity
-    float inv[QR];             // at a piece's end: 1 / sum, or 1
-    uint64_t q_full, q_empty, kv_full[STAGES], kv_empty[STAGES], s_full[2], s_empty[2], p_full,
-        pv_done, o_empty, drain[2];
+    float factor[2][MAX_ROWS]; // a tile's corrections by row, by tile parity
+    float inv[MAX_ROWS];       // at a piece's end: 1 / sum, or 1
+    uint64_t q_full, q_empty, pair_full[PAIRS], pair_empty[PAIRS], rope_full[ROPES],
+        rope_empty[ROPES], s_full[2], s_empty[2], p_full, pv_done, o_empty, drain[2];
     long long warp_tiles[THREADS / 32];
     long long total, begin;
     int b0, t0, tile0;         // where the CTA's run begins
@@ -75,24 +89,28 @@ __device__ __forceinline__ Sequence sequence_of(const LatentParams &p, int b, in
     return s;
 }
 
+template <int QR>
 __device__ __forceinline__ int units_of(const LatentParams &p, const Sequence &s)
 {
     return (s.n * p.H + QR - 1) / QR;
 }
 
 // Keys that the rows of unit t see, and their tiles.
+template <int QR>
 __device__ __forceinline__ int keys_of(const LatentParams &p, const Sequence &s, int t)
 {
     return s.prior + (min(t * QR + QR, s.n * p.H) - 1) / p.H + 1;
 }
 
+template <int QR>
 __device__ __forceinline__ int tiles_of(const LatentParams &p, const Sequence &s, int t)
 {
-    return (keys_of(p, s, t) + KT - 1) / KT;
+    return (keys_of<QR>(p, s, t) + KT - 1) / KT;
 }
 
 // Tiles of the sequences 32 `chunk` + lane, a warp at a time: each lane its own, or, where
 // one of them has many units, all lanes together one sequence after the other.
+template <int QR>
 __device__ __forceinline__ long long chunk_tiles(const LatentParams &p, int chunk, int lane)
 {
     const int b = chunk * 32 + lane;
@@ -102,18 +120,18 @@ __device__ __forceinline__ long long chunk_tiles(const LatentParams &p, int chun
         s = sequence_of(p, b, code);
     if (code != NA_OK && blockIdx.x == 0)
         na_report(p.status, code);
-    const int units = units_of(p, s);
+    const int units = units_of<QR>(p, s);
     long long sum = 0;
     if (!__any_sync(0xffffffffu, units > 16)) {
         for (int t = 0; t < units; t++)
-            sum += tiles_of(p, s, t);
+            sum += tiles_of<QR>(p, s, t);
         return sum;
     }
     for (int i = 0; i < 32; i++) {
         const Sequence o{0, __shfl_sync(0xffffffffu, s.n, i), __shfl_sync(0xffffffffu, s.prior, i)};
         long long x = 0;
-        for (int t = lane; t < units_of(p, o); t += 32)
-            x += tiles_of(p, o, t);
+        for (int t = lane; t < units_of<QR>(p, o); t += 32)
+            x += tiles_of<QR>(p, o, t);
 #pragma unroll
         for (int k = 16; k; k >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, k);
@@ -155,15 +173,16 @@ __device__ __forceinline__ int run_of(const LatentParams &p, long long total, lo
 
 // The CTA's run: sm.total, sm.begin and the unit and tile that it begins with.  Each warp
 // sums a range of sequences; the one whose range holds the beginning looks it up.
-template <int R>
-__device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R> &sm, int warp, int lane)
+template <int R, int QR>
+__device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R, QR> &sm, int warp,
+                                         int lane)
 {
     constexpr int WARPS = THREADS / 32;
     const int chunks = (p.batch + 31) / 32, per = (chunks + WARPS - 1) / WARPS;
     const int c0 = min(warp * per, chunks), c1 = min(c0 + per, chunks);
     long long mine = 0, chunk_sum = 0;  // (a single chunk's sums are kept)
     for (int c = c0; c < c1; c++) {
-        chunk_sum = chunk_tiles(p, c, lane);
+        chunk_sum = chunk_tiles<QR>(p, c, lane);
         mine += chunk_sum;
     }
 #pragma unroll
@@ -186,7 +205,7 @@ __device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R> &s
     if (begin >= before && begin < before + mine) {
         for (int c = c0; c < c1; c++) {
             if (per > 1)
-                chunk_sum = chunk_tiles(p, c, lane);
+                chunk_sum = chunk_tiles<QR>(p, c, lane);
             const long long upto = inclusive_sum(chunk_sum, lane);
             const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
             if (past) {
@@ -195,7 +214,7 @@ __device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R> &s
                 int code;
                 const Sequence s = sequence_of(p, b, code);
                 for (int t = 0;; t += 32) {
-                    const long long x = t + lane < units_of(p, s) ? tiles_of(p, s, t + lane) : 0;
+                    const long long x = t + lane < units_of<QR>(p, s) ? tiles_of<QR>(p, s, t + lane) : 0;
                     const long long y = inclusive_sum(x, lane);
                     const unsigned m = __ballot_sync(0xffffffffu, before + y > begin);
                     if (m) {
@@ -218,6 +237,7 @@ __device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R> &s
 }
 
 // One after the other, the pieces of the CTA's run.  Every warp role walks them for itself.
+template <int QR>
 struct Walk {
     int b, t, tile;       // next: sequence, unit, tile of it
     long long left;       // tiles of the run from there
@@ -228,7 +248,7 @@ struct Walk {
     int unit, lo, hi, tiles, keys;
 
     template <int R>
-    __device__ __forceinline__ Walk(const LatentParams &p, const LatentSmem<R> &sm)
+    __device__ __forceinline__ Walk(const LatentParams &p, const LatentSmem<R, QR> &sm)
         : b(sm.b0), t(sm.t0), tile(sm.tile0),
           left(run_begin(p, sm.total, blockIdx.x + 1) - sm.begin), have(false)
     {
@@ -241,21 +261,21 @@ struct Walk {
         int code;
         while (!have) {
             s = sequence_of(p, b, code);
-            have = t < units_of(p, s);
+            have = t < units_of<QR>(p, s);
             if (!have) {
                 b++;
                 t = 0;
             }
         }
         unit = t;
-        keys = keys_of(p, s, t);
+        keys = keys_of<QR>(p, s, t);
         tiles = (keys + KT - 1) / KT;
         lo = tile;
         hi = (int)min((long long)tiles, lo + left);
         left -= hi - lo;
         tile = 0;
         t++;
-        have = t < units_of(p, s);
+        have = t < units_of<QR>(p, s);
         if (!have) {
             b++;
             t = 0;
@@ -305,17 +325,17 @@ __device__ __forceinline__ bool softmax_any(bool x)
     return any != 0;
 }
 
-template <int R>
+template <int R, int QR>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ PagedView pg,
                        const __grid_constant__ CUtensorMap map_q,
                        const __grid_constant__ CUtensorMap map_kv)
 {
-    typedef LatentSmem<R> Smem;
-    constexpr int CB = Smem::CB, STAGES = Smem::STAGES;
-    constexpr int DB = R / 128;                        // blocks of 128 dims: M of O^T
-    constexpr uint32_t S_COL = DB * QR;                // O^T block d at column 64 d, then S
+    typedef LatentSmem<R, QR> Smem;
+    constexpr int CB = Smem::CB, DB = Smem::DB, PAIRS = Smem::PAIRS, ROPES = Smem::ROPES;
+    constexpr uint32_t S_COL = DB * QR;                // O^T block d at column QR d, then S
     constexpr uint32_t TMEM_COLS = S_COL + 128 <= 256 ? 256 : 512;
+    constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~uintptr_t(1023));
@@ -325,9 +345,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::prefetch_tmap(&map_kv);
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
-        for (int i = 0; i < STAGES; i++) {
-            mbar_init(&sm.kv_full[i], 1);
-            mbar_init(&sm.kv_empty[i], 1);
+        for (int i = 0; i < PAIRS; i++) {
+            mbar_init(&sm.pair_full[i], 1);
+            mbar_init(&sm.pair_empty[i], 1);
+        }
+        for (int i = 0; i < ROPES; i++) {
+            mbar_init(&sm.rope_full[i], 1);
+            mbar_init(&sm.rope_empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sm.s_full[i], 1);
@@ -345,10 +369,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     grid_dependency_wait();
     grid_dependents_launch();
     tc::fence_before_sync();
-    find_run<R>(p, sm, warp, lane);
+    find_run<R, QR>(p, sm, warp, lane);
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
-    Walk w(p, sm);
+    Walk<QR> w(p, sm);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer --
@@ -356,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int in_page = (1 << pg.page_log) - 1;
         const uint64_t policy = l2_policy_evict_first();
         const bool read_once = p.max_new_len * p.H <= QR;  // one unit a sequence
-        int g = 0, pieces = 0;
+        int g = 0, pairs = 0, pieces = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) {
             if (!warp_wait(bar, parity, &sm.abort_flag)) {
@@ -384,30 +408,39 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (pieces > 0 && !wait_all(&sm.q_empty, (pieces - 1) & 1))
                 break;
             if (lane == 0)
-                mbar_arrive_expect_tx(&sm.q_full, CB * BLOCK_BYTES);
+                mbar_arrive_expect_tx(&sm.q_full, CB * QR * 128);
             __syncwarp();
             if (lane < CB)
                 tc::tma_load_2d(sm.q[lane], &map_q, lane * 64, (int)w.row0(p), &sm.q_full);
-            for (int j = w.lo; j < w.hi; j++, g++) {
-                const int st = g % STAGES;
+            for (int j = w.lo; ok && j < w.hi; j++) {
                 const int next = page_of(j + 1);
-                if (!wait_all(&sm.kv_empty[st], ((g / STAGES) & 1) ^ 1))
-                    break;
                 const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&sm.kv_full[st], n * CB * (128u << box_log));
-                __syncwarp();
                 const int first = (id << pg.page_log) + (pg.page_log > 6 ? (j * KT) & in_page : 0);
-                for (int i0 = 0; i0 < boxes * CB; i0 += 32) {
-                    const int i = i0 + lane, box = i & (boxes - 1), cb = i / boxes;
-                    const int from = __shfl_sync(0xffffffffu, first, box);
-                    if (box < n && cb < CB) {
-                        bf16 *dst = sm.kv[st][cb] + (box << box_log) * 64;
+                const int box = lane & (boxes - 1), block = lane / boxes;
+                const int from = __shfl_sync(0xffffffffu, first, box);
+                // `blocks` column blocks from column x on, a box of a page's rows per lane
+                auto load = [&](bf16 *dst, int x, int blocks, uint64_t *bar) {
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, n * blocks * (128u << box_log));
+                    __syncwarp();
+                    if (box < n && block < blocks) {
+                        bf16 *to = dst + block * (KT * 64) + (box << box_log) * 64;
                         if (read_once)
-                            tc::tma_load_2d_hint(dst, &map_kv, cb * 64, from, &sm.kv_full[st], policy);
+                            tc::tma_load_2d_hint(to, &map_kv, x + block * 64, from, bar, policy);
                         else
-                            tc::tma_load_2d(dst, &map_kv, cb * 64, from, &sm.kv_full[st]);
+                            tc::tma_load_2d(to, &map_kv, x + block * 64, from, bar);
                     }
+                };
+                const int rs = g % ROPES;
+                if (!wait_all(&sm.rope_empty[rs], ((g / ROPES) & 1) ^ 1))
+                    break;
+                load(sm.rope[rs], R, 1, &sm.rope_full[rs]);
+                g++;
+                for (int c = 0; c < DB; c++, pairs++) {
+                    const int ps = pairs % PAIRS;
+                    if (!wait_all(&sm.pair_empty[ps], ((pairs / PAIRS) & 1) ^ 1))
+                        break;
+                    load(sm.pair[ps][0], c * 128, 2, &sm.pair_full[ps]);
                 }
                 id = next;
             }
@@ -416,23 +449,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             if (pieces > 0)
                 drain_wait(&sm.q_full, (pieces - 1) & 1, p.status);
-            for (int i = g - 1; i >= 0 && i >= g - STAGES; i--)
-                drain_wait(&sm.kv_full[i % STAGES], (i / STAGES) & 1, p.status);
+            for (int i = g - 1; i >= 0 && i >= g - ROPES; i--)
+                drain_wait(&sm.rope_full[i % ROPES], (i / ROPES) & 1, p.status);
+            for (int i = pairs - 1; i >= 0 && i >= pairs - PAIRS; i--)
+                drain_wait(&sm.pair_full[i % PAIRS], (i / PAIRS) & 1, p.status);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------- S = Q K^T issue --
         if (elect_one()) {
-            constexpr uint32_t idesc = tc::idesc_bf16_f32(QR, KT, false, false);
-            constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
+            constexpr uint32_t idesc = tc::idesc_bf16_f32(MAX_ROWS, KT, false, false);
+            constexpr uint32_t Q16 = (QR * 128) >> 4;  // a column block of Q
             const uint64_t qd = tc::desc_kmajor_sw128(smem_addr(sm.q[0]));
-            const uint64_t kd0 = tc::desc_kmajor_sw128(smem_addr(sm.kv[0][0]));
+            const uint64_t rd0 = tc::desc_kmajor_sw128(smem_addr(sm.rope[0]));
+            const uint64_t kd0 = tc::desc_kmajor_sw128(smem_addr(sm.pair[0][0]));
             bool ok = true;
-            int g = 0;
+            bool issued = false;
+            int g = 0, pairs = 0;
             for (int piece = 0; ok && w.next(p); piece++) {
                 ok = mbar_wait_bounded(&sm.q_full, piece & 1);
                 for (int j = w.lo; ok && j < w.hi; j++, g++) {
-                    const int st = g % STAGES, sb = g & 1;
-                    ok = mbar_wait_bounded(&sm.kv_full[st], (g / STAGES) & 1);
+                    const int sb = g & 1, rs = g % ROPES;
+                    ok = mbar_wait_bounded(&sm.rope_full[rs], (g / ROPES) & 1);
                     if (ok && g >= 2)
                         ok = mbar_wait_bounded(&sm.s_empty[sb], ((g >> 1) - 1) & 1);
                     if (!ok || aborted(&sm.abort_flag)) {
@@ -440,13 +477,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint64_t kd = kd0 + (uint64_t)(st * CB * BLOCK16);
                     const uint32_t s_t = tmem + S_COL + sb * KT;
+                    // 16 columns, 32 bytes of a block's rows, per instruction
+                    const uint64_t rd = rd0 + (uint64_t)(rs * BLOCK16);
 #pragma unroll
-                    for (int k = 0; k < CB * 4; k++) {
-                        const uint32_t off = (k >> 2) * BLOCK16 + (k & 3) * 2;
-                        tc::mma_ss(s_t, qd + off, kd + off, idesc, k > 0);
+                    for (int k = 0; k < 4; k++)
+                        tc::mma_ss(s_t, qd + (CB - 1) * Q16 + k * 2, rd + k * 2, idesc, k > 0);
+                    issued = true;
+                    tc::mma_commit(&sm.rope_empty[rs]);
+#pragma unroll
+                    for (int c = 0; c < DB; c++, pairs++) {
+                        const int ps = pairs % PAIRS;
+                        ok = ok && mbar_wait_bounded(&sm.pair_full[ps], (pairs / PAIRS) & 1);
+                        if (!ok)
+                            continue;
+                        tc::fence_after_sync();
+                        const uint64_t kd = kd0 + (uint64_t)(ps * 2 * BLOCK16);
+#pragma unroll
+                        for (int k = 0; k < 8; k++)
+                            tc::mma_ss(s_t, qd + (2 * c + (k >> 2)) * Q16 + (k & 3) * 2,
+                                       kd + (k >> 2) * BLOCK16 + (k & 3) * 2, idesc, true);
                     }
+                    if (!ok)
+                        break;
                     tc::mma_commit(&sm.s_full[sb]);
                     if (j == w.hi - 1)
                         tc::mma_commit(&sm.q_empty);
@@ -454,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (!ok)
                 set_abort(&sm.abort_flag, p.status);
-            if (g > 0) {  // all issued MMAs complete before tensor memory is released
+            if (issued) {  // all issued MMAs complete before tensor memory is released
                 tc::mma_commit(&sm.drain[0]);
                 drain_wait(&sm.drain[0], 0, p.status);
             }
@@ -462,11 +515,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 2) {
         // ----------------------------------------------------- O^T += V^T P^T issue --
         if (elect_one()) {
-            constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
-            const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_addr(sm.kv[0][0]), BLOCK_BYTES);
+            const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_addr(sm.pair[0][0]), BLOCK_BYTES);
             const uint64_t pd = tc::desc_kmajor_sw128(smem_addr(sm.p));
             bool ok = true;
-            int g = 0;
+            int g = 0, pairs = 0;
             for (int piece = 0; ok && w.next(p); piece++) {
                 // the rows' columns in whole sixteens
                 const uint32_t idesc =
@@ -474,22 +526,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (piece > 0)
                     ok = mbar_wait_bounded(&sm.o_empty, (piece - 1) & 1);
                 for (int j = w.lo; ok && j < w.hi; j++, g++) {
-                    const int st = g % STAGES;
-                    ok = mbar_wait_bounded(&sm.p_full, g & 1) &&
-                         mbar_wait_bounded(&sm.kv_full[st], (g / STAGES) & 1);
+                    ok = mbar_wait_bounded(&sm.p_full, g & 1);
+#pragma unroll
+                    for (int d = 0; d < DB; d++)  // (long complete: S has read the tile)
+                        ok = ok && mbar_wait_bounded(&sm.pair_full[(pairs + d) % PAIRS],
+                                                     ((pairs + d) / PAIRS) & 1);
                     if (!ok || aborted(&sm.abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint64_t vd = vd0 + (uint64_t)(st * CB * BLOCK16);
 #pragma unroll
-                    for (int d = 0; d < DB; d++)
+                    for (int d = 0; d < DB; d++, pairs++) {
+                        const int ps = pairs % PAIRS;
+                        const uint64_t vd = vd0 + (uint64_t)(ps * 2 * BLOCK16);
 #pragma unroll
                         for (int k = 0; k < KT / 16; k++)  // 16 keys: rows of 128 B of V, 32 B of a row of P
-                            tc::mma_ss(tmem + d * QR, vd + (uint64_t)(2 * d * BLOCK16 + k * 128),
-                                       pd + (uint64_t)(k * 2), idesc, j > w.lo || k > 0);
-                    tc::mma_commit(&sm.kv_empty[st]);
+                            tc::mma_ss(tmem + d * QR, vd + (uint64_t)(k * 128), pd + (uint64_t)(k * 2), idesc,
+                                       j > w.lo || k > 0);
+                        tc::mma_commit(&sm.pair_empty[ps]);
+                    }
                     tc::mma_commit(&sm.pv_done);
                 }
             }
@@ -604,11 +660,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc::tmem_wait_st();
                 }
                 if (ok && j0 + KT > w.keys)
-                    ok = warp_wait(&sm.kv_full[g % STAGES], (g / STAGES) & 1, &sm.abort_flag);
+                    for (int c = 0; c < DB; c++)
+                        ok = ok && warp_wait(&sm.pair_full[(g * DB + c) % PAIRS],
+                                             ((g * DB + c) / PAIRS) & 1, &sm.abort_flag);
                 if (ok) {
 #pragma unroll
                     for (int i = 0; i < 16; i++) {
                         const int r = ra + 8 * (i & 1);
+                        if (QR < MAX_ROWS && r >= QR)
+                            continue;
                         *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(sm.p) + r * 128 +
                                                       (((i >> 1) ^ (r & 7)) << 4) + (lane & 3) * 4) = pk[i];
                     }
@@ -616,10 +676,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         // Rows behind the last key hold whatever was there: zeros, so that no
                         // weight of 0 meets a NaN.  (S of this tile has been read off.)
                         const int from = w.keys - j0;
-                        uint4 *v = reinterpret_cast<uint4 *>(sm.kv[g % STAGES][0]);
-                        for (int i = tid; i < (KT - from) * 8 * (R / 64); i += 128) {
-                            const int cb = i / ((KT - from) * 8), k = i - cb * ((KT - from) * 8);
-                            v[cb * (BLOCK_BYTES / 16) + from * 8 + k] = make_uint4(0, 0, 0, 0);
+                        const int per = (KT - from) * 8;
+                        for (int i = tid; i < per * 2 * DB; i += 128) {
+                            const int cb = i / per, k = i - cb * per;
+                            uint4 *v = reinterpret_cast<uint4 *>(
+                                sm.pair[(g * DB + (cb >> 1)) % PAIRS][cb & 1]);
+                            v[from * 8 + k] = make_uint4(0, 0, 0, 0);
                         }
                     }
                     tc::fence_proxy_async_smem();
@@ -697,7 +759,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // finished: R / 4 threads a row, MERGE_ROWS rows a CTA.
 constexpr int MERGE_ROWS = 4;
 
-template <int R>
+template <int R, int QR>
 __global__ void __launch_bounds__(R / 4 * MERGE_ROWS)
     latent_merge_kernel(const __grid_constant__ LatentParams p)
 {
@@ -758,7 +820,7 @@ __global__ void __launch_bounds__(R / 4 * MERGE_ROWS)
     reinterpret_cast<uint2 *>(p.out + ((size_t)cut.x + r) * R)[x] = u;
 }
 
-template <int R>
+template <int R, int QR>
 cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
     CUtensorMap mq, mkv;
@@ -770,22 +832,22 @@ cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStre
     if (!make_bf16_tile_map(&mq, p.q, 2, q_dims, strides, q_box) ||
         !make_bf16_tile_map(&mkv, p.cache, 2, kv_dims, strides, kv_box))
         return cudaErrorInvalidValue;
-    constexpr size_t smem = sizeof(LatentSmem<R>) + 1024;
+    constexpr size_t smem = sizeof(LatentSmem<R, QR>) + 1024;
     // one CTA per SM, so that its tensor memory is its own
     static_assert(smem > (116u << 10) && smem <= 232448, "shared memory of one CTA per SM");
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = once_per_device(configured, [] {
-        return cudaFuncSetAttribute(latent_attn_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(latent_attn_kernel<R, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)smem);
     });
     if (e != cudaSuccess)
         return e;
-    e = launch_kernel(latent_attn_kernel<R>, dim3(p.grid), dim3(THREADS), smem, stream, p, pg, mq, mkv);
+    e = launch_kernel(latent_attn_kernel<R, QR>, dim3(p.grid), dim3(THREADS), smem, stream, p, pg, mq, mkv);
     if (e != cudaSuccess || p.grid == 1)
         return e;
     const long long rows = (long long)p.max_new_len * p.H;
     const int most = rows < QR ? (int)rows : QR;
-    return launch_kernel(latent_merge_kernel<R>, dim3(p.grid, (most + MERGE_ROWS - 1) / MERGE_ROWS),
+    return launch_kernel(latent_merge_kernel<R, QR>, dim3(p.grid, (most + MERGE_ROWS - 1) / MERGE_ROWS),
                          dim3(R / 4 * MERGE_ROWS), 0, stream, p);
 }
 
@@ -793,9 +855,10 @@ cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStre
 
 cudaError_t launch_latent(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
+    const bool few = p.unit_rows == 32;
     switch (p.R) {
-    case 512: return launch_latent_t<512>(p, pg, stream);
-    case 256: return launch_latent_t<256>(p, pg, stream);
-    default: return launch_latent_t<128>(p, pg, stream);
+    case 512: return few ? launch_latent_t<512, 32>(p, pg, stream) : launch_latent_t<512, 64>(p, pg, stream);
+    case 256: return few ? launch_latent_t<256, 32>(p, pg, stream) : launch_latent_t<256, 64>(p, pg, stream);
+    default: return few ? launch_latent_t<128, 32>(p, pg, stream) : launch_latent_t<128, 64>(p, pg, stream);
     }
 }
