@@ -19,14 +19,15 @@ struct LatentParams {
     int H, R, rd, batch, capacity;
     float scale_log2;          // score scale * log2(e)
     int total_tokens, max_new_len, max_total_len;
-    int unit_rows;             // 32 or 64
-    int grid;                  // CTAs, each taking an equal run of key tiles
+    int unit_rows;             // 32, 64 or 128
+    int grid;                  // CTAs (pairs of them for 128 rows), each with an equal run of key tiles
+    int cut_by_sequence;       // one unit a sequence: cut[b], else by run
     const int32_t *cu_seqlens, *cache_lens;
     const bf16 *q, *cache;
     bf16 *out;
-    float *part_o;             // [2 grid][unit_rows][R]: rows of a cut unit, CTA c's first piece at 2 c
+    float *part_o;             // [2 grid][unit_rows][R]: rows of a cut unit, run c's first piece at 2 c
     float *part_ml;            // [2 grid][unit_rows][2]: (max, sum), log2 domain
-    int4 *cut;                 // [grid]: of the unit that CTA c begins and others finish
+    int4 *cut;                 // [grid]: first row, rows, first and last run of a unit (last -1: not cut)
     int32_t *status;
 };
 
@@ -42,8 +43,12 @@ struct ExpandedParams {
     int32_t *status;
 };
 
-// Query rows (token, head) of a unit: 32 where no sequence of the call has more.
-inline int latent_unit_rows(long long most_rows) { return most_rows <= 32 ? 32 : 64; }
+// Query rows (token, head) of a unit: enough for those of any sequence, 128 (64 in each of a
+// pair of CTAs) at most.
+inline int latent_unit_rows(long long most_rows)
+{
+    return most_rows <= 32 ? 32 : (most_rows <= 64 ? 64 : 128);
+}
 constexpr int kLatentKeys = 64;  // keys of a tile
 constexpr int kExpandedRows = 128;  // query tokens of an expanded tile
 

@@ -48,10 +48,11 @@ int done(cudaError_t e) { return e == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
 
 struct LatentPlan {
     int grid, unit_rows;
+    bool cut_by_sequence;
     size_t part_o, ws_bytes;
 };
 
-// One CTA per SM, fewer where the bounds allow no more tiles than that.
+// One CTA or pair of CTAs per SM or two, fewer where the bounds allow no more tiles than that.
 LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int max_total_len)
 {
     LatentPlan pl{};
@@ -59,7 +60,9 @@ LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int m
     const long long rows = (long long)max_new_len * c->num_heads;
     pl.unit_rows = latent_unit_rows(rows);
     const double tiles = (double)batch * ceil_div(rows, pl.unit_rows) * ceil_div(max_total_len, kLatentKeys);
-    pl.grid = (int)std::max(1.0, std::min((double)sm_count(), tiles));
+    const int most = pl.unit_rows > 64 ? std::max(sm_count() / 2, 1) : sm_count();
+    pl.grid = (int)std::max(1.0, std::min((double)most, tiles));
+    pl.cut_by_sequence = rows <= pl.unit_rows && batch <= pl.grid;
     pl.part_o = (size_t)2 * pl.grid * pl.unit_rows * c->kv_rank;
     pl.ws_bytes = (pl.part_o + (size_t)2 * pl.grid * pl.unit_rows * 2) * sizeof(float) +
                   pl.grid * sizeof(int4);
@@ -161,7 +164,7 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     if (max_total_len > capacity)
         return NA_ERR_CAPACITY;
     // query rows are addressed by 32-bit tensor-map coordinates
-    if ((long long)total_tokens * cfg->num_heads > INT_MAX - 64)
+    if ((long long)total_tokens * cfg->num_heads > INT_MAX - 256)
         return NA_ERR_UNSUPPORTED;
     // (a sequence has no more new tokens than the call)
     max_new_len = std::min(max_new_len, total_tokens);
@@ -180,6 +183,7 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     p.max_total_len = max_total_len;
     p.unit_rows = pl.unit_rows;
     p.grid = pl.grid;
+    p.cut_by_sequence = pl.cut_by_sequence;
     p.cu_seqlens = cu_seqlens;
     p.cache_lens = cache_lens;
     p.q = static_cast<const bf16 *>(q_lat);

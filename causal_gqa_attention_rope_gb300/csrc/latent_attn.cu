@@ -26,14 +26,22 @@
 // raised only when a score exceeds it by more than 2^8, and then all four warps
 // rescale the columns of O^T by the factors in shared memory.
 //
+// Sequences of more than 64 rows (chunks, drafted tokens, many heads) take units of 128 rows
+// in pairs of CTAs, 64 rows each: one reads the even column blocks of a tile, the other
+// the odd ones, both by TMA multicast into both, so that a tile comes from L2 once for
+// 128 rows.  A slot of a ring is free when the products of both CTAs are done with it.
+//
 // Work: the key tiles of all units, one after the other, are cut into one equal run
-// per CTA (one CTA per SM), whatever the lengths.  A unit that a cut goes through is
-// left in pieces (unnormalised rows with maximum and sum) which a second pass
-// joins.  CTA c has at most two: the end of a unit that an earlier CTA began (slot 2
-// c) and the beginning of one that others finish (slot 2 c + 1).
+// per CTA (or pair; one CTA per SM), whatever the lengths; a unit costs UNIT_STEPS more, about
+// what its Q and its results hold a CTA up.  A unit that a cut goes through is left in pieces
+// (unnormalised rows with maximum and sum) which a second pass joins.  Run c has at
+// most two: the end of a unit that an earlier one began (slot 2 c) and the beginning of
+// one that others finish (slot 2 c + 1).
+#include <algorithm>
 #include <climits>
 
 #include "latent.cuh"
+#include "na_host.cuh"
 #include "tc_primitives.cuh"
 #include "tile_waits.cuh"
 
@@ -42,6 +50,7 @@ namespace {
 constexpr int KT = kLatentKeys;
 constexpr int MAX_ROWS = 64;               // M of S, whatever a unit's rows are
 constexpr int THREADS = 256;
+constexpr int UNIT_STEPS = 1;
 constexpr uint32_t BLOCK_BYTES = KT * 128;  // 64 keys of 64 bf16: a column block of a tile
 
 // QR: rows of a unit.  With 32 the products' rows 32 .. 63 are whatever lies behind a block of
@@ -60,9 +69,9 @@ struct __align__(1024) LatentSmem {
     float inv[MAX_ROWS];       // at a piece's end: 1 / sum, or 1
     uint64_t q_full, q_empty, pair_full[PAIRS], pair_empty[PAIRS], rope_full[ROPES],
         rope_empty[ROPES], s_full[2], s_empty[2], p_full, pv_done, o_empty, drain[2];
-    long long warp_tiles[THREADS / 32];
+    long long warp_steps[THREADS / 32];
     long long total, begin;
-    int b0, t0, tile0;         // where the CTA's run begins
+    int b0, t0, step0;         // where the CTA's run begins
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -89,29 +98,30 @@ __device__ __forceinline__ Sequence sequence_of(const LatentParams &p, int b, in
     return s;
 }
 
-template <int QR>
+template <int UR>
 __device__ __forceinline__ int units_of(const LatentParams &p, const Sequence &s)
 {
-    return (s.n * p.H + QR - 1) / QR;
+    return (s.n * p.H + UR - 1) / UR;
 }
 
-// Keys that the rows of unit t see, and their tiles.
-template <int QR>
+// Keys that the rows of unit t see.
+template <int UR>
 __device__ __forceinline__ int keys_of(const LatentParams &p, const Sequence &s, int t)
 {
-    return s.prior + (min(t * QR + QR, s.n * p.H) - 1) / p.H + 1;
+    return s.prior + (min(t * UR + UR, s.n * p.H) - 1) / p.H + 1;
 }
 
-template <int QR>
-__device__ __forceinline__ int tiles_of(const LatentParams &p, const Sequence &s, int t)
+// What the unit counts for in a run: steps.
+template <int UR>
+__device__ __forceinline__ int steps_of(const LatentParams &p, const Sequence &s, int t)
 {
-    return (keys_of<QR>(p, s, t) + KT - 1) / KT;
+    return (keys_of<UR>(p, s, t) + KT - 1) / KT + UNIT_STEPS;
 }
 
-// Tiles of the sequences 32 `chunk` + lane, a warp at a time: each lane its own, or, where
+// Steps of the sequences 32 `chunk` + lane, a warp at a time: each lane its own, or, where
 // one of them has many units, all lanes together one sequence after the other.
-template <int QR>
-__device__ __forceinline__ long long chunk_tiles(const LatentParams &p, int chunk, int lane)
+template <int UR>
+__device__ __forceinline__ long long chunk_steps(const LatentParams &p, int chunk, int lane)
 {
     const int b = chunk * 32 + lane;
     Sequence s{0, 0, 0};
@@ -120,18 +130,18 @@ __device__ __forceinline__ long long chunk_tiles(const LatentParams &p, int chun
         s = sequence_of(p, b, code);
     if (code != NA_OK && blockIdx.x == 0)
         na_report(p.status, code);
-    const int units = units_of<QR>(p, s);
+    const int units = units_of<UR>(p, s);
     long long sum = 0;
     if (!__any_sync(0xffffffffu, units > 16)) {
         for (int t = 0; t < units; t++)
-            sum += tiles_of<QR>(p, s, t);
+            sum += steps_of<UR>(p, s, t);
         return sum;
     }
     for (int i = 0; i < 32; i++) {
         const Sequence o{0, __shfl_sync(0xffffffffu, s.n, i), __shfl_sync(0xffffffffu, s.prior, i)};
         long long x = 0;
-        for (int t = lane; t < units_of<QR>(p, o); t += 32)
-            x += tiles_of<QR>(p, o, t);
+        for (int t = lane; t < units_of<UR>(p, o); t += 32)
+            x += steps_of<UR>(p, o, t);
 #pragma unroll
         for (int k = 16; k; k >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, k);
@@ -152,52 +162,51 @@ __device__ __forceinline__ long long inclusive_sum(long long x, int lane)
     return x;
 }
 
-// CTAs that have work (all others have empty runs), and the first tile of CTA c's run; the
-// runs of `total` tiles are as equal as can be, none of them empty.
-__device__ __forceinline__ long long busy_ctas(const LatentParams &p, long long total)
+// Runs that have work (all others are empty), and the first step of run c; the runs of
+// `total` steps are as equal as can be, none of them empty.
+__device__ __forceinline__ long long busy_runs(const LatentParams &p, long long total)
 {
     return min((long long)p.grid, total);
 }
 
 __device__ __forceinline__ long long run_begin(const LatentParams &p, long long total, int c)
 {
-    const long long busy = busy_ctas(p, total);
+    const long long busy = busy_runs(p, total);
     return c >= busy ? total : total * c / busy;
 }
 
-// The CTA whose run holds the tile before `end`: the last c with total c / busy < end.
+// The run that holds the step before `end`: the last c with total c / busy < end.
 __device__ __forceinline__ int run_of(const LatentParams &p, long long total, long long end)
 {
-    return (int)((end * busy_ctas(p, total) + total - 1) / total) - 1;
+    return (int)((end * busy_runs(p, total) + total - 1) / total) - 1;
 }
 
-// The CTA's run: sm.total, sm.begin and the unit and tile that it begins with.  Each warp
+// Run `run`: sm.total, sm.begin and the unit and step of it that it begins with.  Each warp
 // sums a range of sequences; the one whose range holds the beginning looks it up.
-template <int R, int QR>
-__device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R, QR> &sm, int warp,
-                                         int lane)
+template <int UR, class Smem>
+__device__ __forceinline__ void find_run(const LatentParams &p, Smem &sm, int run, int warp, int lane)
 {
     constexpr int WARPS = THREADS / 32;
     const int chunks = (p.batch + 31) / 32, per = (chunks + WARPS - 1) / WARPS;
     const int c0 = min(warp * per, chunks), c1 = min(c0 + per, chunks);
     long long mine = 0, chunk_sum = 0;  // (a single chunk's sums are kept)
     for (int c = c0; c < c1; c++) {
-        chunk_sum = chunk_tiles<QR>(p, c, lane);
+        chunk_sum = chunk_steps<UR>(p, c, lane);
         mine += chunk_sum;
     }
 #pragma unroll
     for (int k = 16; k; k >>= 1)
         mine += __shfl_xor_sync(0xffffffffu, mine, k);
     if (lane == 0)
-        sm.warp_tiles[warp] = mine;
+        sm.warp_steps[warp] = mine;
     __syncthreads();
     long long total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; w++) {
-        before += w < warp ? sm.warp_tiles[w] : 0;
-        total += sm.warp_tiles[w];
+        before += w < warp ? sm.warp_steps[w] : 0;
+        total += sm.warp_steps[w];
     }
-    const long long begin = run_begin(p, total, blockIdx.x);
+    const long long begin = run_begin(p, total, run);
     if (threadIdx.x == 0) {
         sm.total = total;
         sm.begin = begin;
@@ -205,7 +214,7 @@ __device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R, QR
     if (begin >= before && begin < before + mine) {
         for (int c = c0; c < c1; c++) {
             if (per > 1)
-                chunk_sum = chunk_tiles<QR>(p, c, lane);
+                chunk_sum = chunk_steps<UR>(p, c, lane);
             const long long upto = inclusive_sum(chunk_sum, lane);
             const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
             if (past) {
@@ -214,7 +223,7 @@ __device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R, QR
                 int code;
                 const Sequence s = sequence_of(p, b, code);
                 for (int t = 0;; t += 32) {
-                    const long long x = t + lane < units_of<QR>(p, s) ? tiles_of<QR>(p, s, t + lane) : 0;
+                    const long long x = t + lane < units_of<UR>(p, s) ? steps_of<UR>(p, s, t + lane) : 0;
                     const long long y = inclusive_sum(x, lane);
                     const unsigned m = __ballot_sync(0xffffffffu, before + y > begin);
                     if (m) {
@@ -222,7 +231,7 @@ __device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R, QR
                         if (lane == k) {
                             sm.b0 = b;
                             sm.t0 = t + k;
-                            sm.tile0 = (int)(begin - (before + y - x));
+                            sm.step0 = (int)(begin - (before + y - x));
                         }
                         break;
                     }
@@ -236,21 +245,21 @@ __device__ __forceinline__ void find_run(const LatentParams &p, LatentSmem<R, QR
     __syncthreads();
 }
 
-// One after the other, the pieces of the CTA's run.  Every warp role walks them for itself.
-template <int QR>
+// One after the other, the pieces of a run.  Every warp role walks them for itself.
+template <int UR>
 struct Walk {
-    int b, t, tile;       // next: sequence, unit, tile of it
-    long long left;       // tiles of the run from there
+    int b, t, step;       // next: sequence, unit, step of it
+    long long left;       // steps of the run from there
     Sequence s;
     bool have;
 
-    // the piece: tiles [lo, hi) of unit `unit` of sequence s
-    int unit, lo, hi, tiles, keys;
+    // the piece: tiles [lo, hi) of `tiles` of unit `unit` of sequence `seq`, which has `keys`
+    int seq, unit, lo, hi, tiles, keys;
 
-    template <int R>
-    __device__ __forceinline__ Walk(const LatentParams &p, const LatentSmem<R, QR> &sm)
-        : b(sm.b0), t(sm.t0), tile(sm.tile0),
-          left(run_begin(p, sm.total, blockIdx.x + 1) - sm.begin), have(false)
+    template <class Smem>
+    __device__ __forceinline__ Walk(const LatentParams &p, const Smem &sm, int run)
+        : b(sm.b0), t(sm.t0), step(sm.step0), left(run_begin(p, sm.total, run + 1) - sm.begin),
+          have(false)
     {
     }
 
@@ -261,35 +270,38 @@ struct Walk {
         int code;
         while (!have) {
             s = sequence_of(p, b, code);
-            have = t < units_of<QR>(p, s);
+            have = t < units_of<UR>(p, s);
             if (!have) {
                 b++;
                 t = 0;
             }
         }
+        seq = b;
         unit = t;
-        keys = keys_of<QR>(p, s, t);
+        keys = keys_of<UR>(p, s, t);
         tiles = (keys + KT - 1) / KT;
-        lo = tile;
-        hi = (int)min((long long)tiles, lo + left);
-        left -= hi - lo;
-        tile = 0;
+        const int end = (int)min((long long)tiles + UNIT_STEPS, step + left);
+        lo = max(step - UNIT_STEPS, 0);
+        hi = max(end - UNIT_STEPS, 0);
+        left -= end - step;
+        step = 0;
         t++;
-        have = t < units_of<QR>(p, s);
+        have = t < units_of<UR>(p, s);
         if (!have) {
             b++;
             t = 0;
         }
-        return true;
+        return hi > lo;  // (none: the run ends within the unit's first steps)
     }
 
-    __device__ __forceinline__ int rows(const LatentParams &p) const
+    // rows of the unit from `at` on, `most` at most, and the first one among the call's
+    __device__ __forceinline__ int rows(const LatentParams &p, int at, int most) const
     {
-        return min(QR, s.n * p.H - unit * QR);
+        return max(min(most, s.n * p.H - unit * UR - at), 0);
     }
     __device__ __forceinline__ long long row0(const LatentParams &p) const
     {
-        return (long long)s.tok0 * p.H + unit * QR;
+        return (long long)s.tok0 * p.H + unit * UR;
     }
 };
 
@@ -325,7 +337,13 @@ __device__ __forceinline__ bool softmax_any(bool x)
     return any != 0;
 }
 
-template <int R, int QR>
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// CL: CTAs of a unit, QR rows each.
+template <int R, int QR, int CL>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ PagedView pg,
                        const __grid_constant__ CUtensorMap map_q,
@@ -336,6 +354,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t S_COL = DB * QR;                // O^T block d at column QR d, then S
     constexpr uint32_t TMEM_COLS = S_COL + 128 <= 256 ? 256 : 512;
     constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
+    constexpr int UR = QR * CL;
+    constexpr uint16_t EVERY = (1 << CL) - 1;
+    const int run = blockIdx.x / CL, rank = CL > 1 ? blockIdx.x % CL : 0;
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~uintptr_t(1023));
@@ -347,11 +368,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&sm.q_empty, 1);
         for (int i = 0; i < PAIRS; i++) {
             mbar_init(&sm.pair_full[i], 1);
-            mbar_init(&sm.pair_empty[i], 1);
+            mbar_init(&sm.pair_empty[i], CL);
         }
         for (int i = 0; i < ROPES; i++) {
             mbar_init(&sm.rope_full[i], 1);
-            mbar_init(&sm.rope_empty[i], 1);
+            mbar_init(&sm.rope_empty[i], CL);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sm.s_full[i], 1);
@@ -369,17 +390,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     grid_dependency_wait();
     grid_dependents_launch();
     tc::fence_before_sync();
-    find_run<R, QR>(p, sm, warp, lane);
+    find_run<UR>(p, sm, run, warp, lane);
+    if constexpr (CL > 1)
+        cluster_sync();  // the other CTA's barriers are there
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
-    Walk<QR> w(p, sm);
+    Walk<UR> w(p, sm, run);
+    auto commit_all = [](uint64_t *bar) {  // in both CTAs of a pair
+        if constexpr (CL > 1)
+            tc::mma_commit_multicast(bar, EVERY);
+        else
+            tc::mma_commit(bar);
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer --
         const int box_log = min(pg.page_log, 6), boxes = KT >> box_log;
         const int in_page = (1 << pg.page_log) - 1;
         const uint64_t policy = l2_policy_evict_first();
-        const bool read_once = p.max_new_len * p.H <= QR;  // one unit a sequence
+        const bool read_once = (long long)p.max_new_len * p.H <= QR;  // one unit a sequence
         int g = 0, pairs = 0, pieces = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) {
@@ -391,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             return ok;
         };
         for (; ok && w.next(p); pieces++) {
-            const int32_t *row = pg.table + (size_t)(w.t ? w.b : w.b - 1) * pg.pages_per_seq;
+            const int32_t *row = pg.table + (size_t)w.seq * pg.pages_per_seq;
             // this lane's page of a tile (boxes of them), or -1
             auto page_of = [&](int j) {
                 const int at = j * KT + (lane << box_log);
@@ -411,21 +440,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_arrive_expect_tx(&sm.q_full, CB * QR * 128);
             __syncwarp();
             if (lane < CB)
-                tc::tma_load_2d(sm.q[lane], &map_q, lane * 64, (int)w.row0(p), &sm.q_full);
+                tc::tma_load_2d(sm.q[lane], &map_q, lane * 64, (int)w.row0(p) + rank * QR, &sm.q_full);
             for (int j = w.lo; ok && j < w.hi; j++) {
                 const int next = page_of(j + 1);
                 const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
                 const int first = (id << pg.page_log) + (pg.page_log > 6 ? (j * KT) & in_page : 0);
                 const int box = lane & (boxes - 1), block = lane / boxes;
                 const int from = __shfl_sync(0xffffffffu, first, box);
-                // `blocks` column blocks from column x on, a box of a page's rows per lane
-                auto load = [&](bf16 *dst, int x, int blocks, uint64_t *bar) {
+                // `blocks` column blocks from column x on, a box of a page's rows per lane; of a pair of
+                // CTAs each copies those of its parity (from `parity` on) to both
+                auto load = [&](bf16 *dst, int x, int blocks, int parity, uint64_t *bar) {
                     if (lane == 0)
                         mbar_arrive_expect_tx(bar, n * blocks * (128u << box_log));
                     __syncwarp();
-                    if (box < n && block < blocks) {
+                    if (box < n && block < blocks && (CL == 1 || (block + parity) % CL == rank)) {
                         bf16 *to = dst + block * (KT * 64) + (box << box_log) * 64;
-                        if (read_once)
+                        if constexpr (CL > 1)
+                            tc::tma_load_2d_multicast(to, &map_kv, x + block * 64, from, bar, EVERY);
+                        else if (read_once)
                             tc::tma_load_2d_hint(to, &map_kv, x + block * 64, from, bar, policy);
                         else
                             tc::tma_load_2d(to, &map_kv, x + block * 64, from, bar);
@@ -434,13 +466,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int rs = g % ROPES;
                 if (!wait_all(&sm.rope_empty[rs], ((g / ROPES) & 1) ^ 1))
                     break;
-                load(sm.rope[rs], R, 1, &sm.rope_full[rs]);
+                load(sm.rope[rs], R, 1, g, &sm.rope_full[rs]);
                 g++;
                 for (int c = 0; c < DB; c++, pairs++) {
                     const int ps = pairs % PAIRS;
                     if (!wait_all(&sm.pair_empty[ps], ((pairs / PAIRS) & 1) ^ 1))
                         break;
-                    load(sm.pair[ps][0], c * 128, 2, &sm.pair_full[ps]);
+                    load(sm.pair[ps][0], c * 128, 2, 0, &sm.pair_full[ps]);
                 }
                 id = next;
             }
@@ -484,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int k = 0; k < 4; k++)
                         tc::mma_ss(s_t, qd + (CB - 1) * Q16 + k * 2, rd + k * 2, idesc, k > 0);
                     issued = true;
-                    tc::mma_commit(&sm.rope_empty[rs]);
+                    commit_all(&sm.rope_empty[rs]);
 #pragma unroll
                     for (int c = 0; c < DB; c++, pairs++) {
                         const int ps = pairs % PAIRS;
@@ -520,9 +552,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             int g = 0, pairs = 0;
             for (int piece = 0; ok && w.next(p); piece++) {
-                // the rows' columns in whole sixteens
-                const uint32_t idesc =
-                    tc::idesc_bf16_f32(128, (w.rows(p) + 15) / 16 * 16, true, false);
+                // the rows' columns in whole sixteens (a CTA without rows works on for its pair)
+                const uint32_t idesc = tc::idesc_bf16_f32(
+                    128, max((w.rows(p, rank * QR, QR) + 15) / 16 * 16, 16), true, false);
                 if (piece > 0)
                     ok = mbar_wait_bounded(&sm.o_empty, (piece - 1) & 1);
                 for (int j = w.lo; ok && j < w.hi; j++, g++) {
@@ -544,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int k = 0; k < KT / 16; k++)  // 16 keys: rows of 128 B of V, 32 B of a row of P
                             tc::mma_ss(tmem + d * QR, vd + (uint64_t)(k * 128), pd + (uint64_t)(k * 2), idesc,
                                        j > w.lo || k > 0);
-                        tc::mma_commit(&sm.pair_empty[ps]);
+                        commit_all(&sm.pair_empty[ps]);
                     }
                     tc::mma_commit(&sm.pv_done);
                 }
@@ -564,15 +596,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float sl2 = p.scale_log2;
         bool ok = true;
         int g = 0;
-        if (tid == 0)
-            p.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
+        // Where a unit that begins here is told to the second pass: by sequence where each has one
+        // unit, else by run.
+        const bool leader = tid == 0 && rank == 0;
+        if (leader && !p.cut_by_sequence)
+            p.cut[run] = make_int4(0, 0, 0, -1);
         while (ok && w.next(p)) {
-            const int rows = w.rows(p);
+            const int rows = w.rows(p, rank * QR, QR);
             int lim[2];  // keys that the rows see
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const int r = ra + 8 * h;
-                lim[h] = r < rows ? w.s.prior + (w.unit * QR + r) / p.H + 1 : 0;
+                lim[h] = r < rows ? w.s.prior + (w.unit * UR + rank * QR + r) / p.H + 1 : 0;
             }
             float m_ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
             for (int j = w.lo; j < w.hi; j++, g++) {
@@ -694,7 +729,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // ------------------------------------------------------- a piece's rows --
             ok = ok && warp_wait(&sm.pv_done, (g - 1) & 1, &sm.abort_flag);
             const bool whole = w.lo == 0 && w.hi == w.tiles;
-            const int slot = 2 * blockIdx.x + (w.lo == 0 ? 1 : 0);
+            const size_t slot_row = (size_t)(2 * run + (w.lo == 0 ? 1 : 0)) * UR + rank * QR;
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
@@ -702,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if ((lane & 3) == 0) {
                     sm.inv[ra + 8 * h] = whole ? (sum[h] > 0.f ? 1.0f / sum[h] : 0.f) : 1.f;
                     if (!whole && ok && ra + 8 * h < rows)
-                        reinterpret_cast<float2 *>(p.part_ml)[(size_t)slot * QR + ra + 8 * h] =
+                        reinterpret_cast<float2 *>(p.part_ml)[slot_row + ra + 8 * h] =
                             make_float2(m_ref[h], sum[h]);
                 }
             }
@@ -711,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 break;
             }
             tc::fence_after_sync();
-            const long long row0 = w.row0(p);
+            const long long row0 = w.row0(p) + rank * QR;
 #pragma unroll 1
             for (int c = 0; c < DB * QR; c += 32) {
                 const int r0 = c & (QR - 1), dim = (c / QR) * 128 + quarter * 32 + lane;
@@ -727,7 +762,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (r0 + i < rows)
                             dst[(size_t)i * R] = __float2bfloat16_rn(__uint_as_float(o[i]) * sm.inv[r0 + i]);
                 } else {
-                    float *dst = p.part_o + ((size_t)slot * QR + r0) * R + dim;
+                    float *dst = p.part_o + (slot_row + r0) * R + dim;
 #pragma unroll
                     for (int i = 0; i < 32; i++)
                         if (r0 + i < rows)
@@ -738,10 +773,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm.o_empty);
-            if (w.lo == 0 && !whole && tid == 0) {
+            if (w.lo == 0 && leader) {
                 // the unit ends (tiles - hi) behind the end of this run
-                const long long end = run_begin(p, sm.total, blockIdx.x + 1) + (w.tiles - w.hi);
-                p.cut[blockIdx.x] = make_int4((int)row0, rows, blockIdx.x, run_of(p, sm.total, end));
+                const long long end = run_begin(p, sm.total, run + 1) + (w.tiles - w.hi);
+                if (!whole || p.cut_by_sequence)
+                    p.cut[p.cut_by_sequence ? w.seq : run] = make_int4(
+                        (int)w.row0(p), w.rows(p, 0, UR), run, whole ? -1 : run_of(p, sm.total, end));
             }
         }
         if (!ok && lane == 0)
@@ -753,29 +790,46 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, TMEM_COLS);
     }
+    if constexpr (CL > 1)
+        cluster_sync();  // the other CTA copies and arrives into this one's shared memory
 }
 
-// Joins the pieces of the unit that CTA blockIdx.x of the first pass began and others
-// finished: R / 4 threads a row, MERGE_ROWS rows a CTA.
-constexpr int MERGE_ROWS = 4;
+// Joins the pieces of a cut unit.  R / 4 threads take a row's pieces, 8 in flight; with GROUPS
+// = 4 as many groups take a quarter of them each and are added up at the end.
+constexpr int MERGE_THREADS_PER_DIM = 4;  // rows or groups of a CTA
 
-template <int R, int QR>
-__global__ void __launch_bounds__(R / 4 * MERGE_ROWS)
+template <int R, int UR, int GROUPS>
+__global__ void __launch_bounds__(R / 4 * MERGE_THREADS_PER_DIM)
     latent_merge_kernel(const __grid_constant__ LatentParams p)
 {
+    constexpr int ROWS = MERGE_THREADS_PER_DIM / GROUPS;
+    __shared__ float4 sums[GROUPS > 1 ? GROUPS - 1 : 1][R / 4];
     grid_dependency_wait();
     grid_dependents_launch();
+    if (p.cut_by_sequence) {  // a sequence without a unit has no entry
+        int code;
+        if (sequence_of(p, blockIdx.x, code).n == 0)
+            return;
+    }
     const int4 cut = p.cut[blockIdx.x];
-    const int r = blockIdx.y * MERGE_ROWS + threadIdx.x / (R / 4), x = threadIdx.x % (R / 4);
-    const int lane = threadIdx.x & 31;
+    const int part = threadIdx.x / (R / 4), x = threadIdx.x % (R / 4), lane = threadIdx.x & 31;
+    const int r = blockIdx.y * ROWS + (GROUPS > 1 ? 0 : part), group = GROUPS > 1 ? part : 0;
     if (cut.w < 0 || r >= cut.y)
         return;
     const int pieces = cut.w - cut.z + 1;
-    // piece i in slot 2 c + 1 for the first CTA, 2 c for those after it
-    auto slot = [&](int i) { return (size_t)(2 * (cut.z + i) + (i == 0 ? 1 : 0)) * QR + r; };
+    // piece i in slot 2 c + 1 of the first run, 2 c of those after it
+    auto slot = [&](int i) { return (size_t)(2 * (cut.z + i) + (i == 0 ? 1 : 0)) * UR + r; };
+    auto load = [&](int i) { return reinterpret_cast<const float4 *>(p.part_o + slot(i) * R)[x]; };
     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml);
-    float M = -INFINITY;
-    for (int i = lane; i < pieces; i += 32)
+    // the group's first 8 pieces, and 32 pieces' maxima and sums, asked for together
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+        if (group + k * GROUPS < pieces)
+            v[k] = load(group + k * GROUPS);
+    const float2 mine = lane < pieces ? ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+    float M = mine.x;
+    for (int i = lane + 32; i < pieces; i += 32)
         M = fmaxf(M, ml[slot(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
@@ -785,23 +839,24 @@ __global__ void __launch_bounds__(R / 4 * MERGE_ROWS)
     for (int i0 = 0; i0 < pieces; i0 += 32) {
         float weight = 0.f;
         if (i0 + lane < pieces) {
-            const float2 v = ml[slot(i0 + lane)];
-            if (v.x != -INFINITY) {
-                weight = exp2f(v.x - M);
-                L = fmaf(v.y, weight, L);
+            const float2 m = i0 == 0 ? mine : ml[slot(i0 + lane)];
+            if (m.x != -INFINITY) {
+                weight = exp2f(m.x - M);
+                L = fmaf(m.y, weight, L);
             }
         }
         const int n = min(32, pieces - i0);
-        for (int i = 0; i < n; i += 8) {
-            float4 v[8];
+        for (int i = group; i < n; i += 8 * GROUPS) {
+            if (i0 + i != group) {
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-                if (i + k < n)
-                    v[k] = reinterpret_cast<const float4 *>(p.part_o + slot(i0 + i + k) * R)[x];
+                for (int k = 0; k < 8; k++)
+                    if (i + k * GROUPS < n)
+                        v[k] = load(i0 + i + k * GROUPS);
+            }
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                const float wk = __shfl_sync(0xffffffffu, weight, min(i + k, 31));
-                if (i + k < n) {
+                const float wk = __shfl_sync(0xffffffffu, weight, min(i + k * GROUPS, 31));
+                if (i + k * GROUPS < n) {
                     acc.x = fmaf(v[k].x, wk, acc.x);
                     acc.y = fmaf(v[k].y, wk, acc.y);
                     acc.z = fmaf(v[k].z, wk, acc.z);
@@ -813,6 +868,21 @@ __global__ void __launch_bounds__(R / 4 * MERGE_ROWS)
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         L += __shfl_xor_sync(0xffffffffu, L, o);
+    if constexpr (GROUPS > 1) {
+        if (group > 0)
+            sums[group - 1][x] = acc;
+        __syncthreads();
+        if (group > 0)
+            return;
+#pragma unroll
+        for (int k = 0; k < GROUPS - 1; k++) {
+            const float4 a = sums[k][x];
+            acc.x += a.x;
+            acc.y += a.y;
+            acc.z += a.z;
+            acc.w += a.w;
+        }
+    }
     const float inv = L > 0.f ? 1.0f / L : 0.f;
     uint2 u;
     u.x = pack_bf16x2(acc.x * inv, acc.y * inv);
@@ -820,7 +890,7 @@ __global__ void __launch_bounds__(R / 4 * MERGE_ROWS)
     reinterpret_cast<uint2 *>(p.out + ((size_t)cut.x + r) * R)[x] = u;
 }
 
-template <int R, int QR>
+template <int R, int QR, int CL>
 cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
     CUtensorMap mq, mkv;
@@ -837,28 +907,45 @@ cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStre
     static_assert(smem > (116u << 10) && smem <= 232448, "shared memory of one CTA per SM");
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = once_per_device(configured, [] {
-        return cudaFuncSetAttribute(latent_attn_kernel<R, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)smem);
+        return cudaFuncSetAttribute(latent_attn_kernel<R, QR, CL>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess)
         return e;
-    e = launch_kernel(latent_attn_kernel<R, QR>, dim3(p.grid), dim3(THREADS), smem, stream, p, pg, mq, mkv);
+    e = launch_kernel_cluster(latent_attn_kernel<R, QR, CL>, dim3(p.grid * CL), dim3(THREADS), smem,
+                              CL > 1 ? CL : 0, stream, p, pg, mq, mkv);
     if (e != cudaSuccess || p.grid == 1)
         return e;
-    const long long rows = (long long)p.max_new_len * p.H;
-    const int most = rows < QR ? (int)rows : QR;
-    return launch_kernel(latent_merge_kernel<R, QR>, dim3(p.grid, (most + MERGE_ROWS - 1) / MERGE_ROWS),
-                         dim3(R / 4 * MERGE_ROWS), 0, stream, p);
+    constexpr int UR = QR * CL;
+    const int rows = (int)std::min((long long)p.max_new_len * p.H, (long long)UR);
+    const dim3 block(R / 4 * MERGE_THREADS_PER_DIM);
+    const int entries = p.cut_by_sequence ? p.batch : p.grid;
+    // Few units have many pieces each (4 long contexts of 16 heads: the pass took 10 us with a
+    // thread per dim and row, every entry of every run looked at).
+    if ((long long)entries * rows <= 2 * sm_count())
+        return launch_kernel(latent_merge_kernel<R, UR, 4>, dim3(entries, rows), block, 0, stream, p);
+    return launch_kernel(latent_merge_kernel<R, UR, 1>,
+                         dim3(entries, (rows + MERGE_THREADS_PER_DIM - 1) / MERGE_THREADS_PER_DIM),
+                         block, 0, stream, p);
+}
+
+template <int R>
+cudaError_t launch_latent_rows(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
+{
+    switch (p.unit_rows) {
+    case 32: return launch_latent_t<R, 32, 1>(p, pg, stream);
+    case 64: return launch_latent_t<R, 64, 1>(p, pg, stream);
+    default: return launch_latent_t<R, 64, 2>(p, pg, stream);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_latent(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
-    const bool few = p.unit_rows == 32;
     switch (p.R) {
-    case 512: return few ? launch_latent_t<512, 32>(p, pg, stream) : launch_latent_t<512, 64>(p, pg, stream);
-    case 256: return few ? launch_latent_t<256, 32>(p, pg, stream) : launch_latent_t<256, 64>(p, pg, stream);
-    default: return few ? launch_latent_t<128, 32>(p, pg, stream) : launch_latent_t<128, 64>(p, pg, stream);
+    case 512: return launch_latent_rows<512>(p, pg, stream);
+    case 256: return launch_latent_rows<256>(p, pg, stream);
+    default: return launch_latent_rows<128>(p, pg, stream);
     }
 }
