@@ -13,14 +13,19 @@ using namespace rope;
 
 // ------------------------------------------------------------------- fork --
 //
-// One CTA: a step's tables are a few thousand entries, and every phase needs what
-// the phase before found about all sequences.  Counts of references change by
-// atomics on integers, whose order does not show, and only for parents that have
-// not exactly one child (kids - 1 for a shared page, -1 for an ended sequence's).
-// Free pages are then found in index order by a scan, page rank k going to the
-// sequence whose range of missing pages holds k.
+// A cluster of FORK_CTAS: a step's tables are a few thousand entries, and every phase
+// needs what the phase before found about all sequences, so the CTAs meet in between and
+// leave what all of them need in everybody's shared memory.  A warp takes a new row, which
+// it copies from its parent's, or an old row without a child.  Counts of references change
+// by atomics on integers, whose order does not show, and only for parents that have not
+// exactly one child (kids - 1 for a shared page, -1 for an ended sequence's).  Free pages
+// are then found in index order by a scan, page rank k going to the sequence whose range of
+// missing pages holds k.  Bound by latency: 256 sequences in 9000 pages took one CTA 26 us,
+// 17 of them for the rows.
 
-constexpr int FORK_THREADS = 1024;
+constexpr int FORK_CTAS = 8;
+constexpr int FORK_THREADS = 512;
+constexpr int FORK_PAGES = 8;  // pages per thread and round of the scan
 
 // Exclusive prefix sum of one value per thread over the CTA; `total` gets the sum.
 __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total)
@@ -37,7 +42,7 @@ __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total)
     if (lane == 31)
         warp_sums[warp] = x;
     __syncthreads();
-    const int w = warp_sums[lane];  // FORK_THREADS / 32 = 32 warps
+    const int w = lane < FORK_THREADS / 32 ? warp_sums[lane] : 0;
     int before = lane < warp ? w : 0, all = w;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -48,112 +53,124 @@ __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total)
     return before + x - v;
 }
 
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// x into the word at `at`'s place in CTA `rank` of the cluster.
+__device__ __forceinline__ void store_in_cta(int *at, int rank, int x)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(at)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+
 __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkParams p)
 {
     extern __shared__ int fork_smem[];
-    int *kids = fork_smem;              // [old_batch]
-    int *first = kids + p.old_batch;    // [old_batch]  lowest child
-    int *held = first + p.old_batch;    // [old_batch]  pages of the row
-    int *start = held + p.old_batch;    // [batch]  first missing entry
-    int *offs = start + p.batch;        // [batch + 1]  missing entries before sequence b
-    __shared__ int warp_sums[32];
+    int *kids = fork_smem;               // [old_batch]
+    int *first = kids + p.old_batch;     // [old_batch]  lowest child
+    int *lens = first + p.old_batch;     // [old_batch]
+    int *parents = lens + p.old_batch;   // [batch]
+    int *start = parents + p.batch;      // [batch]  first missing entry
+    int *offs = start + p.batch;         // [batch]  missing entries before sequence b
+    __shared__ int warp_sums[32], free_of[FORK_CTAS];
     grid_dependency_wait();
     grid_dependents_launch();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.pages_per_seq;
 
     for (int i = tid; i < p.old_batch; i += FORK_THREADS) {
         kids[i] = 0;
         first[i] = INT_MAX;
+        lens[i] = max(__ldg(p.lens + i), 0);
     }
-    for (int i = tid; i < p.num_pages; i += FORK_THREADS)
-        p.new_ref[i] = __ldg(p.ref + i);
-    __syncthreads();
     for (int b = tid; b < p.batch; b += FORK_THREADS) {
-        const int par = __ldg(p.parents + b);
+        int par = __ldg(p.parents + b);
         if (par >= p.old_batch) {
             na_report(p.status, NA_ERR_INVALID_ARG);
-        } else if (par >= 0) {
-            atomicAdd(&kids[par], 1);
-            atomicMin(&first[par], b);
+            par = -1;
         }
+        parents[b] = max(par, -1);
     }
+    for (int i = rank * FORK_THREADS + tid; i < p.num_pages; i += FORK_CTAS * FORK_THREADS)
+        p.new_ref[i] = __ldg(p.ref + i);
     __syncthreads();
+    for (int b = tid; b < p.batch; b += FORK_THREADS)
+        if (parents[b] >= 0) {
+            atomicAdd(&kids[parents[b]], 1);
+            atomicMin(&first[parents[b]], b);
+        }
+    cluster_sync();  // (and every thread of the CTA)
 
-    // Old rows: a warp each.  How many pages a row holds, and what becomes of their counts.
-    for (int r = warp; r < p.old_batch; r += FORK_THREADS / 32) {
-        const int32_t *row = p.table + (size_t)r * P;
-        const int full = max(__ldg(p.lens + r), 0) >> p.page_log;
-        const int k = kids[r];
-        int n = P;
+    // Items: new rows, then old rows (of which those without a child).
+    for (int i = rank * (FORK_THREADS / 32) + warp; i < p.batch + p.old_batch;
+         i += FORK_CTAS * (FORK_THREADS / 32)) {
+        const bool fresh = i < p.batch;
+        const int row = fresh ? parents[i] : (kids[i - p.batch] == 0 ? i - p.batch : -1);
+        if (!fresh && row < 0)
+            continue;
+        int grow = fresh && p.grow ? __ldg(p.grow + i) : 0;
+        const int n = row >= 0 ? lens[row] : 0, full = n >> p.page_log;
+        // the row's counts change: once for each page, by the lowest child or without one
+        const bool elder = row >= 0 && (!fresh || first[row] == i);
+        const int shared = row >= 0 ? kids[row] - 1 : 0;
+        int32_t *to = p.new_table + (size_t)i * P;
+        int held = P;
+        bool end = false;
         for (int base = 0; base < P; base += 128) {
             int e[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int j = base + i * 32 + lane;
-                e[i] = j < P ? __ldg(row + j) : -1;
+            for (int k = 0; k < 4; k++) {
+                const int j = base + k * 32 + lane;
+                e[k] = row >= 0 && j < P && !end ? __ldg(p.table + (size_t)row * P + j) : -1;
             }
-            bool end = false;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const unsigned bad = __ballot_sync(0xffffffffu, (unsigned)e[i] >= (unsigned)p.num_pages);
-                if (end)
-                    continue;
-                const int good = bad ? __ffs(bad) - 1 : 32;
-                const int j = base + i * 32 + lane;
-                if (lane < good) {
-                    const int delta = k == 0 ? -1 : (j < full ? k - 1 : 0);
-                    if (delta != 0)
-                        atomicAdd(p.new_ref + e[i], delta);
-                }
-                if (bad) {
+            for (int k = 0; k < 4; k++) {
+                const int j0 = base + k * 32, j = j0 + lane;
+                const bool is_page = !end && (unsigned)e[k] < (unsigned)p.num_pages;
+                const unsigned bad = __ballot_sync(0xffffffffu, !is_page);
+                const int good = bad ? __ffs(bad) - 1 : 32;  // 0 behind the row's end
+                if (bad && !end) {
                     end = true;
-                    n = min(base + i * 32 + good, P);
-                    if (lane == good && e[i] >= 0)
+                    held = min(j0 + good, P);
+                    if (elder && lane == good && e[k] >= 0)
                         na_report(p.status, NA_ERR_PAGE);
                 }
+                const int delta = fresh && j >= full ? 0 : shared;
+                if (elder && lane < good && delta != 0)
+                    atomicAdd(p.new_ref + e[k], delta);
+                if (fresh && j < P)
+                    to[j] = lane < good && (elder || j < full) ? e[k] : -1;
             }
-            if (end)
+            if (end && !fresh)
                 break;
         }
-        if (lane == 0)
-            held[r] = n;
-    }
-    __syncthreads();
-
-    // New rows: a warp each.
-    for (int b = warp; b < p.batch; b += FORK_THREADS / 32) {
-        int par = __ldg(p.parents + b);
-        if (par >= p.old_batch)
-            par = -1;
-        const int n = par >= 0 ? max(__ldg(p.lens + par), 0) : 0;
-        int grow = p.grow ? __ldg(p.grow + b) : 0;
-        const int have = par >= 0 ? held[par] : 0;
-        const bool elder = par >= 0 && first[par] == b;
-        const int mine = elder ? have : min(n >> p.page_log, have);
+        if (!fresh)
+            continue;
+        held = row >= 0 ? held : 0;
+        const int mine = elder ? held : min(full, held);
+        const long long pages = ((long long)n + max(grow, 0) + (1 << p.page_log) - 1) >> p.page_log;
+        if (lane < FORK_CTAS) {
+            store_in_cta(start + i, lane, mine);
+            store_in_cta(offs + i, lane, max((int)min(pages, (long long)P) - mine, 0));
+        }
         if (lane == 0) {
             if (grow < 0)
                 na_report(p.status, NA_ERR_INVALID_ARG);
-            if (((long long)have << p.page_log) < n)
+            if (((long long)held << p.page_log) < n)
                 na_report(p.status, NA_ERR_PAGE);
-        }
-        grow = max(grow, 0);
-        const long long pages = ((long long)n + grow + (1 << p.page_log) - 1) >> p.page_log;
-        if (pages > P && lane == 0)
-            na_report(p.status, NA_ERR_CAPACITY);
-        const int32_t *from = p.table + (size_t)max(par, 0) * P;
-        int32_t *to = p.new_table + (size_t)b * P;
-        for (int j = lane; j < P; j += 32)
-            to[j] = j < mine ? __ldg(from + j) : -1;
-        if (lane == 0) {
-            start[b] = mine;
-            offs[b] = max((int)min(pages, (long long)P) - mine, 0);
-            p.new_lens[b] = n;
+            if (pages > P)
+                na_report(p.status, NA_ERR_CAPACITY);
+            p.new_lens[i] = n;
+            // a part-filled page that is there is copied for all children but the first
+            p.copy_src[i] = row >= 0 && !elder && (n & ((1 << p.page_log) - 1)) && full < held;
         }
     }
-    __syncthreads();
+    cluster_sync();
 
-    // Missing pages before each sequence's.
+    // Missing pages before each sequence's, in every CTA.
     int missing = 0;
     for (int base = 0; base < p.batch; base += FORK_THREADS) {
         const int b = base + tid;
@@ -163,52 +180,67 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
             offs[b] = missing + before;
         missing += sum;
     }
-    if (tid == 0)
-        offs[p.batch] = missing;
-    __syncthreads();
 
-    // Free pages in order, four to a thread and round.
-    int found = 0;
-    for (int base = 0; base < p.num_pages && found < missing; base += 4 * FORK_THREADS) {
-        const int i0 = base + 4 * tid;
+    // Free pages in order: a CTA's run of pages, counted, then ranked behind the runs before.
+    constexpr int ROUND = FORK_THREADS * FORK_PAGES;
+    const int run = (p.num_pages + FORK_CTAS - 1) / FORK_CTAS;
+    const int p0 = min(rank * run, p.num_pages), p1 = min(p0 + run, p.num_pages);
+    auto free_at = [&](int at) {  // which of FORK_PAGES pages are free
         unsigned free = 0;
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (i0 + i < p.num_pages && __ldcg(p.new_ref + i0 + i) == 0)
+        for (int i = 0; i < FORK_PAGES; i++)
+            if (at + i < p1 && __ldcg(p.new_ref + at + i) == 0)
                 free |= 1u << i;
+        return free;
+    };
+    const unsigned free0 = free_at(p0 + FORK_PAGES * tid);  // the first round's
+    int count = __popc(free0);
+    for (int at = p0 + ROUND + FORK_PAGES * tid; at < p1; at += ROUND)
+        count += __popc(free_at(at));
+    int total;
+    block_prefix(count, warp_sums, total);
+    if (tid < FORK_CTAS)
+        store_in_cta(free_of + rank, tid, total);
+    cluster_sync();
+    int found = 0, all = 0;
+#pragma unroll
+    for (int c = 0; c < FORK_CTAS; c++) {
+        found += c < rank ? free_of[c] : 0;
+        all += free_of[c];
+    }
+    for (int base = p0; base < p1 && found < missing; base += ROUND) {
+        const int at = base + FORK_PAGES * tid;
+        const unsigned free = base == p0 ? free0 : free_at(at);
         int sum;
-        int rank = found + block_prefix(__popc(free), warp_sums, sum);
+        int k = found + block_prefix(__popc(free), warp_sums, sum);
         found += sum;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if (!(free >> i & 1) || rank >= missing)
+        for (int i = 0; i < FORK_PAGES; i++) {
+            if (!(free >> i & 1) || k >= missing)
                 continue;
-            int lo = 0, hi = p.batch - 1;  // the last b with offs[b] <= rank
+            int lo = 0, hi = p.batch - 1;  // the last b with offs[b] <= k
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (offs[mid] <= rank)
+                if (offs[mid] <= k)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
-            p.new_table[(size_t)lo * P + start[lo] + (rank - offs[lo])] = i0 + i;
-            p.new_ref[i0 + i] = 1;
-            rank++;
+            p.new_table[(size_t)lo * P + start[lo] + (k - offs[lo])] = at + i;
+            p.new_ref[at + i] = 1;
+            k++;
         }
     }
-    if (found < missing && tid == 0)
+    if (all < missing && rank == 0 && tid == 0)
         na_report(p.status, NA_ERR_CAPACITY);
-    __syncthreads();
+    cluster_sync();
 
-    for (int b = tid; b < p.batch; b += FORK_THREADS) {
-        const int par = __ldg(p.parents + b);
+    for (int b = rank * FORK_THREADS + tid; b < p.batch; b += FORK_CTAS * FORK_THREADS) {
         int src = -1, dst = -1;
-        if (par >= 0 && par < p.old_batch && first[par] != b) {
-            const int n = max(__ldg(p.lens + par), 0), j = n >> p.page_log;
-            if ((n & ((1 << p.page_log) - 1)) && j < held[par]) {
-                dst = __ldcg(p.new_table + (size_t)b * P + j);
-                src = dst >= 0 ? __ldg(p.table + (size_t)par * P + j) : -1;
-            }
+        if (__ldcg(p.copy_src + b)) {
+            const int j = lens[parents[b]] >> p.page_log;
+            dst = __ldcg(p.new_table + (size_t)b * P + j);
+            src = dst >= 0 ? __ldg(p.table + (size_t)parents[b] * P + j) : -1;
         }
         p.copy_src[b] = src;
         p.copy_dst[b] = dst;
@@ -357,91 +389,124 @@ struct Words<1> {
 
 constexpr int COMPACT_THREADS = 256;
 constexpr int COMPACT_ROWS = 16;
-constexpr int COMPACT_HEADS = 4;  // heads whose loads are in flight together
+constexpr int COMPACT_LOADS = 4;  // units whose loads a thread has in flight
 
-// bf16: a CTA moves COMPACT_ROWS rows of one sequence.  A thread takes one unit of a
-// row for every kv head, so that cos and sin are computed once for all heads.
+// bf16: a CTA moves COMPACT_ROWS rows of one sequence, all kv heads of K and V: where they
+// come from and go to, and cos and sin of their shifts, are found once and left in shared
+// memory.  Then units of 16 bytes (pairs of them where K turns), consecutive lanes along a
+// row, COMPACT_LOADS loads ahead of the stores.
 template <int W>
 __global__ void __launch_bounds__(COMPACT_THREADS)
     pages_compact_kernel(const __grid_constant__ CompactParams p,
                          const __grid_constant__ RopeTurns turns, int row_blocks)
 {
     typedef typename Words<W>::T Word;
+    extern __shared__ float4 cos_sin[];  // [row][rd / 2]
+    __shared__ long long src_at[COMPACT_ROWS], dst_at[COMPACT_ROWS];  // element of head 0; -1: no place
+    __shared__ int shift_of[COMPACT_ROWS];
     grid_dependency_wait();
     grid_dependents_launch();
     const int b = blockIdx.x / row_blocks, j0 = (blockIdx.x - b * row_blocks) * COMPACT_ROWS;
     const int n = min(kept_rows(p, b) - j0, COMPACT_ROWS);
-    const int pairs = p.turn ? p.rd / 2 / W : 0;
-    const int k_units = pairs + (p.d - (p.turn ? p.rd : 0)) / W;
-    const int units = k_units + (p.to_v ? p.d / W : 0);
-    for (int i = threadIdx.x; i < n * units; i += COMPACT_THREADS) {
-        const int r = i / units;
-        int u = i - r * units;
+    if (n <= 0)
+        return;
+    const int half = p.turn ? p.rd / 2 : 0;
+    if (threadIdx.x < n) {
         Move m;
-        if (!find_move(p, b, j0 + r, m))
-            continue;
-        const bool is_v = u >= k_units;
+        const bool there = find_move(p, b, j0 + threadIdx.x, m);
+        src_at[threadIdx.x] =
+            there ? (((long long)m.src * p.KV << p.from.page_log) + m.src_slot) * p.d : -1;
+        dst_at[threadIdx.x] = there ? (((long long)m.dst * p.KV << p.to.page_log) + m.dst_slot) * p.d : -1;
+        shift_of[threadIdx.x] = there ? m.shift : 0;
+    }
+    __syncthreads();
+    const long long src_head = (long long)p.d << p.from.page_log, dst_head = (long long)p.d << p.to.page_log;
+
+    // What does not turn: V, and K's other dimensions.
+    const int k_plain = (p.d - 2 * half) / W, units = k_plain + (p.to_v ? p.d / W : 0);
+    const int per_row = units * p.KV;
+    auto plain = [&](int i, const Word *&from, Word *&to) {
+        const int r = i / per_row, y = i - r * per_row, g = y / units;
+        int u = y - g * units;
+        const bool is_v = u >= k_plain;
         if (is_v)
-            u -= k_units;
-        const size_t src_head = (size_t)p.d << p.from.page_log, dst_head = (size_t)p.d << p.to.page_log;
-        const bf16 *from = reinterpret_cast<const bf16 *>(is_v ? p.from_v : p.from_k) +
-                           (size_t)m.src * p.KV * src_head + (size_t)m.src_slot * p.d;
-        bf16 *to = reinterpret_cast<bf16 *>(is_v ? p.to_v : p.to_k) + (size_t)m.dst * p.KV * dst_head +
-                   (size_t)m.dst_slot * p.d;
-        if (is_v || u >= pairs) {
-            const int e = is_v ? u * W : (p.turn ? plain_unit<W>(p, u - pairs) : (u - pairs) * W);
-            for (int g = 0; g < p.KV; g += COMPACT_HEADS) {
-                Word x[COMPACT_HEADS];
+            u -= k_plain;
+        const int e = is_v || !p.turn ? u * W : plain_unit<W>(p, u);
+        from = reinterpret_cast<const Word *>(reinterpret_cast<const bf16 *>(is_v ? p.from_v : p.from_k) +
+                                              src_at[r] + g * src_head + e);
+        to = reinterpret_cast<Word *>(reinterpret_cast<bf16 *>(is_v ? p.to_v : p.to_k) + dst_at[r] +
+                                      g * dst_head + e);
+        return src_at[r] >= 0;
+    };
+    for (int i0 = threadIdx.x; i0 < n * per_row; i0 += COMPACT_THREADS * COMPACT_LOADS) {
+        Word x[COMPACT_LOADS];
+        Word *to[COMPACT_LOADS];
 #pragma unroll
-                for (int h = 0; h < COMPACT_HEADS; h++)
-                    if (g + h < p.KV)
-                        x[h] = *reinterpret_cast<const Word *>(from + (g + h) * src_head + e);
-#pragma unroll
-                for (int h = 0; h < COMPACT_HEADS; h++)
-                    if (g + h < p.KV)
-                        *reinterpret_cast<Word *>(to + (g + h) * dst_head + e) = x[h];
-            }
-            continue;
+        for (int k = 0; k < COMPACT_LOADS; k++) {
+            const int i = i0 + k * COMPACT_THREADS;
+            const Word *from;
+            if (i < n * per_row && plain(i, from, to[k]))
+                x[k] = *from;
+            else
+                to[k] = nullptr;
         }
-        int e0, e1;
-        pair_unit<W>(p, u, e0, e1);
-        float4 cs[W];
-        for (int g = 0; g < p.KV; g += COMPACT_HEADS) {
-            Word x0[COMPACT_HEADS], x1[COMPACT_HEADS];
 #pragma unroll
-            for (int h = 0; h < COMPACT_HEADS; h++)
-                if (g + h < p.KV) {
-                    x0[h] = *reinterpret_cast<const Word *>(from + (g + h) * src_head + e0);
-                    x1[h] = *reinterpret_cast<const Word *>(from + (g + h) * src_head + e1);
+        for (int k = 0; k < COMPACT_LOADS; k++)
+            if (to[k])
+                *to[k] = x[k];
+    }
+    if (half == 0)
+        return;
+
+    for (int i = threadIdx.x; i < n * half; i += COMPACT_THREADS) {
+        const int r = i / half;
+        cos_sin[i] = turn_back(turns, i - r * half, shift_of[r]);
+    }
+    __syncthreads();
+    const int pairs = half / W, pairs_per_row = pairs * p.KV;
+    for (int i0 = threadIdx.x; i0 < n * pairs_per_row; i0 += COMPACT_THREADS * 2) {
+        Word x0[2], x1[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int i = i0 + k * COMPACT_THREADS, r = i / pairs_per_row, y = i - r * pairs_per_row;
+            if (i >= n * pairs_per_row || src_at[r] < 0)
+                continue;
+            int e0, e1;
+            pair_unit<W>(p, y % pairs, e0, e1);
+            const bf16 *from = reinterpret_cast<const bf16 *>(p.from_k) + src_at[r] + y / pairs * src_head;
+            x0[k] = *reinterpret_cast<const Word *>(from + e0);
+            x1[k] = *reinterpret_cast<const Word *>(from + e1);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int i = i0 + k * COMPACT_THREADS, r = i / pairs_per_row, y = i - r * pairs_per_row;
+            if (i >= n * pairs_per_row || src_at[r] < 0)
+                continue;
+            const int u = y % pairs;
+            int e0, e1;
+            pair_unit<W>(p, u, e0, e1);
+            if (shift_of[r] != 0) {  // (a row that stays keeps its bits, NaN's too)
+                const float4 *cs = cos_sin + r * half + u * W;
+                float a[2 * W], z[2 * W];
+                Words<W>::widen(x0[k], a);
+                Words<W>::widen(x1[k], a + W);
+#pragma unroll
+                for (int w = 0; w < W; w++) {
+                    rotate_exact(p.interleaved ? a[2 * w] : a[w], p.interleaved ? a[2 * w + 1] : a[W + w],
+                                 cs[w], 1.0f, z[2 * w], z[2 * w + 1]);
                 }
-            if (g == 0) {
+                float lo[W], hi[W];  // z holds the pairs one after the other
 #pragma unroll
-                for (int w = 0; w < W; w++)
-                    cs[w] = turn_back(turns, u * W + w, m.shift);
+                for (int w = 0; w < W; w++) {
+                    lo[w] = p.interleaved ? z[w] : z[2 * w];
+                    hi[w] = p.interleaved ? z[W + w] : z[2 * w + 1];
+                }
+                x0[k] = Words<W>::round(lo);
+                x1[k] = Words<W>::round(hi);
             }
-#pragma unroll
-            for (int h = 0; h < COMPACT_HEADS; h++) {
-                if (g + h >= p.KV)
-                    continue;
-                float a[2 * W], y[2 * W];
-                Words<W>::widen(x0[h], a);
-                Words<W>::widen(x1[h], a + W);
-                if (p.interleaved) {
-#pragma unroll
-                    for (int w = 0; w < W; w++)
-                        rotate_exact(a[2 * w], a[2 * w + 1], cs[w], 1.0f, y[2 * w], y[2 * w + 1]);
-                } else {
-#pragma unroll
-                    for (int w = 0; w < W; w++)
-                        rotate_exact(a[w], a[W + w], cs[w], 1.0f, y[w], y[W + w]);
-                }
-                if (m.shift != 0) {  // (a row that stays keeps its bits, NaN's too)
-                    x0[h] = Words<W>::round(y);
-                    x1[h] = Words<W>::round(y + W);
-                }
-                *reinterpret_cast<Word *>(to + (g + h) * dst_head + e0) = x0[h];
-                *reinterpret_cast<Word *>(to + (g + h) * dst_head + e1) = x1[h];
-            }
+            bf16 *to = reinterpret_cast<bf16 *>(p.to_k) + dst_at[r] + y / pairs * dst_head;
+            *reinterpret_cast<Word *>(to + e0) = x0[k];
+            *reinterpret_cast<Word *>(to + e1) = x1[k];
         }
     }
 }
@@ -586,15 +651,16 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
 
 cudaError_t launch_pages_fork(const ForkParams &p, cudaStream_t stream)
 {
-    const size_t smem = (3 * (size_t)p.old_batch + 2 * (size_t)p.batch + 1) * sizeof(int);
+    const size_t smem = 3 * ((size_t)p.old_batch + p.batch) * sizeof(int);
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = once_per_device(configured, [] {
         return cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (5 * kMaxForkBatch + 1) * (int)sizeof(int));
+                                    6 * kMaxForkBatch * (int)sizeof(int));
     });
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(pages_fork_kernel, dim3(1), dim3(FORK_THREADS), smem, stream, p);
+    return launch_kernel_cluster(pages_fork_kernel, dim3(FORK_CTAS), dim3(FORK_THREADS), smem, FORK_CTAS,
+                                 stream, p);
 }
 
 cudaError_t launch_pages_copy(const PageCopyParams &p, cudaStream_t stream)
@@ -637,7 +703,8 @@ cudaError_t launch_pages_compact(const CompactParams &p, bool e4m3, const RopeTu
     const int blocks = (p.max_keep + COMPACT_ROWS - 1) / COMPACT_ROWS;
     if ((long long)blocks * p.batch > INT_MAX)
         return cudaErrorInvalidConfiguration;
+    const size_t smem = (size_t)COMPACT_ROWS * (p.turn ? p.rd / 2 : 0) * sizeof(float4);  // 16 KB at most
     return launch_kernel(unit ? pages_compact_kernel<1> : pages_compact_kernel<8>,
-                         dim3((unsigned)(blocks * p.batch)), dim3(COMPACT_THREADS), 0, stream, p,
+                         dim3((unsigned)(blocks * p.batch)), dim3(COMPACT_THREADS), smem, stream, p,
                          turns, blocks);
 }
