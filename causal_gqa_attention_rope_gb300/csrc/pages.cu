@@ -24,8 +24,8 @@ using namespace rope;
 // 17 of them for the rows.
 
 constexpr int FORK_CTAS = 8;
-constexpr int FORK_THREADS = 512;
-constexpr int FORK_PAGES = 8;  // pages per thread and round of the scan
+constexpr int FORK_THREADS = 1024;
+constexpr int FORK_PAGES = 2;  // pages per thread and round of the scan
 
 // Exclusive prefix sum of one value per thread over the CTA; `total` gets the sum.
 __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total)
@@ -214,18 +214,22 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
         int sum;
         int k = found + block_prefix(__popc(free), warp_sums, sum);
         found += sum;
+        if (!free || k >= missing)
+            continue;
+        int lo = 0, hi = p.batch - 1;  // the last b with offs[b] <= k
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (offs[mid] <= k)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
 #pragma unroll
         for (int i = 0; i < FORK_PAGES; i++) {
             if (!(free >> i & 1) || k >= missing)
                 continue;
-            int lo = 0, hi = p.batch - 1;  // the last b with offs[b] <= k
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (offs[mid] <= k)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
+            while (lo + 1 < p.batch && offs[lo + 1] <= k)
+                lo++;
             p.new_table[(size_t)lo * P + start[lo] + (k - offs[lo])] = at + i;
             p.new_ref[at + i] = 1;
             k++;
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
                          const __grid_constant__ RopeTurns turns, int row_blocks)
 {
     typedef typename Words<W>::T Word;
-    extern __shared__ float4 cos_sin[];  // [row][rd / 2]
+    extern __shared__ float4 cos_sin[];  // [row][W][pairs / W]: without bank conflicts between units
     __shared__ long long src_at[COMPACT_ROWS], dst_at[COMPACT_ROWS];  // element of head 0; -1: no place
     __shared__ int shift_of[COMPACT_ROWS];
     grid_dependency_wait();
@@ -459,8 +463,8 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
         return;
 
     for (int i = threadIdx.x; i < n * half; i += COMPACT_THREADS) {
-        const int r = i / half;
-        cos_sin[i] = turn_back(turns, i - r * half, shift_of[r]);
+        const int r = i / half, u = i - r * half;
+        cos_sin[r * half + u % W * (half / W) + u / W] = turn_back(turns, u, shift_of[r]);
     }
     __syncthreads();
     const int pairs = half / W, pairs_per_row = pairs * p.KV;
@@ -486,14 +490,14 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
             int e0, e1;
             pair_unit<W>(p, u, e0, e1);
             if (shift_of[r] != 0) {  // (a row that stays keeps its bits, NaN's too)
-                const float4 *cs = cos_sin + r * half + u * W;
+                const float4 *cs = cos_sin + r * half + u;
                 float a[2 * W], z[2 * W];
                 Words<W>::widen(x0[k], a);
                 Words<W>::widen(x1[k], a + W);
 #pragma unroll
                 for (int w = 0; w < W; w++) {
                     rotate_exact(p.interleaved ? a[2 * w] : a[w], p.interleaved ? a[2 * w + 1] : a[W + w],
-                                 cs[w], 1.0f, z[2 * w], z[2 * w + 1]);
+                                 cs[w * pairs], 1.0f, z[2 * w], z[2 * w + 1]);
                 }
                 float lo[W], hi[W];  // z holds the pairs one after the other
 #pragma unroll
