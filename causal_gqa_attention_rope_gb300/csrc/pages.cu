@@ -359,15 +359,20 @@ __device__ __forceinline__ int kept_rows(const CompactParams &p, int b)
     return n;
 }
 
-// cos and sin of pair i turned back by `shift` positions (forward for a negative one).
-__device__ __forceinline__ float4 turn_back(const RopeTurns &t, int i, int shift)
+// cos and sin of pair i turned back by `shift` positions (forward for a negative one), each
+// within 2^-24: the phase in 2^-32 of a turn, split into the nearest 1 / 256 turn (a table)
+// and a remainder |r| <= pi / 256, whose series are cut where the next term is below 2^-37.
+__device__ __forceinline__ float2 turn_back(const RopeTurns &t, int i, int shift)
 {
-    float4 c = cos_sin_turns((unsigned)abs(shift), t.hi[i], t.lo[i], kTrig.e);
-    if (shift > 0) {
-        c.z = -c.z;
-        c.w = -c.w;
-    }
-    return c;
+    const uint32_t u = (uint32_t)(((unsigned long long)(unsigned)abs(shift) * t.hi[i]) >> 32) + (1u << 23);
+    const TrigEntry e = kTrig.e[u >> 24];
+    const float r = (float)((int)(u & 0xffffffu) - (1 << 23)) * (kTwoPiHi * 0x1p-32f);
+    const float z = r * r;
+    const float c1 = z * fmaf(z, 1.0f / 24.0f, -0.5f);     // cos r - 1
+    const float sr = fmaf(r * z, -1.0f / 6.0f, r);         // sin r
+    const float c = e.ch + fmaf(e.ch, c1, fmaf(-e.sh, sr, e.cl));
+    const float s = e.sh + fmaf(e.sh, c1, fmaf(e.ch, sr, e.sl));
+    return make_float2(c, shift > 0 ? -s : s);
 }
 
 template <int W>
@@ -393,19 +398,37 @@ struct Words<1> {
 
 constexpr int COMPACT_THREADS = 256;
 constexpr int COMPACT_ROWS = 16;
-constexpr int COMPACT_LOADS = 4;  // units whose loads a thread has in flight
+constexpr int COMPACT_LOADS = 4;       // units whose loads a thread has in flight
+constexpr int COMPACT_TURN_LOADS = 2;  // the same of those that turn
+
+// The first of `units` that this thread takes and the first row it does so for; the next row
+// is `apart` further.  Rows that are narrower than the CTA are taken side by side.
+__device__ __forceinline__ int first_unit(int units, int &row, int &apart)
+{
+    apart = max(COMPACT_THREADS / max(units, 1), 1);
+    if (units >= COMPACT_THREADS) {
+        row = 0;
+        return threadIdx.x;
+    }
+    row = threadIdx.x / max(units, 1);
+    return row < apart ? (int)threadIdx.x - row * units : units;
+}
 
 // bf16: a CTA moves COMPACT_ROWS rows of one sequence, all kv heads of K and V: where they
 // come from and go to, and cos and sin of their shifts, are found once and left in shared
 // memory.  Then units of 16 bytes (pairs of them where K turns), consecutive lanes along a
-// row, COMPACT_LOADS loads ahead of the stores.
+// row, a thread the same one of several rows: COMPACT_LOADS loads ahead of the stores, and
+// one division for all of them.  64 sequences of 512 .. 8192 tokens, 8 kv heads, a quarter
+// kept: 101 us, 0.80 of the copy bandwidth; 86 us where nothing turns, which is what rows of
+// 256 bytes out of four times as many cost.  Turning is bound by instructions: with cos and
+// sin as pairs of fp32 numbers and a division per unit it took 141 us.
 template <int W>
-__global__ void __launch_bounds__(COMPACT_THREADS)
+__global__ void __launch_bounds__(COMPACT_THREADS, 5)
     pages_compact_kernel(const __grid_constant__ CompactParams p,
                          const __grid_constant__ RopeTurns turns, int row_blocks)
 {
     typedef typename Words<W>::T Word;
-    extern __shared__ float4 cos_sin[];  // [row][W][pairs / W]: without bank conflicts between units
+    extern __shared__ float2 cos_sin[];  // [row][W][pairs / W]: without bank conflicts between units
     __shared__ long long src_at[COMPACT_ROWS], dst_at[COMPACT_ROWS];  // element of head 0; -1: no place
     __shared__ int shift_of[COMPACT_ROWS];
     grid_dependency_wait();
@@ -428,36 +451,31 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
 
     // What does not turn: V, and K's other dimensions.
     const int k_plain = (p.d - 2 * half) / W, units = k_plain + (p.to_v ? p.d / W : 0);
-    const int per_row = units * p.KV;
-    auto plain = [&](int i, const Word *&from, Word *&to) {
-        const int r = i / per_row, y = i - r * per_row, g = y / units;
+    int r0, rows_apart;
+    for (int y = first_unit(units * p.KV, r0, rows_apart); y < units * p.KV; y += COMPACT_THREADS) {
+        const int g = y / units;
         int u = y - g * units;
         const bool is_v = u >= k_plain;
         if (is_v)
             u -= k_plain;
         const int e = is_v || !p.turn ? u * W : plain_unit<W>(p, u);
-        from = reinterpret_cast<const Word *>(reinterpret_cast<const bf16 *>(is_v ? p.from_v : p.from_k) +
-                                              src_at[r] + g * src_head + e);
-        to = reinterpret_cast<Word *>(reinterpret_cast<bf16 *>(is_v ? p.to_v : p.to_k) + dst_at[r] +
-                                      g * dst_head + e);
-        return src_at[r] >= 0;
-    };
-    for (int i0 = threadIdx.x; i0 < n * per_row; i0 += COMPACT_THREADS * COMPACT_LOADS) {
-        Word x[COMPACT_LOADS];
-        Word *to[COMPACT_LOADS];
+        const bf16 *from = reinterpret_cast<const bf16 *>(is_v ? p.from_v : p.from_k) + g * src_head + e;
+        bf16 *to = reinterpret_cast<bf16 *>(is_v ? p.to_v : p.to_k) + g * dst_head + e;
+        for (int ra = r0; ra < n; ra += rows_apart * COMPACT_LOADS) {
+            Word x[COMPACT_LOADS];
 #pragma unroll
-        for (int k = 0; k < COMPACT_LOADS; k++) {
-            const int i = i0 + k * COMPACT_THREADS;
-            const Word *from;
-            if (i < n * per_row && plain(i, from, to[k]))
-                x[k] = *from;
-            else
-                to[k] = nullptr;
+            for (int k = 0; k < COMPACT_LOADS; k++) {
+                const int r = ra + k * rows_apart;
+                if (r < n && src_at[r] >= 0)
+                    x[k] = *reinterpret_cast<const Word *>(from + src_at[r]);
+            }
+#pragma unroll
+            for (int k = 0; k < COMPACT_LOADS; k++) {
+                const int r = ra + k * rows_apart;
+                if (r < n && src_at[r] >= 0)
+                    *reinterpret_cast<Word *>(to + dst_at[r]) = x[k];
+            }
         }
-#pragma unroll
-        for (int k = 0; k < COMPACT_LOADS; k++)
-            if (to[k])
-                *to[k] = x[k];
     }
     if (half == 0)
         return;
@@ -467,50 +485,52 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
         cos_sin[r * half + u % W * (half / W) + u / W] = turn_back(turns, u, shift_of[r]);
     }
     __syncthreads();
-    const int pairs = half / W, pairs_per_row = pairs * p.KV;
-    for (int i0 = threadIdx.x; i0 < n * pairs_per_row; i0 += COMPACT_THREADS * 2) {
-        Word x0[2], x1[2];
+    const int pairs = half / W;
+    for (int y = first_unit(pairs * p.KV, r0, rows_apart); y < pairs * p.KV; y += COMPACT_THREADS) {
+        const int g = y / pairs, u = y - g * pairs;
+        int e0, e1;
+        pair_unit<W>(p, u, e0, e1);
+        const bf16 *from = reinterpret_cast<const bf16 *>(p.from_k) + g * src_head;
+        bf16 *to = reinterpret_cast<bf16 *>(p.to_k) + g * dst_head;
+        for (int ra = r0; ra < n; ra += rows_apart * COMPACT_TURN_LOADS) {
+            Word x0[COMPACT_TURN_LOADS], x1[COMPACT_TURN_LOADS];
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const int i = i0 + k * COMPACT_THREADS, r = i / pairs_per_row, y = i - r * pairs_per_row;
-            if (i >= n * pairs_per_row || src_at[r] < 0)
-                continue;
-            int e0, e1;
-            pair_unit<W>(p, y % pairs, e0, e1);
-            const bf16 *from = reinterpret_cast<const bf16 *>(p.from_k) + src_at[r] + y / pairs * src_head;
-            x0[k] = *reinterpret_cast<const Word *>(from + e0);
-            x1[k] = *reinterpret_cast<const Word *>(from + e1);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const int i = i0 + k * COMPACT_THREADS, r = i / pairs_per_row, y = i - r * pairs_per_row;
-            if (i >= n * pairs_per_row || src_at[r] < 0)
-                continue;
-            const int u = y % pairs;
-            int e0, e1;
-            pair_unit<W>(p, u, e0, e1);
-            if (shift_of[r] != 0) {  // (a row that stays keeps its bits, NaN's too)
-                const float4 *cs = cos_sin + r * half + u;
-                float a[2 * W], z[2 * W];
-                Words<W>::widen(x0[k], a);
-                Words<W>::widen(x1[k], a + W);
-#pragma unroll
-                for (int w = 0; w < W; w++) {
-                    rotate_exact(p.interleaved ? a[2 * w] : a[w], p.interleaved ? a[2 * w + 1] : a[W + w],
-                                 cs[w * pairs], 1.0f, z[2 * w], z[2 * w + 1]);
+            for (int k = 0; k < COMPACT_TURN_LOADS; k++) {
+                const int r = ra + k * rows_apart;
+                if (r < n && src_at[r] >= 0) {
+                    x0[k] = *reinterpret_cast<const Word *>(from + src_at[r] + e0);
+                    x1[k] = *reinterpret_cast<const Word *>(from + src_at[r] + e1);
                 }
-                float lo[W], hi[W];  // z holds the pairs one after the other
-#pragma unroll
-                for (int w = 0; w < W; w++) {
-                    lo[w] = p.interleaved ? z[w] : z[2 * w];
-                    hi[w] = p.interleaved ? z[W + w] : z[2 * w + 1];
-                }
-                x0[k] = Words<W>::round(lo);
-                x1[k] = Words<W>::round(hi);
             }
-            bf16 *to = reinterpret_cast<bf16 *>(p.to_k) + dst_at[r] + y / pairs * dst_head;
-            *reinterpret_cast<Word *>(to + e0) = x0[k];
-            *reinterpret_cast<Word *>(to + e1) = x1[k];
+#pragma unroll
+            for (int k = 0; k < COMPACT_TURN_LOADS; k++) {
+                const int r = ra + k * rows_apart;
+                if (r >= n || src_at[r] < 0)
+                    continue;
+                if (shift_of[r] != 0) {  // (a row that stays keeps its bits, NaN's too)
+                    const float2 *cs = cos_sin + r * half + u;
+                    float a[2 * W], z[2 * W], lo[W], hi[W];
+                    Words<W>::widen(x0[k], a);
+                    Words<W>::widen(x1[k], a + W);
+#pragma unroll
+                    for (int w = 0; w < W; w++) {  // z: the pairs one after the other
+                        const float2 c = cs[w * pairs];
+                        const float a0 = p.interleaved ? a[2 * w] : a[w];
+                        const float a1 = p.interleaved ? a[2 * w + 1] : a[W + w];
+                        z[2 * w] = fmaf(a0, c.x, -a1 * c.y);
+                        z[2 * w + 1] = fmaf(a1, c.x, a0 * c.y);
+                    }
+#pragma unroll
+                    for (int w = 0; w < W; w++) {
+                        lo[w] = p.interleaved ? z[w] : z[2 * w];
+                        hi[w] = p.interleaved ? z[W + w] : z[2 * w + 1];
+                    }
+                    x0[k] = Words<W>::round(lo);
+                    x1[k] = Words<W>::round(hi);
+                }
+                *reinterpret_cast<Word *>(to + dst_at[r] + e0) = x0[k];
+                *reinterpret_cast<Word *>(to + dst_at[r] + e1) = x1[k];
+            }
         }
     }
 }
@@ -612,11 +632,11 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
         load(e1, x[1]);
 #pragma unroll
         for (int w = 0; w < W; w++) {
-            const float4 c = turn_back(turns, u * W + w, m.shift);
+            const float2 c = turn_back(turns, u * W + w, m.shift);
             // the pair's places: its halves, or two neighbours of the 2 W elements
             const int i0 = p.interleaved ? 2 * w : w, i1 = p.interleaved ? 2 * w + 1 : W + w;
             const float a0 = x[i0 / W][i0 % W], a1 = x[i1 / W][i1 % W];
-            const float y0 = fmaf(a0, c.x, -a1 * c.z), y1 = fmaf(a1, c.x, a0 * c.z);
+            const float y0 = fmaf(a0, c.x, -a1 * c.y), y1 = fmaf(a1, c.x, a0 * c.y);
             row[(i0 < W ? e0 : e1) + i0 % W] = y0;
             row[(i1 < W ? e0 : e1) + i1 % W] = y1;
             amax = fmaxf(amax, fmaxf(fabsf(y0), fabsf(y1)));
@@ -707,7 +727,7 @@ cudaError_t launch_pages_compact(const CompactParams &p, bool e4m3, const RopeTu
     const int blocks = (p.max_keep + COMPACT_ROWS - 1) / COMPACT_ROWS;
     if ((long long)blocks * p.batch > INT_MAX)
         return cudaErrorInvalidConfiguration;
-    const size_t smem = (size_t)COMPACT_ROWS * (p.turn ? p.rd / 2 : 0) * sizeof(float4);  // 16 KB at most
+    const size_t smem = (size_t)COMPACT_ROWS * (p.turn ? p.rd / 2 : 0) * sizeof(float2);  // 8 KB at most
     return launch_kernel(unit ? pages_compact_kernel<1> : pages_compact_kernel<8>,
                          dim3((unsigned)(blocks * p.batch)), dim3(COMPACT_THREADS), smem, stream, p,
                          turns, blocks);
