@@ -35,7 +35,9 @@ struct ExpandedParams {
     int H, dn, rd, dv, batch;
     float scale_log2;
     int total_tokens, total_keys, max_new_len, max_key_len;
-    int q_tiles;
+    int tall;                  // units of 256 rows, else of 128
+    int units;                 // of all sequences, with the longest one's tiles each
+    int cut_units, pieces;     // tall: the last units, cut into pieces of their keys (a cluster each)
     const int32_t *cu_seqlens, *key_starts, *key_lens;
     const bf16 *q, *kv, *k_pe;
     long long k_pe_stride;     // elements
@@ -50,9 +52,12 @@ inline int latent_unit_rows(long long most_rows)
     return most_rows <= 32 ? 32 : (most_rows <= 64 ? 64 : 128);
 }
 constexpr int kLatentKeys = 64;  // keys of a tile
-constexpr int kExpandedRows = 128;  // query tokens of an expanded tile
+constexpr int kExpandedMaxPieces = 8;  // CTAs of a cluster
+constexpr int kExpandedRows = 128;  // query tokens of an expanded tile; a tall unit has two
 
 cudaError_t launch_latent_append(const LatentAppendParams &p, const PagedView &pg,
                                  const RopeTurns &turns, cudaStream_t stream);
 cudaError_t launch_latent(const LatentParams &p, const PagedView &pg, cudaStream_t stream);
+// Clusters of that many CTAs of the tall kernel that the device runs at a time.
+int latent_expanded_clusters(int ctas);
 cudaError_t launch_latent_expanded(const ExpandedParams &p, cudaStream_t stream);

@@ -9,6 +9,8 @@
 
 namespace {
 
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
 int check_cfg(const na_latent_cfg *c)
 {
     if (!c || c->num_heads <= 0)
@@ -56,7 +58,6 @@ struct LatentPlan {
 LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int max_total_len)
 {
     LatentPlan pl{};
-    const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
     const long long rows = (long long)max_new_len * c->num_heads;
     pl.unit_rows = latent_unit_rows(rows);
     const double tiles = (double)batch * ceil_div(rows, pl.unit_rows) * ceil_div(max_total_len, kLatentKeys);
@@ -67,6 +68,52 @@ LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int m
     pl.ws_bytes = (pl.part_o + (size_t)2 * pl.grid * pl.unit_rows * 2) * sizeof(float) +
                   pl.grid * sizeof(int4);
     return pl;
+}
+
+// Which kernel an expanded call takes, and what it cuts.  Tall units (256 rows, one CTA per SM) carry
+// more products per byte of shared memory, 128-row units on two CTAs per SM begin and end behind
+// one another; a tall unit may be cut into pieces of its keys, a cluster of up to 8 CTAs.
+//   - Fewer tall units than SMs: all are cut (128 tokens after 4096, 8 heads: 53.2 us on 128-row
+//     units, 57.2 on tall ones, 20.1 in eight pieces).  A piece costs its CTA ~8 us
+//     besides its keys, hence 256 of them at least.  Ragged batches only have bounds: a sequence
+//     counts for half a unit beside its tokens, and a few clusters that wait do no harm.
+//   - Batches of equal lengths: the units left over after the last whole wave of SMs, in a launch of
+//     their own, which from 4096 keys on gains more than it costs (2048 tokens after 16384, 40
+//     heads: 746 us uncut, 625; after 1024: 109 and 128).
+//   - Below 1024 keys a row on average the 128-row units are faster (1024 tokens of one prompt, 8
+//     heads: 16.3 us against 19.2; 16 prompts of 1 .. 512 tokens, 32 heads: 86 against
+//     107 in tiles of 128 keys), and so they are for sequences of few tokens, whose tall units are mostly empty (64 of
+//     1 .. 60 tokens after 1000 .. 2000: 366 against 452).
+int plan_expanded(ExpandedParams &p)
+{
+    const int sms = sm_count(), keys = std::min(p.max_key_len, p.total_keys);
+    const bool equal = (long long)p.batch * p.max_new_len == p.total_tokens;
+    const double per_tile = (double)p.H * p.batch;
+    const double tall_units = per_tile * ceil_div(p.max_new_len, 2 * kExpandedRows);
+    const double short_units = per_tile * ceil_div(p.max_new_len, kExpandedRows);
+    if (short_units > INT_MAX / 8)
+        return NA_ERR_UNSUPPORTED;
+    const double busy = equal ? tall_units
+                              : std::min(tall_units, p.H * (p.total_tokens / (2.0 * kExpandedRows) +
+                                                            p.batch / 2.0));
+    const double most = equal ? 1.0 : 1.15;
+    int pieces = kExpandedMaxPieces;
+    while (pieces > 1 && (busy > most * latent_expanded_clusters(pieces) || keys / pieces < 256))
+        pieces--;
+    int cut = pieces > 1 ? (int)tall_units : 0;
+    const int keys_per_row = (cut ? keys : std::min(keys, p.total_keys / p.batch)) - p.max_new_len / 2;
+    p.tall = keys_per_row >= 1024 && (cut || p.total_tokens >= 96ll * p.batch);
+    if (p.tall && !cut && equal && keys >= 4096) {
+        const int rest = (int)tall_units % sms;
+        pieces = rest ? kExpandedMaxPieces : 1;
+        while (pieces > 1 && rest > latent_expanded_clusters(pieces))
+            pieces--;
+        cut = pieces > 1 ? rest : 0;
+    }
+    p.units = (int)(p.tall ? tall_units : short_units);
+    p.pieces = pieces;
+    p.cut_units = cut;
+    return NA_OK;
 }
 
 }  // namespace
@@ -222,9 +269,6 @@ int na_attn_latent_expanded(const na_latent_cfg *cfg, int32_t batch, const int32
         return NA_ERR_UNSUPPORTED;
     max_new_len = std::min(max_new_len, total_tokens);
     ExpandedParams p{};
-    p.q_tiles = (max_new_len + kExpandedRows - 1) / kExpandedRows;
-    if ((double)p.q_tiles * cfg->num_heads * batch > INT_MAX)
-        return NA_ERR_UNSUPPORTED;
     p.H = cfg->num_heads;
     p.dn = cfg->nope_dim;
     p.rd = cfg->rope_dim;
@@ -244,6 +288,8 @@ int na_attn_latent_expanded(const na_latent_cfg *cfg, int32_t batch, const int32
     p.k_pe_stride = k_pe_stride;
     p.out = static_cast<bf16 *>(out);
     p.status = status;
+    if ((rc = plan_expanded(p)) != NA_OK)
+        return rc;
     if ((rc = bind_context()) != NA_OK)
         return rc;
     return done(launch_latent_expanded(p, static_cast<cudaStream_t>(stream)));

@@ -337,11 +337,6 @@ __device__ __forceinline__ bool softmax_any(bool x)
     return any != 0;
 }
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // CL: CTAs of a unit, QR rows each.
 template <int R, int QR, int CL>
 __global__ void __launch_bounds__(THREADS, 1)

@@ -6,6 +6,7 @@
 
 #include "pages.cuh"
 #include "rope_math.cuh"
+#include "tile_waits.cuh"
 
 namespace {
 
@@ -51,11 +52,6 @@ __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total)
     }
     total = all;
     return before + x - v;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // x into the word at `at`'s place in CTA `rank` of the cluster.

@@ -57,3 +57,40 @@ __device__ __forceinline__ bool elect_one()
         : "=r"(one));
     return one != 0;
 }
+
+// All threads of all CTAs of the cluster; what was written before is seen after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One arrival on the barrier at `bar`'s offset in CTA `rank` of the cluster; a thread there that
+// waits with mbar_wait_cluster sees what was written before.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t *bar, int rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(bar)), "r"(rank));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    const long long start = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; i++) {
+            uint32_t done;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(smem_addr(bar)), "r"(parity)
+                : "memory");
+            if (done)
+                return true;
+        }
+        if (clock64() - start > NA_WAIT_LIMIT_CYCLES)
+            return false;
+    }
+}

@@ -280,6 +280,43 @@ def test_expanded_shared_keys_and_long_context():
     check_expanded(2, 128, 64, 128, [257], [4000])
 
 
+@pytest.mark.parametrize("dn,dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+@pytest.mark.parametrize("rd,new,lens", [
+    (64, [300], [1437]),                # two units of 256 rows, the last of less than a tile
+    (32, [2900], [2600]),               # whole tiles see nothing
+    (64, [512, 640, 1, 0, 900], [512, 2000, 1, 40, 1300]),
+])
+def test_expanded_cut_into_pieces(dn, dv, rd, new, lens):
+    """Few units with many keys: clusters, some of whose CTAs have no keys."""
+    check_expanded(2, dn, rd, dv, new, lens, seed=dn + dv)
+
+
+def test_expanded_tall_units():
+    """More units of 256 rows than SMs."""
+    check_expanded(80, 64, 64, 64, [200, 270], [1100, 1300])
+
+
+def test_expanded_last_wave_cut():
+    """160 equal units of 4100 keys and more: those after the last whole wave are cut."""
+    import causal_gqa_attention_rope_gb300 as na
+    H, n, m = 160, 150, 4170
+    cfg = na.LatentConfig(H, rope_dim=64, nope_dim=64, v_dim=128)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    q, kv, pe = (torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)
+                 for s in ((n, H, 128), (m, H, 192), (m, 64)))
+    out, status = torch.full((n, H, 128), 3.0, dtype=torch.bfloat16, device=DEV), ints([0])
+    na.na_attn_latent_expanded(cfg, ints([0, n]), ints([0]), ints([m]), n, m, q, kv, pe, out, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    heads = [0, 1, 80] + list(range(148, 160))
+    q, kv, pe, got = (x.cpu() for x in (q[:, heads], kv[:, heads], pe, out[:, heads]))
+    k = torch.cat([kv[..., :64], pe[:, None].expand(-1, len(heads), -1)], dim=-1)
+    ref, tol = attend(q, k.transpose(0, 1), kv[..., 64:].transpose(0, 1),
+                      torch.arange(m - n + 1, m + 1), 1 / math.sqrt(128))
+    assert ((got.double() - ref).abs() <= tol).all()
+    assert not (out == 3.0).all(dim=-1).any()
+
+
 def test_expanded_reports():
     import causal_gqa_attention_rope_gb300 as na
     cfg = na.LatentConfig(2, rope_dim=32, nope_dim=64, v_dim=64)
