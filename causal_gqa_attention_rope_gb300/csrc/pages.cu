@@ -21,7 +21,8 @@ using namespace rope;
 // by atomics on integers, whose order does not show, and only for parents that have not
 // exactly one child (kids - 1 for a shared page, -1 for an ended sequence's).  Free pages
 // are then found in index order by a scan, page rank k going to the sequence whose range of
-// missing pages holds k.  Bound by latency: 256 sequences in 9000 pages took one CTA 26 us,
+// missing pages holds k, and a copy to the one that gets its sequence's first.  Bound by latency:
+// 256 sequences in 9000 pages take 8 us, one CTA took 26,
 // 17 of them for the rows.
 
 constexpr int FORK_CTAS = 8;
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     int *parents = lens + p.old_batch;   // [batch]
     int *start = parents + p.batch;      // [batch]  first missing entry
     int *offs = start + p.batch;         // [batch]  missing entries before sequence b
+    int *copied = offs + p.batch;        // [batch]  page whose copy is the first missing entry, or -1
     __shared__ int warp_sums[32], free_of[FORK_CTAS];
     grid_dependency_wait();
     grid_dependents_launch();
@@ -148,8 +150,12 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
         held = row >= 0 ? held : 0;
         const int mine = elder ? held : min(full, held);
         const long long pages = ((long long)n + max(grow, 0) + (1 << p.page_log) - 1) >> p.page_log;
+        // a part-filled page that is there is copied for all children but the first
+        const bool copies = row >= 0 && !elder && (n & ((1 << p.page_log) - 1)) && full < held;
+        const int copy = copies ? __ldg(p.table + (size_t)row * P + full) : -1;
         if (lane < FORK_CTAS) {
             store_in_cta(start + i, lane, mine);
+            store_in_cta(copied + i, lane, copy);
             store_in_cta(offs + i, lane, max((int)min(pages, (long long)P) - mine, 0));
         }
         if (lane == 0) {
@@ -160,8 +166,8 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
             if (pages > P)
                 na_report(p.status, NA_ERR_CAPACITY);
             p.new_lens[i] = n;
-            // a part-filled page that is there is copied for all children but the first
-            p.copy_src[i] = row >= 0 && !elder && (n & ((1 << p.page_log) - 1)) && full < held;
+            p.copy_src[i] = -1;  // until a page is found
+            p.copy_dst[i] = -1;
         }
     }
     cluster_sync();
@@ -228,23 +234,15 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
                 lo++;
             p.new_table[(size_t)lo * P + start[lo] + (k - offs[lo])] = at + i;
             p.new_ref[at + i] = 1;
+            if (k == offs[lo] && copied[lo] >= 0) {
+                p.copy_src[lo] = copied[lo];
+                p.copy_dst[lo] = at + i;
+            }
             k++;
         }
     }
     if (all < missing && rank == 0 && tid == 0)
         na_report(p.status, NA_ERR_CAPACITY);
-    cluster_sync();
-
-    for (int b = rank * FORK_THREADS + tid; b < p.batch; b += FORK_CTAS * FORK_THREADS) {
-        int src = -1, dst = -1;
-        if (__ldcg(p.copy_src + b)) {
-            const int j = lens[parents[b]] >> p.page_log;
-            dst = __ldcg(p.new_table + (size_t)b * P + j);
-            src = dst >= 0 ? __ldg(p.table + (size_t)parents[b] * P + j) : -1;
-        }
-        p.copy_src[b] = src;
-        p.copy_dst[b] = dst;
-    }
 }
 
 // ------------------------------------------------------------------- copy --
@@ -671,11 +669,11 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
 
 cudaError_t launch_pages_fork(const ForkParams &p, cudaStream_t stream)
 {
-    const size_t smem = 3 * ((size_t)p.old_batch + p.batch) * sizeof(int);
+    const size_t smem = (3 * (size_t)p.old_batch + 4 * (size_t)p.batch) * sizeof(int);
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = once_per_device(configured, [] {
         return cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    6 * kMaxForkBatch * (int)sizeof(int));
+                                    7 * kMaxForkBatch * (int)sizeof(int));
     });
     if (e != cudaSuccess)
         return e;
