@@ -22,6 +22,8 @@ struct LatentParams {
     int unit_rows;             // 32, 64 or 128
     int grid;                  // CTAs (pairs of them for 128 rows), each with an equal run of key tiles
     int cut_by_sequence;       // one unit a sequence: cut[b], else by run
+    int pieces;                // > 0: no runs; `grid` units (of all sequences, with the longest
+                               // one's each), a cluster of that many CTAs each, 32 or 64 rows
     const int32_t *cu_seqlens, *cache_lens;
     const bf16 *q, *cache;
     bf16 *out;
@@ -52,12 +54,13 @@ inline int latent_unit_rows(long long most_rows)
     return most_rows <= 32 ? 32 : (most_rows <= 64 ? 64 : 128);
 }
 constexpr int kLatentKeys = 64;  // keys of a tile
+constexpr int kLatentMaxPieces = 8;  // CTAs of a cluster
 constexpr int kExpandedMaxPieces = 8;  // CTAs of a cluster
 constexpr int kExpandedRows = 128;  // query tokens of an expanded tile; a tall unit has two
 
 cudaError_t launch_latent_append(const LatentAppendParams &p, const PagedView &pg,
                                  const RopeTurns &turns, cudaStream_t stream);
 cudaError_t launch_latent(const LatentParams &p, const PagedView &pg, cudaStream_t stream);
-// Clusters of that many CTAs of the tall kernel that the device runs at a time.
-int latent_expanded_clusters(int ctas);
+// Clusters of that many CTAs, one per SM, that the device runs at a time.
+int sm_clusters(int ctas);
 cudaError_t launch_latent_expanded(const ExpandedParams &p, cudaStream_t stream);

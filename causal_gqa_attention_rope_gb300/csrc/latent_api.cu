@@ -7,6 +7,7 @@
 #include "latent.cuh"
 #include "na_host.cuh"
 
+
 namespace {
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -51,10 +52,16 @@ int done(cudaError_t e) { return e == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
 struct LatentPlan {
     int grid, unit_rows;
     bool cut_by_sequence;
+    int joined_grid, pieces;  // pieces > 0: units of their own clusters instead of runs
     size_t part_o, ws_bytes;
 };
 
-// One CTA or pair of CTAs per SM or two, fewer where the bounds allow no more tiles than that.
+// Runs: one CTA or pair of CTAs per SM, fewer where the bounds allow no more tiles than that, and
+// a second pass.  Units joined in their own clusters need neither the search for a run's
+// beginning nor the pass, which is 2.5 to 3 us less, worth some 3 tiles of 512 latent
+// numbers or 5 of fewer; but a cluster has 8 CTAs at most and none helps another (4
+// heads, 333 keys of 128: 9.9 us by runs, 6.7; 16 heads, 512 numbers, 1000 keys: 13.9 and 12.2,
+// 4000 keys: 15.6 and 20.7).  The lengths are bounds: batches are taken for 0.6 of them.
 LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int max_total_len)
 {
     LatentPlan pl{};
@@ -67,6 +74,17 @@ LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int m
     pl.part_o = (size_t)2 * pl.grid * pl.unit_rows * c->kv_rank;
     pl.ws_bytes = (pl.part_o + (size_t)2 * pl.grid * pl.unit_rows * 2) * sizeof(float) +
                   pl.grid * sizeof(int4);
+    const int joined_rows = rows <= 32 ? 32 : 64;
+    const double units = (double)batch * ceil_div(rows, joined_rows);
+    const int longest = (int)ceil_div(max_total_len, kLatentKeys);
+    int pieces = std::min(kLatentMaxPieces, longest);
+    while (pieces > 1 && units > sm_clusters(pieces))
+        pieces--;
+    const double by_runs = tiles * (batch > 1 ? 0.6 : 1.0) / most + (c->kv_rank == 512 ? 3 : 5);
+    if (pieces > 0 && units <= sm_count() && ceil_div(longest, pieces) <= by_runs) {
+        pl.pieces = pieces;
+        pl.joined_grid = (int)units;
+    }
     return pl;
 }
 
@@ -98,7 +116,7 @@ int plan_expanded(ExpandedParams &p)
                                                             p.batch / 2.0));
     const double most = equal ? 1.0 : 1.15;
     int pieces = kExpandedMaxPieces;
-    while (pieces > 1 && (busy > most * latent_expanded_clusters(pieces) || keys / pieces < 256))
+    while (pieces > 1 && (busy > most * sm_clusters(pieces) || keys / pieces < 256))
         pieces--;
     int cut = pieces > 1 ? (int)tall_units : 0;
     const int keys_per_row = (cut ? keys : std::min(keys, p.total_keys / p.batch)) - p.max_new_len / 2;
@@ -106,7 +124,7 @@ int plan_expanded(ExpandedParams &p)
     if (p.tall && !cut && equal && keys >= 4096) {
         const int rest = (int)tall_units % sms;
         pieces = rest ? kExpandedMaxPieces : 1;
-        while (pieces > 1 && rest > latent_expanded_clusters(pieces))
+        while (pieces > 1 && rest > sm_clusters(pieces))
             pieces--;
         cut = pieces > 1 ? rest : 0;
     }
@@ -228,8 +246,9 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     p.total_tokens = total_tokens;
     p.max_new_len = max_new_len;
     p.max_total_len = max_total_len;
-    p.unit_rows = pl.unit_rows;
-    p.grid = pl.grid;
+    p.unit_rows = pl.pieces ? std::min(pl.unit_rows, 64) : pl.unit_rows;
+    p.grid = pl.pieces ? pl.joined_grid : pl.grid;
+    p.pieces = pl.pieces;
     p.cut_by_sequence = pl.cut_by_sequence;
     p.cu_seqlens = cu_seqlens;
     p.cache_lens = cache_lens;

@@ -69,6 +69,7 @@ struct __align__(1024) LatentSmem {
     float inv[MAX_ROWS];       // at a piece's end: 1 / sum, or 1
     uint64_t q_full, q_empty, pair_full[PAIRS], pair_empty[PAIRS], rope_full[ROPES],
         rope_empty[ROPES], s_full[2], s_empty[2], p_full, pv_done, o_empty, drain[2];
+    float2 ml[MAX_ROWS];       // at a joined piece's end: the rows' (max, sum)
     long long warp_steps[THREADS / 32];
     long long total, begin;
     int b0, t0, step0;         // where the CTA's run begins
@@ -263,6 +264,25 @@ struct Walk {
     {
     }
 
+    // Piece `piece` of p.pieces of a unit of its own (none where the sequence has fewer units).
+    __device__ __forceinline__ Walk(const LatentParams &p, int index, int piece) : left(0), have(false)
+    {
+        const int units = (p.max_new_len * p.H + UR - 1) / UR;  // of the longest sequence
+        b = index / units;
+        t = index % units;
+        int code;
+        s = sequence_of(p, b, code);
+        if (code != NA_OK && t == 0 && piece == 0 && threadIdx.x == 0)
+            na_report(p.status, code);
+        if (t >= units_of<UR>(p, s))
+            return;
+        const int all = (keys_of<UR>(p, s, t) + KT - 1) / KT;
+        const int from = (int)((long long)all * piece / p.pieces);
+        step = from + UNIT_STEPS;
+        left = (int)((long long)all * (piece + 1) / p.pieces) - from;
+        have = true;
+    }
+
     __device__ __forceinline__ bool next(const LatentParams &p)
     {
         if (left <= 0)
@@ -337,8 +357,115 @@ __device__ __forceinline__ bool softmax_any(bool x)
     return any != 0;
 }
 
-// CL: CTAs of a unit, QR rows each.
-template <int R, int QR, int CL>
+// `at`'s place in CTA `rank` of the cluster, and what is there.
+__device__ __forceinline__ uint32_t place_in_cta(const void *at, int rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(at)), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ float4 load_cluster_4(const void *at, int rank)
+{
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(place_in_cta(at, rank))
+                 : "memory");
+    return x;
+}
+
+__device__ __forceinline__ float2 load_cluster_2(const void *at, int rank)
+{
+    float2 x;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(x.x), "=f"(x.y)
+                 : "r"(place_in_cta(at, rank))
+                 : "memory");
+    return x;
+}
+
+// The rows of a unit whose pieces P CTAs of a cluster hold, each unnormalised in `stage` (rows of
+// R + 4) with their maxima and sums in `ml`: CTA `piece` joins every P-th row.  Other CTAs'
+// shared memory gives some 14 bytes a cycle (64 rows of 512 in pieces: 4 us), so that
+// nothing is asked for twice, and the own piece not through the cluster; P is known to the compiler,
+// because loads behind a branch were waited for one by one.
+template <int R, int P>
+__device__ __forceinline__ void join_rows_of(const LatentParams &p, const float *stage, const float2 *ml,
+                                             float (*weight)[MAX_ROWS], int piece, int rows, long long row0)
+{
+    constexpr int AT_ONCE = THREADS / (R / 4);
+    if (threadIdx.x < rows) {
+        float2 of[P];
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int c = 0; c < P; c++)
+            of[c] = load_cluster_2(ml + threadIdx.x, c);
+#pragma unroll
+        for (int c = 0; c < P; c++)
+            m = fmaxf(m, of[c].x);
+#pragma unroll
+        for (int c = 0; c < P; c++) {
+            of[c].x = of[c].x == -INFINITY ? 0.f : exp2f(of[c].x - m);
+            l = fmaf(of[c].x, of[c].y, l);
+        }
+        const float inv = l > 0.f ? 1.0f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < P; c++)
+            weight[c][threadIdx.x] = of[c].x * inv;
+    }
+    __syncthreads();
+    // (a few rows at a time where a row has few pieces; the last stands for those behind it)
+    constexpr int ROWS = P == 1 ? 4 : (P <= 3 ? 2 : 1), STEP = P * AT_ONCE;
+    const int x = threadIdx.x % (R / 4) * 4;
+    for (int r0 = piece + P * (threadIdx.x / (R / 4)); r0 < rows; r0 += ROWS * STEP) {
+        float4 v[ROWS][P];
+#pragma unroll
+        for (int i = 0; i < ROWS; i++) {
+            const float *row = stage + min(r0 + i * STEP, rows - 1) * (R + 4) + x;
+            v[i][0] = *reinterpret_cast<const float4 *>(row);
+#pragma unroll
+            for (int k = 1; k < P; k++)
+                v[i][k] = load_cluster_4(row, piece + k < P ? piece + k : piece + k - P);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; i++) {
+            const int r = r0 + i * STEP;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < P; k++) {
+                const float w = weight[piece + k < P ? piece + k : piece + k - P][min(r, rows - 1)];
+                if (w != 0.f)  // (a piece without keys holds whatever was there)
+                    o = make_float4(fmaf(w, v[i][k].x, o.x), fmaf(w, v[i][k].y, o.y),
+                                    fmaf(w, v[i][k].z, o.z), fmaf(w, v[i][k].w, o.w));
+            }
+            if (r < rows)
+                *reinterpret_cast<uint2 *>(p.out + (row0 + r) * R + x) =
+                    make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        }
+    }
+}
+
+template <int R>
+__device__ __forceinline__ void join_rows(const LatentParams &p, const float *stage, const float2 *ml,
+                                          float (*weight)[MAX_ROWS], int piece, int rows, long long row0)
+{
+    static_assert(kLatentMaxPieces == 8, "cases");
+    switch (p.pieces) {
+    case 1: return join_rows_of<R, 1>(p, stage, ml, weight, piece, rows, row0);
+    case 2: return join_rows_of<R, 2>(p, stage, ml, weight, piece, rows, row0);
+    case 3: return join_rows_of<R, 3>(p, stage, ml, weight, piece, rows, row0);
+    case 4: return join_rows_of<R, 4>(p, stage, ml, weight, piece, rows, row0);
+    case 5: return join_rows_of<R, 5>(p, stage, ml, weight, piece, rows, row0);
+    case 6: return join_rows_of<R, 6>(p, stage, ml, weight, piece, rows, row0);
+    case 7: return join_rows_of<R, 7>(p, stage, ml, weight, piece, rows, row0);
+    default: return join_rows_of<R, 8>(p, stage, ml, weight, piece, rows, row0);
+    }
+}
+
+// CL: CTAs of a unit, QR rows each.  JOINED: a cluster of p.pieces CTAs per unit, a piece of its keys
+// each, instead of runs.
+template <int R, int QR, int CL, bool JOINED>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ PagedView pg,
                        const __grid_constant__ CUtensorMap map_q,
@@ -351,7 +478,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
     constexpr int UR = QR * CL;
     constexpr uint16_t EVERY = (1 << CL) - 1;
-    const int run = blockIdx.x / CL, rank = CL > 1 ? blockIdx.x % CL : 0;
+    static_assert(!JOINED || CL == 1, "a cluster shares tiles or joins pieces");
+    const int group = JOINED ? p.pieces : CL;
+    const int run = blockIdx.x / group, rank = CL > 1 ? blockIdx.x % CL : 0;
+    const int piece = JOINED ? blockIdx.x % group : 0;
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~uintptr_t(1023));
@@ -385,12 +515,31 @@ __global__ void __launch_bounds__(THREADS, 1)
     grid_dependency_wait();
     grid_dependents_launch();
     tc::fence_before_sync();
-    find_run<UR>(p, sm, run, warp, lane);
+    if constexpr (JOINED)
+        __syncthreads();
+    else
+        find_run<UR>(p, sm, run, warp, lane);
     if constexpr (CL > 1)
         cluster_sync();  // the other CTA's barriers are there
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
-    Walk<UR> w(p, sm, run);
+    auto begin_walk = [&] {
+        if constexpr (JOINED)
+            return Walk<UR>(p, run, piece);
+        else
+            return Walk<UR>(p, sm, run);
+    };
+    Walk<UR> w = begin_walk();
+    int join_count = 0;          // rows of the unit, for all threads
+    long long join_row0 = 0;
+    if constexpr (JOINED) {
+        if (w.have) {
+            join_row0 = (long long)w.s.tok0 * p.H + (long long)w.t * UR;
+            join_count = min(UR, w.s.n * p.H - w.t * UR);
+        }
+    }
+    float *stage = reinterpret_cast<float *>(&sm.pair[0]);  // idle when a piece's rows are done
+    static_assert(!JOINED || sizeof(float) * QR * (R + 4) <= sizeof(sm.pair) + sizeof(sm.rope), "staged rows");
     auto commit_all = [](uint64_t *bar) {  // in both CTAs of a pair
         if constexpr (CL > 1)
             tc::mma_commit_multicast(bar, EVERY);
@@ -594,8 +743,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Where a unit that begins here is told to the second pass: by sequence where each has one
         // unit, else by run.
         const bool leader = tid == 0 && rank == 0;
-        if (leader && !p.cut_by_sequence)
+        if (!JOINED && leader && !p.cut_by_sequence)
             p.cut[run] = make_int4(0, 0, 0, -1);
+        if (JOINED && tid < MAX_ROWS)
+            sm.ml[tid] = make_float2(-INFINITY, 0.f);  // until there are keys
         while (ok && w.next(p)) {
             const int rows = w.rows(p, rank * QR, QR);
             int lim[2];  // keys that the rows see
@@ -723,7 +874,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // ------------------------------------------------------- a piece's rows --
             ok = ok && warp_wait(&sm.pv_done, (g - 1) & 1, &sm.abort_flag);
-            const bool whole = w.lo == 0 && w.hi == w.tiles;
+            const bool whole = !JOINED && w.lo == 0 && w.hi == w.tiles;
             const size_t slot_row = (size_t)(2 * run + (w.lo == 0 ? 1 : 0)) * UR + rank * QR;
 #pragma unroll
             for (int h = 0; h < 2; h++) {
@@ -731,7 +882,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
                 if ((lane & 3) == 0) {
                     sm.inv[ra + 8 * h] = whole ? (sum[h] > 0.f ? 1.0f / sum[h] : 0.f) : 1.f;
-                    if (!whole && ok && ra + 8 * h < rows)
+                    if (JOINED && ra + 8 * h < rows)
+                        sm.ml[ra + 8 * h] = make_float2(m_ref[h], sum[h]);
+                    else if (!whole && ok && ra + 8 * h < rows)
                         reinterpret_cast<float2 *>(p.part_ml)[slot_row + ra + 8 * h] =
                             make_float2(m_ref[h], sum[h]);
                 }
@@ -750,7 +903,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t o[32];
                 tc::tmem_ld32(tmem + lane_off + c, o);
                 tc::tmem_wait_ld();
-                if (whole) {
+                if constexpr (JOINED) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        if (r0 + i < rows)
+                            stage[(r0 + i) * (R + 4) + dim] = __uint_as_float(o[i]);
+                } else if (whole) {
                     bf16 *dst = p.out + (row0 + r0) * R + dim;
 #pragma unroll
                     for (int i = 0; i < 32; i++)
@@ -768,7 +926,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm.o_empty);
-            if (w.lo == 0 && leader) {
+            if (!JOINED && w.lo == 0 && leader) {
                 // the unit ends (tiles - hi) behind the end of this run
                 const long long end = run_begin(p, sm.total, run + 1) + (w.tiles - w.hi);
                 if (!whole || p.cut_by_sequence)
@@ -784,6 +942,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 1) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, TMEM_COLS);
+    }
+    if constexpr (JOINED) {  // (a CTA whose waits gave up has reported it: what there is gets joined)
+        if (p.pieces > 1)
+            cluster_sync();
+        // (the weights lie over P, which is done with)
+        static_assert(sizeof(float) * kLatentMaxPieces * MAX_ROWS <= sizeof(sm.p), "weights");
+        join_rows<R>(p, stage, sm.ml, reinterpret_cast<float(*)[MAX_ROWS]>(sm.p), piece, join_count,
+                     join_row0);
+        if (p.pieces > 1)
+            cluster_sync();  // until then the others read this one's rows
     }
     if constexpr (CL > 1)
         cluster_sync();  // the other CTA copies and arrives into this one's shared memory
@@ -885,7 +1053,7 @@ __global__ void __launch_bounds__(R / 4 * MERGE_THREADS_PER_DIM)
     reinterpret_cast<uint2 *>(p.out + ((size_t)cut.x + r) * R)[x] = u;
 }
 
-template <int R, int QR, int CL>
+template <int R, int QR, int CL, bool JOINED>
 cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
     CUtensorMap mq, mkv;
@@ -902,14 +1070,15 @@ cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStre
     static_assert(smem > (116u << 10) && smem <= 232448, "shared memory of one CTA per SM");
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = once_per_device(configured, [] {
-        return cudaFuncSetAttribute(latent_attn_kernel<R, QR, CL>,
+        return cudaFuncSetAttribute(latent_attn_kernel<R, QR, CL, JOINED>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess)
         return e;
-    e = launch_kernel_cluster(latent_attn_kernel<R, QR, CL>, dim3(p.grid * CL), dim3(THREADS), smem,
-                              CL > 1 ? CL : 0, stream, p, pg, mq, mkv);
-    if (e != cudaSuccess || p.grid == 1)
+    const int cluster = JOINED ? p.pieces : CL;
+    e = launch_kernel_cluster(latent_attn_kernel<R, QR, CL, JOINED>, dim3(p.grid * cluster), dim3(THREADS),
+                              smem, cluster > 1 ? cluster : 0, stream, p, pg, mq, mkv);
+    if (JOINED || e != cudaSuccess || p.grid == 1)
         return e;
     constexpr int UR = QR * CL;
     const int rows = (int)std::min((long long)p.max_new_len * p.H, (long long)UR);
@@ -927,10 +1096,13 @@ cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStre
 template <int R>
 cudaError_t launch_latent_rows(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
+    if (p.pieces > 0)
+        return p.unit_rows == 32 ? launch_latent_t<R, 32, 1, true>(p, pg, stream)
+                                 : launch_latent_t<R, 64, 1, true>(p, pg, stream);
     switch (p.unit_rows) {
-    case 32: return launch_latent_t<R, 32, 1>(p, pg, stream);
-    case 64: return launch_latent_t<R, 64, 1>(p, pg, stream);
-    default: return launch_latent_t<R, 64, 2>(p, pg, stream);
+    case 32: return launch_latent_t<R, 32, 1, false>(p, pg, stream);
+    case 64: return launch_latent_t<R, 64, 1, false>(p, pg, stream);
+    default: return launch_latent_t<R, 64, 2, false>(p, pg, stream);
     }
 }
 

@@ -558,44 +558,68 @@ __device__ __forceinline__ int load_cluster_word(uint32_t a)
     return x;
 }
 
-// A unit's rows from the pieces of its keys, a CTA of the cluster each: those of 1 / pieces of the
-// warps here, staged unnormalised with their maxima and sums by every CTA.
+// A unit's rows from the P pieces of its keys, a CTA of the cluster each: those of 1 / P of the
+// warps here, staged unnormalised with their maxima and sums by every CTA.  Other CTAs' shared
+// memory gives some 14 bytes a cycle (5 us for a unit), so that nothing is asked for
+// twice, and the own piece not through the cluster; P is known to the compiler, because loads
+// behind a branch were waited for one by one.
+template <int DV, int P>
+__device__ __forceinline__ void join_rows_of(const ExpandedParams &p, const Unit &u, const float *stage,
+                                             const int *abort_flag, int piece, int warp, int lane)
+{
+    int bad = 0;
+#pragma unroll
+    for (int c = 0; c < P; c++)
+        bad |= load_cluster_word(place_in_cta(abort_flag, c));
+    if (bad)
+        return;
+    bf16 *out = rows_out<DV>(p, u);
+    const int x = min(lane * 4, DV - 4);
+    for (int r = piece + P * warp; r < u.rows; r += P * (tall::THREADS / 32)) {
+        const float *row = stage + r * (DV + 4);
+        // lane k has the maximum and sum of the k-th piece from this one on
+        const int at = piece + min(lane, P - 1);
+        const float4 ml = load_cluster(place_in_cta(row + DV, at < P ? at : at - P));
+        float4 v[P];
+        v[0] = *reinterpret_cast<const float4 *>(row + x);
+#pragma unroll
+        for (int k = 1; k < P; k++)
+            v[k] = load_cluster(place_in_cta(row + x, piece + k < P ? piece + k : piece + k - P));
+        float m = ml.x;
+#pragma unroll
+        for (int k = 1; k < kExpandedMaxPieces; k *= 2)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        m = __shfl_sync(0xffffffffu, m, 0);
+        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < P; k++) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            l = fmaf(wk, __shfl_sync(0xffffffffu, ml.y, k), l);
+            o = make_float4(fmaf(wk, v[k].x, o.x), fmaf(wk, v[k].y, o.y), fmaf(wk, v[k].z, o.z),
+                            fmaf(wk, v[k].w, o.w));
+        }
+        const float inv = l > 0.f ? 1.0f / l : 0.f;
+        if (lane * 4 < DV)
+            *reinterpret_cast<uint2 *>(out + (size_t)r * p.H * DV + x) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+}
+
 template <int DV>
 __device__ __forceinline__ void join_rows(const ExpandedParams &p, const Unit &u, const float *stage,
                                           const int *abort_flag, int piece, int pieces, int warp, int lane)
 {
-    for (int c = 0; c < pieces; c++)
-        if (load_cluster_word(place_in_cta(abort_flag, c)) != 0)
-            return;
-    bf16 *out = rows_out<DV>(p, u);
-    const int warps = blockDim.x / 32;
-    for (int r = piece * warps + warp; r < u.rows; r += pieces * warps) {
-        float2 ml[kExpandedMaxPieces];
-        float m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int c = 0; c < kExpandedMaxPieces; c++) {
-            if (c < pieces) {
-                const float4 x = load_cluster(place_in_cta(stage + r * (DV + 4) + DV, c));
-                ml[c] = make_float2(x.x, x.y);
-                m = fmaxf(m, x.x);
-            }
-        }
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < kExpandedMaxPieces; c++) {
-            if (c < pieces) {
-                const float w = ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - m);
-                l = fmaf(w, ml[c].y, l);
-                if (lane * 4 < DV) {
-                    const float4 x = load_cluster(place_in_cta(stage + r * (DV + 4) + lane * 4, c));
-                    o = make_float4(fmaf(w, x.x, o.x), fmaf(w, x.y, o.y), fmaf(w, x.z, o.z), fmaf(w, x.w, o.w));
-                }
-            }
-        }
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
-        if (lane * 4 < DV)
-            *reinterpret_cast<uint2 *>(out + (size_t)r * p.H * DV + lane * 4) =
-                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    static_assert(kExpandedMaxPieces == 8, "cases, and lanes with a piece");
+    switch (pieces) {
+    case 2: return join_rows_of<DV, 2>(p, u, stage, abort_flag, piece, warp, lane);
+    case 3: return join_rows_of<DV, 3>(p, u, stage, abort_flag, piece, warp, lane);
+    case 4: return join_rows_of<DV, 4>(p, u, stage, abort_flag, piece, warp, lane);
+    case 5: return join_rows_of<DV, 5>(p, u, stage, abort_flag, piece, warp, lane);
+    case 6: return join_rows_of<DV, 6>(p, u, stage, abort_flag, piece, warp, lane);
+    case 7: return join_rows_of<DV, 7>(p, u, stage, abort_flag, piece, warp, lane);
+    default: return join_rows_of<DV, 8>(p, u, stage, abort_flag, piece, warp, lane);
     }
 }
 
@@ -912,9 +936,9 @@ cudaError_t launch_tall_t(const ExpandedParams &p, cudaStream_t stream)
 
 }  // namespace
 
-int latent_expanded_clusters(int ctas)
+int sm_clusters(int ctas)
 {
-    // (all instances have one CTA per SM: one stands for them)
+    // (any kernel with one CTA per SM will do)
     static std::atomic<int> cached[kMaxDevices][kExpandedMaxPieces + 1];
     const int dev = current_device_index();
     int n = dev >= 0 ? cached[dev][ctas].load(std::memory_order_relaxed) : 0;
