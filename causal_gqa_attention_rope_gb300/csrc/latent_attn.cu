@@ -529,6 +529,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         else
             return Walk<UR>(p, sm, run);
     };
+    // The sequence's first pages, asked for beside its lengths.
+    int early = -1;
+    if constexpr (JOINED) {
+        const int b = run / ((p.max_new_len * p.H + UR - 1) / UR);
+        if (warp == 0 && lane < pg.pages_per_seq)
+            early = __ldg(pg.table + (size_t)b * pg.pages_per_seq + lane);
+    }
     Walk<UR> w = begin_walk();
     int join_count = 0;          // rows of the unit, for all threads
     long long join_row0 = 0;
@@ -567,10 +574,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int32_t *row = pg.table + (size_t)w.seq * pg.pages_per_seq;
             // this lane's page of a tile (boxes of them), or -1
             auto page_of = [&](int j) {
-                const int at = j * KT + (lane << box_log);
+                const int at = j * KT + (lane << box_log), entry = at >> pg.page_log;
+                int id = JOINED ? __shfl_sync(0xffffffffu, early, entry & 31) : 0;
                 if (lane >= boxes || j >= w.hi || at >= w.keys)
                     return -1;
-                int id = __ldg(row + (at >> pg.page_log));
+                if (!JOINED || entry >= 32)
+                    id = __ldg(row + entry);
                 if ((unsigned)id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
                     na_report(p.status, NA_ERR_PAGE);
                     id = 0;
@@ -939,10 +948,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
-        tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, TMEM_COLS);
-    }
     if constexpr (JOINED) {  // (a CTA whose waits gave up has reported it: what there is gets joined)
         if (p.pieces > 1)
             cluster_sync();
@@ -952,6 +957,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                      join_row0);
         if (p.pieces > 1)
             cluster_sync();  // until then the others read this one's rows
+    }
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, TMEM_COLS);
     }
     if constexpr (CL > 1)
         cluster_sync();  // the other CTA copies and arrives into this one's shared memory

@@ -29,30 +29,45 @@ constexpr int FORK_CTAS = 8;
 constexpr int FORK_THREADS = 1024;
 constexpr int FORK_PAGES = 2;  // pages per thread and round of the scan
 
-// Exclusive prefix sum of one value per thread over the CTA; `total` gets the sum.
-__device__ __forceinline__ int block_prefix(int v, int *warp_sums, int &total)
+// Exclusive prefix sums of N values per thread over the CTA; `total` gets the sums.
+template <int N>
+__device__ __forceinline__ void block_prefix(int (&v)[N], int (*warp_sums)[FORK_THREADS / 32], int (&total)[N])
 {
+    static_assert(FORK_THREADS == 1024, "a lane per warp");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    int x[N], before[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o)
-            x += y;
-    }
+    for (int n = 0; n < N; n++)
+        x[n] = v[n];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const int y = __shfl_up_sync(0xffffffffu, x[n], o);
+            if (lane >= o)
+                x[n] += y;
+        }
     __syncthreads();  // the sums of an earlier call have been read
     if (lane == 31)
-        warp_sums[warp] = x;
-    __syncthreads();
-    const int w = lane < FORK_THREADS / 32 ? warp_sums[lane] : 0;
-    int before = lane < warp ? w : 0, all = w;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
+        for (int n = 0; n < N; n++)
+            warp_sums[n][warp] = x[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        total[n] = warp_sums[n][lane];
+        before[n] = lane < warp ? total[n] : 0;
     }
-    total = all;
-    return before + x - v;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            before[n] += __shfl_xor_sync(0xffffffffu, before[n], o);
+            total[n] += __shfl_xor_sync(0xffffffffu, total[n], o);
+        }
+#pragma unroll
+    for (int n = 0; n < N; n++)
+        v[n] = before[n] + x[n] - v[n];
 }
 
 // x into the word at `at`'s place in CTA `rank` of the cluster.
@@ -73,27 +88,32 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     int *start = parents + p.batch;      // [batch]  first missing entry
     int *offs = start + p.batch;         // [batch]  missing entries before sequence b
     int *copied = offs + p.batch;        // [batch]  page whose copy is the first missing entry, or -1
-    __shared__ int warp_sums[32], free_of[FORK_CTAS];
+    __shared__ int warp_sums[2][FORK_THREADS / 32], free_of[FORK_CTAS];
     grid_dependency_wait();
     grid_dependents_launch();
     const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.pages_per_seq;
 
+    // (what the first round needs is asked for together)
+    const int page0 = rank * FORK_THREADS + tid;
+    const int len0 = tid < p.old_batch ? __ldg(p.lens + tid) : 0;
+    const int parent0 = tid < p.batch ? __ldg(p.parents + tid) : 0;
+    const int ref0 = page0 < p.num_pages ? __ldg(p.ref + page0) : 0;
     for (int i = tid; i < p.old_batch; i += FORK_THREADS) {
         kids[i] = 0;
         first[i] = INT_MAX;
-        lens[i] = max(__ldg(p.lens + i), 0);
+        lens[i] = max(i == tid ? len0 : __ldg(p.lens + i), 0);
     }
     for (int b = tid; b < p.batch; b += FORK_THREADS) {
-        int par = __ldg(p.parents + b);
+        int par = b == tid ? parent0 : __ldg(p.parents + b);
         if (par >= p.old_batch) {
             na_report(p.status, NA_ERR_INVALID_ARG);
             par = -1;
         }
         parents[b] = max(par, -1);
     }
-    for (int i = rank * FORK_THREADS + tid; i < p.num_pages; i += FORK_CTAS * FORK_THREADS)
-        p.new_ref[i] = __ldg(p.ref + i);
+    for (int i = page0; i < p.num_pages; i += FORK_CTAS * FORK_THREADS)
+        p.new_ref[i] = i == page0 ? ref0 : __ldg(p.ref + i);
     __syncthreads();
     for (int b = tid; b < p.batch; b += FORK_THREADS)
         if (parents[b] >= 0) {
@@ -114,19 +134,22 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
         // the row's counts change: once for each page, by the lowest child or without one
         const bool elder = row >= 0 && (!fresh || first[row] == i);
         const int shared = row >= 0 ? kids[row] - 1 : 0;
+        const int32_t *from = p.table + (size_t)max(row, 0) * P;
         int32_t *to = p.new_table + (size_t)i * P;
-        int held = P;
+        int held = P, part_filled = -1;  // entry `full`, in one of the lanes
         bool end = false;
         for (int base = 0; base < P; base += 128) {
             int e[4];
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 const int j = base + k * 32 + lane;
-                e[k] = row >= 0 && j < P && !end ? __ldg(p.table + (size_t)row * P + j) : -1;
+                e[k] = row >= 0 && j < P && !end ? __ldg(from + j) : -1;
             }
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 const int j0 = base + k * 32, j = j0 + lane;
+                if (j0 >= P)
+                    break;
                 const bool is_page = !end && (unsigned)e[k] < (unsigned)p.num_pages;
                 const unsigned bad = __ballot_sync(0xffffffffu, !is_page);
                 const int good = bad ? __ffs(bad) - 1 : 32;  // 0 behind the row's end
@@ -141,6 +164,8 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
                     atomicAdd(p.new_ref + e[k], delta);
                 if (fresh && j < P)
                     to[j] = lane < good && (elder || j < full) ? e[k] : -1;
+                if (j == full)
+                    part_filled = e[k];
             }
             if (end && !fresh)
                 break;
@@ -152,7 +177,8 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
         const long long pages = ((long long)n + max(grow, 0) + (1 << p.page_log) - 1) >> p.page_log;
         // a part-filled page that is there is copied for all children but the first
         const bool copies = row >= 0 && !elder && (n & ((1 << p.page_log) - 1)) && full < held;
-        const int copy = copies ? __ldg(p.table + (size_t)row * P + full) : -1;
+        const int page = __shfl_sync(0xffffffffu, part_filled, full & 31);
+        const int copy = copies ? page : -1;
         if (lane < FORK_CTAS) {
             store_in_cta(start + i, lane, mine);
             store_in_cta(copied + i, lane, copy);
@@ -172,18 +198,8 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     }
     cluster_sync();
 
-    // Missing pages before each sequence's, in every CTA.
-    int missing = 0;
-    for (int base = 0; base < p.batch; base += FORK_THREADS) {
-        const int b = base + tid;
-        int sum;
-        const int before = block_prefix(b < p.batch ? offs[b] : 0, warp_sums, sum);
-        if (b < p.batch)
-            offs[b] = missing + before;
-        missing += sum;
-    }
-
-    // Free pages in order: a CTA's run of pages, counted, then ranked behind the runs before.
+    // Missing pages before each sequence's, in every CTA, and free pages in order: a CTA's run of
+    // pages, counted, then ranked behind the runs before.
     constexpr int ROUND = FORK_THREADS * FORK_PAGES;
     const int run = (p.num_pages + FORK_CTAS - 1) / FORK_CTAS;
     const int p0 = min(rank * run, p.num_pages), p1 = min(p0 + run, p.num_pages);
@@ -199,8 +215,16 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     int count = __popc(free0);
     for (int at = p0 + ROUND + FORK_PAGES * tid; at < p1; at += ROUND)
         count += __popc(free_at(at));
-    int total;
-    block_prefix(count, warp_sums, total);
+    int missing = 0, total = 0;
+    for (int base = 0; base < p.batch; base += FORK_THREADS) {
+        const int b = base + tid;
+        int v[2] = {b < p.batch ? offs[b] : 0, base == 0 ? count : 0}, sum[2];
+        block_prefix(v, warp_sums, sum);
+        if (b < p.batch)
+            offs[b] = missing + v[0];
+        missing += sum[0];
+        total += sum[1];
+    }
     if (tid < FORK_CTAS)
         store_in_cta(free_of + rank, tid, total);
     cluster_sync();
@@ -213,9 +237,10 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     for (int base = p0; base < p1 && found < missing; base += ROUND) {
         const int at = base + FORK_PAGES * tid;
         const unsigned free = base == p0 ? free0 : free_at(at);
-        int sum;
-        int k = found + block_prefix(__popc(free), warp_sums, sum);
-        found += sum;
+        int v[1] = {__popc(free)}, sum[1];
+        block_prefix(v, warp_sums, sum);
+        int k = found + v[0];
+        found += sum[0];
         if (!free || k >= missing)
             continue;
         int lo = 0, hi = p.batch - 1;  // the last b with offs[b] <= k
