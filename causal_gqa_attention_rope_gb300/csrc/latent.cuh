@@ -63,4 +63,6 @@ cudaError_t launch_latent_append(const LatentAppendParams &p, const PagedView &p
 cudaError_t launch_latent(const LatentParams &p, const PagedView &pg, cudaStream_t stream);
 // Clusters of that many CTAs, one per SM, that the device runs at a time.
 int sm_clusters(int ctas);
+// Absorbed attention in units of 128 rows, kv_rank 256 and 512, without the second pass.
+cudaError_t launch_latent_pair(const LatentParams &p, const PagedView &pg, cudaStream_t stream);
 cudaError_t launch_latent_expanded(const ExpandedParams &p, cudaStream_t stream);

@@ -40,17 +40,15 @@
 #include <algorithm>
 #include <climits>
 
-#include "latent.cuh"
+#include "latent_runs.cuh"
 #include "na_host.cuh"
 #include "tc_primitives.cuh"
 #include "tile_waits.cuh"
 
 namespace {
 
-constexpr int KT = kLatentKeys;
 constexpr int MAX_ROWS = 64;               // M of S, whatever a unit's rows are
 constexpr int THREADS = 256;
-constexpr int UNIT_STEPS = 1;
 constexpr uint32_t BLOCK_BYTES = KT * 128;  // 64 keys of 64 bf16: a column block of a tile
 
 // QR: rows of a unit.  With 32 the products' rows 32 .. 63 are whatever lies behind a block of
@@ -77,254 +75,6 @@ struct __align__(1024) LatentSmem {
     int abort_flag;
 };
 
-struct Sequence {
-    int tok0, n, prior;
-};
-
-// Sequence b; n = 0 where it breaks the call's bounds (`code` says how).
-__device__ __forceinline__ Sequence sequence_of(const LatentParams &p, int b, int &code)
-{
-    Sequence s;
-    s.tok0 = __ldg(p.cu_seqlens + b);
-    s.n = __ldg(p.cu_seqlens + b + 1) - s.tok0;
-    s.prior = __ldg(p.cache_lens + b);
-    code = NA_OK;
-    if (s.n > p.max_new_len || s.tok0 < 0 || (b == 0 && s.tok0 != 0) ||
-        (long long)s.tok0 + s.n > p.total_tokens)
-        code = NA_ERR_INVALID_ARG;
-    else if (s.n > 0 && (s.prior < 0 || (long long)s.prior + s.n > min(p.capacity, p.max_total_len)))
-        code = NA_ERR_CAPACITY;
-    if (code != NA_OK || s.n < 0)
-        s.n = 0;
-    return s;
-}
-
-template <int UR>
-__device__ __forceinline__ int units_of(const LatentParams &p, const Sequence &s)
-{
-    return (s.n * p.H + UR - 1) / UR;
-}
-
-// Keys that the rows of unit t see.
-template <int UR>
-__device__ __forceinline__ int keys_of(const LatentParams &p, const Sequence &s, int t)
-{
-    return s.prior + (min(t * UR + UR, s.n * p.H) - 1) / p.H + 1;
-}
-
-// What the unit counts for in a run: steps.
-template <int UR>
-__device__ __forceinline__ int steps_of(const LatentParams &p, const Sequence &s, int t)
-{
-    return (keys_of<UR>(p, s, t) + KT - 1) / KT + UNIT_STEPS;
-}
-
-// Steps of the sequences 32 `chunk` + lane, a warp at a time: each lane its own, or, where
-// one of them has many units, all lanes together one sequence after the other.
-template <int UR>
-__device__ __forceinline__ long long chunk_steps(const LatentParams &p, int chunk, int lane)
-{
-    const int b = chunk * 32 + lane;
-    Sequence s{0, 0, 0};
-    int code = NA_OK;
-    if (b < p.batch)
-        s = sequence_of(p, b, code);
-    if (code != NA_OK && blockIdx.x == 0)
-        na_report(p.status, code);
-    const int units = units_of<UR>(p, s);
-    long long sum = 0;
-    if (!__any_sync(0xffffffffu, units > 16)) {
-        for (int t = 0; t < units; t++)
-            sum += steps_of<UR>(p, s, t);
-        return sum;
-    }
-    for (int i = 0; i < 32; i++) {
-        const Sequence o{0, __shfl_sync(0xffffffffu, s.n, i), __shfl_sync(0xffffffffu, s.prior, i)};
-        long long x = 0;
-        for (int t = lane; t < units_of<UR>(p, o); t += 32)
-            x += steps_of<UR>(p, o, t);
-#pragma unroll
-        for (int k = 16; k; k >>= 1)
-            x += __shfl_xor_sync(0xffffffffu, x, k);
-        if (lane == i)
-            sum = x;
-    }
-    return sum;
-}
-
-__device__ __forceinline__ long long inclusive_sum(long long x, int lane)
-{
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    return x;
-}
-
-// Runs that have work (all others are empty), and the first step of run c; the runs of
-// `total` steps are as equal as can be, none of them empty.
-__device__ __forceinline__ long long busy_runs(const LatentParams &p, long long total)
-{
-    return min((long long)p.grid, total);
-}
-
-__device__ __forceinline__ long long run_begin(const LatentParams &p, long long total, int c)
-{
-    const long long busy = busy_runs(p, total);
-    return c >= busy ? total : total * c / busy;
-}
-
-// The run that holds the step before `end`: the last c with total c / busy < end.
-__device__ __forceinline__ int run_of(const LatentParams &p, long long total, long long end)
-{
-    return (int)((end * busy_runs(p, total) + total - 1) / total) - 1;
-}
-
-// Run `run`: sm.total, sm.begin and the unit and step of it that it begins with.  Each warp
-// sums a range of sequences; the one whose range holds the beginning looks it up.
-template <int UR, class Smem>
-__device__ __forceinline__ void find_run(const LatentParams &p, Smem &sm, int run, int warp, int lane)
-{
-    constexpr int WARPS = THREADS / 32;
-    const int chunks = (p.batch + 31) / 32, per = (chunks + WARPS - 1) / WARPS;
-    const int c0 = min(warp * per, chunks), c1 = min(c0 + per, chunks);
-    long long mine = 0, chunk_sum = 0;  // (a single chunk's sums are kept)
-    for (int c = c0; c < c1; c++) {
-        chunk_sum = chunk_steps<UR>(p, c, lane);
-        mine += chunk_sum;
-    }
-#pragma unroll
-    for (int k = 16; k; k >>= 1)
-        mine += __shfl_xor_sync(0xffffffffu, mine, k);
-    if (lane == 0)
-        sm.warp_steps[warp] = mine;
-    __syncthreads();
-    long long total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; w++) {
-        before += w < warp ? sm.warp_steps[w] : 0;
-        total += sm.warp_steps[w];
-    }
-    const long long begin = run_begin(p, total, run);
-    if (threadIdx.x == 0) {
-        sm.total = total;
-        sm.begin = begin;
-    }
-    if (begin >= before && begin < before + mine) {
-        for (int c = c0; c < c1; c++) {
-            if (per > 1)
-                chunk_sum = chunk_steps<UR>(p, c, lane);
-            const long long upto = inclusive_sum(chunk_sum, lane);
-            const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
-            if (past) {
-                const int i = __ffs(past) - 1, b = c * 32 + i;
-                before += __shfl_sync(0xffffffffu, upto - chunk_sum, i);
-                int code;
-                const Sequence s = sequence_of(p, b, code);
-                for (int t = 0;; t += 32) {
-                    const long long x = t + lane < units_of<UR>(p, s) ? steps_of<UR>(p, s, t + lane) : 0;
-                    const long long y = inclusive_sum(x, lane);
-                    const unsigned m = __ballot_sync(0xffffffffu, before + y > begin);
-                    if (m) {
-                        const int k = __ffs(m) - 1;
-                        if (lane == k) {
-                            sm.b0 = b;
-                            sm.t0 = t + k;
-                            sm.step0 = (int)(begin - (before + y - x));
-                        }
-                        break;
-                    }
-                    before += __shfl_sync(0xffffffffu, y, 31);
-                }
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, upto, 31);
-        }
-    }
-    __syncthreads();
-}
-
-// One after the other, the pieces of a run.  Every warp role walks them for itself.
-template <int UR>
-struct Walk {
-    int b, t, step;       // next: sequence, unit, step of it
-    long long left;       // steps of the run from there
-    Sequence s;
-    bool have;
-
-    // the piece: tiles [lo, hi) of `tiles` of unit `unit` of sequence `seq`, which has `keys`
-    int seq, unit, lo, hi, tiles, keys;
-
-    template <class Smem>
-    __device__ __forceinline__ Walk(const LatentParams &p, const Smem &sm, int run)
-        : b(sm.b0), t(sm.t0), step(sm.step0), left(run_begin(p, sm.total, run + 1) - sm.begin),
-          have(false)
-    {
-    }
-
-    // Piece `piece` of p.pieces of a unit of its own (none where the sequence has fewer units).
-    __device__ __forceinline__ Walk(const LatentParams &p, int index, int piece) : left(0), have(false)
-    {
-        const int units = (p.max_new_len * p.H + UR - 1) / UR;  // of the longest sequence
-        b = index / units;
-        t = index % units;
-        int code;
-        s = sequence_of(p, b, code);
-        if (code != NA_OK && t == 0 && piece == 0 && threadIdx.x == 0)
-            na_report(p.status, code);
-        if (t >= units_of<UR>(p, s))
-            return;
-        const int all = (keys_of<UR>(p, s, t) + KT - 1) / KT;
-        const int from = (int)((long long)all * piece / p.pieces);
-        step = from + UNIT_STEPS;
-        left = (int)((long long)all * (piece + 1) / p.pieces) - from;
-        have = true;
-    }
-
-    __device__ __forceinline__ bool next(const LatentParams &p)
-    {
-        if (left <= 0)
-            return false;
-        int code;
-        while (!have) {
-            s = sequence_of(p, b, code);
-            have = t < units_of<UR>(p, s);
-            if (!have) {
-                b++;
-                t = 0;
-            }
-        }
-        seq = b;
-        unit = t;
-        keys = keys_of<UR>(p, s, t);
-        tiles = (keys + KT - 1) / KT;
-        const int end = (int)min((long long)tiles + UNIT_STEPS, step + left);
-        lo = max(step - UNIT_STEPS, 0);
-        hi = max(end - UNIT_STEPS, 0);
-        left -= end - step;
-        step = 0;
-        t++;
-        have = t < units_of<UR>(p, s);
-        if (!have) {
-            b++;
-            t = 0;
-        }
-        return hi > lo;  // (none: the run ends within the unit's first steps)
-    }
-
-    // rows of the unit from `at` on, `most` at most, and the first one among the call's
-    __device__ __forceinline__ int rows(const LatentParams &p, int at, int most) const
-    {
-        return max(min(most, s.n * p.H - unit * UR - at), 0);
-    }
-    __device__ __forceinline__ long long row0(const LatentParams &p) const
-    {
-        return (long long)s.tok0 * p.H + unit * UR;
-    }
-};
-
 // 16 lanes x 64 columns of tensor memory: thread l gets columns 8 i + 2 (l % 4) + {0, 1}
 // of lane l / 4 in r[4 i], r[4 i + 1] and of lane l / 4 + 8 in r[4 i + 2], r[4 i + 3].
 __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
@@ -342,29 +92,7 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr));
 }
 
-// Barrier of the four softmax warps that also says whether any thread's `x` holds.
-__device__ __forceinline__ bool softmax_any(bool x)
-{
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(any)
-        : "r"(x ? 1u : 0u)
-        : "memory");
-    return any != 0;
-}
-
-// `at`'s place in CTA `rank` of the cluster, and what is there.
-__device__ __forceinline__ uint32_t place_in_cta(const void *at, int rank)
-{
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(at)), "r"(rank));
-    return a;
-}
-
+// What is at `at`'s place in CTA `rank` of the cluster.
 __device__ __forceinline__ float4 load_cluster_4(const void *at, int rank)
 {
     float4 x;
@@ -518,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if constexpr (JOINED)
         __syncthreads();
     else
-        find_run<UR>(p, sm, run, warp, lane);
+        find_run<UR, THREADS / 32>(p, sm, run, warp, lane);
     if constexpr (CL > 1)
         cluster_sync();  // the other CTA's barriers are there
     tc::fence_after_sync();
@@ -572,21 +300,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         };
         for (; ok && w.next(p); pieces++) {
             const int32_t *row = pg.table + (size_t)w.seq * pg.pages_per_seq;
-            // this lane's page of a tile (boxes of them), or -1
-            auto page_of = [&](int j) {
-                const int at = j * KT + (lane << box_log), entry = at >> pg.page_log;
+            // This lane's page of a tile (boxes of them): its table entry, asked for two tiles ahead and
+            // not looked at before the tile's turn (800 cycles a tile otherwise), then checked; -1
+            // where there is none.
+            auto has_page = [&](int j) {
+                return lane < boxes && j < w.hi && j * KT + (lane << box_log) < w.keys;
+            };
+            auto ask = [&](int j) {
+                const int entry = (j * KT + (lane << box_log)) >> pg.page_log;
                 int id = JOINED ? __shfl_sync(0xffffffffu, early, entry & 31) : 0;
-                if (lane >= boxes || j >= w.hi || at >= w.keys)
-                    return -1;
-                if (!JOINED || entry >= 32)
+                if (has_page(j) && (!JOINED || entry >= 32))
                     id = __ldg(row + entry);
+                return id;
+            };
+            auto checked = [&](int j, int id) {
+                if (!has_page(j))
+                    return -1;
                 if ((unsigned)id >= (unsigned)pg.num_pages) {  // reported; page 0 is read instead
                     na_report(p.status, NA_ERR_PAGE);
                     id = 0;
                 }
                 return id;
             };
-            int id = page_of(w.lo);
+            int asked = ask(w.lo), asked_next = ask(w.lo + 1);
             if (pieces > 0 && !wait_all(&sm.q_empty, (pieces - 1) & 1))
                 break;
             if (lane == 0)
@@ -595,7 +331,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane < CB)
                 tc::tma_load_2d(sm.q[lane], &map_q, lane * 64, (int)w.row0(p) + rank * QR, &sm.q_full);
             for (int j = w.lo; ok && j < w.hi; j++) {
-                const int next = page_of(j + 1);
+                const int id = checked(j, asked);
+                asked = asked_next;
+                asked_next = ask(j + 2);
                 const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
                 const int first = (id << pg.page_log) + (pg.page_log > 6 ? (j * KT) & in_page : 0);
                 const int box = lane & (boxes - 1), block = lane / boxes;
@@ -627,7 +365,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                     load(sm.pair[ps][0], c * 128, 2, 0, &sm.pair_full[ps]);
                 }
-                id = next;
             }
         }
         // every copy issued lands before the CTA can exit
@@ -1062,6 +799,24 @@ __global__ void __launch_bounds__(R / 4 * MERGE_THREADS_PER_DIM)
     reinterpret_cast<uint2 *>(p.out + ((size_t)cut.x + r) * R)[x] = u;
 }
 
+// Second pass: the units that runs left in pieces.
+template <int R, int UR>
+cudaError_t launch_merge(const LatentParams &p, cudaStream_t stream)
+{
+    if (p.grid == 1)
+        return cudaSuccess;
+    const int rows = (int)std::min((long long)p.max_new_len * p.H, (long long)UR);
+    const dim3 block(R / 4 * MERGE_THREADS_PER_DIM);
+    const int entries = p.cut_by_sequence ? p.batch : p.grid;
+    // Few units have many pieces each (4 long contexts of 16 heads: the pass took 10 us with a
+    // thread per dim and row, every entry of every run looked at).
+    if ((long long)entries * rows <= 2 * sm_count())
+        return launch_kernel(latent_merge_kernel<R, UR, 4>, dim3(entries, rows), block, 0, stream, p);
+    return launch_kernel(latent_merge_kernel<R, UR, 1>,
+                         dim3(entries, (rows + MERGE_THREADS_PER_DIM - 1) / MERGE_THREADS_PER_DIM),
+                         block, 0, stream, p);
+}
+
 template <int R, int QR, int CL, bool JOINED>
 cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
@@ -1087,19 +842,9 @@ cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStre
     const int cluster = JOINED ? p.pieces : CL;
     e = launch_kernel_cluster(latent_attn_kernel<R, QR, CL, JOINED>, dim3(p.grid * cluster), dim3(THREADS),
                               smem, cluster > 1 ? cluster : 0, stream, p, pg, mq, mkv);
-    if (JOINED || e != cudaSuccess || p.grid == 1)
+    if (JOINED || e != cudaSuccess)
         return e;
-    constexpr int UR = QR * CL;
-    const int rows = (int)std::min((long long)p.max_new_len * p.H, (long long)UR);
-    const dim3 block(R / 4 * MERGE_THREADS_PER_DIM);
-    const int entries = p.cut_by_sequence ? p.batch : p.grid;
-    // Few units have many pieces each (4 long contexts of 16 heads: the pass took 10 us with a
-    // thread per dim and row, every entry of every run looked at).
-    if ((long long)entries * rows <= 2 * sm_count())
-        return launch_kernel(latent_merge_kernel<R, UR, 4>, dim3(entries, rows), block, 0, stream, p);
-    return launch_kernel(latent_merge_kernel<R, UR, 1>,
-                         dim3(entries, (rows + MERGE_THREADS_PER_DIM - 1) / MERGE_THREADS_PER_DIM),
-                         block, 0, stream, p);
+    return launch_merge<R, QR * CL>(p, stream);
 }
 
 template <int R>
@@ -1111,7 +856,13 @@ cudaError_t launch_latent_rows(const LatentParams &p, const PagedView &pg, cudaS
     switch (p.unit_rows) {
     case 32: return launch_latent_t<R, 32, 1, false>(p, pg, stream);
     case 64: return launch_latent_t<R, 64, 1, false>(p, pg, stream);
-    default: return launch_latent_t<R, 64, 2, false>(p, pg, stream);
+    default:
+        if constexpr (R == 128) {
+            return launch_latent_t<R, 64, 2, false>(p, pg, stream);
+        } else {
+            const cudaError_t e = launch_latent_pair(p, pg, stream);
+            return e != cudaSuccess ? e : launch_merge<R, 128>(p, stream);
+        }
     }
 }
 
