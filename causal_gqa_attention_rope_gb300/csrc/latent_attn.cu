@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         sm.factor[g & 1][ra + 8 * h] = alpha[h];
                 }
                 // (a warp whose wait gave up still comes here, so that the others go on to see it)
-                const bool rescale = softmax_any(raise || !ok);
+                const bool rescale = any_of(raise || !ok, 1, 128);
                 if (aborted(&sm.abort_flag))
                     ok = false;
                 uint32_t pk[16];
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             make_float2(m_ref[h], sum[h]);
                 }
             }
-            if (softmax_any(!ok)) {
+            if (any_of(!ok, 1, 128)) {
                 ok = false;
                 break;
             }

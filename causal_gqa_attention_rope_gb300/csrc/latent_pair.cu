@@ -20,12 +20,16 @@
 // also says that they are there.  K's and Q's copies of both CTAs complete on the first one's
 // barriers.  That the second one's weights are written and its S read it tells by a word
 // per warp, again by st.async: an arrival on the first one's barrier that released at cluster
-// scope took some 900 cycles a tile (206 us -> 190; with messages XX).  What a message
+// scope took some 900 cycles a tile (drafted tokens 190 us, 159 with messages).  What a message
 // speaks of is done before it is sent: P by the proxy fence in the shared memory that holds it, S
 // in registers.
 //
-// Warps: 0 loads Q and K, 8 V; of the first CTA 1 issues S, 2 issues O^T; 4 .. 7 softmax: thread
-// (32 q + lane) has row 32 (q % 2) + lane and half of a tile's keys.
+// Warps: 0 loads Q and K, 3 V; of the first CTA 1 issues S, 2 issues O^T, of the second 1 tells
+// that V has landed; 4 .. 7 and 8 .. 11 softmax of the even and the odd tiles (one group of
+// four warps took 1500 cycles a tile, most of them latencies of its many meetings: drafted
+// tokens 159 us, 145 with two groups): thread (32 q +
+// lane) has row 32 (q % 2) + lane and half of a tile's keys.  The reference maximum goes from
+// group to group as soon as a tile's maximum is known.
 #include <climits>
 
 #include "latent_runs.cuh"
@@ -35,7 +39,7 @@
 namespace {
 
 constexpr int QR = 64, UR = 2 * QR;
-constexpr int THREADS = 288;
+constexpr int THREADS = 384;
 constexpr int NUM_S = 4;
 constexpr uint32_t Q_BLOCK = QR * 128, K_BLOCK = KT / 2 * 128, V_BLOCK = KT * 128;  // of 64 columns
 
@@ -49,11 +53,13 @@ struct __align__(1024) PairSmem {
     bf16 v[ST][2 * DB][KT * 64];
     bf16 p[2][QR * 64];
     float factor[2][UR];       // of all rows, from both CTAs
-    float halves[2][2][QR];    // maxima of a row's two threads; at a piece's end their sums
+    float halves[2][2][QR];    // by group: maxima of a row's two threads; at a piece's end their sums
+    float m_ref[2][QR];        // reference maxima after even and odd tiles
     uint64_t q_full, q_empty, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST];
-    uint64_t s_full[NUM_S], s_read[NUM_S], p_full[2], pv_done[2], f_full[2], o_empty, drain[2];
-    // of the first CTA: s_read and p_full of the second
-    uint64_t s_peer[NUM_S], p_peer[2];
+    uint64_t s_full[NUM_S], s_read[NUM_S], m_done[2], p_full[2], pv_done[2], f_full[2], sums_full,
+        o_empty, drain[2];
+    // of the first CTA: s_read, p_full and v_full of the second
+    uint64_t s_peer[NUM_S], p_peer[2], v_peer[ST];
     float told;                // what its messages write
     long long warp_steps[THREADS / 32];
     long long total, begin;
@@ -71,12 +77,10 @@ __device__ __forceinline__ void store_async(const float *at, const uint64_t *bar
                  : "memory");
 }
 
-constexpr int MESSAGES = 4;  // a word from each softmax warp of the second CTA
-
-// The first CTA waits for the second one's messages.
-__device__ __forceinline__ bool wait_told(uint64_t *bar, uint32_t parity)
+// The first CTA waits for `words` words of the second.
+__device__ __forceinline__ bool wait_told(uint64_t *bar, uint32_t parity, int words)
 {
-    mbar_arrive_expect_tx(bar, MESSAGES * 4);
+    mbar_arrive_expect_tx(bar, words * 4);
     return mbar_wait_cluster(bar, parity);
 }
 
@@ -106,6 +110,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_empty[i], 1);
+            mbar_init(&sm.v_peer[i], 1);
         }
         for (int i = 0; i < NUM_S; i++) {
             mbar_init(&sm.s_full[i], 1);
@@ -113,13 +118,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&sm.s_peer[i], 1);
         }
         for (int i = 0; i < 2; i++) {
+            mbar_init(&sm.m_done[i], 4);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.p_peer[i], 1);
             mbar_init(&sm.pv_done[i], 1);
             mbar_init(&sm.f_full[i], 1);
             mbar_init(&sm.drain[i], 1);
         }
-        mbar_init(&sm.o_empty, 8);  // the softmax warps of both CTAs
+        mbar_init(&sm.sums_full, 1);
+        mbar_init(&sm.o_empty, 16);  // the softmax warps of both CTAs
         sm.abort_flag = 0;
         fence_barrier_init();
     }
@@ -134,7 +141,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = sm.tmem_base;
     Walk<UR> w(p, sm, run);
 
-    if (warp == 0 || warp == 8) {
+    if (warp == 0 || warp == 3) {
         // ----------------------------------------------------------- producers --
         const bool is_k = warp == 0;
         const int box_log = min(pg.page_log, 6), boxes = KT >> box_log;  // rows of one page in a tile
@@ -233,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ok = mbar_wait_bounded(&sm.k_full[st], (g / ST) & 1);
                     if (ok && g >= NUM_S)
                         ok = mbar_wait_bounded(&sm.s_read[sb], (g / NUM_S - 1) & 1) &&
-                             wait_told(&sm.s_peer[sb], (g / NUM_S - 1) & 1);
+                             wait_told(&sm.s_peer[sb], (g / NUM_S - 1) & 1, 4);
                     if (!ok || aborted(&sm.abort_flag)) {
                         ok = false;
                         break;
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             for (int i = max(g - NUM_S, 0); ok && i < g; i++)  // no message is under way at the end
-                ok = wait_told(&sm.s_peer[i % NUM_S], (i / NUM_S) & 1);
+                ok = wait_told(&sm.s_peer[i % NUM_S], (i / NUM_S) & 1, 4);
             if (!ok)
                 set_abort(&sm.abort_flag, p.status);
             if (issued) {  // all issued MMAs complete before tensor memory is released
@@ -273,15 +280,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (piece > 0)
                     ok = mbar_wait_cluster(&sm.o_empty, (piece - 1) & 1);
                 for (int j = w.lo; ok && j < w.hi; j++, g++) {
-                    // (V of both CTAs: their softmax warps have waited for it)
-                    ok = mbar_wait_bounded(&sm.p_full[g & 1], (g >> 1) & 1) &&
-                         wait_told(&sm.p_peer[g & 1], (g >> 1) & 1);
+                    const int st = g % ST;
+                    ok = mbar_wait_bounded(&sm.v_full[st], (g / ST) & 1) &&
+                         wait_told(&sm.v_peer[st], (g / ST) & 1, 1) &&
+                         mbar_wait_bounded(&sm.p_full[g & 1], (g >> 1) & 1) &&
+                         wait_told(&sm.p_peer[g & 1], (g >> 1) & 1, 4);
                     if (!ok || aborted(&sm.abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    const int st = g % ST;
                     const uint64_t pd = pd0 + (uint64_t)((g & 1) * (Q_BLOCK >> 4));
 #pragma unroll
                     for (int d = 0; d < DB; d++) {
@@ -302,26 +310,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 drain_wait(&sm.drain[1], 0, p.status);
             }
         }
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp == 1) {
+        // ------------------------- of the second CTA: tells the first that V has landed --
+        if (lane == 0) {
+            bool ok = true;
+            for (int g = 0; ok && w.next(p);)
+                for (int j = w.lo; ok && j < w.hi; j++, g++) {
+                    ok = mbar_wait_bounded(&sm.v_full[g % ST], (g / ST) & 1) && !aborted(&sm.abort_flag);
+                    if (ok)
+                        store_async(&sm.told, &sm.v_peer[g % ST], 0, 0.f);
+                }
+            if (!ok)
+                set_abort(&sm.abort_flag, p.status);
+        }
+    } else if (warp >= 4) {
         // -------------------------------------------------------------- softmax --
-        const int quarter = warp & 3, tid = threadIdx.x - 128;
+        const int group = warp >= 8, quarter = warp & 3, tid = threadIdx.x & 127;
         const int r = (quarter & 1) * 32 + lane, half = quarter >> 1;  // row, and keys 32 half .. + 31
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const float sl2 = p.scale_log2;
         bool ok = true;
-        int g = 0, f = 0;  // tiles; exchanges of factors
-        // x of this CTA's rows to both CTAs; they are in sm.factor[f & 1] when this has returned true
-        auto exchange_begin = [&](float x) {
+        int g = 0;  // tiles, those of group g & 1
+        // x of this CTA's rows to both CTAs, into `to` (of all rows) ...
+        auto send = [&](float *to, uint64_t *bar, float x) {
             if (half == 0)
 #pragma unroll
                 for (int c = 0; c < 2; c++)
-                    store_async(&sm.factor[f & 1][rank * QR + r], &sm.f_full[f & 1], c, x);
+                    store_async(to + rank * QR + r, bar, c, x);
             if (tid == 0)
-                mbar_arrive_expect_tx(&sm.f_full[f & 1], UR * 4);
+                mbar_arrive_expect_tx(bar, UR * 4);
         };
-        auto exchange_end = [&] {
-            const bool done = mbar_wait_cluster(&sm.f_full[f & 1], (f >> 1) & 1) && !aborted(&sm.abort_flag);
-            f++;
+        // ... where they are when this has returned true.
+        auto received = [&](uint64_t *bar, uint32_t parity) {
+            const bool done = mbar_wait_cluster(bar, parity) && !aborted(&sm.abort_flag);
             return __all_sync(0xffffffffu, done) != 0;
         };
         // An arrival of this warp, in the second CTA as a message to the first.
@@ -334,16 +355,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                     store_async(&sm.told, peer, 0, 0.f);
             }
         };
-        const bool leader = tid == 0 && rank == 0;
+        const bool leader = threadIdx.x == 128 && rank == 0;
         if (leader && !p.cut_by_sequence)
             p.cut[run] = make_int4(0, 0, 0, -1);
-        while (ok && w.next(p)) {
+        for (int piece = 0; ok && w.next(p); piece++) {
             const int rows = w.rows(p, 0, UR), mine = w.rows(p, rank * QR, QR);
             // keys that the row sees
             const int lim = r < mine ? w.s.prior + (w.unit * UR + rank * QR + r) / p.H + 1 : 0;
-            float m_ref = -INFINITY, sum = 0.f;
-            for (int j = w.lo; j < w.hi; j++, g++) {
-                const int j0 = j * KT, sb = g % NUM_S, st = g % ST;
+            const int g0 = g, g_end = g + w.hi - w.lo;
+            float m_own = -INFINITY, sum = 0.f;  // of this group's tiles
+            for (g += (g ^ group) & 1; g < g_end; g += 2) {
+                const int j0 = (w.lo + g - g0) * KT, sb = g % NUM_S, st = g % ST;
                 ok = ok && warp_wait(&sm.s_full[sb], (g / NUM_S) & 1, &sm.abort_flag);
                 uint32_t s[32];
                 if (ok) {
@@ -352,6 +374,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc::tmem_wait_ld();
                     tc::fence_before_sync();
                     tell(&sm.s_read[sb], &sm.s_peer[sb]);
+                    // The product before the last is done: its P, and all that the group had for
+                    // it here and in the other CTA, may be written over.
+                    if (g >= 2)
+                        ok = warp_wait(&sm.pv_done[group], ((g >> 1) - 1) & 1, &sm.abort_flag);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; i++)
@@ -367,20 +393,30 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 16; i++)
                     mx = max3f(mx, __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-                sm.halves[f & 1][half][r] = mx;
+                sm.halves[group][half][r] = mx;
                 // (a warp whose wait gave up still comes here, so that the others go on to see it)
-                if (softmax_any(!ok)) {
+                if (any_of(!ok, 1 + group, 128)) {
                     ok = false;
                     break;
                 }
-                mx = fmaxf(mx, sm.halves[f & 1][half ^ 1][r]) * sl2;
-                float alpha = 1.f;  // (1 as well where there is nothing to rescale yet)
+                mx = fmaxf(mx, sm.halves[group][half ^ 1][r]) * sl2;
+                // the reference after the tile before, which the other group had
+                float m_ref = -INFINITY, alpha = 1.f;  // (1 as well where there is nothing to rescale yet)
+                if (g > g0) {
+                    ok = warp_wait(&sm.m_done[group ^ 1], ((g - 1) >> 1) & 1, &sm.abort_flag);
+                    m_ref = sm.m_ref[group ^ 1][r];
+                }
                 if (mx > m_ref + 8.0f) {
                     if (m_ref != -INFINITY)
                         alpha = ex2_mufu(m_ref - mx);
                     m_ref = mx;
                 }
-                exchange_begin(alpha);
+                if (half == 0)
+                    sm.m_ref[group][r] = m_ref;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.m_done[group]);
+                send(sm.factor[group], &sm.f_full[group], alpha);
                 const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
                 float2 acc = make_float2(0.f, 0.f);
                 uint32_t pk[16];
@@ -393,34 +429,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                     acc = __fadd2_rn(acc, e);
                     pk[i] = pack_bf16x2(e.x, e.y);
                 }
-                sum = fmaf(sum, alpha, acc.x + acc.y);
-                // the buffer of P is free when the product before the last is done
-                if (g >= 2)
-                    ok = warp_wait(&sm.pv_done[g & 1], ((g >> 1) - 1) & 1, &sm.abort_flag);
-                if (ok) {
-#pragma unroll
-                    for (int c = 0; c < 4; c++)
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(sm.p[g & 1]) + r * 128 +
-                                                   (((half * 4 + c) ^ (r & 7)) << 4)) =
-                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                    ok = warp_wait(&sm.v_full[st], (g / ST) & 1, &sm.abort_flag);
+                if (m_own != m_ref) {
+                    sum *= m_own == -INFINITY ? 0.f : ex2_mufu(m_own - m_ref);
+                    m_own = m_ref;
                 }
+                sum += acc.x + acc.y;
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(sm.p[group]) + r * 128 +
+                                               (((half * 4 + c) ^ (r & 7)) << 4)) =
+                        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                 if (ok && j0 + KT > w.keys) {
                     // Rows behind the last key hold whatever was there: zeros, so that no weight of 0
                     // meets a NaN.
+                    ok = warp_wait(&sm.v_full[st], (g / ST) & 1, &sm.abort_flag);
                     const int from = w.keys - j0, per = (KT - from) * 8;
-                    for (int i = tid; i < per * 2 * DB; i += 128)
+                    for (int i = tid; ok && i < per * 2 * DB; i += 128)
                         reinterpret_cast<uint4 *>(sm.v[st][i / per])[from * 8 + i % per] =
                             make_uint4(0, 0, 0, 0);
                 }
-                ok = exchange_end() && ok;
-                const float4 fs = reinterpret_cast<const float4 *>(sm.factor[(f - 1) & 1])[lane];
-                if (ok && __any_sync(0xffffffffu, fs.x != 1.f || fs.y != 1.f || fs.z != 1.f || fs.w != 1.f)) {
+                ok = received(&sm.f_full[group], (g >> 1) & 1) && ok;
+                const float4 fs = reinterpret_cast<const float4 *>(sm.factor[group])[lane];
+                if (__any_sync(0xffffffffu, fs.x != 1.f || fs.y != 1.f || fs.z != 1.f || fs.w != 1.f) && ok) {
                     // O^T is touched only to rescale it, when the last product has landed
-                    ok = warp_wait(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sm.abort_flag);
+                    ok = warp_wait(&sm.pv_done[group ^ 1], ((g - 1) >> 1) & 1, &sm.abort_flag);
                     if (ok) {
                         tc::fence_after_sync();
-                        const float *fac = sm.factor[(f - 1) & 1];
 #pragma unroll 1
                         for (int c = 0; c < DB * UR; c += 32) {
                             uint32_t o[32];
@@ -428,7 +462,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tc::tmem_wait_ld();
 #pragma unroll
                             for (int i = 0; i < 32; i++)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[(c & (UR - 1)) + i]);
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) *
+                                                       sm.factor[group][(c & (UR - 1)) + i]);
                             tc::tmem_st32(tmem + lane_off + c, o);
                         }
                         tc::tmem_wait_st();
@@ -437,29 +472,35 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (ok) {
                     tc::fence_proxy_async_smem();
                     tc::fence_before_sync();
-                    tell(&sm.p_full[g & 1], &sm.p_peer[g & 1]);
+                    tell(&sm.p_full[group], &sm.p_peer[group]);
                 }
             }
             // ------------------------------------------------------- a piece's rows --
-            if (ok)
+            g = g_end;
+            if (ok)  // (the last product; all before it are done then)
                 ok = warp_wait(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sm.abort_flag);
-            const bool whole = w.lo == 0 && w.hi == w.tiles;
-            const size_t slot_row = (size_t)(2 * run + (w.lo == 0 ? 1 : 0)) * UR;
-            sm.halves[f & 1][half][r] = sum;
-            if (softmax_any(!ok)) {
+            if (any_of(!ok, 3, 256)) {
                 ok = false;
                 break;
             }
-            sum += sm.halves[f & 1][half ^ 1][r];
-            if (!whole && half == 0 && r < mine)
+            const float m_ref = sm.m_ref[(g - 1) & 1][r];
+            if (m_own != m_ref)
+                sum *= m_own == -INFINITY ? 0.f : ex2_mufu(m_own - m_ref);
+            sm.halves[group][half][r] = sum;
+            named_barrier_sync(3, 256);
+            sum = (sm.halves[0][0][r] + sm.halves[0][1][r]) + (sm.halves[1][0][r] + sm.halves[1][1][r]);
+            const bool whole = w.lo == 0 && w.hi == w.tiles;
+            const size_t slot_row = (size_t)(2 * run + (w.lo == 0 ? 1 : 0)) * UR;
+            if (!whole && group == 0 && half == 0 && r < mine)
                 reinterpret_cast<float2 *>(p.part_ml)[slot_row + rank * QR + r] = make_float2(m_ref, sum);
-            exchange_begin(whole ? (sum > 0.f ? 1.0f / sum : 0.f) : 1.f);
-            ok = exchange_end();
-            const float *inv = sm.factor[(f - 1) & 1];
+            float *inv = reinterpret_cast<float *>(sm.p[0]);  // (P is done with here and in the other CTA)
+            if (group == 0)
+                send(inv, &sm.sums_full, whole ? (sum > 0.f ? 1.0f / sum : 0.f) : 1.f);
+            ok = received(&sm.sums_full, piece & 1);
             tc::fence_after_sync();
             const long long row0 = w.row0(p);
 #pragma unroll 1
-            for (int c = 0; ok && c < DB * UR; c += 32) {
+            for (int c = group * 32; ok && c < DB * UR; c += 64) {
                 const int r0 = c & (UR - 1), dim = (2 * (c / UR) + rank) * 128 + quarter * 32 + lane;
                 if (r0 >= rows)
                     continue;
@@ -471,7 +512,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 32; i++)
                         if (r0 + i < rows)
-                            dst[(size_t)i * R] = __float2bfloat16_rn(__uint_as_float(o[i]) * inv[r0 + i]);
+                            dst[(size_t)i * R] =
+                                __float2bfloat16_rn(__uint_as_float(o[i]) * inv[r0 + i]);
                 } else {
                     float *dst = p.part_o + (slot_row + r0) * R + dim;
 #pragma unroll
@@ -480,7 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             dst[(size_t)i * R] = __uint_as_float(o[i]);
                 }
             }
-            if (softmax_any(!ok)) {  // (and the sums and factors have been read)
+            if (any_of(!ok, 3, 256)) {  // (and the sums and maxima have been read)
                 ok = false;
                 break;
             }

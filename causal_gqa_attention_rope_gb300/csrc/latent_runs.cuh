@@ -258,17 +258,17 @@ struct Walk {
     }
 };
 
-// Barrier of the four softmax warps that also says whether any thread's `x` holds.
-__device__ __forceinline__ bool softmax_any(bool x)
+// Named barrier that also says whether any thread's `x` holds.
+__device__ __forceinline__ bool any_of(bool x, int id, int threads)
 {
     uint32_t any;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"(x ? 1u : 0u)
+        : "r"(x ? 1u : 0u), "r"(id), "r"(threads)
         : "memory");
     return any != 0;
 }
