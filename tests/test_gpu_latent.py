@@ -202,6 +202,56 @@ def test_absorbed_growing_scores():
     check_absorbed(20, 256, 64, 64, [1499], [1], pool=(pool, table), q=q)
 
 
+@pytest.mark.parametrize("k", range(1, 9))
+@pytest.mark.parametrize("H,R,rd", [(5, 512, 64), (40, 128, 32), (64, 256, 48)])
+def test_absorbed_short_contexts(H, R, rd, k):
+    """k tiles in as many pieces, joined in a cluster; beside them sequences with fewer tiles."""
+    check_absorbed(H, R, rd, 64, [64 * k - 30], [1], seed=k)
+    check_absorbed(H, R, rd, 16, [64 * k - 1, 2, 64], [1, 1, 1], seed=k)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("R,rd", [(512, 64), (256, 48), (128, 16)])
+def test_absorbed_many_rows_of_long_contexts(R, rd, page):
+    """Units of 128 rows in pairs of CTAs, whole and in pieces; the second CTA's half without rows."""
+    check_absorbed(24, R, rd, page, [5000, 3, 2000, 10, 777], [9, 1, 4, 0, 6], seed=page)
+    check_absorbed(131, R, rd, page, [4095], [1], seed=page + 1)
+
+
+@pytest.mark.parametrize("R", [512, 256])
+def test_absorbed_growing_scores_in_pairs(R):
+    """Rows of either CTA raise their reference maxima, in tiles of either group."""
+    n = 6100
+    pool, table = make_latent([n], R + 64, 64, 15)
+    pages = table[0, :-(-n // 64)].long()
+    flat = pool[pages].flatten(0, 1)
+    q = randn(16, 1, 100, R + 64)
+    up = torch.linspace(0, 6, len(flat))[:, None]
+    for h in (3, 77, 99):
+        flat = (flat.float() + up * q[0, h].float() / q[0, h].float().norm()).to(torch.bfloat16)
+        up = (up * 1.3).roll(64 * h, 0)
+    flat[n:] = nan_bf16(1, 1)
+    pool[pages] = flat.view(len(pages), 64, R + 64)
+    check_absorbed(100, R, 64, 64, [n - 1], [1], pool=(pool, table), q=q)
+
+
+def test_absorbed_reports_in_pairs():
+    import causal_gqa_attention_rope_gb300 as na
+    cfg = na.LatentConfig(100, 256, 64)
+    pool, table = make_latent([4000, 50], 320, 32, 3)
+    q = randn(4, 2, 100, 320)
+    bad = table.clone()
+    bad[0, 77] = pool.shape[0]
+    out, status = absorbed(cfg, pool, bad, [3999, 49], [1, 1], q)
+    assert status == na.NA_ERR_PAGE
+    rows = rows_of(pool, table, 1, 50)[None]
+    ref, tol = attend(q[1:], rows, rows[..., :256], torch.tensor([50]), 1 / math.sqrt(192))
+    assert ((out[1:].double() - ref).abs() <= tol).all()
+    out, status = absorbed(cfg, pool, table, [3999, 49], [1, 1], q, bounds=(1, 3999))
+    assert status == na.NA_ERR_CAPACITY and (out[:1] == 3.0).all()
+    assert ((out[1:].double() - ref).abs() <= tol).all()
+
+
 def test_absorbed_large_values():
     check_absorbed(9, 512, 64, 64, [300, 20], [1, 4], mag=3.0)
 
