@@ -456,7 +456,12 @@ __global__ void __launch_bounds__(two::THREADS, 2)
             const bool corr = weigh_tile<BN / 32>(tmem + S_COL0 + sb * BN + lane_off, j0, u.pos_lo,
                                                   u.pos_lo + r, u.k_end, p.scale_log2, st, alpha);
             if (j0 + BN > u.k_end) {  // rows behind the last visible key may hold any bits
+                // (V's barrier only tells the phases of two tiles apart: V of the tile before has
+                // landed when its product is done)
                 const int vs = j % VST;
+                if (j >= 1 &&
+                    !(ok = warp_wait(&sm.o_done[(j - 1) % NUM_S], ((j - 1) / NUM_S) & 1, &sm.abort_flag)))
+                    break;
                 if (!(ok = warp_wait(&sm.v_full[vs], (j / VST) & 1, &sm.abort_flag)))
                     break;
                 if (r < BN && r >= u.k_end - j0)

@@ -346,6 +346,45 @@ def test_expanded_tall_units():
     check_expanded(80, 64, 64, 64, [200, 270], [1100, 1300])
 
 
+def test_expanded_prompts_of_many_lengths():
+    """Enough units for two CTAs on every SM, most of them ending inside a tile; NaN between sequences."""
+    import random
+
+    import causal_gqa_attention_rope_gb300 as na
+    r, H = random.Random(11), 32
+    new = [r.randint(1, 512) for _ in range(16)]
+    lens = [n + r.randint(0, 1000) for n in new]
+    starts, at = [], 0
+    for n in lens:
+        starts.append(at)
+        at += n + 70
+    cfg, T, cu = na.LatentConfig(H, rope_dim=64, nope_dim=128, v_dim=128), sum(new), packed(new)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, kv, pe = (torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)
+                 for s in ((T, H, 192), (at, H, 256), (at, 64)))
+    for s, n in zip(starts, lens):
+        kv[s + n:s + n + 70], pe[s + n:s + n + 70] = math.nan, math.nan
+    out, status = torch.full((T, H, 128), 3.0, dtype=torch.bfloat16, device=DEV), ints([0])
+    heads = [0, 13, 31]
+    want = []
+    for b, n in enumerate(new):
+        k0, m = starts[b], lens[b]
+        kv_b, pe_b = kv[k0:k0 + m][:, heads].cpu(), pe[k0:k0 + m].cpu()
+        k = torch.cat([kv_b[..., :128], pe_b[:, None].expand(-1, len(heads), -1)], dim=-1)
+        want.append(attend(q[cu[b]:cu[b + 1]][:, heads].cpu(), k.transpose(0, 1),
+                           kv_b[..., 128:].transpose(0, 1), torch.arange(m - n + 1, m + 1), 1 / math.sqrt(192)))
+    for _ in range(5):
+        out.fill_(3.0)
+        na.na_attn_latent_expanded(cfg, ints(cu), ints(starts), ints(lens), max(new), max(lens), q, kv, pe, out,
+                                   status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        for b, (ref, tol) in enumerate(want):
+            got = out[cu[b]:cu[b + 1]][:, heads].cpu().double()
+            assert ((got - ref).abs() <= tol).all(), b
+        assert not torch.isnan(out).any()
+
+
 def test_expanded_last_wave_cut():
     """160 equal units of 4100 keys and more: those after the last whole wave are cut."""
     import causal_gqa_attention_rope_gb300 as na
