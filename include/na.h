@@ -650,8 +650,8 @@ int na_attn_latent_expanded(const na_latent_cfg *cfg, int32_t batch, const int32
  * library).  Every wait of the library's kernels for a copy or a tensor-core
  * operation gives up after about a second (2^31 SM cycles) and writes
  * NA_ERR_DEVICE_TIMEOUT into the caller's status word instead of hanging.  (The
- * CTAs of a cluster in na_attn_decode_paged also meet in hardware barriers, which
- * every thread reaches whatever its own waits said.)  This call runs that same bounded wait, in a
+ * CTAs of a cluster in na_attn_decode_paged, the latent attention calls and na_pages_fork
+ * also meet in hardware barriers, which every thread reaches whatever its own waits said.)  This call runs that same bounded wait, in a
  * one-CTA kernel, on a barrier that nothing ever completes: after about a
  * second *status holds NA_ERR_DEVICE_TIMEOUT (unless it already held an error),
  * the kernel returns normally and the context stays usable.

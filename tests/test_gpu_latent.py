@@ -544,3 +544,62 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     for a, b in zip(first, (outs[0], wide[0], cache.kv)):
         assert torch.equal(bits(a), bits(b))
+
+
+def test_readme_example_runs():
+    """The README's latent example as written, its rows and both forms finite, the fork's copy equal."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    blocks = re.findall(r"```python\n(.*?)```", text, flags=re.S)
+    scope = {}
+    for block in (blocks[0], blocks[2]):
+        exec(compile(block, "README example", "exec"), scope)
+    assert torch.isfinite(scope["out"].float()).all() and torch.isfinite(scope["out1"].float()).all()
+    two, page = scope["two"], int(scope["dst"][1])
+    assert scope["new_lens"].tolist() == [129, 129] and two.page_table[1, :3].tolist() == [0, 1, page]
+    assert torch.equal(bits(two.kv[page]), bits(two.kv[2]))
+
+
+def test_long_contexts_at_once_and_captured():
+    """Absorbed pairs and expanded pieces, clusters both, on two streams at once; then captured."""
+    import causal_gqa_attention_rope_gb300 as na
+    H, R, n, m = 72, 256, 3, 6000
+    cfg = na.LatentConfig(H, R, 64, 64, 64)
+    pool, table = make_latent([m], R + 64, 64, 1)
+    cache, status = na.PagedLatentCache(pool.to(DEV), table.to(DEV)), ints([0])
+    g = torch.Generator(device=DEV).manual_seed(8)
+    q, big_q, kv, pe = (torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)
+                        for s in ((n, H, R + 64), (300, H, 128), (m, H, 128), (m, 64)))
+    cu, prior, cu_big, zero, keys = ints([0, n]), ints([m - n]), ints([0, 300]), ints([0]), ints([m])
+    size = na.na_latent_paged_workspace_size(cfg, 1, n, n, m)
+    outs = [torch.zeros(n, H, R, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    wide = [torch.zeros(300, H, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    spaces = [na.workspace(size, DEV) for _ in range(2)]
+
+    def step(i):
+        na.na_attn_latent_paged(cfg, cu, prior, n, m, q, cache, outs[i], workspace=spaces[i], status=status)
+        na.na_attn_latent_expanded(cfg, cu_big, zero, keys, 300, m, big_q, kv, pe, wide[i], status=status)
+
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                step(i)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(bits(outs[0]), bits(outs[1])) and torch.equal(bits(wide[0]), bits(wide[1]))
+    first = outs[0].clone(), wide[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(0)
+    outs[0].zero_()
+    wide[0].zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(first[0]), bits(outs[0])) and torch.equal(bits(first[1]), bits(wide[0]))
+    rows = rows_of(pool, table, 0, m)[None]
+    ref, tol = attend(q.cpu(), rows, rows[..., :R], torch.arange(m - n + 1, m + 1), 1 / math.sqrt(128))
+    assert ((first[0].cpu().double() - ref).abs() <= tol).all()
