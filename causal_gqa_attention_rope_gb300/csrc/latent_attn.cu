@@ -26,17 +26,18 @@
 // raised only when a score exceeds it by more than 2^8, and then all four warps
 // rescale the columns of O^T by the factors in shared memory.
 //
-// Sequences of more than 64 rows (chunks, drafted tokens, many heads) take units of 128 rows
-// in pairs of CTAs, 64 rows each: one reads the even column blocks of a tile, the other
-// the odd ones, both by TMA multicast into both, so that a tile comes from L2 once for
-// 128 rows.  A slot of a ring is free when the products of both CTAs are done with it.
+// Work: by runs (latent_runs.cuh), one per CTA, one CTA per SM.  A unit that a cut goes through is
+// left in pieces (unnormalised rows with maximum and sum) which a second pass joins.  Run c
+// has at most two: the end of a unit that an earlier one began (slot 2 c) and the beginning of one
+// that others finish (slot 2 c + 1).  Short contexts instead take a cluster of up to 8 CTAs per unit
+// (JOINED), which join its pieces out of one another's shared memory: no search for the run's
+// beginning, no second pass, and the sequence's first pages asked for beside its lengths.
 //
-// Work: the key tiles of all units, one after the other, are cut into one equal run
-// per CTA (or pair; one CTA per SM), whatever the lengths; a unit costs UNIT_STEPS more, about
-// what its Q and its results hold a CTA up.  A unit that a cut goes through is left in pieces
-// (unnormalised rows with maximum and sum) which a second pass joins.  Run c has at
-// most two: the end of a unit that an earlier one began (slot 2 c) and the beginning of
-// one that others finish (slot 2 c + 1).
+// Sequences of more than 64 rows (chunks, drafted tokens, many heads) take units of 128 rows in
+// pairs of CTAs: latent_pair.cu.  With 128 latent numbers, which that kernel does not split, each CTA
+// of a pair has 64 rows here, one reads the even column blocks of a tile, the other the odd ones,
+// both by TMA multicast into both, so that a tile comes from L2 once for 128 rows.  A slot of
+// a ring is free when the products of both CTAs are done with it.
 #include <algorithm>
 #include <climits>
 

@@ -551,9 +551,9 @@ def test_readme_example_runs():
     import os
     import re
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
-    blocks = re.findall(r"```python\n(.*?)```", text, flags=re.S)
+    first, latent = (re.findall(rf"```{kind}\n(.*?)```", text, flags=re.S)[0] for kind in ("python", "py"))
     scope = {}
-    for block in (blocks[0], blocks[2]):
+    for block in (first, latent):
         exec(compile(block, "README example", "exec"), scope)
     assert torch.isfinite(scope["out"].float()).all() and torch.isfinite(scope["out1"].float()).all()
     two, page = scope["two"], int(scope["dst"][1])
