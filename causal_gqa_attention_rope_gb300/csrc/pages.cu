@@ -26,14 +26,13 @@ using namespace rope;
 // 17 of them for the rows.
 
 constexpr int FORK_CTAS = 8;
-constexpr int FORK_THREADS = 1024;
+constexpr int FORK_AHEAD = 4;  // entries per lane and round of a row
 constexpr int FORK_PAGES = 2;  // pages per thread and round of the scan
 
 // Exclusive prefix sums of N values per thread over the CTA; `total` gets the sums.
-template <int N>
-__device__ __forceinline__ void block_prefix(int (&v)[N], int (*warp_sums)[FORK_THREADS / 32], int (&total)[N])
+template <int THREADS, int N>
+__device__ __forceinline__ void block_prefix(int (&v)[N], int (*warp_sums)[THREADS / 32], int (&total)[N])
 {
-    static_assert(FORK_THREADS == 1024, "a lane per warp");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x[N], before[N];
 #pragma unroll
@@ -55,7 +54,7 @@ __device__ __forceinline__ void block_prefix(int (&v)[N], int (*warp_sums)[FORK_
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < N; n++) {
-        total[n] = warp_sums[n][lane];
+        total[n] = lane < THREADS / 32 ? warp_sums[n][lane] : 0;
         before[n] = lane < warp ? total[n] : 0;
     }
 #pragma unroll
@@ -78,7 +77,8 @@ __device__ __forceinline__ void store_in_cta(int *at, int rank, int x)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 
-__global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkParams p)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) pages_fork_kernel(const ForkParams p)
 {
     extern __shared__ int fork_smem[];
     int *kids = fork_smem;               // [old_batch]
@@ -88,23 +88,23 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     int *start = parents + p.batch;      // [batch]  first missing entry
     int *offs = start + p.batch;         // [batch]  missing entries before sequence b
     int *copied = offs + p.batch;        // [batch]  page whose copy is the first missing entry, or -1
-    __shared__ int warp_sums[2][FORK_THREADS / 32], free_of[FORK_CTAS];
+    __shared__ int warp_sums[2][THREADS / 32], free_of[FORK_CTAS];
     grid_dependency_wait();
     grid_dependents_launch();
     const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.pages_per_seq;
 
     // (what the first round needs is asked for together)
-    const int page0 = rank * FORK_THREADS + tid;
+    const int page0 = rank * THREADS + tid;
     const int len0 = tid < p.old_batch ? __ldg(p.lens + tid) : 0;
     const int parent0 = tid < p.batch ? __ldg(p.parents + tid) : 0;
     const int ref0 = page0 < p.num_pages ? __ldg(p.ref + page0) : 0;
-    for (int i = tid; i < p.old_batch; i += FORK_THREADS) {
+    for (int i = tid; i < p.old_batch; i += THREADS) {
         kids[i] = 0;
         first[i] = INT_MAX;
         lens[i] = max(i == tid ? len0 : __ldg(p.lens + i), 0);
     }
-    for (int b = tid; b < p.batch; b += FORK_THREADS) {
+    for (int b = tid; b < p.batch; b += THREADS) {
         int par = b == tid ? parent0 : __ldg(p.parents + b);
         if (par >= p.old_batch) {
             na_report(p.status, NA_ERR_INVALID_ARG);
@@ -112,10 +112,10 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
         }
         parents[b] = max(par, -1);
     }
-    for (int i = page0; i < p.num_pages; i += FORK_CTAS * FORK_THREADS)
+    for (int i = page0; i < p.num_pages; i += FORK_CTAS * THREADS)
         p.new_ref[i] = i == page0 ? ref0 : __ldg(p.ref + i);
     __syncthreads();
-    for (int b = tid; b < p.batch; b += FORK_THREADS)
+    for (int b = tid; b < p.batch; b += THREADS)
         if (parents[b] >= 0) {
             atomicAdd(&kids[parents[b]], 1);
             atomicMin(&first[parents[b]], b);
@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     cluster_sync();  // (and every thread of the CTA)
 
     // Items: new rows, then old rows (of which those without a child).
-    for (int i = rank * (FORK_THREADS / 32) + warp; i < p.batch + p.old_batch;
-         i += FORK_CTAS * (FORK_THREADS / 32)) {
+    for (int i = rank * (THREADS / 32) + warp; i < p.batch + p.old_batch;
+         i += FORK_CTAS * (THREADS / 32)) {
         const bool fresh = i < p.batch;
         const int row = fresh ? parents[i] : (kids[i - p.batch] == 0 ? i - p.batch : -1);
         if (!fresh && row < 0)
@@ -138,15 +138,15 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
         int32_t *to = p.new_table + (size_t)i * P;
         int held = P, part_filled = -1;  // entry `full`, in one of the lanes
         bool end = false;
-        for (int base = 0; base < P; base += 128) {
-            int e[4];
+        for (int base = 0; base < P; base += 32 * FORK_AHEAD) {
+            int e[FORK_AHEAD];
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
+            for (int k = 0; k < FORK_AHEAD; k++) {
                 const int j = base + k * 32 + lane;
                 e[k] = row >= 0 && j < P && !end ? __ldg(from + j) : -1;
             }
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
+            for (int k = 0; k < FORK_AHEAD; k++) {
                 const int j0 = base + k * 32, j = j0 + lane;
                 if (j0 >= P)
                     break;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
 
     // Missing pages before each sequence's, in every CTA, and free pages in order: a CTA's run of
     // pages, counted, then ranked behind the runs before.
-    constexpr int ROUND = FORK_THREADS * FORK_PAGES;
+    constexpr int ROUND = THREADS * FORK_PAGES;
     const int run = (p.num_pages + FORK_CTAS - 1) / FORK_CTAS;
     const int p0 = min(rank * run, p.num_pages), p1 = min(p0 + run, p.num_pages);
     auto free_at = [&](int at) {  // which of FORK_PAGES pages are free
@@ -216,10 +216,10 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
     for (int at = p0 + ROUND + FORK_PAGES * tid; at < p1; at += ROUND)
         count += __popc(free_at(at));
     int missing = 0, total = 0;
-    for (int base = 0; base < p.batch; base += FORK_THREADS) {
+    for (int base = 0; base < p.batch; base += THREADS) {
         const int b = base + tid;
         int v[2] = {b < p.batch ? offs[b] : 0, base == 0 ? count : 0}, sum[2];
-        block_prefix(v, warp_sums, sum);
+        block_prefix<THREADS>(v, warp_sums, sum);
         if (b < p.batch)
             offs[b] = missing + v[0];
         missing += sum[0];
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkPara
         const int at = base + FORK_PAGES * tid;
         const unsigned free = base == p0 ? free0 : free_at(at);
         int v[1] = {__popc(free)}, sum[1];
-        block_prefix(v, warp_sums, sum);
+        block_prefix<THREADS>(v, warp_sums, sum);
         int k = found + v[0];
         found += sum[0];
         if (!free || k >= missing)
@@ -692,18 +692,33 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
 
 }  // namespace
 
-cudaError_t launch_pages_fork(const ForkParams &p, cudaStream_t stream)
+namespace {
+
+template <int THREADS>
+cudaError_t launch_fork_t(const ForkParams &p, cudaStream_t stream)
 {
     const size_t smem = (3 * (size_t)p.old_batch + 4 * (size_t)p.batch) * sizeof(int);
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = once_per_device(configured, [] {
-        return cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(pages_fork_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     7 * kMaxForkBatch * (int)sizeof(int));
     });
     if (e != cudaSuccess)
         return e;
-    return launch_kernel_cluster(pages_fork_kernel, dim3(FORK_CTAS), dim3(FORK_THREADS), smem, FORK_CTAS,
+    return launch_kernel_cluster(pages_fork_kernel<THREADS>, dim3(FORK_CTAS), dim3(THREADS), smem, FORK_CTAS,
                                  stream, p);
+}
+
+}  // namespace
+
+// A warp per row, new or old, as far as a CTA has them: fewer threads meet faster (32 sequences:
+// 8.2 us by 1024 threads, 6.8 by 256), more rows at a time are worth that (256: 10.7 and 14.7).
+cudaError_t launch_pages_fork(const ForkParams &p, cudaStream_t stream)
+{
+    const int warps = (p.batch + p.old_batch + FORK_CTAS - 1) / FORK_CTAS;
+    return warps <= 8    ? launch_fork_t<256>(p, stream)
+           : warps <= 16 ? launch_fork_t<512>(p, stream)
+                         : launch_fork_t<1024>(p, stream);
 }
 
 cudaError_t launch_pages_copy(const PageCopyParams &p, cudaStream_t stream)
