@@ -39,6 +39,7 @@ struct ExpandedParams {
     int total_tokens, total_keys, max_new_len, max_key_len;
     int tall;                  // units of 256 rows, else of 128
     int units;                 // of all sequences, with the longest one's tiles each
+    int sms, in_turn;          // tall: CTAs that run at a time, and whether each takes units in turn
     int cut_units, pieces;     // tall: the last units, cut into pieces of their keys (a cluster each)
     const int32_t *cu_seqlens, *key_starts, *key_lens;
     const bf16 *q, *kv, *k_pe;

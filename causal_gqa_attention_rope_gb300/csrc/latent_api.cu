@@ -98,6 +98,10 @@ LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int m
 //   - Batches of equal lengths: the units left over after the last whole wave of SMs, in a launch of
 //     their own, which from 4096 keys on gains more than it costs (2048 tokens after 16384, 40
 //     heads: 746 us uncut, 625; after 1024: 109 and 128).
+//   - Where all units have about as many keys, CTAs take them in turn, the next one's beginning beside
+//     the end of the last (4 prompts of 1024 tokens after 16384, 40 heads: 1167 us by a CTA
+//     per unit, 1082; 8 of 256 after 4096: 183 and 179); where they differ more the hardware's order,
+//     a CTA for each, balances them better (8 prompts of 100 .. 1000 after 1536, 8 heads: 78 and 91).
 //   - Below 1024 keys a row on average the 128-row units are faster (1024 tokens of one prompt, 8
 //     heads: 16.3 us against 19.2; 16 prompts of 1 .. 512 tokens, 32 heads: 86 against
 //     107 in tiles of 128 keys), and so they are for sequences of few tokens, whose tall units are mostly empty (64 of
@@ -129,6 +133,8 @@ int plan_expanded(ExpandedParams &p)
         cut = pieces > 1 ? rest : 0;
     }
     p.units = (int)(p.tall ? tall_units : short_units);
+    p.sms = sms;
+    p.in_turn = equal && 2ll * p.max_new_len <= keys;
     p.pieces = pieces;
     p.cut_units = cut;
     return NA_OK;

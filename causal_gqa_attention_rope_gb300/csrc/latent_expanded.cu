@@ -25,8 +25,9 @@
 // A unit can be cut into pieces of its keys: the CTAs of a cluster take one each and join their rows
 // out of one another's shared memory.  That fills the SMs where units are few, and the last wave:
 // 2048 tokens after 28672, 40 heads, are 320 units on 152 SMs: 1033 us, 962 with the last 16 in six
-// pieces (1619 TFLOP/s).
+// pieces, 948 with the others in turn (1640 TFLOP/s).
 //
+#include <algorithm>
 #include <climits>
 
 #include "latent.cuh"
@@ -52,7 +53,7 @@ struct Unit {
 // Units run with the last query tiles, which see most keys, first; up to 32 sequences in order
 // of decreasing keys, so that the longest units start first.
 template <int UR>
-__device__ __forceinline__ Unit find_unit(const ExpandedParams &p, int index, int lane)
+__device__ __forceinline__ Unit find_unit(const ExpandedParams &p, int index, int lane, bool reporter)
 {
     Unit u;
     const int units = (p.max_new_len + UR - 1) / UR;  // of a sequence and head
@@ -78,13 +79,13 @@ __device__ __forceinline__ Unit find_unit(const ExpandedParams &p, int index, in
     u.run = false;
     if (u.n > p.max_new_len || u.tok0 < 0 || (b == 0 && u.tok0 != 0) ||
         (long long)u.tok0 + u.n > p.total_tokens) {
-        if (u.r0 == 0 && u.head == 0 && threadIdx.x == 0)
+        if (u.r0 == 0 && u.head == 0 && reporter)
             na_report(p.status, NA_ERR_INVALID_ARG);
     } else if (u.rows <= 0) {
         // padding: the sequence has fewer tiles
     } else if (keys < 0 || u.start < 0 || keys > p.max_key_len ||
                (long long)u.start + keys > p.total_keys) {
-        if (threadIdx.x == 0)
+        if (reporter)
             na_report(p.status, NA_ERR_CAPACITY);
     } else {
         u.run = true;
@@ -100,10 +101,10 @@ __device__ __forceinline__ bf16 *rows_out(const ExpandedParams &p, const Unit &u
 
 // Rows that see no key.
 template <int DV>
-__device__ __forceinline__ void store_zeros(const ExpandedParams &p, const Unit &u)
+__device__ __forceinline__ void store_zeros(const ExpandedParams &p, const Unit &u, int tid, int threads)
 {
     bf16 *out = rows_out<DV>(p, u);
-    for (int i = threadIdx.x; i < u.rows * (DV / 8); i += blockDim.x)
+    for (int i = tid; i < u.rows * (DV / 8); i += threads)
         *reinterpret_cast<uint4 *>(out + (size_t)(i / (DV / 8)) * p.H * DV + i % (DV / 8) * 8) =
             make_uint4(0, 0, 0, 0);
 }
@@ -307,11 +308,11 @@ __global__ void __launch_bounds__(two::THREADS, 2)
     grid_dependency_wait();
     grid_dependents_launch();
 
-    const Unit u = find_unit<BM>(p, blockIdx.x, lane);
+    const Unit u = find_unit<BM>(p, blockIdx.x, lane, threadIdx.x == 0);
     if (!u.run)
         return;
     if (u.k_end <= 0) {
-        store_zeros<DV>(p, u);
+        store_zeros<DV>(p, u, threadIdx.x, THREADS);
         return;
     }
     const int n_tiles = (u.k_end + BN - 1) / BN;
@@ -503,7 +504,11 @@ __global__ void __launch_bounds__(two::THREADS, 2)
 
 // ---------------------------------------------------- 256 rows, in pieces of their keys --
 //
-// Warps: 0 .. 7 softmax, a row of the two tiles per thread, 8 producer, 9 issues all products.
+// Warps: 0 .. 7 softmax, a row of the two tiles per thread, 8 producer, 9 issues all products, 10
+// finds the next units.  Where plan_expanded() lets a CTA take units in turn, the roles go on to the
+// next as soon as they are done with one: its keys and queries are on their way while the
+// last products run, and its first scores are behind them while the rows are stored (2048 tokens
+// after 4096, 40 heads: 216 us by a CTA per unit, 191).
 
 namespace tall {
 constexpr int THREADS = 384;
@@ -524,8 +529,10 @@ struct __align__(1024) TallSmem {
     static constexpr int SLOTS = 14 - tall::TILES * QB;
     bf16 q[tall::TILES][QB][BM * 64];
     bf16 ring[SLOTS][tall::BN * 64];
-    uint64_t q_full[tall::TILES], full[SLOTS], empty[SLOTS];
-    uint64_t s_full[tall::TILES], p_full[tall::TILES], o_done, drain;
+    uint64_t q_full[tall::TILES], q_empty[tall::TILES], full[SLOTS], empty[SLOTS];
+    uint64_t s_full[tall::TILES], p_full[tall::TILES], o_done[tall::TILES], o_empty[tall::TILES], drain;
+    uint64_t unit_full[2], unit_empty[2];
+    Unit unit[2];              // the next ones, handed to all roles; rows 0: no more
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -628,10 +635,19 @@ __device__ __forceinline__ void join_rows(const ExpandedParams &p, const Unit &u
     }
 }
 
+// Units are handed out in rounds of one per CTA, every other round in reverse, since they come in
+// order of decreasing keys.
+__device__ __forceinline__ int unit_of_round(int round)
+{
+    const int at = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    return round * gridDim.x + at;
+}
+
 template <int DN, int DV>
 __global__ void __launch_bounds__(tall::THREADS, 1)
     latent_expanded_tall_kernel(const __grid_constant__ ExpandedParams p, const int first_unit,
-                                const int pieces, const __grid_constant__ CUtensorMap map_q,
+                                const int units, const int pieces,
+                                const __grid_constant__ CUtensorMap map_q,
                                 const __grid_constant__ CUtensorMap map_kv,
                                 const __grid_constant__ CUtensorMap map_pe)
 {
@@ -642,42 +658,59 @@ __global__ void __launch_bounds__(tall::THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 8 * 32) {  // (the producer)
         tc::prefetch_tmap(&map_q);
         tc::prefetch_tmap(&map_kv);
         tc::prefetch_tmap(&map_pe);
         for (int t = 0; t < TILES; t++) {
             mbar_init(&sm.q_full[t], 1);
+            mbar_init(&sm.q_empty[t], 1);
             mbar_init(&sm.s_full[t], 1);
             mbar_init(&sm.p_full[t], 4);
+            mbar_init(&sm.o_done[t], 1);
+            mbar_init(&sm.o_empty[t], 4);
         }
         for (int i = 0; i < SLOTS; i++) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
-        mbar_init(&sm.o_done, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sm.unit_full[i], 1);
+            mbar_init(&sm.unit_empty[i], 10);  // the producer, the issuer and the softmax warps
+        }
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
         fence_barrier_init();
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    const Unit u = find_unit<UR>(p, first_unit + blockIdx.x / pieces, lane);
-    const int piece = blockIdx.x % pieces;
-    if (!u.run)  // (all CTAs of a cluster)
+    const int piece = blockIdx.x % pieces;  // (with pieces a CTA has one unit)
+    auto index_of = [&](int round) { return pieces > 1 ? blockIdx.x / pieces : unit_of_round(round); };
+    const bool single = pieces > 1 || units <= (int)gridDim.x;  // the CTA has no other unit
+    const Unit found = find_unit<UR>(p, first_unit + index_of(0), lane, threadIdx.x == 0);
+    const bool begun = found.run && found.k_end > 0;
+    if (found.run && !begun && piece == 0)
+        store_zeros<DV>(p, found, threadIdx.x, THREADS);
+    if (single && !begun)  // (all CTAs of a cluster)
         return;
-    if (u.k_end <= 0) {
-        if (piece == 0)
-            store_zeros<DV>(p, u);
-        return;
-    }
-    const int all_tiles = (u.k_end + BN - 1) / BN;
-    const int first = (int)((long long)all_tiles * piece / pieces);
-    const int n_tiles = (int)((long long)all_tiles * (piece + 1) / pieces) - first;  // may be 0
-    const int n_items = n_tiles * PER, qt = u.rows > BM ? 2 : 1;
-    auto load = [&](int item) {
+
+    // What a piece has of a unit.
+    struct Span {
+        int first, tiles;  // key tiles; there may be none
+        int qt;            // query tiles
+        __device__ __forceinline__ Span(const Unit &u, int piece, int pieces)
+        {
+            const int all = (u.k_end + BN - 1) / BN;
+            first = (int)((long long)all * piece / pieces);
+            tiles = (int)((long long)all * (piece + 1) / pieces) - first;
+            qt = u.rows > BM ? 2 : 1;
+        }
+    };
+
+    // Column block i of a unit's keys, Q behind the first keys: `item` of the ring.
+    auto load_block = [&](const Unit &u, const Span &sp, int i, int item) {
         const At at(item);
-        const int j = item / PER, c = item % PER, y = u.start + (first + j) * BN;
+        const int c = i % PER, y = u.start + (sp.first + i / PER) * BN;
         uint64_t *bar = &sm.full[at.slot];
         mbar_arrive_expect_tx(bar, BLOCK);
         if (c < QB - 1) {
@@ -685,51 +718,124 @@ __global__ void __launch_bounds__(tall::THREADS, 1)
         } else if (c == QB - 1) {
             tc::tma_load_2d(sm.ring[at.slot], &map_pe, 0, y, bar);
         } else {
-            // V's blocks at ascending places: where the ring ends between them the first
-            // slot takes the first dims
+            // V's blocks at ascending places: where the ring ends between them the first slot
+            // takes the first dims
             const bool swapped = VB == 2 && (item - (c - QB)) % SLOTS == SLOTS - 1;
-            tc::tma_load_3d(sm.ring[at.slot], &map_kv, DN + (swapped ? 1 - (c - QB) : c - QB) * 64,
-                            u.head, y, bar);
+            tc::tma_load_3d(sm.ring[at.slot], &map_kv, DN + (swapped ? 1 - (c - QB) : c - QB) * 64, u.head,
+                            y, bar);
         }
     };
-    const int pre = min(n_items, SLOTS);
-    if (threadIdx.x == 0 && n_tiles > 0) {  // (fresh slots need no wait)
-        for (int t = 0; t < qt; t++) {
-            mbar_arrive_expect_tx(&sm.q_full[t], QB * Q_BLOCK);
-            for (int c = 0; c < QB; c++)
-                tc::tma_load_3d(sm.q[t][c], &map_q, c * 64, u.head, u.tok0 + u.r0 + t * BM, &sm.q_full[t]);
-            if (t == 0)
-                for (int i = 0; i < pre; i++)
-                    load(i);
+    auto load_q = [&](const Unit &u, int t) {
+        mbar_arrive_expect_tx(&sm.q_full[t], QB * Q_BLOCK);
+        for (int c = 0; c < QB; c++)
+            tc::tma_load_3d(sm.q[t][c], &map_q, c * 64, u.head, u.tok0 + u.r0 + t * BM, &sm.q_full[t]);
+    };
+    // The first unit's: fresh slots need no wait.
+    const Span sp0(found, piece, pieces);
+    const int early = begun ? min(sp0.tiles * PER, SLOTS) : 0;
+    if (threadIdx.x == 8 * 32)
+        for (int i = 0; i < early; i++) {
+            if (i == QB)
+                for (int t = 0; t < sp0.qt; t++)
+                    load_q(found, t);
+            load_block(found, sp0, i, i);
         }
-    }
     if (warp == 9)
         tc::tmem_alloc(&sm.tmem_base, TMEM_COLS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
+    // The CTA's k-th unit: the one found first, then those handed out, if `wait` says they are there.
+    // `ok` falls with a wait that gave up; false when there is no other.
+    auto next_unit = [&](int k, Unit &u, bool &ok, auto &&wait, bool arrive) {
+        if (begun && k == 0) {
+            u = found;
+            return true;
+        }
+        if (single)
+            return false;
+        const int h = k - begun;
+        ok = wait(&sm.unit_full[h & 1], (h >> 1) & 1);
+        if (!ok)
+            return false;
+        u = sm.unit[h & 1];
+        if (arrive)
+            mbar_arrive(&sm.unit_empty[h & 1]);
+        return u.rows > 0;
+    };
+    auto bounded = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); };
 
     static_assert(sizeof(float) * UR * (DV + 4) <= sizeof(sm.q) + sizeof(sm.ring),
-                  "the rows are staged over Q, K and V, idle by then");
+                  "the rows of a piece are staged over Q, K and V, idle by then");
     float *stage = reinterpret_cast<float *>(&sm.q[0]);
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ producer --
-        if (lane == 0 && n_tiles > 0) {
-            int issued = pre;
-            for (; issued < n_items; issued++) {
-                const At at(issued);
-                if (!mbar_wait_bounded(&sm.empty[at.slot], at.parity ^ 1) || aborted(&sm.abort_flag)) {
-                    set_abort(&sm.abort_flag, p.status);
-                    break;
-                }
-                load(issued);
+    if (warp == 10 && !single) {
+        // --------------------------------------------------------------- units --
+        int handed = 0;
+        bool ok = true;
+        auto hand = [&](const Unit &u) {
+            const int i = handed & 1;
+            ok = warp_wait(&sm.unit_empty[i], ((handed >> 1) & 1) ^ 1, &sm.abort_flag);
+            if (ok && lane == 0) {
+                sm.unit[i] = u;
+                mbar_arrive(&sm.unit_full[i]);
             }
+            handed++;
+        };
+        for (int round = 1; ok && round * (int)gridDim.x < units; round++) {
+            const int index = index_of(round);
+            if (index >= units)
+                continue;
+            const Unit u = find_unit<UR>(p, first_unit + index, lane, lane == 0);
+            if (!u.run)
+                continue;
+            if (u.k_end <= 0) {
+                store_zeros<DV>(p, u, lane, 32);
+                continue;
+            }
+            hand(u);
+        }
+        Unit none{};
+        if (ok)
+            hand(none);
+        if (!ok && lane == 0)
+            set_abort(&sm.abort_flag, p.status);
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ producer --
+        if (lane == 0) {
+            // loaded so far: column blocks, and Q of the two tiles
+            int item = early, queries[2] = {early > 0, early > 0 && sp0.qt > 1};
+            bool ok = true;
+            Unit u;
+            for (int n = 0; ok && next_unit(n, u, ok, bounded, true); n++) {
+                const Span sp(u, piece, pieces);
+                for (int i = n == 0 ? early : 0; ok && i < sp.tiles * PER; i++, item++) {
+                    if (i == QB)
+#pragma unroll
+                        for (int t = 0; t < TILES; t++)
+                            if (t < sp.qt && ok) {
+                                ok = mbar_wait_bounded(&sm.q_empty[t], (queries[t] & 1) ^ 1) &&
+                                     !aborted(&sm.abort_flag);
+                                if (ok) {
+                                    load_q(u, t);
+                                    queries[t]++;
+                                }
+                            }
+                    const At at(item);
+                    ok = ok && mbar_wait_bounded(&sm.empty[at.slot], at.parity ^ 1) && !aborted(&sm.abort_flag);
+                    if (!ok)
+                        break;
+                    load_block(u, sp, i, item);
+                }
+            }
+            if (!ok)
+                set_abort(&sm.abort_flag, p.status);
             // every copy issued lands before the CTA can exit
-            for (int t = 0; t < qt; t++)
-                drain_wait(&sm.q_full[t], 0, p.status);
-            for (int i = max(issued - SLOTS, 0); i < issued; i++)
+            for (int t = 0; t < TILES; t++)
+                if (queries[t] > 0)
+                    drain_wait(&sm.q_full[t], (queries[t] - 1) & 1, p.status);
+            for (int i = max(item - SLOTS, 0); i < item; i++)
                 drain_wait(&sm.full[At(i).slot], At(i).parity, p.status);
         }
     } else if (warp == 9) {
@@ -737,125 +843,189 @@ __global__ void __launch_bounds__(tall::THREADS, 1)
         // One thread issues all products, and the tensor cores take them in that order: S of a
         // tile is written over weights that the product before it has read, and what S's
         // commit tells is also true of that product.
-        if (elect_one() && n_tiles > 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN, false, false);
             constexpr uint32_t idesc_o = tc::idesc_bf16_f32(BM, DV, false, true);
             constexpr uint32_t B16 = BLOCK >> 4;
             const uint64_t qd0 = tc::desc_kmajor_sw128(smem_addr(sm.q[0][0]));
             const uint64_t kd0 = tc::desc_kmajor_sw128(smem_addr(sm.ring[0]));
-            bool ok = true;
-            auto scores = [&](int j, int t) {
-                const uint64_t qd = qd0 + (uint64_t)(t * QB * B16);
+            bool ok = true, issued = false;
+            int base = 0;                        // the unit's first column block in the ring
+            int had[2] = {0, 0}, weighed[2] = {0, 0};  // by query tile: units, and products with V
+            Unit u;
+            for (int n = 0; ok && next_unit(n, u, ok, bounded, true); n++) {
+                const Span sp(u, piece, pieces);
+                auto scores = [&](int j, int t) {
+                    const uint64_t qd = qd0 + (uint64_t)(t * QB * B16);
+                    if (j == 0)
+                        ok = ok && mbar_wait_bounded(&sm.q_full[t], had[t] & 1);
 #pragma unroll
-                for (int c = 0; c < QB; c++) {
-                    const At at(j * PER + c);
-                    if (t == 0)
-                        ok = ok && mbar_wait_bounded(&sm.full[at.slot], at.parity);
-                    if (!ok)
-                        return;
-                    if (t == 0)
-                        tc::fence_after_sync();
-                    const uint64_t kd = kd0 + (uint64_t)(at.slot * B16);
+                    for (int c = 0; c < QB; c++) {
+                        const At at(base + j * PER + c);
+                        if (t == 0)
+                            ok = ok && mbar_wait_bounded(&sm.full[at.slot], at.parity);
+                        if (!ok)
+                            return;
+                        if (t == 0 || c == 0)
+                            tc::fence_after_sync();
+                        const uint64_t kd = kd0 + (uint64_t)(at.slot * B16);
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        tc::mma_ss(tmem + t * BN, qd + c * B16 + k * 2, kd + k * 2, idesc_s, c > 0 || k > 0);
-                }
-                tc::mma_commit(&sm.s_full[t]);
-                if (t == qt - 1)
-                    for (int c = 0; c < QB; c++)
-                        tc::mma_commit(&sm.empty[At(j * PER + c).slot]);
-            };
-            for (int t = 0; t < qt && ok; t++) {
-                ok = mbar_wait_bounded(&sm.q_full[t], 0);
-                if (ok)
+                        for (int i = 0; i < 4; i++)
+                            tc::mma_ss(tmem + t * BN, qd + c * B16 + i * 2, kd + i * 2, idesc_s,
+                                       c > 0 || i > 0);
+                    }
+                    issued = true;
+                    tc::mma_commit(&sm.s_full[t]);
+                    if (t == sp.qt - 1)
+                        for (int c = 0; c < QB; c++)
+                            tc::mma_commit(&sm.empty[At(base + j * PER + c).slot]);
+                    if (j == sp.tiles - 1)
+                        tc::mma_commit(&sm.q_empty[t]);
+                };
+                for (int t = 0; t < sp.qt && sp.tiles > 0; t++)
                     scores(0, t);
-            }
-            for (int j = 0; j < n_tiles && ok; j++) {
-                const At v0(j * PER + QB), v1(j * PER + PER - 1);
-                const int lo = min(v0.slot, v1.slot), hi = max(v0.slot, v1.slot);
-                const uint64_t vd = tc::desc_mnmajor_sw128(smem_addr(sm.ring[lo]), (hi - lo) * BLOCK);
-                for (int t = 0; t < qt && ok; t++) {
-                    ok = mbar_wait_bounded(&sm.p_full[t], j & 1) &&
-                         mbar_wait_bounded(&sm.full[v0.slot], v0.parity) &&
-                         mbar_wait_bounded(&sm.full[v1.slot], v1.parity) && !aborted(&sm.abort_flag);
-                    if (!ok)
-                        break;
-                    tc::fence_after_sync();
+                for (int j = 0; j < sp.tiles && ok; j++) {
+                    const At v0(base + j * PER + QB), v1(base + j * PER + PER - 1);
+                    const int lo = min(v0.slot, v1.slot), hi = max(v0.slot, v1.slot);
+                    const uint64_t vd = tc::desc_mnmajor_sw128(smem_addr(sm.ring[lo]), (hi - lo) * BLOCK);
 #pragma unroll
-                    for (int k = 0; k < BN / 16; k++)  // 16 keys = 16 rows of 128 B per step
-                        tc::mma_ts(tmem + O_COL0 + t * DV, tmem + t * BN + k * 8, vd + (uint64_t)(k * 128),
-                                   idesc_o, j > 0 || k > 0);
-                    if (t == qt - 1)
-                        for (int c = 0; c < VB; c++)
-                            tc::mma_commit(&sm.empty[At(j * PER + QB + c).slot]);
-                    if (j + 1 < n_tiles)
-                        scores(j + 1, t);
+                    for (int t = 0; t < TILES; t++) {
+                        if (t >= sp.qt || !ok)
+                            break;
+                        ok = mbar_wait_bounded(&sm.p_full[t], weighed[t]++ & 1) &&
+                             mbar_wait_bounded(&sm.full[v0.slot], v0.parity) &&
+                             mbar_wait_bounded(&sm.full[v1.slot], v1.parity);
+                        if (ok && j == 0 && had[t] > 0)  // the last unit's rows are out of O
+                            ok = mbar_wait_bounded(&sm.o_empty[t], (had[t] - 1) & 1);
+                        if (!ok || aborted(&sm.abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int i = 0; i < BN / 16; i++)  // 16 keys = 16 rows of 128 B per step
+                            tc::mma_ts(tmem + O_COL0 + t * DV, tmem + t * BN + i * 8,
+                                       vd + (uint64_t)(i * 128), idesc_o, j > 0 || i > 0);
+                        if (t == sp.qt - 1)
+                            for (int c = 0; c < VB; c++)
+                                tc::mma_commit(&sm.empty[At(base + j * PER + QB + c).slot]);
+                        if (j + 1 < sp.tiles)
+                            scores(j + 1, t);
+                        else
+                            tc::mma_commit(&sm.o_done[t]);
+                    }
                 }
+                base += sp.tiles * PER;
+                if (sp.tiles > 0)
+#pragma unroll
+                    for (int t = 0; t < TILES; t++)
+                        had[t] += t < sp.qt;
             }
             if (!ok)
                 set_abort(&sm.abort_flag, p.status);
-            else
-                tc::mma_commit(&sm.o_done);
-            // all issued MMAs complete before tensor memory is released
-            tc::mma_commit(&sm.drain);
-            drain_wait(&sm.drain, 0, p.status);
+            if (issued) {  // all issued MMAs complete before tensor memory is released
+                tc::mma_commit(&sm.drain);
+                drain_wait(&sm.drain, 0, p.status);
+            }
         }
     } else if (warp < 8) {
         // -------------------------------------------------------------- softmax --
         const int t = warp / 4, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16, o_t = tmem + O_COL0 + t * DV + lane_off;
-        const int pos_lo = u.pos_lo + t * BM, k_end = min(u.k_end, pos_lo + BM);
-        RowState st;
         bool ok = true;
-        if (t < qt) {
-            for (int j = 0; ok && j < n_tiles; j++) {
-                const int j0 = (first + j) * BN;
-                if (!(ok = warp_wait(&sm.s_full[t], j & 1, &sm.abort_flag)))
-                    break;
-                tc::fence_after_sync();
-                float alpha;
-                const bool corr = weigh_tile<BN / 32>(tmem + t * BN + lane_off, j0, pos_lo, pos_lo + r,
-                                                      k_end, p.scale_log2, st, alpha);
-                if (t == 0 && j0 + BN > u.k_end) {  // rows behind the last visible key may hold any bits
-                    for (int c = 0; c < VB; c++) {
-                        const At at(j * PER + QB + c);
-                        ok = ok && warp_wait(&sm.full[at.slot], at.parity, &sm.abort_flag);
-                        if (ok && r >= u.k_end - j0)
-                            zero_row(sm.ring[at.slot], r);
-                    }
-                    if (!ok)
+        int base = 0, had = 0, weighed = 0;  // as the issuing thread counts them
+        auto by_warp = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, &sm.abort_flag); };
+        Unit u;
+        for (int n = 0; ok && next_unit(n, u, ok, by_warp, false); n++) {
+            __syncwarp();
+            if (lane == 0 && n >= begun)
+                mbar_arrive(&sm.unit_empty[(n - begun) & 1]);
+            const Span sp(u, piece, pieces);
+            if (t < sp.qt) {
+                const int pos_lo = u.pos_lo + t * BM, k_end = min(u.k_end, pos_lo + BM);
+                RowState st;
+                for (int j = 0; ok && j < sp.tiles; j++) {
+                    const int j0 = (sp.first + j) * BN;
+                    if (!(ok = warp_wait(&sm.s_full[t], weighed++ & 1, &sm.abort_flag)))
                         break;
-                    tc::fence_proxy_async_smem();
+                    tc::fence_after_sync();
+                    float alpha;
+                    const bool corr = weigh_tile<BN / 32>(tmem + t * BN + lane_off, j0, pos_lo, pos_lo + r,
+                                                          k_end, p.scale_log2, st, alpha);
+                    if (t == 0 && j0 + BN > u.k_end) {  // rows behind the last visible key may hold any bits
+                        for (int c = 0; c < VB; c++) {
+                            const At at(base + j * PER + QB + c);
+                            ok = ok && warp_wait(&sm.full[at.slot], at.parity, &sm.abort_flag);
+                            if (ok && r >= u.k_end - j0)
+                                zero_row(sm.ring[at.slot], r);
+                        }
+                        if (!ok)
+                            break;
+                        tc::fence_proxy_async_smem();
+                    }
+                    if (__any_sync(0xffffffffu, corr))  // (O holds all of the tiles before)
+                        rescale_rows<DV>(o_t, corr ? alpha : 1.f);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.p_full[t]);
                 }
-                if (__any_sync(0xffffffffu, corr))  // (O holds all of the tiles before)
-                    rescale_rows<DV>(o_t, corr ? alpha : 1.f);
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sm.p_full[t]);
+                if (pieces == 1) {
+                    if (!ok || !(ok = warp_wait(&sm.o_done[t], had & 1, &sm.abort_flag)))
+                        break;
+                    tc::fence_after_sync();
+                    uint32_t o[DV / 32][32];
+#pragma unroll
+                    for (int c = 0; c < DV / 32; c++)
+                        tc::tmem_ld32(o_t + c * 32, o[c]);
+                    tc::tmem_wait_ld();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.o_empty[t]);
+                    if (t * BM + r < u.rows) {
+                        const float inv = st.l > 0.f ? 1.0f / st.l : 0.f;
+                        uint4 *row = reinterpret_cast<uint4 *>(rows_out<DV>(p, u) + (size_t)(t * BM + r) * p.H * DV);
+#pragma unroll
+                        for (int c = 0; c < DV / 8; c++) {
+                            const uint32_t *x = &o[c / 4][c % 4 * 8];
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; i++)
+                                w[i] = pack_bf16x2(__uint_as_float(x[2 * i]) * inv,
+                                                   __uint_as_float(x[2 * i + 1]) * inv);
+                            row[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                } else {
+                    // the row unnormalised, its maximum and sum in the padding
+                    float *rows = stage + t * BM * (DV + 4);
+                    if (sp.tiles == 0) {
+                        for (int c = 0; c < DV; c += 4)
+                            *reinterpret_cast<float4 *>(rows + r * (DV + 4) + c) =
+                                make_float4(0.f, 0.f, 0.f, 0.f);
+                    } else {
+                        for (int i = 0; i < sp.qt; i++)  // all products are done with what lies there
+                            ok = ok && warp_wait(&sm.o_done[i], 0, &sm.abort_flag);
+                        if (!ok)
+                            break;
+                        tc::fence_after_sync();
+                        stage_row<DV>(o_t, 1.f, rows, r);
+                    }
+                    *reinterpret_cast<float2 *>(rows + r * (DV + 4) + DV) = make_float2(st.m_ref, st.l);
+                }
+                had++;
             }
-            float *row = stage + t * BM * (DV + 4);
-            if (n_tiles == 0) {
-                for (int c = 0; c < DV; c += 4)
-                    *reinterpret_cast<float4 *>(row + r * (DV + 4) + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-            } else if (ok && warp_wait(&sm.o_done, 0, &sm.abort_flag)) {
-                tc::fence_after_sync();
-                stage_row<DV>(o_t, pieces > 1 ? 1.f : (st.l > 0.f ? 1.0f / st.l : 0.f), row, r);
-            } else if (lane == 0) {
-                set_abort(&sm.abort_flag, p.status);
-            }
-            if (pieces > 1)  // (the row's padding has its maximum and sum)
-                *reinterpret_cast<float2 *>(row + r * (DV + 4) + DV) = make_float2(st.m_ref, st.l);
+            base += sp.tiles * PER;
         }
+        if (!ok && lane == 0)
+            set_abort(&sm.abort_flag, p.status);
     }
     tc::fence_before_sync();
-    __syncthreads();  // the staged rows are complete (unless a wait gave up)
-    if (pieces == 1) {
-        if (!aborted(&sm.abort_flag))
-            store_rows<DV>(p, u, stage, warp, lane);
-    } else {
+    __syncthreads();
+    if (pieces > 1) {
         cluster_sync();
-        join_rows<DV>(p, u, stage, &sm.abort_flag, piece, pieces, warp, lane);
+        join_rows<DV>(p, found, stage, &sm.abort_flag, piece, pieces, warp, lane);
         cluster_sync();  // until then the other CTAs read this one's rows
     }
     if (warp == 9) {
@@ -928,14 +1098,15 @@ cudaError_t launch_tall_t(const ExpandedParams &p, cudaStream_t stream)
         return e;
     const int whole = p.units - p.cut_units;
     if (whole > 0) {
-        e = launch_kernel(latent_expanded_tall_kernel<DN, DV>, dim3((unsigned)whole), dim3(THREADS), smem,
-                          stream, p, 0, 1, mq, mkv, mpe);
+        e = launch_kernel(latent_expanded_tall_kernel<DN, DV>, dim3((unsigned)(p.in_turn ? std::min(whole, p.sms) : whole)),
+                          dim3(THREADS), smem, stream, p, 0, whole, 1, mq, mkv, mpe);
         if (e != cudaSuccess)
             return e;
     }
     if (p.cut_units > 0)
         e = launch_kernel_cluster(latent_expanded_tall_kernel<DN, DV>, dim3((unsigned)(p.cut_units * p.pieces)),
-                                  dim3(THREADS), smem, p.pieces, stream, p, whole, p.pieces, mq, mkv, mpe);
+                                  dim3(THREADS), smem, p.pieces, stream, p, whole, p.cut_units, p.pieces, mq, mkv,
+                                  mpe);
     return e;
 }
 
