@@ -19,7 +19,7 @@ struct LatentParams {
     int H, R, rd, batch, capacity;
     float scale_log2;          // score scale * log2(e)
     int total_tokens, max_new_len, max_total_len;
-    int unit_rows;             // 32, 64 or 128
+    int unit_rows;             // 32, 64 or 128 (R > 128)
     int grid;                  // CTAs (pairs of them for 128 rows), each with an equal run of key tiles
     int cut_by_sequence;       // one unit a sequence: cut[b], else by run
     int pieces;                // > 0: no runs; `grid` units (of all sequences, with the longest
@@ -49,10 +49,10 @@ struct ExpandedParams {
 };
 
 // Query rows (token, head) of a unit: enough for those of any sequence, 128 (64 in each of a
-// pair of CTAs) at most.
-inline int latent_unit_rows(long long most_rows)
+// pair of CTAs) at most, 64 with 128 latent numbers, which pairs do not split.
+inline int latent_unit_rows(long long most_rows, int kv_rank)
 {
-    return most_rows <= 32 ? 32 : (most_rows <= 64 ? 64 : 128);
+    return most_rows <= 32 ? 32 : (most_rows <= 64 || kv_rank == 128 ? 64 : 128);
 }
 constexpr int kLatentKeys = 64;  // keys of a tile
 constexpr int kLatentMaxPieces = 8;  // CTAs of a cluster

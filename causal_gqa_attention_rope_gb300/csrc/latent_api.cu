@@ -66,7 +66,7 @@ LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int m
 {
     LatentPlan pl{};
     const long long rows = (long long)max_new_len * c->num_heads;
-    pl.unit_rows = latent_unit_rows(rows);
+    pl.unit_rows = latent_unit_rows(rows, c->kv_rank);
     const double tiles = (double)batch * ceil_div(rows, pl.unit_rows) * ceil_div(max_total_len, kLatentKeys);
     const int most = pl.unit_rows > 64 ? std::max(sm_count() / 2, 1) : sm_count();
     pl.grid = (int)std::max(1.0, std::min((double)most, tiles));

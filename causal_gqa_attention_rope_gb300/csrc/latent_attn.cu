@@ -34,10 +34,9 @@
 // beginning, no second pass, and the sequence's first pages asked for beside its lengths.
 //
 // Sequences of more than 64 rows (chunks, drafted tokens, many heads) take units of 128 rows in
-// pairs of CTAs: latent_pair.cu.  With 128 latent numbers, which that kernel does not split, each CTA
-// of a pair has 64 rows here, one reads the even column blocks of a tile, the other the odd ones,
-// both by TMA multicast into both, so that a tile comes from L2 once for 128 rows.  A slot of
-// a ring is free when the products of both CTAs are done with it.
+// pairs of CTAs: latent_pair.cu.  With 128 latent numbers, which that kernel does not split, they
+// take units of 64 rows here, each of which loads its tiles, from L2 where another has had them (64
+// sequences of 512 .. 8192 keys, 2 .. 8 tokens of 32 heads: 98 us).
 #include <algorithm>
 #include <climits>
 
@@ -192,9 +191,8 @@ __device__ __forceinline__ void join_rows(const LatentParams &p, const float *st
     }
 }
 
-// CL: CTAs of a unit, QR rows each.  JOINED: a cluster of p.pieces CTAs per unit, a piece of its keys
-// each, instead of runs.
-template <int R, int QR, int CL, bool JOINED>
+// JOINED: a cluster of p.pieces CTAs per unit, a piece of its keys each, instead of runs.
+template <int R, int QR, bool JOINED>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ PagedView pg,
                        const __grid_constant__ CUtensorMap map_q,
@@ -205,11 +203,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t S_COL = DB * QR;                // O^T block d at column QR d, then S
     constexpr uint32_t TMEM_COLS = S_COL + 128 <= 256 ? 256 : 512;
     constexpr uint32_t BLOCK16 = BLOCK_BYTES >> 4;
-    constexpr int UR = QR * CL;
-    constexpr uint16_t EVERY = (1 << CL) - 1;
-    static_assert(!JOINED || CL == 1, "a cluster shares tiles or joins pieces");
-    const int group = JOINED ? p.pieces : CL;
-    const int run = blockIdx.x / group, rank = CL > 1 ? blockIdx.x % CL : 0;
+    const int group = JOINED ? p.pieces : 1;
+    const int run = blockIdx.x / group;
     const int piece = JOINED ? blockIdx.x % group : 0;
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -222,11 +217,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&sm.q_empty, 1);
         for (int i = 0; i < PAIRS; i++) {
             mbar_init(&sm.pair_full[i], 1);
-            mbar_init(&sm.pair_empty[i], CL);
+            mbar_init(&sm.pair_empty[i], 1);
         }
         for (int i = 0; i < ROPES; i++) {
             mbar_init(&sm.rope_full[i], 1);
-            mbar_init(&sm.rope_empty[i], CL);
+            mbar_init(&sm.rope_empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sm.s_full[i], 1);
@@ -247,41 +242,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     if constexpr (JOINED)
         __syncthreads();
     else
-        find_run<UR, THREADS / 32>(p, sm, run, warp, lane);
-    if constexpr (CL > 1)
-        cluster_sync();  // the other CTA's barriers are there
+        find_run<QR, THREADS / 32>(p, sm, run, warp, lane);
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
     auto begin_walk = [&] {
         if constexpr (JOINED)
-            return Walk<UR>(p, run, piece);
+            return Walk<QR>(p, run, piece);
         else
-            return Walk<UR>(p, sm, run);
+            return Walk<QR>(p, sm, run);
     };
     // The sequence's first pages, asked for beside its lengths.
     int early = -1;
     if constexpr (JOINED) {
-        const int b = run / ((p.max_new_len * p.H + UR - 1) / UR);
+        const int b = run / ((p.max_new_len * p.H + QR - 1) / QR);
         if (warp == 0 && lane < pg.pages_per_seq)
             early = __ldg(pg.table + (size_t)b * pg.pages_per_seq + lane);
     }
-    Walk<UR> w = begin_walk();
+    Walk<QR> w = begin_walk();
     int join_count = 0;          // rows of the unit, for all threads
     long long join_row0 = 0;
     if constexpr (JOINED) {
         if (w.have) {
-            join_row0 = (long long)w.s.tok0 * p.H + (long long)w.t * UR;
-            join_count = min(UR, w.s.n * p.H - w.t * UR);
+            join_row0 = (long long)w.s.tok0 * p.H + (long long)w.t * QR;
+            join_count = min(QR, w.s.n * p.H - w.t * QR);
         }
     }
     float *stage = reinterpret_cast<float *>(&sm.pair[0]);  // idle when a piece's rows are done
     static_assert(!JOINED || sizeof(float) * QR * (R + 4) <= sizeof(sm.pair) + sizeof(sm.rope), "staged rows");
-    auto commit_all = [](uint64_t *bar) {  // in both CTAs of a pair
-        if constexpr (CL > 1)
-            tc::mma_commit_multicast(bar, EVERY);
-        else
-            tc::mma_commit(bar);
-    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer --
@@ -330,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_arrive_expect_tx(&sm.q_full, CB * QR * 128);
             __syncwarp();
             if (lane < CB)
-                tc::tma_load_2d(sm.q[lane], &map_q, lane * 64, (int)w.row0(p) + rank * QR, &sm.q_full);
+                tc::tma_load_2d(sm.q[lane], &map_q, lane * 64, (int)w.row0(p), &sm.q_full);
             for (int j = w.lo; ok && j < w.hi; j++) {
                 const int id = checked(j, asked);
                 asked = asked_next;
@@ -339,17 +326,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int first = (id << pg.page_log) + (pg.page_log > 6 ? (j * KT) & in_page : 0);
                 const int box = lane & (boxes - 1), block = lane / boxes;
                 const int from = __shfl_sync(0xffffffffu, first, box);
-                // `blocks` column blocks from column x on, a box of a page's rows per lane; of a pair of
-                // CTAs each copies those of its parity (from `parity` on) to both
-                auto load = [&](bf16 *dst, int x, int blocks, int parity, uint64_t *bar) {
+                // `blocks` column blocks from column x on, a box of a page's rows per lane
+                auto load = [&](bf16 *dst, int x, int blocks, uint64_t *bar) {
                     if (lane == 0)
                         mbar_arrive_expect_tx(bar, n * blocks * (128u << box_log));
                     __syncwarp();
-                    if (box < n && block < blocks && (CL == 1 || (block + parity) % CL == rank)) {
+                    if (box < n && block < blocks) {
                         bf16 *to = dst + block * (KT * 64) + (box << box_log) * 64;
-                        if constexpr (CL > 1)
-                            tc::tma_load_2d_multicast(to, &map_kv, x + block * 64, from, bar, EVERY);
-                        else if (read_once)
+                        if (read_once)
                             tc::tma_load_2d_hint(to, &map_kv, x + block * 64, from, bar, policy);
                         else
                             tc::tma_load_2d(to, &map_kv, x + block * 64, from, bar);
@@ -358,13 +342,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int rs = g % ROPES;
                 if (!wait_all(&sm.rope_empty[rs], ((g / ROPES) & 1) ^ 1))
                     break;
-                load(sm.rope[rs], R, 1, g, &sm.rope_full[rs]);
+                load(sm.rope[rs], R, 1, &sm.rope_full[rs]);
                 g++;
                 for (int c = 0; c < DB; c++, pairs++) {
                     const int ps = pairs % PAIRS;
                     if (!wait_all(&sm.pair_empty[ps], ((pairs / PAIRS) & 1) ^ 1))
                         break;
-                    load(sm.pair[ps][0], c * 128, 2, 0, &sm.pair_full[ps]);
+                    load(sm.pair[ps][0], c * 128, 2, &sm.pair_full[ps]);
                 }
             }
         }
@@ -407,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int k = 0; k < 4; k++)
                         tc::mma_ss(s_t, qd + (CB - 1) * Q16 + k * 2, rd + k * 2, idesc, k > 0);
                     issued = true;
-                    commit_all(&sm.rope_empty[rs]);
+                    tc::mma_commit(&sm.rope_empty[rs]);
 #pragma unroll
                     for (int c = 0; c < DB; c++, pairs++) {
                         const int ps = pairs % PAIRS;
@@ -443,9 +427,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             int g = 0, pairs = 0;
             for (int piece = 0; ok && w.next(p); piece++) {
-                // the rows' columns in whole sixteens (a CTA without rows works on for its pair)
-                const uint32_t idesc = tc::idesc_bf16_f32(
-                    128, max((w.rows(p, rank * QR, QR) + 15) / 16 * 16, 16), true, false);
+                // the rows' columns in whole sixteens
+                const uint32_t idesc = tc::idesc_bf16_f32(128, (w.rows(p, 0, QR) + 15) / 16 * 16, true, false);
                 if (piece > 0)
                     ok = mbar_wait_bounded(&sm.o_empty, (piece - 1) & 1);
                 for (int j = w.lo; ok && j < w.hi; j++, g++) {
@@ -467,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int k = 0; k < KT / 16; k++)  // 16 keys: rows of 128 B of V, 32 B of a row of P
                             tc::mma_ss(tmem + d * QR, vd + (uint64_t)(k * 128), pd + (uint64_t)(k * 2), idesc,
                                        j > w.lo || k > 0);
-                        commit_all(&sm.pair_empty[ps]);
+                        tc::mma_commit(&sm.pair_empty[ps]);
                     }
                     tc::mma_commit(&sm.pv_done);
                 }
@@ -489,18 +472,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         int g = 0;
         // Where a unit that begins here is told to the second pass: by sequence where each has one
         // unit, else by run.
-        const bool leader = tid == 0 && rank == 0;
+        const bool leader = tid == 0;
         if (!JOINED && leader && !p.cut_by_sequence)
             p.cut[run] = make_int4(0, 0, 0, -1);
         if (JOINED && tid < MAX_ROWS)
             sm.ml[tid] = make_float2(-INFINITY, 0.f);  // until there are keys
         while (ok && w.next(p)) {
-            const int rows = w.rows(p, rank * QR, QR);
+            const int rows = w.rows(p, 0, QR);
             int lim[2];  // keys that the rows see
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const int r = ra + 8 * h;
-                lim[h] = r < rows ? w.s.prior + (w.unit * UR + rank * QR + r) / p.H + 1 : 0;
+                lim[h] = r < rows ? w.s.prior + (w.unit * QR + r) / p.H + 1 : 0;
             }
             float m_ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
             for (int j = w.lo; j < w.hi; j++, g++) {
@@ -622,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // ------------------------------------------------------- a piece's rows --
             ok = ok && warp_wait(&sm.pv_done, (g - 1) & 1, &sm.abort_flag);
             const bool whole = !JOINED && w.lo == 0 && w.hi == w.tiles;
-            const size_t slot_row = (size_t)(2 * run + (w.lo == 0 ? 1 : 0)) * UR + rank * QR;
+            const size_t slot_row = (size_t)(2 * run + (w.lo == 0 ? 1 : 0)) * QR;
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
@@ -641,7 +624,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 break;
             }
             tc::fence_after_sync();
-            const long long row0 = w.row0(p) + rank * QR;
+            const long long row0 = w.row0(p);
 #pragma unroll 1
             for (int c = 0; c < DB * QR; c += 32) {
                 const int r0 = c & (QR - 1), dim = (c / QR) * 128 + quarter * 32 + lane;
@@ -678,7 +661,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const long long end = run_begin(p, sm.total, run + 1) + (w.tiles - w.hi);
                 if (!whole || p.cut_by_sequence)
                     p.cut[p.cut_by_sequence ? w.seq : run] = make_int4(
-                        (int)w.row0(p), w.rows(p, 0, UR), run, whole ? -1 : run_of(p, sm.total, end));
+                        (int)w.row0(p), rows, run, whole ? -1 : run_of(p, sm.total, end));
             }
         }
         if (!ok && lane == 0)
@@ -700,8 +683,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, TMEM_COLS);
     }
-    if constexpr (CL > 1)
-        cluster_sync();  // the other CTA copies and arrives into this one's shared memory
 }
 
 // Joins the pieces of a cut unit.  R / 4 threads take a row's pieces, 8 in flight; with GROUPS
@@ -818,7 +799,7 @@ cudaError_t launch_merge(const LatentParams &p, cudaStream_t stream)
                          block, 0, stream, p);
 }
 
-template <int R, int QR, int CL, bool JOINED>
+template <int R, int QR, bool JOINED>
 cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
     CUtensorMap mq, mkv;
@@ -835,36 +816,33 @@ cudaError_t launch_latent_t(const LatentParams &p, const PagedView &pg, cudaStre
     static_assert(smem > (116u << 10) && smem <= 232448, "shared memory of one CTA per SM");
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = once_per_device(configured, [] {
-        return cudaFuncSetAttribute(latent_attn_kernel<R, QR, CL, JOINED>,
+        return cudaFuncSetAttribute(latent_attn_kernel<R, QR, JOINED>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess)
         return e;
-    const int cluster = JOINED ? p.pieces : CL;
-    e = launch_kernel_cluster(latent_attn_kernel<R, QR, CL, JOINED>, dim3(p.grid * cluster), dim3(THREADS),
+    const int cluster = JOINED ? p.pieces : 1;
+    e = launch_kernel_cluster(latent_attn_kernel<R, QR, JOINED>, dim3(p.grid * cluster), dim3(THREADS),
                               smem, cluster > 1 ? cluster : 0, stream, p, pg, mq, mkv);
     if (JOINED || e != cudaSuccess)
         return e;
-    return launch_merge<R, QR * CL>(p, stream);
+    return launch_merge<R, QR>(p, stream);
 }
 
 template <int R>
 cudaError_t launch_latent_rows(const LatentParams &p, const PagedView &pg, cudaStream_t stream)
 {
     if (p.pieces > 0)
-        return p.unit_rows == 32 ? launch_latent_t<R, 32, 1, true>(p, pg, stream)
-                                 : launch_latent_t<R, 64, 1, true>(p, pg, stream);
-    switch (p.unit_rows) {
-    case 32: return launch_latent_t<R, 32, 1, false>(p, pg, stream);
-    case 64: return launch_latent_t<R, 64, 1, false>(p, pg, stream);
-    default:
-        if constexpr (R == 128) {
-            return launch_latent_t<R, 64, 2, false>(p, pg, stream);
-        } else {
+        return p.unit_rows == 32 ? launch_latent_t<R, 32, true>(p, pg, stream)
+                                 : launch_latent_t<R, 64, true>(p, pg, stream);
+    if (p.unit_rows == 32)
+        return launch_latent_t<R, 32, false>(p, pg, stream);
+    if constexpr (R > 128)
+        if (p.unit_rows > 64) {
             const cudaError_t e = launch_latent_pair(p, pg, stream);
             return e != cudaSuccess ? e : launch_merge<R, 128>(p, stream);
         }
-    }
+    return launch_latent_t<R, 64, false>(p, pg, stream);
 }
 
 }  // namespace
