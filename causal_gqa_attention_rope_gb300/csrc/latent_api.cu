@@ -49,11 +49,36 @@ int check_cache(const na_paged_latent_cache *c, int batch, PagedView *view)
 
 int done(cudaError_t e) { return e == cudaSuccess ? NA_OK : NA_ERR_CUDA; }
 
-struct LatentPlan {
-    int grid, unit_rows;
+// How a call's work is cut into runs, and what of its results the workspace holds.
+struct LatentRuns {
+    int grid, unit_rows, most;  // `most`: runs that the device has at a time
+    double tiles;
     bool cut_by_sequence;
+    size_t slot_rows;           // partial rows
+    size_t ws_bytes;
+};
+
+// The size of the workspace goes by these bounds alone, new lengths no longer than the call, and
+// never falls when one of them grows, so that one buffer serves every smaller step: partial rows
+// for as many runs of 64 rows as there are SMs (pairs of CTAs have half as many of 128), or for all
+// tiles where there are fewer, and an entry per SM whatever a unit's rows are.
+LatentRuns plan_runs(const na_latent_cfg *c, int batch, int total_tokens, int max_new_len, int max_total_len)
+{
+    LatentRuns r{};
+    const long long rows = (long long)std::min(max_new_len, total_tokens) * c->num_heads;
+    r.unit_rows = latent_unit_rows(rows, c->kv_rank);
+    r.tiles = (double)batch * ceil_div(rows, r.unit_rows) * ceil_div(max_total_len, kLatentKeys);
+    r.most = r.unit_rows > 64 ? std::max(sm_count() / 2, 1) : sm_count();
+    r.grid = (int)std::max(1.0, std::min((double)r.most, r.tiles));
+    r.cut_by_sequence = rows <= r.unit_rows && batch <= r.grid;
+    const double runs = std::max(sm_count(), 2) * (double)std::min(r.unit_rows, 64);
+    r.slot_rows = 2 * (size_t)std::min(runs, std::max(r.tiles, 1.0) * r.unit_rows);
+    r.ws_bytes = r.slot_rows * (c->kv_rank + 2) * sizeof(float) + sm_count() * sizeof(int4);
+    return r;
+}
+
+struct LatentPlan : LatentRuns {
     int joined_grid, pieces;  // pieces > 0: units of their own clusters instead of runs
-    size_t part_o, ws_bytes;
 };
 
 // Runs: one CTA or pair of CTAs per SM, fewer where the bounds allow no more tiles than that, and
@@ -62,25 +87,18 @@ struct LatentPlan {
 // numbers or 5 of fewer; but a cluster has 8 CTAs at most and none helps another (4
 // heads, 333 keys of 128: 9.9 us by runs, 6.7; 16 heads, 512 numbers, 1000 keys: 13.9 and 12.2,
 // 4000 keys: 15.6 and 20.7).  The lengths are bounds: batches are taken for 0.6 of them.
-LatentPlan plan_latent(const na_latent_cfg *c, int batch, int max_new_len, int max_total_len)
+LatentPlan plan_latent(const na_latent_cfg *c, int batch, int total_tokens, int max_new_len,
+                       int max_total_len)
 {
-    LatentPlan pl{};
-    const long long rows = (long long)max_new_len * c->num_heads;
-    pl.unit_rows = latent_unit_rows(rows, c->kv_rank);
-    const double tiles = (double)batch * ceil_div(rows, pl.unit_rows) * ceil_div(max_total_len, kLatentKeys);
-    const int most = pl.unit_rows > 64 ? std::max(sm_count() / 2, 1) : sm_count();
-    pl.grid = (int)std::max(1.0, std::min((double)most, tiles));
-    pl.cut_by_sequence = rows <= pl.unit_rows && batch <= pl.grid;
-    pl.part_o = (size_t)2 * pl.grid * pl.unit_rows * c->kv_rank;
-    pl.ws_bytes = (pl.part_o + (size_t)2 * pl.grid * pl.unit_rows * 2) * sizeof(float) +
-                  pl.grid * sizeof(int4);
+    LatentPlan pl{plan_runs(c, batch, total_tokens, max_new_len, max_total_len), 0, 0};
+    const long long rows = (long long)std::min(max_new_len, total_tokens) * c->num_heads;
     const int joined_rows = rows <= 32 ? 32 : 64;
     const double units = (double)batch * ceil_div(rows, joined_rows);
     const int longest = (int)ceil_div(max_total_len, kLatentKeys);
     int pieces = std::min(kLatentMaxPieces, longest);
     while (pieces > 1 && units > sm_clusters(pieces))
         pieces--;
-    const double by_runs = tiles * (batch > 1 ? 0.6 : 1.0) / most + (c->kv_rank == 512 ? 3 : 5);
+    const double by_runs = pl.tiles * (batch > 1 ? 0.6 : 1.0) / pl.most + (c->kv_rank == 512 ? 3 : 5);
     if (pieces > 0 && units <= sm_count() && ceil_div(longest, pieces) <= by_runs) {
         pl.pieces = pieces;
         pl.joined_grid = (int)units;
@@ -208,7 +226,7 @@ int na_latent_paged_workspace_size(const na_latent_cfg *cfg, int32_t batch, int3
         return rc;
     if (!bytes || batch <= 0 || total_tokens < 0 || max_new_len < 0 || max_total_len < 0)
         return NA_ERR_INVALID_ARG;
-    *bytes = plan_latent(cfg, batch, max_new_len, max_total_len).ws_bytes;
+    *bytes = plan_runs(cfg, batch, total_tokens, max_new_len, max_total_len).ws_bytes;
     return NA_OK;
 }
 
@@ -237,9 +255,7 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     // query rows are addressed by 32-bit tensor-map coordinates
     if ((long long)total_tokens * cfg->num_heads > INT_MAX - 256)
         return NA_ERR_UNSUPPORTED;
-    // (a sequence has no more new tokens than the call)
-    max_new_len = std::min(max_new_len, total_tokens);
-    const LatentPlan pl = plan_latent(cfg, batch, max_new_len, max_total_len);
+    const LatentPlan pl = plan_latent(cfg, batch, total_tokens, max_new_len, max_total_len);
     if (!workspace || ws_bytes < pl.ws_bytes || !aligned16(workspace))
         return NA_ERR_WORKSPACE;
     LatentParams p{};
@@ -250,7 +266,7 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     p.capacity = capacity;
     p.scale_log2 = score_scale_log2(cfg);
     p.total_tokens = total_tokens;
-    p.max_new_len = max_new_len;
+    p.max_new_len = std::min(max_new_len, total_tokens);  // (no sequence has more)
     p.max_total_len = max_total_len;
     p.unit_rows = pl.pieces ? std::min(pl.unit_rows, 64) : pl.unit_rows;
     p.grid = pl.pieces ? pl.joined_grid : pl.grid;
@@ -262,8 +278,8 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
     p.cache = static_cast<const bf16 *>(cache->kv);
     p.out = static_cast<bf16 *>(out);
     p.part_o = static_cast<float *>(workspace);
-    p.part_ml = p.part_o + pl.part_o;
-    p.cut = reinterpret_cast<int4 *>(p.part_ml + (size_t)2 * pl.grid * pl.unit_rows * 2);
+    p.part_ml = p.part_o + pl.slot_rows * cfg->kv_rank;
+    p.cut = reinterpret_cast<int4 *>(p.part_ml + pl.slot_rows * 2);
     p.status = status;
     if ((rc = bind_context()) != NA_OK)
         return rc;

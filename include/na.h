@@ -615,7 +615,8 @@ int na_attn_latent_paged(const na_latent_cfg *cfg, int32_t batch, const int32_t 
                          const na_paged_latent_cache *cache, void *out, void *workspace,
                          size_t ws_bytes, int32_t *status, void *stream);
 
-/* Workspace bytes (HOST out-parameter) that na_attn_latent_paged needs for these bounds. */
+/* Workspace bytes (HOST out-parameter) that na_attn_latent_paged needs for these bounds; enough for
+ * every call of this configuration with smaller ones. */
 int na_latent_paged_workspace_size(const na_latent_cfg *cfg, int32_t batch, int32_t total_tokens,
                                    int32_t max_new_len, int32_t max_total_len, size_t *bytes);
 
