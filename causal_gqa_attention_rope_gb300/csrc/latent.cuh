@@ -29,7 +29,8 @@ struct LatentParams {
     bf16 *out;
     float *part_o;             // [2 grid][unit_rows][R]: rows of a cut unit, run c's first piece at 2 c
     float *part_ml;            // [2 grid][unit_rows][2]: (max, sum), log2 domain
-    int4 *cut;                 // [grid]: first row, rows, first and last run of a unit (last -1: not cut)
+    int4 *cut;                 // [grid]: first row, rows, first and last run of a unit (last -1: not cut);
+                               // by sequence, written only where a unit's first piece is done
     int32_t *status;
 };
 
@@ -53,6 +54,12 @@ struct ExpandedParams {
 inline int latent_unit_rows(long long most_rows, int kv_rank)
 {
     return most_rows <= 32 ? 32 : (most_rows <= 64 || kv_rank == 128 ? 64 : 128);
+}
+// Whether an entry of `cut` names runs of the call.  One whose kernel gave a wait up (and reported it)
+// was not written: it is whatever the workspace held, and nothing may be addressed by it.
+__host__ __device__ inline bool names_runs(const int4 &cut, int grid)
+{
+    return cut.z >= 0 && cut.z <= cut.w && cut.w < grid;
 }
 constexpr int kLatentKeys = 64;  // keys of a tile
 constexpr int kLatentMaxPieces = 8;  // CTAs of a cluster

@@ -697,15 +697,16 @@ __global__ void __launch_bounds__(R / 4 * MERGE_THREADS_PER_DIM)
     __shared__ float4 sums[GROUPS > 1 ? GROUPS - 1 : 1][R / 4];
     grid_dependency_wait();
     grid_dependents_launch();
-    if (p.cut_by_sequence) {  // a sequence without a unit has no entry
+    int4 cut = p.cut[blockIdx.x];
+    if (p.cut_by_sequence) {  // a sequence without a unit has no entry, any other's rows are its own
         int code;
-        if (sequence_of(p, blockIdx.x, code).n == 0)
-            return;
+        const Sequence s = sequence_of(p, blockIdx.x, code);
+        cut.x = s.tok0 * p.H;
+        cut.y = s.n * p.H;
     }
-    const int4 cut = p.cut[blockIdx.x];
     const int part = threadIdx.x / (R / 4), x = threadIdx.x % (R / 4), lane = threadIdx.x & 31;
     const int r = blockIdx.y * ROWS + (GROUPS > 1 ? 0 : part), group = GROUPS > 1 ? part : 0;
-    if (cut.w < 0 || r >= cut.y)
+    if (!names_runs(cut, p.grid) || r >= cut.y)
         return;
     const int pieces = cut.w - cut.z + 1;
     // piece i in slot 2 c + 1 of the first run, 2 c of those after it
