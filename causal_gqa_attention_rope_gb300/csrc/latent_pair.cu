@@ -18,11 +18,10 @@
 // O^T has the rows along its columns and the dims in both CTAs, so each of them rescales and
 // normalises all 128 rows: the factors go to both by st.async, whose barrier
 // also says that they are there.  K's and Q's copies of both CTAs complete on the first one's
-// barriers.  That the second one's weights are written and its S read it tells by a word
-// per warp, again by st.async: an arrival on the first one's barrier that released at cluster
-// scope took some 900 cycles a tile (drafted tokens 190 us, 159 with messages).  What a message
-// speaks of is done before it is sent: P by the proxy fence in the shared memory that holds it, S
-// in registers.
+// barriers.  That the second one's weights are written, its S read and its V landed its warps tell by
+// arriving there too.  All that they speak of is in their own CTA's shared memory or in
+// registers, so the release before the arrival is one of shared memory alone: one of all
+// memory took some 900 cycles a tile (drafted tokens 191 us, 144 so).
 //
 // Warps: 0 loads Q and K, 3 V; of the first CTA 1 issues S, 2 issues O^T, of the second 1 tells
 // that V has landed; 4 .. 7 and 8 .. 11 softmax of the even and the odd tiles (one group of
@@ -58,9 +57,7 @@ struct __align__(1024) PairSmem {
     uint64_t q_full, q_empty, k_full[ST], k_empty[ST], v_full[ST], v_empty[ST];
     uint64_t s_full[NUM_S], s_read[NUM_S], m_done[2], p_full[2], pv_done[2], f_full[2], sums_full,
         o_empty, drain[2];
-    // of the first CTA: s_read, p_full and v_full of the second
-    uint64_t s_peer[NUM_S], p_peer[2], v_peer[ST];
-    float told;                // what its messages write
+    uint64_t v_other[ST];      // of the first CTA: the second one's V has landed
     long long warp_steps[THREADS / 32];
     long long total, begin;
     int b0, t0, step0;         // where the pair's run begins
@@ -77,11 +74,14 @@ __device__ __forceinline__ void store_async(const float *at, const uint64_t *bar
                  : "memory");
 }
 
-// The first CTA waits for `words` words of the second.
-__device__ __forceinline__ bool wait_told(uint64_t *bar, uint32_t parity, int words)
+// One arrival on the barrier at `bar`'s place in the first CTA.  A thread there that waits with
+// mbar_wait_cluster sees what is in this CTA's shared memory by now, this thread's writes and
+// those that it has seen.
+__device__ __forceinline__ void arrive_in_first(const uint64_t *bar)
 {
-    mbar_arrive_expect_tx(bar, words * 4);
-    return mbar_wait_cluster(bar, parity);
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(place_in_cta(bar, 0))
+                 : "memory");
 }
 
 template <int R>
@@ -110,17 +110,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_empty[i], 1);
-            mbar_init(&sm.v_peer[i], 1);
+            mbar_init(&sm.v_other[i], 1);
         }
         for (int i = 0; i < NUM_S; i++) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.s_read[i], 4);
-            mbar_init(&sm.s_peer[i], 1);
+            mbar_init(&sm.s_read[i], 8);  // a group's warps of both CTAs
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sm.m_done[i], 4);
-            mbar_init(&sm.p_full[i], 4);
-            mbar_init(&sm.p_peer[i], 1);
+            mbar_init(&sm.p_full[i], 8);
             mbar_init(&sm.pv_done[i], 1);
             mbar_init(&sm.f_full[i], 1);
             mbar_init(&sm.drain[i], 1);
@@ -239,8 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int sb = g % NUM_S, st = g % ST;
                     ok = mbar_wait_bounded(&sm.k_full[st], (g / ST) & 1);
                     if (ok && g >= NUM_S)
-                        ok = mbar_wait_bounded(&sm.s_read[sb], (g / NUM_S - 1) & 1) &&
-                             wait_told(&sm.s_peer[sb], (g / NUM_S - 1) & 1, 4);
+                        ok = mbar_wait_cluster(&sm.s_read[sb], (g / NUM_S - 1) & 1);
                     if (!ok || aborted(&sm.abort_flag)) {
                         ok = false;
                         break;
@@ -259,8 +256,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tc::mma_commit_pair(&sm.q_empty);
                 }
             }
-            for (int i = max(g - NUM_S, 0); ok && i < g; i++)  // no message is under way at the end
-                ok = wait_told(&sm.s_peer[i % NUM_S], (i / NUM_S) & 1, 4);
+            for (int i = max(g - NUM_S, 0); ok && i < g; i++)  // no arrival is under way at the end
+                ok = mbar_wait_cluster(&sm.s_read[i % NUM_S], (i / NUM_S) & 1);
             if (!ok)
                 set_abort(&sm.abort_flag, p.status);
             if (issued) {  // all issued MMAs complete before tensor memory is released
@@ -282,9 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = w.lo; ok && j < w.hi; j++, g++) {
                     const int st = g % ST;
                     ok = mbar_wait_bounded(&sm.v_full[st], (g / ST) & 1) &&
-                         wait_told(&sm.v_peer[st], (g / ST) & 1, 1) &&
-                         mbar_wait_bounded(&sm.p_full[g & 1], (g >> 1) & 1) &&
-                         wait_told(&sm.p_peer[g & 1], (g >> 1) & 1, 4);
+                         mbar_wait_cluster(&sm.v_other[st], (g / ST) & 1) &&
+                         mbar_wait_cluster(&sm.p_full[g & 1], (g >> 1) & 1);
                     if (!ok || aborted(&sm.abort_flag)) {
                         ok = false;
                         break;
@@ -318,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = w.lo; ok && j < w.hi; j++, g++) {
                     ok = mbar_wait_bounded(&sm.v_full[g % ST], (g / ST) & 1) && !aborted(&sm.abort_flag);
                     if (ok)
-                        store_async(&sm.told, &sm.v_peer[g % ST], 0, 0.f);
+                        arrive_in_first(&sm.v_other[g % ST]);
                 }
             if (!ok)
                 set_abort(&sm.abort_flag, p.status);
@@ -345,14 +341,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool done = mbar_wait_cluster(bar, parity) && !aborted(&sm.abort_flag);
             return __all_sync(0xffffffffu, done) != 0;
         };
-        // An arrival of this warp, in the second CTA as a message to the first.
-        auto tell = [&](uint64_t *own, uint64_t *peer) {
+        // An arrival of this warp in the first CTA.
+        auto tell = [&](uint64_t *bar) {
             __syncwarp();
             if (lane == 0) {
                 if (rank == 0)
-                    mbar_arrive(own);
+                    mbar_arrive(bar);
                 else
-                    store_async(&sm.told, peer, 0, 0.f);
+                    arrive_in_first(bar);
             }
         };
         const bool leader = threadIdx.x == 128 && rank == 0;
@@ -373,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc::tmem_ld32(tmem + S_COL + sb * (KT / 2) + lane_off, s);
                     tc::tmem_wait_ld();
                     tc::fence_before_sync();
-                    tell(&sm.s_read[sb], &sm.s_peer[sb]);
+                    tell(&sm.s_read[sb]);
                     // The product before the last is done: its P, and all that the group had for
                     // it here and in the other CTA, may be written over.
                     if (g >= 2)
@@ -472,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (ok) {
                     tc::fence_proxy_async_smem();
                     tc::fence_before_sync();
-                    tell(&sm.p_full[group], &sm.p_peer[group]);
+                    tell(&sm.p_full[group]);
                 }
             }
             // ------------------------------------------------------- a piece's rows --

@@ -32,3 +32,19 @@ def test_one_workspace_for_steps_of_many_sizes(R, rd):
         assert status == 0
         got, status = absorbed(cfg, pool, table, prior, new, q, workspace=shared)
         assert status == 0 and torch.equal(bits(got), bits(alone))
+
+
+@pytest.mark.parametrize("R,H,new", [(512, 32, 8), (512, 128, 1), (256, 40, 5), (128, 32, 8)])
+def test_many_rows_again_and_again(R, H, new):
+    """Units of two CTAs: the same bits from every call, next to the 64-bit statement once."""
+    import causal_gqa_attention_rope_gb300 as na
+    prior = [3000, 129, 1, 6000, 64, 777]
+    check_absorbed(H, R, 64, 64, prior, [new] * 6, seed=31)
+    cfg = na.LatentConfig(H, R, 64)
+    pool, table = make_latent([n + new for n in prior], R + 64, 64, 32)
+    q = randn(33, 6 * new, H, R + 64)
+    first, status = absorbed(cfg, pool, table, prior, [new] * 6, q)
+    assert status == 0
+    for _ in range(20):
+        got, status = absorbed(cfg, pool, table, prior, [new] * 6, q)
+        assert status == 0 and torch.equal(bits(got), bits(first))
