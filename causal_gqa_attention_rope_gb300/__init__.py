@@ -805,17 +805,12 @@ def _rows(t, name: str, width: int):
         raise ValueError("libna operates on CUDA tensors only")
     if t.numel() == 0:
         return None, width
-    lead = t.dim() - 2  # the dimension of the rows; those before it have to follow one another
-    if t.stride(-1) != 1 or any(t.shape[i] > 1 and t.stride(i) != t.stride(i + 1) * t.shape[i + 1]
-                                for i in range(lead)):
+    # the last dimension of rows gives their distance, those before it have to follow one another; a
+    # dimension of size 1 has a stride that says nothing, and a single row any distance
+    dims = [i for i in range(t.dim() - 1) if t.shape[i] > 1]
+    if t.stride(-1) != 1 or any(t.stride(i) != t.stride(j) * t.shape[j] for i, j in zip(dims, dims[1:])):
         raise ValueError(f"{name}: rows have to be contiguous and equally far apart")
-    if t.shape[lead] > 1:
-        return t.data_ptr(), t.stride(lead)
-    # one row in the last such dimension: the next one's stride is the distance
-    for i in range(lead - 1, -1, -1):
-        if t.shape[i] > 1:
-            return t.data_ptr(), t.stride(i)
-    return t.data_ptr(), max(t.stride(lead), width)
+    return t.data_ptr(), t.stride(dims[-1]) if dims else width
 
 
 def na_latent_append_paged(cfg: LatentConfig, rope: RopeConfig, cu_seqlens, cache_lens, kv, q, q_out,

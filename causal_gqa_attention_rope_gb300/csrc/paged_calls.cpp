@@ -111,7 +111,8 @@ struct Reader {
     }
 
     // Rows of `width` bf16 elements, equally far apart, of which the first dimension has at
-    // least `rows` (times `heads` of a second one unless that is 0); their distance.
+    // least `rows` (times `heads` of a second one unless that is 0); their distance.  (A dimension of
+    // size 1 has a stride that says nothing, and a single row any distance.)
     void *row_ptr(PyObject *o, int64_t rows, int64_t heads, int64_t width, int64_t &stride)
     {
         stride = 0;
@@ -123,11 +124,14 @@ struct Reader {
         const int64_t dims = heads ? 3 : 2;
         ok = t.is_cuda() && t.layout() == at::kStrided && t.get_device() == device &&
              t.scalar_type() == at::kBFloat16 && t.dim() == dims && t.size(0) >= rows &&
-             t.size(dims - 1) == width && t.stride(dims - 1) == 1 &&
-             (!heads || (t.size(1) == heads && t.stride(0) == t.stride(1) * heads));
+             t.size(dims - 1) == width && t.stride(dims - 1) == 1 && (!heads || t.size(1) == heads);
         if (!ok)
             return nullptr;
-        stride = t.stride(dims - 2);
+        stride = t.size(0) > 1 ? t.stride(0) : width;
+        if (heads > 1) {
+            ok = t.size(0) <= 1 || t.stride(0) == t.stride(1) * heads;
+            stride = t.stride(1);
+        }
         return t.data_ptr();
     }
     // Every size of an int32 tensor.
