@@ -54,6 +54,9 @@ int na_pages_fork(int32_t batch, int32_t old_batch, const int32_t *parents, cons
     if (log < 0 || batch > kMaxForkBatch || old_batch > kMaxForkBatch ||
         (long long)pages_per_seq > (0x7fffffffLL >> log) || num_pages > (0x7fffffff >> log))
         return NA_ERR_UNSUPPORTED;
+    // the entries that a step has to fill are counted, and ranked, in 32 bits
+    if ((long long)batch * pages_per_seq > INT_MAX)
+        return NA_ERR_UNSUPPORTED;
     return done(launch_pages_fork(ForkParams{batch, old_batch, pages_per_seq, log, num_pages, parents,
                                              grow, lens, table, ref, new_table, new_ref, new_lens,
                                              copy_src, copy_dst, status},

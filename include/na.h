@@ -466,8 +466,8 @@ int na_decode_workspace_size(const na_attn_cfg *cfg, int32_t batch, int32_t max_
  *           than pages_per_seq (the entries that are missing are -1, a copy
  *           without a page -1 -> -1).
  * Errors: NA_ERR_INVALID_ARG for null pointers (status and grow may be NULL) and
- * sizes below 1, NA_ERR_UNSUPPORTED for a page size other than 16, 32, 64, 128 or
- * more than 4096 sequences.
+ * sizes below 1, NA_ERR_UNSUPPORTED for a page size other than 16, 32, 64, 128,
+ * more than 4096 sequences or a new table of more than 2^31 - 1 entries.
  */
 int na_pages_fork(int32_t batch, int32_t old_batch, const int32_t *parents, const int32_t *grow,
                   const int32_t *lens, const int32_t *table, int32_t pages_per_seq,
