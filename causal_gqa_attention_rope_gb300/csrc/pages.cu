@@ -734,11 +734,13 @@ cudaError_t launch_pages_copy(const PageCopyParams &p, cudaStream_t stream)
 cudaError_t launch_pages_compact(const CompactParams &p, bool e4m3, const RopeTurns &turns,
                                  cudaStream_t stream)
 {
+    // rows that a sequence can have: a loose bound costs no CTAs
+    const long long rows = p.max_keep < p.to_positions ? p.max_keep : p.to_positions;
     // words of 8 elements where pairs, their start and the rest come in such
     const int unit = p.turn ? (p.rd | 2 * p.rot_start) & 15 : 0;
     if (e4m3) {
         const int page = 1 << p.to.page_log;
-        const int blocks = (p.max_keep + page - 1) / page;
+        const int blocks = (int)((rows + page - 1) / page);
         if ((long long)blocks * p.batch > INT_MAX)
             return cudaErrorInvalidConfiguration;
         const dim3 grid((unsigned)(blocks * p.batch), 2 * p.KV);
@@ -758,7 +760,7 @@ cudaError_t launch_pages_compact(const CompactParams &p, bool e4m3, const RopeTu
             return e;
         return launch_kernel(kernel, grid, dim3(COMPACT_THREADS), smem, stream, p, turns, blocks);
     }
-    const int blocks = (p.max_keep + COMPACT_ROWS - 1) / COMPACT_ROWS;
+    const int blocks = (int)((rows + COMPACT_ROWS - 1) / COMPACT_ROWS);
     if ((long long)blocks * p.batch > INT_MAX)
         return cudaErrorInvalidConfiguration;
     const size_t smem = (size_t)COMPACT_ROWS * (p.turn ? p.rd / 2 : 0) * sizeof(float2);  // 8 KB at most
