@@ -600,6 +600,7 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
     const int pairs = turn ? p.rd / 2 / W : 0;
     const int units = pairs + (p.d - (turn ? p.rd : 0)) / W;
     float amax = 0.f;
+    bool any = false;  // of the rows is moved
     for (int i = threadIdx.x; i < n * units; i += COMPACT_THREADS) {
         const int r = i / units, u = i - r * units;
         Move m;
@@ -608,6 +609,7 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
             moved[r] = there;
         if (!there)
             continue;
+        any = true;
         const uint8_t *from = (is_v ? p.from_v : p.from_k) +
                               ((((size_t)m.src * p.KV + g) << p.from.page_log) + m.src_slot) * p.d;
         uint32_t s = __ldg((is_v ? p.from.v_scale : p.from.k_scale) + (size_t)m.src * p.KV + g);
@@ -666,12 +668,11 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if ((threadIdx.x & 31) == 0)
         amax_of[threadIdx.x >> 5] = amax;
-    __syncthreads();
+    if (!__syncthreads_or(any))
+        return;  // reported with the rows; the page keeps its bytes and what they stand for
 #pragma unroll
     for (int w = 0; w < COMPACT_THREADS / 32; w++)
         amax = fmaxf(amax, amax_of[w]);
-    if ((unsigned)dst >= (unsigned)p.to.num_pages)
-        return;  // reported with the rows
     const int s = min(scale_byte(amax), 254);
     // 2^(127 - s) in two factors: the first of a small scale alone exceeds fp32
     const int up = 127 - s, half = up / 2;

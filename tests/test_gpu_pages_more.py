@@ -43,3 +43,20 @@ def test_a_loose_bound(fmt, top):
                     assert ((x - y).abs() <= 2.0 ** -4 * x.abs() + torch.exp2(t - 10)[:, None]).all()
     if top > 64:
         assert compact(old.to(DEV), new.to(DEV), [40, 65], top) == na.NA_ERR_CAPACITY
+
+
+def test_a_page_of_skipped_rows_keeps_its_scale():
+    """None of its rows is moved: its bytes stand for what they stood for."""
+    import causal_gqa_attention_rope_gb300 as na
+    old, new = make_paged([40, 20], 2, 64, 16, "e4m3", 3), make_paged([40, 40], 2, 64, 16, "e4m3", 4)
+    a, z = old.to(DEV), new.to(DEV)
+    a.page_table = a.page_table.clone()
+    a.page_table[0, 1] = old.k.shape[0]
+    assert compact(a, z, [40, 20], 40) == na.NA_ERR_PAGE
+    skipped, moved = int(new.table[0, 1]), [int(new.table[0, 0]), int(new.table[1, 0])]
+    for was, scale, got, got_scale in ((new.k, new.k_scale, z.k, z.k_scale), (new.v, new.v_scale, z.v, z.v_scale)):
+        got, got_scale = got.cpu(), got_scale.cpu()
+        assert torch.equal(bits(got[skipped]), bits(was[skipped]))
+        assert torch.equal(got_scale[skipped], scale[skipped])
+        for pid in moved:
+            assert not torch.equal(bits(got[pid]), bits(was[pid]))
