@@ -599,83 +599,95 @@ __global__ void __launch_bounds__(COMPACT_THREADS)
     const bool turn = p.turn && !is_v;
     const int pairs = turn ? p.rd / 2 / W : 0;
     const int units = pairs + (p.d - (turn ? p.rd : 0)) / W;
-    float amax = 0.f;
-    bool any = false;  // of the rows is moved
-    for (int i = threadIdx.x; i < n * units; i += COMPACT_THREADS) {
-        const int r = i / units, u = i - r * units;
-        Move m;
-        const bool there = find_move(p, b, j0 + r, m);
-        if (u == 0)
-            moved[r] = there;
-        if (!there)
-            continue;
-        any = true;
-        const uint8_t *from = (is_v ? p.from_v : p.from_k) +
-                              ((((size_t)m.src * p.KV + g) << p.from.page_log) + m.src_slot) * p.d;
-        uint32_t s = __ldg((is_v ? p.from.v_scale : p.from.k_scale) + (size_t)m.src * p.KV + g);
-        if (s == 255) {
-            na_report(p.status, NA_ERR_UNSUPPORTED);
-            s = 254;
-        }
-        const float mul = e8m0_value(s);
-        float *row = rows + r * p.d;
-        auto load = [&](int e, float (&x)[W]) {
-            if constexpr (W == 8) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(from + e);
-                uint32_t h[4];
-                e4m3x4_to_f16(w.x, h[0], h[1]);
-                e4m3x4_to_f16(w.y, h[2], h[3]);
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
-                    x[2 * k] = f.x * mul;
-                    x[2 * k + 1] = f.y * mul;
-                }
-            } else {
-                x[0] = e4m3_value(from[e]) * mul;
+    // The rows times 2^-down: 0, then 16 where a value exceeds fp32, whose largest is then infinite
+    // (scales of 2^119 and more; what that loses at the other end is far below the page's
+    // smallest step).
+    float amax;
+    int down = 0;
+    for (;; down = 16) {
+        amax = -1.f;  // no row is moved
+        for (int i = threadIdx.x; i < n * units; i += COMPACT_THREADS) {
+            const int r = i / units, u = i - r * units;
+            Move m;
+            const bool there = find_move(p, b, j0 + r, m);
+            if (u == 0)
+                moved[r] = there;
+            if (!there)
+                continue;
+            amax = fmaxf(amax, 0.f);
+            const uint8_t *from = (is_v ? p.from_v : p.from_k) +
+                                  ((((size_t)m.src * p.KV + g) << p.from.page_log) + m.src_slot) * p.d;
+            uint32_t s = __ldg((is_v ? p.from.v_scale : p.from.k_scale) + (size_t)m.src * p.KV + g);
+            if (s == 255) {
+                na_report(p.status, NA_ERR_UNSUPPORTED);
+                s = 254;
             }
-        };
-        if (u >= pairs) {
-            const int e = turn ? plain_unit<W>(p, u - pairs) : u * W;
-            float x[W];
-            load(e, x);
+            const float mul = e8m0_value(s) * exp2i(-down);
+            float *row = rows + r * p.d;
+            auto load = [&](int e, float (&x)[W]) {
+                if constexpr (W == 8) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(from + e);
+                    uint32_t h[4];
+                    e4m3x4_to_f16(w.x, h[0], h[1]);
+                    e4m3x4_to_f16(w.y, h[2], h[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                        x[2 * k] = f.x * mul;
+                        x[2 * k + 1] = f.y * mul;
+                    }
+                } else {
+                    x[0] = e4m3_value(from[e]) * mul;
+                }
+            };
+            if (u >= pairs) {
+                const int e = turn ? plain_unit<W>(p, u - pairs) : u * W;
+                float x[W];
+                load(e, x);
+#pragma unroll
+                for (int w = 0; w < W; w++) {
+                    row[e + w] = x[w];
+                    amax = fmaxf(amax, fabsf(x[w]));
+                }
+                continue;
+            }
+            int e0, e1;
+            pair_unit<W>(p, u, e0, e1);
+            float x[2][W];
+            load(e0, x[0]);
+            load(e1, x[1]);
 #pragma unroll
             for (int w = 0; w < W; w++) {
-                row[e + w] = x[w];
-                amax = fmaxf(amax, fabsf(x[w]));
+                const float2 c = turn_back(turns, u * W + w, m.shift);
+                // the pair's places: its halves, or two neighbours of the 2 W elements
+                const int i0 = p.interleaved ? 2 * w : w, i1 = p.interleaved ? 2 * w + 1 : W + w;
+                const float a0 = x[i0 / W][i0 % W], a1 = x[i1 / W][i1 % W];
+                const float y0 = fmaf(a0, c.x, -a1 * c.y), y1 = fmaf(a1, c.x, a0 * c.y);
+                row[(i0 < W ? e0 : e1) + i0 % W] = y0;
+                row[(i1 < W ? e0 : e1) + i1 % W] = y1;
+                amax = fmaxf(amax, fmaxf(fabsf(y0), fabsf(y1)));
+                if (fmaxf(fabsf(a0), fabsf(a1)) == INFINITY)
+                    amax = INFINITY;  // (what is turned may be infinity less infinity)
             }
-            continue;
         }
-        int e0, e1;
-        pair_unit<W>(p, u, e0, e1);
-        float x[2][W];
-        load(e0, x[0]);
-        load(e1, x[1]);
 #pragma unroll
-        for (int w = 0; w < W; w++) {
-            const float2 c = turn_back(turns, u * W + w, m.shift);
-            // the pair's places: its halves, or two neighbours of the 2 W elements
-            const int i0 = p.interleaved ? 2 * w : w, i1 = p.interleaved ? 2 * w + 1 : W + w;
-            const float a0 = x[i0 / W][i0 % W], a1 = x[i1 / W][i1 % W];
-            const float y0 = fmaf(a0, c.x, -a1 * c.y), y1 = fmaf(a1, c.x, a0 * c.y);
-            row[(i0 < W ? e0 : e1) + i0 % W] = y0;
-            row[(i1 < W ? e0 : e1) + i1 % W] = y1;
-            amax = fmaxf(amax, fmaxf(fabsf(y0), fabsf(y1)));
-        }
+        for (int o = 16; o; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if ((threadIdx.x & 31) == 0)
+            amax_of[threadIdx.x >> 5] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < COMPACT_THREADS / 32; w++)
+            amax = fmaxf(amax, amax_of[w]);
+        if (amax != INFINITY || down)
+            break;
+        __syncthreads();  // all have read the page's largest
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((threadIdx.x & 31) == 0)
-        amax_of[threadIdx.x >> 5] = amax;
-    if (!__syncthreads_or(any))
+    if (amax < 0.f)
         return;  // reported with the rows; the page keeps its bytes and what they stand for
-#pragma unroll
-    for (int w = 0; w < COMPACT_THREADS / 32; w++)
-        amax = fmaxf(amax, amax_of[w]);
-    const int s = min(scale_byte(amax), 254);
-    // 2^(127 - s) in two factors: the first of a small scale alone exceeds fp32
-    const int up = 127 - s, half = up / 2;
+    const int s = min(scale_byte(amax) + down, 254);
+    // 2^(127 - s + down) in two factors: the first of a small scale alone exceeds fp32
+    const int up = 127 - s + down, half = up / 2;
     const float m0 = exp2i(half), m1 = exp2i(up - half);
     const size_t page = (size_t)dst * p.KV + g;
     uint8_t *to = (is_v ? p.to_v : p.to_k) + (page << p.to.page_log) * p.d;

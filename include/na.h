@@ -501,10 +501,10 @@ int na_pages_copy(int32_t num_kv_heads, int32_t head_dim, const na_paged_kv_cach
  * contiguous `to` it gathers sequences out of their pages.
  * bf16: an unturned row is moved bit for bit; a turned value is rounded once to
  * bf16 (within one ulp, correctly but for 2^-22 of its pair next to a rounding border).
- * E4M3: a new page's scale is the smallest power of two 2^e with max |x| <= 448 * 2^e
- * over the rows moved into it, x the stored values turned in fp32 (within 2^-20 of
- * the row's largest), and every x is rounded once to x * 2^-e.  (Other slots of such a page
- * keep their bytes, a page into which no row is moved its scale too.)
+ * E4M3: a new page's scale is the smallest power of two 2^e, -127 <= e <= 127, with
+ * max |x| <= 448 * 2^e over the rows moved into it, x the stored values turned in fp32
+ * (within 2^-20 of the row's largest), and every x is rounded once to x * 2^-e.  (Other
+ * slots of such a page keep their bytes, a page into which no row is moved its scale too.)
  *
  *   from, to   caches of one dtype; their page sizes may differ, and they may be
  *              the same pools.  No page that `to` writes may be one that `from`

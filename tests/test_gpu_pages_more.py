@@ -60,3 +60,40 @@ def test_a_page_of_skipped_rows_keeps_its_scale():
         assert torch.equal(got_scale[skipped], scale[skipped])
         for pid in moved:
             assert not torch.equal(bits(got[pid]), bits(was[pid]))
+
+
+@pytest.mark.parametrize("rd", [0, 64, 34])
+@pytest.mark.parametrize("scales", [(254, 254, 254), (254, 0, 250), (247, 246, 130), (0, 0, 0), (1, 254, 0)], ids=str)
+def test_compact_of_scales_beyond_fp32(scales, rd):
+    """Stored values of 448 * 2^127 exceed fp32; what they stand for is moved all the same."""
+    import causal_gqa_attention_rope_gb300 as na
+    KV, d, page, new_page = 2, 64, 16, 32
+    old, new = make_paged([48], KV, d, page, "e4m3", 5), make_paged([0], KV, d, new_page, "e4m3", 6, room=48)
+    for pool, scale in ((old.k, old.k_scale), (old.v, old.v_scale)):
+        if rd:  # a turn makes 2^0.5 of a value at most: 362 of 256
+            pool.view(torch.uint8).copy_((pool.float() / 2).to(pool.dtype).view(torch.uint8))
+        for i, s in enumerate(scales):
+            scale[old.table[0, i]] = s
+    keep = list(range(3, 9)) + list(range(20, 30)) + [46, 33, 40, 47, 10] + list(range(11, 16)) + list(range(40, 48))
+    rope = na.RopeConfig(base=1e4)
+    z = new.to(DEV)
+    assert compact(old.to(DEV), z, [len(keep)], len(keep), keep=ints([keep]), rope=rope if rd else None,
+                   rotary_dim=rd) == 0
+    at = torch.tensor(keep)
+    for pool, scale, got, got_scale, is_k in ((old.k, old.k_scale, z.k.cpu(), z.k_scale.cpu(), True),
+                                              (old.v, old.v_scale, z.v.cpu(), z.v_scale.cpu(), False)):
+        for lo in range(0, len(keep), new_page):
+            rows = at[lo:lo + new_page]
+            sid, pid = old.table[0, rows // page].long(), int(new.table[0, lo // new_page])
+            x = pool.view(torch.uint8)[sid, :, rows % page].view(pool.dtype).double()
+            x = x * torch.exp2(scale[sid].double() - 127)[..., None]
+            if rd and is_k:
+                x = turned(x, (torch.arange(lo, lo + len(rows)) - rows)[:, None], rope, 0, rd)
+            amax, e = x.abs().amax(dim=(0, 2)), got_scale[pid].double() - 127
+            near = 2.0 ** -20  # of the page's largest, as fp32 turns it
+            assert (amax * (1 - near) <= 448 * torch.exp2(e)).all()
+            assert ((amax * (1 + near) > 448 * torch.exp2(e - 1)) | (e == -127)).all()
+            y = got[pid, :, :len(rows)].permute(1, 0, 2).contiguous().double() * torch.exp2(e)[:, None]
+            # half a step of E4M3: 2^-4 of the value, 2^-10 of the scale below its normal range
+            tol = 2.0 ** -4 * x.abs() + torch.exp2(e - 10)[:, None] + near * amax[:, None]
+            assert ((y - x).abs() <= tol).all()
