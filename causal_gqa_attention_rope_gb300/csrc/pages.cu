@@ -22,8 +22,8 @@ using namespace rope;
 // exactly one child (kids - 1 for a shared page, -1 for an ended sequence's).  Free pages
 // are then found in index order by a scan, page rank k going to the sequence whose range of
 // missing pages holds k, and a copy to the one that gets its sequence's first.  Bound by latency:
-// 256 sequences in 9000 pages take 8 us, one CTA took 26,
-// 17 of them for the rows.
+// 256 sequences in 8750 pages take 8.4 us by itself, 9.9 where 95 of them get a copy of a page
+// (11 with the launch that copies them); one CTA took 26, 17 of them for the rows.
 
 constexpr int FORK_CTAS = 8;
 constexpr int FORK_AHEAD = 4;  // entries per lane and round of a row
@@ -724,8 +724,9 @@ cudaError_t launch_fork_t(const ForkParams &p, cudaStream_t stream)
 
 }  // namespace
 
-// A warp per row, new or old, as far as a CTA has them: fewer threads meet faster (32 sequences:
-// 8.2 us by 1024 threads, 6.8 by 256), more rows at a time are worth that (256: 10.7 and 14.7).
+// A warp per row, new or old, as far as a CTA has them: fewer threads meet faster (32 sequences with
+// the launch that copies: 8.2 us by 1024 threads, 6.8 by 256), more rows at a time are worth that
+// (256 so: 10.7 and 14.7).
 cudaError_t launch_pages_fork(const ForkParams &p, cudaStream_t stream)
 {
     const int warps = (p.batch + p.old_batch + FORK_CTAS - 1) / FORK_CTAS;

@@ -636,6 +636,7 @@ int na_latent_paged_workspace_size(const na_latent_cfg *cfg, int32_t batch, int3
  *   k_pe  bf16, rd elements a key, k_pe_stride elements apart (a multiple of 8): the rotated
  *         part of latent rows.
  *   out   bf16 [total_tokens][H][dv].
+ *   total_keys  at least 1 where there are tokens (NA_ERR_INVALID_ARG).
  *   status  NA_ERR_INVALID_ARG for a new length above max_new_len or outside the call's
  *           tokens, NA_ERR_CAPACITY for keys above max_key_len or outside the total_keys
  *           rows; such a sequence is skipped.
