@@ -25,7 +25,7 @@
 // A unit can be cut into pieces of its keys: the CTAs of a cluster take one each and join their rows
 // out of one another's shared memory.  That fills the SMs where units are few, and the last wave:
 // 2048 tokens after 28672, 40 heads, are 320 units on 152 SMs: 1033 us, with the last 16 in six
-// pieces, and the others in turn, 944 .. 989 from run to run (1650 .. 1575 TFLOP/s).
+// pieces, and the others in turn, 944 .. 997 from run to run (1650 .. 1560 TFLOP/s).
 #include <algorithm>
 #include <climits>
 
